@@ -128,6 +128,11 @@ def _padded(q):
     return wide[..., :n]
 
 
+def _by_block(s):
+    """Scales stored block after block, as the quantiser and the norm store them."""
+    return s.transpose(-1, -2).contiguous().transpose(-1, -2)
+
+
 def _uneven(g, m, n):
     """Values as activations have them: rows and some columns of other sizes."""
     x = torch.randn(m, n, generator=g, device="cuda")
@@ -157,7 +162,7 @@ def prepare(case, seed):
         m = case["m"]
         s["a"], s["sa"] = _quantise(_uneven(g, m, k), case["fa"], 1, False)
         s["b"], s["sb"] = _quantise(torch.randn(n, k, generator=g, device="cuda") / math.sqrt(k), "e4m3", case["rows"], False)
-        s["a"], s["b"] = _padded(s["a"]), _padded(s["b"])
+        s["a"], s["b"], s["sa"], s["sb"] = _padded(s["a"]), _padded(s["b"]), _by_block(s["sa"]), _by_block(s["sb"])
         s["c"] = _rows(g, m, n, T16[case["d"]]) if case["c"] else None
         return s
     at = _offsets(case, seed)
@@ -166,9 +171,9 @@ def prepare(case, seed):
     s["at"] = torch.tensor(at, dtype=torch.int32, device="cuda")
     if op == "grouped_f8":
         s["a"], s["sa"] = _quantise(_uneven(g, tokens, k), "e4m3", 1, False)
-        s["a"] = _padded(s["a"])
+        s["a"], s["sa"] = _padded(s["a"]), _by_block(s["sa"])
         w, sw = zip(*(_quantise(torch.randn(n, k, generator=g, device="cuda") / math.sqrt(k), "e4m3", 128, False) for _ in range(e)))
-        s["b"], s["sb"] = _padded(torch.stack([x.view(torch.uint8) for x in w]).view(F8["e4m3"])), torch.stack(sw)
+        s["b"], s["sb"] = _padded(torch.stack([x.view(torch.uint8) for x in w]).view(F8["e4m3"])), _by_block(torch.stack(sw))
         return s
     t = T16[case["t"]]
     if op == "grouped_w":
