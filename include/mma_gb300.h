@@ -91,7 +91,9 @@ typedef enum {
   MMA_I8 = 3,
   MMA_F64 = 4,
   MMA_F32 = 5,
-  MMA_I32 = 6
+  MMA_I32 = 6,
+  MMA_F8E4M3 = 7, /* 8-bit floating point, 448 the largest value */
+  MMA_F8E5M2 = 8  /* 8-bit floating point, 57344 the largest finite value */
 } mma_dtype_t;
 
 typedef enum { MMA_COL_MAJOR = 0, MMA_ROW_MAJOR = 1 } mma_layout_t;
@@ -383,6 +385,173 @@ mma_status_t mma_gemm_i8_noalloc(int64_t M, int64_t N, int64_t K,
                                  const void *A, int64_t lda, const void *B,
                                  int64_t ldb, const void *C, int64_t ldc,
                                  void *D, int64_t ldd, void *stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * 8-bit floating-point operands with scales, and products grouped by expert
+ * ------------------------------------------------------------------------
+ *
+ * An 8-bit operand is a matrix q of E4M3 or E5M2 values and FP32 scales: the
+ * value of element (i, k) is q[i][k] * S(i / r, k / 128), with r = 1 (a scale
+ * for each block of 128 along a row) or r = 128 (square blocks).  S(i, b) is
+ * at S[i * s_row + b * s_blk]; both strides are given in elements and are
+ * >= 0, the scales are 4-byte aligned.  s_row = 1 (the scales of one k block
+ * for all rows side by side) is the order that is read fastest.
+ *
+ * Unlike the calls above, these ask of their outputs (and of C) no more than
+ * the alignment of one element; inputs keep the rule of 16-byte rows, except
+ * that scales and offsets need 4 bytes.
+ */
+
+/*
+ * mma_rmsnorm_f8 -- root-mean-square norm of the rows of X + R, in 8 bits.
+ *
+ *     h = x + r,   y = h * w / sqrt(mean(h^2) + eps)     (FP32 throughout)
+ *     s = max(max |y| over 128 columns / 448, 2^-126),   q = y / s  (E4M3)
+ *
+ * type   : MMA_F16, MMA_BF16 or MMA_F32, of X, R, H and Y.
+ * w_type : of W (N elements): `type` or MMA_F32.
+ * R      : M x N residual, or NULL (then h = x).
+ * pow2   : nonzero -- s is rounded up to a power of two.
+ * H      : M x N, the sum rounded to `type` (the next layer's residual), or
+ *          NULL.  May be X or R itself, with the same leading dimension.
+ * Y      : M x N, y rounded to `type`, or NULL.
+ * Q, S   : M x N E4M3 values and their scales (1 x 128 blocks), or both
+ *          NULL.  One of Y and Q is required.  Q's rows start on 16-byte
+ *          boundaries, as the products read them.
+ * A NaN or infinity in a row makes its row NaN; one that w brings into a
+ * block makes that block's scale NaN or infinite and its values NaN or zero.
+ */
+mma_status_t mma_rmsnorm_f8(int type, int w_type, int64_t M, int64_t N,
+                            const void *X, int64_t ldx, const void *R,
+                            int64_t ldr, const void *W, float eps, int pow2,
+                            void *H, int64_t ldh, void *Y, int64_t ldy,
+                            void *Q, int64_t ldq, float *S, int64_t s_row,
+                            int64_t s_blk, void *stream);
+
+/*
+ * mma_rmsnorm_backward -- gradient of the norm, from the stored sum H:
+ *
+ *     g = dy * w,  DX = g / rms - h * mean(g h) / rms^3 + R
+ *     DW[j] = sum over rows of dy * h / rms               (FP32)
+ *
+ * R is the gradient that reaches H from elsewhere, or NULL; DX is the
+ * gradient of X and of the forward's residual alike, and may be DY or R.
+ * DW is summed in a fixed order (the same bits from run to run), through
+ * the library's scratch buffer (2 * SMs * N * 4 bytes at most;
+ * MMA_ERR_NO_MEMORY if it cannot grow).  Types as in mma_rmsnorm_f8.
+ * M == 0 gives DW = 0.
+ */
+mma_status_t mma_rmsnorm_backward(int type, int w_type, int64_t M, int64_t N,
+                                  const void *DY, int64_t lddy, const void *H,
+                                  int64_t ldh, const void *W, float eps,
+                                  const void *R, int64_t ldr, void *DX,
+                                  int64_t lddx, float *DW, void *stream);
+
+/*
+ * mma_quantize_f8 -- X (M x N; MMA_F16, MMA_BF16 or MMA_F32) as 8-bit values
+ * of type f8_type with scales:
+ *
+ *     s = max(max |x| over the block / format's largest value, 2^-126)
+ *     q = x / s, to nearest
+ *
+ * block_rows : 1 or 128 (the blocks are block_rows x 128).
+ * transpose  : nonzero -- Q is N x M, the transpose; its blocks of 128 run
+ *              along its rows, that is, down X's columns.
+ * pow2       : nonzero -- s is rounded up to a power of two.
+ * Q's rows start on 16-byte boundaries.  A block with a NaN has a NaN
+ * scale, one with an infinity an infinite scale.
+ */
+mma_status_t mma_quantize_f8(int type, int f8_type, int64_t M, int64_t N,
+                             int block_rows, int transpose, int pow2,
+                             const void *X, int64_t ldx, void *Q, int64_t ldq,
+                             float *S, int64_t s_row, int64_t s_blk,
+                             void *stream);
+
+/*
+ * mma_gemm_f8 -- D = A * B + C for 8-bit operands with scales, B
+ * column-major: with a = q * s of A and b of B,
+ *
+ *     D[i][j] = C[i][j] + sum_b SA(i, b) SB(j / sb_rows, b)
+ *                             * sum_{k in block b} qa[i][k] qb[j][k]
+ *
+ * type_a, type_b : MMA_F8E4M3 or MMA_F8E5M2, each.
+ * type_d         : MMA_F32, MMA_BF16 or MMA_F16, of C and D.
+ * A, SA          : M x K, scales of 1 x 128 blocks.
+ * B, SB          : N x K, scales of sb_rows x 128 blocks, sb_rows 1 or 128.
+ * C              : M x N or NULL; may be D with the same leading dimension.
+ * Block products are summed in the tensor core's FP32, scaled by the FP32
+ * product of the two scales and added in FP32; D is rounded once.  The
+ * gradients are the same call on quantised gradients and transposes (see
+ * mma_quantize_f8); sb_rows = 1 serves the weight's.
+ */
+mma_status_t mma_gemm_f8(int type_a, int type_b, int type_d, int64_t M,
+                         int64_t N, int64_t K, const void *A, int64_t lda,
+                         const float *SA, int64_t sa_row, int64_t sa_blk,
+                         const void *B, int64_t ldb, const float *SB,
+                         int sb_rows, int64_t sb_row, int64_t sb_blk,
+                         const void *C, int64_t ldc, void *D, int64_t ldd,
+                         void *stream);
+
+/*
+ * mma_gemm_grouped -- products grouped by expert: the T rows of A are sorted
+ * by group, group e is rows [offsets[e], offsets[e + 1]), and
+ *
+ *     D[i] = A[i] * B_e + C[i]     for the rows i of each group e.
+ *
+ * type_in  : MMA_F16 or MMA_BF16 (A, B); type_d : that or MMA_F32 (C, D).
+ * groups   : 0 .. MMA_MAX_GROUPS (more: MMA_ERR_UNSUPPORTED).
+ * offsets  : groups + 1 int32 values in DEVICE memory, read when the kernel
+ *            runs; non-decreasing, within [0, T].  Values outside are
+ *            clamped and decreasing ones raised to the one before; rows of
+ *            no group are not written.  Groups may be empty.
+ * B        : B_e at B + e * stride_b elements, column-major (N x K stored)
+ *            or row-major (K x N stored; the input gradient of the
+ *            column-major product with N and K exchanged).
+ * C        : T x N or NULL; may be D with the same leading dimension.
+ * Sums are FP32 (chunks of 256 from the tensor core, added to nearest).
+ */
+#define MMA_MAX_GROUPS 1024
+mma_status_t mma_gemm_grouped(int type_in, int type_d, int64_t groups,
+                              int64_t T, int64_t N, int64_t K, const void *A,
+                              int64_t lda, const void *B, int64_t ldb,
+                              int64_t stride_b, int layout_b,
+                              const int32_t *offsets, const void *C,
+                              int64_t ldc, void *D, int64_t ldd, void *stream);
+
+/*
+ * mma_gemm_grouped_wgrad -- the weight gradient of mma_gemm_grouped:
+ *
+ *     D_e = DY_e^T * X_e + C_e     (N x K, over the rows of group e)
+ *
+ * DY is T x N, X is T x K; D_e is at D + e * stride_d, C_e at
+ * C + e * stride_c (C may be D with the same strides: accumulation).  An
+ * empty group gives D_e = C_e, or zeros.  Other arguments as above.
+ */
+mma_status_t mma_gemm_grouped_wgrad(int type_in, int type_d, int64_t groups,
+                                    int64_t T, int64_t N, int64_t K,
+                                    const void *DY, int64_t lddy,
+                                    const void *X, int64_t ldx,
+                                    const int32_t *offsets, const void *C,
+                                    int64_t ldc, int64_t stride_c, void *D,
+                                    int64_t ldd, int64_t stride_d,
+                                    void *stream);
+
+/*
+ * mma_gemm_grouped_f8 -- mma_gemm_grouped with column-major 8-bit B and the
+ * operands and scales of mma_gemm_f8; the scales of B_e start at
+ * SB + e * sb_group.
+ */
+mma_status_t mma_gemm_grouped_f8(int type_a, int type_b, int type_d,
+                                 int64_t groups, int64_t T, int64_t N,
+                                 int64_t K, const void *A, int64_t lda,
+                                 const float *SA, int64_t sa_row,
+                                 int64_t sa_blk, const void *B, int64_t ldb,
+                                 int64_t stride_b, const float *SB,
+                                 int sb_rows, int64_t sb_group, int64_t sb_row,
+                                 int64_t sb_blk, const int32_t *offsets,
+                                 const void *C, int64_t ldc, void *D,
+                                 int64_t ldd, void *stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *mma_status_string(int status);

@@ -15,7 +15,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIBNAME = "libmma_gb300.so"
 
 MMA_F16, MMA_BF16, MMA_I8, MMA_F64, MMA_F32, MMA_I32 = 1, 2, 3, 4, 5, 6
+MMA_F8E4M3, MMA_F8E5M2 = 7, 8
 MMA_COL_MAJOR, MMA_ROW_MAJOR = 0, 1
+MMA_MAX_GROUPS = 1024
 STATUS = {0: "MMA_OK", 1: "MMA_ERR_INVALID_ARG", 2: "MMA_ERR_UNSUPPORTED",
           3: "MMA_ERR_MISALIGNED", 4: "MMA_ERR_LAUNCH", 5: "MMA_ERR_TIMEOUT",
           6: "MMA_ERR_NO_DEVICE", 7: "MMA_ERR_NO_MEMORY"}
@@ -23,6 +25,7 @@ STATUS = {0: "MMA_OK", 1: "MMA_ERR_INVALID_ARG", 2: "MMA_ERR_UNSUPPORTED",
 # The exported entry points and their ctypes signatures (kept in step with
 # include/mma_gb300.h; tests check both lists against the header).
 _p, _i64, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+_f32 = ctypes.c_float
 SIGNATURES = {
     "mma_gemm": (_int, [_int, _int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p,
                         _i64, _p, _i64, _p]),
@@ -38,6 +41,26 @@ SIGNATURES = {
                               _int, _int, _p, _i64, _p, _i64, _int, _p]),
     "mma_gemm_i8_noalloc": (_int, [_i64, _i64, _i64, _p, _i64, _p, _i64, _p,
                                    _i64, _p, _i64, _p]),
+    "mma_rmsnorm_f8": (_int, [_int, _int, _i64, _i64, _p, _i64, _p, _i64, _p,
+                              _f32, _int, _p, _i64, _p, _i64, _p, _i64, _p,
+                              _i64, _i64, _p]),
+    "mma_rmsnorm_backward": (_int, [_int, _int, _i64, _i64, _p, _i64, _p, _i64,
+                                    _p, _f32, _p, _i64, _p, _i64, _p, _p]),
+    "mma_quantize_f8": (_int, [_int, _int, _i64, _i64, _int, _int, _int, _p,
+                               _i64, _p, _i64, _p, _i64, _i64, _p]),
+    "mma_gemm_f8": (_int, [_int, _int, _int, _i64, _i64, _i64, _p, _i64, _p,
+                           _i64, _i64, _p, _i64, _p, _int, _i64, _i64, _p,
+                           _i64, _p, _i64, _p]),
+    "mma_gemm_grouped": (_int, [_int, _int, _i64, _i64, _i64, _i64, _p, _i64,
+                                _p, _i64, _i64, _int, _p, _p, _i64, _p, _i64,
+                                _p]),
+    "mma_gemm_grouped_wgrad": (_int, [_int, _int, _i64, _i64, _i64, _i64, _p,
+                                      _i64, _p, _i64, _p, _p, _i64, _i64, _p,
+                                      _i64, _i64, _p]),
+    "mma_gemm_grouped_f8": (_int, [_int, _int, _int, _i64, _i64, _i64, _i64,
+                                   _p, _i64, _p, _i64, _i64, _p, _i64, _i64,
+                                   _p, _int, _i64, _i64, _i64, _p, _p, _i64,
+                                   _p, _i64, _p]),
     "mma_device_status": (_int, [_p]),
     "mma_selftest_wait_timeout": (_int, [_i64, _p]),
     "mma_selftest_gemm_abort": (_int, [_int, _i64, _p, _p, _p, _p]),
@@ -314,6 +337,327 @@ def gemm_batched(A, B, C=None, D=None, *, group: int = 1, abid: int = 0,
                              D.data_ptr(), N, batch, group, abid, blgp,
                              _stream(stream))
     _check("mma_gemm_batched_ex", st)
+    return D
+
+
+# --------------------------------------------------------------------------
+# 8-bit operands with scales, products grouped by expert
+
+def _code(dtype):
+    """The ABI's code of a floating-point tensor type (None if it has none)."""
+    torch = _torch()
+    return {torch.float32: MMA_F32, torch.float16: MMA_F16,
+            torch.bfloat16: MMA_BF16, torch.float8_e4m3fn: MMA_F8E4M3,
+            torch.float8_e5m2: MMA_F8E5M2}.get(dtype)
+
+
+def _take(name, t, dtypes, shape):
+    """Check a tensor argument: its type, its shape (None: any extent) and
+    that it is on the GPU."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != g
+                                    for w, g in zip(shape, t.shape)):
+        want = tuple("*" if s is None else s for s in shape)
+        raise ValueError(f"{name} must have shape {want}, not {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t
+
+
+def _rows(name, t) -> int:
+    """Leading dimension of the last two axes: contiguous rows.  A single
+    row has any leading dimension; its own length rounded up to 16 bytes
+    meets every rule."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    if t.shape[-2] > 1:
+        return t.stride(-2)
+    per = 16 // t.element_size()
+    return -(-t.shape[-1] // per) * per
+
+
+def _empty_rows(m, n, dtype, device):
+    """An m x n tensor whose rows start on 16-byte boundaries."""
+    torch = _torch()
+    per = 16 // torch.empty((), dtype=dtype).element_size()
+    return torch.empty((m, -(-n // per) * per), dtype=dtype, device=device)[:, :n]
+
+
+def _empty_scales(rows, blocks, device):
+    """Scales (rows, blocks), the rows of one block side by side."""
+    return _torch().empty((blocks, rows), dtype=_torch().float32,
+                          device=device).t()
+
+
+def _scale_strides(t):
+    """(row, block) strides of a scale tensor, in elements."""
+    return (t.stride(-2) if t.shape[-2] > 1 else 1,
+            t.stride(-1) if t.shape[-1] > 1 else 0)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _addend(name, C, D, shape, out_dtype, device):
+    """C and D of a product: their common type, and D allocated if absent."""
+    torch = _torch()
+    given = D if D is not None else C
+    dtype = given.dtype if given is not None else out_dtype
+    for n, t in ((f"{name}: C", C), (f"{name}: D", D)):
+        if t is not None:
+            _take(n, t, (dtype,), shape)
+    if out_dtype is not None and dtype != out_dtype:
+        raise TypeError(f"{name}: C and D must be of type {out_dtype}")
+    return dtype, (torch.empty(shape, dtype=dtype, device=device)
+                   if D is None else D)
+
+
+def rmsnorm_f8(X, W, residual=None, *, eps: float = 1e-6, pow2: bool = False,
+               y: bool = False, stream=None):
+    """Root-mean-square norm of ``X + residual`` with an 8-bit output.
+
+    ``h = X + residual``, ``y = h * W / sqrt(mean(h**2) + eps)`` per row, and
+    ``y`` in E4M3 with one FP32 scale for each 128 columns (with ``pow2`` a
+    power of two).  ``X``, ``residual``: (M, N) float16, bfloat16 or float32;
+    ``W``: (N,) of that type or float32.  Returns ``(Q, S, H)``: Q (M, N)
+    float8_e4m3fn, S (M, ceil(N / 128)), H the sum in X's type (X itself
+    without a residual); with ``y=True`` also y in X's type.
+    """
+    torch = _torch()
+    kinds = (torch.float16, torch.bfloat16, torch.float32)
+    _take("X", X, kinds, (None, None))
+    M, N = X.shape
+    _take("W", W, (X.dtype, torch.float32), (N,))
+    if W.shape[0] > 1 and W.stride(0) != 1:
+        raise ValueError("W must be contiguous")
+    H = X
+    if residual is not None:
+        _take("residual", residual, (X.dtype,), (M, N))
+        H = _empty_rows(M, N, X.dtype, X.device)
+    Q = _empty_rows(M, N, torch.float8_e4m3fn, X.device)
+    S = _empty_scales(M, -(-N // 128), X.device)
+    Y = _empty_rows(M, N, X.dtype, X.device) if y else None
+    s_row, s_blk = _scale_strides(S)
+    st = load().mma_rmsnorm_f8(
+        _code(X.dtype), _code(W.dtype), M, N, X.data_ptr(), _rows("X", X),
+        _ptr(residual), 0 if residual is None else _rows("residual", residual),
+        W.data_ptr(), eps, int(bool(pow2)),
+        None if residual is None else H.data_ptr(),
+        0 if residual is None else _rows("H", H), _ptr(Y),
+        0 if Y is None else _rows("Y", Y), Q.data_ptr(), _rows("Q", Q),
+        S.data_ptr(), s_row, s_blk, _stream(stream))
+    _check("mma_rmsnorm_f8", st)
+    return (Q, S, H, Y) if y else (Q, S, H)
+
+
+def rmsnorm_backward(dY, H, W, dH=None, *, eps: float = 1e-6, stream=None):
+    """Gradient of the norm of ``rmsnorm_f8`` (taken at the unrounded y).
+
+    ``dY``: gradient of y; ``H``: the sum that the forward returned; ``dH``:
+    gradient that reaches H from elsewhere.  Returns ``(dX, dW)``: dX, the
+    gradient of X and of the residual alike, in H's type, and dW (N,)
+    float32.
+    """
+    torch = _torch()
+    kinds = (torch.float16, torch.bfloat16, torch.float32)
+    _take("H", H, kinds, (None, None))
+    M, N = H.shape
+    _take("dY", dY, (H.dtype,), (M, N))
+    _take("W", W, (H.dtype, torch.float32), (N,))
+    if W.shape[0] > 1 and W.stride(0) != 1:
+        raise ValueError("W must be contiguous")
+    if dH is not None:
+        _take("dH", dH, (H.dtype,), (M, N))
+    dX = _empty_rows(M, N, H.dtype, H.device)
+    dW = torch.empty((N,), dtype=torch.float32, device=H.device)
+    st = load().mma_rmsnorm_backward(
+        _code(H.dtype), _code(W.dtype), M, N, dY.data_ptr(), _rows("dY", dY),
+        H.data_ptr(), _rows("H", H), W.data_ptr(), eps, _ptr(dH),
+        0 if dH is None else _rows("dH", dH), dX.data_ptr(), _rows("dX", dX),
+        dW.data_ptr(), _stream(stream))
+    _check("mma_rmsnorm_backward", st)
+    return dX, dW
+
+
+def quantize_f8(X, *, fmt: str = "e4m3", block_rows: int = 1,
+                transpose: bool = False, pow2: bool = False, stream=None):
+    """``X`` (M, N) in 8-bit floating point with a scale for each block.
+
+    ``fmt``: "e4m3" or "e5m2"; blocks of ``block_rows`` (1 or 128) x 128 of
+    the result, which is X or, with ``transpose``, its transpose (N, M).
+    Returns ``(Q, S)`` with S (ceil(rows / block_rows), ceil(columns / 128)).
+    """
+    torch = _torch()
+    _take("X", X, (torch.float16, torch.bfloat16, torch.float32), (None, None))
+    kinds = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+    if fmt not in kinds:
+        raise ValueError(f"fmt must be e4m3 or e5m2, not {fmt!r}")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    M, N = X.shape
+    m, n = (N, M) if transpose else (M, N)
+    Q = _empty_rows(m, n, kinds[fmt], X.device)
+    S = _empty_scales(-(-m // block_rows), -(-n // 128), X.device)
+    s_row, s_blk = _scale_strides(S)
+    st = load().mma_quantize_f8(
+        _code(X.dtype), _code(kinds[fmt]), M, N, block_rows, int(bool(transpose)),
+        int(bool(pow2)), X.data_ptr(), _rows("X", X), Q.data_ptr(),
+        _rows("Q", Q), S.data_ptr(), s_row, s_blk, _stream(stream))
+    _check("mma_quantize_f8", st)
+    return Q, S
+
+
+def _scale_rows(SB, N):
+    """Rows of B that share a scale, from the scales' shape."""
+    if SB.shape[-2] == N:
+        return 1
+    if SB.shape[-2] == -(-N // 128):
+        return 128
+    raise ValueError(f"SB must have {N} or {-(-N // 128)} rows, not {SB.shape[-2]}")
+
+
+def gemm_f8(A, SA, B, SB, C=None, D=None, *, out_dtype=None, stream=None):
+    """D = A @ B^T + C for 8-bit operands with scales.
+
+    ``A``: (M, K), ``B``: (N, K), each float8_e4m3fn or float8_e5m2;
+    ``SA``: (M, ceil(K / 128)) float32; ``SB``: (N, ceil(K / 128)) or, a scale
+    for each 128 x 128 block, (ceil(N / 128), ceil(K / 128)).  ``C``, ``D``:
+    (M, N) bfloat16, float16 or float32 (``out_dtype``, bfloat16 unless C or D
+    is given).  Any strides of the scales; those of ``quantize_f8`` are read
+    fastest.  Returns D.
+    """
+    torch = _torch()
+    f8 = (torch.float8_e4m3fn, torch.float8_e5m2)
+    _take("A", A, f8, (None, None))
+    M, K = A.shape
+    _take("B", B, f8, (None, K))
+    N = B.shape[0]
+    kb = -(-K // 128)
+    _take("SA", SA, (torch.float32,), (M, kb))
+    _take("SB", SB, (torch.float32,), (None, kb))
+    sb_rows = _scale_rows(SB, N)
+    if out_dtype is None and C is None and D is None:
+        out_dtype = torch.bfloat16
+    dtype, D = _addend("gemm_f8", C, D, (M, N), out_dtype, A.device)
+    st = load().mma_gemm_f8(
+        _code(A.dtype), _code(B.dtype), _code(dtype) or 0, M, N, K,
+        A.data_ptr(), _rows("A", A), SA.data_ptr(), *_scale_strides(SA),
+        B.data_ptr(), _rows("B", B), SB.data_ptr(), sb_rows,
+        *_scale_strides(SB), _ptr(C), 0 if C is None else _rows("C", C),
+        D.data_ptr(), _rows("D", D), _stream(stream))
+    _check("mma_gemm_f8", st)
+    return D
+
+
+def _offsets(offsets, groups):
+    _take("offsets", offsets, (_torch().int32,), (groups + 1,))
+    if not offsets.is_contiguous():
+        raise ValueError("offsets must be contiguous")
+    return offsets.data_ptr()
+
+
+def _slices(name, t) -> int:
+    """Elements between the matrices of a (groups, rows, columns) tensor."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * _rows(name, t)
+
+
+def gemm_grouped(A, B, offsets, C=None, D=None, *, b_layout: str = "col",
+                 out_dtype=None, stream=None):
+    """Products grouped by expert: ``D[i] = A[i] @ B[e]^T + C[i]`` for the rows
+    i in ``[offsets[e], offsets[e + 1])`` of each expert e.
+
+    ``A``: (T, K) float16 or bfloat16, rows sorted by expert; ``B``: (E, N, K),
+    or (E, K, N) with ``b_layout="row"`` (then ``A[i] @ B[e]``: the gradient of
+    the input); ``offsets``: (E + 1,) int32 on the GPU; ``C``, ``D``: (T, N) of
+    A's type or float32 (``out_dtype``, A's unless C or D is given).  Rows of
+    no expert are not written.  Returns D.
+    """
+    torch = _torch()
+    _take("A", A, (torch.float16, torch.bfloat16), (None, None))
+    T, K = A.shape
+    if b_layout not in ("col", "row"):
+        raise ValueError(b_layout)
+    row = b_layout == "row"
+    _take("B", B, (A.dtype,), (None, K, None) if row else (None, None, K))
+    groups, N = B.shape[0], B.shape[2 if row else 1]
+    at = _offsets(offsets, groups)
+    if out_dtype is None and C is None and D is None:
+        out_dtype = A.dtype
+    dtype, D = _addend("gemm_grouped", C, D, (T, N), out_dtype, A.device)
+    st = load().mma_gemm_grouped(
+        _code(A.dtype), _code(dtype) or 0, groups, T, N, K, A.data_ptr(),
+        _rows("A", A), B.data_ptr(), _rows("B", B), _slices("B", B),
+        MMA_ROW_MAJOR if row else MMA_COL_MAJOR, at, _ptr(C),
+        0 if C is None else _rows("C", C), D.data_ptr(), _rows("D", D),
+        _stream(stream))
+    _check("mma_gemm_grouped", st)
+    return D
+
+
+def gemm_grouped_wgrad(dY, X, offsets, C=None, D=None, *, out_dtype=None,
+                       stream=None):
+    """Weight gradient of ``gemm_grouped``: ``D[e] = dY_e^T @ X_e + C[e]`` over
+    the rows of expert e.
+
+    ``dY``: (T, N), ``X``: (T, K), float16 or bfloat16; ``C``, ``D``: (E, N, K)
+    of that type or float32 (``out_dtype``, float32 unless C or D is given;
+    C may be D, to accumulate).  An expert without rows gives C[e], or zeros.
+    Returns D.
+    """
+    torch = _torch()
+    _take("dY", dY, (torch.float16, torch.bfloat16), (None, None))
+    T, N = dY.shape
+    _take("X", X, (dY.dtype,), (T, None))
+    K = X.shape[1]
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must hold one value more than there are experts")
+    groups = offsets.shape[0] - 1
+    at = _offsets(offsets, groups)
+    if out_dtype is None and C is None and D is None:
+        out_dtype = torch.float32
+    dtype, D = _addend("gemm_grouped_wgrad", C, D, (groups, N, K), out_dtype,
+                       dY.device)
+    st = load().mma_gemm_grouped_wgrad(
+        _code(dY.dtype), _code(dtype) or 0, groups, T, N, K, dY.data_ptr(),
+        _rows("dY", dY), X.data_ptr(), _rows("X", X), at, _ptr(C),
+        0 if C is None else _rows("C", C), 0 if C is None else _slices("C", C),
+        D.data_ptr(), _rows("D", D), _slices("D", D), _stream(stream))
+    _check("mma_gemm_grouped_wgrad", st)
+    return D
+
+
+def gemm_grouped_f8(A, SA, B, SB, offsets, C=None, D=None, *, out_dtype=None,
+                    stream=None):
+    """``gemm_grouped`` for 8-bit operands with scales.
+
+    ``A``: (T, K) and ``SA``: (T, ceil(K / 128)) as in ``gemm_f8``; ``B``:
+    (E, N, K); ``SB``: (E, N, ceil(K / 128)) or (E, ceil(N / 128),
+    ceil(K / 128)).  Returns D (T, N), bfloat16 unless given otherwise.
+    """
+    torch = _torch()
+    f8 = (torch.float8_e4m3fn, torch.float8_e5m2)
+    _take("A", A, f8, (None, None))
+    T, K = A.shape
+    _take("B", B, f8, (None, None, K))
+    groups, N = B.shape[:2]
+    kb = -(-K // 128)
+    _take("SA", SA, (torch.float32,), (T, kb))
+    _take("SB", SB, (torch.float32,), (groups, None, kb))
+    sb_rows = _scale_rows(SB, N)
+    at = _offsets(offsets, groups)
+    if out_dtype is None and C is None and D is None:
+        out_dtype = torch.bfloat16
+    dtype, D = _addend("gemm_grouped_f8", C, D, (T, N), out_dtype, A.device)
+    st = load().mma_gemm_grouped_f8(
+        _code(A.dtype), _code(B.dtype), _code(dtype) or 0, groups, T, N, K,
+        A.data_ptr(), _rows("A", A), SA.data_ptr(), *_scale_strides(SA),
+        B.data_ptr(), _rows("B", B), _slices("B", B), SB.data_ptr(), sb_rows,
+        SB.stride(0), *_scale_strides(SB), at, _ptr(C),
+        0 if C is None else _rows("C", C), D.data_ptr(), _rows("D", D),
+        _stream(stream))
+    _check("mma_gemm_grouped_f8", st)
     return D
 
 

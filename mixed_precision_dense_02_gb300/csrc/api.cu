@@ -636,3 +636,326 @@ extern "C" const char* mma_status_string(int status) {
 }
 
 extern "C" int mma_version(void) { return 200; }
+
+// ---------------------------- 8-bit operands and products grouped by expert
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool dim_ok(int64_t d) { return d >= 0 && d <= kMaxDim; }
+
+// Element size of a 16- or 32-bit floating-point type, or 0.
+int64_t float_bytes(int type) {
+  return type == MMA_F32 ? 4 : type == MMA_F16 || type == MMA_BF16 ? 2 : 0;
+}
+
+bool is_f8(int type) { return type == MMA_F8E4M3 || type == MMA_F8E5M2; }
+
+// An input of `rows` rows of `len` elements: 16-byte rows.
+mma_status_t check_in(const void* p, int64_t ld, int64_t len, int64_t eb) {
+  if (p == nullptr || ld < len) return MMA_ERR_INVALID_ARG;
+  return aligned16(p) && ld_ok(ld, eb) ? MMA_OK : MMA_ERR_MISALIGNED;
+}
+
+// An output (or C): rows of `len` elements, aligned to one element.
+mma_status_t check_out(const void* p, int64_t ld, int64_t len, int64_t eb) {
+  if (p == nullptr || ld < len) return MMA_ERR_INVALID_ARG;
+  return (reinterpret_cast<uintptr_t>(p) & uintptr_t(eb - 1)) == 0
+             ? MMA_OK
+             : MMA_ERR_MISALIGNED;
+}
+
+mma_status_t check_scales(const float* s, int64_t row, int64_t blk) {
+  if (s == nullptr || row < 0 || blk < 0) return MMA_ERR_INVALID_ARG;
+  return aligned4(s) ? MMA_OK : MMA_ERR_MISALIGNED;
+}
+
+// D of a product, and C, which may be NULL or D itself.
+mma_status_t check_cd(const void* C, int64_t ldc, const void* D, int64_t ldd,
+                      int64_t len, int64_t eb) {
+  mma_status_t st = check_out(D, ldd, len, eb);
+  if (st != MMA_OK || C == nullptr) return st;
+  if (C == D && ldc != ldd) return MMA_ERR_INVALID_ARG;
+  return check_out(C, ldc, len, eb);
+}
+
+// Slices of `rows` rows of `len` elements, `stride` elements apart.
+bool slices_ok(int64_t groups, int64_t stride, int64_t rows, int64_t ld,
+               int64_t len) {
+  return groups <= 1 || stride >= (rows - 1) * ld + len;
+}
+
+#define MMA_CHECK(expr)                       \
+  do {                                        \
+    const mma_status_t st_ = (expr);          \
+    if (st_ != MMA_OK) return st_;            \
+  } while (0)
+
+mma_status_t gemm_f8(int type_a, int type_b, int type_d, int64_t groups,
+                     int64_t M, int64_t N, int64_t K, const void* A,
+                     int64_t lda, const float* SA, int64_t sa_row,
+                     int64_t sa_blk, const void* B, int64_t ldb,
+                     int64_t stride_b, const float* SB, int sb_rows,
+                     int64_t sb_group, int64_t sb_row, int64_t sb_blk,
+                     bool grouped, const int32_t* offsets, const void* C,
+                     int64_t ldc, void* D, int64_t ldd, void* stream) {
+  const int64_t eb = float_bytes(type_d);
+  if (!is_f8(type_a) || !is_f8(type_b) || eb == 0) return MMA_ERR_UNSUPPORTED;
+  if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K) || groups < 0)
+    return MMA_ERR_INVALID_ARG;
+  if (sb_rows != 1 && sb_rows != 128) return MMA_ERR_INVALID_ARG;
+  if (groups > kMaxGroups) return MMA_ERR_UNSUPPORTED;
+  if (groups == 0 || M == 0 || N == 0) return MMA_OK;
+  if (grouped && offsets == nullptr) return MMA_ERR_INVALID_ARG;
+  if (grouped && !aligned4(offsets)) return MMA_ERR_MISALIGNED;
+  MMA_CHECK(check_cd(C, ldc, D, ldd, N, eb));
+  if (K > 0) {
+    if (sb_group < 0 || !slices_ok(groups, stride_b, N, ldb, K))
+      return MMA_ERR_INVALID_ARG;
+    MMA_CHECK(check_scales(SA, sa_row, sa_blk));
+    MMA_CHECK(check_scales(SB, sb_row, sb_blk));
+    MMA_CHECK(check_in(A, lda, K, 1));
+    MMA_CHECK(check_in(B, ldb, K, 1));
+    if (groups > 1 && !ld_ok(stride_b, 1)) return MMA_ERR_MISALIGNED;
+  }
+  int dev = -1;
+  const DeviceInfo* info = device_info(&dev);
+  if (!info) return MMA_ERR_NO_DEVICE;
+  Ctx ctx = make_ctx(stream, dev, info);
+  attach_profile(ctx);
+  F8Problem f = {};
+  f.a_e5m2 = type_a == MMA_F8E5M2;
+  f.b_e5m2 = type_b == MMA_F8E5M2;
+  f.d_type = type_d;
+  f.groups = groups;
+  f.rows = M;
+  f.N = N;
+  f.K = K;
+  f.A = A;
+  f.lda = lda;
+  f.SA = SA;
+  f.sa_row = sa_row;
+  f.sa_blk = sa_blk;
+  f.B = B;
+  f.ldb = ldb;
+  f.stride_b = stride_b;
+  f.SB = SB;
+  f.sb_rows = sb_rows;
+  f.sb_group = sb_group;
+  f.sb_row = sb_row;
+  f.sb_blk = sb_blk;
+  f.offsets = offsets;
+  f.C = C;
+  f.ldc = ldc;
+  f.D = D;
+  f.ldd = ldd;
+  return launch_gemm_f8(ctx, f);
+}
+
+}  // namespace
+
+extern "C" mma_status_t mma_gemm_f8(
+    int type_a, int type_b, int type_d, int64_t M, int64_t N, int64_t K,
+    const void* A, int64_t lda, const float* SA, int64_t sa_row,
+    int64_t sa_blk, const void* B, int64_t ldb, const float* SB, int sb_rows,
+    int64_t sb_row, int64_t sb_blk, const void* C, int64_t ldc, void* D,
+    int64_t ldd, void* stream) {
+  return gemm_f8(type_a, type_b, type_d, 1, M, N, K, A, lda, SA, sa_row, sa_blk,
+                 B, ldb, 0, SB, sb_rows, 0, sb_row, sb_blk, false, nullptr, C,
+                 ldc, D, ldd, stream);
+}
+
+extern "C" mma_status_t mma_gemm_grouped_f8(
+    int type_a, int type_b, int type_d, int64_t groups, int64_t T, int64_t N,
+    int64_t K, const void* A, int64_t lda, const float* SA, int64_t sa_row,
+    int64_t sa_blk, const void* B, int64_t ldb, int64_t stride_b,
+    const float* SB, int sb_rows, int64_t sb_group, int64_t sb_row,
+    int64_t sb_blk, const int32_t* offsets, const void* C, int64_t ldc, void* D,
+    int64_t ldd, void* stream) {
+  return gemm_f8(type_a, type_b, type_d, groups, T, N, K, A, lda, SA, sa_row,
+                 sa_blk, B, ldb, stride_b, SB, sb_rows, sb_group, sb_row, sb_blk,
+                 true, offsets, C, ldc, D, ldd, stream);
+}
+
+extern "C" mma_status_t mma_gemm_grouped(
+    int type_in, int type_d, int64_t groups, int64_t T, int64_t N, int64_t K,
+    const void* A, int64_t lda, const void* B, int64_t ldb, int64_t stride_b,
+    int layout_b, const int32_t* offsets, const void* C, int64_t ldc, void* D,
+    int64_t ldd, void* stream) {
+  if ((type_in != MMA_F16 && type_in != MMA_BF16) ||
+      (type_d != type_in && type_d != MMA_F32))
+    return MMA_ERR_UNSUPPORTED;
+  if (layout_b != MMA_COL_MAJOR && layout_b != MMA_ROW_MAJOR)
+    return MMA_ERR_INVALID_ARG;
+  if (!dim_ok(T) || !dim_ok(N) || !dim_ok(K) || groups < 0)
+    return MMA_ERR_INVALID_ARG;
+  if (groups > kMaxGroups) return MMA_ERR_UNSUPPORTED;
+  if (groups == 0 || T == 0 || N == 0) return MMA_OK;
+  const bool row = layout_b == MMA_ROW_MAJOR;
+  if (offsets == nullptr) return MMA_ERR_INVALID_ARG;
+  if (!aligned4(offsets)) return MMA_ERR_MISALIGNED;
+  MMA_CHECK(check_cd(C, ldc, D, ldd, N, float_bytes(type_d)));
+  if (K > 0) {
+    if (!slices_ok(groups, stride_b, row ? K : N, ldb, row ? N : K))
+      return MMA_ERR_INVALID_ARG;
+    MMA_CHECK(check_in(A, lda, K, 2));
+    MMA_CHECK(check_in(B, ldb, row ? N : K, 2));
+    if (groups > 1 && !ld_ok(stride_b, 2)) return MMA_ERR_MISALIGNED;
+  }
+  int dev = -1;
+  const DeviceInfo* info = device_info(&dev);
+  if (!info) return MMA_ERR_NO_DEVICE;
+  Ctx ctx = make_ctx(stream, dev, info);
+  attach_profile(ctx);
+  GroupedProblem g = {};
+  g.bf16 = type_in == MMA_BF16;
+  g.b_row_major = row;
+  g.d_type = type_d;
+  g.groups = groups;
+  g.rows = T;
+  g.N = N;
+  g.K = K;
+  g.A = A;
+  g.lda = lda;
+  g.B = B;
+  g.ldb = ldb;
+  g.stride_b = stride_b;
+  g.offsets = offsets;
+  g.C = C;
+  g.ldc = ldc;
+  g.D = D;
+  g.ldd = ldd;
+  return launch_gemm_grouped(ctx, g);
+}
+
+extern "C" mma_status_t mma_gemm_grouped_wgrad(
+    int type_in, int type_d, int64_t groups, int64_t T, int64_t N, int64_t K,
+    const void* DY, int64_t lddy, const void* X, int64_t ldx,
+    const int32_t* offsets, const void* C, int64_t ldc, int64_t stride_c,
+    void* D, int64_t ldd, int64_t stride_d, void* stream) {
+  if ((type_in != MMA_F16 && type_in != MMA_BF16) ||
+      (type_d != type_in && type_d != MMA_F32))
+    return MMA_ERR_UNSUPPORTED;
+  if (!dim_ok(T) || !dim_ok(N) || !dim_ok(K) || groups < 0)
+    return MMA_ERR_INVALID_ARG;
+  if (groups > kMaxGroups) return MMA_ERR_UNSUPPORTED;
+  if (groups == 0 || N == 0 || K == 0) return MMA_OK;
+  if (offsets == nullptr) return MMA_ERR_INVALID_ARG;
+  if (!aligned4(offsets)) return MMA_ERR_MISALIGNED;
+  MMA_CHECK(check_cd(C, ldc, D, ldd, K, float_bytes(type_d)));
+  if (!slices_ok(groups, stride_d, N, ldd, K) ||
+      (C != nullptr && !slices_ok(groups, stride_c, N, ldc, K)) ||
+      (C != nullptr && C == D && groups > 1 && stride_c != stride_d))
+    return MMA_ERR_INVALID_ARG;
+  if (T > 0) {
+    MMA_CHECK(check_in(DY, lddy, N, 2));
+    MMA_CHECK(check_in(X, ldx, K, 2));
+  }
+  int dev = -1;
+  const DeviceInfo* info = device_info(&dev);
+  if (!info) return MMA_ERR_NO_DEVICE;
+  Ctx ctx = make_ctx(stream, dev, info);
+  attach_profile(ctx);
+  WgradProblem g = {};
+  g.bf16 = type_in == MMA_BF16;
+  g.d_type = type_d;
+  g.groups = groups;
+  g.rows = T;
+  g.N = N;
+  g.K = K;
+  g.DY = DY;
+  g.lddy = lddy;
+  g.X = X;
+  g.ldx = ldx;
+  g.offsets = offsets;
+  g.C = C;
+  g.ldc = ldc;
+  g.stride_c = stride_c;
+  g.D = D;
+  g.ldd = ldd;
+  g.stride_d = stride_d;
+  return launch_gemm_grouped_wgrad(ctx, g);
+}
+
+extern "C" mma_status_t mma_rmsnorm_f8(
+    int type, int w_type, int64_t M, int64_t N, const void* X, int64_t ldx,
+    const void* R, int64_t ldr, const void* W, float eps, int pow2, void* H,
+    int64_t ldh, void* Y, int64_t ldy, void* Q, int64_t ldq, float* S,
+    int64_t s_row, int64_t s_blk, void* stream) {
+  const int64_t eb = float_bytes(type);
+  if (eb == 0 || (w_type != type && w_type != MMA_F32)) return MMA_ERR_UNSUPPORTED;
+  if (!dim_ok(M) || !dim_ok(N) || !(eps >= 0.f)) return MMA_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return MMA_OK;
+  if (Y == nullptr && Q == nullptr) return MMA_ERR_INVALID_ARG;
+  if ((H != nullptr && H == X && ldh != ldx) ||
+      (H != nullptr && H == R && ldh != ldr))
+    return MMA_ERR_INVALID_ARG;
+  MMA_CHECK(check_in(X, ldx, N, eb));
+  if (R) MMA_CHECK(check_in(R, ldr, N, eb));
+  MMA_CHECK(check_in(W, N, N, 16));
+  if (H) MMA_CHECK(check_in(H, ldh, N, eb));
+  if (Y) MMA_CHECK(check_in(Y, ldy, N, eb));
+  if (Q) {
+    MMA_CHECK(check_scales(S, s_row, s_blk));
+    MMA_CHECK(check_in(Q, ldq, N, 1));
+  }
+  int dev = -1;
+  const DeviceInfo* info = device_info(&dev);
+  if (!info) return MMA_ERR_NO_DEVICE;
+  Ctx ctx = make_ctx(stream, dev, info);
+  return launch_rmsnorm(ctx, NormProblem{type, w_type, M, N, X, ldx, R, ldr, W,
+                                         eps, pow2 != 0, H, ldh, Y, ldy, Q, ldq,
+                                         S, s_row, s_blk});
+}
+
+extern "C" mma_status_t mma_rmsnorm_backward(
+    int type, int w_type, int64_t M, int64_t N, const void* DY, int64_t lddy,
+    const void* H, int64_t ldh, const void* W, float eps, const void* R,
+    int64_t ldr, void* DX, int64_t lddx, float* DW, void* stream) {
+  const int64_t eb = float_bytes(type);
+  if (eb == 0 || (w_type != type && w_type != MMA_F32)) return MMA_ERR_UNSUPPORTED;
+  if (!dim_ok(M) || !dim_ok(N) || !(eps >= 0.f)) return MMA_ERR_INVALID_ARG;
+  if (N == 0) return MMA_OK;
+  if (DW == nullptr) return MMA_ERR_INVALID_ARG;
+  if (!aligned4(DW)) return MMA_ERR_MISALIGNED;
+  if (M > 0) {
+    if ((DX == DY && lddx != lddy) || (R != nullptr && DX == R && lddx != ldr))
+      return MMA_ERR_INVALID_ARG;
+    MMA_CHECK(check_in(DY, lddy, N, eb));
+    MMA_CHECK(check_in(H, ldh, N, eb));
+    MMA_CHECK(check_in(W, N, N, 16));
+    if (R) MMA_CHECK(check_in(R, ldr, N, eb));
+    MMA_CHECK(check_in(DX, lddx, N, eb));
+  }
+  int dev = -1;
+  const DeviceInfo* info = device_info(&dev);
+  if (!info) return MMA_ERR_NO_DEVICE;
+  Ctx ctx = make_ctx(stream, dev, info);
+  const NormBackProblem p = {type, w_type, M, N, DY, lddy, H, ldh, W, eps,
+                             R, ldr, DX, lddx, DW};
+  return with_workspace(ctx, rmsnorm_backward_workspace_bytes(ctx.num_sms, M, N),
+                        [&](void* ws) { return launch_rmsnorm_backward(ctx, p, ws); });
+}
+
+extern "C" mma_status_t mma_quantize_f8(
+    int type, int f8_type, int64_t M, int64_t N, int block_rows, int transpose,
+    int pow2, const void* X, int64_t ldx, void* Q, int64_t ldq, float* S,
+    int64_t s_row, int64_t s_blk, void* stream) {
+  const int64_t eb = float_bytes(type);
+  if (eb == 0 || !is_f8(f8_type)) return MMA_ERR_UNSUPPORTED;
+  if (!dim_ok(M) || !dim_ok(N) || (block_rows != 1 && block_rows != 128))
+    return MMA_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return MMA_OK;
+  MMA_CHECK(check_in(X, ldx, N, eb));
+  MMA_CHECK(check_in(Q, ldq, transpose ? M : N, 1));
+  MMA_CHECK(check_scales(S, s_row, s_blk));
+  int dev = -1;
+  const DeviceInfo* info = device_info(&dev);
+  if (!info) return MMA_ERR_NO_DEVICE;
+  Ctx ctx = make_ctx(stream, dev, info);
+  return launch_quantize_f8(ctx, QuantProblem{type, f8_type == MMA_F8E5M2,
+                                              transpose != 0, pow2 != 0,
+                                              block_rows, M, N, X, ldx, Q, ldq,
+                                              S, s_row, s_blk});
+}

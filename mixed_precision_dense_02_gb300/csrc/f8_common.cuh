@@ -1,0 +1,174 @@
+// What the kernels that make 8-bit operands share: element access by type,
+// the scale of a block and the rounding to 8 bits.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+#include "kernels.h"
+
+namespace mmagb {
+
+constexpr int kScaleBlock = 128;
+
+// A 16-byte vector of T as floats.  kN elements per vector.
+template <class T>
+struct Vec;
+
+template <>
+struct Vec<float> {
+  static constexpr int kN = 4;
+  __device__ static void unpack(const uint4& v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+  }
+  __device__ static uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]),
+                      __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+  __device__ static float one(float v) { return v; }
+  __device__ static float round(float v) { return v; }
+};
+
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  __device__ static void unpack(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ static uint4 pack(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ static float one(__nv_bfloat16 v) { return __bfloat162float(v); }
+  __device__ static __nv_bfloat16 round(float v) { return __float2bfloat16_rn(v); }
+};
+
+template <>
+struct Vec<__half> {
+  static constexpr int kN = 8;
+  __device__ static void unpack(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = p.x;
+      f[2 * i + 1] = p.y;
+    }
+  }
+  __device__ static uint4 pack(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ static float one(__half v) { return __half2float(v); }
+  __device__ static __half round(float v) { return __float2half_rn(v); }
+};
+
+// The 16 bytes of a row's vector `v`.  The last vector of a row may reach
+// past its n elements, but never past the 16-byte chunk that holds its last
+// one, because rows start on 16-byte boundaries; what lies there is cleared.
+template <class T>
+__device__ __forceinline__ void load_row(const T* row, int64_t v, int64_t n,
+                                         float (&f)[Vec<T>::kN]) {
+  constexpr int E = Vec<T>::kN;
+  if (v * E >= n) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) f[j] = 0.f;
+    return;
+  }
+  Vec<T>::unpack(__ldg(reinterpret_cast<const uint4*>(row) + v), f);
+  if ((v + 1) * E > n) {
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (v * E + j >= n) f[j] = 0.f;
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void store_row(T* row, int64_t v, int64_t n,
+                                          const float (&f)[Vec<T>::kN]) {
+  constexpr int E = Vec<T>::kN;
+  if ((v + 1) * E <= n) {
+    *(reinterpret_cast<uint4*>(row) + v) = Vec<T>::pack(f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (v * E + j < n) row[v * E + j] = Vec<T>::round(f[j]);
+  }
+}
+
+// Largest magnitude as the bits of |x|: integer order is the order of the
+// magnitudes, with NaN above infinity, so a NaN among them wins.
+__device__ __forceinline__ uint32_t abs_bits(float x) {
+  return __float_as_uint(x) & 0x7FFFFFFFu;
+}
+
+template <bool E5M2>
+constexpr float f8_max() { return E5M2 ? 57344.f : 448.f; }
+
+// The scale of a block whose largest magnitude has the bits `m`: that over
+// the format's largest value, at least 2^-126 (so that a block of zeros, or
+// of values whose quotient underflows, has a scale that can be divided by).
+// With pow2 it is rounded up to a power of two.  A NaN or infinity in the
+// block makes the scale one.
+template <bool E5M2>
+__device__ __forceinline__ float block_scale(uint32_t m, bool pow2) {
+  float s = __fdiv_rn(__uint_as_float(m), f8_max<E5M2>());
+  if (s < 1.17549435e-38f) s = 1.17549435e-38f;
+  if (pow2) {
+    uint32_t b = __float_as_uint(s);
+    if ((b & 0x7FFFFFu) && b < 0x7F800000u) b = (b + 0x800000u) & 0xFF800000u;
+    s = __uint_as_float(b);
+  }
+  return s;
+}
+
+// Two values, already divided by their scale, in 8 bits (to nearest, ties
+// to even; beyond the largest value that value; NaN stays NaN).
+template <bool E5M2>
+__device__ __forceinline__ uint32_t to_f8x2(float lo, float hi) {
+  return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE,
+                                           E5M2 ? __NV_E5M2 : __NV_E4M3));
+}
+
+// Store E values of vector v of a row in 8 bits, times inv.
+template <bool E5M2, int E>
+__device__ __forceinline__ void store_f8(uint8_t* row, int64_t v, int64_t n,
+                                         const float (&y)[E], float inv) {
+  uint32_t w[E / 4];
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i)
+    w[i] = to_f8x2<E5M2>(y[4 * i] * inv, y[4 * i + 1] * inv) |
+           (to_f8x2<E5M2>(y[4 * i + 2] * inv, y[4 * i + 3] * inv) << 16);
+  if ((v + 1) * E <= n) {
+    if constexpr (E == 8)
+      *reinterpret_cast<uint2*>(row + v * 8) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(row + v * 4) = w[0];
+  } else {
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (v * E + j < n) row[v * E + j] = uint8_t(w[j / 4] >> (8 * (j & 3)));
+  }
+}
+
+}  // namespace mmagb

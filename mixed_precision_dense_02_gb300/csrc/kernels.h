@@ -166,6 +166,123 @@ mma_status_t launch_batched16(const Ctx& ctx, bool bf16, int64_t batch,
                               int group, int abid, int blgp, const void* A,
                               const void* B, const float* C, float* D);
 
+// Most groups of one grouped product (their row ranges sit in shared memory).
+constexpr int kMaxGroups = MMA_MAX_GROUPS;
+
+// 8-bit product (gemm_grouped.cu): rows of A in `groups` groups with a B
+// each (one group without offsets); scales in FP32, strides in elements.
+struct F8Problem {
+  bool a_e5m2, b_e5m2;
+  int d_type;
+  int64_t groups, rows, N, K;
+  const void* A;
+  int64_t lda;
+  const float* SA;
+  int64_t sa_row, sa_blk;
+  const void* B;
+  int64_t ldb, stride_b;
+  const float* SB;
+  int sb_rows;
+  int64_t sb_group, sb_row, sb_blk;
+  const int* offsets;
+  const void* C;
+  int64_t ldc;
+  void* D;
+  int64_t ldd;
+};
+mma_status_t launch_gemm_f8(const Ctx& ctx, const F8Problem& f);
+
+// Grouped FP16/BF16 product, rows of A sorted by group.
+struct GroupedProblem {
+  bool bf16, b_row_major;
+  int d_type;
+  int64_t groups, rows, N, K;
+  const void* A;
+  int64_t lda;
+  const void* B;
+  int64_t ldb, stride_b;
+  const int* offsets;
+  const void* C;
+  int64_t ldc;
+  void* D;
+  int64_t ldd;
+};
+mma_status_t launch_gemm_grouped(const Ctx& ctx, const GroupedProblem& g);
+
+// Its weight gradient: D_e = C_e + DY_e^T X_e over the rows of group e.
+struct WgradProblem {
+  bool bf16;
+  int d_type;
+  int64_t groups, rows, N, K;
+  const void* DY;
+  int64_t lddy;
+  const void* X;
+  int64_t ldx;
+  const int* offsets;
+  const void* C;
+  int64_t ldc, stride_c;
+  void* D;
+  int64_t ldd, stride_d;
+};
+mma_status_t launch_gemm_grouped_wgrad(const Ctx& ctx, const WgradProblem& g);
+
+// Root-mean-square norm with the residual's addition (rmsnorm.cu).  Element
+// types MMA_F16, MMA_BF16, MMA_F32; NULL pointers as in the C ABI.
+struct NormProblem {
+  int type, w_type;
+  int64_t M, N;
+  const void* X;
+  int64_t ldx;
+  const void* R;
+  int64_t ldr;
+  const void* W;
+  float eps;
+  bool pow2;
+  void* H;
+  int64_t ldh;
+  void* Y;
+  int64_t ldy;
+  void* Q;
+  int64_t ldq;
+  float* S;
+  int64_t s_row, s_blk;
+};
+mma_status_t launch_rmsnorm(const Ctx& ctx, const NormProblem& p);
+
+struct NormBackProblem {
+  int type, w_type;
+  int64_t M, N;
+  const void* DY;
+  int64_t lddy;
+  const void* H;
+  int64_t ldh;
+  const void* W;
+  float eps;
+  const void* R;  // gradient of the sum itself, or NULL
+  int64_t ldr;
+  void* DX;
+  int64_t lddx;
+  float* DW;
+};
+size_t rmsnorm_backward_workspace_bytes(int num_sms, int64_t M, int64_t N);
+mma_status_t launch_rmsnorm_backward(const Ctx& ctx, const NormBackProblem& p,
+                                     void* workspace);
+
+// 8-bit quantisation (quantize.cu).
+struct QuantProblem {
+  int type;
+  bool e5m2, transpose, pow2;
+  int block_rows;
+  int64_t M, N;
+  const void* X;
+  int64_t ldx;
+  void* Q;
+  int64_t ldq;
+  float* S;
+  int64_t s_row, s_blk;
+};
+mma_status_t launch_quantize_f8(const Ctx& ctx, const QuantProblem& p);
+
 // Failure-detection self-test of the tcgen05 GEMM itself: a 256 x 256 x
 // 256 BF16 product on single CTAs (cluster 1) or a CTA pair (cluster 2)
 // whose producer issues no loads and whose bounded waits give up after

@@ -435,6 +435,85 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(bool bf16, int m, int n) {
          | (static_cast<uint32_t>(m >> 4) << 24);   // M / 16
 }
 
+// D[tmem] (+)= A[smem] * B[smem], kind::f8f6f4 (8-bit floating-point
+// inputs, FP32 accumulation), K = 32; CL = 2: the pair form.
+template <int CL>
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc,
+                                        uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  if constexpr (CL == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Shared-memory matrix descriptor for an MN-major operand tile of 16-bit
+// elements written by TMA with 128-byte swizzling, box 64 (M or N) x 64
+// (K): 128-byte rows of 64 consecutive M/N elements, one row per k; 8-row
+// atoms 1024 bytes apart along K (stride offset), the next 64 M/N elements
+// one box (8192 bytes) further (leading offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);  // start address
+  d |= static_cast<uint64_t>(8192u >> 4) << 16;          // leading offset
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;          // stride offset
+  d |= static_cast<uint64_t>(1u) << 46;                  // descriptor version
+  d |= static_cast<uint64_t>(2u) << 61;                  // 128-byte swizzle
+  return d;
+}
+
+// Instruction descriptor of tcgen05.mma with FP32 accumulation, without
+// its N field (N / 8 at bit 17).  Formats: kind::f16 0 = F16, 1 = BF16;
+// kind::f8f6f4 0 = E4M3, 1 = E5M2.
+__host__ __device__ constexpr uint32_t idesc_f32(uint32_t fmt_a, uint32_t fmt_b,
+                                                 bool a_mn, bool b_mn, int m) {
+  return (1u << 4) | (fmt_a << 7) | (fmt_b << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// ------------------------------------------------- packed FP32 arithmetic
+
+__device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b,
+                                              uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // -------------------------------------------------------------- mma.sync
 
 // m16n8k16 BF16 x BF16 + F32 -> F32
