@@ -343,75 +343,126 @@ def gemm_batched(A, B, C=None, D=None, *, group: int = 1, abid: int = 0,
 # --------------------------------------------------------------------------
 # 8-bit operands with scales, products grouped by expert
 
-def _code(dtype):
-    """The ABI's code of a floating-point tensor type (None if it has none)."""
-    torch = _torch()
-    return {torch.float32: MMA_F32, torch.float16: MMA_F16,
-            torch.bfloat16: MMA_BF16, torch.float8_e4m3fn: MMA_F8E4M3,
-            torch.float8_e5m2: MMA_F8E5M2}.get(dtype)
+# These calls serve single tokens too, where the kernel takes a few
+# microseconds: what Python does per call is kept short (types looked up in
+# tables, no temporary tensors, the stream's handle without a Stream object).
+
+_KIND = {}
 
 
-def _take(name, t, dtypes, shape):
+def _kinds():
+    """Tensor types: their ABI codes, and the sets that arguments may have."""
+    if not _KIND:
+        torch = _torch()
+        _KIND["wide"] = {torch.float32: MMA_F32, torch.float16: MMA_F16,
+                         torch.bfloat16: MMA_BF16}
+        _KIND["half"] = {torch.float16: MMA_F16, torch.bfloat16: MMA_BF16}
+        _KIND["f8"] = {torch.float8_e4m3fn: MMA_F8E4M3,
+                       torch.float8_e5m2: MMA_F8E5M2}
+        _KIND["scale"] = {torch.float32: MMA_F32}
+        _KIND["offset"] = {torch.int32: MMA_I32}
+        _KIND["fmt"] = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+    return _KIND
+
+
+def _raw_stream(stream, device):
+    """The cudaStream_t of `stream`, or of the device's current stream."""
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(device.index)
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _take(name, t, kinds, *shape):
     """Check a tensor argument: its type, its shape (None: any extent) and
-    that it is on the GPU."""
-    if t.dtype not in dtypes:
+    that it is on the GPU.  Returns the type's ABI code."""
+    code = kinds.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != g
-                                    for w, g in zip(shape, t.shape)):
+    got = t.shape
+    if len(got) != len(shape) or any(w is not None and w != g
+                                     for w, g in zip(shape, got)):
         want = tuple("*" if s is None else s for s in shape)
-        raise ValueError(f"{name} must have shape {want}, not {tuple(t.shape)}")
+        raise ValueError(f"{name} must have shape {want}, not {tuple(got)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t
+    return code
 
 
 def _rows(name, t) -> int:
     """Leading dimension of the last two axes: contiguous rows.  A single
     row has any leading dimension; its own length rounded up to 16 bytes
     meets every rule."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    shape, stride = t.shape, t.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    if t.shape[-2] > 1:
-        return t.stride(-2)
-    per = 16 // t.element_size()
-    return -(-t.shape[-1] // per) * per
+    if shape[-2] > 1:
+        return stride[-2]
+    per = 16 // t.dtype.itemsize
+    return -(-shape[-1] // per) * per
 
 
 def _empty_rows(m, n, dtype, device):
     """An m x n tensor whose rows start on 16-byte boundaries."""
     torch = _torch()
-    per = 16 // torch.empty((), dtype=dtype).element_size()
-    return torch.empty((m, -(-n // per) * per), dtype=dtype, device=device)[:, :n]
+    per = 16 // dtype.itemsize
+    wide = -(-n // per) * per
+    t = torch.empty((m, wide), dtype=dtype, device=device)
+    return t if wide == n else t[:, :n]
 
 
 def _empty_scales(rows, blocks, device):
     """Scales (rows, blocks), the rows of one block side by side."""
-    return _torch().empty((blocks, rows), dtype=_torch().float32,
-                          device=device).t()
+    torch = _torch()
+    return torch.empty_strided((rows, blocks), (1, rows), dtype=torch.float32,
+                               device=device)
 
 
 def _scale_strides(t):
     """(row, block) strides of a scale tensor, in elements."""
-    return (t.stride(-2) if t.shape[-2] > 1 else 1,
-            t.stride(-1) if t.shape[-1] > 1 else 0)
+    shape, stride = t.shape, t.stride()
+    return (stride[-2] if shape[-2] > 1 else 1, stride[-1] if shape[-1] > 1 else 0)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _addend(name, C, D, shape, out_dtype, device):
-    """C and D of a product: their common type, and D allocated if absent."""
-    torch = _torch()
+def _weight(W, X, n):
+    """The ABI code of a norm's weights: of X's type or float32."""
+    kinds = _kinds()["wide"]
+    code = _take("W", W, kinds, n)
+    if code != MMA_F32 and W.dtype != X.dtype:
+        raise TypeError(f"W must be {X.dtype} or torch.float32, not {W.dtype}")
+    if n > 1 and W.stride(0) != 1:
+        raise ValueError("W must be contiguous")
+    return code
+
+
+def _same(name, t, X, *shape):
+    if t.dtype != X.dtype:
+        raise TypeError(f"{name} must be {X.dtype}, not {t.dtype}")
+    _take(name, t, _kinds()["wide"], *shape)
+
+
+def _result(name, C, D, shape, out_dtype, device):
+    """C and D of a product: their type's code, and D allocated if absent."""
     given = D if D is not None else C
-    dtype = given.dtype if given is not None else out_dtype
-    for n, t in ((f"{name}: C", C), (f"{name}: D", D)):
+    if given is not None:
+        if out_dtype is not None and given.dtype != out_dtype:
+            raise TypeError(f"{name}: C and D must be of type {out_dtype}")
+        out_dtype = given.dtype
+    kinds = _kinds()["wide"]
+    for n, t in (("C", C), ("D", D)):
         if t is not None:
-            _take(n, t, (dtype,), shape)
-    if out_dtype is not None and dtype != out_dtype:
-        raise TypeError(f"{name}: C and D must be of type {out_dtype}")
-    return dtype, (torch.empty(shape, dtype=dtype, device=device)
-                   if D is None else D)
+            if t.dtype != out_dtype:
+                raise TypeError(f"{name}: C and D must have one type")
+            _take(f"{name}: {n}", t, kinds, *shape)
+    code = kinds.get(out_dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported result type {out_dtype}")
+    if D is None:
+        D = _torch().empty(shape, dtype=out_dtype, device=device)
+    return code, D
 
 
 def rmsnorm_f8(X, W, residual=None, *, eps: float = 1e-6, pow2: bool = False,
@@ -425,29 +476,25 @@ def rmsnorm_f8(X, W, residual=None, *, eps: float = 1e-6, pow2: bool = False,
     float8_e4m3fn, S (M, ceil(N / 128)), H the sum in X's type (X itself
     without a residual); with ``y=True`` also y in X's type.
     """
-    torch = _torch()
-    kinds = (torch.float16, torch.bfloat16, torch.float32)
-    _take("X", X, kinds, (None, None))
+    kinds = _kinds()
+    code = _take("X", X, kinds["wide"], None, None)
     M, N = X.shape
-    _take("W", W, (X.dtype, torch.float32), (N,))
-    if W.shape[0] > 1 and W.stride(0) != 1:
-        raise ValueError("W must be contiguous")
-    H = X
+    w_code = _weight(W, X, N)
+    dtype, device = X.dtype, X.device
+    H, h_ptr, ldh, ldr = X, None, 0, 0
     if residual is not None:
-        _take("residual", residual, (X.dtype,), (M, N))
-        H = _empty_rows(M, N, X.dtype, X.device)
-    Q = _empty_rows(M, N, torch.float8_e4m3fn, X.device)
-    S = _empty_scales(M, -(-N // 128), X.device)
-    Y = _empty_rows(M, N, X.dtype, X.device) if y else None
-    s_row, s_blk = _scale_strides(S)
+        _same("residual", residual, X, M, N)
+        ldr = _rows("residual", residual)
+        H = _empty_rows(M, N, dtype, device)
+        h_ptr, ldh = H.data_ptr(), _rows("H", H)
+    Q = _empty_rows(M, N, kinds["fmt"]["e4m3"], device)
+    S = _empty_scales(M, -(-N // 128), device)
+    Y = _empty_rows(M, N, dtype, device) if y else None
     st = load().mma_rmsnorm_f8(
-        _code(X.dtype), _code(W.dtype), M, N, X.data_ptr(), _rows("X", X),
-        _ptr(residual), 0 if residual is None else _rows("residual", residual),
-        W.data_ptr(), eps, int(bool(pow2)),
-        None if residual is None else H.data_ptr(),
-        0 if residual is None else _rows("H", H), _ptr(Y),
+        code, w_code, M, N, X.data_ptr(), _rows("X", X), _ptr(residual), ldr,
+        W.data_ptr(), eps, 1 if pow2 else 0, h_ptr, ldh, _ptr(Y),
         0 if Y is None else _rows("Y", Y), Q.data_ptr(), _rows("Q", Q),
-        S.data_ptr(), s_row, s_blk, _stream(stream))
+        S.data_ptr(), 1, M, _raw_stream(stream, device))
     _check("mma_rmsnorm_f8", st)
     return (Q, S, H, Y) if y else (Q, S, H)
 
@@ -461,22 +508,20 @@ def rmsnorm_backward(dY, H, W, dH=None, *, eps: float = 1e-6, stream=None):
     float32.
     """
     torch = _torch()
-    kinds = (torch.float16, torch.bfloat16, torch.float32)
-    _take("H", H, kinds, (None, None))
+    code = _take("H", H, _kinds()["wide"], None, None)
     M, N = H.shape
-    _take("dY", dY, (H.dtype,), (M, N))
-    _take("W", W, (H.dtype, torch.float32), (N,))
-    if W.shape[0] > 1 and W.stride(0) != 1:
-        raise ValueError("W must be contiguous")
+    _same("dY", dY, H, M, N)
+    w_code = _weight(W, H, N)
     if dH is not None:
-        _take("dH", dH, (H.dtype,), (M, N))
-    dX = _empty_rows(M, N, H.dtype, H.device)
-    dW = torch.empty((N,), dtype=torch.float32, device=H.device)
+        _same("dH", dH, H, M, N)
+    device = H.device
+    dX = _empty_rows(M, N, H.dtype, device)
+    dW = torch.empty((N,), dtype=torch.float32, device=device)
     st = load().mma_rmsnorm_backward(
-        _code(H.dtype), _code(W.dtype), M, N, dY.data_ptr(), _rows("dY", dY),
-        H.data_ptr(), _rows("H", H), W.data_ptr(), eps, _ptr(dH),
+        code, w_code, M, N, dY.data_ptr(), _rows("dY", dY), H.data_ptr(),
+        _rows("H", H), W.data_ptr(), eps, _ptr(dH),
         0 if dH is None else _rows("dH", dH), dX.data_ptr(), _rows("dX", dX),
-        dW.data_ptr(), _stream(stream))
+        dW.data_ptr(), _raw_stream(stream, device))
     _check("mma_rmsnorm_backward", st)
     return dX, dW
 
@@ -489,33 +534,35 @@ def quantize_f8(X, *, fmt: str = "e4m3", block_rows: int = 1,
     the result, which is X or, with ``transpose``, its transpose (N, M).
     Returns ``(Q, S)`` with S (ceil(rows / block_rows), ceil(columns / 128)).
     """
-    torch = _torch()
-    _take("X", X, (torch.float16, torch.bfloat16, torch.float32), (None, None))
-    kinds = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
-    if fmt not in kinds:
+    kinds = _kinds()
+    code = _take("X", X, kinds["wide"], None, None)
+    f8 = kinds["fmt"].get(fmt)
+    if f8 is None:
         raise ValueError(f"fmt must be e4m3 or e5m2, not {fmt!r}")
-    if block_rows not in (1, 128):
+    if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
     M, N = X.shape
     m, n = (N, M) if transpose else (M, N)
-    Q = _empty_rows(m, n, kinds[fmt], X.device)
-    S = _empty_scales(-(-m // block_rows), -(-n // 128), X.device)
-    s_row, s_blk = _scale_strides(S)
+    device = X.device
+    Q = _empty_rows(m, n, f8, device)
+    s_rows = -(-m // block_rows)
+    S = _empty_scales(s_rows, -(-n // 128), device)
     st = load().mma_quantize_f8(
-        _code(X.dtype), _code(kinds[fmt]), M, N, block_rows, int(bool(transpose)),
-        int(bool(pow2)), X.data_ptr(), _rows("X", X), Q.data_ptr(),
-        _rows("Q", Q), S.data_ptr(), s_row, s_blk, _stream(stream))
+        code, kinds["f8"][f8], M, N, block_rows, 1 if transpose else 0,
+        1 if pow2 else 0, X.data_ptr(), _rows("X", X), Q.data_ptr(),
+        _rows("Q", Q), S.data_ptr(), 1, s_rows, _raw_stream(stream, device))
     _check("mma_quantize_f8", st)
     return Q, S
 
 
 def _scale_rows(SB, N):
     """Rows of B that share a scale, from the scales' shape."""
-    if SB.shape[-2] == N:
+    rows = SB.shape[-2]
+    if rows == N:
         return 1
-    if SB.shape[-2] == -(-N // 128):
+    if rows == -(-N // 128):
         return 128
-    raise ValueError(f"SB must have {N} or {-(-N // 128)} rows, not {SB.shape[-2]}")
+    raise ValueError(f"SB must have {N} or {-(-N // 128)} rows, not {rows}")
 
 
 def gemm_f8(A, SA, B, SB, C=None, D=None, *, out_dtype=None, stream=None):
@@ -528,32 +575,32 @@ def gemm_f8(A, SA, B, SB, C=None, D=None, *, out_dtype=None, stream=None):
     is given).  Any strides of the scales; those of ``quantize_f8`` are read
     fastest.  Returns D.
     """
-    torch = _torch()
-    f8 = (torch.float8_e4m3fn, torch.float8_e5m2)
-    _take("A", A, f8, (None, None))
+    kinds = _kinds()
+    f8, scale = kinds["f8"], kinds["scale"]
+    a_code = _take("A", A, f8, None, None)
     M, K = A.shape
-    _take("B", B, f8, (None, K))
+    b_code = _take("B", B, f8, None, K)
     N = B.shape[0]
     kb = -(-K // 128)
-    _take("SA", SA, (torch.float32,), (M, kb))
-    _take("SB", SB, (torch.float32,), (None, kb))
-    sb_rows = _scale_rows(SB, N)
+    _take("SA", SA, scale, M, kb)
+    _take("SB", SB, scale, None, kb)
     if out_dtype is None and C is None and D is None:
-        out_dtype = torch.bfloat16
-    dtype, D = _addend("gemm_f8", C, D, (M, N), out_dtype, A.device)
+        out_dtype = _torch().bfloat16
+    device = A.device
+    d_code, D = _result("gemm_f8", C, D, (M, N), out_dtype, device)
     st = load().mma_gemm_f8(
-        _code(A.dtype), _code(B.dtype), _code(dtype) or 0, M, N, K,
-        A.data_ptr(), _rows("A", A), SA.data_ptr(), *_scale_strides(SA),
-        B.data_ptr(), _rows("B", B), SB.data_ptr(), sb_rows,
-        *_scale_strides(SB), _ptr(C), 0 if C is None else _rows("C", C),
-        D.data_ptr(), _rows("D", D), _stream(stream))
+        a_code, b_code, d_code, M, N, K, A.data_ptr(), _rows("A", A),
+        SA.data_ptr(), *_scale_strides(SA), B.data_ptr(), _rows("B", B),
+        SB.data_ptr(), _scale_rows(SB, N), *_scale_strides(SB), _ptr(C),
+        0 if C is None else _rows("C", C), D.data_ptr(), _rows("D", D),
+        _raw_stream(stream, device))
     _check("mma_gemm_f8", st)
     return D
 
 
 def _offsets(offsets, groups):
-    _take("offsets", offsets, (_torch().int32,), (groups + 1,))
-    if not offsets.is_contiguous():
+    _take("offsets", offsets, _kinds()["offset"], groups + 1)
+    if groups and offsets.stride(0) != 1:
         raise ValueError("offsets must be contiguous")
     return offsets.data_ptr()
 
@@ -574,24 +621,27 @@ def gemm_grouped(A, B, offsets, C=None, D=None, *, b_layout: str = "col",
     A's type or float32 (``out_dtype``, A's unless C or D is given).  Rows of
     no expert are not written.  Returns D.
     """
-    torch = _torch()
-    _take("A", A, (torch.float16, torch.bfloat16), (None, None))
+    code = _take("A", A, _kinds()["half"], None, None)
     T, K = A.shape
     if b_layout not in ("col", "row"):
         raise ValueError(b_layout)
     row = b_layout == "row"
-    _take("B", B, (A.dtype,), (None, K, None) if row else (None, None, K))
+    if row:
+        _same("B", B, A, None, K, None)
+    else:
+        _same("B", B, A, None, None, K)
     groups, N = B.shape[0], B.shape[2 if row else 1]
     at = _offsets(offsets, groups)
     if out_dtype is None and C is None and D is None:
         out_dtype = A.dtype
-    dtype, D = _addend("gemm_grouped", C, D, (T, N), out_dtype, A.device)
+    device = A.device
+    d_code, D = _result("gemm_grouped", C, D, (T, N), out_dtype, device)
     st = load().mma_gemm_grouped(
-        _code(A.dtype), _code(dtype) or 0, groups, T, N, K, A.data_ptr(),
-        _rows("A", A), B.data_ptr(), _rows("B", B), _slices("B", B),
+        code, d_code, groups, T, N, K, A.data_ptr(), _rows("A", A),
+        B.data_ptr(), _rows("B", B), _slices("B", B),
         MMA_ROW_MAJOR if row else MMA_COL_MAJOR, at, _ptr(C),
         0 if C is None else _rows("C", C), D.data_ptr(), _rows("D", D),
-        _stream(stream))
+        _raw_stream(stream, device))
     _check("mma_gemm_grouped", st)
     return D
 
@@ -606,24 +656,25 @@ def gemm_grouped_wgrad(dY, X, offsets, C=None, D=None, *, out_dtype=None,
     C may be D, to accumulate).  An expert without rows gives C[e], or zeros.
     Returns D.
     """
-    torch = _torch()
-    _take("dY", dY, (torch.float16, torch.bfloat16), (None, None))
+    code = _take("dY", dY, _kinds()["half"], None, None)
     T, N = dY.shape
-    _take("X", X, (dY.dtype,), (T, None))
+    _same("X", X, dY, T, None)
     K = X.shape[1]
     if offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must hold one value more than there are experts")
     groups = offsets.shape[0] - 1
     at = _offsets(offsets, groups)
     if out_dtype is None and C is None and D is None:
-        out_dtype = torch.float32
-    dtype, D = _addend("gemm_grouped_wgrad", C, D, (groups, N, K), out_dtype,
-                       dY.device)
+        out_dtype = _torch().float32
+    device = dY.device
+    d_code, D = _result("gemm_grouped_wgrad", C, D, (groups, N, K), out_dtype,
+                        device)
     st = load().mma_gemm_grouped_wgrad(
-        _code(dY.dtype), _code(dtype) or 0, groups, T, N, K, dY.data_ptr(),
-        _rows("dY", dY), X.data_ptr(), _rows("X", X), at, _ptr(C),
+        code, d_code, groups, T, N, K, dY.data_ptr(), _rows("dY", dY),
+        X.data_ptr(), _rows("X", X), at, _ptr(C),
         0 if C is None else _rows("C", C), 0 if C is None else _slices("C", C),
-        D.data_ptr(), _rows("D", D), _slices("D", D), _stream(stream))
+        D.data_ptr(), _rows("D", D), _slices("D", D),
+        _raw_stream(stream, device))
     _check("mma_gemm_grouped_wgrad", st)
     return D
 
@@ -636,27 +687,26 @@ def gemm_grouped_f8(A, SA, B, SB, offsets, C=None, D=None, *, out_dtype=None,
     (E, N, K); ``SB``: (E, N, ceil(K / 128)) or (E, ceil(N / 128),
     ceil(K / 128)).  Returns D (T, N), bfloat16 unless given otherwise.
     """
-    torch = _torch()
-    f8 = (torch.float8_e4m3fn, torch.float8_e5m2)
-    _take("A", A, f8, (None, None))
+    kinds = _kinds()
+    f8, scale = kinds["f8"], kinds["scale"]
+    a_code = _take("A", A, f8, None, None)
     T, K = A.shape
-    _take("B", B, f8, (None, None, K))
-    groups, N = B.shape[:2]
+    b_code = _take("B", B, f8, None, None, K)
+    groups, N = B.shape[0], B.shape[1]
     kb = -(-K // 128)
-    _take("SA", SA, (torch.float32,), (T, kb))
-    _take("SB", SB, (torch.float32,), (groups, None, kb))
-    sb_rows = _scale_rows(SB, N)
+    _take("SA", SA, scale, T, kb)
+    _take("SB", SB, scale, groups, None, kb)
     at = _offsets(offsets, groups)
     if out_dtype is None and C is None and D is None:
-        out_dtype = torch.bfloat16
-    dtype, D = _addend("gemm_grouped_f8", C, D, (T, N), out_dtype, A.device)
+        out_dtype = _torch().bfloat16
+    device = A.device
+    d_code, D = _result("gemm_grouped_f8", C, D, (T, N), out_dtype, device)
     st = load().mma_gemm_grouped_f8(
-        _code(A.dtype), _code(B.dtype), _code(dtype) or 0, groups, T, N, K,
-        A.data_ptr(), _rows("A", A), SA.data_ptr(), *_scale_strides(SA),
-        B.data_ptr(), _rows("B", B), _slices("B", B), SB.data_ptr(), sb_rows,
-        SB.stride(0), *_scale_strides(SB), at, _ptr(C),
-        0 if C is None else _rows("C", C), D.data_ptr(), _rows("D", D),
-        _stream(stream))
+        a_code, b_code, d_code, groups, T, N, K, A.data_ptr(), _rows("A", A),
+        SA.data_ptr(), *_scale_strides(SA), B.data_ptr(), _rows("B", B),
+        _slices("B", B), SB.data_ptr(), _scale_rows(SB, N), SB.stride(0),
+        *_scale_strides(SB), at, _ptr(C), 0 if C is None else _rows("C", C),
+        D.data_ptr(), _rows("D", D), _raw_stream(stream, device))
     _check("mma_gemm_grouped_f8", st)
     return D
 

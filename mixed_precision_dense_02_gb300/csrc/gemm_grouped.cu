@@ -1,33 +1,40 @@
 // Products with scaled 8-bit operands and products grouped by expert, on
 // the tcgen05 tensor cores.  One kernel carries all of them:
 //
-//     D_e[q][p] = C_e[q][p] + sum_k Q_e[q][k] * P_e[p][k]
+//     D[q][p] or D[p][q] = C + sum_k P[p][k] * Q[q][k]
 //
-// with P the operand whose 128 rows fill the tensor core's M side and whose
-// index p is the contiguous one of D, and Q the operand on the N side:
+// with P the operand on the tensor core's M side (128 rows per CTA) and Q
+// the one on its N side:
 //
-//   call                      P (rows p)        Q (rows q)       k
-//   8-bit product             B (N x K)         A (M x K)        K
-//   grouped forward           B_e (N x K)       A (token x K)    K
-//   grouped, row-major B      B_e (K x N)^T     A (token x K)    K
-//   grouped weight gradient   X (token x K)^T   dY (token x N)^T tokens of e
+//   call                          P (rows p)       Q (rows q)       k
+//   grouped forward               B_e (N x K)      A (token x K)    K
+//   grouped, row-major B          B_e (K x N)^T    A (token x K)    K
+//   grouped weight gradient       X (token x K)^T  dY (token x N)^T tokens
+//   8-bit, few rows or scales     B_e (N x K)      A (token x K)    K
+//     of single rows of B
+//   8-bit, many rows (ROWS)       A (token x K)    B_e (N x K)      K
 //
-// so D's rows leave the kernel as runs of consecutive p, one per lane, and
-// the ragged dimension of a group (its tokens) is the N side, whose extent
-// is chosen per tile in steps of 16: a group of 300 tokens costs 304 rows of
-// tensor work, not 384.
+// In all but the last D's rows leave the kernel as runs of consecutive p,
+// one per lane, and the ragged dimension of a group (its tokens) is the N
+// side, whose extent is chosen per tile in steps of 16 (32 with CTA pairs):
+// a group of 300 tokens costs 320 rows of tensor work, not 384 or 512.  With
+// ROWS a lane holds one token, so that both scales of an 8-bit block product
+// are one number per lane.
 //
 // Arithmetic.  The tensor core's FP32 sums drop low bits on the way (a
-// relative error that grows with the length of the sum, 1.2e-7 at 128 terms
+// relative error that grows with the length of the sum: 1.2e-7 at 128 terms
 // and 4.2e-6 at 4096, measured against 64 bits), so K is cut into chunks;
 // each chunk's sum is added to FP32 registers, rounded to nearest.  With
 // 8-bit operands a chunk is one block of 128 and the addition multiplies by
-// the block's two scales: acc += (sp * sq) * t.
+// the product of the block's two scales: acc += (sp * sq) * t.
 //
-// Roles, as in the dense kernel: warp 0 loads operand boxes by TMA into a
-// ring of stages of 128 bytes of k, warp 1 issues the MMAs into two
-// accumulators in tensor memory, eight warps add the chunks up in registers
-// and store D.
+// Roles: warp 0 loads operand boxes by TMA into a ring of stages of 128
+// bytes of k, warp 1 issues the MMAs into two accumulators in tensor memory,
+// eight warps add the chunks up in registers and store D.  CL = 2: a pair of
+// CTAs shares one MMA of 256 rows of P, each staging its own 128 rows and
+// half of Q, so that a stage brings 32 KB per SM instead of 48; every SM
+// streaming from L2 gets about 69 bytes per clock, and the stage's MMAs take
+// 512 clocks.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -43,45 +50,59 @@ namespace {
 
 constexpr int kP = 128;  // rows of P per CTA
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+// One warpgroup for the loads and MMAs (two of its warps idle), two for the
+// epilogue.  384 threads start with 168 registers each; with 128 sums per
+// lane the epilogue takes 224 and leaves the first warpgroup 56
+// (56 + 2 * 224 = 3 * 168): at 168 the sums spill, and a spill is an L2
+// round trip because shared memory leaves no L1 (8-bit 8192 x 8192 x 4096:
+// 1290 us with the spills).
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kLaunchRegs = 168, kLoadRegs = 56, kEpiRegs = 224;
+static_assert(kLoadRegs + 2 * kEpiRegs <= 3 * kLaunchRegs, "registers");
+constexpr int kBand = 16;  // p tiles of a band of the raster
 
-// What a launch computes (see the table above).  Group e's rows of Q are
-// [row[e], row[e + 1]) of `offsets` (one group of q_size rows without
-// offsets); for the weight gradient those are its k range and every group
-// has q_size rows of Q.
+// What a launch computes (see the table above).  Group e's tokens are
+// [row[e], row[e + 1]) of `offsets` (one group of rows_total without
+// offsets): rows of Q, rows of P with ROWS, the k range for the weight
+// gradient.  The sides that no group cuts have p_size and q_size rows.
 struct GroupedArgs {
   int p_size, q_size, k_size, groups, rows_total;
   const int* offsets;
   uint32_t idesc;  // without the N field
   int kb_per_chunk;
   int d_type;  // MMA_F32, MMA_F16 or MMA_BF16
+  int vec4;    // ROWS: four elements of a row of D (and C) can move at once
   const void* C;
   int64_t ldc, c_group;
   void* D;
   int64_t ldd, d_group;
-  // 8-bit operands: the scale of row p (or of the 128 rows around it, with
-  // p_shift = 7) of group e for k block b at sp[e * sp_group +
-  // (p >> p_shift) * sp_row + b * sp_blk]; of row q at sq[q * sq_row + b * sq_blk]
+  // 8-bit operands.  The scale of row p for k block b: sp[e * sp_group +
+  // (p >> p_shift) * sp_row + b * sp_blk]; likewise of row q.
   const float* sp;
   int64_t sp_group, sp_row, sp_blk;
   int p_shift;
   const float* sq;
-  int64_t sq_row, sq_blk;
+  int64_t sq_group, sq_row, sq_blk;
+  int q_shift;
   unsigned* status;
 };
 
-template <int BN, int STAGES>
+template <bool KIND8, bool ROWS, int CL, int BN, int STAGES>
 struct Layout {
   static constexpr int P_BYTES = kP * 128;
-  static constexpr int Q_BYTES = BN * 128;
+  static constexpr int Q_BYTES = BN / CL * 128;
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
-  static constexpr int SCALE_OFFSET = STAGES * STAGE_BYTES;
-  // q scales of the warp's columns, two buffers per warp
-  static constexpr int SCALE_BYTES = kEpiWarps * 2 * (BN / 2) * 4;
-  static constexpr int BAR_OFFSET = SCALE_OFFSET + SCALE_BYTES;
-  static constexpr int NUM_BARS = 2 * STAGES + 5;
+  // 8-bit: chunks whose scales are fetched at a time
+  static constexpr int G = ROWS ? 4 : 2;
+  // per epilogue warp: staging of 32 rows x 16 columns of FP32 (ROWS), or
+  // the q scales of two sets of G chunks
+  static constexpr int WARP_BYTES =
+      ROWS ? 2048 : KIND8 ? 2 * G * (BN / 2) * 4 : 0;
+  static constexpr int WARP_OFFSET = STAGES * STAGE_BYTES;
+  static constexpr int BAR_OFFSET = WARP_OFFSET + kEpiWarps * WARP_BYTES;
+  static constexpr int NUM_BARS = 3 * STAGES + 5;
   static constexpr int GROUP_OFFSET = BAR_OFFSET + NUM_BARS * 8 + 24;
-  static int alloc(int groups) {
+  static constexpr int alloc(int groups) {
     return GROUP_OFFSET + 2 * (groups + 1) * 4 + 1024;  // base alignment
   }
   static constexpr uint32_t TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
@@ -89,11 +110,11 @@ struct Layout {
 
 // One tile of work.
 struct Tile {
-  int e;         // group
-  int p0;        // first row of P
-  int q0, q1;    // rows of Q (rows of D)
-  int nt;        // MMA N: q1 - q0 rounded up to 16
-  int k0, k1;    // k range
+  int e;       // group
+  int p0, p1;  // rows of P: first of the tile, end of the group's or operand's
+  int q0, q1;  // rows of Q
+  int nt;      // MMA N: q1 - q0 rounded up
+  int k0, k1;  // k range
 };
 
 __device__ __forceinline__ float load_c(const void* c, int64_t i, int t) {
@@ -101,6 +122,51 @@ __device__ __forceinline__ float load_c(const void* c, int64_t i, int t) {
   if (t == MMA_BF16)
     return __bfloat162float(static_cast<const __nv_bfloat16*>(c)[i]);
   return __half2float(static_cast<const __half*>(c)[i]);
+}
+
+__device__ __forceinline__ void store_d(void* d, int64_t i, int t, float v) {
+  if (t == MMA_F32)
+    static_cast<float*>(d)[i] = v;
+  else if (t == MMA_BF16)
+    static_cast<__nv_bfloat16*>(d)[i] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half*>(d)[i] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ float4 load_c4(const void* c, int64_t i, int t) {
+  if (t == MMA_F32)
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(c) + i);
+  const uint2 w =
+      *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(c) + i);
+  float2 lo, hi;
+  if (t == MMA_BF16) {
+    lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
+    hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
+  } else {
+    lo = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+    hi = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+  }
+  return make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+
+__device__ __forceinline__ void store_d4(void* d, int64_t i, int t, float4 v) {
+  if (t == MMA_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(d) + i) = v;
+    return;
+  }
+  uint2 w;
+  if (t == MMA_BF16) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z, v.w);
+    w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                   *reinterpret_cast<const uint32_t*>(&hi));
+  } else {
+    const __half2 lo = __floats2half2_rn(v.x, v.y);
+    const __half2 hi = __floats2half2_rn(v.z, v.w);
+    w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                   *reinterpret_cast<const uint32_t*>(&hi));
+  }
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(d) + i) = w;
 }
 
 // Drain without giving up on the abort flag.
@@ -116,19 +182,39 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity,
   }
 }
 
+// A group that ends inside a stage's k rows: its last MMA step of 16 holds
+// `n` rows of the next group from row `row` on, which become zeros in both
+// operands (in one alone, an infinity in the other would leave NaN).  The
+// stage holds boxes of 64 k rows of 128 bytes: two of P, QR / 64 of Q.
+template <int QR>
+__device__ __forceinline__ void zero_rows(uint8_t* stage, int row, int n, int lane) {
+  const int per_box = n * 8;
+  for (int i = lane; i < (kP + QR) / 64 * per_box; i += 32) {
+    const int box = i / per_box, r = i - box * per_box;
+    *reinterpret_cast<uint4*>(stage + box * 8192 + row * 128 + r * 16) =
+        make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 // KIND8: 8-bit operands with scales, else 16-bit.  P_MN, Q_MN: the operand
 // is stored with its row index contiguous (16-bit only).  RAGK: the groups
-// cut the k range (the weight gradient).
-template <bool KIND8, bool P_MN, bool Q_MN, bool RAGK, int BN, int STAGES>
+// cut the k range (the weight gradient).  ROWS: D[p][q], the groups cut P.
+template <bool KIND8, bool P_MN, bool Q_MN, bool RAGK, bool ROWS, int CL, int BN,
+          int STAGES>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP,
                         const __grid_constant__ CUtensorMap tmQ,
                         const __grid_constant__ GroupedArgs a) {
-  using L = Layout<BN, STAGES>;
+  using L = Layout<KIND8, ROWS, CL, BN, STAGES>;
   constexpr int KE = KIND8 ? 128 : 64;  // k elements per stage
+  constexpr int PT = kP * CL;           // rows of P per tile
+  constexpr int QS = 16 * CL;           // granularity of the MMA's N
   constexpr int HALF = BN / 2;          // most columns of an epilogue warp
   constexpr int CB = HALF < 32 ? HALF : 32;
   constexpr int NB = HALF / CB;
+  constexpr bool kSplitRegs = HALF == 128;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -137,24 +223,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* done = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* cut_ok = done + 1;  // pair, RAGK: rank 1's part of a cut block
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cut_ok + STAGES);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* grow = reinterpret_cast<int*>(smem + L::GROUP_OFFSET);  // groups + 1
   int* gunit = grow + a.groups + 1;                            // groups + 1
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int p_tiles = (a.p_size + kP - 1) / kP;
-  const int q_tiles = (a.q_size + BN - 1) / BN;  // RAGK: per group
+  const int rank = CL > 1 ? int(cluster_ctarank()) : 0;
+  const int p_tiles = (a.p_size + PT - 1) / PT;  // ROWS: of no meaning
+  const int q_tiles = (a.q_size + BN - 1) / BN;  // RAGK, ROWS
 
   if (threadIdx.x == 32) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&cut_ok[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], kEpiWarps);
+      mbar_init(&tempty[i], CL * kEpiWarps);
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -188,7 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       hi = max(hi, row);
       int lo = __shfl_up_sync(0xffffffffu, hi, 1);
       if (lane == 0) lo = row;
-      int n = RAGK ? q_tiles * p_tiles : ((hi - lo + BN - 1) / BN) * p_tiles;
+      int n = RAGK ? q_tiles * p_tiles
+              : ROWS ? ((hi - lo + PT - 1) / PT) * q_tiles
+                     : ((hi - lo + BN - 1) / BN) * p_tiles;
+      if (i >= a.groups) n = 0;
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, n, d);
         if (lane >= d) n += o;
@@ -202,16 +294,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, L::TMEM_COLS);
-    tmem_relinquish();
+    if constexpr (CL == 1) {
+      tmem_alloc(tmem_slot, L::TMEM_COLS);
+      tmem_relinquish();
+    } else {
+      tmem_alloc_pair(tmem_slot, L::TMEM_COLS);
+      tmem_relinquish_pair();
+    }
   }
   tc_fence_before();
+  if constexpr (CL > 1)
+    cluster_sync();  // the peer's barriers exist before anything targets them
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int units = gunit[a.groups];
+  const int first_unit = blockIdx.x / CL;
+  const int unit_step = gridDim.x / CL;
 
-  // Unit u: its group by bisection, then p tiles fastest.
+  // Unit u: its group by bisection; within the group bands of kBand p tiles,
+  // p fastest, so that what runs at one time shares few panels.
   auto decode = [&](int u) {
     int lo = 0, hi = a.groups;
     while (hi - lo > 1) {
@@ -221,29 +323,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     Tile t;
     t.e = lo;
     const int r = u - gunit[lo];
-    const int first = RAGK ? 0 : grow[lo];
-    const int rows = RAGK ? a.q_size : grow[lo + 1] - first;
-    const int tiles = (rows + BN - 1) / BN;
-    // the group's rows are shared out evenly, in steps of 16
-    const int step = ((rows + tiles - 1) / tiles + 15) & ~15;
-    const int qi = r / p_tiles;
-    t.p0 = (r - qi * p_tiles) * kP;
-    t.q0 = first + qi * step;
-    t.q1 = min(t.q0 + step, first + rows);
-    t.nt = (t.q1 - t.q0 + 15) & ~15;
-    t.k0 = RAGK ? grow[lo] : 0;
-    t.k1 = RAGK ? grow[lo + 1] : a.k_size;
+    const int g0 = grow[lo], g1 = grow[lo + 1];
+    const int np = ROWS ? (g1 - g0 + PT - 1) / PT : p_tiles;
+    const int nq = (gunit[lo + 1] - gunit[lo]) / np;
+    const int band = r / (kBand * nq);
+    const int bp = min(np - band * kBand, kBand);
+    const int in = r - band * kBand * nq;
+    const int pi = band * kBand + in % bp, qi = in / bp;
+    if constexpr (ROWS) {
+      t.p0 = g0 + pi * PT;
+      t.p1 = g1;
+      t.q0 = qi * BN;
+      t.q1 = min(t.q0 + BN, a.q_size);
+    } else {
+      t.p0 = pi * PT;
+      t.p1 = a.p_size;
+      // the rows are shared out evenly between the q tiles
+      const int first = RAGK ? 0 : g0;
+      const int rows = RAGK ? a.q_size : g1 - g0;
+      const int step = ((rows + nq - 1) / nq + QS - 1) / QS * QS;
+      t.q0 = first + min(qi * step, rows);
+      t.q1 = first + min(qi * step + step, rows);
+    }
+    t.nt = max((t.q1 - t.q0 + QS - 1) / QS * QS, QS);
+    t.k0 = RAGK ? g0 : 0;
+    t.k1 = RAGK ? g1 : a.k_size;
     return t;
   };
 
+  if (warp < 4) {
+  if constexpr (kSplitRegs) registers_give<kLoadRegs>();
   if (warp == 0) {
     // ------------------------------------------------ TMA producer
     if (elect_one()) {
       int stage = 0;
       uint32_t phase = 0, issued = 0;
+      uint32_t cut_fills = 0;  // parity of the cut fills of each stage
       bool ok = true;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      // the leader CTA's full barriers, which count both CTAs' bytes
+      const uint32_t full_lead =
+          CL > 1 ? mapa_shared(smem_u32(&full[0]), 0) : 0u;
+      for (int u = first_unit; u < units && ok; u += unit_step) {
         const Tile t = decode(u);
+        const int py = t.p0 + rank * kP;
+        const int qy = t.q0 + rank * (t.nt / CL);
         for (int k = t.k0; k < t.k1; k += KE) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.status)) {
             ok = false;
@@ -251,19 +374,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           uint8_t* sp = smem + stage * L::STAGE_BYTES;
           uint8_t* sq = sp + L::P_BYTES;
-          mbar_arrive_expect_tx(&full[stage], L::STAGE_BYTES);
-          if constexpr (P_MN) {
-            for (int i = 0; i < kP / 64; ++i)
-              tma_load_3d(&tmP, &full[stage], sp + i * 8192, t.p0 + 64 * i, k,
-                          RAGK ? 0 : t.e);
+          // A pair's loads complete on the leader's barrier, except those
+          // of a block that a group ends in (cut): there each CTA has to
+          // see its own part land.
+          const bool cut = RAGK && CL > 1 && t.k1 - k < KE;
+          uint32_t bar = 0;
+          if constexpr (CL > 1) {
+            if (rank == 0 || cut)
+              mbar_arrive_expect_tx(&full[stage],
+                                    cut ? L::STAGE_BYTES : CL * L::STAGE_BYTES);
+            bar = cut ? mapa_shared(smem_u32(&full[stage]), rank)
+                      : full_lead + uint32_t(stage) * 8u;
+            if (cut) cut_fills ^= 1u << stage;
           } else {
-            tma_load_3d(&tmP, &full[stage], sp, k, t.p0, t.e);
+            mbar_arrive_expect_tx(&full[stage], L::STAGE_BYTES);
+          }
+          auto load = [&](const CUtensorMap* m, uint8_t* dst, int x, int y, int z) {
+            if constexpr (CL > 1)
+              tma_load_3d_pair(m, bar, dst, x, y, z);
+            else
+              tma_load_3d(m, &full[stage], dst, x, y, z);
+          };
+          const int zp = RAGK || ROWS ? 0 : t.e;
+          const int zq = ROWS ? t.e : 0;
+          if constexpr (P_MN) {
+            for (int i = 0; i < kP / 64; ++i) load(&tmP, sp + i * 8192, py + 64 * i, k, zp);
+          } else {
+            load(&tmP, sp, k, py, zp);
           }
           if constexpr (Q_MN) {
-            for (int i = 0; i < BN / 64; ++i)
-              tma_load_3d(&tmQ, &full[stage], sq + i * 8192, t.q0 + 64 * i, k, 0);
+            for (int i = 0; i < BN / CL / 64; ++i)
+              load(&tmQ, sq + i * 8192, qy + 64 * i, k, zq);
           } else {
-            tma_load_3d(&tmQ, &full[stage], sq, k, t.q0, 0);
+            load(&tmQ, sq, k, qy, zq);
           }
           ++issued;
           if (++stage == STAGES) {
@@ -272,22 +415,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // after an abort, let the loads in flight land before the CTA exits
-      if (!ok)
-        for (int s = 0; s < STAGES; ++s) {
-          const uint32_t fills = issued / STAGES + (uint32_t(s) < issued % STAGES);
-          if (fills) wait_drain(&full[s], (fills - 1) & 1u, a.status);
-        }
+      for (int s = 0; s < STAGES; ++s) {
+        const uint32_t fills = issued / STAGES + (uint32_t(s) < issued % STAGES);
+        if (!fills) continue;
+        // after an abort, let the loads in flight land before the CTA exits
+        if (!ok && rank == 0) wait_drain(&full[s], (fills - 1) & 1u, a.status);
+        if (!ok && rank == 1)
+          wait_drain(&full[s], ~(cut_fills >> s) & 1u, a.status);
+        // with a pair, the last release of each stage is the leader's
+        // commit; wait until it has arrived on this CTA
+        if (CL > 1) wait_drain(&empty[s], (fills - 1) & 1u, a.status);
+      }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------ MMA issuer
     // (the whole warp walks the stages; lane 0 issues)
     int stage = 0;
     uint32_t phase = 0, acc_phase = 0;
+    [[maybe_unused]] uint32_t cut_phase = 0;  // one bit per stage
     int acc = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+    for (int u = first_unit; u < units && ok; u += unit_step) {
       const Tile t = decode(u);
       const uint32_t idesc = a.idesc | (uint32_t(t.nt >> 3) << 17);
       int in_chunk = 0;
@@ -304,23 +453,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int left = t.k1 - k;
         int steps = 4;
         if constexpr (RAGK) {
-          // The group ends inside this block: its last step of 16 holds
-          // rows of the next group, which become zeros in both operands
-          // (in one of them alone, an infinity in the other would leave
-          // NaN).
           if (left < KE) {
             steps = (left + 15) >> 4;
-            const int zrows = steps * 16 - left;
-            const int units16 = zrows * 8;
-            for (int i = lane; i < (kP / 64 + BN / 64) * units16; i += 32) {
-              const int box = i / units16, r = i - box * units16;
-              uint8_t* dst = box < kP / 64 ? sp + box * 8192
-                                           : sp + L::P_BYTES + (box - kP / 64) * 8192;
-              *reinterpret_cast<uint4*>(dst + left * 128 + r * 16) =
-                  make_uint4(0, 0, 0, 0);
+            zero_rows<BN / CL>(sp, left, steps * 16 - left, lane);
+            if constexpr (CL > 1) {
+              ok = mbar_wait_cluster(&cut_ok[stage], (cut_phase >> stage) & 1u,
+                                     abort_flag, a.status);
+              if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+              cut_phase ^= 1u << stage;
             }
-            fence_proxy_async_smem();
-            __syncwarp();
           }
         }
         tc_fence_after();
@@ -338,12 +479,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (RAGK && s >= steps) break;
             const uint32_t accum = (in_chunk != 0 || s != 0) ? 1u : 0u;
             if constexpr (KIND8)
-              umma_f8<1>(d_tmem, dp + s * kStepP, dq + s * kStepQ, idesc, accum);
-            else
+              umma_f8<CL>(d_tmem, dp + s * kStepP, dq + s * kStepQ, idesc, accum);
+            else if constexpr (CL == 1)
               umma_f16(d_tmem, dp + s * kStepP, dq + s * kStepQ, idesc, accum);
+            else
+              umma_f16_pair(d_tmem, dp + s * kStepP, dq + s * kStepQ, idesc, accum);
           }
-          umma_commit(&empty[stage]);
-          if (last) umma_commit(&tfull[acc]);
+          if constexpr (CL == 1) {
+            umma_commit(&empty[stage]);
+            if (last) umma_commit(&tfull[acc]);
+          } else {
+            umma_commit_pair(&empty[stage], 3u);
+            if (last) umma_commit_pair(&tfull[acc], 3u);
+          }
         }
         __syncwarp();
         if (++stage == STAGES) {
@@ -361,69 +509,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Every MMA issued above completes before tensor memory is released.
     if (lane == 0) {
-      umma_commit(done);
+      if constexpr (CL == 1)
+        umma_commit(done);
+      else
+        umma_commit_pair(done, 1u);
       wait_drain(done, 0, a.status);
     }
     __syncwarp();
+  } else if (RAGK && CL > 1 && warp == 1) {
+    // ------------------------------------------------ rank 1's cut blocks
+    // Clears the rows beyond the group in this CTA's part of a stage and
+    // tells the leader, which issues the MMAs that read it.
+    int stage = 0;
+    uint32_t cut_phase = 0;
+    for (int u = first_unit; u < units; u += unit_step) {
+      const Tile t = decode(u);
+      const int blocks = (t.k1 - t.k0 + KE - 1) / KE;
+      const int left = (t.k1 - t.k0) - (blocks - 1) * KE;
+      if (blocks > 0 && left < KE) {
+        const int s = (stage + blocks - 1) % STAGES;
+        const bool ok =
+            mbar_wait(&full[s], (cut_phase >> s) & 1u, abort_flag, a.status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        cut_phase ^= 1u << s;
+        zero_rows<BN / CL>(smem + s * L::STAGE_BYTES, left,
+                           ((left + 15) >> 4) * 16 - left, lane);
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&cut_ok[s]), 0));
+        __syncwarp();
+      }
+      stage = (stage + blocks) % STAGES;
+    }
+  }
   } else {
     // ------------------------------------------------ epilogue warps
-    // A warp owns 32 rows of P (its tensor-memory lane quarter) and every
-    // other block of CB columns.
-    const int ew = warp - 2;
+    // A warp owns 32 rows of P (its tensor-memory lane quarter) and, of the
+    // columns, its half (ROWS) or every other block of CB.
+    if constexpr (kSplitRegs) registers_take<kEpiRegs>();
+    const int ew = warp - 4;
     const int quarter = warp & 3;
     const int h = ew >> 2;
-    float* sqs = reinterpret_cast<float*>(smem + L::SCALE_OFFSET) + ew * 2 * HALF;
+    auto column = [&](int i) { return ROWS ? h * HALF + i * CB : (2 * i + h) * CB; };
+    float* wbuf = reinterpret_cast<float*>(smem + L::WARP_OFFSET + ew * L::WARP_BYTES);
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+    for (int u = first_unit; u < units && ok; u += unit_step) {
+      __syncwarp();
       const Tile t = decode(u);
-      const int p = t.p0 + quarter * 32 + lane;
+      const int pw = t.p0 + rank * kP + quarter * 32;
+      const int p = pw + lane;
       uint64_t sum[HALF / 2];
 #pragma unroll
       for (int j = 0; j < HALF / 2; ++j) sum[j] = 0ull;
       const int num_kb = (t.k1 - t.k0 + KE - 1) / KE;
       const int chunks = (num_kb + a.kb_per_chunk - 1) / a.kb_per_chunk;
-      // 8-bit: the scales of chunk ch (one k block): this lane's row of P
-      // and one column per block of columns
-      [[maybe_unused]] float spv = 0.f, sqv[NB];
-      [[maybe_unused]] auto load_scales = [&](int ch) {
-        spv = 0.f;
-        if (p < a.p_size)
-          spv = __ldg(a.sp + t.e * a.sp_group + (p >> a.p_shift) * a.sp_row +
-                      ch * a.sp_blk);
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          const int q = t.q0 + (2 * i + h) * CB + lane;
-          sqv[i] = 0.f;
-          if (lane < CB && q < t.q1) sqv[i] = __ldg(a.sq + q * a.sq_row + ch * a.sq_blk);
-        }
-      };
-      if constexpr (KIND8)
-        if (chunks > 0) load_scales(0);
-      for (int ch = 0; ch < chunks; ++ch) {
-        [[maybe_unused]] float* buf = sqs + (ch & 1) * HALF;
-        [[maybe_unused]] uint64_t sp2 = 0;
-        if constexpr (KIND8) {
-          if (lane < CB) {
-#pragma unroll
-            for (int i = 0; i < NB; ++i) buf[i * CB + lane] = sqv[i];
-          }
-          sp2 = pack_f32x2(__float_as_uint(spv), __float_as_uint(spv));
-          __syncwarp();
-          if (ch + 1 < chunks) load_scales(ch + 1);
-        }
-        ok = mbar_wait(&tfull[acc], acc_phase, abort_flag, a.status);
-        if (!__all_sync(0xffffffffu, ok)) {
+      // Wait for chunk sums in tensor memory, add them (through `add`, for
+      // each block of columns) and return the accumulator.
+      auto take = [&](auto&& add) {
+        const bool got = mbar_wait(&tfull[acc], acc_phase, abort_flag, a.status);
+        if (!__all_sync(0xffffffffu, got)) {
           ok = false;
-          break;
+          return;
         }
         tc_fence_after();
         const uint32_t taddr =
             tmem_base + uint32_t(acc * BN) + (uint32_t(quarter * 32) << 16);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-          const int col = (2 * i + h) * CB;
+          const int col = column(i);
           if (col >= t.nt) continue;
           uint32_t r[CB];
           if constexpr (CB == 32)
@@ -431,70 +584,191 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             tmem_ld_32x32b_x16(taddr + col, r);
           tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < CB; j += 4) {
-            uint64_t& s0 = sum[(i * CB + j) / 2];
-            uint64_t& s1 = sum[(i * CB + j) / 2 + 1];
-            const uint64_t t0 = pack_f32x2(r[j], r[j + 1]);
-            const uint64_t t1 = pack_f32x2(r[j + 2], r[j + 3]);
-            if constexpr (KIND8) {
-              const ulonglong2 v =
-                  *reinterpret_cast<const ulonglong2*>(buf + i * CB + j);
-              s0 = fma_f32x2(mul_f32x2(v.x, sp2), t0, s0);
-              s1 = fma_f32x2(mul_f32x2(v.y, sp2), t1, s1);
-            } else {
-              s0 = add_f32x2(s0, t0);
-              s1 = add_f32x2(s1, t1);
-            }
-          }
+          add(i, r);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[acc]);
+        if (lane == 0) {
+          if constexpr (CL == 1)
+            mbar_arrive(&tempty[acc]);
+          else
+            mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
+        }
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
+      };
+      if constexpr (!KIND8) {
+        for (int ch = 0; ch < chunks && ok; ++ch)
+          take([&](int i, const uint32_t (&r)[CB]) {
+#pragma unroll
+            for (int j = 0; j < CB; j += 2) {
+              uint64_t& s = sum[(i * CB + j) / 2];
+              s = add_f32x2(s, pack_f32x2(r[j], r[j + 1]));
+            }
+          });
+      } else {
+        // The scales of G chunks are fetched while the G before them are
+        // added: this lane's row of P, and one column of Q per block of
+        // columns (ROWS: the scale of the 128 columns around this half).
+        constexpr int G = L::G;
+        constexpr int NQ = ROWS ? 1 : NB;
+        const float* sp = a.sp + (ROWS ? 0 : t.e * a.sp_group) +
+                          (p >> a.p_shift) * a.sp_row;
+        const bool live = p < t.p1;
+        float spc[G], sqc[G][NQ], spn[G], sqn[G][NQ];
+        auto fetch = [&](int ch, float (&fp)[G], float (&fq)[G][NQ]) {
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const bool in = ch + g < chunks;
+            fp[g] = in && live ? __ldg(sp + (ch + g) * a.sp_blk) : 0.f;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+              const int q = ROWS ? t.q0 + h * HALF : t.q0 + column(i) + lane;
+              fq[g][i] = 0.f;
+              if (in && q < t.q1 && (ROWS || lane < CB))
+                fq[g][i] = __ldg(a.sq + (ROWS ? t.e * a.sq_group : 0) +
+                                 (q >> a.q_shift) * a.sq_row + (ch + g) * a.sq_blk);
+            }
+          }
+        };
+        fetch(0, spc, sqc);
+        for (int ch = 0; ch < chunks && ok; ch += G) {
+          float* buf = wbuf + ((ch / G) & 1) * G * HALF;
+          if constexpr (!ROWS) {
+            if (lane < CB) {
+#pragma unroll
+              for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < NB; ++i) buf[g * HALF + i * CB + lane] = sqc[g][i];
+            }
+            __syncwarp();
+          }
+          fetch(ch + G, spn, sqn);
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            if (ch + g >= chunks || !ok) continue;
+            const float s1 = ROWS ? spc[g] * sqc[g][0] : spc[g];
+            const uint64_t s2 = pack_f32x2(__float_as_uint(s1), __float_as_uint(s1));
+            take([&](int i, const uint32_t (&r)[CB]) {
+              if constexpr (ROWS) {
+#pragma unroll
+                for (int j = 0; j < CB; j += 2) {
+                  uint64_t& s = sum[(i * CB + j) / 2];
+                  s = fma_f32x2(s2, pack_f32x2(r[j], r[j + 1]), s);
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < CB; j += 4) {
+                  const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(
+                      buf + g * HALF + i * CB + j);
+                  uint64_t& s0 = sum[(i * CB + j) / 2];
+                  uint64_t& s1 = sum[(i * CB + j) / 2 + 1];
+                  s0 = fma_f32x2(mul_f32x2(v.x, s2), pack_f32x2(r[j], r[j + 1]), s0);
+                  s1 = fma_f32x2(mul_f32x2(v.y, s2), pack_f32x2(r[j + 2], r[j + 3]), s1);
+                }
+              }
+            });
+          }
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            spc[g] = spn[g];
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) sqc[g][i] = sqn[g][i];
+          }
+        }
       }
       if (!ok) break;
-      if (p >= a.p_size) continue;
-      const int64_t group = RAGK ? t.e : 0;
+      if constexpr (ROWS) {
+        // 16 columns at a time through shared memory, so that four lanes
+        // store one row's 16 columns and a warp eight rows
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const int q = t.q0 + (2 * i + h) * CB;
-        if (q >= t.q1) continue;
-        float v[CB];
+        for (int c = 0; c < HALF / 16; ++c) {
+          const int q = t.q0 + h * HALF + c * 16;
+          if (q >= t.q1) continue;
+          __syncwarp();
 #pragma unroll
-        for (int j = 0; j < CB; j += 2)
-          unpack_f32x2(sum[(i * CB + j) / 2], v[j], v[j + 1]);
-        if (a.C) {
-          const int64_t ci = group * a.c_group + int64_t(q) * a.ldc + p;
+          for (int j = 0; j < 4; ++j) {
+            ulonglong2 v;
+            v.x = sum[c * 8 + 2 * j];
+            v.y = sum[c * 8 + 2 * j + 1];
+            *reinterpret_cast<ulonglong2*>(wbuf + lane * 16 +
+                                           ((j ^ ((lane >> 1) & 3)) << 2)) = v;
+          }
+          __syncwarp();
 #pragma unroll
-          for (int j = 0; j < CB; ++j)
-            if (q + j < t.q1) v[j] += load_c(a.C, ci + j * a.ldc, a.d_type);
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2), j = lane & 3;
+            float4 v = *reinterpret_cast<const float4*>(
+                wbuf + r * 16 + ((j ^ ((r >> 1) & 3)) << 2));
+            const int col = q + 4 * j;
+            if (pw + r >= t.p1 || col >= t.q1) continue;
+            const int64_t di = int64_t(pw + r) * a.ldd + col;
+            const int64_t ci = int64_t(pw + r) * a.ldc + col;
+            if (a.vec4 && col + 4 <= t.q1) {
+              if (a.C) {
+                const float4 w = load_c4(a.C, ci, a.d_type);
+                v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+              }
+              store_d4(a.D, di, a.d_type, v);
+            } else {
+              const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (col + x < t.q1)
+                  store_d(a.D, di + x, a.d_type,
+                          f[x] + (a.C ? load_c(a.C, ci + x, a.d_type) : 0.f));
+            }
+          }
         }
-        const int64_t di = group * a.d_group + int64_t(q) * a.ldd + p;
-        if (a.d_type == MMA_F32) {
-          float* d = static_cast<float*>(a.D) + di;
+      } else {
+        if (p >= t.p1) continue;
+        const int64_t group = RAGK ? t.e : 0;
 #pragma unroll
-          for (int j = 0; j < CB; ++j)
-            if (q + j < t.q1) d[j * a.ldd] = v[j];
-        } else if (a.d_type == MMA_BF16) {
-          __nv_bfloat16* d = static_cast<__nv_bfloat16*>(a.D) + di;
+        for (int i = 0; i < NB; ++i) {
+          const int q = t.q0 + column(i);
+          if (q >= t.q1) continue;
+          float v[CB];
 #pragma unroll
-          for (int j = 0; j < CB; ++j)
-            if (q + j < t.q1) d[j * a.ldd] = __float2bfloat16_rn(v[j]);
-        } else {
-          __half* d = static_cast<__half*>(a.D) + di;
+          for (int j = 0; j < CB; j += 2)
+            unpack_f32x2(sum[(i * CB + j) / 2], v[j], v[j + 1]);
+          if (a.C) {
+            const int64_t ci = group * a.c_group + int64_t(q) * a.ldc + p;
 #pragma unroll
-          for (int j = 0; j < CB; ++j)
-            if (q + j < t.q1) d[j * a.ldd] = __float2half_rn(v[j]);
+            for (int j = 0; j < CB; ++j)
+              if (q + j < t.q1) v[j] += load_c(a.C, ci + j * a.ldc, a.d_type);
+          }
+          const int64_t di = group * a.d_group + int64_t(q) * a.ldd + p;
+          if (a.d_type == MMA_F32) {
+            float* d = static_cast<float*>(a.D) + di;
+#pragma unroll
+            for (int j = 0; j < CB; ++j)
+              if (q + j < t.q1) d[j * a.ldd] = v[j];
+          } else if (a.d_type == MMA_BF16) {
+            __nv_bfloat16* d = static_cast<__nv_bfloat16*>(a.D) + di;
+#pragma unroll
+            for (int j = 0; j < CB; ++j)
+              if (q + j < t.q1) d[j * a.ldd] = __float2bfloat16_rn(v[j]);
+          } else {
+            __half* d = static_cast<__half*>(a.D) + di;
+#pragma unroll
+            for (int j = 0; j < CB; ++j)
+              if (q + j < t.q1) d[j * a.ldd] = __float2half_rn(v[j]);
+          }
         }
       }
     }
   }
   tc_fence_before();
+  if constexpr (CL > 1)
+    cluster_sync();  // neither CTA leaves while the other may still signal it
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, L::TMEM_COLS);
+  if (warp == 1) {
+    if constexpr (CL == 1)
+      tmem_dealloc(tmem_base, L::TMEM_COLS);
+    else
+      tmem_dealloc_pair(tmem_base, L::TMEM_COLS);
+  }
 }
 
 // ----------------------------------------------------------------- host
@@ -521,95 +795,144 @@ bool make_map(CUtensorMap* map, const void* base, int elem, int64_t inner,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct Operands {
-  const void* P;
-  int64_t ldp, p_slice;  // p_slice: elements between the groups' P
-  const void* Q;
-  int64_t ldq;
-  int64_t p_rows_total, q_rows_total;  // extents of the maps' rows
+// An operand: K-major (rows of k) or MN-major (k rows), `rows` of them in a
+// slice, `slices` slices.
+struct Operand {
+  const void* p;
+  int64_t ld, rows, slices, slice;
 };
 
-template <bool KIND8, bool P_MN, bool Q_MN, bool RAGK, int BN, int STAGES>
-mma_status_t run(const Ctx& ctx, const Operands& o, const GroupedArgs& a) {
-  using L = Layout<BN, STAGES>;
+template <bool KIND8, bool P_MN, bool Q_MN, bool RAGK, bool ROWS, int CL, int BN,
+          int STAGES>
+mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
+                 const GroupedArgs& a) {
+  using L = Layout<KIND8, ROWS, CL, BN, STAGES>;
   constexpr int EB = KIND8 ? 1 : 2;
   constexpr int KE = KIND8 ? 128 : 64;
-  const int64_t p_tiles = (a.p_size + kP - 1) / kP;
-  const int64_t most =
-      RAGK ? int64_t(a.groups) * ((a.q_size + BN - 1) / BN) * p_tiles
-           : (int64_t(a.rows_total) / BN + (a.offsets ? a.groups : 1)) * p_tiles;
+  constexpr int PT = kP * CL;
+  const int64_t p_tiles = (a.p_size + PT - 1) / PT;
+  const int64_t q_tiles = (a.q_size + BN - 1) / BN;
+  // an upper bound of the units, whatever the offsets
+  const int64_t cuts = a.offsets ? a.groups : 1;
+  const int64_t most = RAGK   ? a.groups * q_tiles * p_tiles
+                       : ROWS ? (a.rows_total / PT + cuts) * q_tiles
+                              : (a.rows_total / BN + cuts) * p_tiles;
   if (most > int64_t(INT32_MAX) / 2) return MMA_ERR_UNSUPPORTED;
+  auto map_of = [&](CUtensorMap* m, const Operand& o, bool mn, int64_t len, int box) {
+    // no k at all (D = C): the kernel loads nothing but wants a valid map
+    if (a.k_size == 0)
+      return make_map(m, reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(a.D) &
+                                                 ~uintptr_t(15)),
+                      EB, 64, 1, 64, 1, 64, 64, 1);
+    const int64_t slice = o.slices > 1 ? o.slice : o.ld;  // unused when 1
+    return mn ? make_map(m, o.p, EB, len, o.rows, o.ld, o.slices, slice, 64, 64)
+              : make_map(m, o.p, EB, a.k_size, o.rows, o.ld, o.slices, slice, KE, box);
+  };
   CUtensorMap tp, tq;
-  bool ok_p, ok_q;
-  if (a.k_size == 0) {
-    // Nothing to load (D = C): the kernel still wants two valid maps.
-    void* any = reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(a.D) & ~uintptr_t(15));
-    ok_p = make_map(&tp, any, EB, 64, 1, 64, 1, 64, 64, 1);
-    tq = tp;
-    ok_q = ok_p;
-  } else {
-    const int64_t slices = RAGK ? 1 : a.groups;
-    const int64_t slice = slices > 1 ? o.p_slice : o.ldp;  // unused when 1
-    ok_p = P_MN ? make_map(&tp, o.P, EB, a.p_size, o.p_rows_total, o.ldp, slices,
-                           slice, 64, 64)
-                : make_map(&tp, o.P, EB, a.k_size, o.p_rows_total, o.ldp, slices,
-                           slice, KE, kP);
-    ok_q = Q_MN ? make_map(&tq, o.Q, EB, a.q_size, o.q_rows_total, o.ldq, 1,
-                           o.ldq, 64, 64)
-                : make_map(&tq, o.Q, EB, a.k_size, o.q_rows_total, o.ldq, 1,
-                           o.ldq, KE, BN);
-  }
-  if (!ok_p || !ok_q) return MMA_ERR_LAUNCH;
-  auto kern = gemm_grouped_kernel<KIND8, P_MN, Q_MN, RAGK, BN, STAGES>;
-  static_assert(L::GROUP_OFFSET + 2 * (kMaxGroups + 1) * 4 + 1024 <= 232448,
-                "shared memory per CTA");
-  static PerContext<bool> attr;
-  bool ok = false;
-  if (!attr.get(ctx, &ok, [&](bool* v) {
-        *v = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  L::alloc(kMaxGroups)) == cudaSuccess;
-        if (!*v) cudaGetLastError();
-        return *v;
+  if (!map_of(&tp, P, P_MN, a.p_size, kP) || !map_of(&tq, Q, Q_MN, a.q_size, BN / CL))
+    return MMA_ERR_LAUNCH;
+  auto kern = gemm_grouped_kernel<KIND8, P_MN, Q_MN, RAGK, ROWS, CL, BN, STAGES>;
+  static_assert(L::alloc(kMaxGroups) <= 232448, "shared memory per CTA");
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = size_t(L::alloc(a.groups));
+  cfg.stream = ctx.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CL;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // clusters resident at once, once per context and instantiation
+  static PerContext<int> resident;
+  int clusters = 0;
+  if (!resident.get(ctx, &clusters, [&](int* v) {
+        bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       L::alloc(kMaxGroups)) == cudaSuccess;
+        // the split of the registers counts on the launch's
+        cudaFuncAttributes fa = {};
+        ok = ok && cudaFuncGetAttributes(&fa, kern) == cudaSuccess &&
+             (BN < 256 || fa.numRegs == kLaunchRegs);
+        *v = ctx.num_sms;
+        if (ok && CL > 1) {
+          cudaLaunchConfig_t probe = cfg;
+          probe.dynamicSmemBytes = size_t(L::alloc(kMaxGroups));
+          probe.gridDim = dim3(unsigned(CL * (ctx.num_sms / CL)), 1, 1);
+          ok = cudaOccupancyMaxActiveClusters(v, kern, &probe) == cudaSuccess && *v > 0;
+        }
+        if (!ok) cudaGetLastError();
+        return ok;
       }))
     return MMA_ERR_LAUNCH;
-  const int grid = int(most < ctx.num_sms ? most : ctx.num_sms);
+  if (clusters > most) clusters = int(most);
+  cfg.gridDim = dim3(unsigned(clusters * CL), 1, 1);
   ctx.mark_start();
-  kern<<<grid, kThreads, L::alloc(a.groups), ctx.stream>>>(tp, tq, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tp, tq, a);
   ctx.mark_stop();
-  return cudaGetLastError() == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
+}
+
+bool elements_aligned(const void* p, int64_t ld, int bytes) {
+  return p == nullptr || ((reinterpret_cast<uintptr_t>(p) & uintptr_t(4 * bytes - 1)) == 0 &&
+                          (ld & 3) == 0);
 }
 
 }  // namespace
 
 mma_status_t launch_gemm_f8(const Ctx& ctx, const F8Problem& f) {
   GroupedArgs a = {};
-  a.p_size = int(f.N);
-  a.q_size = int(f.rows);
   a.k_size = int(f.K);
   a.groups = int(f.groups);
   a.rows_total = int(f.rows);
   a.offsets = f.offsets;
-  a.idesc = idesc_f32(f.b_e5m2, f.a_e5m2, false, false, kP);
   a.kb_per_chunk = 1;
   a.d_type = f.d_type;
   a.C = f.C;
   a.ldc = f.ldc;
   a.D = f.D;
   a.ldd = f.ldd;
+  a.status = ctx.status;
+  const Operand A = {f.A, f.lda, f.rows, 1, 0};
+  const Operand B = {f.B, f.ldb, f.N, f.groups, f.stride_b};
+  const int shift = f.sb_rows == 128 ? 7 : 0;
+  const int64_t per = (f.rows + f.groups - 1) / f.groups;
+  // Many rows: a lane per row of A.  That needs one scale of B for the
+  // columns of a lane's half tile; a tile holds 256 rows of one group.
+  if (shift == 7 && per > 128) {
+    const int db = f.d_type == MMA_F32 ? 4 : 2;
+    a.p_size = int(f.rows);
+    a.q_size = int(f.N);
+    a.vec4 = elements_aligned(f.D, f.ldd, db) && elements_aligned(f.C, f.ldc, db);
+    a.idesc = idesc_f32(f.a_e5m2, f.b_e5m2, false, false, 2 * kP);
+    a.sp = f.SA;
+    a.sp_row = f.sa_row;
+    a.sp_blk = f.sa_blk;
+    a.sq = f.SB;
+    a.sq_group = f.sb_group;
+    a.sq_row = f.sb_row;
+    a.sq_blk = f.sb_blk;
+    a.q_shift = 7;
+    return run<true, false, false, false, true, 2, 256, 6>(ctx, A, B, a);
+  }
+  a.p_size = int(f.N);
+  a.q_size = int(f.rows);
   a.sp = f.SB;
   a.sp_group = f.sb_group;
   a.sp_row = f.sb_row;
   a.sp_blk = f.sb_blk;
-  a.p_shift = f.sb_rows == 128 ? 7 : 0;
+  a.p_shift = shift;
   a.sq = f.SA;
   a.sq_row = f.sa_row;
   a.sq_blk = f.sa_blk;
-  a.status = ctx.status;
-  const Operands o = {f.B, f.ldb, f.stride_b, f.A, f.lda, f.N, f.rows};
-  const int64_t per = (f.rows + f.groups - 1) / f.groups;
-  if (per <= 32) return run<true, false, false, false, 32, 8>(ctx, o, a);
-  if (per <= 128) return run<true, false, false, false, 128, 6>(ctx, o, a);
-  return run<true, false, false, false, 256, 4>(ctx, o, a);
+  if (per > 128) {
+    a.idesc = idesc_f32(f.b_e5m2, f.a_e5m2, false, false, 2 * kP);
+    return run<true, false, false, false, false, 2, 256, 6>(ctx, B, A, a);
+  }
+  a.idesc = idesc_f32(f.b_e5m2, f.a_e5m2, false, false, kP);
+  if (per <= 32) return run<true, false, false, false, false, 1, 32, 8>(ctx, B, A, a);
+  return run<true, false, false, false, false, 1, 128, 6>(ctx, B, A, a);
 }
 
 mma_status_t launch_gemm_grouped(const Ctx& ctx, const GroupedProblem& g) {
@@ -627,17 +950,18 @@ mma_status_t launch_gemm_grouped(const Ctx& ctx, const GroupedProblem& g) {
   a.D = g.D;
   a.ldd = g.ldd;
   a.status = ctx.status;
-  a.idesc = idesc_f32(g.bf16, g.bf16, g.b_row_major, false, kP);
   const int64_t per = (g.rows + g.groups - 1) / g.groups;
-  const Operands o = {g.B, g.ldb, g.stride_b, g.A, g.lda,
-                      g.b_row_major ? g.K : g.N, g.rows};
+  const Operand A = {g.A, g.lda, g.rows, 1, 0};
+  const Operand B = {g.B, g.ldb, g.b_row_major ? g.K : g.N, g.groups, g.stride_b};
+  const bool pair = per > 128;
+  a.idesc = idesc_f32(g.bf16, g.bf16, g.b_row_major, false, pair ? 2 * kP : kP);
   if (g.b_row_major) {
-    if (per <= 128) return run<false, true, false, false, 128, 6>(ctx, o, a);
-    return run<false, true, false, false, 256, 4>(ctx, o, a);
+    if (pair) return run<false, true, false, false, false, 2, 256, 6>(ctx, B, A, a);
+    return run<false, true, false, false, false, 1, 128, 6>(ctx, B, A, a);
   }
-  if (per <= 32) return run<false, false, false, false, 32, 8>(ctx, o, a);
-  if (per <= 128) return run<false, false, false, false, 128, 6>(ctx, o, a);
-  return run<false, false, false, false, 256, 4>(ctx, o, a);
+  if (pair) return run<false, false, false, false, false, 2, 256, 6>(ctx, B, A, a);
+  if (per <= 32) return run<false, false, false, false, false, 1, 32, 8>(ctx, B, A, a);
+  return run<false, false, false, false, false, 1, 128, 6>(ctx, B, A, a);
 }
 
 mma_status_t launch_gemm_grouped_wgrad(const Ctx& ctx, const WgradProblem& g) {
@@ -657,9 +981,10 @@ mma_status_t launch_gemm_grouped_wgrad(const Ctx& ctx, const WgradProblem& g) {
   a.ldd = g.ldd;
   a.d_group = g.stride_d;
   a.status = ctx.status;
-  a.idesc = idesc_f32(g.bf16, g.bf16, true, true, kP);
-  const Operands o = {g.X, g.ldx, 0, g.DY, g.lddy, g.rows, g.rows};
-  return run<false, true, true, true, 256, 4>(ctx, o, a);
+  a.idesc = idesc_f32(g.bf16, g.bf16, true, true, 2 * kP);
+  const Operand X = {g.X, g.ldx, g.rows, 1, 0};
+  const Operand DY = {g.DY, g.lddy, g.rows, 1, 0};
+  return run<false, true, true, true, false, 2, 256, 6>(ctx, X, DY, a);
 }
 
 }  // namespace mmagb
