@@ -92,15 +92,16 @@ struct Layout {
   static constexpr int P_BYTES = kP * 128;
   static constexpr int Q_BYTES = BN / CL * 128;
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
-  // 8-bit: chunks whose scales are fetched at a time
-  static constexpr int G = ROWS ? 4 : 2;
-  // per epilogue warp: staging of 32 rows x 16 columns of FP32 (ROWS), or
-  // the q scales of two sets of G chunks
-  static constexpr int WARP_BYTES =
-      ROWS ? 2048 : KIND8 ? 2 * G * (BN / 2) * 4 : 0;
-  static constexpr int WARP_OFFSET = STAGES * STAGE_BYTES;
+  // 8-bit: a ring of the chunks' scales, 128 of P, then those of Q (ROWS:
+  // of the two halves of the columns)
+  static constexpr int SLOTS = KIND8 ? 8 : 0;
+  static constexpr int SLOT_FLOATS = kP + (ROWS ? 4 : BN);
+  static constexpr int SCALE_OFFSET = STAGES * STAGE_BYTES;
+  // per epilogue warp: staging of 32 rows x 16 columns of FP32 (ROWS)
+  static constexpr int WARP_BYTES = ROWS ? 2048 : 0;
+  static constexpr int WARP_OFFSET = SCALE_OFFSET + SLOTS * SLOT_FLOATS * 4;
   static constexpr int BAR_OFFSET = WARP_OFFSET + kEpiWarps * WARP_BYTES;
-  static constexpr int NUM_BARS = 3 * STAGES + 5;
+  static constexpr int NUM_BARS = 4 * STAGES + 5 + 2 * SLOTS;
   static constexpr int GROUP_OFFSET = BAR_OFFSET + NUM_BARS * 8 + 24;
   static constexpr int alloc(int groups) {
     return GROUP_OFFSET + 2 * (groups + 1) * 4 + 1024;  // base alignment
@@ -223,8 +224,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* done = tempty + 2;
-  uint64_t* cut_ok = done + 1;  // pair, RAGK: rank 1's part of a cut block
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cut_ok + STAGES);
+  uint64_t* cut_in = done + 1;         // RAGK: a cut block has landed here
+  uint64_t* cut_ok = cut_in + STAGES;  // and its zeros are in place (leader)
+  uint64_t* sfull = cut_ok + STAGES;
+  uint64_t* sempty = sfull + L::SLOTS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + L::SLOTS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* grow = reinterpret_cast<int*>(smem + L::GROUP_OFFSET);  // groups + 1
   int* gunit = grow + a.groups + 1;                            // groups + 1
@@ -239,7 +243,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&cut_ok[s], 1);
+      mbar_init(&cut_in[s], 1);
+      mbar_init(&cut_ok[s], CL);
+    }
+    for (int s = 0; s < L::SLOTS; ++s) {
+      mbar_init(&sfull[s], 32);
+      mbar_init(&sempty[s], kEpiWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
@@ -374,26 +383,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           uint8_t* sp = smem + stage * L::STAGE_BYTES;
           uint8_t* sq = sp + L::P_BYTES;
-          // A pair's loads complete on the leader's barrier, except those
-          // of a block that a group ends in (cut): there each CTA has to
-          // see its own part land.
-          const bool cut = RAGK && CL > 1 && t.k1 - k < KE;
-          uint32_t bar = 0;
-          if constexpr (CL > 1) {
-            if (rank == 0 || cut)
-              mbar_arrive_expect_tx(&full[stage],
-                                    cut ? L::STAGE_BYTES : CL * L::STAGE_BYTES);
-            bar = cut ? mapa_shared(smem_u32(&full[stage]), rank)
-                      : full_lead + uint32_t(stage) * 8u;
-            if (cut) cut_fills ^= 1u << stage;
-          } else {
-            mbar_arrive_expect_tx(&full[stage], L::STAGE_BYTES);
+          // A pair's loads complete on the leader's barrier.  Those of a
+          // block that a group ends in (cut) complete on a barrier of each
+          // CTA's own, where its rows beyond the group are cleared.
+          const bool cut = RAGK && t.k1 - k < KE;
+          [[maybe_unused]] uint32_t bar = full_lead + uint32_t(stage) * 8u;
+          if (cut) {
+            if (rank == 0) mbar_arrive(&full[stage]);
+            mbar_arrive_expect_tx(&cut_in[stage], L::STAGE_BYTES);
+            if (CL > 1) bar = mapa_shared(smem_u32(&cut_in[stage]), rank);
+            cut_fills ^= 1u << stage;
+          } else if (rank == 0) {
+            mbar_arrive_expect_tx(&full[stage], CL * L::STAGE_BYTES);
           }
           auto load = [&](const CUtensorMap* m, uint8_t* dst, int x, int y, int z) {
             if constexpr (CL > 1)
               tma_load_3d_pair(m, bar, dst, x, y, z);
             else
-              tma_load_3d(m, &full[stage], dst, x, y, z);
+              tma_load_3d(m, cut ? &cut_in[stage] : &full[stage], dst, x, y, z);
           };
           const int zp = RAGK || ROWS ? 0 : t.e;
           const int zq = ROWS ? t.e : 0;
@@ -420,8 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!fills) continue;
         // after an abort, let the loads in flight land before the CTA exits
         if (!ok && rank == 0) wait_drain(&full[s], (fills - 1) & 1u, a.status);
-        if (!ok && rank == 1)
-          wait_drain(&full[s], ~(cut_fills >> s) & 1u, a.status);
+        if (!ok && RAGK) wait_drain(&cut_in[s], ~(cut_fills >> s) & 1u, a.status);
         // with a pair, the last release of each stage is the leader's
         // commit; wait until it has arrived on this CTA
         if (CL > 1) wait_drain(&empty[s], (fills - 1) & 1u, a.status);
@@ -430,53 +436,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------ MMA issuer
-    // (the whole warp walks the stages; lane 0 issues)
-    int stage = 0;
-    uint32_t phase = 0, acc_phase = 0;
-    [[maybe_unused]] uint32_t cut_phase = 0;  // one bit per stage
-    int acc = 0;
-    bool ok = true;
-    for (int u = first_unit; u < units && ok; u += unit_step) {
-      const Tile t = decode(u);
-      const uint32_t idesc = a.idesc | (uint32_t(t.nt >> 3) << 17);
-      int in_chunk = 0;
-      for (int k = t.k0; k < t.k1; k += KE) {
-        const uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
-        if (in_chunk == 0) {
-          ok = mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, a.status);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          tc_fence_after();
-        }
-        ok = mbar_wait(&full[stage], phase, abort_flag, a.status);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        uint8_t* sp = smem + stage * L::STAGE_BYTES;
-        const int left = t.k1 - k;
-        int steps = 4;
-        if constexpr (RAGK) {
-          if (left < KE) {
-            steps = (left + 15) >> 4;
-            zero_rows<BN / CL>(sp, left, steps * 16 - left, lane);
-            if constexpr (CL > 1) {
+    // One thread.  Issuing waits for room in the tensor pipe, so the next
+    // stage's barrier is looked at before the last MMA of a stage is issued.
+    if (elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      [[maybe_unused]] uint32_t cut_phase = 0;  // one bit per stage
+      int acc = 0;
+      bool ok = true, ready = false;
+      for (int u = first_unit; u < units && ok; u += unit_step) {
+        const Tile t = decode(u);
+        const uint32_t idesc = a.idesc | (uint32_t(t.nt >> 3) << 17);
+        int in_chunk = 0;
+        for (int k = t.k0; k < t.k1; k += KE) {
+          const uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
+          if (in_chunk == 0)
+            ok = mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, a.status);
+          if (ok && !ready) ok = mbar_wait(&full[stage], phase, abort_flag, a.status);
+          const int left = t.k1 - k;
+          int steps = 4;
+          if constexpr (RAGK) {
+            if (ok && left < KE) {
+              steps = (left + 15) >> 4;
               ok = mbar_wait_cluster(&cut_ok[stage], (cut_phase >> stage) & 1u,
                                      abort_flag, a.status);
-              if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
               cut_phase ^= 1u << stage;
             }
           }
-        }
-        tc_fence_after();
-        const bool last = in_chunk + 1 == a.kb_per_chunk || left <= KE;
-        if (lane == 0) {
-          const uint32_t sa = smem_u32(sp);
+          if (!ok) break;
+          tc_fence_after();
+          const bool last = in_chunk + 1 == a.kb_per_chunk || left <= KE;
+          const uint32_t sa = smem_u32(smem + stage * L::STAGE_BYTES);
           const uint64_t dp = P_MN ? sw128_mnmajor_desc(sa) : sw128_kmajor_desc(sa);
           const uint64_t dq = Q_MN ? sw128_mnmajor_desc(sa + L::P_BYTES)
                                    : sw128_kmajor_desc(sa + L::P_BYTES);
           // 32 bytes of a row (K-major) or 16 rows (MN-major) per step
           constexpr uint64_t kStepP = P_MN ? 128 : 2;
           constexpr uint64_t kStepQ = Q_MN ? 128 : 2;
+          const int next = stage + 1 == STAGES ? 0 : stage + 1;
+          const uint32_t next_phase = next ? phase : phase ^ 1u;
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            if (RAGK && s >= steps) break;
+            if (s == 3) ready = mbar_test(&full[next], next_phase);
+            if (RAGK && s >= steps) continue;
             const uint32_t accum = (in_chunk != 0 || s != 0) ? 1u : 0u;
             if constexpr (KIND8)
               umma_f8<CL>(d_tmem, dp + s * kStepP, dq + s * kStepQ, idesc, accum);
@@ -492,23 +494,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit_pair(&empty[stage], 3u);
             if (last) umma_commit_pair(&tfull[acc], 3u);
           }
-        }
-        __syncwarp();
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-        if (last) {
-          in_chunk = 0;
-          acc ^= 1;
-          if (acc == 0) acc_phase ^= 1u;
-        } else {
-          ++in_chunk;
+          stage = next;
+          phase = next_phase;
+          if (last) {
+            in_chunk = 0;
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+          } else {
+            ++in_chunk;
+          }
         }
       }
-    }
-    // Every MMA issued above completes before tensor memory is released.
-    if (lane == 0) {
+      // Every MMA issued above completes before tensor memory is released.
       if constexpr (CL == 1)
         umma_commit(done);
       else
@@ -516,12 +513,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_drain(done, 0, a.status);
     }
     __syncwarp();
-  } else if (RAGK && CL > 1 && warp == 1) {
-    // ------------------------------------------------ rank 1's cut blocks
+  } else if (RAGK && warp == 2) {
+    // ------------------------------------------------ cut blocks
     // Clears the rows beyond the group in this CTA's part of a stage and
     // tells the leader, which issues the MMAs that read it.
     int stage = 0;
-    uint32_t cut_phase = 0;
+    uint32_t cut_phase = 0;  // one bit per stage
     for (int u = first_unit; u < units; u += unit_step) {
       const Tile t = decode(u);
       const int blocks = (t.k1 - t.k0 + KE - 1) / KE;
@@ -529,16 +526,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (blocks > 0 && left < KE) {
         const int s = (stage + blocks - 1) % STAGES;
         const bool ok =
-            mbar_wait(&full[s], (cut_phase >> s) & 1u, abort_flag, a.status);
+            mbar_wait(&cut_in[s], (cut_phase >> s) & 1u, abort_flag, a.status);
         if (!__all_sync(0xffffffffu, ok)) break;
         cut_phase ^= 1u << s;
         zero_rows<BN / CL>(smem + s * L::STAGE_BYTES, left,
                            ((left + 15) >> 4) * 16 - left, lane);
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&cut_ok[s]), 0));
+        if (lane == 0) {
+          if constexpr (CL == 1)
+            mbar_arrive(&cut_ok[s]);
+          else
+            mbar_arrive_cluster(mapa_shared(smem_u32(&cut_ok[s]), 0));
+        }
         __syncwarp();
       }
       stage = (stage + blocks) % STAGES;
     }
+  } else if (KIND8 && warp == 3) {
+    // ------------------------------------------------ scales
+    // Those of each chunk (one k block) by cp.async into a ring, zero beyond
+    // the operands; every lane's copies count as one arrival.
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const float* ring = reinterpret_cast<const float*>(smem + L::SCALE_OFFSET);
+    for (int u = first_unit; u < units && ok; u += unit_step) {
+      const Tile t = decode(u);
+      constexpr int NP = kP / 32, NQ = ROWS ? 1 : BN / 32;
+      const float *src_p[NP], *src_q[NQ];
+      int len_p = 0, len_q = 0;  // one bit each: within the operand
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int p = t.p0 + rank * kP + i * 32 + lane;
+        len_p |= int(p < t.p1) << i;
+        src_p[i] = a.sp + (ROWS ? 0 : t.e * a.sp_group) +
+                   (int64_t(min(p, t.p1 - 1)) >> a.p_shift) * a.sp_row;
+      }
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const int q = ROWS ? t.q0 + lane * HALF : t.q0 + i * 32 + lane;
+        len_q |= int(q < t.q1) << i;
+        src_q[i] = a.sq + (ROWS ? t.e * a.sq_group : 0) +
+                   (int64_t(min(q, t.q1 - 1)) >> a.q_shift) * a.sq_row;
+      }
+      for (int k = t.k0; k < t.k1; k += KE) {
+        ok = mbar_wait(&sempty[slot], phase ^ 1u, abort_flag, a.status);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        const uint32_t dst = smem_u32(ring + slot * L::SLOT_FLOATS);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          cp_async_4_zfill(dst + (i * 32 + lane) * 4, src_p[i], ((len_p >> i) & 1) * 4);
+          src_p[i] += a.sp_blk;
+        }
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          if (!ROWS || lane < 2)
+            cp_async_4_zfill(dst + (kP + i * 32 + lane) * 4, src_q[i],
+                             ((len_q >> i) & 1) * 4);
+          src_q[i] += a.sq_blk;
+        }
+        cp_async_mbar_arrive(&sfull[slot]);
+        if (++slot == L::SLOTS) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    cp_async_commit();
+    cp_async_wait<0>();  // none is in flight when the CTA ends
   }
   } else {
     // ------------------------------------------------ epilogue warps
@@ -549,7 +603,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3;
     const int h = ew >> 2;
     auto column = [&](int i) { return ROWS ? h * HALF + i * CB : (2 * i + h) * CB; };
-    float* wbuf = reinterpret_cast<float*>(smem + L::WARP_OFFSET + ew * L::WARP_BYTES);
+    [[maybe_unused]] float* wbuf =
+        reinterpret_cast<float*>(smem + L::WARP_OFFSET + ew * L::WARP_BYTES);
+    [[maybe_unused]] const float* ring =
+        reinterpret_cast<const float*>(smem + L::SCALE_OFFSET);
+    [[maybe_unused]] int slot = 0;
+    [[maybe_unused]] uint32_t slot_phase = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
@@ -563,8 +622,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < HALF / 2; ++j) sum[j] = 0ull;
       const int num_kb = (t.k1 - t.k0 + KE - 1) / KE;
       const int chunks = (num_kb + a.kb_per_chunk - 1) / a.kb_per_chunk;
-      // Wait for chunk sums in tensor memory, add them (through `add`, for
-      // each block of columns) and return the accumulator.
+      // Wait for a chunk's sums in tensor memory, add them (through `add`,
+      // for each block of columns) and return the accumulator.  The next
+      // block is on its way while one is added.
       auto take = [&](auto&& add) {
         const bool got = mbar_wait(&tfull[acc], acc_phase, abort_flag, a.status);
         if (!__all_sync(0xffffffffu, got)) {
@@ -574,17 +634,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t taddr =
             tmem_base + uint32_t(acc * BN) + (uint32_t(quarter * 32) << 16);
+        uint32_t r[2][CB];
+        auto load = [&](int i) {
+          if (column(i) >= t.nt) return;
+          if constexpr (CB == 32)
+            tmem_ld_32x32b_x32(taddr + column(i), r[i & 1]);
+          else
+            tmem_ld_32x32b_x16(taddr + column(i), r[i & 1]);
+        };
+        load(0);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-          const int col = column(i);
-          if (col >= t.nt) continue;
-          uint32_t r[CB];
-          if constexpr (CB == 32)
-            tmem_ld_32x32b_x32(taddr + col, r);
-          else
-            tmem_ld_32x32b_x16(taddr + col, r);
           tmem_ld_wait();
-          add(i, r);
+          if (i + 1 < NB) load(i + 1);
+          if (column(i) < t.nt) add(i, r[i & 1]);
         }
         tc_fence_before();
         __syncwarp();
@@ -597,8 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       };
-      if constexpr (!KIND8) {
-        for (int ch = 0; ch < chunks && ok; ++ch)
+      for (int ch = 0; ch < chunks && ok; ++ch) {
+        if constexpr (!KIND8) {
           take([&](int i, const uint32_t (&r)[CB]) {
 #pragma unroll
             for (int j = 0; j < CB; j += 2) {
@@ -606,74 +669,36 @@ __global__ void __launch_bounds__(kThreads, 1)
               s = add_f32x2(s, pack_f32x2(r[j], r[j + 1]));
             }
           });
-      } else {
-        // The scales of G chunks are fetched while the G before them are
-        // added: this lane's row of P, and one column of Q per block of
-        // columns (ROWS: the scale of the 128 columns around this half).
-        constexpr int G = L::G;
-        constexpr int NQ = ROWS ? 1 : NB;
-        const float* sp = a.sp + (ROWS ? 0 : t.e * a.sp_group) +
-                          (p >> a.p_shift) * a.sp_row;
-        const bool live = p < t.p1;
-        float spc[G], sqc[G][NQ], spn[G], sqn[G][NQ];
-        auto fetch = [&](int ch, float (&fp)[G], float (&fq)[G][NQ]) {
+        } else {
+          const bool got = mbar_wait(&sfull[slot], slot_phase, abort_flag, a.status);
+          if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+          const float* sc = ring + slot * L::SLOT_FLOATS;
+          float s1 = sc[quarter * 32 + lane];
+          if constexpr (ROWS) s1 *= sc[kP + h];
+          const uint64_t s2 = pack_f32x2(__float_as_uint(s1), __float_as_uint(s1));
+          take([&](int i, const uint32_t (&r)[CB]) {
+            if constexpr (ROWS) {
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            const bool in = ch + g < chunks;
-            fp[g] = in && live ? __ldg(sp + (ch + g) * a.sp_blk) : 0.f;
-#pragma unroll
-            for (int i = 0; i < NQ; ++i) {
-              const int q = ROWS ? t.q0 + h * HALF : t.q0 + column(i) + lane;
-              fq[g][i] = 0.f;
-              if (in && q < t.q1 && (ROWS || lane < CB))
-                fq[g][i] = __ldg(a.sq + (ROWS ? t.e * a.sq_group : 0) +
-                                 (q >> a.q_shift) * a.sq_row + (ch + g) * a.sq_blk);
-            }
-          }
-        };
-        fetch(0, spc, sqc);
-        for (int ch = 0; ch < chunks && ok; ch += G) {
-          float* buf = wbuf + ((ch / G) & 1) * G * HALF;
-          if constexpr (!ROWS) {
-            if (lane < CB) {
-#pragma unroll
-              for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int i = 0; i < NB; ++i) buf[g * HALF + i * CB + lane] = sqc[g][i];
-            }
-            __syncwarp();
-          }
-          fetch(ch + G, spn, sqn);
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            if (ch + g >= chunks || !ok) continue;
-            const float s1 = ROWS ? spc[g] * sqc[g][0] : spc[g];
-            const uint64_t s2 = pack_f32x2(__float_as_uint(s1), __float_as_uint(s1));
-            take([&](int i, const uint32_t (&r)[CB]) {
-              if constexpr (ROWS) {
-#pragma unroll
-                for (int j = 0; j < CB; j += 2) {
-                  uint64_t& s = sum[(i * CB + j) / 2];
-                  s = fma_f32x2(s2, pack_f32x2(r[j], r[j + 1]), s);
-                }
-              } else {
-#pragma unroll
-                for (int j = 0; j < CB; j += 4) {
-                  const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(
-                      buf + g * HALF + i * CB + j);
-                  uint64_t& s0 = sum[(i * CB + j) / 2];
-                  uint64_t& s1 = sum[(i * CB + j) / 2 + 1];
-                  s0 = fma_f32x2(mul_f32x2(v.x, s2), pack_f32x2(r[j], r[j + 1]), s0);
-                  s1 = fma_f32x2(mul_f32x2(v.y, s2), pack_f32x2(r[j + 2], r[j + 3]), s1);
-                }
+              for (int j = 0; j < CB; j += 2) {
+                uint64_t& s = sum[(i * CB + j) / 2];
+                s = fma_f32x2(s2, pack_f32x2(r[j], r[j + 1]), s);
               }
-            });
-          }
+            } else {
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            spc[g] = spn[g];
-#pragma unroll
-            for (int i = 0; i < NQ; ++i) sqc[g][i] = sqn[g][i];
+              for (int j = 0; j < CB; j += 4) {
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(
+                    sc + kP + column(i) + j);
+                uint64_t& u0 = sum[(i * CB + j) / 2];
+                uint64_t& u1 = sum[(i * CB + j) / 2 + 1];
+                u0 = fma_f32x2(mul_f32x2(v.x, s2), pack_f32x2(r[j], r[j + 1]), u0);
+                u1 = fma_f32x2(mul_f32x2(v.y, s2), pack_f32x2(r[j + 2], r[j + 3]), u1);
+              }
+            }
+          });
+          if (lane == 0) mbar_arrive(&sempty[slot]);  // after take's __syncwarp
+          if (++slot == L::SLOTS) {
+            slot = 0;
+            slot_phase ^= 1u;
           }
         }
       }
@@ -695,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            ((j ^ ((lane >> 1) & 3)) << 2)) = v;
           }
           __syncwarp();
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             const int r = i * 8 + (lane >> 2), j = lane & 3;
             float4 v = *reinterpret_cast<const float4*>(
@@ -711,12 +736,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               store_d4(a.D, di, a.d_type, v);
             } else {
-              const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (col + x < t.q1)
-                  store_d(a.D, di + x, a.d_type,
-                          f[x] + (a.C ? load_c(a.C, ci + x, a.d_type) : 0.f));
+#pragma unroll 1
+              for (int x = 0; x < 4 && col + x < t.q1; ++x) {
+                const float f = x == 0 ? v.x : x == 1 ? v.y : x == 2 ? v.z : v.w;
+                store_d(a.D, di + x, a.d_type,
+                        f + (a.C ? load_c(a.C, ci + x, a.d_type) : 0.f));
+              }
             }
           }
         }
@@ -743,16 +768,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < CB; ++j)
               if (q + j < t.q1) d[j * a.ldd] = v[j];
-          } else if (a.d_type == MMA_BF16) {
-            __nv_bfloat16* d = static_cast<__nv_bfloat16*>(a.D) + di;
-#pragma unroll
-            for (int j = 0; j < CB; ++j)
-              if (q + j < t.q1) d[j * a.ldd] = __float2bfloat16_rn(v[j]);
           } else {
-            __half* d = static_cast<__half*>(a.D) + di;
+            uint16_t* d = static_cast<uint16_t*>(a.D) + di;
+            const bool bf16 = a.d_type == MMA_BF16;
 #pragma unroll
             for (int j = 0; j < CB; ++j)
-              if (q + j < t.q1) d[j * a.ldd] = __float2half_rn(v[j]);
+              if (q + j < t.q1)
+                d[j * a.ldd] = bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v[j]))
+                                    : __half_as_ushort(__float2half_rn(v[j]));
           }
         }
       }

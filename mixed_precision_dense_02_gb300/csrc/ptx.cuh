@@ -133,6 +133,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether that phase has completed, without waiting at all.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // As mbar_try_wait, acquiring at cluster scope: for a barrier that another
 // CTA of the cluster arrives on to hand over its own memory writes.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar,
@@ -631,6 +644,22 @@ __device__ __forceinline__ void cp_async_16_zfill(uint32_t saddr,
                                                   const void* g, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(saddr),
                "l"(g), "r"(bytes)
+               : "memory");
+}
+
+// Four bytes, or zero with bytes = 0.
+__device__ __forceinline__ void cp_async_4_zfill(uint32_t saddr, const void* g,
+                                                 int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(saddr),
+               "l"(g), "r"(bytes)
+               : "memory");
+}
+
+// One of the arrivals that `bar` was initialised with, made when this
+// thread's earlier cp.async have landed.
+__device__ __forceinline__ void cp_async_mbar_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                   smem_u32(bar))
                : "memory");
 }
 
