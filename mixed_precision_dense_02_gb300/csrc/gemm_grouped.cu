@@ -71,7 +71,9 @@ struct GroupedArgs {
   uint32_t idesc;  // without the N field
   int kb_per_chunk;
   int d_type;  // MMA_F32, MMA_F16 or MMA_BF16
-  int vec4;    // ROWS: four elements of a row of D (and C) can move at once
+  // ROWS: four elements of a row of D (and C) can move at once; D is 16-bit,
+  // there is no C and eight can
+  int vec4, vec8;
   const void* C;
   int64_t ldc, c_group;
   void* D;
@@ -134,6 +136,16 @@ __device__ __forceinline__ void store_d(void* d, int64_t i, int t, float v) {
     static_cast<__half*>(d)[i] = __float2half_rn(v);
 }
 
+// Two FP32 values rounded to 16 bits, lo in the low half.
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf16) {
+  if (bf16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 __device__ __forceinline__ float4 load_c4(const void* c, int64_t i, int t) {
   if (t == MMA_F32)
     return *reinterpret_cast<const float4*>(static_cast<const float*>(c) + i);
@@ -155,18 +167,8 @@ __device__ __forceinline__ void store_d4(void* d, int64_t i, int t, float4 v) {
     *reinterpret_cast<float4*>(static_cast<float*>(d) + i) = v;
     return;
   }
-  uint2 w;
-  if (t == MMA_BF16) {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z, v.w);
-    w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                   *reinterpret_cast<const uint32_t*>(&hi));
-  } else {
-    const __half2 lo = __floats2half2_rn(v.x, v.y);
-    const __half2 hi = __floats2half2_rn(v.z, v.w);
-    w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                   *reinterpret_cast<const uint32_t*>(&hi));
-  }
+  const bool bf16 = t == MMA_BF16;
+  const uint2 w = make_uint2(pack16(v.x, v.y, bf16), pack16(v.z, v.w, bf16));
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(d) + i) = w;
 }
 
@@ -623,8 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int num_kb = (t.k1 - t.k0 + KE - 1) / KE;
       const int chunks = (num_kb + a.kb_per_chunk - 1) / a.kb_per_chunk;
       // Wait for a chunk's sums in tensor memory, add them (through `add`,
-      // for each block of columns) and return the accumulator.  The next
-      // block is on its way while one is added.
+      // for each block of columns) and return the accumulator as soon as its
+      // last block is in registers.  (Two blocks in flight were slower: the
+      // other warp of the scheduler covers the latency, and the registers
+      // are needed for the sums.)
       auto take = [&](auto&& add) {
         const bool got = mbar_wait(&tfull[acc], acc_phase, abort_flag, a.status);
         if (!__all_sync(0xffffffffu, got)) {
@@ -634,28 +638,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t taddr =
             tmem_base + uint32_t(acc * BN) + (uint32_t(quarter * 32) << 16);
-        uint32_t r[2][CB];
-        auto load = [&](int i) {
-          if (column(i) >= t.nt) return;
-          if constexpr (CB == 32)
-            tmem_ld_32x32b_x32(taddr + column(i), r[i & 1]);
-          else
-            tmem_ld_32x32b_x16(taddr + column(i), r[i & 1]);
-        };
-        load(0);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-          tmem_ld_wait();
-          if (i + 1 < NB) load(i + 1);
-          if (column(i) < t.nt) add(i, r[i & 1]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CL == 1)
-            mbar_arrive(&tempty[acc]);
-          else
-            mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
+          const bool in = column(i) < t.nt;
+          uint32_t r[CB];
+          if (in) {
+            if constexpr (CB == 32)
+              tmem_ld_32x32b_x32(taddr + column(i), r);
+            else
+              tmem_ld_32x32b_x16(taddr + column(i), r);
+            tmem_ld_wait();
+          }
+          if (i + 1 == NB) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (CL == 1)
+                mbar_arrive(&tempty[acc]);
+              else
+                mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
+            }
+          }
+          if (in) add(i, r);
         }
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
@@ -695,7 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           });
-          if (lane == 0) mbar_arrive(&sempty[slot]);  // after take's __syncwarp
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[slot]);
           if (++slot == L::SLOTS) {
             slot = 0;
             slot_phase ^= 1u;
@@ -704,6 +709,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if constexpr (ROWS) {
+        if (a.vec8) {
+          // 16-bit D without C: 32 columns at a time, rounded, through
+          // shared memory, so that four lanes store 64 bytes of a row and a
+          // warp eight rows
+          const bool bf16 = a.d_type == MMA_BF16;
+#pragma unroll
+          for (int c = 0; c < HALF / 32; ++c) {
+            const int q = t.q0 + h * HALF + c * 32;
+            if (q >= t.q1) continue;
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                float lo, hi;
+                unpack_f32x2(sum[c * 16 + j * 4 + x], lo, hi);
+                w[x] = pack16(lo, hi, bf16);
+              }
+              *reinterpret_cast<uint4*>(wbuf + lane * 16 +
+                                        ((j ^ ((lane >> 1) & 3)) << 2)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+            const int j = lane & 3;
+            const int col = q + 8 * j;
+            uint16_t* d = static_cast<uint16_t*>(a.D) + int64_t(pw) * a.ldd + col;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = i * 8 + (lane >> 2);
+              const uint4 v = *reinterpret_cast<const uint4*>(
+                  wbuf + r * 16 + ((j ^ ((r >> 1) & 3)) << 2));
+              if (pw + r >= t.p1 || col >= t.q1) continue;
+              if (col + 8 <= t.q1) {
+                *reinterpret_cast<uint4*>(d + r * a.ldd) = v;
+              } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int x = 0; x < 7; ++x)
+                  if (col + x < t.q1)
+                    d[r * a.ldd + x] = uint16_t(w[x >> 1] >> (16 * (x & 1)));
+              }
+            }
+          }
+          continue;
+        }
         // 16 columns at a time through shared memory, so that four lanes
         // store one row's 16 columns and a warp eight rows
 #pragma unroll
@@ -774,8 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < CB; ++j)
               if (q + j < t.q1)
-                d[j * a.ldd] = bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v[j]))
-                                    : __half_as_ushort(__float2half_rn(v[j]));
+                d[j * a.ldd] = uint16_t(pack16(v[j], 0.f, bf16));
           }
         }
       }
@@ -897,9 +947,9 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
   return e == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
 }
 
-bool elements_aligned(const void* p, int64_t ld, int bytes) {
-  return p == nullptr || ((reinterpret_cast<uintptr_t>(p) & uintptr_t(4 * bytes - 1)) == 0 &&
-                          (ld & 3) == 0);
+// Whether `n` consecutive elements at multiples of n in a row can move at once.
+bool elements_aligned(const void* p, int64_t ld, int bytes, int n) {
+  return (reinterpret_cast<uintptr_t>(p) & uintptr_t(n * bytes - 1)) == 0 && ld % n == 0;
 }
 
 }  // namespace
@@ -927,7 +977,9 @@ mma_status_t launch_gemm_f8(const Ctx& ctx, const F8Problem& f) {
     const int db = f.d_type == MMA_F32 ? 4 : 2;
     a.p_size = int(f.rows);
     a.q_size = int(f.N);
-    a.vec4 = elements_aligned(f.D, f.ldd, db) && elements_aligned(f.C, f.ldc, db);
+    a.vec4 = elements_aligned(f.D, f.ldd, db, 4) &&
+             (f.C == nullptr || elements_aligned(f.C, f.ldc, db, 4));
+    a.vec8 = db == 2 && f.C == nullptr && elements_aligned(f.D, f.ldd, db, 8);
     a.idesc = idesc_f32(f.a_e5m2, f.b_e5m2, false, false, 2 * kP);
     a.sp = f.SA;
     a.sp_row = f.sa_row;
