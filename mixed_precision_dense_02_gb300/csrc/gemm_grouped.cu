@@ -94,10 +94,12 @@ struct Layout {
   static constexpr int P_BYTES = kP * 128;
   static constexpr int Q_BYTES = BN / CL * 128;
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
-  // 8-bit: a ring of the chunks' scales, 128 of P, then those of Q (ROWS:
-  // of the two halves of the columns)
-  static constexpr int SLOTS = KIND8 ? 8 : 0;
-  static constexpr int SLOT_FLOATS = kP + (ROWS ? 4 : BN);
+  // 8-bit: a ring of the chunks' scales, G chunks per slot; a chunk's are
+  // 128 of P, then those of Q (ROWS: of the two halves of the columns)
+  static constexpr int G = 4;
+  static constexpr int SLOTS = KIND8 ? 3 : 0;
+  static constexpr int CHUNK_FLOATS = kP + (ROWS ? 4 : BN);
+  static constexpr int SLOT_FLOATS = G * CHUNK_FLOATS;
   static constexpr int SCALE_OFFSET = STAGES * STAGE_BYTES;
   // per epilogue warp: staging of 32 rows x 16 columns of FP32 (ROWS)
   static constexpr int WARP_BYTES = ROWS ? 2048 : 0;
@@ -570,21 +572,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         src_q[i] = a.sq + (ROWS ? t.e * a.sq_group : 0) +
                    (int64_t(min(q, t.q1 - 1)) >> a.q_shift) * a.sq_row;
       }
-      for (int k = t.k0; k < t.k1; k += KE) {
+      const int chunks = (t.k1 - t.k0 + KE - 1) / KE;
+      for (int ch = 0; ch < chunks; ch += L::G) {
         ok = mbar_wait(&sempty[slot], phase ^ 1u, abort_flag, a.status);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        const uint32_t dst = smem_u32(ring + slot * L::SLOT_FLOATS);
+        uint32_t dst = smem_u32(ring + slot * L::SLOT_FLOATS);
+        for (int g = 0; g < L::G && ch + g < chunks; ++g, dst += L::CHUNK_FLOATS * 4) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          cp_async_4_zfill(dst + (i * 32 + lane) * 4, src_p[i], ((len_p >> i) & 1) * 4);
-          src_p[i] += a.sp_blk;
-        }
+          for (int i = 0; i < NP; ++i) {
+            cp_async_4_zfill(dst + (i * 32 + lane) * 4, src_p[i], ((len_p >> i) & 1) * 4);
+            src_p[i] += a.sp_blk;
+          }
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          if (!ROWS || lane < 2)
-            cp_async_4_zfill(dst + (kP + i * 32 + lane) * 4, src_q[i],
-                             ((len_q >> i) & 1) * 4);
-          src_q[i] += a.sq_blk;
+          for (int i = 0; i < NQ; ++i) {
+            if (!ROWS || lane < 2)
+              cp_async_4_zfill(dst + (kP + i * 32 + lane) * 4, src_q[i],
+                               ((len_q >> i) & 1) * 4);
+            src_q[i] += a.sq_blk;
+          }
         }
         cp_async_mbar_arrive(&sfull[slot]);
         if (++slot == L::SLOTS) {
@@ -614,6 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
+    // the leader's barriers that hand the accumulators back
+    const uint32_t tempty_lead = mapa_shared(smem_u32(&tempty[0]), 0);
     for (int u = first_unit; u < units && ok; u += unit_step) {
       __syncwarp();
       const Tile t = decode(u);
@@ -652,20 +659,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i + 1 == NB) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-              if constexpr (CL == 1)
-                mbar_arrive(&tempty[acc]);
-              else
-                mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
-            }
+            mbar_arrive_remote_if(tempty_lead + uint32_t(acc) * 8u, lane == 0);
           }
           if (in) add(i, r);
         }
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       };
-      for (int ch = 0; ch < chunks && ok; ++ch) {
-        if constexpr (!KIND8) {
+      if constexpr (!KIND8) {
+        for (int ch = 0; ch < chunks && ok; ++ch)
           take([&](int i, const uint32_t (&r)[CB]) {
 #pragma unroll
             for (int j = 0; j < CB; j += 2) {
@@ -673,32 +675,42 @@ __global__ void __launch_bounds__(kThreads, 1)
               s = add_f32x2(s, pack_f32x2(r[j], r[j + 1]));
             }
           });
-        } else {
+      } else {
+        for (int ch = 0; ch < chunks && ok; ch += L::G) {
           const bool got = mbar_wait(&sfull[slot], slot_phase, abort_flag, a.status);
           if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
           const float* sc = ring + slot * L::SLOT_FLOATS;
-          float s1 = sc[quarter * 32 + lane];
-          if constexpr (ROWS) s1 *= sc[kP + h];
-          const uint64_t s2 = pack_f32x2(__float_as_uint(s1), __float_as_uint(s1));
-          take([&](int i, const uint32_t (&r)[CB]) {
-            if constexpr (ROWS) {
+          const int n = min(L::G, chunks - ch);
+          auto scale = [&](int g) {
+            const float* s = sc + g * L::CHUNK_FLOATS;
+            return ROWS ? s[quarter * 32 + lane] * s[kP + h] : s[quarter * 32 + lane];
+          };
+          float s1 = scale(0);
+#pragma unroll 1
+          for (int g = 0; g < n && ok; ++g) {
+            const uint64_t s2 = pack_f32x2(__float_as_uint(s1), __float_as_uint(s1));
+            s1 = scale(min(g + 1, n - 1));  // on its way during this chunk
+            [[maybe_unused]] const float* sq = sc + g * L::CHUNK_FLOATS + kP;
+            take([&](int i, const uint32_t (&r)[CB]) {
+              if constexpr (ROWS) {
 #pragma unroll
-              for (int j = 0; j < CB; j += 2) {
-                uint64_t& s = sum[(i * CB + j) / 2];
-                s = fma_f32x2(s2, pack_f32x2(r[j], r[j + 1]), s);
-              }
-            } else {
+                for (int j = 0; j < CB; j += 2) {
+                  uint64_t& s = sum[(i * CB + j) / 2];
+                  s = fma_f32x2(s2, pack_f32x2(r[j], r[j + 1]), s);
+                }
+              } else {
 #pragma unroll
-              for (int j = 0; j < CB; j += 4) {
-                const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(
-                    sc + kP + column(i) + j);
-                uint64_t& u0 = sum[(i * CB + j) / 2];
-                uint64_t& u1 = sum[(i * CB + j) / 2 + 1];
-                u0 = fma_f32x2(mul_f32x2(v.x, s2), pack_f32x2(r[j], r[j + 1]), u0);
-                u1 = fma_f32x2(mul_f32x2(v.y, s2), pack_f32x2(r[j + 2], r[j + 3]), u1);
+                for (int j = 0; j < CB; j += 4) {
+                  const ulonglong2 v =
+                      *reinterpret_cast<const ulonglong2*>(sq + column(i) + j);
+                  uint64_t& u0 = sum[(i * CB + j) / 2];
+                  uint64_t& u1 = sum[(i * CB + j) / 2 + 1];
+                  u0 = fma_f32x2(mul_f32x2(v.x, s2), pack_f32x2(r[j], r[j + 1]), u0);
+                  u1 = fma_f32x2(mul_f32x2(v.y, s2), pack_f32x2(r[j + 2], r[j + 3]), u1);
+                }
               }
-            }
-          });
+            });
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sempty[slot]);
           if (++slot == L::SLOTS) {

@@ -84,6 +84,17 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
                : "memory");
 }
 
+// mbar_arrive_remote by the lanes that have `doit`, without a branch.
+__device__ __forceinline__ void mbar_arrive_remote_if(uint32_t cluster_addr,
+                                                      bool doit) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr),
+      "r"(uint32_t(doit))
+      : "memory");
+}
+
 // Programmatic dependent launch: wait until the grid this one depends on
 // has completed and its memory operations are visible (a no-op when the
 // kernel was launched without the programmatic-serialization attribute).
