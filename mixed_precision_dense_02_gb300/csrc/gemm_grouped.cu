@@ -448,65 +448,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       [[maybe_unused]] uint32_t cut_phase = 0;  // one bit per stage
       int acc = 0;
       bool ok = true, ready = false;
+      const uint32_t s0 = smem_u32(smem);
+      const uint64_t dp0 = P_MN ? sw128_mnmajor_desc(s0) : sw128_kmajor_desc(s0);
+      const uint64_t dq0 = Q_MN ? sw128_mnmajor_desc(s0 + L::P_BYTES)
+                                : sw128_kmajor_desc(s0 + L::P_BYTES);
+      // 32 bytes of a row (K-major) or 16 rows (MN-major) per step
+      constexpr uint32_t kStepP = P_MN ? 128 : 2;
+      constexpr uint32_t kStepQ = Q_MN ? 128 : 2;
       for (int u = first_unit; u < units && ok; u += unit_step) {
         const Tile t = decode(u);
         const uint32_t idesc = a.idesc | (uint32_t(t.nt >> 3) << 17);
-        int in_chunk = 0;
-        for (int k = t.k0; k < t.k1; k += KE) {
-          const uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
-          if (in_chunk == 0)
-            ok = mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, a.status);
-          if (ok && !ready) ok = mbar_wait(&full[stage], phase, abort_flag, a.status);
-          const int left = t.k1 - k;
-          int steps = 4;
-          if constexpr (RAGK) {
-            if (ok && left < KE) {
-              steps = (left + 15) >> 4;
-              ok = mbar_wait_cluster(&cut_ok[stage], (cut_phase >> stage) & 1u,
-                                     abort_flag, a.status);
-              cut_phase ^= 1u << stage;
-            }
-          }
+        int left = t.k1 - t.k0;  // k still to be issued
+        while (left > 0 && ok) {
+          ok = mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, a.status);
           if (!ok) break;
           tc_fence_after();
-          const bool last = in_chunk + 1 == a.kb_per_chunk || left <= KE;
-          const uint32_t sa = smem_u32(smem + stage * L::STAGE_BYTES);
-          const uint64_t dp = P_MN ? sw128_mnmajor_desc(sa) : sw128_kmajor_desc(sa);
-          const uint64_t dq = Q_MN ? sw128_mnmajor_desc(sa + L::P_BYTES)
-                                   : sw128_kmajor_desc(sa + L::P_BYTES);
-          // 32 bytes of a row (K-major) or 16 rows (MN-major) per step
-          constexpr uint64_t kStepP = P_MN ? 128 : 2;
-          constexpr uint64_t kStepQ = Q_MN ? 128 : 2;
-          const int next = stage + 1 == STAGES ? 0 : stage + 1;
-          const uint32_t next_phase = next ? phase : phase ^ 1u;
+          const uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
+          uint32_t accum = 0;
+          for (int i = a.kb_per_chunk; i > 0 && left > 0; --i) {
+            if (!ready) ok = mbar_wait(&full[stage], phase, abort_flag, a.status);
+            int steps = 4;
+            if constexpr (RAGK) {
+              if (ok && left < KE) {
+                steps = (left + 15) >> 4;
+                ok = mbar_wait_cluster(&cut_ok[stage], (cut_phase >> stage) & 1u,
+                                       abort_flag, a.status);
+                cut_phase ^= 1u << stage;
+              }
+            }
+            if (!ok) break;
+            tc_fence_after();
+            // (the start address is the low bits of a descriptor)
+            const uint64_t dp = dp0 + uint32_t(stage * (L::STAGE_BYTES >> 4));
+            const uint64_t dq = dq0 + uint32_t(stage * (L::STAGE_BYTES >> 4));
+            uint64_t* const done_with = &empty[stage];
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            if (s == 3) ready = mbar_test(&full[next], next_phase);
-            if (RAGK && s >= steps) continue;
-            const uint32_t accum = (in_chunk != 0 || s != 0) ? 1u : 0u;
-            if constexpr (KIND8)
-              umma_f8<CL>(d_tmem, dp + s * kStepP, dq + s * kStepQ, idesc, accum);
-            else if constexpr (CL == 1)
-              umma_f16(d_tmem, dp + s * kStepP, dq + s * kStepQ, idesc, accum);
+            for (int s = 0; s < 4; ++s) {
+              if (s == 3) ready = mbar_test(&full[stage], phase);
+              if (RAGK && s >= steps) continue;
+              if constexpr (KIND8)
+                umma_f8<CL>(d_tmem, dp + s * kStepP, dq + s * kStepQ, idesc, accum);
+              else if constexpr (CL == 1)
+                umma_f16(d_tmem, dp + s * kStepP, dq + s * kStepQ, idesc, accum);
+              else
+                umma_f16_pair(d_tmem, dp + s * kStepP, dq + s * kStepQ, idesc, accum);
+              accum = 1;
+            }
+            if constexpr (CL == 1)
+              umma_commit(done_with);
             else
-              umma_f16_pair(d_tmem, dp + s * kStepP, dq + s * kStepQ, idesc, accum);
+              umma_commit_pair(done_with, 3u);
+            left -= KE;
           }
-          if constexpr (CL == 1) {
-            umma_commit(&empty[stage]);
-            if (last) umma_commit(&tfull[acc]);
-          } else {
-            umma_commit_pair(&empty[stage], 3u);
-            if (last) umma_commit_pair(&tfull[acc], 3u);
-          }
-          stage = next;
-          phase = next_phase;
-          if (last) {
-            in_chunk = 0;
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1u;
-          } else {
-            ++in_chunk;
-          }
+          if (!ok) break;
+          if constexpr (CL == 1)
+            umma_commit(&tfull[acc]);
+          else
+            umma_commit_pair(&tfull[acc], 3u);
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
         }
       }
       // Every MMA issued above completes before tensor memory is released.
@@ -626,28 +630,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile t = decode(u);
       const int pw = t.p0 + rank * kP + quarter * 32;
       const int p = pw + lane;
-      uint64_t sum[HALF / 2];
+      float sum[HALF];
 #pragma unroll
-      for (int j = 0; j < HALF / 2; ++j) sum[j] = 0ull;
+      for (int j = 0; j < HALF; ++j) sum[j] = 0.f;
       const int num_kb = (t.k1 - t.k0 + KE - 1) / KE;
       const int chunks = (num_kb + a.kb_per_chunk - 1) / a.kb_per_chunk;
       // Wait for a chunk's sums in tensor memory, add them (through `add`,
       // for each block of columns) and return the accumulator as soon as its
-      // last block is in registers.  (Two blocks in flight were slower: the
-      // other warp of the scheduler covers the latency, and the registers
-      // are needed for the sums.)
+      // last block is in registers.  Scalar additions and one block in
+      // flight: packed pairs of FP32 and a second block cost registers that
+      // the sums need (four blocks of 32 columns by eight warps: 344 clocks,
+      // packed 728, of which reading tensor memory is 170).  With ROWS nearly
+      // every tile has all its columns, so what lies beyond nt is added like
+      // the rest, to sums that are not stored.
       auto take = [&](auto&& add) {
-        const bool got = mbar_wait(&tfull[acc], acc_phase, abort_flag, a.status);
-        if (!__all_sync(0xffffffffu, got)) {
-          ok = false;
-          return;
-        }
+        mbar_wait_lean(&tfull[acc], acc_phase, abort_flag, a.status);
         tc_fence_after();
         const uint32_t taddr =
             tmem_base + uint32_t(acc * BN) + (uint32_t(quarter * 32) << 16);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-          const bool in = column(i) < t.nt;
+          const bool in = ROWS || column(i) < t.nt;
           uint32_t r[CB];
           if (in) {
             if constexpr (CB == 32)
@@ -664,52 +667,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (in) add(i, r);
         }
         acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
+        acc_phase ^= uint32_t(acc == 0);
       };
       if constexpr (!KIND8) {
-        for (int ch = 0; ch < chunks && ok; ++ch)
+        for (int ch = 0; ch < chunks; ++ch)
           take([&](int i, const uint32_t (&r)[CB]) {
 #pragma unroll
-            for (int j = 0; j < CB; j += 2) {
-              uint64_t& s = sum[(i * CB + j) / 2];
-              s = add_f32x2(s, pack_f32x2(r[j], r[j + 1]));
-            }
+            for (int j = 0; j < CB; ++j) sum[i * CB + j] += __uint_as_float(r[j]);
           });
       } else {
-        for (int ch = 0; ch < chunks && ok; ch += L::G) {
-          const bool got = mbar_wait(&sfull[slot], slot_phase, abort_flag, a.status);
-          if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+        for (int ch = 0; ch < chunks; ch += L::G) {
+          mbar_wait_lean(&sfull[slot], slot_phase, abort_flag, a.status);
           const float* sc = ring + slot * L::SLOT_FLOATS;
-          const int n = min(L::G, chunks - ch);
-          auto scale = [&](int g) {
-            const float* s = sc + g * L::CHUNK_FLOATS;
-            return ROWS ? s[quarter * 32 + lane] * s[kP + h] : s[quarter * 32 + lane];
-          };
-          float s1 = scale(0);
 #pragma unroll 1
-          for (int g = 0; g < n && ok; ++g) {
-            const uint64_t s2 = pack_f32x2(__float_as_uint(s1), __float_as_uint(s1));
-            s1 = scale(min(g + 1, n - 1));  // on its way during this chunk
-            [[maybe_unused]] const float* sq = sc + g * L::CHUNK_FLOATS + kP;
+          for (int g = min(L::G, chunks - ch); g > 0; --g) {
+            const float sp = ROWS ? sc[quarter * 32 + lane] * sc[kP + h]
+                                  : sc[quarter * 32 + lane];
             take([&](int i, const uint32_t (&r)[CB]) {
               if constexpr (ROWS) {
 #pragma unroll
-                for (int j = 0; j < CB; j += 2) {
-                  uint64_t& s = sum[(i * CB + j) / 2];
-                  s = fma_f32x2(s2, pack_f32x2(r[j], r[j + 1]), s);
-                }
+                for (int j = 0; j < CB; ++j)
+                  sum[i * CB + j] = fmaf(sp, __uint_as_float(r[j]), sum[i * CB + j]);
               } else {
 #pragma unroll
                 for (int j = 0; j < CB; j += 4) {
-                  const ulonglong2 v =
-                      *reinterpret_cast<const ulonglong2*>(sq + column(i) + j);
-                  uint64_t& u0 = sum[(i * CB + j) / 2];
-                  uint64_t& u1 = sum[(i * CB + j) / 2 + 1];
-                  u0 = fma_f32x2(mul_f32x2(v.x, s2), pack_f32x2(r[j], r[j + 1]), u0);
-                  u1 = fma_f32x2(mul_f32x2(v.y, s2), pack_f32x2(r[j + 2], r[j + 3]), u1);
+                  const float4 v =
+                      *reinterpret_cast<const float4*>(sc + kP + column(i) + j);
+                  float* const s = sum + i * CB + j;
+                  s[0] = fmaf(v.x * sp, __uint_as_float(r[j]), s[0]);
+                  s[1] = fmaf(v.y * sp, __uint_as_float(r[j + 1]), s[1]);
+                  s[2] = fmaf(v.z * sp, __uint_as_float(r[j + 2]), s[2]);
+                  s[3] = fmaf(v.w * sp, __uint_as_float(r[j + 3]), s[3]);
                 }
               }
             });
+            sc += L::CHUNK_FLOATS;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sempty[slot]);
@@ -719,6 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      ok = !__any_sync(0xffffffffu, *abort_flag != 0);
       if (!ok) break;
       if constexpr (ROWS) {
         if (a.vec8) {
@@ -735,11 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 4; ++j) {
               uint32_t w[4];
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                float lo, hi;
-                unpack_f32x2(sum[c * 16 + j * 4 + x], lo, hi);
-                w[x] = pack16(lo, hi, bf16);
-              }
+              for (int x = 0; x < 4; ++x)
+                w[x] = pack16(sum[c * 32 + j * 8 + 2 * x], sum[c * 32 + j * 8 + 2 * x + 1], bf16);
               *reinterpret_cast<uint4*>(wbuf + lane * 16 +
                                         ((j ^ ((lane >> 1) & 3)) << 2)) =
                   make_uint4(w[0], w[1], w[2], w[3]);
@@ -776,11 +766,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            ulonglong2 v;
-            v.x = sum[c * 8 + 2 * j];
-            v.y = sum[c * 8 + 2 * j + 1];
-            *reinterpret_cast<ulonglong2*>(wbuf + lane * 16 +
-                                           ((j ^ ((lane >> 1) & 3)) << 2)) = v;
+            const float* const s = sum + c * 16 + 4 * j;
+            *reinterpret_cast<float4*>(wbuf + lane * 16 +
+                                       ((j ^ ((lane >> 1) & 3)) << 2)) =
+                make_float4(s[0], s[1], s[2], s[3]);
           }
           __syncwarp();
 #pragma unroll 1
@@ -817,8 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (q >= t.q1) continue;
           float v[CB];
 #pragma unroll
-          for (int j = 0; j < CB; j += 2)
-            unpack_f32x2(sum[(i * CB + j) / 2], v[j], v[j + 1]);
+          for (int j = 0; j < CB; ++j) v[j] = sum[i * CB + j];
           if (a.C) {
             const int64_t ci = group * a.c_group + int64_t(q) * a.ldc + p;
 #pragma unroll

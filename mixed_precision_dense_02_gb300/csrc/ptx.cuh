@@ -216,6 +216,16 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
 }
 
+// mbar_wait for inner loops of whole warps: after a failure it returns like
+// after a success (and from then on quickly, the abort flag being up); the
+// caller looks at the flag where it next can.
+__device__ __forceinline__ void mbar_wait_lean(uint64_t* bar, uint32_t parity,
+                                               volatile int* abort_flag,
+                                               unsigned* status) {
+  mbar_wait(bar, parity, abort_flag, status);
+  __syncwarp();
+}
+
 // Change this warpgroup's registers per thread (every warp of it executes
 // this); the launch's registers are shared out anew, never added to.
 template <int N>
@@ -560,37 +570,6 @@ __host__ __device__ constexpr uint32_t idesc_f32(uint32_t fmt_a, uint32_t fmt_b,
                                                  bool a_mn, bool b_mn, int m) {
   return (1u << 4) | (fmt_a << 7) | (fmt_b << 10) | ((a_mn ? 1u : 0u) << 15) |
          ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(m >> 4) << 24);
-}
-
-// ------------------------------------------------- packed FP32 arithmetic
-
-__device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-
-__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b,
-                                              uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 
 // -------------------------------------------------------------- mma.sync
