@@ -438,15 +438,18 @@ mma_status_t mma_rmsnorm_f8(int type, int w_type, int64_t M, int64_t N,
  * R is the gradient that reaches H from elsewhere, or NULL; DX is the
  * gradient of X and of the forward's residual alike, and may be DY or R.
  * DW is summed in a fixed order (the same bits from run to run), through
- * the library's scratch buffer (2 * SMs * N * 4 bytes at most;
- * MMA_ERR_NO_MEMORY if it cannot grow).  Types as in mma_rmsnorm_f8.
- * M == 0 gives DW = 0.
+ * `workspace`: device memory of the caller, 4-byte aligned, of at least
+ * mma_rmsnorm_backward_workspace(M, N) bytes (at most 304 * N * 4), which
+ * the call's work on `stream` uses and nothing else may meanwhile.  Types as
+ * in mma_rmsnorm_f8.  M == 0 gives DW = 0.
  */
+int64_t mma_rmsnorm_backward_workspace(int64_t M, int64_t N);
 mma_status_t mma_rmsnorm_backward(int type, int w_type, int64_t M, int64_t N,
                                   const void *DY, int64_t lddy, const void *H,
                                   int64_t ldh, const void *W, float eps,
                                   const void *R, int64_t ldr, void *DX,
-                                  int64_t lddx, float *DW, void *stream);
+                                  int64_t lddx, float *DW, void *workspace,
+                                  int64_t workspace_bytes, void *stream);
 
 /*
  * mma_quantize_f8 -- X (M x N; MMA_F16, MMA_BF16 or MMA_F32) as 8-bit values

@@ -45,7 +45,9 @@ SIGNATURES = {
                               _f32, _int, _p, _i64, _p, _i64, _p, _i64, _p,
                               _i64, _i64, _p]),
     "mma_rmsnorm_backward": (_int, [_int, _int, _i64, _i64, _p, _i64, _p, _i64,
-                                    _p, _f32, _p, _i64, _p, _i64, _p, _p]),
+                                    _p, _f32, _p, _i64, _p, _i64, _p, _p, _i64,
+                                    _p]),
+    "mma_rmsnorm_backward_workspace": (_i64, [_i64, _i64]),
     "mma_quantize_f8": (_int, [_int, _int, _i64, _i64, _int, _int, _int, _p,
                                _i64, _p, _i64, _p, _i64, _i64, _p]),
     "mma_gemm_f8": (_int, [_int, _int, _int, _i64, _i64, _i64, _p, _i64, _p,
@@ -517,11 +519,14 @@ def rmsnorm_backward(dY, H, W, dH=None, *, eps: float = 1e-6, stream=None):
     device = H.device
     dX = _empty_rows(M, N, H.dtype, device)
     dW = torch.empty((N,), dtype=torch.float32, device=device)
+    need = load().mma_rmsnorm_backward_workspace(M, N)
+    # (freed by this stream's allocator only after the call's work)
+    ws = torch.empty((need,), dtype=torch.uint8, device=device)
     st = load().mma_rmsnorm_backward(
         code, w_code, M, N, dY.data_ptr(), _rows("dY", dY), H.data_ptr(),
         _rows("H", H), W.data_ptr(), eps, _ptr(dH),
         0 if dH is None else _rows("dH", dH), dX.data_ptr(), _rows("dX", dX),
-        dW.data_ptr(), _raw_stream(stream, device))
+        dW.data_ptr(), ws.data_ptr(), need, _raw_stream(stream, device))
     _check("mma_rmsnorm_backward", st)
     return dX, dW
 

@@ -909,16 +909,25 @@ extern "C" mma_status_t mma_rmsnorm_f8(
                                          S, s_row, s_blk});
 }
 
+extern "C" int64_t mma_rmsnorm_backward_workspace(int64_t M, int64_t N) {
+  return dim_ok(M) && dim_ok(N) ? rmsnorm_backward_workspace_bytes(M, N) : 0;
+}
+
 extern "C" mma_status_t mma_rmsnorm_backward(
     int type, int w_type, int64_t M, int64_t N, const void* DY, int64_t lddy,
     const void* H, int64_t ldh, const void* W, float eps, const void* R,
-    int64_t ldr, void* DX, int64_t lddx, float* DW, void* stream) {
+    int64_t ldr, void* DX, int64_t lddx, float* DW, void* workspace,
+    int64_t workspace_bytes, void* stream) {
   const int64_t eb = float_bytes(type);
   if (eb == 0 || (w_type != type && w_type != MMA_F32)) return MMA_ERR_UNSUPPORTED;
   if (!dim_ok(M) || !dim_ok(N) || !(eps >= 0.f)) return MMA_ERR_INVALID_ARG;
   if (N == 0) return MMA_OK;
   if (DW == nullptr) return MMA_ERR_INVALID_ARG;
   if (!aligned4(DW)) return MMA_ERR_MISALIGNED;
+  const int64_t need = rmsnorm_backward_workspace_bytes(M, N);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+    return MMA_ERR_INVALID_ARG;
+  if (need > 0 && !aligned4(workspace)) return MMA_ERR_MISALIGNED;
   if (M > 0) {
     if ((DX == DY && lddx != lddy) || (R != nullptr && DX == R && lddx != ldr))
       return MMA_ERR_INVALID_ARG;
@@ -934,8 +943,7 @@ extern "C" mma_status_t mma_rmsnorm_backward(
   Ctx ctx = make_ctx(stream, dev, info);
   const NormBackProblem p = {type, w_type, M, N, DY, lddy, H, ldh, W, eps,
                              R, ldr, DX, lddx, DW};
-  return with_workspace(ctx, rmsnorm_backward_workspace_bytes(ctx.num_sms, M, N),
-                        [&](void* ws) { return launch_rmsnorm_backward(ctx, p, ws); });
+  return launch_rmsnorm_backward(ctx, p, workspace);
 }
 
 extern "C" mma_status_t mma_quantize_f8(

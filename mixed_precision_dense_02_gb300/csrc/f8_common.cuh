@@ -83,19 +83,11 @@ struct Vec<__half> {
   __device__ static __half round(float v) { return __float2half_rn(v); }
 };
 
-// The 16 bytes of a row's vector `v`.  The last vector of a row may reach
-// past its n elements, but never past the 16-byte chunk that holds its last
-// one, because rows start on 16-byte boundaries; what lies there is cleared.
+// Clear what lies past a row's n elements in its vector v.
 template <class T>
-__device__ __forceinline__ void load_row(const T* row, int64_t v, int64_t n,
-                                         float (&f)[Vec<T>::kN]) {
+__device__ __forceinline__ void clear_tail(int64_t v, int64_t n,
+                                           float (&f)[Vec<T>::kN]) {
   constexpr int E = Vec<T>::kN;
-  if (v * E >= n) {
-#pragma unroll
-    for (int j = 0; j < E; ++j) f[j] = 0.f;
-    return;
-  }
-  Vec<T>::unpack(__ldg(reinterpret_cast<const uint4*>(row) + v), f);
   if ((v + 1) * E > n) {
 #pragma unroll
     for (int j = 0; j < E; ++j)
@@ -103,11 +95,29 @@ __device__ __forceinline__ void load_row(const T* row, int64_t v, int64_t n,
   }
 }
 
+// The 16 bytes of a row's vector `v`, zeros beyond the row.  The last vector
+// of a row may reach past its n elements (TAIL: they are not a multiple of
+// a vector's), but never past the 16-byte chunk that holds its last one,
+// because rows start on 16-byte boundaries; clear_tail clears what lies there.
 template <class T>
+__device__ __forceinline__ uint4 load_raw(const T* row, int64_t v, int64_t n) {
+  return v * Vec<T>::kN < n ? __ldg(reinterpret_cast<const uint4*>(row) + v)
+                            : make_uint4(0, 0, 0, 0);
+}
+
+template <class T, bool TAIL = true>
+__device__ __forceinline__ void load_row(const T* row, int64_t v, int64_t n,
+                                         float (&f)[Vec<T>::kN]) {
+  Vec<T>::unpack(load_raw(row, v, n), f);
+  if constexpr (TAIL) clear_tail<T>(v, n, f);
+}
+
+// (v is a vector of the row)
+template <class T, bool TAIL = true>
 __device__ __forceinline__ void store_row(T* row, int64_t v, int64_t n,
                                           const float (&f)[Vec<T>::kN]) {
   constexpr int E = Vec<T>::kN;
-  if ((v + 1) * E <= n) {
+  if (!TAIL || (v + 1) * E <= n) {
     *(reinterpret_cast<uint4*>(row) + v) = Vec<T>::pack(f);
   } else {
 #pragma unroll
@@ -120,6 +130,13 @@ __device__ __forceinline__ void store_row(T* row, int64_t v, int64_t n,
 // magnitudes, with NaN above infinity, so a NaN among them wins.
 __device__ __forceinline__ uint32_t abs_bits(float x) {
   return __float_as_uint(x) & 0x7FFFFFFFu;
+}
+
+// The larger of two magnitudes, NaN if one is.
+__device__ __forceinline__ float abs_max(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
 }
 
 template <bool E5M2>
@@ -151,7 +168,7 @@ __device__ __forceinline__ uint32_t to_f8x2(float lo, float hi) {
 }
 
 // Store E values of vector v of a row in 8 bits, times inv.
-template <bool E5M2, int E>
+template <bool E5M2, int E, bool TAIL = true>
 __device__ __forceinline__ void store_f8(uint8_t* row, int64_t v, int64_t n,
                                          const float (&y)[E], float inv) {
   uint32_t w[E / 4];
@@ -159,7 +176,7 @@ __device__ __forceinline__ void store_f8(uint8_t* row, int64_t v, int64_t n,
   for (int i = 0; i < E / 4; ++i)
     w[i] = to_f8x2<E5M2>(y[4 * i] * inv, y[4 * i + 1] * inv) |
            (to_f8x2<E5M2>(y[4 * i + 2] * inv, y[4 * i + 3] * inv) << 16);
-  if ((v + 1) * E <= n) {
+  if (!TAIL || (v + 1) * E <= n) {
     if constexpr (E == 8)
       *reinterpret_cast<uint2*>(row + v * 8) = make_uint2(w[0], w[1]);
     else

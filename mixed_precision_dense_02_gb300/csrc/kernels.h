@@ -264,7 +264,7 @@ struct NormBackProblem {
   int64_t lddx;
   float* DW;
 };
-size_t rmsnorm_backward_workspace_bytes(int num_sms, int64_t M, int64_t N);
+int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t N);
 mma_status_t launch_rmsnorm_backward(const Ctx& ctx, const NormBackProblem& p,
                                      void* workspace);
 

@@ -15,8 +15,10 @@
 // reaches h from elsewhere).
 //
 // Both are bound by memory: each input is read once and each output written
-// once, a row is held in registers between its two uses.  Rows wider than
-// the registers hold are read twice (the second time from L2).
+// once, a row is held in registers between its two uses.
+#include <algorithm>
+#include <type_traits>
+
 #include "f8_common.cuh"
 
 namespace mmagb {
@@ -64,186 +66,267 @@ __device__ __forceinline__ void load_weight(const void* W, bool w32, int64_t v,
   }
 }
 
-// One row per block; VPT 16-byte vectors per thread are kept in registers
-// (VPT = 0: none, the row is read again).
-template <class T, int VPT>
-__global__ void __launch_bounds__(1024)
+// Rows b, b + gridDim.x, ... per block, a row at a time: VPT 16-byte vectors
+// per thread stay in registers between the sum of squares and the output,
+// and the next row's loads are issued before this row's sum is exchanged.
+template <class T, int VPT, int MAXT, bool TAIL>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1)
     rmsnorm_kernel(const NormProblem p, bool w32) {
   constexpr int E = Vec<T>::kN;
   constexpr int kLanes = kScaleBlock / E;  // lanes that share a block
-  __shared__ float2 red[32];
-  const int64_t row = blockIdx.x;
-  const T* x = static_cast<const T*>(p.X) + row * p.ldx;
-  const T* r = p.R ? static_cast<const T*>(p.R) + row * p.ldr : nullptr;
-  T* hrow = p.H ? static_cast<T*>(p.H) + row * p.ldh : nullptr;
-  T* yrow = p.Y ? static_cast<T*>(p.Y) + row * p.ldy : nullptr;
-  uint8_t* qrow = p.Q ? static_cast<uint8_t*>(p.Q) + row * p.ldq : nullptr;
-  auto load = [&](int64_t v, float (&h)[E]) {
-    load_row(x, v, p.N, h);
-    if (r) {
-      float t[E];
-      load_row(r, v, p.N, t);
-#pragma unroll
-      for (int j = 0; j < E; ++j) h[j] += t[j];
-    }
-  };
-  auto emit = [&](int64_t v, const float (&h)[E], float rstd) {
-    float y[E];
-    load_weight<T>(p.W, w32, v, p.N, y);
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      y[j] = h[j] * rstd * y[j];
-      // columns past the end (rstd may be infinite or NaN) do not count
-      if (v * E + j >= p.N) y[j] = 0.f;
-      m = max(m, abs_bits(y[j]));
-    }
-    const bool live = v * E < p.N;
-    if (yrow && live) store_row(yrow, v, p.N, y);
-    if (!qrow) return;
-#pragma unroll
-    for (int d = kLanes / 2; d > 0; d >>= 1)
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float s = block_scale<false>(m, p.pow2);
-    if (!live) return;
-    store_f8<false>(qrow, v, p.N, y, __fdiv_rn(1.f, s));
-    if (threadIdx.x % kLanes == 0)
-      p.S[row * p.s_row + (v * E / kScaleBlock) * p.s_blk] = s;
-  };
-  const int64_t vectors = (p.N + E - 1) / E;
-  float h[VPT > 0 ? VPT : 1][E];
-  float ss = 0.f;
-  if constexpr (VPT > 0) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) load(threadIdx.x + i * blockDim.x, h[i]);
+  __shared__ float2 red[2][32];
+  const T* const X = static_cast<const T*>(p.X);
+  const T* const R = static_cast<const T*>(p.R);
+  const int64_t n = p.N;
+  uint4 xr[VPT], rr[VPT];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
+      xr[i] = load_raw(X + row * p.ldx, threadIdx.x + i * blockDim.x, n);
+    if (R) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        rr[i] = load_raw(R + row * p.ldr, threadIdx.x + i * blockDim.x, n);
+    }
+  };
+  fetch(blockIdx.x);
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, flip ^= 1) {
+    float h[VPT][E];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      Vec<T>::unpack(xr[i], h[i]);
+      if (R) {
+        float t[E];
+        Vec<T>::unpack(rr[i], t);
+#pragma unroll
+        for (int j = 0; j < E; ++j) h[i][j] += t[j];
+      }
+      if constexpr (TAIL) clear_tail<T>(threadIdx.x + i * blockDim.x, n, h[i]);
 #pragma unroll
       for (int j = 0; j < E; ++j) ss = fmaf(h[i][j], h[i][j], ss);
-  } else {
-    for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
-      load(v, h[0]);
-#pragma unroll
-      for (int j = 0; j < E; ++j) ss = fmaf(h[0][j], h[0][j], ss);
     }
-  }
-  ss = block_sum2(ss, 0.f, red).x;
-  const float rstd = __frsqrt_rn(ss / float(p.N) + p.eps);
-  if constexpr (VPT > 0) {
+    if (row + gridDim.x < p.M) fetch(row + gridDim.x);
+    ss = block_sum2(ss, 0.f, red[flip]).x;
+    const float rstd = __frsqrt_rn(ss / float(n) + p.eps);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int64_t v = threadIdx.x + i * blockDim.x;
-      if (hrow && v * E < p.N) store_row(hrow, v, p.N, h[i]);
-      emit(v, h[i], rstd);
-    }
-  } else {
-    // whole warps take part in the block maxima: round up to the block
-    for (int64_t v = threadIdx.x; v < (vectors + 31) / 32 * 32; v += blockDim.x) {
-      load(v, h[0]);
-      if (hrow && v * E < p.N) store_row(hrow, v, p.N, h[0]);
-      emit(v, h[0], rstd);
+      const bool live = v * E < n;
+      if (p.H && live)
+        store_row<T, TAIL>(static_cast<T*>(p.H) + row * p.ldh, v, n, h[i]);
+      float y[E];
+      load_weight<T>(p.W, w32, v, n, y);
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        y[j] = h[i][j] * rstd * y[j];
+        // columns past the end (rstd may be infinite or NaN) do not count
+        if (TAIL && v * E + j >= n) y[j] = 0.f;
+        m = abs_max(m, y[j]);
+      }
+      if (!live) m = 0.f;
+      if (p.Y && live)
+        store_row<T, TAIL>(static_cast<T*>(p.Y) + row * p.ldy, v, n, y);
+      if (!p.Q) continue;
+#pragma unroll
+      for (int d = kLanes / 2; d > 0; d >>= 1)
+        m = abs_max(m, __shfl_xor_sync(0xffffffffu, m, d));
+      const float s = block_scale<false>(abs_bits(m), p.pow2);
+      if (!live) continue;
+      store_f8<false, E, TAIL>(static_cast<uint8_t*>(p.Q) + row * p.ldq, v, n, y,
+                               __fdiv_rn(1.f, s));
+      if (threadIdx.x % kLanes == 0)
+        p.S[row * p.s_row + (v * E / kScaleBlock) * p.s_blk] = s;
     }
   }
 }
 
-// Rows b, b + gridDim.x, ... per block.  The block's share of dw stays in
-// registers and goes to row b of `part` at the end (VPT = 0: it is added up
-// there); the shares are added in a fixed order by sum_parts_kernel, so the
-// result does not change from run to run.
-template <class T, int VPT>
+// Rows wider than the registers hold: one row per block, read twice.
+template <class T>
 __global__ void __launch_bounds__(1024)
+    rmsnorm_wide_kernel(const NormProblem p, bool w32) {
+  constexpr int E = Vec<T>::kN;
+  constexpr int kLanes = kScaleBlock / E;
+  __shared__ float2 red[32];
+  const int64_t row = blockIdx.x, n = p.N;
+  const T* x = static_cast<const T*>(p.X) + row * p.ldx;
+  const T* r = p.R ? static_cast<const T*>(p.R) + row * p.ldr : nullptr;
+  float h[E];
+  auto load = [&](int64_t v) {
+    load_row(x, v, n, h);
+    if (r) {
+      float t[E];
+      load_row(r, v, n, t);
+#pragma unroll
+      for (int j = 0; j < E; ++j) h[j] += t[j];
+    }
+  };
+  const int64_t vectors = (n + E - 1) / E;
+  float ss = 0.f;
+  for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
+    load(v);
+#pragma unroll
+    for (int j = 0; j < E; ++j) ss = fmaf(h[j], h[j], ss);
+  }
+  ss = block_sum2(ss, 0.f, red).x;
+  const float rstd = __frsqrt_rn(ss / float(n) + p.eps);
+  // whole warps take part in the block maxima: round up to the block
+  for (int64_t v = threadIdx.x; v < (vectors + 31) / 32 * 32; v += blockDim.x) {
+    load(v);
+    const bool live = v < vectors;
+    if (p.H && live) store_row(static_cast<T*>(p.H) + row * p.ldh, v, n, h);
+    float y[E];
+    load_weight<T>(p.W, w32, v, n, y);
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      y[j] = v * E + j < n ? h[j] * rstd * y[j] : 0.f;
+      m = abs_max(m, y[j]);
+    }
+    if (p.Y && live) store_row(static_cast<T*>(p.Y) + row * p.ldy, v, n, y);
+    if (!p.Q) continue;
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1)
+      m = abs_max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float s = block_scale<false>(abs_bits(m), p.pow2);
+    if (!live) continue;
+    store_f8<false>(static_cast<uint8_t*>(p.Q) + row * p.ldq, v, n, y,
+                    __fdiv_rn(1.f, s));
+    if (threadIdx.x % kLanes == 0)
+      p.S[row * p.s_row + (v * E / kScaleBlock) * p.s_blk] = s;
+  }
+}
+
+// Rows b, b + gridDim.x, ... per block, the next row's loads issued before
+// this row's sums are exchanged.  The block's share of dw stays in registers
+// and goes to row b of `part` at the end; the shares are added in a fixed
+// order by sum_parts_kernel, so the result does not change from run to run.
+template <class T, int VPT, int MAXT, bool TAIL>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1)
     rmsnorm_backward_kernel(const NormBackProblem p, bool w32,
                             float* __restrict__ part) {
   constexpr int E = Vec<T>::kN;
-  constexpr int V = VPT > 0 ? VPT : 1;
   __shared__ float2 red[2][32];
-  float dw[V][E], w[V][E];
-  if constexpr (VPT > 0) {
+  const T* const DY = static_cast<const T*>(p.DY);
+  const T* const H = static_cast<const T*>(p.H);
+  const int64_t n = p.N;
+  float dw[VPT][E];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      load_weight<T>(p.W, w32, threadIdx.x + i * blockDim.x, p.N, w[i]);
+  for (int i = 0; i < VPT; ++i)
 #pragma unroll
-      for (int j = 0; j < E; ++j) dw[i][j] = 0.f;
+    for (int j = 0; j < E; ++j) dw[i][j] = 0.f;
+  uint4 dr[VPT], hr[VPT];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      hr[i] = load_raw(H + row * p.ldh, threadIdx.x + i * blockDim.x, n);
+      dr[i] = load_raw(DY + row * p.lddy, threadIdx.x + i * blockDim.x, n);
     }
-  }
-  const int64_t vectors = (p.N + E - 1) / E;
-  float* mine = part + int64_t(blockIdx.x) * p.N;
+  };
+  if (blockIdx.x < p.M) fetch(blockIdx.x);
   int flip = 0;
   for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, flip ^= 1) {
-    const T* dyr = static_cast<const T*>(p.DY) + row * p.lddy;
-    const T* hr = static_cast<const T*>(p.H) + row * p.ldh;
-    const T* rr = p.R ? static_cast<const T*>(p.R) + row * p.ldr : nullptr;
-    T* dxr = static_cast<T*>(p.DX) + row * p.lddx;
-    float dy[V][E], h[V][E];
+    float dy[VPT][E], h[VPT][E];
+    uint4 rr[VPT];
     float ss = 0.f, gh = 0.f;
-    auto sums = [&](int i) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int64_t v = threadIdx.x + i * blockDim.x;
+      if (p.R) rr[i] = load_raw(static_cast<const T*>(p.R) + row * p.ldr, v, n);
+      Vec<T>::unpack(hr[i], h[i]);
+      Vec<T>::unpack(dr[i], dy[i]);
+      if constexpr (TAIL) {
+        clear_tail<T>(v, n, h[i]);
+        clear_tail<T>(v, n, dy[i]);
+      }
+      float w[E];
+      load_weight<T>(p.W, w32, v, n, w);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         ss = fmaf(h[i][j], h[i][j], ss);
-        gh = fmaf(dy[i][j] * w[i][j], h[i][j], gh);
+        gh = fmaf(dy[i][j] * w[j], h[i][j], gh);
       }
+    }
+    if (row + gridDim.x < p.M) fetch(row + gridDim.x);
+    const float2 s = block_sum2(ss, gh, red[flip]);
+    const float rstd = __frsqrt_rn(s.x / float(n) + p.eps);
+    const float c = rstd * rstd * rstd * (s.y / float(n));
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int64_t v = threadIdx.x + i * blockDim.x;
+      float w[E], o[E];
+      load_weight<T>(p.W, w32, v, n, w);
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const float d = dy[i][j] * rstd;
+        dw[i][j] = fmaf(d, h[i][j], dw[i][j]);
+        o[j] = fmaf(d, w[j], -c * h[i][j]);
+      }
+      if (p.R) {
+        float r[E];
+        Vec<T>::unpack(rr[i], r);
+#pragma unroll
+        for (int j = 0; j < E; ++j) o[j] += r[j];
+      }
+      if (v * E < n)
+        store_row<T, TAIL>(static_cast<T*>(p.DX) + row * p.lddx, v, n, o);
+    }
+  }
+  float* mine = part + int64_t(blockIdx.x) * n;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const int64_t at = (threadIdx.x + int64_t(i) * blockDim.x) * E + j;
+      if (at < n) mine[at] = dw[i][j];
+    }
+}
+
+// Rows wider than the registers hold: read twice, dw added up in `part`.
+template <class T>
+__global__ void __launch_bounds__(1024)
+    rmsnorm_backward_wide_kernel(const NormBackProblem p, bool w32,
+                                 float* __restrict__ part) {
+  constexpr int E = Vec<T>::kN;
+  __shared__ float2 red[2][32];
+  const int64_t n = p.N, vectors = (n + E - 1) / E;
+  float* mine = part + int64_t(blockIdx.x) * n;
+  float dy[E], h[E], w[E];
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, flip ^= 1) {
+    auto load = [&](int64_t v) {
+      load_row(static_cast<const T*>(p.H) + row * p.ldh, v, n, h);
+      load_row(static_cast<const T*>(p.DY) + row * p.lddy, v, n, dy);
+      load_weight<T>(p.W, w32, v, n, w);
     };
-    if constexpr (VPT > 0) {
+    float ss = 0.f, gh = 0.f;
+    for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
+      load(v);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        load_row(hr, threadIdx.x + i * blockDim.x, p.N, h[i]);
-        load_row(dyr, threadIdx.x + i * blockDim.x, p.N, dy[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i) sums(i);
-    } else {
-      for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
-        load_row(hr, v, p.N, h[0]);
-        load_row(dyr, v, p.N, dy[0]);
-        load_weight<T>(p.W, w32, v, p.N, w[0]);
-        sums(0);
+      for (int j = 0; j < E; ++j) {
+        ss = fmaf(h[j], h[j], ss);
+        gh = fmaf(dy[j] * w[j], h[j], gh);
       }
     }
     const float2 s = block_sum2(ss, gh, red[flip]);
-    const float rstd = __frsqrt_rn(s.x / float(p.N) + p.eps);
-    const float c = rstd * rstd * (s.y / float(p.N));
-    auto emit = [&](int i, int64_t v) {
-      if (v * E >= p.N) return;
+    const float rstd = __frsqrt_rn(s.x / float(n) + p.eps);
+    const float c = rstd * rstd * rstd * (s.y / float(n));
+    for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
+      load(v);
       float o[E], r[E];
-      if (rr) load_row(rr, v, p.N, r);
+      if (p.R) load_row(static_cast<const T*>(p.R) + row * p.ldr, v, n, r);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        o[j] = rstd * (dy[i][j] * w[i][j] - h[i][j] * c);
-        if (rr) o[j] += r[j];
+        const float d = dy[j] * rstd;
+        o[j] = fmaf(d, w[j], -c * h[j]) + (p.R ? r[j] : 0.f);
+        const int64_t at = v * E + j;
+        if (at < n)
+          mine[at] = fmaf(d, h[j], row == blockIdx.x ? 0.f : mine[at]);
       }
-      store_row(dxr, v, p.N, o);
-    };
-    if constexpr (VPT > 0) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        emit(i, threadIdx.x + i * blockDim.x);
-#pragma unroll
-        for (int j = 0; j < E; ++j) dw[i][j] = fmaf(dy[i][j] * rstd, h[i][j], dw[i][j]);
-      }
-    } else {
-      for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
-        load_row(hr, v, p.N, h[0]);
-        load_row(dyr, v, p.N, dy[0]);
-        load_weight<T>(p.W, w32, v, p.N, w[0]);
-        emit(0, v);
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const int64_t n = v * E + j;
-          if (n < p.N)
-            mine[n] = fmaf(dy[0][j] * rstd, h[0][j],
-                           row == blockIdx.x ? 0.f : mine[n]);
-        }
-      }
+      store_row(static_cast<T*>(p.DX) + row * p.lddx, v, n, o);
     }
-  }
-  if constexpr (VPT > 0) {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int64_t n = (threadIdx.x + int64_t(i) * blockDim.x) * E + j;
-        if (n < p.N) mine[n] = dw[i][j];
-      }
   }
 }
 
@@ -268,43 +351,68 @@ __global__ void __launch_bounds__(1024)
   if (threadIdx.x == 0 && c < n) out[c] = s;
 }
 
-int backward_blocks(int num_sms, int64_t M) {
-  const int64_t most = int64_t(num_sms) * 2;
-  return int(M < most ? M : most);
-}
+constexpr int kMostParts = 304;  // blocks of the backward pass, two per SM
 
-// Vectors per thread and threads per block for rows of `vectors` vectors.
-void shape(int64_t vectors, int* vpt, int* threads) {
-  *vpt = vectors <= 512 ? 1 : vectors <= 1024 ? 2 : vectors <= 4096 ? 4 : 0;
-  const int64_t per = *vpt ? (vectors + *vpt - 1) / *vpt : 1024;
-  *threads = int((per + 31) / 32 * 32);
+// Calls f(VPT, MAXT, threads) for rows of `vectors` vectors: up to 256
+// threads with up to 4 vectors each, so that several rows are under way per
+// SM, wider rows up to 512 threads.  False: too wide.
+template <class F>
+bool with_shape(int64_t vectors, F&& f) {
+  auto threads = [&](int vpt) { return int((vectors + vpt - 1) / vpt + 31) / 32 * 32; };
+  using std::integral_constant;
+#define MMA_SHAPE(V, T) \
+  f(integral_constant<int, V>{}, integral_constant<int, T>{}, threads(V)), true
+  if (vectors <= 256) return MMA_SHAPE(1, 256);
+  if (vectors <= 512) return MMA_SHAPE(2, 256);
+  if (vectors <= 768) return MMA_SHAPE(3, 256);
+  if (vectors <= 1024) return MMA_SHAPE(4, 256);
+  if (vectors <= 2048) return MMA_SHAPE(4, 512);
+#undef MMA_SHAPE
+  return false;
 }
 
 template <class T>
 mma_status_t forward(const Ctx& ctx, const NormProblem& p, bool w32) {
-  int vpt, threads;
-  shape((p.N + Vec<T>::kN - 1) / Vec<T>::kN, &vpt, &threads);
-  const unsigned grid = unsigned(p.M);
-  switch (vpt) {
-    case 1: rmsnorm_kernel<T, 1><<<grid, threads, 0, ctx.stream>>>(p, w32); break;
-    case 2: rmsnorm_kernel<T, 2><<<grid, threads, 0, ctx.stream>>>(p, w32); break;
-    case 4: rmsnorm_kernel<T, 4><<<grid, threads, 0, ctx.stream>>>(p, w32); break;
-    default: rmsnorm_kernel<T, 0><<<grid, threads, 0, ctx.stream>>>(p, w32);
-  }
+  constexpr int E = Vec<T>::kN;
+  const int64_t vectors = (p.N + E - 1) / E;
+  auto launch = [&](auto vpt, auto maxt, int threads) {
+    constexpr int V = decltype(vpt)::value, B = decltype(maxt)::value;
+    // as many blocks as run at once, each taking rows in turn
+    const int64_t most = int64_t(ctx.num_sms) * (768 / threads + (threads > 768));
+    const unsigned grid = unsigned(std::min(p.M, most));
+    if (p.N % E)
+      rmsnorm_kernel<T, V, B, true><<<grid, threads, 0, ctx.stream>>>(p, w32);
+    else
+      rmsnorm_kernel<T, V, B, false><<<grid, threads, 0, ctx.stream>>>(p, w32);
+  };
+  bool fits = true;
+  if (p.M <= ctx.num_sms && vectors <= 1024)
+    // one row per SM at most: the whole row at once
+    launch(std::integral_constant<int, 1>{}, std::integral_constant<int, 1024>{},
+           int(vectors + 31) / 32 * 32);
+  else
+    fits = with_shape(vectors, launch);
+  if (!fits)
+    rmsnorm_wide_kernel<T><<<unsigned(p.M), 1024, 0, ctx.stream>>>(p, w32);
   return cudaGetLastError() == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
 }
 
 template <class T>
 mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32,
                       float* part) {
-  int vpt, threads;
-  shape((p.N + Vec<T>::kN - 1) / Vec<T>::kN, &vpt, &threads);
-  const int grid = backward_blocks(ctx.num_sms, p.M);
-  if (grid > 0) switch (vpt) {
-    case 1: rmsnorm_backward_kernel<T, 1><<<grid, threads, 0, ctx.stream>>>(p, w32, part); break;
-    case 2: rmsnorm_backward_kernel<T, 2><<<grid, threads, 0, ctx.stream>>>(p, w32, part); break;
-    case 4: rmsnorm_backward_kernel<T, 4><<<grid, threads, 0, ctx.stream>>>(p, w32, part); break;
-    default: rmsnorm_backward_kernel<T, 0><<<grid, threads, 0, ctx.stream>>>(p, w32, part);
+  constexpr int E = Vec<T>::kN;
+  const int grid = int(std::min<int64_t>(p.M, std::min(kMostParts, 2 * ctx.num_sms)));
+  if (grid > 0) {
+    const bool fits = with_shape(
+        (p.N + E - 1) / E, [&](auto vpt, auto maxt, int threads) {
+          constexpr int V = decltype(vpt)::value, B = decltype(maxt)::value;
+          if (p.N % E)
+            rmsnorm_backward_kernel<T, V, B, true><<<grid, threads, 0, ctx.stream>>>(p, w32, part);
+          else
+            rmsnorm_backward_kernel<T, V, B, false><<<grid, threads, 0, ctx.stream>>>(p, w32, part);
+        });
+    if (!fits)
+      rmsnorm_backward_wide_kernel<T><<<grid, 1024, 0, ctx.stream>>>(p, w32, part);
   }
   sum_parts_kernel<<<unsigned((p.N + 31) / 32), dim3(32, 32), 0, ctx.stream>>>(
       part, grid, p.N, p.DW);
@@ -322,8 +430,8 @@ mma_status_t launch_rmsnorm(const Ctx& ctx, const NormProblem& p) {
   }
 }
 
-size_t rmsnorm_backward_workspace_bytes(int num_sms, int64_t M, int64_t N) {
-  return size_t(backward_blocks(num_sms, M)) * size_t(N) * 4;
+int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t N) {
+  return std::min<int64_t>(M, kMostParts) * N * 4;
 }
 
 mma_status_t launch_rmsnorm_backward(const Ctx& ctx, const NormBackProblem& p,
