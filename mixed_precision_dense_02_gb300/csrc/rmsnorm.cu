@@ -20,6 +20,7 @@
 #include <type_traits>
 
 #include "f8_common.cuh"
+#include "ptx.cuh"
 
 namespace mmagb {
 namespace {
@@ -199,92 +200,129 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// Rows b, b + gridDim.x, ... per block, the next row's loads issued before
-// this row's sums are exchanged.  The block's share of dw stays in registers
-// and goes to row b of `part` at the end; the shares are added in a fixed
-// order by sum_parts_kernel, so the result does not change from run to run.
-template <class T, int VPT, int MAXT, bool TAIL>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1)
-    rmsnorm_backward_kernel(const NormBackProblem p, bool w32,
-                            float* __restrict__ part) {
+// Rows b, b + gridDim.x, ... per block, through a ring of `stages` rows of
+// h, dy and r in shared memory that bulk copies fill ahead; each thread
+// reads its VPT vectors twice, for the sums and for the output, so that only
+// its share of dw stays in registers.  That goes to row b of `part` at the
+// end; the shares are added in a fixed order by sum_parts_kernel, so the
+// result does not change from run to run.
+template <class T, int VPT>
+__global__ void __launch_bounds__(512, VPT <= 2 ? 2 : 1)
+    rmsnorm_backward_kernel(const NormBackProblem p, bool w32, int stages,
+                            int row_bytes, float* __restrict__ part,
+                            unsigned* status) {
   constexpr int E = Vec<T>::kN;
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[2][32];
-  const T* const DY = static_cast<const T*>(p.DY);
-  const T* const H = static_cast<const T*>(p.H);
+  __shared__ uint64_t full[4];
+  __shared__ int abort_flag;
   const int64_t n = p.N;
+  const int tensors = p.R ? 3 : 2;
+  const int stage_bytes = tensors * row_bytes;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    abort_flag = 0;
+    fence_mbarrier_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  auto fetch = [&](int64_t row, int s) {
+    if (row >= p.M) return;
+    uint8_t* dst = ring + s * stage_bytes;
+    mbar_arrive_expect_tx(&full[s], uint32_t(stage_bytes));
+    bulk_load(dst, static_cast<const T*>(p.H) + row * p.ldh, row_bytes, &full[s]);
+    bulk_load(dst + row_bytes, static_cast<const T*>(p.DY) + row * p.lddy,
+              row_bytes, &full[s]);
+    if (p.R)
+      bulk_load(dst + 2 * row_bytes, static_cast<const T*>(p.R) + row * p.ldr,
+                row_bytes, &full[s]);
+  };
+  if (threadIdx.x == 0)
+    for (int s = 0; s < stages; ++s)
+      fetch(blockIdx.x + int64_t(s) * gridDim.x, s);
   float dw[VPT][E];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int j = 0; j < E; ++j) dw[i][j] = 0.f;
-  uint4 dr[VPT], hr[VPT];
-  auto fetch = [&](int64_t row) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      hr[i] = load_raw(H + row * p.ldh, threadIdx.x + i * blockDim.x, n);
-      dr[i] = load_raw(DY + row * p.lddy, threadIdx.x + i * blockDim.x, n);
-    }
+  // vector v of a row in the ring, zeros beyond the row
+  auto load = [&](const uint8_t* row, int v, float (&f)[E]) {
+    const bool in = int64_t(v) * E < n;
+    Vec<T>::unpack(in ? *(reinterpret_cast<const uint4*>(row) + v)
+                      : make_uint4(0, 0, 0, 0), f);
+    clear_tail<T>(v, n, f);
   };
-  if (blockIdx.x < p.M) fetch(blockIdx.x);
-  int flip = 0;
-  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, flip ^= 1) {
-    float dy[VPT][E], h[VPT][E];
-    uint4 rr[VPT];
+  int s = 0, flip = 0;
+  uint32_t phase = 0;
+  const float over_n = 1.f / float(n);
+  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
+    const uint8_t* hs = ring + s * stage_bytes;
+    const uint8_t* ds = hs + row_bytes;
+    const uint8_t* rs = ds + row_bytes;
+    // (after a failed wait the rest runs on whatever is there; the status
+    // word tells)
+    mbar_wait(&full[s], phase, &abort_flag, status);
     float ss = 0.f, gh = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int64_t v = threadIdx.x + i * blockDim.x;
-      if (p.R) rr[i] = load_raw(static_cast<const T*>(p.R) + row * p.ldr, v, n);
-      Vec<T>::unpack(hr[i], h[i]);
-      Vec<T>::unpack(dr[i], dy[i]);
-      if constexpr (TAIL) {
-        clear_tail<T>(v, n, h[i]);
-        clear_tail<T>(v, n, dy[i]);
-      }
-      float w[E];
+      const int v = threadIdx.x + i * blockDim.x;
+      float h[E], dy[E], w[E];
+      load(hs, v, h);
+      load(ds, v, dy);
       load_weight<T>(p.W, w32, v, n, w);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        ss = fmaf(h[i][j], h[i][j], ss);
-        gh = fmaf(dy[i][j] * w[j], h[i][j], gh);
+        ss = fmaf(h[j], h[j], ss);
+        gh = fmaf(dy[j] * w[j], h[j], gh);
       }
     }
-    if (row + gridDim.x < p.M) fetch(row + gridDim.x);
-    const float2 s = block_sum2(ss, gh, red[flip]);
-    const float rstd = __frsqrt_rn(s.x / float(n) + p.eps);
-    const float c = rstd * rstd * rstd * (s.y / float(n));
+    const float2 sum = block_sum2(ss, gh, red[flip]);
+    if (blockDim.x == 32) __syncwarp();
+    // Every thread is past the row before: its stage takes the row that is
+    // `stages` rows after it.
+    if (threadIdx.x == 0 && row != blockIdx.x)
+      fetch(row + int64_t(stages - 1) * gridDim.x, s == 0 ? stages - 1 : s - 1);
+    const float rstd = __frsqrt_rn(sum.x * over_n + p.eps);
+    const float c = rstd * rstd * rstd * (sum.y * over_n);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int64_t v = threadIdx.x + i * blockDim.x;
-      float w[E], o[E];
+      const int v = threadIdx.x + i * blockDim.x;
+      if (int64_t(v) * E >= n) continue;
+      float h[E], dy[E], w[E], o[E];
+      load(hs, v, h);
+      load(ds, v, dy);
       load_weight<T>(p.W, w32, v, n, w);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        const float d = dy[i][j] * rstd;
-        dw[i][j] = fmaf(d, h[i][j], dw[i][j]);
-        o[j] = fmaf(d, w[j], -c * h[i][j]);
+        const float d = dy[j] * rstd;
+        dw[i][j] = fmaf(d, h[j], dw[i][j]);
+        o[j] = fmaf(d, w[j], -c * h[j]);
       }
       if (p.R) {
         float r[E];
-        Vec<T>::unpack(rr[i], r);
+        load(rs, v, r);
 #pragma unroll
         for (int j = 0; j < E; ++j) o[j] += r[j];
       }
-      if (v * E < n)
-        store_row<T, TAIL>(static_cast<T*>(p.DX) + row * p.lddx, v, n, o);
+      store_row(static_cast<T*>(p.DX) + row * p.lddx, v, n, o);
     }
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+    flip ^= 1;
   }
   float* mine = part + int64_t(blockIdx.x) * n;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i)
+  for (int i = 0; i < VPT; ++i) {
+    const int64_t at = int64_t(threadIdx.x + i * blockDim.x) * E;
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const int64_t at = (threadIdx.x + int64_t(i) * blockDim.x) * E + j;
-      if (at < n) mine[at] = dw[i][j];
-    }
+    for (int j = 0; j < E; ++j)
+      if (at + j < n) mine[at + j] = dw[i][j];
+  }
 }
 
-// Rows wider than the registers hold: read twice, dw added up in `part`.
+// Rows too wide for that: read twice, dw added up in `part`.
 template <class T>
 __global__ void __launch_bounds__(1024)
     rmsnorm_backward_wide_kernel(const NormBackProblem p, bool w32,
@@ -402,17 +440,34 @@ mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32,
                       float* part) {
   constexpr int E = Vec<T>::kN;
   const int grid = int(std::min<int64_t>(p.M, std::min(kMostParts, 2 * ctx.num_sms)));
-  if (grid > 0) {
-    const bool fits = with_shape(
-        (p.N + E - 1) / E, [&](auto vpt, auto maxt, int threads) {
-          constexpr int V = decltype(vpt)::value, B = decltype(maxt)::value;
-          if (p.N % E)
-            rmsnorm_backward_kernel<T, V, B, true><<<grid, threads, 0, ctx.stream>>>(p, w32, part);
-          else
-            rmsnorm_backward_kernel<T, V, B, false><<<grid, threads, 0, ctx.stream>>>(p, w32, part);
-        });
-    if (!fits)
-      rmsnorm_backward_wide_kernel<T><<<grid, 1024, 0, ctx.stream>>>(p, w32, part);
+  const int64_t vectors = (p.N + E - 1) / E;
+  // Two blocks per SM and two to four rows ahead, as far as 220 KB allow.
+  const int vpt = vectors <= 512 ? 1 : vectors <= 1024 ? 2 : 4;
+  const int64_t stage = vectors * 16 * (p.R ? 3 : 2);
+  const int64_t room = (vpt <= 2 ? 110 : 220) * 1024;
+  const int stages = int(std::min<int64_t>(4, room / std::max<int64_t>(stage, 1)));
+  if (grid > 0 && vectors <= 2048 && stages >= 2) {
+    const int threads = int((vectors + vpt - 1) / vpt + 31) / 32 * 32;
+    auto run = [&](auto kernel, PerContext<bool>& attr) {
+      bool ok = false;
+      if (!attr.get(ctx, &ok, [&](bool* v) {
+            *v = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      220 * 1024) == cudaSuccess;
+            if (!*v) cudaGetLastError();
+            return *v;
+          }))
+        return false;
+      kernel<<<grid, threads, size_t(stages) * stage, ctx.stream>>>(
+          p, w32, stages, int(vectors * 16), part, ctx.status);
+      return true;
+    };
+    static PerContext<bool> a1, a2, a4;
+    const bool ok = vpt == 1   ? run(rmsnorm_backward_kernel<T, 1>, a1)
+                    : vpt == 2 ? run(rmsnorm_backward_kernel<T, 2>, a2)
+                               : run(rmsnorm_backward_kernel<T, 4>, a4);
+    if (!ok) return MMA_ERR_LAUNCH;
+  } else if (grid > 0) {
+    rmsnorm_backward_wide_kernel<T><<<grid, 1024, 0, ctx.stream>>>(p, w32, part);
   }
   sum_parts_kernel<<<unsigned((p.N + 31) / 32), dim3(32, 32), 0, ctx.stream>>>(
       part, grid, p.N, p.DW);
