@@ -15,9 +15,15 @@
 // Bound by memory: x is read once, q written once.
 #include <algorithm>
 
+#include <cudaTypedefs.h>
+
 #include "f8_common.cuh"
+#include "ptx.cuh"
 
 namespace mmagb {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // gemm_tc.cu
+
 namespace {
 
 // Blocks of 1 x 128, not transposed: a group of lanes per block of columns,
@@ -69,116 +75,202 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// One 128 x 128 tile per block, held in registers: a thread has RPT
+// 128 x 128 tiles in turn per block, the next two on their way by TMA while
+// one is worked on (one tile per block, loaded by its threads, left memory
+// idle in between: 4000 x 8192 FP32 took 60 us).  A thread has RPT = 8
 // consecutive rows of one vector of E columns.  SQUARE: one scale for the
 // tile, else (transposed only) one per column.  The transposed bytes go
-// through shared memory, RPT of one column at a time.
+// through shared memory, eight of one column at a time; a row's 8-byte pieces
+// are permuted by the column's vector so that neither side has bank
+// conflicts.
+template <class T>
+struct Tile {
+  static constexpr int E = Vec<T>::kN;
+  static constexpr int VEC = kScaleBlock / E;   // vectors per tile row
+  static constexpr int RPT = 8;
+  static constexpr int THREADS = VEC * kScaleBlock / RPT;
+  static constexpr int BYTES = kScaleBlock * kScaleBlock * int(sizeof(T));
+  static constexpr int STAGES = 2;
+  static constexpr int SMEM = STAGES * BYTES + kScaleBlock * kScaleBlock + 128;
+  static constexpr int PER_SM = sizeof(T) == 4 ? 1 : 2;
+};
+
 template <class T, bool E5M2, bool SQUARE, bool TRANS>
-__global__ void __launch_bounds__(256)
-    quantize_tile_kernel(const QuantProblem p, int64_t tiles_n) {
-  constexpr int E = Vec<T>::kN;
-  constexpr int VEC = kScaleBlock / E;  // vectors per tile row
-  constexpr int TR = 256 / VEC;         // rows of threads
-  constexpr int RPT = kScaleBlock / TR;
-  constexpr int PITCH = 144;
-  __shared__ uint32_t red[SQUARE ? 8 : TR * kScaleBlock];
+__global__ void __launch_bounds__(Tile<T>::THREADS, Tile<T>::PER_SM)
+    quantize_tile_kernel(const __grid_constant__ CUtensorMap map,
+                         const QuantProblem p, int64_t tiles_n, int64_t tiles,
+                         unsigned* status) {
+  using L = Tile<T>;
+  constexpr int E = L::E, VEC = L::VEC, RPT = L::RPT;
+  constexpr int TR = kScaleBlock / RPT;  // rows of threads
+  constexpr int WARPS = L::THREADS / 32;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  uint8_t* turned = smem + L::STAGES * L::BYTES;
+  __shared__ float red[SQUARE ? 2 * WARPS : TR * kScaleBlock];
   __shared__ float inv_of[SQUARE ? 1 : kScaleBlock];
-  __shared__ __align__(16) uint8_t turned[TRANS ? kScaleBlock * PITCH : 16];
-  const int64_t tm = blockIdx.x / tiles_n, tn = blockIdx.x - tm * tiles_n;
-  const int64_t m0 = tm * kScaleBlock, n0 = tn * kScaleBlock;
+  __shared__ uint64_t full[L::STAGES];
+  __shared__ int abort_flag;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::STAGES; ++s) mbar_init(&full[s], 1);
+    abort_flag = 0;
+    fence_mbarrier_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  auto fetch = [&](int64_t t, int s) {
+    if (t >= tiles) return;
+    mbar_arrive_expect_tx(&full[s], L::BYTES);
+    tma_load_3d(&map, &full[s], smem + s * L::BYTES,
+                int(t % tiles_n) * kScaleBlock, int(t / tiles_n) * kScaleBlock, 0);
+  };
+  if (threadIdx.x == 0)
+    for (int s = 0; s < L::STAGES; ++s)
+      fetch(blockIdx.x + int64_t(s) * gridDim.x, s);
   const int c = threadIdx.x % VEC, tr = threadIdx.x / VEC;
-  const int64_t v = n0 / E + c;
-  float x[RPT][E];
+  int s = 0, flip = 0;
+  uint32_t phase = 0;
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, flip ^= 1) {
+    const int64_t tm = t / tiles_n, tn = t - tm * tiles_n;
+    const int64_t m0 = tm * kScaleBlock, n0 = tn * kScaleBlock;
+    // (after a failed wait the rest runs on whatever is there; the status
+    // word tells)
+    mbar_wait(&full[s], phase, &abort_flag, status);
+    float x[RPT][E];
+    const uint4* src = reinterpret_cast<const uint4*>(smem + s * L::BYTES);
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const int64_t row = m0 + tr * RPT + i;
-    if (row < p.M)
-      load_row(static_cast<const T*>(p.X) + row * p.ldx, v, p.N, x[i]);
-    else
-      for (int j = 0; j < E; ++j) x[i][j] = 0.f;
-  }
-  float inv[SQUARE ? 1 : E];
-  if constexpr (SQUARE) {
-    uint32_t m = 0;
+    for (int i = 0; i < RPT; ++i) Vec<T>::unpack(src[(tr * RPT + i) * VEC + c], x[i]);
+    float inv[SQUARE ? 1 : E];
+    if constexpr (SQUARE) {
+      float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < RPT; ++i)
+      for (int i = 0; i < RPT; ++i)
 #pragma unroll
-      for (int j = 0; j < E; ++j) m = max(m, abs_bits(x[i][j]));
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-    __syncthreads();
-    for (int w = 0; w < 8; ++w) m = max(m, red[w]);
-    const float s = block_scale<E5M2>(m, p.pow2);
-    inv[0] = __fdiv_rn(1.f, s);
-    if (threadIdx.x == 0)
-      p.S[(TRANS ? tn : tm) * p.s_row + (TRANS ? tm : tn) * p.s_blk] = s;
-  } else {
+        for (int j = 0; j < E; ++j) m = abs_max(m, x[i][j]);
+      const uint32_t w = __reduce_max_sync(0xffffffffu, abs_bits(m));
+      if ((threadIdx.x & 31) == 0) red[flip * WARPS + (threadIdx.x >> 5)] = __uint_as_float(w);
+      __syncthreads();
+      m = 0.f;
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      uint32_t m = 0;
+      for (int k = 0; k < WARPS; ++k) m = abs_max(m, red[flip * WARPS + k]);
+      const float sc = block_scale<E5M2>(abs_bits(m), p.pow2);
+      inv[0] = __fdiv_rn(1.f, sc);
+      if (threadIdx.x == 0)
+        p.S[(TRANS ? tn : tm) * p.s_row + (TRANS ? tm : tn) * p.s_blk] = sc;
+    } else {
 #pragma unroll
-      for (int i = 0; i < RPT; ++i) m = max(m, abs_bits(x[i][j]));
-      red[tr * kScaleBlock + c * E + j] = m;
-    }
-    __syncthreads();
-    if (threadIdx.x < kScaleBlock) {
-      uint32_t m = 0;
-      for (int t = 0; t < TR; ++t) m = max(m, red[t * kScaleBlock + threadIdx.x]);
-      const float s = block_scale<E5M2>(m, p.pow2);
-      inv_of[threadIdx.x] = __fdiv_rn(1.f, s);
-      if (n0 + threadIdx.x < p.N)
-        p.S[(n0 + threadIdx.x) * p.s_row + tm * p.s_blk] = s;
-    }
-    __syncthreads();
+      for (int j = 0; j < E; ++j) {
+        float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < E; ++j) inv[j] = inv_of[c * E + j];
-  }
-  if constexpr (!TRANS) {
-    if (v * E < p.N)
-#pragma unroll
-      for (int i = 0; i < RPT; ++i) {
-        const int64_t row = m0 + tr * RPT + i;
-        if (row < p.M)
-          store_f8<E5M2>(static_cast<uint8_t*>(p.Q) + row * p.ldq, v, p.N, x[i],
-                         inv[0]);
+        for (int i = 0; i < RPT; ++i) m = abs_max(m, x[i][j]);
+        red[tr * kScaleBlock + j * VEC + c] = m;  // j-major: no conflicts
       }
-  } else {
+      __syncthreads();
+      if (threadIdx.x < kScaleBlock) {
+        const int col = (threadIdx.x % VEC) * E + threadIdx.x / VEC;
+        float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const float f = inv[SQUARE ? 0 : j];
-      uint32_t w[RPT / 4];
-#pragma unroll
-      for (int i = 0; i < RPT / 4; ++i)
-        w[i] = to_f8x2<E5M2>(x[4 * i][j] * f, x[4 * i + 1][j] * f) |
-               (to_f8x2<E5M2>(x[4 * i + 2][j] * f, x[4 * i + 3][j] * f) << 16);
-      uint8_t* dst = turned + (c * E + j) * PITCH + tr * RPT;
-      if constexpr (RPT == 8)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-      else
-        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int k = 0; k < TR; ++k) m = abs_max(m, red[k * kScaleBlock + threadIdx.x]);
+        const float sc = block_scale<E5M2>(abs_bits(m), p.pow2);
+        inv_of[threadIdx.x] = __fdiv_rn(1.f, sc);
+        if (n0 + col < p.N) p.S[(n0 + col) * p.s_row + tm * p.s_blk] = sc;
+      }
     }
-    __syncthreads();
-    // 16-byte chunks of the output's rows
+    // every thread has taken its part of the stage
+    if (threadIdx.x == 0) fetch(t + int64_t(L::STAGES) * gridDim.x, s);
+    if (++s == L::STAGES) {
+      s = 0;
+      phase ^= 1u;
+    }
+    if constexpr (!SQUARE) {
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = threadIdx.x + 256 * i;
-      const int n = k >> 3, m = (k & 7) * 16;
-      if (n0 + n >= p.N || m0 + m >= p.M) continue;
-      const uint8_t* src = turned + n * PITCH + m;
-      uint8_t* dst = static_cast<uint8_t*>(p.Q) + (n0 + n) * p.ldq + m0 + m;
-      if (m0 + m + 16 <= p.M) {
-        *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
-      } else {
-        for (int b = 0; m0 + m + b < p.M; ++b) dst[b] = src[b];
+      for (int j = 0; j < E; ++j) inv[j] = inv_of[j * VEC + c];
+    }
+    if constexpr (!TRANS) {
+      const int64_t v = n0 / E + c;
+      if (v * E < p.N)
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+          const int64_t row = m0 + tr * RPT + i;
+          if (row < p.M)
+            store_f8<E5M2>(static_cast<uint8_t*>(p.Q) + row * p.ldq, v, p.N, x[i],
+                           inv[0]);
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const float f = inv[SQUARE ? 0 : j];
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          w[i] = to_f8x2<E5M2>(x[4 * i][j] * f, x[4 * i + 1][j] * f) |
+                 (to_f8x2<E5M2>(x[4 * i + 2][j] * f, x[4 * i + 3][j] * f) << 16);
+        *reinterpret_cast<uint2*>(turned + (c * E + j) * kScaleBlock +
+                                  ((tr ^ (c & 15)) << 3)) = make_uint2(w[0], w[1]);
+      }
+      __syncthreads();
+      // 16-byte chunks of the output's rows
+#pragma unroll
+      for (int i = 0; i < kScaleBlock * 8 / L::THREADS; ++i) {
+        const int k = threadIdx.x + L::THREADS * i;
+        const int n = k >> 3, ch = k & 7, sw = (n / E) & 15;
+        if (n0 + n >= p.N || m0 + ch * 16 >= p.M) continue;
+        uint4 v = *reinterpret_cast<const uint4*>(turned + n * kScaleBlock +
+                                                  ((ch ^ (sw >> 1)) << 4));
+        if (sw & 1) v = make_uint4(v.z, v.w, v.x, v.y);
+        uint8_t* dst = static_cast<uint8_t*>(p.Q) + (n0 + n) * p.ldq + m0 + ch * 16;
+        if (m0 + ch * 16 + 16 <= p.M) {
+          *reinterpret_cast<uint4*>(dst) = v;
+        } else {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int b = 0; b < 15; ++b)
+            if (m0 + ch * 16 + b < p.M) dst[b] = uint8_t(w[b >> 2] >> (8 * (b & 3)));
+        }
       }
     }
   }
 }
 
+template <class T, bool E5M2, bool SQUARE, bool TRANS>
+mma_status_t run_tiles(const Ctx& ctx, const QuantProblem& p) {
+  using L = Tile<T>;
+  const int64_t tiles_n = (p.N + kScaleBlock - 1) / kScaleBlock;
+  const int64_t tiles = (p.M + kScaleBlock - 1) / kScaleBlock * tiles_n;
+  auto enc = encode_fn();
+  if (!enc) return MMA_ERR_LAUNCH;
+  CUtensorMap map;
+  cuuint64_t dims[3] = {cuuint64_t(p.N), cuuint64_t(p.M), 1};
+  cuuint64_t strides[2] = {cuuint64_t(p.ldx) * sizeof(T), cuuint64_t(p.ldx) * sizeof(T)};
+  cuuint32_t box[3] = {kScaleBlock, kScaleBlock, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  if (enc(&map, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+          3, const_cast<void*>(p.X), dims, strides, box, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return MMA_ERR_LAUNCH;
+  auto kern = quantize_tile_kernel<T, E5M2, SQUARE, TRANS>;
+  static PerContext<bool> attr;
+  bool ok = false;
+  if (!attr.get(ctx, &ok, [&](bool* v) {
+        *v = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  L::SMEM) == cudaSuccess;
+        if (!*v) cudaGetLastError();
+        return *v;
+      }))
+    return MMA_ERR_LAUNCH;
+  const unsigned grid =
+      unsigned(std::min<int64_t>(tiles, int64_t(ctx.num_sms) * L::PER_SM));
+  kern<<<grid, L::THREADS, L::SMEM, ctx.stream>>>(map, p, tiles_n, tiles, ctx.status);
+  return cudaGetLastError() == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
+}
+
 template <class T, bool E5M2>
 mma_status_t quantize(const Ctx& ctx, const QuantProblem& p) {
   const int64_t tiles_n = (p.N + kScaleBlock - 1) / kScaleBlock;
-  const int64_t tiles = (p.M + kScaleBlock - 1) / kScaleBlock * tiles_n;
   if (p.block_rows == 1 && !p.transpose) {
     constexpr int E = Vec<T>::kN;
     const int64_t vectors = tiles_n * (kScaleBlock / E);  // whole blocks
@@ -189,17 +281,11 @@ mma_status_t quantize(const Ctx& ctx, const QuantProblem& p) {
       quantize_rows_kernel<T, E5M2, true><<<grid, threads, 0, ctx.stream>>>(p);
     else
       quantize_rows_kernel<T, E5M2, false><<<grid, threads, 0, ctx.stream>>>(p);
-  } else {
-    if (tiles > INT32_MAX) return MMA_ERR_UNSUPPORTED;
-    const unsigned grid = unsigned(tiles);
-    if (!p.transpose)
-      quantize_tile_kernel<T, E5M2, true, false><<<grid, 256, 0, ctx.stream>>>(p, tiles_n);
-    else if (p.block_rows == 128)
-      quantize_tile_kernel<T, E5M2, true, true><<<grid, 256, 0, ctx.stream>>>(p, tiles_n);
-    else
-      quantize_tile_kernel<T, E5M2, false, true><<<grid, 256, 0, ctx.stream>>>(p, tiles_n);
+    return cudaGetLastError() == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
   }
-  return cudaGetLastError() == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
+  if (!p.transpose) return run_tiles<T, E5M2, true, false>(ctx, p);
+  if (p.block_rows == 128) return run_tiles<T, E5M2, true, true>(ctx, p);
+  return run_tiles<T, E5M2, false, true>(ctx, p);
 }
 
 template <class T>
