@@ -35,9 +35,15 @@
 // half of Q, so that a stage brings 32 KB per SM instead of 48; every SM
 // streaming from L2 gets about 69 bytes per clock, and the stage's MMAs take
 // 512 clocks.
+//
+// Few tiles (a token or a few through one matrix): a cluster of up to six
+// CTAs shares a tile's k range (SPLIT); the sums meet in the shared memory of
+// its first CTA, which adds them in order of rank.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -89,7 +95,7 @@ struct GroupedArgs {
   unsigned* status;
 };
 
-template <bool KIND8, bool ROWS, int CL, int BN, int STAGES>
+template <bool KIND8, bool ROWS, bool SPLIT, int CL, int BN, int STAGES>
 struct Layout {
   static constexpr int P_BYTES = kP * 128;
   static constexpr int Q_BYTES = BN / CL * 128;
@@ -105,12 +111,24 @@ struct Layout {
   static constexpr int WARP_BYTES = ROWS ? 2048 : 0;
   static constexpr int WARP_OFFSET = SCALE_OFFSET + SLOTS * SLOT_FLOATS * 4;
   static constexpr int BAR_OFFSET = WARP_OFFSET + kEpiWarps * WARP_BYTES;
-  static constexpr int NUM_BARS = 4 * STAGES + 5 + 2 * SLOTS;
+  // Accumulators in tensor memory: as many as fit (with 32 columns 256 of
+  // the 512, for two CTAs per SM).  A chunk's way through the MMAs, the
+  // epilogue and back takes some 1000 clocks whatever its size.
+  static constexpr int ACCS = BN == 32 ? 8 : 512 / BN;
+  static constexpr int NUM_BARS =
+      4 * STAGES + 1 + 2 * ACCS + 2 * SLOTS + (SPLIT ? 2 * kEpiWarps : 0);
   static constexpr int GROUP_OFFSET = BAR_OFFSET + NUM_BARS * 8 + 24;
-  static constexpr int alloc(int groups) {
-    return GROUP_OFFSET + 2 * (groups + 1) * 4 + 1024;  // base alignment
+  static constexpr int round16(int v) { return (v + 15) & ~15; }
+  // SPLIT: sums of the other ranks, for each epilogue warp
+  static constexpr int PART_FLOATS = 32 * (BN / 2);
+  static constexpr int part_offset(int groups) {
+    return round16(GROUP_OFFSET + 2 * (groups + 1) * 4);
   }
-  static constexpr uint32_t TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
+  static constexpr int alloc(int groups, int split) {
+    return part_offset(groups) + (split - 1) * kEpiWarps * PART_FLOATS * 4 +
+           1024;  // base alignment
+  }
+  static constexpr uint32_t TMEM_COLS = ACCS * BN;
 };
 
 // One tile of work.
@@ -206,13 +224,14 @@ __device__ __forceinline__ void zero_rows(uint8_t* stage, int row, int n, int la
 // KIND8: 8-bit operands with scales, else 16-bit.  P_MN, Q_MN: the operand
 // is stored with its row index contiguous (16-bit only).  RAGK: the groups
 // cut the k range (the weight gradient).  ROWS: D[p][q], the groups cut P.
-template <bool KIND8, bool P_MN, bool Q_MN, bool RAGK, bool ROWS, int CL, int BN,
-          int STAGES>
-__global__ void __launch_bounds__(kThreads, 1)
+// SPLIT: the CTAs of a cluster share the k range (CL = 1, K-major).
+template <bool KIND8, bool P_MN, bool Q_MN, bool RAGK, bool ROWS, bool SPLIT, int CL,
+          int BN, int STAGES>
+__global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
     gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP,
                         const __grid_constant__ CUtensorMap tmQ,
                         const __grid_constant__ GroupedArgs a) {
-  using L = Layout<KIND8, ROWS, CL, BN, STAGES>;
+  using L = Layout<KIND8, ROWS, SPLIT, CL, BN, STAGES>;
   constexpr int KE = KIND8 ? 128 : 64;  // k elements per stage
   constexpr int PT = kP * CL;           // rows of P per tile
   constexpr int QS = 16 * CL;           // granularity of the MMA's N
@@ -226,13 +245,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFFSET);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* done = tempty + 2;
+  uint64_t* tempty = tfull + L::ACCS;
+  uint64_t* done = tempty + L::ACCS;
   uint64_t* cut_in = done + 1;         // RAGK: a cut block has landed here
   uint64_t* cut_ok = cut_in + STAGES;  // and its zeros are in place (leader)
   uint64_t* sfull = cut_ok + STAGES;
   uint64_t* sempty = sfull + L::SLOTS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + L::SLOTS);
+  // SPLIT, one per epilogue warp: the other ranks' sums are here (rank 0);
+  // this rank's have been taken (the others)
+  uint64_t* part_full = sempty + L::SLOTS;
+  uint64_t* part_free = part_full + (SPLIT ? kEpiWarps : 0);
+  uint32_t* tmem_slot =
+      reinterpret_cast<uint32_t*>(part_free + (SPLIT ? kEpiWarps : 0));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* grow = reinterpret_cast<int*>(smem + L::GROUP_OFFSET);  // groups + 1
   int* gunit = grow + a.groups + 1;                            // groups + 1
@@ -240,6 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = CL > 1 ? int(cluster_ctarank()) : 0;
+  const int krank = SPLIT ? int(cluster_ctarank()) : 0;
+  const int ksplit = SPLIT ? int(cluster_size()) : 1;
   const int p_tiles = (a.p_size + PT - 1) / PT;  // ROWS: of no meaning
   const int q_tiles = (a.q_size + BN - 1) / BN;  // RAGK, ROWS
 
@@ -254,11 +280,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sfull[s], 32);
       mbar_init(&sempty[s], kEpiWarps);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < L::ACCS; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], CL * kEpiWarps);
     }
     mbar_init(done, 1);
+    if constexpr (SPLIT)
+      for (int i = 0; i < kEpiWarps; ++i) {
+        mbar_init(&part_full[i], ksplit > 1 ? ksplit - 1 : 1);
+        mbar_init(&part_free[i], 1);
+      }
     *abort_flag = 0;
     fence_mbarrier_init();
     fence_proxy_async_smem();
@@ -316,14 +347,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   tc_fence_before();
-  if constexpr (CL > 1)
-    cluster_sync();  // the peer's barriers exist before anything targets them
+  if constexpr (CL > 1 || SPLIT)
+    cluster_sync();  // the others' barriers exist before anything targets them
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int units = gunit[a.groups];
-  const int first_unit = blockIdx.x / CL;
-  const int unit_step = gridDim.x / CL;
+  const int first_unit = blockIdx.x / (CL * ksplit);
+  const int unit_step = gridDim.x / (CL * ksplit);
 
   // Unit u: its group by bisection; within the group bands of kBand p tiles,
   // p fastest, so that what runs at one time shares few panels.
@@ -361,6 +392,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     t.nt = max((t.q1 - t.q0 + QS - 1) / QS * QS, QS);
     t.k0 = RAGK ? g0 : 0;
     t.k1 = RAGK ? g1 : a.k_size;
+    if constexpr (SPLIT) {
+      const int64_t blocks = (a.k_size + KE - 1) / KE;
+      t.k0 = int(blocks * krank / ksplit) * KE;
+      t.k1 = min(int(blocks * (krank + 1) / ksplit) * KE, a.k_size);
+    }
     return t;
   };
 
@@ -509,8 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit(&tfull[acc]);
           else
             umma_commit_pair(&tfull[acc], 3u);
-          acc ^= 1;
-          if (acc == 0) acc_phase ^= 1u;
+          if (++acc == L::ACCS) {
+            acc = 0;
+            acc_phase ^= 1u;
+          }
         }
       }
       // Every MMA issued above completes before tensor memory is released.
@@ -567,14 +605,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int p = t.p0 + rank * kP + i * 32 + lane;
         len_p |= int(p < t.p1) << i;
         src_p[i] = a.sp + (ROWS ? 0 : t.e * a.sp_group) +
-                   (int64_t(min(p, t.p1 - 1)) >> a.p_shift) * a.sp_row;
+                   (int64_t(min(p, t.p1 - 1)) >> a.p_shift) * a.sp_row +
+                   (t.k0 / KE) * a.sp_blk;
       }
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
         const int q = ROWS ? t.q0 + lane * HALF : t.q0 + i * 32 + lane;
         len_q |= int(q < t.q1) << i;
         src_q[i] = a.sq + (ROWS ? t.e * a.sq_group : 0) +
-                   (int64_t(min(q, t.q1 - 1)) >> a.q_shift) * a.sq_row;
+                   (int64_t(min(q, t.q1 - 1)) >> a.q_shift) * a.sq_row +
+                   (t.k0 / KE) * a.sq_blk;
       }
       const int chunks = (t.k1 - t.k0 + KE - 1) / KE;
       for (int ch = 0; ch < chunks; ch += L::G) {
@@ -623,8 +663,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    // the leader's barriers that hand the accumulators back
-    const uint32_t tempty_lead = mapa_shared(smem_u32(&tempty[0]), 0);
+    // the issuing CTA's barriers that hand the accumulators back
+    const uint32_t tempty_lead =
+        mapa_shared(smem_u32(&tempty[0]), CL > 1 ? 0 : cluster_ctarank());
+    [[maybe_unused]] uint32_t part_phase = 0;
+    [[maybe_unused]] const int part_at =
+        L::part_offset(a.groups) + ew * L::PART_FLOATS * 4;
     for (int u = first_unit; u < units && ok; u += unit_step) {
       __syncwarp();
       const Tile t = decode(u);
@@ -666,8 +710,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (in) add(i, r);
         }
-        acc ^= 1;
-        acc_phase ^= uint32_t(acc == 0);
+        if (++acc == L::ACCS) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
       };
       if constexpr (!KIND8) {
         for (int ch = 0; ch < chunks; ++ch)
@@ -713,6 +759,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = !__any_sync(0xffffffffu, *abort_flag != 0);
       if (!ok) break;
+      if constexpr (SPLIT) {
+        if (ksplit > 1) {
+          // only the columns that hold rows of D travel
+          const int cols = t.q1 - t.q0;
+          if (krank > 0) {
+            mbar_wait_lean(&part_free[ew], part_phase ^ 1u, abort_flag, a.status);
+            const uint32_t dst = mapa_shared(
+                smem_u32(smem + part_at + (krank - 1) * kEpiWarps * L::PART_FLOATS * 4), 0);
+#pragma unroll
+            for (int j = 0; j < HALF; ++j)
+              if (column(j / CB) + j % CB < cols)
+                st_cluster_f32(dst + (j * 32 + lane) * 4, sum[j]);
+            __syncwarp();
+            if (lane == 0)
+              mbar_arrive_cluster(mapa_shared(smem_u32(&part_full[ew]), 0));
+            __syncwarp();
+            part_phase ^= 1u;
+            continue;
+          }
+          const bool got =
+              mbar_wait_cluster(&part_full[ew], part_phase, abort_flag, a.status);
+          if (!__all_sync(0xffffffffu, got)) break;
+          for (int r = 1; r < ksplit; ++r) {
+            const float* src = reinterpret_cast<const float*>(
+                smem + part_at + (r - 1) * kEpiWarps * L::PART_FLOATS * 4);
+#pragma unroll
+            for (int j = 0; j < HALF; ++j)
+              if (column(j / CB) + j % CB < cols) sum[j] += src[j * 32 + lane];
+          }
+          __syncwarp();
+          if (lane == 0)
+            for (int r = 1; r < ksplit; ++r)
+              mbar_arrive_cluster(mapa_shared(smem_u32(&part_free[ew]), r));
+          __syncwarp();
+          part_phase ^= 1u;
+        }
+      }
       if constexpr (ROWS) {
         if (a.vec8) {
           // 16-bit D without C: 32 columns at a time, rounded, through
@@ -832,8 +915,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   tc_fence_before();
-  if constexpr (CL > 1)
-    cluster_sync();  // neither CTA leaves while the other may still signal it
+  if constexpr (CL > 1 || SPLIT)
+    cluster_sync();  // no CTA leaves while another may still signal it
   __syncthreads();
   tc_fence_after();
   if (warp == 1) {
@@ -875,11 +958,11 @@ struct Operand {
   int64_t ld, rows, slices, slice;
 };
 
-template <bool KIND8, bool P_MN, bool Q_MN, bool RAGK, bool ROWS, int CL, int BN,
-          int STAGES>
+template <bool KIND8, bool P_MN, bool Q_MN, bool RAGK, bool ROWS, bool SPLIT, int CL,
+          int BN, int STAGES>
 mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
                  const GroupedArgs& a) {
-  using L = Layout<KIND8, ROWS, CL, BN, STAGES>;
+  using L = Layout<KIND8, ROWS, SPLIT, CL, BN, STAGES>;
   constexpr int EB = KIND8 ? 1 : 2;
   constexpr int KE = KIND8 ? 128 : 64;
   constexpr int PT = kP * CL;
@@ -904,34 +987,48 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
   CUtensorMap tp, tq;
   if (!map_of(&tp, P, P_MN, a.p_size, kP) || !map_of(&tq, Q, Q_MN, a.q_size, BN / CL))
     return MMA_ERR_LAUNCH;
-  auto kern = gemm_grouped_kernel<KIND8, P_MN, Q_MN, RAGK, ROWS, CL, BN, STAGES>;
-  static_assert(L::alloc(kMaxGroups) <= 232448, "shared memory per CTA");
+  auto kern = gemm_grouped_kernel<KIND8, P_MN, Q_MN, RAGK, ROWS, SPLIT, CL, BN, STAGES>;
+  constexpr int kMostSplit = SPLIT ? 6 : 1;
+  static_assert(L::alloc(kMaxGroups, kMostSplit) <= 232448, "shared memory per CTA");
+  // SPLIT: as many CTAs per tile as leave every tile a cluster at once, each
+  // with four k blocks at least
+  int split = 1;
+  if constexpr (SPLIT) {
+    const int64_t blocks = (int64_t(a.k_size) + KE - 1) / KE;
+    const int64_t s = std::min<int64_t>(ctx.num_sms / std::max<int64_t>(most, 1), blocks / 4);
+    split = int(std::max<int64_t>(1, std::min<int64_t>(s, kMostSplit)));
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = size_t(L::alloc(a.groups));
+  cfg.dynamicSmemBytes = size_t(L::alloc(a.groups, split));
   cfg.stream = ctx.stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CL;
+  attr[0].val.clusterDim.x = unsigned(CL * split);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // clusters resident at once, once per context and instantiation
-  static PerContext<int> resident;
+  // clusters resident at once (with few groups), once per context and
+  // instantiation
+  static PerContext<int> resident[kMostSplit];
   int clusters = 0;
-  if (!resident.get(ctx, &clusters, [&](int* v) {
+  if (!resident[split - 1].get(ctx, &clusters, [&](int* v) {
         bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       L::alloc(kMaxGroups)) == cudaSuccess;
+                                       L::alloc(kMaxGroups, kMostSplit)) == cudaSuccess;
         // the split of the registers counts on the launch's
         cudaFuncAttributes fa = {};
         ok = ok && cudaFuncGetAttributes(&fa, kern) == cudaSuccess &&
              (BN < 256 || fa.numRegs == kLaunchRegs);
-        *v = ctx.num_sms;
-        if (ok && CL > 1) {
+        if (ok && CL * split == 1) {
+          ok = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                   v, kern, kThreads, size_t(L::alloc(64, 1))) == cudaSuccess && *v > 0;
+          *v *= ctx.num_sms;
+        }
+        if (ok && CL * split > 1) {
           cudaLaunchConfig_t probe = cfg;
-          probe.dynamicSmemBytes = size_t(L::alloc(kMaxGroups));
-          probe.gridDim = dim3(unsigned(CL * (ctx.num_sms / CL)), 1, 1);
+          probe.dynamicSmemBytes = size_t(L::alloc(kMaxGroups, split));
+          probe.gridDim = dim3(unsigned(CL * split * (ctx.num_sms / (CL * split))), 1, 1);
           ok = cudaOccupancyMaxActiveClusters(v, kern, &probe) == cudaSuccess && *v > 0;
         }
         if (!ok) cudaGetLastError();
@@ -939,7 +1036,7 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
       }))
     return MMA_ERR_LAUNCH;
   if (clusters > most) clusters = int(most);
-  cfg.gridDim = dim3(unsigned(clusters * CL), 1, 1);
+  cfg.gridDim = dim3(unsigned(clusters * CL * split), 1, 1);
   ctx.mark_start();
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tp, tq, a);
   ctx.mark_stop();
@@ -989,7 +1086,7 @@ mma_status_t launch_gemm_f8(const Ctx& ctx, const F8Problem& f) {
     a.sq_row = f.sb_row;
     a.sq_blk = f.sb_blk;
     a.q_shift = 7;
-    return run<true, false, false, false, true, 2, 256, 6>(ctx, A, B, a);
+    return run<true, false, false, false, true, false, 2, 256, 6>(ctx, A, B, a);
   }
   a.p_size = int(f.N);
   a.q_size = int(f.rows);
@@ -1003,11 +1100,11 @@ mma_status_t launch_gemm_f8(const Ctx& ctx, const F8Problem& f) {
   a.sq_blk = f.sa_blk;
   if (per > 128) {
     a.idesc = idesc_f32(f.b_e5m2, f.a_e5m2, false, false, 2 * kP);
-    return run<true, false, false, false, false, 2, 256, 6>(ctx, B, A, a);
+    return run<true, false, false, false, false, false, 2, 256, 6>(ctx, B, A, a);
   }
   a.idesc = idesc_f32(f.b_e5m2, f.a_e5m2, false, false, kP);
-  if (per <= 32) return run<true, false, false, false, false, 1, 32, 8>(ctx, B, A, a);
-  return run<true, false, false, false, false, 1, 128, 6>(ctx, B, A, a);
+  if (per <= 32) return run<true, false, false, false, false, true, 1, 32, 5>(ctx, B, A, a);
+  return run<true, false, false, false, false, false, 1, 128, 6>(ctx, B, A, a);
 }
 
 mma_status_t launch_gemm_grouped(const Ctx& ctx, const GroupedProblem& g) {
@@ -1031,12 +1128,12 @@ mma_status_t launch_gemm_grouped(const Ctx& ctx, const GroupedProblem& g) {
   const bool pair = per > 128;
   a.idesc = idesc_f32(g.bf16, g.bf16, g.b_row_major, false, pair ? 2 * kP : kP);
   if (g.b_row_major) {
-    if (pair) return run<false, true, false, false, false, 2, 256, 6>(ctx, B, A, a);
-    return run<false, true, false, false, false, 1, 128, 6>(ctx, B, A, a);
+    if (pair) return run<false, true, false, false, false, false, 2, 256, 6>(ctx, B, A, a);
+    return run<false, true, false, false, false, false, 1, 128, 6>(ctx, B, A, a);
   }
-  if (pair) return run<false, false, false, false, false, 2, 256, 6>(ctx, B, A, a);
-  if (per <= 32) return run<false, false, false, false, false, 1, 32, 8>(ctx, B, A, a);
-  return run<false, false, false, false, false, 1, 128, 6>(ctx, B, A, a);
+  if (pair) return run<false, false, false, false, false, false, 2, 256, 6>(ctx, B, A, a);
+  if (per <= 32) return run<false, false, false, false, false, true, 1, 32, 5>(ctx, B, A, a);
+  return run<false, false, false, false, false, false, 1, 128, 6>(ctx, B, A, a);
 }
 
 mma_status_t launch_gemm_grouped_wgrad(const Ctx& ctx, const WgradProblem& g) {
@@ -1059,7 +1156,7 @@ mma_status_t launch_gemm_grouped_wgrad(const Ctx& ctx, const WgradProblem& g) {
   a.idesc = idesc_f32(g.bf16, g.bf16, true, true, 2 * kP);
   const Operand X = {g.X, g.ldx, g.rows, 1, 0};
   const Operand DY = {g.DY, g.lddy, g.rows, 1, 0};
-  return run<false, true, true, true, false, 2, 256, 6>(ctx, X, DY, a);
+  return run<false, true, true, true, false, false, 2, 256, 6>(ctx, X, DY, a);
 }
 
 }  // namespace mmagb

@@ -50,6 +50,18 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+// Store to shared memory of a CTA of the cluster (a shared::cluster address).
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v)
+               : "memory");
+}
+
 // Cluster-wide barrier (every thread of every CTA of the cluster), with
 // release/acquire ordering of shared-memory operations across the CTAs.
 // The non-.aligned forms tolerate warps whose lanes arrive separately.
