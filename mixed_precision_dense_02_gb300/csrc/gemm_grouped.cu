@@ -268,6 +268,12 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
   const int ksplit = SPLIT ? int(cluster_size()) : 1;
   const int p_tiles = (a.p_size + PT - 1) / PT;  // ROWS: of no meaning
   const int q_tiles = (a.q_size + BN - 1) / BN;  // RAGK, ROWS
+  // tiles of a group with `rows` rows
+  auto units_of = [&](int rows) {
+    return RAGK ? q_tiles * p_tiles
+           : ROWS ? ((rows + PT - 1) / PT) * q_tiles
+                  : ((rows + BN - 1) / BN) * p_tiles;
+  };
 
   if (threadIdx.x == 32) {
     for (int s = 0; s < STAGES; ++s) {
@@ -294,49 +300,6 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
     fence_mbarrier_init();
     fence_proxy_async_smem();
   }
-  if (warp == 0) {
-    if (lane == 0) {
-      tma_prefetch_desc(&tmP);
-      tma_prefetch_desc(&tmQ);
-    }
-    // Row and unit ranges of the groups.  Offsets are clamped to
-    // [0, rows_total] and made non-decreasing, so that no value of theirs
-    // leads outside the operands.
-    auto at = [&](int i) {
-      if (!a.offsets) return i == 0 ? 0 : a.rows_total;
-      return min(max(__ldg(a.offsets + i), 0), a.rows_total);
-    };
-    int row = at(0), unit = 0;
-    if (lane == 0) {
-      grow[0] = row;
-      gunit[0] = 0;
-    }
-    for (int base = 0; base < a.groups; base += 32) {
-      const int i = base + lane;
-      int hi = i < a.groups ? at(i + 1) : 0;
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, hi, d);
-        if (lane >= d) hi = max(hi, o);
-      }
-      hi = max(hi, row);
-      int lo = __shfl_up_sync(0xffffffffu, hi, 1);
-      if (lane == 0) lo = row;
-      int n = RAGK ? q_tiles * p_tiles
-              : ROWS ? ((hi - lo + PT - 1) / PT) * q_tiles
-                     : ((hi - lo + BN - 1) / BN) * p_tiles;
-      if (i >= a.groups) n = 0;
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, n, d);
-        if (lane >= d) n += o;
-      }
-      if (i < a.groups) {
-        grow[i + 1] = hi;
-        gunit[i + 1] = unit + n;
-      }
-      row = __shfl_sync(0xffffffffu, hi, 31);
-      unit += __shfl_sync(0xffffffffu, n, 31);
-    }
-  }
   if (warp == 1) {
     if constexpr (CL == 1) {
       tmem_alloc(tmem_slot, L::TMEM_COLS);
@@ -346,15 +309,75 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
       tmem_relinquish_pair();
     }
   }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmP);
+    tma_prefetch_desc(&tmQ);
+  }
+  // All of the above overlaps the end of the kernel before this one; nothing
+  // global has been read or written yet.
+  grid_dependency_wait();
+  if (warp == 0) {
+    if (!a.offsets) {
+      if (lane == 0) {
+        grow[0] = 0;
+        grow[1] = a.rows_total;
+        gunit[0] = 0;
+        gunit[1] = units_of(a.rows_total);
+      }
+    } else {
+      // Row and unit ranges of the groups.  Offsets are clamped to
+      // [0, rows_total] and made non-decreasing, so that no value of theirs
+      // leads outside the operands.
+      auto at = [&](int i) {
+        return min(max(__ldg(a.offsets + i), 0), a.rows_total);
+      };
+      int row = at(0), unit = 0;
+      if (lane == 0) {
+        grow[0] = row;
+        gunit[0] = 0;
+      }
+      for (int base = 0; base < a.groups; base += 32) {
+        const int i = base + lane;
+        int hi = i < a.groups ? at(i + 1) : 0;
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, hi, d);
+          if (lane >= d) hi = max(hi, o);
+        }
+        hi = max(hi, row);
+        int lo = __shfl_up_sync(0xffffffffu, hi, 1);
+        if (lane == 0) lo = row;
+        int n = i < a.groups ? units_of(hi - lo) : 0;
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, n, d);
+          if (lane >= d) n += o;
+        }
+        if (i < a.groups) {
+          grow[i + 1] = hi;
+          gunit[i + 1] = unit + n;
+        }
+        row = __shfl_sync(0xffffffffu, hi, 31);
+        unit += __shfl_sync(0xffffffffu, n, 31);
+      }
+    }
+  }
   tc_fence_before();
   if constexpr (CL > 1 || SPLIT)
     cluster_sync();  // the others' barriers exist before anything targets them
   __syncthreads();
   tc_fence_after();
+  grid_dependents_start();
   const uint32_t tmem_base = *tmem_slot;
   const int units = gunit[a.groups];
   const int first_unit = blockIdx.x / (CL * ksplit);
   const int unit_step = gridDim.x / (CL * ksplit);
+
+  [[maybe_unused]] int split_k0 = 0, split_k1 = a.k_size;
+  if (SPLIT && ksplit > 1) {
+    // (at most 2^24 blocks of k times 6)
+    const int blocks = (a.k_size + KE - 1) / KE;
+    split_k0 = blocks * krank / ksplit * KE;
+    split_k1 = min(blocks * (krank + 1) / ksplit * KE, a.k_size);
+  }
 
   // Unit u: its group by bisection; within the group bands of kBand p tiles,
   // p fastest, so that what runs at one time shares few panels.
@@ -369,11 +392,16 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
     const int r = u - gunit[lo];
     const int g0 = grow[lo], g1 = grow[lo + 1];
     const int np = ROWS ? (g1 - g0 + PT - 1) / PT : p_tiles;
-    const int nq = (gunit[lo + 1] - gunit[lo]) / np;
-    const int band = r / (kBand * nq);
-    const int bp = min(np - band * kBand, kBand);
-    const int in = r - band * kBand * nq;
-    const int pi = band * kBand + in % bp, qi = in / bp;
+    const int nq = RAGK || ROWS ? q_tiles : (g1 - g0 + BN - 1) / BN;
+    // (divisions cost a lone thread some hundred clocks each)
+    int pi = r, qi = 0;
+    if (nq > 1) {
+      const int band = np > kBand ? r / (kBand * nq) : 0;
+      const int bp = min(np - band * kBand, kBand);
+      const int in = r - band * kBand * nq;
+      qi = in / bp;
+      pi = band * kBand + in - qi * bp;
+    }
     if constexpr (ROWS) {
       t.p0 = g0 + pi * PT;
       t.p1 = g1;
@@ -385,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
       // the rows are shared out evenly between the q tiles
       const int first = RAGK ? 0 : g0;
       const int rows = RAGK ? a.q_size : g1 - g0;
-      const int step = ((rows + nq - 1) / nq + QS - 1) / QS * QS;
+      const int share = nq > 1 ? (rows + nq - 1) / nq : rows;
+      const int step = (share + QS - 1) / QS * QS;
       t.q0 = first + min(qi * step, rows);
       t.q1 = first + min(qi * step + step, rows);
     }
@@ -393,9 +422,8 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
     t.k0 = RAGK ? g0 : 0;
     t.k1 = RAGK ? g1 : a.k_size;
     if constexpr (SPLIT) {
-      const int64_t blocks = (a.k_size + KE - 1) / KE;
-      t.k0 = int(blocks * krank / ksplit) * KE;
-      t.k1 = min(int(blocks * (krank + 1) / ksplit) * KE, a.k_size);
+      t.k0 = split_k0;
+      t.k1 = split_k1;
     }
     return t;
   };
@@ -915,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
     }
   }
   tc_fence_before();
-  if constexpr (CL > 1 || SPLIT)
+  if (CL > 1 || ksplit > 1)
     cluster_sync();  // no CTA leaves while another may still signal it
   __syncthreads();
   tc_fence_after();
@@ -1002,13 +1030,15 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = size_t(L::alloc(a.groups, split));
   cfg.stream = ctx.stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = unsigned(CL * split);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   // clusters resident at once (with few groups), once per context and
   // instantiation
   static PerContext<int> resident[kMostSplit];
@@ -1027,6 +1057,7 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
         }
         if (ok && CL * split > 1) {
           cudaLaunchConfig_t probe = cfg;
+          probe.numAttrs = 1;
           probe.dynamicSmemBytes = size_t(L::alloc(kMaxGroups, split));
           probe.gridDim = dim3(unsigned(CL * split * (ctx.num_sms / (CL * split))), 1, 1);
           ok = cudaOccupancyMaxActiveClusters(v, kern, &probe) == cudaSuccess && *v > 0;
