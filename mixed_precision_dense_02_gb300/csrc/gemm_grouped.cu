@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
     mbar_init(done, 1);
     if constexpr (SPLIT)
       for (int i = 0; i < kEpiWarps; ++i) {
-        mbar_init(&part_full[i], ksplit > 1 ? ksplit - 1 : 1);
+        mbar_init(&part_full[i], 1);
         mbar_init(&part_free[i], 1);
       }
     *abort_flag = 0;
@@ -313,9 +313,8 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
     tma_prefetch_desc(&tmP);
     tma_prefetch_desc(&tmQ);
   }
-  // All of the above overlaps the end of the kernel before this one; nothing
-  // global has been read or written yet.
-  grid_dependency_wait();
+  // All of this overlaps the end of the kernel before this one, which every
+  // role waits for before its first global access.
   if (warp == 0) {
     if (!a.offsets) {
       if (lane == 0) {
@@ -328,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
       // Row and unit ranges of the groups.  Offsets are clamped to
       // [0, rows_total] and made non-decreasing, so that no value of theirs
       // leads outside the operands.
+      grid_dependency_wait();
       auto at = [&](int i) {
         return min(max(__ldg(a.offsets + i), 0), a.rows_total);
       };
@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
       // the leader CTA's full barriers, which count both CTAs' bytes
       const uint32_t full_lead =
           CL > 1 ? mapa_shared(smem_u32(&full[0]), 0) : 0u;
+      grid_dependency_wait();
       for (int u = first_unit; u < units && ok; u += unit_step) {
         const Tile t = decode(u);
         const int py = t.p0 + rank * kP;
@@ -623,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
     uint32_t phase = 0;
     bool ok = true;
     const float* ring = reinterpret_cast<const float*>(smem + L::SCALE_OFFSET);
+    grid_dependency_wait();
     for (int u = first_unit; u < units && ok; u += unit_step) {
       const Tile t = decode(u);
       constexpr int NP = kP / 32, NQ = ROWS ? 1 : BN / 32;
@@ -695,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
     const uint32_t tempty_lead =
         mapa_shared(smem_u32(&tempty[0]), CL > 1 ? 0 : cluster_ctarank());
     [[maybe_unused]] uint32_t part_phase = 0;
+    grid_dependency_wait();
     [[maybe_unused]] const int part_at =
         L::part_offset(a.groups) + ew * L::PART_FLOATS * 4;
     for (int u = first_unit; u < units && ok; u += unit_step) {
@@ -789,22 +792,26 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
       if (!ok) break;
       if constexpr (SPLIT) {
         if (ksplit > 1) {
-          // only the columns that hold rows of D travel
+          // Only the columns that hold rows of D travel, as stores that
+          // complete on rank 0's barrier: no release, no arrival.
           const int cols = t.q1 - t.q0;
           if (krank > 0) {
             mbar_wait_lean(&part_free[ew], part_phase ^ 1u, abort_flag, a.status);
             const uint32_t dst = mapa_shared(
                 smem_u32(smem + part_at + (krank - 1) * kEpiWarps * L::PART_FLOATS * 4), 0);
+            const uint32_t bar = mapa_shared(smem_u32(&part_full[ew]), 0);
 #pragma unroll
             for (int j = 0; j < HALF; ++j)
               if (column(j / CB) + j % CB < cols)
-                st_cluster_f32(dst + (j * 32 + lane) * 4, sum[j]);
-            __syncwarp();
-            if (lane == 0)
-              mbar_arrive_cluster(mapa_shared(smem_u32(&part_full[ew]), 0));
-            __syncwarp();
+                st_async_f32(dst + (j * 32 + lane) * 4, sum[j], bar);
             part_phase ^= 1u;
             continue;
+          }
+          if (lane == 0) {
+            int mine = 0;  // columns of this warp
+#pragma unroll
+            for (int i = 0; i < NB; ++i) mine += min(max(cols - column(i), 0), CB);
+            mbar_arrive_expect_tx(&part_full[ew], uint32_t((ksplit - 1) * mine * 128));
           }
           const bool got =
               mbar_wait_cluster(&part_full[ew], part_phase, abort_flag, a.status);
@@ -816,11 +823,13 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
             for (int j = 0; j < HALF; ++j)
               if (column(j / CB) + j % CB < cols) sum[j] += src[j * 32 + lane];
           }
-          __syncwarp();
-          if (lane == 0)
-            for (int r = 1; r < ksplit; ++r)
-              mbar_arrive_cluster(mapa_shared(smem_u32(&part_free[ew]), r));
-          __syncwarp();
+          if (u + unit_step < units) {
+            __syncwarp();
+            if (lane == 0)
+              for (int r = 1; r < ksplit; ++r)
+                mbar_arrive_remote(mapa_shared(smem_u32(&part_free[ew]), r));
+            __syncwarp();
+          }
           part_phase ^= 1u;
         }
       }

@@ -56,10 +56,16 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 
-// Store to shared memory of a CTA of the cluster (a shared::cluster address).
-__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v)
-               : "memory");
+// Store to shared memory of a CTA of the cluster that completes on one of
+// that CTA's mbarriers (4 bytes of its transaction count); both addresses
+// are shared::cluster addresses.
+__device__ __forceinline__ void st_async_f32(uint32_t addr, float v,
+                                             uint32_t bar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+          addr),
+      "r"(__float_as_uint(v)), "r"(bar)
+      : "memory");
 }
 
 // Cluster-wide barrier (every thread of every CTA of the cluster), with
