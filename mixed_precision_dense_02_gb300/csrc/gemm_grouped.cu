@@ -76,6 +76,7 @@ struct GroupedArgs {
   const int* offsets;
   uint32_t idesc;  // without the N field
   int kb_per_chunk;
+  int part_cols;  // SPLIT: most columns of an epilogue warp in use
   int d_type;  // MMA_F32, MMA_F16 or MMA_BF16
   // ROWS: four elements of a row of D (and C) can move at once; D is 16-bit,
   // there is no C and eight can
@@ -111,21 +112,21 @@ struct Layout {
   static constexpr int WARP_BYTES = ROWS ? 2048 : 0;
   static constexpr int WARP_OFFSET = SCALE_OFFSET + SLOTS * SLOT_FLOATS * 4;
   static constexpr int BAR_OFFSET = WARP_OFFSET + kEpiWarps * WARP_BYTES;
-  // Accumulators in tensor memory: as many as fit (with 32 columns 256 of
-  // the 512, for two CTAs per SM).  A chunk's way through the MMAs, the
+  // Accumulators in tensor memory: as many as fit (with 32 and 64 columns
+  // 256 of the 512, for two CTAs per SM).  A chunk's way through the MMAs, the
   // epilogue and back takes some 1000 clocks whatever its size.
-  static constexpr int ACCS = BN == 32 ? 8 : 512 / BN;
+  static constexpr int ACCS = BN == 32 ? 8 : BN == 64 ? 4 : 512 / BN;
   static constexpr int NUM_BARS =
       4 * STAGES + 1 + 2 * ACCS + 2 * SLOTS + (SPLIT ? 2 * kEpiWarps : 0);
   static constexpr int GROUP_OFFSET = BAR_OFFSET + NUM_BARS * 8 + 24;
   static constexpr int round16(int v) { return (v + 15) & ~15; }
-  // SPLIT: sums of the other ranks, for each epilogue warp
-  static constexpr int PART_FLOATS = 32 * (BN / 2);
+  // SPLIT: sums of the other ranks, for each epilogue warp 32 lanes times
+  // the columns in use
   static constexpr int part_offset(int groups) {
     return round16(GROUP_OFFSET + 2 * (groups + 1) * 4);
   }
-  static constexpr int alloc(int groups, int split) {
-    return part_offset(groups) + (split - 1) * kEpiWarps * PART_FLOATS * 4 +
+  static constexpr int alloc(int groups, int split, int part_cols) {
+    return part_offset(groups) + (split - 1) * kEpiWarps * part_cols * 128 +
            1024;  // base alignment
   }
   static constexpr uint32_t TMEM_COLS = ACCS * BN;
@@ -227,7 +228,7 @@ __device__ __forceinline__ void zero_rows(uint8_t* stage, int row, int n, int la
 // SPLIT: the CTAs of a cluster share the k range (CL = 1, K-major).
 template <bool KIND8, bool P_MN, bool Q_MN, bool RAGK, bool ROWS, bool SPLIT, int CL,
           int BN, int STAGES>
-__global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP,
                         const __grid_constant__ CUtensorMap tmQ,
                         const __grid_constant__ GroupedArgs a) {
@@ -699,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
     [[maybe_unused]] uint32_t part_phase = 0;
     grid_dependency_wait();
     [[maybe_unused]] const int part_at =
-        L::part_offset(a.groups) + ew * L::PART_FLOATS * 4;
+        L::part_offset(a.groups) + ew * a.part_cols * 128;
     for (int u = first_unit; u < units && ok; u += unit_step) {
       __syncwarp();
       const Tile t = decode(u);
@@ -798,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
           if (krank > 0) {
             mbar_wait_lean(&part_free[ew], part_phase ^ 1u, abort_flag, a.status);
             const uint32_t dst = mapa_shared(
-                smem_u32(smem + part_at + (krank - 1) * kEpiWarps * L::PART_FLOATS * 4), 0);
+                smem_u32(smem + part_at + (krank - 1) * kEpiWarps * a.part_cols * 128), 0);
             const uint32_t bar = mapa_shared(smem_u32(&part_full[ew]), 0);
 #pragma unroll
             for (int j = 0; j < HALF; ++j)
@@ -818,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, BN == 32 ? 2 : 1)
           if (!__all_sync(0xffffffffu, got)) break;
           for (int r = 1; r < ksplit; ++r) {
             const float* src = reinterpret_cast<const float*>(
-                smem + part_at + (r - 1) * kEpiWarps * L::PART_FLOATS * 4);
+                smem + part_at + (r - 1) * kEpiWarps * a.part_cols * 128);
 #pragma unroll
             for (int j = 0; j < HALF; ++j)
               if (column(j / CB) + j % CB < cols) sum[j] += src[j * 32 + lane];
@@ -998,84 +999,89 @@ struct Operand {
 template <bool KIND8, bool P_MN, bool Q_MN, bool RAGK, bool ROWS, bool SPLIT, int CL,
           int BN, int STAGES>
 mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
-                 const GroupedArgs& a) {
+                 const GroupedArgs& args) {
   using L = Layout<KIND8, ROWS, SPLIT, CL, BN, STAGES>;
   constexpr int EB = KIND8 ? 1 : 2;
   constexpr int KE = KIND8 ? 128 : 64;
   constexpr int PT = kP * CL;
-  const int64_t p_tiles = (a.p_size + PT - 1) / PT;
-  const int64_t q_tiles = (a.q_size + BN - 1) / BN;
-  // an upper bound of the units, whatever the offsets
-  const int64_t cuts = a.offsets ? a.groups : 1;
-  const int64_t most = RAGK   ? a.groups * q_tiles * p_tiles
-                       : ROWS ? (a.rows_total / PT + cuts) * q_tiles
-                              : (a.rows_total / BN + cuts) * p_tiles;
+  const int64_t p_tiles = (args.p_size + PT - 1) / PT;
+  const int64_t q_tiles = (args.q_size + BN - 1) / BN;
+  // an upper bound of the units, whatever the offsets: a group with n rows
+  // has at most n tiles' rows of them, and full tiles besides one
+  auto tiles_of = [&](int64_t rows, int64_t per) {
+    return args.offsets
+               ? std::min<int64_t>(rows, rows / per + args.groups)
+               : (rows + per - 1) / per;
+  };
+  const int64_t most = RAGK   ? args.groups * q_tiles * p_tiles
+                       : ROWS ? tiles_of(args.rows_total, PT) * q_tiles
+                              : tiles_of(args.rows_total, BN) * p_tiles;
   if (most > int64_t(INT32_MAX) / 2) return MMA_ERR_UNSUPPORTED;
   auto map_of = [&](CUtensorMap* m, const Operand& o, bool mn, int64_t len, int box) {
     // no k at all (D = C): the kernel loads nothing but wants a valid map
-    if (a.k_size == 0)
-      return make_map(m, reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(a.D) &
+    if (args.k_size == 0)
+      return make_map(m, reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(args.D) &
                                                  ~uintptr_t(15)),
                       EB, 64, 1, 64, 1, 64, 64, 1);
     const int64_t slice = o.slices > 1 ? o.slice : o.ld;  // unused when 1
     return mn ? make_map(m, o.p, EB, len, o.rows, o.ld, o.slices, slice, 64, 64)
-              : make_map(m, o.p, EB, a.k_size, o.rows, o.ld, o.slices, slice, KE, box);
+              : make_map(m, o.p, EB, args.k_size, o.rows, o.ld, o.slices, slice, KE, box);
   };
   CUtensorMap tp, tq;
-  if (!map_of(&tp, P, P_MN, a.p_size, kP) || !map_of(&tq, Q, Q_MN, a.q_size, BN / CL))
+  if (!map_of(&tp, P, P_MN, args.p_size, kP) || !map_of(&tq, Q, Q_MN, args.q_size, BN / CL))
     return MMA_ERR_LAUNCH;
   auto kern = gemm_grouped_kernel<KIND8, P_MN, Q_MN, RAGK, ROWS, SPLIT, CL, BN, STAGES>;
-  constexpr int kMostSplit = SPLIT ? 6 : 1;
-  static_assert(L::alloc(kMaxGroups, kMostSplit) <= 232448, "shared memory per CTA");
-  // SPLIT: as many CTAs per tile as leave every tile a cluster at once, each
-  // with four k blocks at least
+  constexpr int kMostSplit = !SPLIT ? 1 : BN == 32 ? 6 : BN == 64 ? 4 : 2;
+  static_assert(L::alloc(kMaxGroups, kMostSplit, BN / 2) <= 232448, "shared memory per CTA");
+  // SPLIT: as many CTAs per tile as leave every tile's cluster room at once
+  // (two CTAs per SM if their shared memory fits twice), each with four k
+  // blocks at least.  One row, 8192 x 4096: 64 tiles, 14.7 us without.
+  GroupedArgs a = args;
   int split = 1;
   if constexpr (SPLIT) {
     const int64_t blocks = (int64_t(a.k_size) + KE - 1) / KE;
-    const int64_t s = std::min<int64_t>(ctx.num_sms / std::max<int64_t>(most, 1), blocks / 4);
-    split = int(std::max<int64_t>(1, std::min<int64_t>(s, kMostSplit)));
+    a.part_cols = std::min(BN / 2, a.offsets ? BN : a.rows_total);
+    for (int s = kMostSplit; s > 1 && split == 1; --s) {
+      const int64_t slots =
+          ctx.num_sms * (2 * (L::alloc(a.groups, s, a.part_cols) + 1024) <= 233472 ? 2 : 1);
+      if (most * s <= slots && blocks >= 4 * s) split = s;
+    }
   }
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = size_t(L::alloc(a.groups, split));
+  cfg.dynamicSmemBytes = size_t(L::alloc(a.groups, split, a.part_cols));
   cfg.stream = ctx.stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(CL * split);
+  attr[0].val.clusterDim.x = CL;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  // clusters resident at once (with few groups), once per context and
-  // instantiation
-  static PerContext<int> resident[kMostSplit];
-  int clusters = 0;
-  if (!resident[split - 1].get(ctx, &clusters, [&](int* v) {
+  // CTAs (or pairs) that run at once, with few groups and without a split;
+  // once per context and instantiation
+  static PerContext<int> resident;
+  int at_once = 0;
+  if (!resident.get(ctx, &at_once, [&](int* v) {
         bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       L::alloc(kMaxGroups, kMostSplit)) == cudaSuccess;
+                                       L::alloc(kMaxGroups, kMostSplit, BN / 2)) == cudaSuccess;
         // the split of the registers counts on the launch's
         cudaFuncAttributes fa = {};
         ok = ok && cudaFuncGetAttributes(&fa, kern) == cudaSuccess &&
              (BN < 256 || fa.numRegs == kLaunchRegs);
-        if (ok && CL * split == 1) {
-          ok = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                   v, kern, kThreads, size_t(L::alloc(64, 1))) == cudaSuccess && *v > 0;
-          *v *= ctx.num_sms;
-        }
-        if (ok && CL * split > 1) {
-          cudaLaunchConfig_t probe = cfg;
-          probe.numAttrs = 1;
-          probe.dynamicSmemBytes = size_t(L::alloc(kMaxGroups, split));
-          probe.gridDim = dim3(unsigned(CL * split * (ctx.num_sms / (CL * split))), 1, 1);
-          ok = cudaOccupancyMaxActiveClusters(v, kern, &probe) == cudaSuccess && *v > 0;
-        }
+        cudaLaunchConfig_t probe = cfg;
+        probe.numAttrs = 1;
+        probe.dynamicSmemBytes = size_t(L::alloc(64, 1, 0));
+        probe.gridDim = dim3(unsigned(CL * (ctx.num_sms / CL)), 1, 1);
+        ok = ok && cudaOccupancyMaxActiveClusters(v, kern, &probe) == cudaSuccess && *v > 0;
         if (!ok) cudaGetLastError();
         return ok;
       }))
     return MMA_ERR_LAUNCH;
-  if (clusters > most) clusters = int(most);
+  const int64_t clusters = split > 1 ? most : std::min<int64_t>(most, at_once);
+  attr[0].val.clusterDim.x = unsigned(CL * split);
+  cfg.numAttrs = 2;
   cfg.gridDim = dim3(unsigned(clusters * CL * split), 1, 1);
   ctx.mark_start();
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tp, tq, a);
@@ -1087,6 +1093,24 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
 // Whether `n` consecutive elements at multiples of n in a row can move at once.
 bool elements_aligned(const void* p, int64_t ld, int bytes, int n) {
   return (reinterpret_cast<uintptr_t>(p) & uintptr_t(n * bytes - 1)) == 0 && ld % n == 0;
+}
+
+// Up to 128 rows per group (`per`), column-major B: tiles of 32, 64 or 128
+// columns.  With fewer of them than SMs a cluster shares each one's k range;
+// else one CTA per SM with a deep ring streams them (64 experts of 2048 x
+// 4096 with 96 tokens: 62 us, two CTAs per SM with half the ring 66).
+template <bool KIND8>
+mma_status_t few_rows(const Ctx& ctx, const Operand& B, const Operand& A,
+                      const GroupedArgs& a, int64_t per) {
+  const int64_t tiles = (a.p_size + kP - 1) / kP *
+                        (a.offsets ? std::min<int64_t>(a.rows_total, a.groups) : 1);
+  const bool split = tiles < ctx.num_sms;
+  if (per <= 32)
+    return split ? run<KIND8, false, false, false, false, true, 1, 32, 4>(ctx, B, A, a)
+                 : run<KIND8, false, false, false, false, false, 1, 32, 8>(ctx, B, A, a);
+  if (per <= 64) return run<KIND8, false, false, false, false, true, 1, 64, 4>(ctx, B, A, a);
+  return split ? run<KIND8, false, false, false, false, true, 1, 128, 4>(ctx, B, A, a)
+               : run<KIND8, false, false, false, false, false, 1, 128, 6>(ctx, B, A, a);
 }
 
 }  // namespace
@@ -1143,8 +1167,7 @@ mma_status_t launch_gemm_f8(const Ctx& ctx, const F8Problem& f) {
     return run<true, false, false, false, false, false, 2, 256, 6>(ctx, B, A, a);
   }
   a.idesc = idesc_f32(f.b_e5m2, f.a_e5m2, false, false, kP);
-  if (per <= 32) return run<true, false, false, false, false, true, 1, 32, 5>(ctx, B, A, a);
-  return run<true, false, false, false, false, false, 1, 128, 6>(ctx, B, A, a);
+  return few_rows<true>(ctx, B, A, a, per);
 }
 
 mma_status_t launch_gemm_grouped(const Ctx& ctx, const GroupedProblem& g) {
@@ -1172,8 +1195,7 @@ mma_status_t launch_gemm_grouped(const Ctx& ctx, const GroupedProblem& g) {
     return run<false, true, false, false, false, false, 1, 128, 6>(ctx, B, A, a);
   }
   if (pair) return run<false, false, false, false, false, false, 2, 256, 6>(ctx, B, A, a);
-  if (per <= 32) return run<false, false, false, false, false, true, 1, 32, 5>(ctx, B, A, a);
-  return run<false, false, false, false, false, false, 1, 128, 6>(ctx, B, A, a);
+  return few_rows<false>(ctx, B, A, a, per);
 }
 
 mma_status_t launch_gemm_grouped_wgrad(const Ctx& ctx, const WgradProblem& g) {
