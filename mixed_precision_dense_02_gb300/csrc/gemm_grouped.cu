@@ -76,7 +76,7 @@ struct GroupedArgs {
   const int* offsets;
   uint32_t idesc;  // without the N field
   int kb_per_chunk;
-  int part_cols;  // SPLIT: most columns of an epilogue warp in use
+  int part_cols;  // SPLIT: most columns of a tile in use
   int d_type;  // MMA_F32, MMA_F16 or MMA_BF16
   // ROWS: four elements of a row of D (and C) can move at once; D is 16-bit,
   // there is no C and eight can
@@ -104,7 +104,7 @@ struct Layout {
   // 8-bit: a ring of the chunks' scales, G chunks per slot; a chunk's are
   // 128 of P, then those of Q (ROWS: of the two halves of the columns)
   static constexpr int G = 4;
-  static constexpr int SLOTS = KIND8 ? 3 : 0;
+  static constexpr int SLOTS = !KIND8 ? 0 : BN <= 64 ? 2 : 3;
   static constexpr int CHUNK_FLOATS = kP + (ROWS ? 4 : BN);
   static constexpr int SLOT_FLOATS = G * CHUNK_FLOATS;
   static constexpr int SCALE_OFFSET = STAGES * STAGE_BYTES;
@@ -120,14 +120,13 @@ struct Layout {
       4 * STAGES + 1 + 2 * ACCS + 2 * SLOTS + (SPLIT ? 2 * kEpiWarps : 0);
   static constexpr int GROUP_OFFSET = BAR_OFFSET + NUM_BARS * 8 + 24;
   static constexpr int round16(int v) { return (v + 15) & ~15; }
-  // SPLIT: sums of the other ranks, for each epilogue warp 32 lanes times
-  // the columns in use
+  // SPLIT: sums of the other ranks, 128 rows of P times the columns in use
   static constexpr int part_offset(int groups) {
     return round16(GROUP_OFFSET + 2 * (groups + 1) * 4);
   }
   static constexpr int alloc(int groups, int split, int part_cols) {
-    return part_offset(groups) + (split - 1) * kEpiWarps * part_cols * 128 +
-           1024;  // base alignment
+    // (1024: alignment of the base)
+    return part_offset(groups) + (split - 1) * part_cols * kP * 4 + 1024;
   }
   static constexpr uint32_t TMEM_COLS = ACCS * BN;
 };
@@ -700,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     [[maybe_unused]] uint32_t part_phase = 0;
     grid_dependency_wait();
     [[maybe_unused]] const int part_at =
-        L::part_offset(a.groups) + ew * a.part_cols * 128;
+        L::part_offset(a.groups) + (quarter * 32 + lane) * 4;
     for (int u = first_unit; u < units && ok; u += unit_step) {
       __syncwarp();
       const Tile t = decode(u);
@@ -799,12 +798,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
           if (krank > 0) {
             mbar_wait_lean(&part_free[ew], part_phase ^ 1u, abort_flag, a.status);
             const uint32_t dst = mapa_shared(
-                smem_u32(smem + part_at + (krank - 1) * kEpiWarps * a.part_cols * 128), 0);
+                smem_u32(smem + part_at + (krank - 1) * a.part_cols * kP * 4), 0);
             const uint32_t bar = mapa_shared(smem_u32(&part_full[ew]), 0);
 #pragma unroll
             for (int j = 0; j < HALF; ++j)
-              if (column(j / CB) + j % CB < cols)
-                st_async_f32(dst + (j * 32 + lane) * 4, sum[j], bar);
+              if (const int c = column(j / CB) + j % CB; c < cols)
+                st_async_f32(dst + c * kP * 4, sum[j], bar);
             part_phase ^= 1u;
             continue;
           }
@@ -819,10 +818,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
           if (!__all_sync(0xffffffffu, got)) break;
           for (int r = 1; r < ksplit; ++r) {
             const float* src = reinterpret_cast<const float*>(
-                smem + part_at + (r - 1) * kEpiWarps * a.part_cols * 128);
+                smem + part_at + (r - 1) * a.part_cols * kP * 4);
 #pragma unroll
             for (int j = 0; j < HALF; ++j)
-              if (column(j / CB) + j % CB < cols) sum[j] += src[j * 32 + lane];
+              if (const int c = column(j / CB) + j % CB; c < cols) sum[j] += src[c * kP];
           }
           if (u + unit_step < units) {
             __syncwarp();
@@ -1032,7 +1031,7 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
     return MMA_ERR_LAUNCH;
   auto kern = gemm_grouped_kernel<KIND8, P_MN, Q_MN, RAGK, ROWS, SPLIT, CL, BN, STAGES>;
   constexpr int kMostSplit = !SPLIT ? 1 : BN == 32 ? 6 : BN == 64 ? 4 : 2;
-  static_assert(L::alloc(kMaxGroups, kMostSplit, BN / 2) <= 232448, "shared memory per CTA");
+  static_assert(L::alloc(kMaxGroups, kMostSplit, BN) <= 232448, "shared memory per CTA");
   // SPLIT: as many CTAs per tile as leave every tile's cluster room at once
   // (two CTAs per SM if their shared memory fits twice), each with four k
   // blocks at least.  One row, 8192 x 4096: 64 tiles, 14.7 us without.
@@ -1040,7 +1039,7 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
   int split = 1;
   if constexpr (SPLIT) {
     const int64_t blocks = (int64_t(a.k_size) + KE - 1) / KE;
-    a.part_cols = std::min(BN / 2, a.offsets ? BN : a.rows_total);
+    a.part_cols = a.offsets ? BN : std::min(BN, a.rows_total);
     for (int s = kMostSplit; s > 1 && split == 1; --s) {
       const int64_t slots =
           ctx.num_sms * (2 * (L::alloc(a.groups, s, a.part_cols) + 1024) <= 233472 ? 2 : 1);
@@ -1049,7 +1048,12 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
   }
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = size_t(L::alloc(a.groups, split, a.part_cols));
+  // One CTA per SM when there is no more than one for each: were there room
+  // for two, the next call's CTAs would come in pairs beside this one's and
+  // leave SMs idle (16 rows, 8192 x 4096: 10.4 us, else 11.9).
+  int smem = L::alloc(a.groups, split, a.part_cols);
+  if (SPLIT && most * split <= ctx.num_sms) smem = std::max(smem, 118 * 1024);
+  cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = ctx.stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1065,7 +1069,7 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
   int at_once = 0;
   if (!resident.get(ctx, &at_once, [&](int* v) {
         bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       L::alloc(kMaxGroups, kMostSplit, BN / 2)) == cudaSuccess;
+                                       L::alloc(kMaxGroups, kMostSplit, BN)) == cudaSuccess;
         // the split of the registers counts on the launch's
         cudaFuncAttributes fa = {};
         ok = ok && cudaFuncGetAttributes(&fa, kern) == cudaSuccess &&
