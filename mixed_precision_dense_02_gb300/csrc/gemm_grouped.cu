@@ -628,42 +628,35 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     for (int u = first_unit; u < units && ok; u += unit_step) {
       const Tile t = decode(u);
       constexpr int NP = kP / 32, NQ = ROWS ? 1 : BN / 32;
-      const float *src_p[NP], *src_q[NQ];
-      int len_p = 0, len_q = 0;  // one bit each: within the operand
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int p = t.p0 + rank * kP + i * 32 + lane;
-        len_p |= int(p < t.p1) << i;
-        src_p[i] = a.sp + (ROWS ? 0 : t.e * a.sp_group) +
-                   (int64_t(min(p, t.p1 - 1)) >> a.p_shift) * a.sp_row +
-                   (t.k0 / KE) * a.sp_blk;
-      }
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        const int q = ROWS ? t.q0 + lane * HALF : t.q0 + i * 32 + lane;
-        len_q |= int(q < t.q1) << i;
-        src_q[i] = a.sq + (ROWS ? t.e * a.sq_group : 0) +
-                   (int64_t(min(q, t.q1 - 1)) >> a.q_shift) * a.sq_row +
-                   (t.k0 / KE) * a.sq_blk;
-      }
+      // 32 rows per copy; with one scale per 128 rows all of P has one
+      const int p0 = t.p0 + rank * kP + lane;
+      const int q0 = ROWS ? t.q0 + lane * 128 : t.q0 + lane;
+      const float* src_p = a.sp + (ROWS ? 0 : t.e * a.sp_group) +
+                           (int64_t(p0) >> a.p_shift) * a.sp_row + (t.k0 / KE) * a.sp_blk;
+      const float* src_q = a.sq + (ROWS ? t.e * a.sq_group : 0) +
+                           (int64_t(q0) >> a.q_shift) * a.sq_row + (t.k0 / KE) * a.sq_blk;
+      const int64_t step_p = a.p_shift ? 0 : 32 * a.sp_row, step_q = 32 * a.sq_row;
       const int chunks = (t.k1 - t.k0 + KE - 1) / KE;
       for (int ch = 0; ch < chunks; ch += L::G) {
         ok = mbar_wait(&sempty[slot], phase ^ 1u, abort_flag, a.status);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         uint32_t dst = smem_u32(ring + slot * L::SLOT_FLOATS);
         for (int g = 0; g < L::G && ch + g < chunks; ++g, dst += L::CHUNK_FLOATS * 4) {
+          // (beyond the operand nothing is read, and zero is written)
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            cp_async_4_zfill(dst + (i * 32 + lane) * 4, src_p[i], ((len_p >> i) & 1) * 4);
-            src_p[i] += a.sp_blk;
+            const bool in = p0 + i * 32 < t.p1;
+            cp_async_4_zfill(dst + (i * 32 + lane) * 4, in ? src_p + i * step_p : a.sp, in * 4);
           }
 #pragma unroll
           for (int i = 0; i < NQ; ++i) {
+            const bool in = q0 + i * 32 < t.q1;
             if (!ROWS || lane < 2)
-              cp_async_4_zfill(dst + (kP + i * 32 + lane) * 4, src_q[i],
-                               ((len_q >> i) & 1) * 4);
-            src_q[i] += a.sq_blk;
+              cp_async_4_zfill(dst + (kP + i * 32 + lane) * 4,
+                               in ? src_q + i * step_q : a.sq, in * 4);
           }
+          src_p += a.sp_blk;
+          src_q += a.sq_blk;
         }
         cp_async_mbar_arrive(&sfull[slot]);
         if (++slot == L::SLOTS) {
@@ -706,8 +699,29 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
       const int pw = t.p0 + rank * kP + quarter * 32;
       const int p = pw + lane;
       float sum[HALF];
+      if (!ROWS && a.C && krank == 0 && p < t.p1) {
+        // The sums start from C, all of whose loads are under way at once
+        // (and land while the first chunks are computed).
+        const int64_t ci = (RAGK ? t.e * a.c_group : 0) + int64_t(t.q0) * a.ldc + p;
+        auto start = [&](auto read) {
 #pragma unroll
-      for (int j = 0; j < HALF; ++j) sum[j] = 0.f;
+          for (int i = 0; i < NB; ++i) {
+            int64_t at = ci + column(i) * a.ldc;
+            const int left = t.q1 - t.q0 - column(i);
+#pragma unroll
+            for (int j = 0; j < CB; ++j, at += a.ldc)
+              sum[i * CB + j] = j < left ? read(at) : 0.f;
+          }
+        };
+        if (a.d_type == MMA_F32)
+          start([&](int64_t i) { return static_cast<const float*>(a.C)[i]; });
+        else
+          start([&](int64_t i) { return load_c(a.C, i, a.d_type); });
+      } else {
+#pragma unroll
+        for (int j = 0; j < HALF; ++j) sum[j] = 0.f;
+      }
+      __syncwarp();
       const int num_kb = (t.k1 - t.k0 + KE - 1) / KE;
       const int chunks = (num_kb + a.kb_per_chunk - 1) / a.kb_per_chunk;
       // Wait for a chunk's sums in tensor memory, add them (through `add`,
@@ -715,9 +729,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
       // last block is in registers.  Scalar additions and one block in
       // flight: packed pairs of FP32 and a second block cost registers that
       // the sums need (four blocks of 32 columns by eight warps: 344 clocks,
-      // packed 728, of which reading tensor memory is 170).  With ROWS nearly
-      // every tile has all its columns, so what lies beyond nt is added like
-      // the rest, to sums that are not stored.
+      // packed 728, of which reading tensor memory is 170).  Of a tile of 256
+      // columns all are added, those beyond nt to sums that are not stored:
+      // asking cost more (8-bit with row scales 139 us, without 119).
       auto take = [&](auto&& add) {
         mbar_wait_lean(&tfull[acc], acc_phase, abort_flag, a.status);
         tc_fence_after();
@@ -725,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
             tmem_base + uint32_t(acc * BN) + (uint32_t(quarter * 32) << 16);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-          const bool in = ROWS || column(i) < t.nt;
+          const bool in = BN == 256 || column(i) < t.nt;
           uint32_t r[CB];
           if (in) {
             if constexpr (CB == 32)
@@ -924,28 +938,19 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
         for (int i = 0; i < NB; ++i) {
           const int q = t.q0 + column(i);
           if (q >= t.q1) continue;
-          float v[CB];
-#pragma unroll
-          for (int j = 0; j < CB; ++j) v[j] = sum[i * CB + j];
-          if (a.C) {
-            const int64_t ci = group * a.c_group + int64_t(q) * a.ldc + p;
-#pragma unroll
-            for (int j = 0; j < CB; ++j)
-              if (q + j < t.q1) v[j] += load_c(a.C, ci + j * a.ldc, a.d_type);
-          }
-          const int64_t di = group * a.d_group + int64_t(q) * a.ldd + p;
+          int64_t di = group * a.d_group + int64_t(q) * a.ldd + p;
+          const int left = t.q1 - q;
           if (a.d_type == MMA_F32) {
             float* d = static_cast<float*>(a.D) + di;
 #pragma unroll
-            for (int j = 0; j < CB; ++j)
-              if (q + j < t.q1) d[j * a.ldd] = v[j];
+            for (int j = 0; j < CB; ++j, d += a.ldd)
+              if (j < left) *d = sum[i * CB + j];
           } else {
             uint16_t* d = static_cast<uint16_t*>(a.D) + di;
             const bool bf16 = a.d_type == MMA_BF16;
 #pragma unroll
-            for (int j = 0; j < CB; ++j)
-              if (q + j < t.q1)
-                d[j * a.ldd] = uint16_t(pack16(v[j], 0.f, bf16));
+            for (int j = 0; j < CB; ++j, d += a.ldd)
+              if (j < left) *d = uint16_t(pack16(sum[i * CB + j], 0.f, bf16));
           }
         }
       }
