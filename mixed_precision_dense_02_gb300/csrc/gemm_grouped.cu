@@ -65,7 +65,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kLaunchRegs = 168, kLoadRegs = 56, kEpiRegs = 224;
 static_assert(kLoadRegs + 2 * kEpiRegs <= 3 * kLaunchRegs, "registers");
-constexpr int kBand = 16;  // p tiles of a band of the raster
+constexpr int kBand = 16;  // q tiles of a band of the raster
 
 // What a launch computes (see the table above).  Group e's tokens are
 // [row[e], row[e + 1]) of `offsets` (one group of rows_total without
@@ -81,6 +81,7 @@ struct GroupedArgs {
   // ROWS: four elements of a row of D (and C) can move at once; D is 16-bit,
   // there is no C and eight can
   int vec4, vec8;
+  int d_tma;  // ROWS: D may be stored through tmD
   const void* C;
   int64_t ldc, c_group;
   void* D;
@@ -108,9 +109,11 @@ struct Layout {
   static constexpr int CHUNK_FLOATS = kP + (ROWS ? 4 : BN);
   static constexpr int SLOT_FLOATS = G * CHUNK_FLOATS;
   static constexpr int SCALE_OFFSET = STAGES * STAGE_BYTES;
-  // per epilogue warp: staging of 32 rows x 16 columns of FP32 (ROWS)
-  static constexpr int WARP_BYTES = ROWS ? 2048 : 0;
-  static constexpr int WARP_OFFSET = SCALE_OFFSET + SLOTS * SLOT_FLOATS * 4;
+  // per epilogue warp: a ring of blocks of D, 32 rows x 64 bytes (ROWS)
+  static constexpr int BLOCKS = ROWS ? 4 : 0;
+  static constexpr int WARP_BYTES = BLOCKS * 2048;
+  static constexpr int WARP_OFFSET =
+      (SCALE_OFFSET + SLOTS * SLOT_FLOATS * 4 + 1023) / 1024 * 1024;
   static constexpr int BAR_OFFSET = WARP_OFFSET + kEpiWarps * WARP_BYTES;
   // Accumulators in tensor memory: as many as fit (with 32 and 64 columns
   // 256 of the 512, for two CTAs per SM).  A chunk's way through the MMAs, the
@@ -230,6 +233,7 @@ template <bool KIND8, bool P_MN, bool Q_MN, bool RAGK, bool ROWS, bool SPLIT, in
 __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP,
                         const __grid_constant__ CUtensorMap tmQ,
+                        const __grid_constant__ CUtensorMap tmD,
                         const __grid_constant__ GroupedArgs a) {
   using L = Layout<KIND8, ROWS, SPLIT, CL, BN, STAGES>;
   constexpr int KE = KIND8 ? 128 : 64;  // k elements per stage
@@ -379,8 +383,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     split_k1 = min(blocks * (krank + 1) / ksplit * KE, a.k_size);
   }
 
-  // Unit u: its group by bisection; within the group bands of kBand p tiles,
-  // p fastest, so that what runs at one time shares few panels.
+  // Unit u: its group by bisection; within the group bands of kBand q tiles,
+  // q fastest, so that what runs at one time shares few panels (with p
+  // fastest a group's few q tiles read its P panels at different times:
+  // grouped forward 181 us, so 176).
   auto decode = [&](int u) {
     int lo = 0, hi = a.groups;
     while (hi - lo > 1) {
@@ -396,11 +402,11 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     // (divisions cost a lone thread some hundred clocks each)
     int pi = r, qi = 0;
     if (nq > 1) {
-      const int band = np > kBand ? r / (kBand * nq) : 0;
-      const int bp = min(np - band * kBand, kBand);
-      const int in = r - band * kBand * nq;
-      qi = in / bp;
-      pi = band * kBand + in - qi * bp;
+      const int band = nq > kBand ? r / (kBand * np) : 0;
+      const int bq = min(nq - band * kBand, kBand);
+      const int in = r - band * kBand * np;
+      pi = in / bq;
+      qi = band * kBand + in - pi * bq;
     }
     if constexpr (ROWS) {
       t.p0 = g0 + pi * PT;
@@ -690,6 +696,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     const uint32_t tempty_lead =
         mapa_shared(smem_u32(&tempty[0]), CL > 1 ? 0 : cluster_ctarank());
     [[maybe_unused]] uint32_t part_phase = 0;
+    [[maybe_unused]] int block = 0;  // of the ring of blocks of D
     grid_dependency_wait();
     [[maybe_unused]] const int part_at =
         L::part_offset(a.groups) + (quarter * 32 + lane) * 4;
@@ -848,6 +855,59 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
         }
       }
       if constexpr (ROWS) {
+        if (a.d_tma && pw + 32 <= t.p1) {
+          // Blocks of 64 bytes of the warp's rows leave by TMA, which has the
+          // whole next tile's time to move them (stored by the warps they
+          // held up the MMAs: 257 us, nothing stored 224).
+          const bool wide = a.d_type == MMA_F32, bf16 = a.d_type == MMA_BF16;
+          auto send = [&](int c, const uint4 (&w)[4], int cols) {
+            const int q = t.q0 + h * HALF + c * cols;
+            if (q >= t.q1) return;
+            uint8_t* buf = reinterpret_cast<uint8_t*>(wbuf) + block * 2048;
+            if (++block == L::BLOCKS) block = 0;
+            if (lane == 0) bulk_wait_group_read<L::BLOCKS - 1>();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = w[j];
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&tmD, buf, q, pw, 0);
+              bulk_commit_group();
+            }
+          };
+          if (wide) {
+#pragma unroll
+            for (int c = 0; c < HALF / 16; ++c) {
+              uint4 w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float* const s = sum + c * 16 + 4 * j;
+                w[j] = make_uint4(__float_as_uint(s[0]), __float_as_uint(s[1]),
+                                  __float_as_uint(s[2]), __float_as_uint(s[3]));
+              }
+              send(c, w, 16);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < HALF / 32; ++c) {
+              uint4 w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float* const s = sum + c * 32 + 8 * j;
+                w[j] = make_uint4(pack16(s[0], s[1], bf16), pack16(s[2], s[3], bf16),
+                                  pack16(s[4], s[5], bf16), pack16(s[6], s[7], bf16));
+              }
+              send(c, w, 32);
+            }
+          }
+          continue;
+        }
+        // by the warp, through the ring's first block
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+        block = 0;
         if (a.vec8) {
           // 16-bit D without C: 32 columns at a time, rounded, through
           // shared memory, so that four lanes store 64 bytes of a row and a
@@ -956,6 +1016,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
       }
     }
   }
+  if (ROWS && warp >= 4 && lane == 0) bulk_wait_group<0>();  // D is written
   tc_fence_before();
   if (CL > 1 || ksplit > 1)
     cluster_sync();  // no CTA leaves while another may still signal it
@@ -1031,16 +1092,31 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
     return mn ? make_map(m, o.p, EB, len, o.rows, o.ld, o.slices, slice, 64, 64)
               : make_map(m, o.p, EB, args.k_size, o.rows, o.ld, o.slices, slice, KE, box);
   };
-  CUtensorMap tp, tq;
+  CUtensorMap tp, tq, td;
   if (!map_of(&tp, P, P_MN, args.p_size, kP) || !map_of(&tq, Q, Q_MN, args.q_size, BN / CL))
     return MMA_ERR_LAUNCH;
+  GroupedArgs a = args;
+  td = tp;
+  if constexpr (ROWS) {
+    // D by TMA: without C, 16-byte rows, and a width that is a multiple of
+    // 16 bytes (a box clipped inside a 16-byte chunk writes the chunk whole)
+    const int db = args.d_type == MMA_F32 ? 4 : 2;
+    if (args.C == nullptr && (reinterpret_cast<uintptr_t>(args.D) & 15) == 0 &&
+        args.ldd * db % 16 == 0 && int64_t(args.q_size) * db % 16 == 0) {
+      if (!make_cd_map(&td, args.D, args.q_size, args.rows_total, args.ldd,
+                       db == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32
+                               : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                       db))
+        return MMA_ERR_LAUNCH;
+      a.d_tma = 1;
+    }
+  }
   auto kern = gemm_grouped_kernel<KIND8, P_MN, Q_MN, RAGK, ROWS, SPLIT, CL, BN, STAGES>;
   constexpr int kMostSplit = !SPLIT ? 1 : BN == 32 ? 6 : BN == 64 ? 4 : 2;
   static_assert(L::alloc(kMaxGroups, kMostSplit, BN) <= 232448, "shared memory per CTA");
   // SPLIT: as many CTAs per tile as leave every tile's cluster room at once
   // (two CTAs per SM if their shared memory fits twice), each with four k
   // blocks at least.  One row, 8192 x 4096: 64 tiles, 14.7 us without.
-  GroupedArgs a = args;
   int split = 1;
   if constexpr (SPLIT) {
     const int64_t blocks = (int64_t(a.k_size) + KE - 1) / KE;
@@ -1093,7 +1169,7 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
   cfg.numAttrs = 2;
   cfg.gridDim = dim3(unsigned(clusters * CL * split), 1, 1);
   ctx.mark_start();
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tp, tq, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tp, tq, td, a);
   ctx.mark_stop();
   if (e != cudaSuccess) cudaGetLastError();
   return e == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
@@ -1159,7 +1235,7 @@ mma_status_t launch_gemm_f8(const Ctx& ctx, const F8Problem& f) {
     a.sq_row = f.sb_row;
     a.sq_blk = f.sb_blk;
     a.q_shift = 7;
-    return run<true, false, false, false, true, false, 2, 256, 6>(ctx, A, B, a);
+    return run<true, false, false, false, true, false, 2, 256, 4>(ctx, A, B, a);
   }
   a.p_size = int(f.N);
   a.q_size = int(f.rows);
@@ -1187,7 +1263,8 @@ mma_status_t launch_gemm_grouped(const Ctx& ctx, const GroupedProblem& g) {
   a.groups = int(g.groups);
   a.rows_total = int(g.rows);
   a.offsets = g.offsets;
-  a.kb_per_chunk = 4;
+  // (a 16-bit result's own rounding is 500 times what 512 terms lose)
+  a.kb_per_chunk = g.d_type == MMA_F32 ? 4 : 8;
   a.d_type = g.d_type;
   a.C = g.C;
   a.ldc = g.ldc;
@@ -1215,7 +1292,8 @@ mma_status_t launch_gemm_grouped_wgrad(const Ctx& ctx, const WgradProblem& g) {
   a.groups = int(g.groups);
   a.rows_total = int(g.rows);
   a.offsets = g.offsets;
-  a.kb_per_chunk = 4;
+  // (a 16-bit result's own rounding is 500 times what 512 terms lose)
+  a.kb_per_chunk = g.d_type == MMA_F32 ? 4 : 8;
   a.d_type = g.d_type;
   a.C = g.C;
   a.ldc = g.ldc;
