@@ -119,8 +119,12 @@ struct Layout {
   // 256 of the 512, for two CTAs per SM).  A chunk's way through the MMAs, the
   // epilogue and back takes some 1000 clocks whatever its size.
   static constexpr int ACCS = BN == 32 ? 8 : BN == 64 ? 4 : 512 / BN;
+  // Parts of an accumulator that are handed over by themselves (8-bit,
+  // 256 columns: its two halves, each to the four warps that add it), so
+  // that a half's MMAs wait for half the epilogue.
+  static constexpr int HV = KIND8 && BN == 256 ? 2 : 1;
   static constexpr int NUM_BARS =
-      4 * STAGES + 1 + 2 * ACCS + 2 * SLOTS + (SPLIT ? 2 * kEpiWarps : 0);
+      4 * STAGES + 1 + 2 * ACCS * HV + 2 * SLOTS + (SPLIT ? 2 * kEpiWarps : 0);
   static constexpr int GROUP_OFFSET = BAR_OFFSET + NUM_BARS * 8 + 24;
   static constexpr int round16(int v) { return (v + 15) & ~15; }
   // SPLIT: sums of the other ranks, 128 rows of P times the columns in use
@@ -240,6 +244,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
   constexpr int PT = kP * CL;           // rows of P per tile
   constexpr int QS = 16 * CL;           // granularity of the MMA's N
   constexpr int HALF = BN / 2;          // most columns of an epilogue warp
+  constexpr int HV = L::HV;
+  constexpr int QPART = BN / CL / HV;   // rows of Q per box
   constexpr int CB = HALF < 32 ? HALF : 32;
   constexpr int NB = HALF / CB;
   constexpr bool kSplitRegs = HALF == 128;
@@ -249,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFFSET);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
-  uint64_t* tempty = tfull + L::ACCS;
-  uint64_t* done = tempty + L::ACCS;
+  uint64_t* tempty = tfull + L::ACCS * L::HV;
+  uint64_t* done = tempty + L::ACCS * L::HV;
   uint64_t* cut_in = done + 1;         // RAGK: a cut block has landed here
   uint64_t* cut_ok = cut_in + STAGES;  // and its zeros are in place (leader)
   uint64_t* sfull = cut_ok + STAGES;
@@ -290,9 +296,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
       mbar_init(&sfull[s], 32);
       mbar_init(&sempty[s], kEpiWarps);
     }
-    for (int i = 0; i < L::ACCS; ++i) {
+    for (int i = 0; i < L::ACCS * L::HV; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], CL * kEpiWarps);
+      mbar_init(&tempty[i], CL * kEpiWarps / L::HV);
     }
     mbar_init(done, 1);
     if constexpr (SPLIT)
@@ -488,7 +494,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
             for (int i = 0; i < BN / CL / 64; ++i)
               load(&tmQ, sq + i * 8192, qy + 64 * i, k, zq);
           } else {
-            load(&tmQ, sq, k, qy, zq);
+            // (each half's columns from the two CTAs of a pair in equal parts)
+#pragma unroll
+            for (int v = 0; v < HV; ++v) {
+              const int nv = min(max(t.nt - v * HALF, 0), BN / HV);
+              load(&tmQ, sq + v * QPART * 128, k, t.q0 + v * HALF + rank * (nv / CL), zq);
+            }
           }
           ++issued;
           if (++stage == STAGES) {
@@ -531,6 +542,38 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
         const uint32_t idesc = a.idesc | (uint32_t(t.nt >> 3) << 17);
         int left = t.k1 - t.k0;  // k still to be issued
         while (left > 0 && ok) {
+          if constexpr (HV == 2) {
+            // one block of k per chunk, in halves of the columns
+            if (!ready) ok = mbar_wait(&full[stage], phase, abort_flag, a.status);
+            if (!ok) break;
+            const uint64_t dp = dp0 + uint32_t(stage * (L::STAGE_BYTES >> 4));
+            const uint64_t dq = dq0 + uint32_t(stage * (L::STAGE_BYTES >> 4));
+            uint64_t* const done_with = &empty[stage];
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              ok = mbar_wait(&tempty[acc * 2 + v], acc_phase ^ 1u, abort_flag, a.status);
+              if (!ok) break;
+              tc_fence_after();
+              const int nv = min(max(t.nt - v * HALF, 0), HALF);
+              const uint32_t id = a.idesc | (uint32_t(nv >> 3) << 17);
+              const uint32_t d_tmem = tmem_base + uint32_t(acc * BN + v * HALF);
+#pragma unroll
+              for (int s = 0; s < 4; ++s) {
+                if (v == 1 && s == 3) ready = mbar_test(&full[stage], phase);
+                if (nv > 0)
+                  umma_f8<CL>(d_tmem, dp + s * kStepP,
+                              dq + uint32_t(v * QPART * 8) + s * kStepQ, id, s > 0);
+              }
+              if (v == 1) umma_commit_pair(done_with, 3u);
+              umma_commit_pair(&tfull[acc * 2 + v], 3u);
+            }
+            if (!ok) break;
+            left -= KE;
+          } else {
           ok = mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, a.status);
           if (!ok) break;
           tc_fence_after();
@@ -580,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
             umma_commit(&tfull[acc]);
           else
             umma_commit_pair(&tfull[acc], 3u);
+          }
           if (++acc == L::ACCS) {
             acc = 0;
             acc_phase ^= 1u;
@@ -677,12 +721,14 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
   } else {
     // ------------------------------------------------ epilogue warps
     // A warp owns 32 rows of P (its tensor-memory lane quarter) and, of the
-    // columns, its half (ROWS) or every other block of CB.
+    // columns, its half (ROWS, halves) or every other block of CB.
     if constexpr (kSplitRegs) registers_take<kEpiRegs>();
     const int ew = warp - 4;
     const int quarter = warp & 3;
     const int h = ew >> 2;
-    auto column = [&](int i) { return ROWS ? h * HALF + i * CB : (2 * i + h) * CB; };
+    auto column = [&](int i) {
+      return ROWS || HV == 2 ? h * HALF + i * CB : (2 * i + h) * CB;
+    };
     [[maybe_unused]] float* wbuf =
         reinterpret_cast<float*>(smem + L::WARP_OFFSET + ew * L::WARP_BYTES);
     [[maybe_unused]] const float* ring =
@@ -740,7 +786,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
       // columns all are added, those beyond nt to sums that are not stored:
       // asking cost more (8-bit with row scales 139 us, without 119).
       auto take = [&](auto&& add) {
-        mbar_wait_lean(&tfull[acc], acc_phase, abort_flag, a.status);
+        const int ah = HV == 2 ? acc * 2 + h : acc;
+        mbar_wait_lean(&tfull[ah], acc_phase, abort_flag, a.status);
         tc_fence_after();
         const uint32_t taddr =
             tmem_base + uint32_t(acc * BN) + (uint32_t(quarter * 32) << 16);
@@ -758,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
           if (i + 1 == NB) {
             tc_fence_before();
             __syncwarp();
-            mbar_arrive_remote_if(tempty_lead + uint32_t(acc) * 8u, lane == 0);
+            mbar_arrive_remote_if(tempty_lead + uint32_t(ah) * 8u, lane == 0);
           }
           if (in) add(i, r);
         }
@@ -1093,7 +1140,7 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
               : make_map(m, o.p, EB, args.k_size, o.rows, o.ld, o.slices, slice, KE, box);
   };
   CUtensorMap tp, tq, td;
-  if (!map_of(&tp, P, P_MN, args.p_size, kP) || !map_of(&tq, Q, Q_MN, args.q_size, BN / CL))
+  if (!map_of(&tp, P, P_MN, args.p_size, kP) || !map_of(&tq, Q, Q_MN, args.q_size, BN / CL / L::HV))
     return MMA_ERR_LAUNCH;
   GroupedArgs a = args;
   td = tp;
