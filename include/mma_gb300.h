@@ -439,7 +439,7 @@ mma_status_t mma_rmsnorm_f8(int type, int w_type, int64_t M, int64_t N,
  * gradient of X and of the forward's residual alike, and may be DY or R.
  * DW is summed in a fixed order (the same bits from run to run), through
  * `workspace`: device memory of the caller, 4-byte aligned, of at least
- * mma_rmsnorm_backward_workspace(M, N) bytes (at most 304 * N * 4), which
+ * mma_rmsnorm_backward_workspace(M, N) bytes (at most 456 * N * 4), which
  * the call's work on `stream` uses and nothing else may meanwhile.  Types as
  * in mma_rmsnorm_f8.  M == 0 gives DW = 0.
  */

@@ -37,14 +37,14 @@ __device__ __forceinline__ float2 block_sum2(float a, float b, float2* buf) {
   if (warps == 1) return make_float2(a, b);
   if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
   __syncthreads();
-  const int lane = threadIdx.x & 31;
-  const float2 v = lane < warps ? buf[lane] : make_float2(0.f, 0.f);
-  a = v.x;
-  b = v.y;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, d);
-    b += __shfl_xor_sync(0xffffffffu, b, d);
+  // every thread adds the warps' sums in their order (independent reads; a
+  // second tree of shuffles took longer)
+  a = 0.f;
+  b = 0.f;
+#pragma unroll 4
+  for (int w = 0; w < warps; ++w) {
+    a += buf[w].x;
+    b += buf[w].y;
   }
   return make_float2(a, b);
 }
@@ -111,35 +111,55 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1)
     if (row + gridDim.x < p.M) fetch(row + gridDim.x);
     ss = block_sum2(ss, 0.f, red[flip]).x;
     const float rstd = __frsqrt_rn(ss / float(n) + p.eps);
+    // y replaces h; m: the largest magnitude of each vector's scale block
+    float m[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int64_t v = threadIdx.x + i * blockDim.x;
       const bool live = v * E < n;
       if (p.H && live)
         store_row<T, TAIL>(static_cast<T*>(p.H) + row * p.ldh, v, n, h[i]);
-      float y[E];
-      load_weight<T>(p.W, w32, v, n, y);
-      float m = 0.f;
+      float w[E];
+      load_weight<T>(p.W, w32, v, n, w);
+      m[i] = 0.f;
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        y[j] = h[i][j] * rstd * y[j];
+        h[i][j] = h[i][j] * rstd * w[j];
         // columns past the end (rstd may be infinite or NaN) do not count
-        if (TAIL && v * E + j >= n) y[j] = 0.f;
-        m = abs_max(m, y[j]);
+        if (TAIL && v * E + j >= n) h[i][j] = 0.f;
+        m[i] = abs_max(m[i], h[i][j]);
       }
-      if (!live) m = 0.f;
+      if (!live) m[i] = 0.f;
       if (p.Y && live)
-        store_row<T, TAIL>(static_cast<T*>(p.Y) + row * p.ldy, v, n, y);
-      if (!p.Q) continue;
+        store_row<T, TAIL>(static_cast<T*>(p.Y) + row * p.ldy, v, n, h[i]);
+    }
+    if (p.Q) {
 #pragma unroll
-      for (int d = kLanes / 2; d > 0; d >>= 1)
-        m = abs_max(m, __shfl_xor_sync(0xffffffffu, m, d));
-      const float s = block_scale<false>(abs_bits(m), p.pow2);
-      if (!live) continue;
-      store_f8<false, E, TAIL>(static_cast<uint8_t*>(p.Q) + row * p.ldq, v, n, y,
-                               __fdiv_rn(1.f, s));
-      if (threadIdx.x % kLanes == 0)
-        p.S[row * p.s_row + (v * E / kScaleBlock) * p.s_blk] = s;
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int d = kLanes / 2; d > 0; d >>= 1)
+          m[i] = abs_max(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
+      // the thread's VPT scales and reciprocals, each made by another lane of
+      // the block's group
+      const int mine = threadIdx.x % kLanes % 4;
+      float mm = m[0];
+#pragma unroll
+      for (int i = 1; i < VPT; ++i) mm = mine == i ? m[i] : mm;
+      const float s = block_scale<false>(abs_bits(mm), p.pow2);
+      const float inv = __fdiv_rn(1.f, s);
+      const int lane0 = threadIdx.x & 31 & ~(kLanes - 1);
+      if (threadIdx.x % kLanes < VPT) {
+        const int64_t b = (threadIdx.x + int64_t(mine) * blockDim.x) / kLanes;
+        if (b * kScaleBlock < n) p.S[row * p.s_row + b * p.s_blk] = s;
+      }
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int64_t v = threadIdx.x + i * blockDim.x;
+        const float f = __shfl_sync(0xffffffffu, inv, lane0 + i);
+        if (v * E < n)
+          store_f8<false, E, TAIL>(static_cast<uint8_t*>(p.Q) + row * p.ldq, v, n,
+                                   h[i], f);
+      }
     }
   }
 }
@@ -389,7 +409,7 @@ __global__ void __launch_bounds__(1024)
   if (threadIdx.x == 0 && c < n) out[c] = s;
 }
 
-constexpr int kMostParts = 304;  // blocks of the backward pass, two per SM
+constexpr int kMostParts = 456;  // blocks of the backward pass, three per SM
 
 // Calls f(VPT, MAXT, threads) for rows of `vectors` vectors: up to 256
 // threads with up to 4 vectors each, so that several rows are under way per
@@ -439,12 +459,13 @@ template <class T>
 mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32,
                       float* part) {
   constexpr int E = Vec<T>::kN;
-  const int grid = int(std::min<int64_t>(p.M, std::min(kMostParts, 2 * ctx.num_sms)));
+  const int grid = int(std::min<int64_t>(p.M, std::min(kMostParts, 3 * ctx.num_sms)));
   const int64_t vectors = (p.N + E - 1) / E;
-  // Two blocks per SM and two to four rows ahead, as far as 220 KB allow.
+  // Three blocks per SM (one of wide rows) and two to four rows ahead, as
+  // far as 220 KB allow.
   const int vpt = vectors <= 512 ? 1 : vectors <= 1024 ? 2 : 4;
   const int64_t stage = vectors * 16 * (p.R ? 3 : 2);
-  const int64_t room = (vpt <= 2 ? 110 : 220) * 1024;
+  const int64_t room = (vpt <= 2 ? 73 : 220) * 1024;
   const int stages = int(std::min<int64_t>(4, room / std::max<int64_t>(stage, 1)));
   if (grid > 0 && vectors <= 2048 && stages >= 2) {
     const int threads = int((vectors + vpt - 1) / vpt + 31) / 32 * 32;
