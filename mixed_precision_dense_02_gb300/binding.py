@@ -346,10 +346,14 @@ def gemm_batched(A, B, C=None, D=None, *, group: int = 1, abid: int = 0,
 # 8-bit operands with scales, products grouped by expert
 
 # These calls serve single tokens too, where the kernel takes a few
-# microseconds: what Python does per call is kept short (types looked up in
-# tables, no temporary tensors, the stream's handle without a Stream object).
+# microseconds and Python's share counts.  So what a call's argument layouts
+# (types, shapes, strides, device) settle is worked out once per layout and
+# kept as a plan: the checks, the ABI's codes and leading dimensions, the
+# layouts of the results.  A plan holds no tensor and no address.
 
 _KIND = {}
+_PLANS = {}
+_MOST_PLANS = 4096
 
 
 def _kinds():
@@ -367,10 +371,26 @@ def _kinds():
     return _KIND
 
 
-def _raw_stream(stream, device):
+def _key(t):
+    """What a plan may depend on of a tensor."""
+    return None if t is None else (t.dtype, t.shape, t.stride(), t.get_device())
+
+
+def _plan(key, make, *args):
+    """The plan of a call whose argument layouts are `key`."""
+    plan = _PLANS.get(key)
+    if plan is None:
+        if len(_PLANS) >= _MOST_PLANS:
+            _PLANS.clear()
+        plan = make(*args)  # raises what the arguments deserve
+        _PLANS[key] = plan
+    return plan
+
+
+def _raw_stream(stream, index):
     """The cudaStream_t of `stream`, or of the device's current stream."""
     if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(device.index)
+        return _torch()._C._cuda_getCurrentRawStream(index)
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -390,6 +410,14 @@ def _take(name, t, kinds, *shape):
     return code
 
 
+def _one_device(*tensors):
+    """The index of the device that all the tensors are on."""
+    at = {t.get_device() for t in tensors if t is not None}
+    if len(at) > 1:
+        raise ValueError("the tensors must be on one device")
+    return at.pop()
+
+
 def _rows(name, t) -> int:
     """Leading dimension of the last two axes: contiguous rows.  A single
     row has any leading dimension; its own length rounded up to 16 bytes
@@ -399,24 +427,13 @@ def _rows(name, t) -> int:
         raise ValueError(f"{name}: the last axis must be contiguous")
     if shape[-2] > 1:
         return stride[-2]
-    per = 16 // t.dtype.itemsize
-    return -(-shape[-1] // per) * per
+    return _row_of(shape[-1], t.dtype)
 
 
-def _empty_rows(m, n, dtype, device):
-    """An m x n tensor whose rows start on 16-byte boundaries."""
-    torch = _torch()
+def _row_of(n, dtype) -> int:
+    """Elements of a row of n that ends on a 16-byte boundary."""
     per = 16 // dtype.itemsize
-    wide = -(-n // per) * per
-    t = torch.empty((m, wide), dtype=dtype, device=device)
-    return t if wide == n else t[:, :n]
-
-
-def _empty_scales(rows, blocks, device):
-    """Scales (rows, blocks), the rows of one block side by side."""
-    torch = _torch()
-    return torch.empty_strided((rows, blocks), (1, rows), dtype=torch.float32,
-                               device=device)
+    return -(-n // per) * per
 
 
 def _scale_strides(t):
@@ -425,14 +442,9 @@ def _scale_strides(t):
     return (stride[-2] if shape[-2] > 1 else 1, stride[-1] if shape[-1] > 1 else 0)
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 def _weight(W, X, n):
     """The ABI code of a norm's weights: of X's type or float32."""
-    kinds = _kinds()["wide"]
-    code = _take("W", W, kinds, n)
+    code = _take("W", W, _kinds()["wide"], n)
     if code != MMA_F32 and W.dtype != X.dtype:
         raise TypeError(f"W must be {X.dtype} or torch.float32, not {W.dtype}")
     if n > 1 and W.stride(0) != 1:
@@ -446,8 +458,8 @@ def _same(name, t, X, *shape):
     _take(name, t, _kinds()["wide"], *shape)
 
 
-def _result(name, C, D, shape, out_dtype, device):
-    """C and D of a product: their type's code, and D allocated if absent."""
+def _result(name, C, D, shape, out_dtype):
+    """The type of a product's C and D and its code."""
     given = D if D is not None else C
     if given is not None:
         if out_dtype is not None and given.dtype != out_dtype:
@@ -462,9 +474,21 @@ def _result(name, C, D, shape, out_dtype, device):
     code = kinds.get(out_dtype)
     if code is None:
         raise TypeError(f"{name}: unsupported result type {out_dtype}")
-    if D is None:
-        D = _torch().empty(shape, dtype=out_dtype, device=device)
-    return code, D
+    return out_dtype, code
+
+
+def _plan_rmsnorm(X, W, residual):
+    kinds = _kinds()
+    code = _take("X", X, kinds["wide"], None, None)
+    M, N = X.shape
+    w_code = _weight(W, X, N)
+    ldr = 0
+    if residual is not None:
+        _same("residual", residual, X, M, N)
+        ldr = _rows("residual", residual)
+    q = kinds["fmt"]["e4m3"]
+    return (code, w_code, M, N, _rows("X", X), ldr, _row_of(N, X.dtype),
+            q, _row_of(N, q), -(-N // 128), _one_device(X, W, residual))
 
 
 def rmsnorm_f8(X, W, residual=None, *, eps: float = 1e-6, pow2: bool = False,
@@ -478,27 +502,39 @@ def rmsnorm_f8(X, W, residual=None, *, eps: float = 1e-6, pow2: bool = False,
     float8_e4m3fn, S (M, ceil(N / 128)), H the sum in X's type (X itself
     without a residual); with ``y=True`` also y in X's type.
     """
-    kinds = _kinds()
-    code = _take("X", X, kinds["wide"], None, None)
-    M, N = X.shape
-    w_code = _weight(W, X, N)
+    torch = _torch()
+    (code, w_code, M, N, ldx, ldr, ldh, f8, ldq, blocks, index) = _plan(
+        ("norm", _key(X), _key(W), _key(residual)), _plan_rmsnorm, X, W, residual)
     dtype, device = X.dtype, X.device
-    H, h_ptr, ldh, ldr = X, None, 0, 0
+    H, r_ptr, h_ptr = X, None, None
     if residual is not None:
-        _same("residual", residual, X, M, N)
-        ldr = _rows("residual", residual)
-        H = _empty_rows(M, N, dtype, device)
-        h_ptr, ldh = H.data_ptr(), _rows("H", H)
-    Q = _empty_rows(M, N, kinds["fmt"]["e4m3"], device)
-    S = _empty_scales(M, -(-N // 128), device)
-    Y = _empty_rows(M, N, dtype, device) if y else None
+        H = torch.empty_strided((M, N), (ldh, 1), dtype=dtype, device=device)
+        r_ptr, h_ptr = residual.data_ptr(), H.data_ptr()
+    Q = torch.empty_strided((M, N), (ldq, 1), dtype=f8, device=device)
+    # the scales of one block side by side
+    S = torch.empty_strided((M, blocks), (1, M), dtype=torch.float32, device=device)
+    Y = (torch.empty_strided((M, N), (ldh, 1), dtype=dtype, device=device)
+         if y else None)
     st = load().mma_rmsnorm_f8(
-        code, w_code, M, N, X.data_ptr(), _rows("X", X), _ptr(residual), ldr,
-        W.data_ptr(), eps, 1 if pow2 else 0, h_ptr, ldh, _ptr(Y),
-        0 if Y is None else _rows("Y", Y), Q.data_ptr(), _rows("Q", Q),
-        S.data_ptr(), 1, M, _raw_stream(stream, device))
-    _check("mma_rmsnorm_f8", st)
+        code, w_code, M, N, X.data_ptr(), ldx, r_ptr, ldr, W.data_ptr(), eps,
+        1 if pow2 else 0, h_ptr, ldh, None if Y is None else Y.data_ptr(), ldh,
+        Q.data_ptr(), ldq, S.data_ptr(), 1, M, _raw_stream(stream, index))
+    if st:
+        _check("mma_rmsnorm_f8", st)
     return (Q, S, H, Y) if y else (Q, S, H)
+
+
+def _plan_rmsnorm_backward(dY, H, W, dH):
+    code = _take("H", H, _kinds()["wide"], None, None)
+    M, N = H.shape
+    _same("dY", dY, H, M, N)
+    w_code = _weight(W, H, N)
+    if dH is not None:
+        _same("dH", dH, H, M, N)
+    return (code, w_code, M, N, _rows("dY", dY), _rows("H", H),
+            0 if dH is None else _rows("dH", dH), _row_of(N, H.dtype),
+            load().mma_rmsnorm_backward_workspace(M, N),
+            _one_device(dY, H, W, dH))
 
 
 def rmsnorm_backward(dY, H, W, dH=None, *, eps: float = 1e-6, stream=None):
@@ -510,25 +546,35 @@ def rmsnorm_backward(dY, H, W, dH=None, *, eps: float = 1e-6, stream=None):
     float32.
     """
     torch = _torch()
-    code = _take("H", H, _kinds()["wide"], None, None)
-    M, N = H.shape
-    _same("dY", dY, H, M, N)
-    w_code = _weight(W, H, N)
-    if dH is not None:
-        _same("dH", dH, H, M, N)
+    code, w_code, M, N, ldy, ldh, ldr, ldx, need, index = _plan(
+        ("back", _key(dY), _key(H), _key(W), _key(dH)), _plan_rmsnorm_backward,
+        dY, H, W, dH)
     device = H.device
-    dX = _empty_rows(M, N, H.dtype, device)
+    dX = torch.empty_strided((M, N), (ldx, 1), dtype=H.dtype, device=device)
     dW = torch.empty((N,), dtype=torch.float32, device=device)
-    need = load().mma_rmsnorm_backward_workspace(M, N)
-    # (freed by this stream's allocator only after the call's work)
+    # (its memory goes to other work of this stream only after the call's)
     ws = torch.empty((need,), dtype=torch.uint8, device=device)
     st = load().mma_rmsnorm_backward(
-        code, w_code, M, N, dY.data_ptr(), _rows("dY", dY), H.data_ptr(),
-        _rows("H", H), W.data_ptr(), eps, _ptr(dH),
-        0 if dH is None else _rows("dH", dH), dX.data_ptr(), _rows("dX", dX),
-        dW.data_ptr(), ws.data_ptr(), need, _raw_stream(stream, device))
-    _check("mma_rmsnorm_backward", st)
+        code, w_code, M, N, dY.data_ptr(), ldy, H.data_ptr(), ldh, W.data_ptr(),
+        eps, None if dH is None else dH.data_ptr(), ldr, dX.data_ptr(), ldx,
+        dW.data_ptr(), ws.data_ptr(), need, _raw_stream(stream, index))
+    if st:
+        _check("mma_rmsnorm_backward", st)
     return dX, dW
+
+
+def _plan_quantize(X, fmt, block_rows, transpose):
+    kinds = _kinds()
+    code = _take("X", X, kinds["wide"], None, None)
+    f8 = kinds["fmt"].get(fmt)
+    if f8 is None:
+        raise ValueError(f"fmt must be e4m3 or e5m2, not {fmt!r}")
+    if block_rows != 1 and block_rows != 128:
+        raise ValueError("block_rows must be 1 or 128")
+    M, N = X.shape
+    m, n = (N, M) if transpose else (M, N)
+    return (code, f8, kinds["f8"][f8], M, N, _rows("X", X), m, n, _row_of(n, f8),
+            -(-m // block_rows), -(-n // 128), X.get_device())
 
 
 def quantize_f8(X, *, fmt: str = "e4m3", block_rows: int = 1,
@@ -539,24 +585,22 @@ def quantize_f8(X, *, fmt: str = "e4m3", block_rows: int = 1,
     the result, which is X or, with ``transpose``, its transpose (N, M).
     Returns ``(Q, S)`` with S (ceil(rows / block_rows), ceil(columns / 128)).
     """
-    kinds = _kinds()
-    code = _take("X", X, kinds["wide"], None, None)
-    f8 = kinds["fmt"].get(fmt)
-    if f8 is None:
-        raise ValueError(f"fmt must be e4m3 or e5m2, not {fmt!r}")
-    if block_rows != 1 and block_rows != 128:
-        raise ValueError("block_rows must be 1 or 128")
-    M, N = X.shape
-    m, n = (N, M) if transpose else (M, N)
+    torch = _torch()
+    transpose = bool(transpose)
+    code, f8, f8_code, M, N, ldx, m, n, ldq, s_rows, blocks, index = _plan(
+        ("quantize", _key(X), fmt, block_rows, transpose), _plan_quantize, X, fmt,
+        block_rows, transpose)
     device = X.device
-    Q = _empty_rows(m, n, f8, device)
-    s_rows = -(-m // block_rows)
-    S = _empty_scales(s_rows, -(-n // 128), device)
+    Q = torch.empty_strided((m, n), (ldq, 1), dtype=f8, device=device)
+    # the scales of one block side by side
+    S = torch.empty_strided((s_rows, blocks), (1, s_rows), dtype=torch.float32,
+                            device=device)
     st = load().mma_quantize_f8(
-        code, kinds["f8"][f8], M, N, block_rows, 1 if transpose else 0,
-        1 if pow2 else 0, X.data_ptr(), _rows("X", X), Q.data_ptr(),
-        _rows("Q", Q), S.data_ptr(), 1, s_rows, _raw_stream(stream, device))
-    _check("mma_quantize_f8", st)
+        code, f8_code, M, N, block_rows, 1 if transpose else 0, 1 if pow2 else 0,
+        X.data_ptr(), ldx, Q.data_ptr(), ldq, S.data_ptr(), 1, s_rows,
+        _raw_stream(stream, index))
+    if st:
+        _check("mma_quantize_f8", st)
     return Q, S
 
 
@@ -570,16 +614,7 @@ def _scale_rows(SB, N):
     raise ValueError(f"SB must have {N} or {-(-N // 128)} rows, not {rows}")
 
 
-def gemm_f8(A, SA, B, SB, C=None, D=None, *, out_dtype=None, stream=None):
-    """D = A @ B^T + C for 8-bit operands with scales.
-
-    ``A``: (M, K), ``B``: (N, K), each float8_e4m3fn or float8_e5m2;
-    ``SA``: (M, ceil(K / 128)) float32; ``SB``: (N, ceil(K / 128)) or, a scale
-    for each 128 x 128 block, (ceil(N / 128), ceil(K / 128)).  ``C``, ``D``:
-    (M, N) bfloat16, float16 or float32 (``out_dtype``, bfloat16 unless C or D
-    is given).  Any strides of the scales; those of ``quantize_f8`` are read
-    fastest.  Returns D.
-    """
+def _plan_gemm_f8(A, SA, B, SB, C, D, out_dtype):
     kinds = _kinds()
     f8, scale = kinds["f8"], kinds["scale"]
     a_code = _take("A", A, f8, None, None)
@@ -591,28 +626,69 @@ def gemm_f8(A, SA, B, SB, C=None, D=None, *, out_dtype=None, stream=None):
     _take("SB", SB, scale, None, kb)
     if out_dtype is None and C is None and D is None:
         out_dtype = _torch().bfloat16
-    device = A.device
-    d_code, D = _result("gemm_f8", C, D, (M, N), out_dtype, device)
+    dtype, d_code = _result("gemm_f8", C, D, (M, N), out_dtype)
+    return (a_code, b_code, d_code, M, N, K, _rows("A", A), *_scale_strides(SA),
+            _rows("B", B), _scale_rows(SB, N), *_scale_strides(SB),
+            0 if C is None else _rows("C", C), N if D is None else _rows("D", D),
+            dtype, _one_device(A, SA, B, SB, C, D))
+
+
+def gemm_f8(A, SA, B, SB, C=None, D=None, *, out_dtype=None, stream=None):
+    """D = A @ B^T + C for 8-bit operands with scales.
+
+    ``A``: (M, K), ``B``: (N, K), each float8_e4m3fn or float8_e5m2;
+    ``SA``: (M, ceil(K / 128)) float32; ``SB``: (N, ceil(K / 128)) or, a scale
+    for each 128 x 128 block, (ceil(N / 128), ceil(K / 128)).  ``C``, ``D``:
+    (M, N) bfloat16, float16 or float32 (``out_dtype``, bfloat16 unless C or D
+    is given).  Any strides of the scales; those of ``quantize_f8`` are read
+    fastest.  Returns D.
+    """
+    (a_code, b_code, d_code, M, N, K, lda, sa_row, sa_blk, ldb, sb_rows, sb_row,
+     sb_blk, ldc, ldd, dtype, index) = _plan(
+        ("f8", _key(A), _key(SA), _key(B), _key(SB), _key(C), _key(D), out_dtype),
+        _plan_gemm_f8, A, SA, B, SB, C, D, out_dtype)
+    if D is None:
+        D = _torch().empty((M, N), dtype=dtype, device=A.device)
     st = load().mma_gemm_f8(
-        a_code, b_code, d_code, M, N, K, A.data_ptr(), _rows("A", A),
-        SA.data_ptr(), *_scale_strides(SA), B.data_ptr(), _rows("B", B),
-        SB.data_ptr(), _scale_rows(SB, N), *_scale_strides(SB), _ptr(C),
-        0 if C is None else _rows("C", C), D.data_ptr(), _rows("D", D),
-        _raw_stream(stream, device))
-    _check("mma_gemm_f8", st)
+        a_code, b_code, d_code, M, N, K, A.data_ptr(), lda, SA.data_ptr(), sa_row,
+        sa_blk, B.data_ptr(), ldb, SB.data_ptr(), sb_rows, sb_row, sb_blk,
+        None if C is None else C.data_ptr(), ldc, D.data_ptr(), ldd,
+        _raw_stream(stream, index))
+    if st:
+        _check("mma_gemm_f8", st)
     return D
 
 
-def _offsets(offsets, groups):
+def _check_offsets(offsets, groups):
     _take("offsets", offsets, _kinds()["offset"], groups + 1)
     if groups and offsets.stride(0) != 1:
         raise ValueError("offsets must be contiguous")
-    return offsets.data_ptr()
 
 
 def _slices(name, t) -> int:
     """Elements between the matrices of a (groups, rows, columns) tensor."""
     return t.stride(0) if t.shape[0] > 1 else t.shape[1] * _rows(name, t)
+
+
+def _plan_grouped(A, B, offsets, C, D, b_layout, out_dtype):
+    code = _take("A", A, _kinds()["half"], None, None)
+    T, K = A.shape
+    if b_layout not in ("col", "row"):
+        raise ValueError(b_layout)
+    row = b_layout == "row"
+    if row:
+        _same("B", B, A, None, K, None)
+    else:
+        _same("B", B, A, None, None, K)
+    groups, N = B.shape[0], B.shape[2 if row else 1]
+    _check_offsets(offsets, groups)
+    if out_dtype is None and C is None and D is None:
+        out_dtype = A.dtype
+    dtype, d_code = _result("gemm_grouped", C, D, (T, N), out_dtype)
+    return (code, d_code, groups, T, N, K, _rows("A", A), _rows("B", B),
+            _slices("B", B), MMA_ROW_MAJOR if row else MMA_COL_MAJOR,
+            0 if C is None else _rows("C", C), N if D is None else _rows("D", D),
+            dtype, _one_device(A, B, offsets, C, D))
 
 
 def gemm_grouped(A, B, offsets, C=None, D=None, *, b_layout: str = "col",
@@ -626,29 +702,39 @@ def gemm_grouped(A, B, offsets, C=None, D=None, *, b_layout: str = "col",
     A's type or float32 (``out_dtype``, A's unless C or D is given).  Rows of
     no expert are not written.  Returns D.
     """
-    code = _take("A", A, _kinds()["half"], None, None)
-    T, K = A.shape
-    if b_layout not in ("col", "row"):
-        raise ValueError(b_layout)
-    row = b_layout == "row"
-    if row:
-        _same("B", B, A, None, K, None)
-    else:
-        _same("B", B, A, None, None, K)
-    groups, N = B.shape[0], B.shape[2 if row else 1]
-    at = _offsets(offsets, groups)
-    if out_dtype is None and C is None and D is None:
-        out_dtype = A.dtype
-    device = A.device
-    d_code, D = _result("gemm_grouped", C, D, (T, N), out_dtype, device)
+    (code, d_code, groups, T, N, K, lda, ldb, stride_b, layout, ldc, ldd, dtype,
+     index) = _plan(
+        ("grouped", _key(A), _key(B), _key(offsets), _key(C), _key(D), b_layout,
+         out_dtype),
+        _plan_grouped, A, B, offsets, C, D, b_layout, out_dtype)
+    if D is None:
+        D = _torch().empty((T, N), dtype=dtype, device=A.device)
     st = load().mma_gemm_grouped(
-        code, d_code, groups, T, N, K, A.data_ptr(), _rows("A", A),
-        B.data_ptr(), _rows("B", B), _slices("B", B),
-        MMA_ROW_MAJOR if row else MMA_COL_MAJOR, at, _ptr(C),
-        0 if C is None else _rows("C", C), D.data_ptr(), _rows("D", D),
-        _raw_stream(stream, device))
-    _check("mma_gemm_grouped", st)
+        code, d_code, groups, T, N, K, A.data_ptr(), lda, B.data_ptr(), ldb,
+        stride_b, layout, offsets.data_ptr(), None if C is None else C.data_ptr(),
+        ldc, D.data_ptr(), ldd, _raw_stream(stream, index))
+    if st:
+        _check("mma_gemm_grouped", st)
     return D
+
+
+def _plan_wgrad(dY, X, offsets, C, D, out_dtype):
+    code = _take("dY", dY, _kinds()["half"], None, None)
+    T, N = dY.shape
+    _same("X", X, dY, T, None)
+    K = X.shape[1]
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must hold one value more than there are experts")
+    groups = offsets.shape[0] - 1
+    _check_offsets(offsets, groups)
+    if out_dtype is None and C is None and D is None:
+        out_dtype = _torch().float32
+    dtype, d_code = _result("gemm_grouped_wgrad", C, D, (groups, N, K), out_dtype)
+    return (code, d_code, groups, T, N, K, _rows("dY", dY), _rows("X", X),
+            0 if C is None else _rows("C", C), 0 if C is None else _slices("C", C),
+            K if D is None else _rows("D", D),
+            N * K if D is None else _slices("D", D), dtype,
+            _one_device(dY, X, offsets, C, D))
 
 
 def gemm_grouped_wgrad(dY, X, offsets, C=None, D=None, *, out_dtype=None,
@@ -661,27 +747,40 @@ def gemm_grouped_wgrad(dY, X, offsets, C=None, D=None, *, out_dtype=None,
     C may be D, to accumulate).  An expert without rows gives C[e], or zeros.
     Returns D.
     """
-    code = _take("dY", dY, _kinds()["half"], None, None)
-    T, N = dY.shape
-    _same("X", X, dY, T, None)
-    K = X.shape[1]
-    if offsets.dim() != 1 or offsets.shape[0] < 1:
-        raise ValueError("offsets must hold one value more than there are experts")
-    groups = offsets.shape[0] - 1
-    at = _offsets(offsets, groups)
-    if out_dtype is None and C is None and D is None:
-        out_dtype = _torch().float32
-    device = dY.device
-    d_code, D = _result("gemm_grouped_wgrad", C, D, (groups, N, K), out_dtype,
-                        device)
+    (code, d_code, groups, T, N, K, ldy, ldx, ldc, stride_c, ldd, stride_d, dtype,
+     index) = _plan(
+        ("wgrad", _key(dY), _key(X), _key(offsets), _key(C), _key(D), out_dtype),
+        _plan_wgrad, dY, X, offsets, C, D, out_dtype)
+    if D is None:
+        D = _torch().empty((groups, N, K), dtype=dtype, device=dY.device)
     st = load().mma_gemm_grouped_wgrad(
-        code, d_code, groups, T, N, K, dY.data_ptr(), _rows("dY", dY),
-        X.data_ptr(), _rows("X", X), at, _ptr(C),
-        0 if C is None else _rows("C", C), 0 if C is None else _slices("C", C),
-        D.data_ptr(), _rows("D", D), _slices("D", D),
-        _raw_stream(stream, device))
-    _check("mma_gemm_grouped_wgrad", st)
+        code, d_code, groups, T, N, K, dY.data_ptr(), ldy, X.data_ptr(), ldx,
+        offsets.data_ptr(), None if C is None else C.data_ptr(), ldc, stride_c,
+        D.data_ptr(), ldd, stride_d, _raw_stream(stream, index))
+    if st:
+        _check("mma_gemm_grouped_wgrad", st)
     return D
+
+
+def _plan_grouped_f8(A, SA, B, SB, offsets, C, D, out_dtype):
+    kinds = _kinds()
+    f8, scale = kinds["f8"], kinds["scale"]
+    a_code = _take("A", A, f8, None, None)
+    T, K = A.shape
+    b_code = _take("B", B, f8, None, None, K)
+    groups, N = B.shape[0], B.shape[1]
+    kb = -(-K // 128)
+    _take("SA", SA, scale, T, kb)
+    _take("SB", SB, scale, groups, None, kb)
+    _check_offsets(offsets, groups)
+    if out_dtype is None and C is None and D is None:
+        out_dtype = _torch().bfloat16
+    dtype, d_code = _result("gemm_grouped_f8", C, D, (T, N), out_dtype)
+    return (a_code, b_code, d_code, groups, T, N, K, _rows("A", A),
+            *_scale_strides(SA), _rows("B", B), _slices("B", B),
+            _scale_rows(SB, N), SB.stride(0), *_scale_strides(SB),
+            0 if C is None else _rows("C", C), N if D is None else _rows("D", D),
+            dtype, _one_device(A, SA, B, SB, offsets, C, D))
 
 
 def gemm_grouped_f8(A, SA, B, SB, offsets, C=None, D=None, *, out_dtype=None,
@@ -692,27 +791,21 @@ def gemm_grouped_f8(A, SA, B, SB, offsets, C=None, D=None, *, out_dtype=None,
     (E, N, K); ``SB``: (E, N, ceil(K / 128)) or (E, ceil(N / 128),
     ceil(K / 128)).  Returns D (T, N), bfloat16 unless given otherwise.
     """
-    kinds = _kinds()
-    f8, scale = kinds["f8"], kinds["scale"]
-    a_code = _take("A", A, f8, None, None)
-    T, K = A.shape
-    b_code = _take("B", B, f8, None, None, K)
-    groups, N = B.shape[0], B.shape[1]
-    kb = -(-K // 128)
-    _take("SA", SA, scale, T, kb)
-    _take("SB", SB, scale, groups, None, kb)
-    at = _offsets(offsets, groups)
-    if out_dtype is None and C is None and D is None:
-        out_dtype = _torch().bfloat16
-    device = A.device
-    d_code, D = _result("gemm_grouped_f8", C, D, (T, N), out_dtype, device)
+    (a_code, b_code, d_code, groups, T, N, K, lda, sa_row, sa_blk, ldb, stride_b,
+     sb_rows, sb_group, sb_row, sb_blk, ldc, ldd, dtype, index) = _plan(
+        ("grouped_f8", _key(A), _key(SA), _key(B), _key(SB), _key(offsets), _key(C),
+         _key(D), out_dtype),
+        _plan_grouped_f8, A, SA, B, SB, offsets, C, D, out_dtype)
+    if D is None:
+        D = _torch().empty((T, N), dtype=dtype, device=A.device)
     st = load().mma_gemm_grouped_f8(
-        a_code, b_code, d_code, groups, T, N, K, A.data_ptr(), _rows("A", A),
-        SA.data_ptr(), *_scale_strides(SA), B.data_ptr(), _rows("B", B),
-        _slices("B", B), SB.data_ptr(), _scale_rows(SB, N), SB.stride(0),
-        *_scale_strides(SB), at, _ptr(C), 0 if C is None else _rows("C", C),
-        D.data_ptr(), _rows("D", D), _raw_stream(stream, device))
-    _check("mma_gemm_grouped_f8", st)
+        a_code, b_code, d_code, groups, T, N, K, A.data_ptr(), lda, SA.data_ptr(),
+        sa_row, sa_blk, B.data_ptr(), ldb, stride_b, SB.data_ptr(), sb_rows,
+        sb_group, sb_row, sb_blk, offsets.data_ptr(),
+        None if C is None else C.data_ptr(), ldc, D.data_ptr(), ldd,
+        _raw_stream(stream, index))
+    if st:
+        _check("mma_gemm_grouped_f8", st)
     return D
 
 
