@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(1024)
 // its share of dw stays in registers.  That goes to row b of `part` at the
 // end; the shares are added in a fixed order by sum_parts_kernel, so the
 // result does not change from run to run.
-template <class T, int VPT>
+template <class T, int VPT, bool TAIL>
 __global__ void __launch_bounds__(512, VPT <= 2 ? 2 : 1)
     rmsnorm_backward_kernel(const NormBackProblem p, bool w32, int stages,
                             int row_bytes, float* __restrict__ part,
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(512, VPT <= 2 ? 2 : 1)
   __shared__ float2 red[2][32];
   __shared__ uint64_t full[4];
   __shared__ int abort_flag;
-  const int64_t n = p.N;
+  const int n = int(p.N), vectors = (n + E - 1) / E;
   const int tensors = p.R ? 3 : 2;
   const int stage_bytes = tensors * row_bytes;
   if (threadIdx.x == 0) {
@@ -265,12 +265,24 @@ __global__ void __launch_bounds__(512, VPT <= 2 ? 2 : 1)
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int j = 0; j < E; ++j) dw[i][j] = 0.f;
-  // vector v of a row in the ring, zeros beyond the row
+  // vector v of a row in the ring
   auto load = [&](const uint8_t* row, int v, float (&f)[E]) {
-    const bool in = int64_t(v) * E < n;
-    Vec<T>::unpack(in ? *(reinterpret_cast<const uint4*>(row) + v)
-                      : make_uint4(0, 0, 0, 0), f);
-    clear_tail<T>(v, n, f);
+    Vec<T>::unpack(*(reinterpret_cast<const uint4*>(row) + v), f);
+    if constexpr (TAIL) clear_tail<T>(v, n, f);
+  };
+  // the weights: packed in registers, or (FP32) read again
+  uint4 wr[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+    wr[i] = w32 ? make_uint4(0, 0, 0, 0)
+                : load_raw(static_cast<const T*>(p.W), threadIdx.x + i * blockDim.x, n);
+  auto weight = [&](int i, int v, float (&f)[E]) {
+    if (w32) {
+      load_weight<T>(p.W, true, v, n, f);
+    } else {
+      Vec<T>::unpack(wr[i], f);
+      if constexpr (TAIL) clear_tail<T>(v, n, f);
+    }
   };
   int s = 0, flip = 0;
   uint32_t phase = 0;
@@ -286,10 +298,11 @@ __global__ void __launch_bounds__(512, VPT <= 2 ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
+      if (v >= vectors) continue;
       float h[E], dy[E], w[E];
       load(hs, v, h);
       load(ds, v, dy);
-      load_weight<T>(p.W, w32, v, n, w);
+      weight(i, v, w);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         ss = fmaf(h[j], h[j], ss);
@@ -303,20 +316,20 @@ __global__ void __launch_bounds__(512, VPT <= 2 ? 2 : 1)
     if (threadIdx.x == 0 && row != blockIdx.x)
       fetch(row + int64_t(stages - 1) * gridDim.x, s == 0 ? stages - 1 : s - 1);
     const float rstd = __frsqrt_rn(sum.x * over_n + p.eps);
-    const float c = rstd * rstd * rstd * (sum.y * over_n);
+    const float c = -rstd * rstd * rstd * (sum.y * over_n);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      if (int64_t(v) * E >= n) continue;
+      if (v >= vectors) continue;
       float h[E], dy[E], w[E], o[E];
       load(hs, v, h);
       load(ds, v, dy);
-      load_weight<T>(p.W, w32, v, n, w);
+      weight(i, v, w);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const float d = dy[j] * rstd;
         dw[i][j] = fmaf(d, h[j], dw[i][j]);
-        o[j] = fmaf(d, w[j], -c * h[j]);
+        o[j] = fmaf(d, w[j], c * h[j]);
       }
       if (p.R) {
         float r[E];
@@ -324,7 +337,7 @@ __global__ void __launch_bounds__(512, VPT <= 2 ? 2 : 1)
 #pragma unroll
         for (int j = 0; j < E; ++j) o[j] += r[j];
       }
-      store_row(static_cast<T*>(p.DX) + row * p.lddx, v, n, o);
+      store_row<T, TAIL>(static_cast<T*>(p.DX) + row * p.lddx, v, n, o);
     }
     if (++s == stages) {
       s = 0;
@@ -397,7 +410,7 @@ __global__ void __launch_bounds__(1024)
   const int64_t col = int64_t(blockIdx.x) * 32 + threadIdx.x;
   float s = 0.f;
   if (col < n) {
-#pragma unroll 4
+#pragma unroll 16
     for (int g = threadIdx.y; g < parts; g += 32) s += part[g * n + col];
   }
   t[threadIdx.y][threadIdx.x] = s;
@@ -483,9 +496,14 @@ mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32,
       return true;
     };
     static PerContext<bool> a1, a2, a4;
-    const bool ok = vpt == 1   ? run(rmsnorm_backward_kernel<T, 1>, a1)
-                    : vpt == 2 ? run(rmsnorm_backward_kernel<T, 2>, a2)
-                               : run(rmsnorm_backward_kernel<T, 4>, a4);
+    static PerContext<bool> t1, t2, t4;
+    const bool ok =
+        p.N % E ? vpt == 1   ? run(rmsnorm_backward_kernel<T, 1, true>, t1)
+                  : vpt == 2 ? run(rmsnorm_backward_kernel<T, 2, true>, t2)
+                             : run(rmsnorm_backward_kernel<T, 4, true>, t4)
+        : vpt == 1 ? run(rmsnorm_backward_kernel<T, 1, false>, a1)
+        : vpt == 2 ? run(rmsnorm_backward_kernel<T, 2, false>, a2)
+                   : run(rmsnorm_backward_kernel<T, 4, false>, a4);
     if (!ok) return MMA_ERR_LAUNCH;
   } else if (grid > 0) {
     rmsnorm_backward_wide_kernel<T><<<grid, 1024, 0, ctx.stream>>>(p, w32, part);
