@@ -138,6 +138,11 @@ struct Layout {
   static constexpr uint32_t TMEM_COLS = ACCS * BN;
 };
 
+// Maps of boxes of 1, 2, 4 and 8 rows (the weight gradient's zeros).
+struct ZeroMaps {
+  CUtensorMap rows[4];
+};
+
 // One tile of work.
 struct Tile {
   int e;       // group
@@ -212,22 +217,6 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity,
   }
 }
 
-// A group that ends inside a stage's k rows: its last MMA step of 16 holds
-// `n` rows of the next group from row `row` on, which become zeros in both
-// operands (in one alone, an infinity in the other would leave NaN).  The
-// stage holds boxes of 64 k rows of 128 bytes: two of P, QR / 64 of Q.
-template <int QR>
-__device__ __forceinline__ void zero_rows(uint8_t* stage, int row, int n, int lane) {
-  const int per_box = n * 8;
-  for (int i = lane; i < (kP + QR) / 64 * per_box; i += 32) {
-    const int box = i / per_box, r = i - box * per_box;
-    *reinterpret_cast<uint4*>(stage + box * 8192 + row * 128 + r * 16) =
-        make_uint4(0, 0, 0, 0);
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
-}
-
 // KIND8: 8-bit operands with scales, else 16-bit.  P_MN, Q_MN: the operand
 // is stored with its row index contiguous (16-bit only).  RAGK: the groups
 // cut the k range (the weight gradient).  ROWS: D[p][q], the groups cut P.
@@ -238,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP,
                         const __grid_constant__ CUtensorMap tmQ,
                         const __grid_constant__ CUtensorMap tmD,
+                        const __grid_constant__ ZeroMaps tmZ,
                         const __grid_constant__ GroupedArgs a) {
   using L = Layout<KIND8, ROWS, SPLIT, CL, BN, STAGES>;
   constexpr int KE = KIND8 ? 128 : 64;  // k elements per stage
@@ -290,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&cut_in[s], 1);
-      mbar_init(&cut_ok[s], CL);
+      mbar_init(&cut_ok[s], 1);
     }
     for (int s = 0; s < L::SLOTS; ++s) {
       mbar_init(&sfull[s], 32);
@@ -465,9 +455,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
           uint8_t* sp = smem + stage * L::STAGE_BYTES;
           uint8_t* sq = sp + L::P_BYTES;
           // A pair's loads complete on the leader's barrier.  Those of a
-          // block that a group ends in (cut) complete on a barrier of each
-          // CTA's own, where its rows beyond the group are cleared.
-          const bool cut = RAGK && t.k1 - k < KE;
+          // block that a group ends in, inside a step of 16 (cut), complete
+          // on a barrier of each CTA's own, where rows are cleared first.
+          const bool cut = RAGK && t.k1 - k < KE && ((t.k1 - k) & 15);
           [[maybe_unused]] uint32_t bar = full_lead + uint32_t(stage) * 8u;
           if (cut) {
             if (rank == 0) mbar_arrive(&full[stage]);
@@ -585,9 +575,11 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
             if constexpr (RAGK) {
               if (ok && left < KE) {
                 steps = (left + 15) >> 4;
-                ok = mbar_wait_cluster(&cut_ok[stage], (cut_phase >> stage) & 1u,
-                                       abort_flag, a.status);
-                cut_phase ^= 1u << stage;
+                if (left & 15) {
+                  ok = mbar_wait(&cut_ok[stage], (cut_phase >> stage) & 1u, abort_flag,
+                                 a.status);
+                  cut_phase ^= 1u << stage;
+                }
               }
             }
             if (!ok) break;
@@ -640,32 +632,52 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     __syncwarp();
   } else if (RAGK && warp == 2) {
     // ------------------------------------------------ cut blocks
-    // Clears the rows beyond the group in this CTA's part of a stage and
-    // tells the leader, which issues the MMAs that read it.
+    // A group that ends inside a step of 16: the step's other rows are the
+    // next group's and become zeros in both operands (in one alone, an
+    // infinity in the other would leave NaN).  The zeros are TMA loads of
+    // rows beyond a tensor's end (8, 4, 2 or 1 rows of a 64-wide box), issued
+    // when the block has landed; both CTAs' complete on the leader's barrier.
+    // (Zeros written by the warps had to be released to the other CTA, which
+    // took some 1200 clocks per tile: 32 groups of 500 tokens 317 us, of 512
+    // tokens 276.)
     int stage = 0;
     uint32_t cut_phase = 0;  // one bit per stage
+    bool ok = true;
+    const uint32_t cut_lead = mapa_shared(smem_u32(&cut_ok[0]), CL > 1 ? 0 : cluster_ctarank());
     for (int u = first_unit; u < units; u += unit_step) {
       const Tile t = decode(u);
       const int blocks = (t.k1 - t.k0 + KE - 1) / KE;
       const int left = (t.k1 - t.k0) - (blocks - 1) * KE;
-      if (blocks > 0 && left < KE) {
+      if (blocks > 0 && left < KE && (left & 15)) {
+        constexpr int kBoxes = (kP + BN / CL) / 64;
         const int s = (stage + blocks - 1) % STAGES;
-        const bool ok =
-            mbar_wait(&cut_in[s], (cut_phase >> s) & 1u, abort_flag, a.status);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        const int n = 16 - (left & 15);  // rows to clear
+        ok = mbar_wait(&cut_in[s], (cut_phase >> s) & 1u, abort_flag, a.status);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         cut_phase ^= 1u << s;
-        zero_rows<BN / CL>(smem + s * L::STAGE_BYTES, left,
-                           ((left + 15) >> 4) * 16 - left, lane);
-        if (lane == 0) {
-          if constexpr (CL == 1)
-            mbar_arrive(&cut_ok[s]);
+        if (rank == 0 && lane == 0)
+          mbar_arrive_expect_tx(&cut_ok[s], uint32_t(CL * kBoxes * n * 128));
+        __syncwarp();
+        // lane: which power of two of n, which box
+        const int e = lane / kBoxes;
+        if (e < 4 && ((n >> e) & 1)) {
+          const int row = left + (n & ((1 << e) - 1));
+          uint8_t* dst = smem + s * L::STAGE_BYTES + lane % kBoxes * 8192 + row * 128;
+          if constexpr (CL > 1)
+            tma_load_3d_pair(&tmZ.rows[e], cut_lead + uint32_t(s) * 8u, dst, 0,
+                             a.rows_total, 0);
           else
-            mbar_arrive_cluster(mapa_shared(smem_u32(&cut_ok[s]), 0));
+            tma_load_3d(&tmZ.rows[e], &cut_ok[s], dst, 0, a.rows_total, 0);
         }
         __syncwarp();
       }
       stage = (stage + blocks) % STAGES;
     }
+    // after an abort, let the zeros in flight land
+    if (rank == 0 && lane == 0 && *abort_flag)
+      for (int s = 0; s < STAGES; ++s)
+        wait_drain(&cut_ok[s], ~(cut_phase >> s) & 1u, a.status);
+    __syncwarp();
   } else if (KIND8 && warp == 3) {
     // ------------------------------------------------ scales
     // Those of each chunk (one k block) by cp.async into a ring, zero beyond
@@ -1079,12 +1091,13 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
 
 // ----------------------------------------------------------------- host
 
-// A 3-D map over 1- or 2-byte elements with 128-byte swizzle: `inner`
+// A 3-D map over 1- or 2-byte elements, 128-byte swizzle: `inner`
 // contiguous elements, `outer` rows `ld` elements apart, `count` slices
 // `slice` elements apart; box box_inner x box_outer x 1.
 bool make_map(CUtensorMap* map, const void* base, int elem, int64_t inner,
               int64_t outer, int64_t ld, int64_t count, int64_t slice,
-              int box_inner, int box_outer) {
+              int box_inner, int box_outer,
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {cuuint64_t(inner), cuuint64_t(outer), cuuint64_t(count)};
@@ -1096,7 +1109,7 @@ bool make_map(CUtensorMap* map, const void* base, int elem, int64_t inner,
              elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                        : CU_TENSOR_MAP_DATA_TYPE_UINT16,
              3, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1140,10 +1153,18 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
               : make_map(m, o.p, EB, args.k_size, o.rows, o.ld, o.slices, slice, KE, box);
   };
   CUtensorMap tp, tq, td;
+  ZeroMaps tz;
   if (!map_of(&tp, P, P_MN, args.p_size, kP) || !map_of(&tq, Q, Q_MN, args.q_size, BN / CL / L::HV))
     return MMA_ERR_LAUNCH;
   GroupedArgs a = args;
   td = tp;
+  for (int e = 0; e < 4; ++e) {
+    tz.rows[e] = tp;  // (read beyond their end only)
+    if (RAGK && args.k_size > 0 &&
+        !make_map(&tz.rows[e], P.p, EB, args.p_size, P.rows, P.ld, 1, P.ld, 64, 1 << e,
+                  CU_TENSOR_MAP_SWIZZLE_NONE))
+      return MMA_ERR_LAUNCH;
+  }
   if constexpr (ROWS) {
     // D by TMA: without C, 16-byte rows, and a width that is a multiple of
     // 16 bytes (a box clipped inside a 16-byte chunk writes the chunk whole)
@@ -1216,7 +1237,7 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
   cfg.numAttrs = 2;
   cfg.gridDim = dim3(unsigned(clusters * CL * split), 1, 1);
   ctx.mark_start();
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tp, tq, td, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tp, tq, td, tz, a);
   ctx.mark_stop();
   if (e != cudaSuccess) cudaGetLastError();
   return e == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
