@@ -398,9 +398,13 @@ mma_status_t mma_gemm_i8_noalloc(int64_t M, int64_t N, int64_t K,
  * >= 0, the scales are 4-byte aligned.  s_row = 1 (the scales of one k block
  * for all rows side by side) is the order that is read fastest.
  *
- * Unlike the calls above, these ask of their outputs (and of C) no more than
- * the alignment of one element; inputs keep the rule of 16-byte rows, except
- * that scales and offsets need 4 bytes.
+ * Unlike the calls above, the products ask of their outputs (and of C) no
+ * more than the alignment of one element; inputs keep the rule of 16-byte
+ * rows, except that scales and offsets need 4 bytes.  Rows, columns and k of
+ * a product are at most 2^31 - 1025 (more: MMA_ERR_UNSUPPORTED).  None of
+ * these calls allocates memory or waits for the device; all can be captured
+ * in a graph.  The products start while the kernel before them on the stream
+ * ends and wait for it before they touch memory (programmatic launch).
  */
 
 /*
@@ -512,7 +516,8 @@ mma_status_t mma_gemm_f8(int type_a, int type_b, int type_d, int64_t M,
  *            or row-major (K x N stored; the input gradient of the
  *            column-major product with N and K exchanged).
  * C        : T x N or NULL; may be D with the same leading dimension.
- * Sums are FP32 (chunks of 256 from the tensor core, added to nearest).
+ * Sums are FP32 (chunks of 256 terms from the tensor core, 512 for a 16-bit
+ * result, added to nearest).
  */
 #define MMA_MAX_GROUPS 1024
 mma_status_t mma_gemm_grouped(int type_in, int type_d, int64_t groups,

@@ -1141,7 +1141,11 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
   const int64_t most = RAGK   ? args.groups * q_tiles * p_tiles
                        : ROWS ? tiles_of(args.rows_total, PT) * q_tiles
                               : tiles_of(args.rows_total, BN) * p_tiles;
-  if (most > int64_t(INT32_MAX) / 2) return MMA_ERR_UNSUPPORTED;
+  // rows and k are ints on the device, a tile past the end included
+  constexpr int kMost = INT32_MAX - 1024;
+  if (most > int64_t(INT32_MAX) / 2 || args.p_size > kMost || args.q_size > kMost ||
+      args.k_size > kMost || args.rows_total > kMost)
+    return MMA_ERR_UNSUPPORTED;
   auto map_of = [&](CUtensorMap* m, const Operand& o, bool mn, int64_t len, int box) {
     // no k at all (D = C): the kernel loads nothing but wants a valid map
     if (args.k_size == 0)

@@ -138,6 +138,52 @@ def test_f8_scale_strides_and_in_place(m):
     run_f8(m, 641, 1280, d="f32", c=True, inplace=True)
 
 
+@pytest.mark.parametrize("m,n,k", [(300, 520, 1000), (1300, 264, 512), (257, 1032, 130)])
+@pytest.mark.parametrize("d", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,c", [(128, False), (128, True), (1, False)])
+def test_f8_aligned_results(m, n, k, d, rows, c):
+    """Results whose rows start on 16-byte boundaries take the wide stores."""
+    a, sa = f8_operand(1, m, k, "e4m3", 1)
+    b, sb = f8_operand(3, n, k, "e4m3", rows)
+    C = rnd(5, m, n + 8).to(T[d])[:, :n] if c else None
+    g = Guard(m, n, T[d], pad=8)
+    mma.gemm_f8(a, sa, b, sb, C, g.view)
+    av, bv = value(a, sa, 1), value(b, sb, rows)
+    add = C.double() if c else 0
+    close(g.view, av @ bv.t() + add, av.abs() @ bv.abs().t() + (add.abs() if c else 0), k, "aligned")
+    g.check()
+
+
+def test_chained_calls_wait_for_each_other():
+    """Calls start before the ones before them have ended: a chain without
+    synchronisation has the bits of one with."""
+    k = 1024
+    w = [mma.quantize_f8(rnd(20 + i, k, k) / k ** 0.5, block_rows=128) for i in range(3)]
+    e = rnd(30, 3, k, k).to(torch.bfloat16) / 32
+
+    def chain(rows, sync):
+        at = off([0, rows // 3, rows // 3, rows])
+        x, out = rnd(31, rows, k).to(torch.bfloat16), []
+        for i in range(12):
+            q, s = mma.quantize_f8(x)
+            y = mma.gemm_f8(q, s, *w[i % 3])
+            sync()
+            z = mma.gemm_grouped(y, e, at)
+            sync()
+            z = mma.gemm_grouped(z, e, at, b_layout="row", D=y)   # over its own input's input
+            sync()
+            out.append(mma.gemm_grouped_wgrad(z, y, at, out_dtype=torch.bfloat16))
+            sync()
+            x = (z / z.float().abs().mean()).to(torch.bfloat16)
+        return x, out
+
+    for rows in (5, 40, 700):
+        want, want_w = chain(rows, torch.cuda.synchronize)
+        got, got_w = chain(rows, lambda: None)
+        assert bool((got == want).all())
+        assert all(bool((a == b).all()) for a, b in zip(got_w, want_w))
+
+
 def test_f8_many_tiles():
     run_f8(2300, 2200, 512)
     run_f8(2300, 2200, 640, rows=1, d="f32")

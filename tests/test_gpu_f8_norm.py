@@ -214,6 +214,28 @@ def test_norm_backward_against_differences():
         assert abs((loss(h, w + d) - loss(h, w - d)) / 2e-4 - float(dw[j])) < 1e-4
 
 
+@pytest.mark.parametrize("n", [200, 1000, 16400])
+def test_norm_backward_in_place(n):
+    """dX over dY, and over the residual path's gradient, rows of one stride."""
+    m = 700
+    dy, h, r = (rows16(rnd(50 + i, m, n), torch.bfloat16) for i in range(3))
+    w = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    want, want_w = mma.rmsnorm_backward(dy, h, w, r)
+    need = binding.load().mma_rmsnorm_backward_workspace(m, n)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for which in ("dy", "r"):
+        a = {"dy": rows16(dy.double().cpu(), torch.bfloat16),
+             "r": rows16(r.double().cpu(), torch.bfloat16)}
+        dw = torch.empty(n, device="cuda")
+        rc = binding.load().mma_rmsnorm_backward(
+            2, 2, m, n, a["dy"].data_ptr(), a["dy"].stride(0), h.data_ptr(), h.stride(0),
+            w.data_ptr(), 1e-6, a["r"].data_ptr(), a["r"].stride(0), a[which].data_ptr(),
+            a[which].stride(0), dw.data_ptr(), ws.data_ptr(), need, None)
+        torch.cuda.synchronize()
+        assert rc == 0
+        assert bool((a[which] == want).all()) and bool((dw == want_w).all())
+
+
 def test_norm_backward_without_rows():
     z = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
