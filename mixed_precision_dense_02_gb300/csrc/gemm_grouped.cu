@@ -204,6 +204,11 @@ __device__ __forceinline__ void store_d4(void* d, int64_t i, int t, float4 v) {
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(d) + i) = w;
 }
 
+// Row and column of sum s of a lane that holds pairs (PAIRS), counted from
+// its first of each.
+__device__ constexpr int pairs_row(int s) { return ((s >> 4) & 1) * 16 + ((s >> 1) & 1) * 8; }
+__device__ constexpr int pairs_q(int s) { return (s >> 5) * 32 + ((s >> 2) & 3) * 8 + (s & 1); }
+
 // Drain without giving up on the abort flag.
 __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity,
                                            unsigned* status) {
@@ -738,6 +743,11 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     const int ew = warp - 4;
     const int quarter = warp & 3;
     const int h = ew >> 2;
+    // PAIRS: a lane has two columns out of eight of four rows, so that
+    // it needs a quarter of the columns' scales: with all of them, as
+    // broadcasts out of shared memory, one row per lane took @BEFORE@.
+    constexpr bool PAIRS = KIND8 && !ROWS && BN == 256;
+    [[maybe_unused]] const int pair_q = h * HALF + 2 * (lane & 3);
     auto column = [&](int i) {
       return ROWS || HV == 2 ? h * HALF + i * CB : (2 * i + h) * CB;
     };
@@ -764,7 +774,24 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
       const int pw = t.p0 + rank * kP + quarter * 32;
       const int p = pw + lane;
       float sum[HALF];
-      if (!ROWS && a.C && krank == 0 && p < t.p1) {
+      if constexpr (PAIRS) {
+        // (as below)
+        const int left = t.q1 - t.q0 - pair_q;
+        const int64_t ci = int64_t(t.q0 + pair_q) * a.ldc + pw + (lane >> 2);
+        auto start = [&](auto read) {
+#pragma unroll
+          for (int s = 0; s < HALF; ++s) {
+            const int q = pairs_q(s), r = pairs_row(s);
+            sum[s] = a.C && q < left && pw + (lane >> 2) + r < t.p1
+                         ? read(ci + q * a.ldc + r)
+                         : 0.f;
+          }
+        };
+        if (a.d_type == MMA_F32)
+          start([&](int64_t i) { return static_cast<const float*>(a.C)[i]; });
+        else
+          start([&](int64_t i) { return load_c(a.C, i, a.d_type); });
+      } else if (!ROWS && a.C && krank == 0 && p < t.p1) {
         // The sums start from C, all of whose loads are under way at once
         // (and land while the first chunks are computed).
         const int64_t ci = (RAGK ? t.e * a.c_group : 0) + int64_t(t.q0) * a.ldc + p;
@@ -808,10 +835,14 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
           const bool in = BN == 256 || column(i) < t.nt;
           uint32_t r[CB];
           if (in) {
-            if constexpr (CB == 32)
+            if constexpr (PAIRS) {
+              tmem_ld_16x256b_x4(taddr + column(i), r);
+              tmem_ld_16x256b_x4(taddr + column(i) + (16u << 16), r + 16);
+            } else if constexpr (CB == 32) {
               tmem_ld_32x32b_x32(taddr + column(i), r);
-            else
+            } else {
               tmem_ld_32x32b_x16(taddr + column(i), r);
+            }
             tmem_ld_wait();
           }
           if (i + 1 == NB) {
@@ -838,10 +869,27 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
           const float* sc = ring + slot * L::SLOT_FLOATS;
 #pragma unroll 1
           for (int g = min(L::G, chunks - ch); g > 0; --g) {
-            const float sp = ROWS ? sc[quarter * 32 + lane] * sc[kP + h]
-                                  : sc[quarter * 32 + lane];
+            [[maybe_unused]] float sp, spr[4];
+            if constexpr (PAIRS) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) spr[x] = sc[quarter * 32 + (lane >> 2) + 8 * x];
+            } else {
+              sp = ROWS ? sc[quarter * 32 + lane] * sc[kP + h] : sc[quarter * 32 + lane];
+            }
             take([&](int i, const uint32_t (&r)[CB]) {
-              if constexpr (ROWS) {
+              if constexpr (PAIRS) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const float2 v =
+                      *reinterpret_cast<const float2*>(sc + kP + pair_q + i * 32 + x * 8);
+#pragma unroll
+                  for (int y = 0; y < 8; ++y) {
+                    const int j = (y >> 2) * 16 + x * 4 + (y & 3);
+                    sum[i * CB + j] = fmaf((j & 1 ? v.y : v.x) * spr[pairs_row(j) / 8],
+                                           __uint_as_float(r[j]), sum[i * CB + j]);
+                  }
+                }
+              } else if constexpr (ROWS) {
 #pragma unroll
                 for (int j = 0; j < CB; ++j)
                   sum[i * CB + j] = fmaf(sp, __uint_as_float(r[j]), sum[i * CB + j]);
@@ -1049,6 +1097,25 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
               }
             }
           }
+        }
+      } else if constexpr (PAIRS) {
+        // (each store instruction: 8 consecutive p of 4 rows of D)
+        const int left = t.q1 - t.q0 - pair_q;
+        const int rows = t.p1 - pw - (lane >> 2);
+        const int64_t di = int64_t(t.q0 + pair_q) * a.ldd + pw + (lane >> 2);
+        if (a.d_type == MMA_F32) {
+          float* d = static_cast<float*>(a.D) + di;
+#pragma unroll
+          for (int s = 0; s < HALF; ++s)
+            if (pairs_q(s) < left && pairs_row(s) < rows)
+              d[pairs_q(s) * a.ldd + pairs_row(s)] = sum[s];
+        } else {
+          uint16_t* d = static_cast<uint16_t*>(a.D) + di;
+          const bool bf16 = a.d_type == MMA_BF16;
+#pragma unroll
+          for (int s = 0; s < HALF; ++s)
+            if (pairs_q(s) < left && pairs_row(s) < rows)
+              d[pairs_q(s) * a.ldd + pairs_row(s)] = uint16_t(pack16(sum[s], 0.f, bf16));
         }
       } else {
         if (p >= t.p1) continue;

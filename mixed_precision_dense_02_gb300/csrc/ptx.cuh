@@ -494,6 +494,22 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr,
       : "r"(taddr));
 }
 
+// Load 32 consecutive columns of 16 tensor-memory lanes (a half of the warp's
+// 32): a lane holds columns 8 i + 2 (lane % 4) and the next in r[4 i],
+// r[4 i + 1] for row lane / 4, and in r[4 i + 2], r[4 i + 3] for row
+// lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(taddr));
+}
+
 // As above, 16 consecutive columns.
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr,
                                                    uint32_t (&r)[16]) {
