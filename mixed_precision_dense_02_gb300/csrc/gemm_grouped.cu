@@ -104,8 +104,10 @@ struct Layout {
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
   // 8-bit: a ring of the chunks' scales, G chunks per slot; a chunk's are
   // 128 of P, then those of Q (ROWS: of the two halves of the columns)
-  static constexpr int G = 4;
-  static constexpr int SLOTS = !KIND8 ? 0 : BN <= 64 ? 2 : 3;
+  // (an epilogue warp's change of slots takes some 300 clocks: with four
+  // chunks per slot 8192 x 8192 x 4096 took @G4@ us, with eight @G8@)
+  static constexpr int G = BN <= 64 ? 4 : 8;
+  static constexpr int SLOTS = KIND8 ? 2 : 0;
   static constexpr int CHUNK_FLOATS = kP + (ROWS ? 4 : BN);
   static constexpr int SLOT_FLOATS = G * CHUNK_FLOATS;
   static constexpr int SCALE_OFFSET = STAGES * STAGE_BYTES;
@@ -755,8 +757,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
         reinterpret_cast<float*>(smem + L::WARP_OFFSET + ew * L::WARP_BYTES);
     [[maybe_unused]] const float* ring =
         reinterpret_cast<const float*>(smem + L::SCALE_OFFSET);
-    [[maybe_unused]] int slot = 0;
-    [[maybe_unused]] uint32_t slot_phase = 0;
+    [[maybe_unused]] uint32_t fills = 0;  // slots taken so far
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
@@ -852,10 +853,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
           }
           if (in) add(i, r);
         }
-        if (++acc == L::ACCS) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
+        acc = (acc + 1) % L::ACCS;
+        acc_phase ^= acc == 0;
       };
       if constexpr (!KIND8) {
         for (int ch = 0; ch < chunks; ++ch)
@@ -864,11 +863,13 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
             for (int j = 0; j < CB; ++j) sum[i * CB + j] += __uint_as_float(r[j]);
           });
       } else {
-        for (int ch = 0; ch < chunks; ch += L::G) {
-          mbar_wait_lean(&sfull[slot], slot_phase, abort_flag, a.status);
-          const float* sc = ring + slot * L::SLOT_FLOATS;
+        static_assert(L::SLOTS == 2);
 #pragma unroll 1
-          for (int g = min(L::G, chunks - ch); g > 0; --g) {
+        for (int left = chunks; left > 0; left -= L::G, ++fills) {
+          mbar_wait_lean(&sfull[fills & 1], (fills >> 1) & 1, abort_flag, a.status);
+          const float* sc = ring + (fills & 1) * L::SLOT_FLOATS;
+#pragma unroll 1
+          for (int g = min(L::G, left); g > 0; --g) {
             [[maybe_unused]] float sp, spr[4];
             if constexpr (PAIRS) {
 #pragma unroll
@@ -909,11 +910,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
             sc += L::CHUNK_FLOATS;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sempty[slot]);
-          if (++slot == L::SLOTS) {
-            slot = 0;
-            slot_phase ^= 1u;
-          }
+          mbar_arrive_if(&sempty[fills & 1], lane == 0);
         }
       }
       ok = !__any_sync(0xffffffffu, *abort_flag != 0);

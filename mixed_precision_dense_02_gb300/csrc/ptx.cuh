@@ -102,6 +102,16 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
                : "memory");
 }
 
+// mbar_arrive by the lanes that have `doit`, without a branch.
+__device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool doit) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(uint32_t(doit))
+      : "memory");
+}
+
 // mbar_arrive_remote by the lanes that have `doit`, without a branch.
 __device__ __forceinline__ void mbar_arrive_remote_if(uint32_t cluster_addr,
                                                       bool doit) {
@@ -246,8 +256,11 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
 __device__ __forceinline__ void mbar_wait_lean(uint64_t* bar, uint32_t parity,
                                                volatile int* abort_flag,
                                                unsigned* status) {
-  mbar_wait(bar, parity, abort_flag, status);
-  __syncwarp();
+  if (__builtin_expect(
+          !__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity)), 0)) {
+    mbar_wait(bar, parity, abort_flag, status);
+    __syncwarp();
+  }
 }
 
 // Change this warpgroup's registers per thread (every warp of it executes
