@@ -104,8 +104,8 @@ struct Layout {
   static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
   // 8-bit: a ring of the chunks' scales, G chunks per slot; a chunk's are
   // 128 of P, then those of Q (ROWS: of the two halves of the columns)
-  // (an epilogue warp's change of slots takes some 300 clocks: with four
-  // chunks per slot 8192 x 8192 x 4096 took @G4@ us, with eight @G8@)
+  // (a change of slots costs an epilogue warp some 300 clocks: 8192 x 8192 x
+  // 4096 with two chunks per slot 247 us, with four 228, with eight 220)
   static constexpr int G = BN <= 64 ? 4 : 8;
   static constexpr int SLOTS = KIND8 ? 2 : 0;
   static constexpr int CHUNK_FLOATS = kP + (ROWS ? 4 : BN);
@@ -745,9 +745,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     const int ew = warp - 4;
     const int quarter = warp & 3;
     const int h = ew >> 2;
-    // PAIRS: a lane has two columns out of eight of four rows, so that
-    // it needs a quarter of the columns' scales: with all of them, as
-    // broadcasts out of shared memory, one row per lane took @BEFORE@.
+    // PAIRS: a lane has two columns out of eight of four rows, so that it
+    // needs a quarter of the columns' scales, and in pairs (2048 x 4096 x 8200
+    // with C: one row per lane and all scales as broadcasts out of shared
+    // memory 127 us, pairs 104, with packed arithmetic 96).
     constexpr bool PAIRS = KIND8 && !ROWS && BN == 256;
     [[maybe_unused]] const int pair_q = h * HALF + 2 * (lane & 3);
     auto column = [&](int i) {
@@ -819,10 +820,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
       const int chunks = (num_kb + a.kb_per_chunk - 1) / a.kb_per_chunk;
       // Wait for a chunk's sums in tensor memory, add them (through `add`,
       // for each block of columns) and return the accumulator as soon as its
-      // last block is in registers.  Scalar additions and one block in
-      // flight: packed pairs of FP32 and a second block cost registers that
-      // the sums need (four blocks of 32 columns by eight warps: 344 clocks,
-      // packed 728, of which reading tensor memory is 170).  Of a tile of 256
+      // last block is in registers.  Scalar additions (but for PAIRS) and one
+      // block in flight: packed ones and a second block spill sums (8192 x
+      // 8192 x 4096 with square scales 209 us, packed 235, 16 columns at a time
+      // with the next ones on their way 235).  Of a tile of 256
       // columns all are added, those beyond nt to sums that are not stored:
       // asking cost more (8-bit with row scales 139 us, without 119).
       auto take = [&](auto&& add) {
@@ -884,10 +885,16 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
                   const float2 v =
                       *reinterpret_cast<const float2*>(sc + kP + pair_q + i * 32 + x * 8);
 #pragma unroll
-                  for (int y = 0; y < 8; ++y) {
+                  for (int y = 0; y < 8; y += 2) {
                     const int j = (y >> 2) * 16 + x * 4 + (y & 3);
-                    sum[i * CB + j] = fmaf((j & 1 ? v.y : v.x) * spr[pairs_row(j) / 8],
-                                           __uint_as_float(r[j]), sum[i * CB + j]);
+                    const float sp1 = spr[pairs_row(j) / 8];
+                    float* const s = sum + i * CB + j;
+                    const float2 d = __ffma2_rn(
+                        __fmul2_rn(v, make_float2(sp1, sp1)),
+                        make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                        make_float2(s[0], s[1]));
+                    s[0] = d.x;
+                    s[1] = d.y;
                   }
                 }
               } else if constexpr (ROWS) {
