@@ -39,6 +39,22 @@
 // Few tiles (a token or a few through one matrix): a cluster of up to six
 // CTAs shares a tile's k range (SPLIT); the sums meet in the shared memory of
 // its first CTA, which adds them in order of rank.
+//
+// Measured, operands rotating through more than L2, and what bounds it:
+//   8-bit 8192 x 8192 x 4096, square scales, BF16 D: 210 us, 2610 TFLOP/s.
+//     The additions: a chunk's loads of tensor memory and FMAs keep an
+//     epilogue warp some 830 clocks, its MMAs take 530.
+//   8-bit 2048 x 4096 x 8200, row scales, FP32 C and D: 99 us, 1384 TFLOP/s.
+//     The same with a multiplication more per element, and 128 tiles are two
+//     waves of 76 pairs, the second two thirds full.
+//   32 experts of 4096 x 2048, 16384 tokens, BF16: forward 186 us, input
+//     gradient 188, 1480 TFLOP/s.  The tensor pipe at a power-capped clock,
+//     and tiles that a group does not fill.
+//   The same weight gradient in FP32: 310 us.  Writes of D: 1.07 GB, which
+//     take 186 us when there is nothing to add up.
+//   64 experts of 2048 x 4096, 96 tokens, 8-bit: 63 us, 5.9 TB/s.  HBM.
+//   One token, 8192 x 4096, 8-bit: 10.2 us, 3.3 TB/s.  Some 2 us each for the
+//     first loads' latency and for the join of a cluster's sums.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -969,7 +985,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
         if (a.d_tma && pw + 32 <= t.p1) {
           // Blocks of 64 bytes of the warp's rows leave by TMA, which has the
           // whole next tile's time to move them (stored by the warps they
-          // held up the MMAs: 257 us, nothing stored 224).
+          // held up the MMAs: 8192 x 8192 x 4096 257 us, so 228).
           const bool wide = a.d_type == MMA_F32, bf16 = a.d_type == MMA_BF16;
           auto send = [&](int c, const uint4 (&w)[4], int cols) {
             const int q = t.q0 + h * HALF + c * cols;
@@ -1323,10 +1339,13 @@ bool elements_aligned(const void* p, int64_t ld, int bytes, int n) {
   return (reinterpret_cast<uintptr_t>(p) & uintptr_t(n * bytes - 1)) == 0 && ld % n == 0;
 }
 
-// Up to 128 rows per group (`per`), column-major B: tiles of 32, 64 or 128
-// columns.  With fewer of them than SMs a cluster shares each one's k range;
-// else one CTA per SM with a deep ring streams them (64 experts of 2048 x
-// 4096 with 96 tokens: 62 us, two CTAs per SM with half the ring 66).
+// Few rows per group (`per`), column-major B: tiles of 32, 64 or 128 columns.
+// With fewer of them than SMs a cluster shares each one's k range; else one
+// CTA per SM with a deep ring streams them (64 experts of 2048 x 4096 with 96
+// tokens: 62 us, two CTAs per SM with half the ring 66).  8192 x 4096 8-bit,
+// 32 rows: 32 columns 10.4 us, 64 11.0, 128 11.3; 64 rows: 64 columns 12.5 us,
+// 128 12.7; 128 rows: 128 columns 16.0 us, pairs with 256 17.9.  32 experts of
+// 4096 x 2048 by 64 rows, 16-bit, streamed: 64 columns 94.7 us, 128 87.9.
 template <bool KIND8>
 mma_status_t few_rows(const Ctx& ctx, const Operand& B, const Operand& A,
                       const GroupedArgs& a, int64_t per) {
@@ -1336,7 +1355,8 @@ mma_status_t few_rows(const Ctx& ctx, const Operand& B, const Operand& A,
   if (per <= 32)
     return split ? run<KIND8, false, false, false, false, true, 1, 32, 4>(ctx, B, A, a)
                  : run<KIND8, false, false, false, false, false, 1, 32, 8>(ctx, B, A, a);
-  if (per <= 64) return run<KIND8, false, false, false, false, true, 1, 64, 4>(ctx, B, A, a);
+  if (per <= 64 && split)
+    return run<KIND8, false, false, false, false, true, 1, 64, 4>(ctx, B, A, a);
   return split ? run<KIND8, false, false, false, false, true, 1, 128, 4>(ctx, B, A, a)
                : run<KIND8, false, false, false, false, false, 1, 128, 6>(ctx, B, A, a);
 }
@@ -1360,9 +1380,19 @@ mma_status_t launch_gemm_f8(const Ctx& ctx, const F8Problem& f) {
   const Operand B = {f.B, f.ldb, f.N, f.groups, f.stride_b};
   const int shift = f.sb_rows == 128 ? 7 : 0;
   const int64_t per = (f.rows + f.groups - 1) / f.groups;
+  // Few tiles, on single CTAs of 128 x 128: those that one wave takes if B has
+  // a scale for each row (512 x 4096 x 4096: 19.6 us, on pairs 28.8; 512 x 8192
+  // x 4096, two waves: 35.7, on pairs 29.7), and with square scales, where
+  // pairs take half the time, if two CTAs can share each one's long k range
+  // (512 x 1024 x 16384: 38 us, on pairs 53; 1024 x 1024 x 4096: 16.1 and
+  // 16.7; 512 x 1024 x 1024: 8.8 and 7.3; 512 x 4096 x 4096: 20.5 and 17.2).
+  const int64_t tiles = (f.N + kP - 1) / kP *
+                        (f.offsets ? f.rows / kP + f.groups : (f.rows + kP - 1) / kP);
+  const bool few = per <= 128 || (shift == 7 ? 2 * tiles <= ctx.num_sms && f.K >= 4096
+                                             : tiles <= ctx.num_sms);
   // Many rows: a lane per row of A.  That needs one scale of B for the
   // columns of a lane's half tile; a tile holds 256 rows of one group.
-  if (shift == 7 && per > 128) {
+  if (shift == 7 && !few) {
     const int db = f.d_type == MMA_F32 ? 4 : 2;
     a.p_size = int(f.rows);
     a.q_size = int(f.N);
@@ -1390,7 +1420,7 @@ mma_status_t launch_gemm_f8(const Ctx& ctx, const F8Problem& f) {
   a.sq = f.SA;
   a.sq_row = f.sa_row;
   a.sq_blk = f.sa_blk;
-  if (per > 128) {
+  if (!few) {
     a.idesc = idesc_f32(f.b_e5m2, f.a_e5m2, false, false, 2 * kP);
     return run<true, false, false, false, false, false, 2, 256, 6>(ctx, B, A, a);
   }
@@ -1417,6 +1447,8 @@ mma_status_t launch_gemm_grouped(const Ctx& ctx, const GroupedProblem& g) {
   const int64_t per = (g.rows + g.groups - 1) / g.groups;
   const Operand A = {g.A, g.lda, g.rows, 1, 0};
   const Operand B = {g.B, g.ldb, g.b_row_major ? g.K : g.N, g.groups, g.stride_b};
+  // (32 experts of 4096 x 2048: by 128 rows 92 us, on pairs 95; by 160 rows
+  // 120 us, on pairs 97; with row-major B 88 and 91, 119 and 93)
   const bool pair = per > 128;
   a.idesc = idesc_f32(g.bf16, g.bf16, g.b_row_major, false, pair ? 2 * kP : kP);
   if (g.b_row_major) {

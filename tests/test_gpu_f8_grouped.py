@@ -189,6 +189,22 @@ def test_f8_many_tiles():
     run_f8(2300, 2200, 640, rows=1, d="f32")
 
 
+@pytest.mark.parametrize("m,n,k", [(3001, 901, 300), (130, 20000, 136), (5000, 520, 129),
+                                   (20500, 1, 260), (257, 10240, 16)])
+@pytest.mark.parametrize("d,c", [("bf16", True), ("f16", False), ("f32", True), ("f32", False)])
+def test_f8_row_scales_many_tiles(m, n, k, d, c):
+    """More 128 x 128 tiles than SMs: pairs of CTAs."""
+    run_f8(m, n, k, rows=1, d=d, c=c)
+    run_f8(m, n, k, rows=1, d=d, c=True, inplace=True, order="row")
+
+
+@pytest.mark.parametrize("m,n", [(300, 520), (129, 1), (700, 1000)])
+@pytest.mark.parametrize("rows", [1, 128])
+def test_f8_few_tiles_long_reduction(m, n, rows):
+    run_f8(m, n, 4200, rows=rows, c=True)
+    run_f8(m, n, 4096, rows=rows, d="f32")
+
+
 def test_f8_empty_reduction():
     a, sa = torch.empty(7, 0, device="cuda").to(F8["e4m3"]), torch.empty(7, 0, device="cuda")
     b, sb = torch.empty(300, 0, device="cuda").to(F8["e4m3"]), torch.empty(3, 0, device="cuda")
@@ -430,6 +446,27 @@ def test_grouped_f8_shapes(tokens, e):
     bv, av = torch.stack([value(q, s, 128) for q, s in ops]), value(a, sa, 1)
     out = mma.gemm_grouped_f8(a, sa, b, sb, off(at), out_dtype=torch.float32)
     close(out, grouped64(av, bv, at, False), grouped64(av.abs(), bv.abs(), at, False), k, "f8")
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+def test_grouped_f8_many_rows(rows):
+    at = [3, 3, 700, 1213, 1214, 2900]
+    tokens, n, k, e = 3000, 1301, 400, 5
+    a, sa = f8_operand(1, tokens, k, "e4m3", 1)
+    ops = [f8_operand(10 + 2 * i, n, k, "e4m3", rows) for i in range(e)]
+    b = rows16(torch.stack([q.view(torch.uint8) for q, _ in ops]).view(F8["e4m3"]))
+    sb = torch.stack([s for _, s in ops])
+    bv, av = torch.stack([value(q, s, rows) for q, s in ops]), value(a, sa, 1)
+    c = rnd(9, tokens, n).to(torch.bfloat16)
+    g = Guard(tokens, n, torch.bfloat16)
+    g.view.fill_(55.0)
+    mma.gemm_grouped_f8(a, sa, b, sb, off(at), c, g.view)
+    want = grouped64(av, bv, at, False) + c.double()
+    mag = grouped64(av.abs(), bv.abs(), at, False) + c.double().abs()
+    lo, hi = at[0], at[-1]
+    close(g.view[lo:hi], want[lo:hi], mag[lo:hi], k, "f8")
+    assert bool((g.view[:lo] == 55).all()) and bool((g.view[hi:] == 55).all())
+    g.check()
 
 
 def test_repeatable_other_stream_and_graph():
