@@ -17,7 +17,7 @@
 // Both are bound by memory: each input is read once and each output written
 // once, a row is held on chip between its two uses.  BF16, 8192 x 8192:
 // forward 79 us, 5.95 TB/s; one row of 4096 2.7 us, all latency.  Backward,
-// 8190 x 5000 BF16: 65 us, 5.0 TB/s, some 6 us of them for the shares of dw
+// 8190 x 5000 BF16: 63 us, 5.2 TB/s, some 6 us of them for the shares of dw
 // (456 rows written, read and added up by a second kernel).
 #include <algorithm>
 #include <type_traits>
@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(512, VPT <= 2 ? 2 : 1)
     }
     flip ^= 1;
   }
+  grid_dependents_start();
   float* mine = part + int64_t(blockIdx.x) * n;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -405,16 +406,25 @@ __global__ void __launch_bounds__(1024)
 }
 
 // out[n] = sum of part[g][n] over g: 32 columns per block, 32 rows of
-// threads that each add up every 32nd part.
+// threads that each add up every 32nd part, two loads at once (more got in
+// each other's way: backward pass of 8190 x 5000 62.7 us, four 63.7, sixteen
+// 69.9).  Starts beside the end of the kernel that makes the parts.
 __global__ void __launch_bounds__(1024)
     sum_parts_kernel(const float* __restrict__ part, int parts, int64_t n,
                      float* __restrict__ out) {
   __shared__ float t[32][33];
   const int64_t col = int64_t(blockIdx.x) * 32 + threadIdx.x;
   float s = 0.f;
-  if (col < n) {
-#pragma unroll 16
-    for (int g = threadIdx.y; g < parts; g += 32) s += part[g * n + col];
+  grid_dependency_wait();
+  for (int from = threadIdx.y; from < parts; from += 2 * 32) {
+    float v[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int g = from + i * 32;
+      v[i] = g < parts && col < n ? part[g * n + col] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) s += v[i];
   }
   t[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
@@ -511,9 +521,20 @@ mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32,
   } else if (grid > 0) {
     rmsnorm_backward_wide_kernel<T><<<grid, 1024, 0, ctx.stream>>>(p, w32, part);
   }
-  sum_parts_kernel<<<unsigned((p.N + 31) / 32), dim3(32, 32), 0, ctx.stream>>>(
-      part, grid, p.N, p.DW);
-  return cudaGetLastError() == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((p.N + 31) / 32), 1, 1);
+  cfg.blockDim = dim3(32, 32, 1);
+  cfg.stream = ctx.stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, sum_parts_kernel, static_cast<const float*>(part), grid,
+                         p.N, p.DW);
+  const cudaError_t last = cudaGetLastError();
+  return e == cudaSuccess && last == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
 }
 
 }  // namespace
