@@ -413,6 +413,9 @@ mma_status_t mma_gemm_i8_noalloc(int64_t M, int64_t N, int64_t K,
  *     h = x + r,   y = h * w / sqrt(mean(h^2) + eps)     (FP32 throughout)
  *     s = max(max |y| over 128 columns / 448, 2^-126),   q = y / s  (E4M3)
  *
+ * The quotient is formed in FP32, then in 8 bits, each to nearest, ties to
+ * even.
+ *
  * type   : MMA_F16, MMA_BF16 or MMA_F32, of X, R, H and Y.
  * w_type : of W (N elements): `type` or MMA_F32.
  * R      : M x N residual, or NULL (then h = x).
@@ -460,7 +463,7 @@ mma_status_t mma_rmsnorm_backward(int type, int w_type, int64_t M, int64_t N,
  * of type f8_type with scales:
  *
  *     s = max(max |x| over the block / format's largest value, 2^-126)
- *     q = x / s, to nearest
+ *     q = x / s, in FP32 and then in 8 bits, each to nearest, ties to even
  *
  * block_rows : 1 or 128 (the blocks are block_rows x 128).
  * transpose  : nonzero -- Q is N x M, the transpose; its blocks of 128 run

@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "kernels.h"
@@ -139,17 +140,40 @@ __device__ __forceinline__ float abs_max(float a, float b) {
   return r;
 }
 
+// The largest of three.
+__device__ __forceinline__ float abs_max(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 template <bool E5M2>
 constexpr float f8_max() { return E5M2 ? 57344.f : 448.f; }
 
-// The scale of a block whose largest magnitude has the bits `m`: that over
-// the format's largest value, at least 2^-126 (so that a block of zeros, or
-// of values whose quotient underflows, has a scale that can be divided by).
-// With pow2 it is rounded up to a power of two.  A NaN or infinity in the
-// block makes the scale one.
+// m over the format's largest value (7 times a power of two), rounded to
+// nearest: with a reciprocal of two terms, r - hi < 2^-22 r and lo the rest to
+// 24 bits, the sum is 2^-45 off, and no quotient by 7 is nearer than 1/14 of
+// its last place to the middle between two numbers.  Small m are multiplied by
+// 2^64, so that m lo is a normal number.
 template <bool E5M2>
-__device__ __forceinline__ float block_scale(uint32_t m, bool pow2) {
-  float s = __fdiv_rn(__uint_as_float(m), f8_max<E5M2>());
+__device__ __forceinline__ float over_f8_max(float m) {
+  constexpr double r = 1.0 / (E5M2 ? 57344.0 : 448.0);
+  constexpr float hi = float(r * (1.0 - 0x1p-23)), lo = float(r - double(hi));
+  static_assert(lo > 0.f);
+  const bool small = m < 0x1p-64f;
+  const float x = small ? m * 0x1p64f : m;
+  const float s = fmaf(x, hi, x * lo);
+  return small ? s * 0x1p-64f : s;
+}
+
+// The scale of a block whose largest magnitude is `m`: that over the format's
+// largest value, at least 2^-126 (so that a block of zeros, or of values whose
+// quotient underflows, has a scale that can be divided by).  With pow2 it is
+// rounded up to a power of two.  A NaN or infinity in the block makes the scale
+// one.
+template <bool E5M2>
+__device__ __forceinline__ float block_scale(float m, bool pow2) {
+  float s = over_f8_max<E5M2>(m);
   if (s < 1.17549435e-38f) s = 1.17549435e-38f;
   if (pow2) {
     uint32_t b = __float_as_uint(s);
@@ -159,23 +183,53 @@ __device__ __forceinline__ float block_scale(uint32_t m, bool pow2) {
   return s;
 }
 
-// Two values, already divided by their scale, in 8 bits (to nearest, ties
-// to even; beyond the largest value that value; NaN stays NaN).
+// Division by a block's scale s.  x times 1 / s rounds twice, and x / s often
+// lies half-way between two 8-bit values, where the second rounding decides.
+// So the reciprocal has two terms, hi a little below 1 / s and lo = hi (1 - hi
+// s), short of 1 / s - hi by 2^-42 of it, and x / s is fma(x, hi, x lo): an
+// exact tie stays one, and any other quotient is that of FP32 but for the last
+// place of one in some 10^6 (s above 2^100, where lo is subnormal: one in some
+// 10^4).  lo > 0, so that zeros keep their sign.  s infinite: finite x give 0,
+// infinite ones NaN.
+struct Divisor {
+  float hi, lo;
+  Divisor() = default;
+  __device__ __forceinline__ explicit Divisor(float s) {
+    float r;  // within 2^-23 of 1 / s
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    hi = r * (1.f - 0x1p-22f);
+    lo = s < INFINITY ? fmaf(-hi, s, 1.f) * hi : 0.f;
+  }
+  // that of another lane of the warp
+  __device__ __forceinline__ Divisor from(int lane) const {
+    Divisor d;
+    d.hi = __shfl_sync(0xffffffffu, hi, lane);
+    d.lo = __shfl_sync(0xffffffffu, lo, lane);
+    return d;
+  }
+  __device__ __forceinline__ float2 operator()(float a, float b) const {
+    const float2 x = make_float2(a, b);
+    return __ffma2_rn(x, make_float2(hi, hi), __fmul2_rn(x, make_float2(lo, lo)));
+  }
+};
+
+// Two values over their scale, in 8 bits (to nearest, ties to even; beyond
+// the largest value that value; NaN stays NaN).
 template <bool E5M2>
-__device__ __forceinline__ uint32_t to_f8x2(float lo, float hi) {
-  return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE,
+__device__ __forceinline__ uint32_t to_f8x2(const Divisor& d, float lo, float hi) {
+  return uint32_t(__nv_cvt_float2_to_fp8x2(d(lo, hi), __NV_SATFINITE,
                                            E5M2 ? __NV_E5M2 : __NV_E4M3));
 }
 
-// Store E values of vector v of a row in 8 bits, times inv.
+// Store E values of vector v of a row in 8 bits, over their scale.
 template <bool E5M2, int E, bool TAIL = true>
 __device__ __forceinline__ void store_f8(uint8_t* row, int64_t v, int64_t n,
-                                         const float (&y)[E], float inv) {
+                                         const float (&y)[E], const Divisor& d) {
   uint32_t w[E / 4];
 #pragma unroll
   for (int i = 0; i < E / 4; ++i)
-    w[i] = to_f8x2<E5M2>(y[4 * i] * inv, y[4 * i + 1] * inv) |
-           (to_f8x2<E5M2>(y[4 * i + 2] * inv, y[4 * i + 3] * inv) << 16);
+    w[i] = to_f8x2<E5M2>(d, y[4 * i], y[4 * i + 1]) |
+           (to_f8x2<E5M2>(d, y[4 * i + 2], y[4 * i + 3]) << 16);
   if (!TAIL || (v + 1) * E <= n) {
     if constexpr (E == 8)
       *reinterpret_cast<uint2*>(row + v * 8) = make_uint2(w[0], w[1]);

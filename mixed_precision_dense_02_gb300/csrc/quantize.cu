@@ -2,9 +2,7 @@
 // block of 128 values of a row, or of 128 x 128 values, as it is or
 // transposed:
 //     s_b = max(max|x| over block b / format's largest value, 2^-126)
-//     q = x / s_b, rounded to nearest
-// (q is x times the reciprocal of s_b, one rounding more than the quotient;
-// the same when s_b is a power of two).
+//     q = x / s_b, the FP32 quotient rounded to nearest
 //
 // The transposed form serves products that reduce over what is the row index
 // here: the weight's transpose for an input gradient, an activation's or
@@ -29,10 +27,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // gemm_tc.cu
 namespace {
 
 // Blocks of 1 x 128, not transposed: a group of lanes per block of columns,
-// four rows at a time.  The divisions that make a scale and its reciprocal
-// are done for the four rows at once, each by another lane of the group (for
-// every lane by itself they were a third of all instructions: 16384 x 2048
-// BF16 took 37 us).
+// four rows at a time.  The scales and their reciprocals are made for the four
+// rows at once, each by another lane of the group (by every lane for itself:
+// 16384 x 2048 BF16 20.5 us, so 19.6).
 constexpr int kRowsAtOnce = 4;
 
 template <class T, bool E5M2, bool TAIL>
@@ -56,23 +53,23 @@ __global__ void __launch_bounds__(256)
     for (int i = 0; i < kRowsAtOnce; ++i) {
       m[i] = 0.f;
 #pragma unroll
-      for (int j = 0; j < E; ++j) m[i] = abs_max(m[i], x[i][j]);
+      for (int j = 0; j < E; j += 2) m[i] = abs_max(m[i], x[i][j], x[i][j + 1]);
 #pragma unroll
       for (int d = kLanes / 2; d > 0; d >>= 1)
         m[i] = abs_max(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
     }
     const int mine = lane & (kRowsAtOnce - 1);
     const float mm = mine & 2 ? (mine & 1 ? m[3] : m[2]) : (mine & 1 ? m[1] : m[0]);
-    const float s = block_scale<E5M2>(abs_bits(mm), p.pow2);
-    const float inv = __fdiv_rn(1.f, s);
+    const float s = block_scale<E5M2>(mm, p.pow2);
+    const Divisor by(s);
     if (b * kScaleBlock < p.N && lane % kLanes < kRowsAtOnce && row0 + mine < p.M)
       p.S[(row0 + mine) * p.s_row + b * p.s_blk] = s;
 #pragma unroll
     for (int i = 0; i < kRowsAtOnce; ++i) {
-      const float f = __shfl_sync(0xffffffffu, inv, (lane & ~(kLanes - 1)) + i);
+      const Divisor d = by.from((lane & ~(kLanes - 1)) + i);
       if (live && row0 + i < p.M)
         store_f8<E5M2, E, TAIL>(static_cast<uint8_t*>(p.Q) + (row0 + i) * p.ldq, v,
-                                p.N, x[i], f);
+                                p.N, x[i], d);
     }
   }
 }
@@ -111,7 +108,7 @@ __global__ void __launch_bounds__(Tile<T>::THREADS, Tile<T>::PER_SM)
       (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   uint8_t* turned = smem + L::STAGES * L::BYTES;
   __shared__ float red[SQUARE ? 2 * WARPS : TR * kScaleBlock];
-  __shared__ float inv_of[SQUARE ? 1 : kScaleBlock];
+  __shared__ float scale_of[SQUARE ? 1 : kScaleBlock];
   __shared__ uint64_t full[L::STAGES];
   __shared__ int abort_flag;
   if (threadIdx.x == 0) {
@@ -143,21 +140,21 @@ __global__ void __launch_bounds__(Tile<T>::THREADS, Tile<T>::PER_SM)
     const uint4* src = reinterpret_cast<const uint4*>(smem + s * L::BYTES);
 #pragma unroll
     for (int i = 0; i < RPT; ++i) Vec<T>::unpack(src[(tr * RPT + i) * VEC + c], x[i]);
-    float inv[SQUARE ? 1 : E];
+    float scale[SQUARE ? 1 : E];
     if constexpr (SQUARE) {
       float m = 0.f;
 #pragma unroll
       for (int i = 0; i < RPT; ++i)
 #pragma unroll
-        for (int j = 0; j < E; ++j) m = abs_max(m, x[i][j]);
+        for (int j = 0; j < E; j += 2) m = abs_max(m, x[i][j], x[i][j + 1]);
       const uint32_t w = __reduce_max_sync(0xffffffffu, abs_bits(m));
       if ((threadIdx.x & 31) == 0) red[flip * WARPS + (threadIdx.x >> 5)] = __uint_as_float(w);
       __syncthreads();
       m = 0.f;
 #pragma unroll
       for (int k = 0; k < WARPS; ++k) m = abs_max(m, red[flip * WARPS + k]);
-      const float sc = block_scale<E5M2>(abs_bits(m), p.pow2);
-      inv[0] = __fdiv_rn(1.f, sc);
+      const float sc = block_scale<E5M2>(m, p.pow2);
+      scale[0] = sc;
       if (threadIdx.x == 0)
         p.S[(TRANS ? tn : tm) * p.s_row + (TRANS ? tm : tn) * p.s_blk] = sc;
     } else {
@@ -165,7 +162,7 @@ __global__ void __launch_bounds__(Tile<T>::THREADS, Tile<T>::PER_SM)
       for (int j = 0; j < E; ++j) {
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < RPT; ++i) m = abs_max(m, x[i][j]);
+        for (int i = 0; i < RPT; i += 2) m = abs_max(m, x[i][j], x[i + 1][j]);
         red[tr * kScaleBlock + j * VEC + c] = m;  // j-major: no conflicts
       }
       __syncthreads();
@@ -174,8 +171,8 @@ __global__ void __launch_bounds__(Tile<T>::THREADS, Tile<T>::PER_SM)
         float m = 0.f;
 #pragma unroll
         for (int k = 0; k < TR; ++k) m = abs_max(m, red[k * kScaleBlock + threadIdx.x]);
-        const float sc = block_scale<E5M2>(abs_bits(m), p.pow2);
-        inv_of[threadIdx.x] = __fdiv_rn(1.f, sc);
+        const float sc = block_scale<E5M2>(m, p.pow2);
+        scale_of[threadIdx.x] = sc;
         if (n0 + col < p.N) p.S[(n0 + col) * p.s_row + tm * p.s_blk] = sc;
       }
     }
@@ -188,27 +185,28 @@ __global__ void __launch_bounds__(Tile<T>::THREADS, Tile<T>::PER_SM)
     if constexpr (!SQUARE) {
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < E; ++j) inv[j] = inv_of[j * VEC + c];
+      for (int j = 0; j < E; ++j) scale[j] = scale_of[j * VEC + c];
     }
     if constexpr (!TRANS) {
       const int64_t v = n0 / E + c;
+      const Divisor d(scale[0]);
       if (v * E < p.N)
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
           const int64_t row = m0 + tr * RPT + i;
           if (row < p.M)
             store_f8<E5M2>(static_cast<uint8_t*>(p.Q) + row * p.ldq, v, p.N, x[i],
-                           inv[0]);
+                           d);
         }
     } else {
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        const float f = inv[SQUARE ? 0 : j];
+        const Divisor d(scale[SQUARE ? 0 : j]);
         uint32_t w[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          w[i] = to_f8x2<E5M2>(x[4 * i][j] * f, x[4 * i + 1][j] * f) |
-                 (to_f8x2<E5M2>(x[4 * i + 2][j] * f, x[4 * i + 3][j] * f) << 16);
+          w[i] = to_f8x2<E5M2>(d, x[4 * i][j], x[4 * i + 1][j]) |
+                 (to_f8x2<E5M2>(d, x[4 * i + 2][j], x[4 * i + 3][j]) << 16);
         *reinterpret_cast<uint2*>(turned + (c * E + j) * kScaleBlock +
                                   ((tr ^ (c & 15)) << 3)) = make_uint2(w[0], w[1]);
       }

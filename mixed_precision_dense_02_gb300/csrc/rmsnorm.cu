@@ -6,8 +6,7 @@
 //     y = h * w / sqrt(mean(h^2) + eps)
 //     s_b = max(max|y| over block b / 448, 2^-126),  q = y / s_b in E4M3
 // h leaves rounded to the input's type; y is formed from the unrounded sum.
-// q is y times the reciprocal of s_b, one rounding more than the quotient;
-// with s_b a power of two the two are the same.
+// q is the FP32 quotient y / s_b, rounded to nearest.
 //
 // Backward, with g = dy * w and the rounded h that the forward stored:
 //     dx = g / rms - h * mean(g h) / rms^3 + dr,   dw = sum over rows dy h / rms
@@ -16,7 +15,7 @@
 //
 // Both are bound by memory: each input is read once and each output written
 // once, a row is held on chip between its two uses.  BF16, 8192 x 8192:
-// forward 79 us, 5.95 TB/s; one row of 4096 2.7 us, all latency.  Backward,
+// forward 77 us, 6.1 TB/s; one row of 4096 2.7 us, all latency.  Backward,
 // 8190 x 5000 BF16: 63 us, 5.2 TB/s, some 6 us of them for the shares of dw
 // (456 rows written, read and added up by a second kernel).
 #include <algorithm>
@@ -126,11 +125,13 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1)
       load_weight<T>(p.W, w32, v, n, w);
       m[i] = 0.f;
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        h[i][j] = h[i][j] * rstd * w[j];
+      for (int j = 0; j < E; j += 2) {
+        float2 y = __fmul2_rn(make_float2(h[i][j], h[i][j + 1]), make_float2(rstd, rstd));
+        y = __fmul2_rn(y, make_float2(w[j], w[j + 1]));
         // columns past the end (rstd may be infinite or NaN) do not count
-        if (TAIL && v * E + j >= n) h[i][j] = 0.f;
-        m[i] = abs_max(m[i], h[i][j]);
+        h[i][j] = TAIL && v * E + j >= n ? 0.f : y.x;
+        h[i][j + 1] = TAIL && v * E + j + 1 >= n ? 0.f : y.y;
+        m[i] = abs_max(m[i], h[i][j], h[i][j + 1]);
       }
       if (!live) m[i] = 0.f;
       if (p.Y && live)
@@ -142,14 +143,14 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1)
 #pragma unroll
         for (int d = kLanes / 2; d > 0; d >>= 1)
           m[i] = abs_max(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
-      // the thread's VPT scales and reciprocals, each made by another lane of
-      // the block's group
+      // the thread's VPT scales and their reciprocals, each made by another
+      // lane of the block's group
       const int mine = threadIdx.x % kLanes % 4;
       float mm = m[0];
 #pragma unroll
       for (int i = 1; i < VPT; ++i) mm = mine == i ? m[i] : mm;
-      const float s = block_scale<false>(abs_bits(mm), p.pow2);
-      const float inv = __fdiv_rn(1.f, s);
+      const float s = block_scale<false>(mm, p.pow2);
+      const Divisor by(s);
       const int lane0 = threadIdx.x & 31 & ~(kLanes - 1);
       if (threadIdx.x % kLanes < VPT) {
         const int64_t b = (threadIdx.x + int64_t(mine) * blockDim.x) / kLanes;
@@ -158,10 +159,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1)
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int64_t v = threadIdx.x + i * blockDim.x;
-        const float f = __shfl_sync(0xffffffffu, inv, lane0 + i);
+        const Divisor d = by.from(lane0 + i);
         if (v * E < n)
           store_f8<false, E, TAIL>(static_cast<uint8_t*>(p.Q) + row * p.ldq, v, n,
-                                   h[i], f);
+                                   h[i], d);
       }
     }
   }
@@ -214,10 +215,10 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
     for (int d = kLanes / 2; d > 0; d >>= 1)
       m = abs_max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float s = block_scale<false>(abs_bits(m), p.pow2);
+    const float s = block_scale<false>(m, p.pow2);
     if (!live) continue;
     store_f8<false>(static_cast<uint8_t*>(p.Q) + row * p.ldq, v, n, y,
-                    __fdiv_rn(1.f, s));
+                    Divisor(s));
     if (threadIdx.x % kLanes == 0)
       p.S[row * p.s_row + (v * E / kScaleBlock) * p.s_blk] = s;
   }
