@@ -350,6 +350,9 @@ def gemm_batched(A, B, C=None, D=None, *, group: int = 1, abid: int = 0,
 # (types, shapes, strides, device) settle is worked out once per layout and
 # kept as a plan: the checks, the ABI's codes and leading dimensions, the
 # layouts of the results.  A plan holds no tensor and no address.
+#
+# With `stream` given a call runs as if that stream were the current one: its
+# results are that stream's tensors, and what it reads must be ready there.
 
 _KIND = {}
 _PLANS = {}
@@ -387,11 +390,23 @@ def _plan(key, make, *args):
     return plan
 
 
-def _raw_stream(stream, index):
-    """The cudaStream_t of `stream`, or of the device's current stream."""
-    if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(index)
-    return getattr(stream, "cuda_stream", stream)
+def _raw_stream(index):
+    """The cudaStream_t of the device's current stream."""
+    return _torch()._C._cuda_getCurrentRawStream(index)
+
+
+def _under(stream, index, call, *args, **kw):
+    """`call` with `stream` (a torch stream or a cudaStream_t) as the current
+    one.  Results and scratch memory are then allocated on it: a block of
+    another stream's may still be in use by that stream's earlier work, and
+    goes to its later work while the call runs."""
+    cuda = _torch().cuda
+    if not isinstance(stream, cuda.Stream):
+        handle = getattr(stream, "cuda_stream", stream)
+        stream = (cuda.ExternalStream(handle, device=index) if handle
+                  else cuda.default_stream(index))
+    with cuda.stream(stream):
+        return call(*args, **kw)
 
 
 def _take(name, t, kinds, *shape):
@@ -505,6 +520,8 @@ def rmsnorm_f8(X, W, residual=None, *, eps: float = 1e-6, pow2: bool = False,
     torch = _torch()
     (code, w_code, M, N, ldx, ldr, ldh, f8, ldq, blocks, index) = _plan(
         ("norm", _key(X), _key(W), _key(residual)), _plan_rmsnorm, X, W, residual)
+    if stream is not None:
+        return _under(stream, index, rmsnorm_f8, X, W, residual, eps=eps, pow2=pow2, y=y)
     dtype, device = X.dtype, X.device
     H, r_ptr, h_ptr = X, None, None
     if residual is not None:
@@ -518,7 +535,7 @@ def rmsnorm_f8(X, W, residual=None, *, eps: float = 1e-6, pow2: bool = False,
     st = load().mma_rmsnorm_f8(
         code, w_code, M, N, X.data_ptr(), ldx, r_ptr, ldr, W.data_ptr(), eps,
         1 if pow2 else 0, h_ptr, ldh, None if Y is None else Y.data_ptr(), ldh,
-        Q.data_ptr(), ldq, S.data_ptr(), 1, M, _raw_stream(stream, index))
+        Q.data_ptr(), ldq, S.data_ptr(), 1, M, _raw_stream(index))
     if st:
         _check("mma_rmsnorm_f8", st)
     return (Q, S, H, Y) if y else (Q, S, H)
@@ -549,15 +566,17 @@ def rmsnorm_backward(dY, H, W, dH=None, *, eps: float = 1e-6, stream=None):
     code, w_code, M, N, ldy, ldh, ldr, ldx, need, index = _plan(
         ("back", _key(dY), _key(H), _key(W), _key(dH)), _plan_rmsnorm_backward,
         dY, H, W, dH)
+    if stream is not None:
+        return _under(stream, index, rmsnorm_backward, dY, H, W, dH, eps=eps)
     device = H.device
     dX = torch.empty_strided((M, N), (ldx, 1), dtype=H.dtype, device=device)
     dW = torch.empty((N,), dtype=torch.float32, device=device)
-    # (its memory goes to other work of this stream only after the call's)
+    # (its memory goes to other work of the current stream only after the call's)
     ws = torch.empty((need,), dtype=torch.uint8, device=device)
     st = load().mma_rmsnorm_backward(
         code, w_code, M, N, dY.data_ptr(), ldy, H.data_ptr(), ldh, W.data_ptr(),
         eps, None if dH is None else dH.data_ptr(), ldr, dX.data_ptr(), ldx,
-        dW.data_ptr(), ws.data_ptr(), need, _raw_stream(stream, index))
+        dW.data_ptr(), ws.data_ptr(), need, _raw_stream(index))
     if st:
         _check("mma_rmsnorm_backward", st)
     return dX, dW
@@ -590,6 +609,9 @@ def quantize_f8(X, *, fmt: str = "e4m3", block_rows: int = 1,
     code, f8, f8_code, M, N, ldx, m, n, ldq, s_rows, blocks, index = _plan(
         ("quantize", _key(X), fmt, block_rows, transpose), _plan_quantize, X, fmt,
         block_rows, transpose)
+    if stream is not None:
+        return _under(stream, index, quantize_f8, X, fmt=fmt, block_rows=block_rows,
+                      transpose=transpose, pow2=pow2)
     device = X.device
     Q = torch.empty_strided((m, n), (ldq, 1), dtype=f8, device=device)
     # the scales of one block side by side
@@ -598,7 +620,7 @@ def quantize_f8(X, *, fmt: str = "e4m3", block_rows: int = 1,
     st = load().mma_quantize_f8(
         code, f8_code, M, N, block_rows, 1 if transpose else 0, 1 if pow2 else 0,
         X.data_ptr(), ldx, Q.data_ptr(), ldq, S.data_ptr(), 1, s_rows,
-        _raw_stream(stream, index))
+        _raw_stream(index))
     if st:
         _check("mma_quantize_f8", st)
     return Q, S
@@ -647,13 +669,15 @@ def gemm_f8(A, SA, B, SB, C=None, D=None, *, out_dtype=None, stream=None):
      sb_blk, ldc, ldd, dtype, index) = _plan(
         ("f8", _key(A), _key(SA), _key(B), _key(SB), _key(C), _key(D), out_dtype),
         _plan_gemm_f8, A, SA, B, SB, C, D, out_dtype)
+    if stream is not None:
+        return _under(stream, index, gemm_f8, A, SA, B, SB, C, D, out_dtype=out_dtype)
     if D is None:
         D = _torch().empty((M, N), dtype=dtype, device=A.device)
     st = load().mma_gemm_f8(
         a_code, b_code, d_code, M, N, K, A.data_ptr(), lda, SA.data_ptr(), sa_row,
         sa_blk, B.data_ptr(), ldb, SB.data_ptr(), sb_rows, sb_row, sb_blk,
         None if C is None else C.data_ptr(), ldc, D.data_ptr(), ldd,
-        _raw_stream(stream, index))
+        _raw_stream(index))
     if st:
         _check("mma_gemm_f8", st)
     return D
@@ -707,12 +731,15 @@ def gemm_grouped(A, B, offsets, C=None, D=None, *, b_layout: str = "col",
         ("grouped", _key(A), _key(B), _key(offsets), _key(C), _key(D), b_layout,
          out_dtype),
         _plan_grouped, A, B, offsets, C, D, b_layout, out_dtype)
+    if stream is not None:
+        return _under(stream, index, gemm_grouped, A, B, offsets, C, D, b_layout=b_layout,
+                      out_dtype=out_dtype)
     if D is None:
         D = _torch().empty((T, N), dtype=dtype, device=A.device)
     st = load().mma_gemm_grouped(
         code, d_code, groups, T, N, K, A.data_ptr(), lda, B.data_ptr(), ldb,
         stride_b, layout, offsets.data_ptr(), None if C is None else C.data_ptr(),
-        ldc, D.data_ptr(), ldd, _raw_stream(stream, index))
+        ldc, D.data_ptr(), ldd, _raw_stream(index))
     if st:
         _check("mma_gemm_grouped", st)
     return D
@@ -751,12 +778,15 @@ def gemm_grouped_wgrad(dY, X, offsets, C=None, D=None, *, out_dtype=None,
      index) = _plan(
         ("wgrad", _key(dY), _key(X), _key(offsets), _key(C), _key(D), out_dtype),
         _plan_wgrad, dY, X, offsets, C, D, out_dtype)
+    if stream is not None:
+        return _under(stream, index, gemm_grouped_wgrad, dY, X, offsets, C, D,
+                      out_dtype=out_dtype)
     if D is None:
         D = _torch().empty((groups, N, K), dtype=dtype, device=dY.device)
     st = load().mma_gemm_grouped_wgrad(
         code, d_code, groups, T, N, K, dY.data_ptr(), ldy, X.data_ptr(), ldx,
         offsets.data_ptr(), None if C is None else C.data_ptr(), ldc, stride_c,
-        D.data_ptr(), ldd, stride_d, _raw_stream(stream, index))
+        D.data_ptr(), ldd, stride_d, _raw_stream(index))
     if st:
         _check("mma_gemm_grouped_wgrad", st)
     return D
@@ -796,6 +826,9 @@ def gemm_grouped_f8(A, SA, B, SB, offsets, C=None, D=None, *, out_dtype=None,
         ("grouped_f8", _key(A), _key(SA), _key(B), _key(SB), _key(offsets), _key(C),
          _key(D), out_dtype),
         _plan_grouped_f8, A, SA, B, SB, offsets, C, D, out_dtype)
+    if stream is not None:
+        return _under(stream, index, gemm_grouped_f8, A, SA, B, SB, offsets, C, D,
+                      out_dtype=out_dtype)
     if D is None:
         D = _torch().empty((T, N), dtype=dtype, device=A.device)
     st = load().mma_gemm_grouped_f8(
@@ -803,7 +836,7 @@ def gemm_grouped_f8(A, SA, B, SB, offsets, C=None, D=None, *, out_dtype=None,
         sa_row, sa_blk, B.data_ptr(), ldb, stride_b, SB.data_ptr(), sb_rows,
         sb_group, sb_row, sb_blk, offsets.data_ptr(),
         None if C is None else C.data_ptr(), ldc, D.data_ptr(), ldd,
-        _raw_stream(stream, index))
+        _raw_stream(index))
     if st:
         _check("mma_gemm_grouped_f8", st)
     return D
