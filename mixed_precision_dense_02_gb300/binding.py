@@ -219,6 +219,29 @@ def _stream(stream):
     return getattr(stream, "cuda_stream", stream)
 
 
+def _under(stream, index, call, *args, **kw):
+    """`call` with `stream` (a torch stream or a cudaStream_t) as the current
+    one.  Results and scratch memory are then allocated on it: a block of
+    another stream's may still be in use by that stream's earlier work, and
+    goes to its later work while the call runs."""
+    cuda = _torch().cuda
+    if not isinstance(stream, cuda.Stream):
+        handle = getattr(stream, "cuda_stream", stream)
+        stream = (cuda.ExternalStream(handle, device=index) if handle
+                  else cuda.default_stream(index))
+    with cuda.stream(stream):
+        return call(*args, **kw)
+
+
+def _empty(shape, dtype, like, stream):
+    """A result beside `like`, allocated on the call's stream."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    return _under(stream, like.get_device(), torch.empty, shape, dtype=dtype,
+                  device=like.device)
+
+
 def gemm_ex(A, B, C=None, D=None, *, b_layout: str = "col", acc=None,
             stream=None):
     """D = A @ B + C on the GPU.
@@ -251,7 +274,7 @@ def gemm_ex(A, B, C=None, D=None, *, b_layout: str = "col", acc=None,
     if Kb != K:
         raise ValueError(f"K mismatch: {K} vs {Kb}")
     if D is None:
-        D = torch.empty((M, N), dtype=out_dtype, device=A.device)
+        D = _empty((M, N), out_dtype, A, stream)
     for t in (C, D):
         if t is not None and (t.dtype != out_dtype or tuple(t.shape) != (M, N)):
             raise ValueError("C/D must be (M, N) of the accumulator dtype")
@@ -289,7 +312,7 @@ def gemm_i8_ex(A, B, C=None, D=None, *, clamp: bool = False,
     if Kb != K:
         raise ValueError(f"K mismatch: {K} vs {Kb}")
     if D is None:
-        D = torch.empty((M, N), dtype=torch.int32, device=A.device)
+        D = _empty((M, N), torch.int32, A, stream)
     for t in (C, D):
         if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (M, N)):
             raise ValueError("C/D must be (M, N) int32")
@@ -332,7 +355,7 @@ def gemm_batched(A, B, C=None, D=None, *, group: int = 1, abid: int = 0,
         if t is not None and not t.is_contiguous():
             raise ValueError("batched operands must be contiguous")
     if D is None:
-        D = torch.empty((batch, M, N), dtype=out_dtype, device=A.device)
+        D = _empty((batch, M, N), out_dtype, A, stream)
     st = mma_gemm_batched_ex(dt_in, dt_acc, M, N, K, A.data_ptr(), K,
                              B.data_ptr(), K,
                              None if C is None else C.data_ptr(), N,
@@ -393,20 +416,6 @@ def _plan(key, make, *args):
 def _raw_stream(index):
     """The cudaStream_t of the device's current stream."""
     return _torch()._C._cuda_getCurrentRawStream(index)
-
-
-def _under(stream, index, call, *args, **kw):
-    """`call` with `stream` (a torch stream or a cudaStream_t) as the current
-    one.  Results and scratch memory are then allocated on it: a block of
-    another stream's may still be in use by that stream's earlier work, and
-    goes to its later work while the call runs."""
-    cuda = _torch().cuda
-    if not isinstance(stream, cuda.Stream):
-        handle = getattr(stream, "cuda_stream", stream)
-        stream = (cuda.ExternalStream(handle, device=index) if handle
-                  else cuda.default_stream(index))
-    with cuda.stream(stream):
-        return call(*args, **kw)
 
 
 def _take(name, t, kinds, *shape):

@@ -47,6 +47,8 @@ def calls():
     e8, se = zip(*(mma.quantize_f8(v, block_rows=128) for v in e))
     e8 = torch.stack([v.view(torch.uint8) for v in e8]).view(a.dtype)
     se, y = torch.stack(se), rnd(8, m, n)
+    i8 = torch.arange(m * k, device="cuda").remainder(255).sub(127).to(torch.int8).view(m, k)
+    xb = x[:512].reshape(8, 64, k).contiguous()
     return {
         "norm": lambda **s: mma.rmsnorm_f8(x, w, r, y=True, **s),
         "norm backward": lambda **s: mma.rmsnorm_backward(dy, h, w, r, **s),
@@ -55,6 +57,9 @@ def calls():
         "grouped": lambda **s: mma.gemm_grouped(x, e, at, **s),
         "grouped gradient": lambda **s: mma.gemm_grouped_wgrad(y, x, at, **s),
         "grouped f8": lambda **s: mma.gemm_grouped_f8(a, sa, e8, se, at, **s),
+        "gemm": lambda **s: mma.gemm(x, e[0], **s),
+        "gemm_i8_ex": lambda **s: mma.gemm_i8_ex(i8, i8[:n], **s),
+        "gemm_batched": lambda **s: mma.gemm_batched(xb, xb, **s),
     }
 
 
@@ -67,7 +72,8 @@ def same(got, want):
     return all(bool((g == w).all()) for g, w in zip(tensors(got), want))
 
 
-NAMES = ["norm", "norm backward", "quantise", "f8", "grouped", "grouped gradient", "grouped f8"]
+NAMES = ["norm", "norm backward", "quantise", "f8", "grouped", "grouped gradient", "grouped f8",
+         "gemm", "gemm_i8_ex", "gemm_batched"]
 
 
 @pytest.mark.parametrize("name", NAMES)
