@@ -384,16 +384,20 @@ _MOST_PLANS = 4096
 
 def _kinds():
     """Tensor types: their ABI codes, and the sets that arguments may have."""
+    global _KIND
     if not _KIND:
         torch = _torch()
-        _KIND["wide"] = {torch.float32: MMA_F32, torch.float16: MMA_F16,
-                         torch.bfloat16: MMA_BF16}
-        _KIND["half"] = {torch.float16: MMA_F16, torch.bfloat16: MMA_BF16}
-        _KIND["f8"] = {torch.float8_e4m3fn: MMA_F8E4M3,
-                       torch.float8_e5m2: MMA_F8E5M2}
-        _KIND["scale"] = {torch.float32: MMA_F32}
-        _KIND["offset"] = {torch.int32: MMA_I32}
-        _KIND["fmt"] = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+        # (put together aside: another thread sees all of it or nothing)
+        _KIND = {
+            "wide": {torch.float32: MMA_F32, torch.float16: MMA_F16,
+                     torch.bfloat16: MMA_BF16},
+            "half": {torch.float16: MMA_F16, torch.bfloat16: MMA_BF16},
+            "f8": {torch.float8_e4m3fn: MMA_F8E4M3,
+                   torch.float8_e5m2: MMA_F8E5M2},
+            "scale": {torch.float32: MMA_F32},
+            "offset": {torch.int32: MMA_I32},
+            "fmt": {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2},
+        }
     return _KIND
 
 

@@ -1,0 +1,32 @@
+"""The binding's host side, without a GPU."""
+from __future__ import annotations
+
+import threading
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from mixed_precision_dense_02_gb300 import binding
+
+
+def test_tensor_types_are_complete_for_every_thread(monkeypatch):
+    """A thread that asks for the types while another one is putting them
+    together gets all of them."""
+    seen = []
+
+    class Slow:
+        """torch, where looking up an 8-bit type lets another thread run."""
+
+        def __getattr__(self, name):
+            if name == "float8_e4m3fn" and threading.current_thread() is threading.main_thread():
+                t = threading.Thread(target=lambda: seen.append(set(binding._kinds())))
+                t.start()
+                t.join()
+            return getattr(torch, name)
+
+    monkeypatch.setattr(binding, "_KIND", {})
+    monkeypatch.setattr(binding, "_torch", Slow)
+    every = {"wide", "half", "f8", "scale", "offset", "fmt"}
+    assert set(binding._kinds()) == every
+    assert seen and all(s == every for s in seen)
