@@ -418,8 +418,13 @@ def _plan(key, make, *args):
 
 
 def _raw_stream(index):
-    """The cudaStream_t of the device's current stream."""
-    return _torch()._C._cuda_getCurrentRawStream(index)
+    """The cudaStream_t of the current stream of the tensors' device, which has
+    to be the current one: the library launches there."""
+    c = _torch()._C
+    if c._cuda_getDevice() != index:
+        raise ValueError(f"the tensors are on cuda:{index}, the current device is "
+                         f"cuda:{c._cuda_getDevice()}")
+    return c._cuda_getCurrentRawStream(index)
 
 
 def _take(name, t, kinds, *shape):

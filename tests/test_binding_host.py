@@ -30,3 +30,17 @@ def test_tensor_types_are_complete_for_every_thread(monkeypatch):
     every = {"wide", "half", "f8", "scale", "offset", "fmt"}
     assert set(binding._kinds()) == every
     assert seen and all(s == every for s in seen)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """The library launches on the current device; tensors of another one are
+    refused on every call, a plan kept from an earlier call or not."""
+    class Fake:
+        class _C:
+            _cuda_getDevice = staticmethod(lambda: 1)
+            _cuda_getCurrentRawStream = staticmethod(lambda index: 7)
+
+    monkeypatch.setattr(binding, "_torch", lambda: Fake)
+    assert binding._raw_stream(1) == 7
+    with pytest.raises(ValueError, match="cuda:0"):
+        binding._raw_stream(0)
