@@ -320,7 +320,8 @@ __global__ void __launch_bounds__(512, VPT <= 2 ? 2 : 1)
     if (threadIdx.x == 0 && row != blockIdx.x)
       fetch(row + int64_t(stages - 1) * gridDim.x, s == 0 ? stages - 1 : s - 1);
     const float rstd = __frsqrt_rn(sum.x * over_n + p.eps);
-    const float c = -rstd * rstd * rstd * (sum.y * over_n);
+    // (rstd^3 by itself leaves the range of FP32 at rms of 2^42 and 2^-42)
+    const float c = -(sum.y * over_n) * rstd * rstd * rstd;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(1024)
     }
     const float2 s = block_sum2(ss, gh, red[flip]);
     const float rstd = __frsqrt_rn(s.x / float(n) + p.eps);
-    const float c = rstd * rstd * rstd * (s.y / float(n));
+    const float c = s.y / float(n) * rstd * rstd * rstd;
     for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
       load(v);
       float o[E], r[E];
