@@ -20,7 +20,7 @@ SOURCES = ["api.cu", "gemm_tc.cu", "gemm_i8.cu", "gemm_f64.cu", "batched16.cu",
            "noalloc.cu", "selftest.cu", "batched_mma.cu",
            "batched_tile.cu", "gemm_sk.cu", "peaks.cu", "gemm_grouped.cu",
            "rmsnorm.cu", "quantize.cu"]
-HEADERS = ["ptx.cuh", "kernels.h", "f8_common.cuh"]
+HEADERS = ["ptx.cuh", "kernels.h", "f8_common.cuh", "norm_shape.h"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = GENCODE + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler",
                         "-fPIC", "-cudart", "shared", "--expt-relaxed-constexpr"]

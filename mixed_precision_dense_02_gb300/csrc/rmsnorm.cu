@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "f8_common.cuh"
+#include "norm_shape.h"
 #include "ptx.cuh"
 
 namespace mmagb {
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(1024)
   if (threadIdx.x == 0 && c < n) out[c] = s;
 }
 
-constexpr int kMostParts = 456;  // blocks of the backward pass, three per SM
+constexpr int kMostParts = 456;  // blocks of the backward pass, three per SM at most
 
 // Calls f(VPT, MAXT, threads) for rows of `vectors` vectors: up to 256
 // threads with up to 4 vectors each, so that several rows are under way per
@@ -487,16 +488,13 @@ template <class T>
 mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32,
                       float* part) {
   constexpr int E = Vec<T>::kN;
-  const int grid = int(std::min<int64_t>(p.M, std::min(kMostParts, 3 * ctx.num_sms)));
   const int64_t vectors = (p.N + E - 1) / E;
-  // Three blocks per SM (one of wide rows) and two to four rows ahead, as
-  // far as 220 KB allow.
-  const int vpt = vectors <= 512 ? 1 : vectors <= 1024 ? 2 : 4;
-  const int64_t stage = vectors * 16 * (p.R ? 3 : 2);
-  const int64_t room = (vpt <= 2 ? 73 : 220) * 1024;
-  const int stages = int(std::min<int64_t>(4, room / std::max<int64_t>(stage, 1)));
-  if (grid > 0 && vectors <= 2048 && stages >= 2) {
-    const int threads = int((vectors + vpt - 1) / vpt + 31) / 32 * 32;
+  const int tensors = p.R ? 3 : 2;
+  const NormBackShape shape = norm_back_shape(vectors, tensors);
+  const int vpt = shape.vpt;
+  const int at_once = (vpt ? shape.per_sm : 3) * ctx.num_sms;
+  const int grid = int(std::min<int64_t>(p.M, std::min(kMostParts, at_once)));
+  if (grid > 0 && vpt) {
     auto run = [&](auto kernel, PerContext<bool>& attr) {
       bool ok = false;
       if (!attr.get(ctx, &ok, [&](bool* v) {
@@ -506,8 +504,8 @@ mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32,
             return *v;
           }))
         return false;
-      kernel<<<grid, threads, size_t(stages) * stage, ctx.stream>>>(
-          p, w32, stages, int(vectors * 16), part, ctx.status);
+      kernel<<<grid, shape.threads, size_t(shape.stages) * tensors * vectors * 16,
+               ctx.stream>>>(p, w32, shape.stages, int(vectors * 16), part, ctx.status);
       return true;
     };
     static PerContext<bool> a1, a2, a4;
