@@ -299,6 +299,23 @@ mma_status_t mma_selftest_gemm_abort(int cluster, int64_t limit_ns,
                                      void *stream);
 
 /*
+ * mma_selftest_f8_abort -- the same for the kernels of the norm and quantiser
+ * that fetch ahead: kernel 0 is mma_quantize_f8 with blocks of 128 x 128 of a
+ * 1024 x 1024 BF16 X (Q: 1024 x 1024 E4M3, S: 64 floats), kernel 1 that of the
+ * transpose with blocks of 1 x 128 (S: 8192 floats), kernel 2
+ * mma_rmsnorm_backward of 1024 x 1024 BF16 (X as DY, H and W; Q: DX, 1024 x
+ * 1024 BF16; S: DW, 1024 floats; workspace: 456 * 1024 floats).  No loads are
+ * issued and waits end after limit_ns (10^6 .. 10^10 ns): every block stops at
+ * its first wait, drains and returns, Q is not written, nor S by kernels 0 and
+ * 1 (kernel 2 adds up the untouched workspace there).  Buffers are 16-byte
+ * aligned device memory of the caller; workspace is NULL for kernels 0 and 1.
+ * Returns as mma_selftest_gemm_abort.
+ */
+mma_status_t mma_selftest_f8_abort(int kernel, int64_t limit_ns, const void *X,
+                                   void *Q, float *S, void *workspace,
+                                   void *stream);
+
+/*
  * mma_peak_probe -- enqueue one issue-rate probe of a compute pipe on every
  * SM of the current device and report the operations it performs.
  *

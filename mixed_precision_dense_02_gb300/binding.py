@@ -66,6 +66,7 @@ SIGNATURES = {
     "mma_device_status": (_int, [_p]),
     "mma_selftest_wait_timeout": (_int, [_i64, _p]),
     "mma_selftest_gemm_abort": (_int, [_int, _i64, _p, _p, _p, _p]),
+    "mma_selftest_f8_abort": (_int, [_int, _i64, _p, _p, _p, _p, _p]),
     "mma_peak_probe": (_int, [_int, _i64, ctypes.POINTER(ctypes.c_double), _p]),
     "mma_profile_begin": (_int, []),
     "mma_profile_end": (_int, [ctypes.POINTER(ctypes.c_float), _int,
@@ -182,6 +183,13 @@ def mma_selftest_gemm_abort(cluster, limit_ns, A, B, D, stream) -> int:
     limit_ns, so its own abort path runs; mma_device_status then reports
     MMA_ERR_TIMEOUT once."""
     return load().mma_selftest_gemm_abort(cluster, limit_ns, A, B, D, stream)
+
+
+def mma_selftest_f8_abort(kernel, limit_ns, X, Q, S, workspace, stream) -> int:
+    """Run a tile quantiser (kernel 0, 1) or the norm's gradient (2) with no
+    loads and waits limited to limit_ns; mma_device_status then reports
+    MMA_ERR_TIMEOUT once."""
+    return load().mma_selftest_f8_abort(kernel, limit_ns, X, Q, S, workspace, stream)
 
 
 def mma_status_string(status: int) -> str:

@@ -227,19 +227,6 @@ __device__ __forceinline__ void store_d4(void* d, int64_t i, int t, float4 v) {
 __device__ constexpr int pairs_row(int s) { return ((s >> 4) & 1) * 16 + ((s >> 1) & 1) * 8; }
 __device__ constexpr int pairs_q(int s) { return (s >> 5) * 32 + ((s >> 2) & 3) * 8 + (s & 1); }
 
-// Drain without giving up on the abort flag.
-__device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity,
-                                           unsigned* status) {
-  const uint32_t a = smem_u32(bar);
-  const unsigned long long t0 = global_timer_ns();
-  while (!mbar_try_wait(a, parity)) {
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
-      atomicOr(status, kStatusTimeout);
-      return;
-    }
-  }
-}
-
 // KIND8: 8-bit operands with scales, else 16-bit.  P_MN, Q_MN: the operand
 // is stored with its row index contiguous (16-bit only).  RAGK: the groups
 // cut the k range (the weight gradient).  ROWS: D[p][q], the groups cut P.
@@ -525,11 +512,11 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
         const uint32_t fills = issued / STAGES + (uint32_t(s) < issued % STAGES);
         if (!fills) continue;
         // after an abort, let the loads in flight land before the CTA exits
-        if (!ok && rank == 0) wait_drain(&full[s], (fills - 1) & 1u, a.status);
-        if (!ok && RAGK) wait_drain(&cut_in[s], ~(cut_fills >> s) & 1u, a.status);
+        if (!ok && rank == 0) mbar_drain(&full[s], (fills - 1) & 1u, a.status);
+        if (!ok && RAGK) mbar_drain(&cut_in[s], ~(cut_fills >> s) & 1u, a.status);
         // with a pair, the last release of each stage is the leader's
         // commit; wait until it has arrived on this CTA
-        if (CL > 1) wait_drain(&empty[s], (fills - 1) & 1u, a.status);
+        if (CL > 1) mbar_drain(&empty[s], (fills - 1) & 1u, a.status);
       }
     }
     __syncwarp();
@@ -650,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
         umma_commit(done);
       else
         umma_commit_pair(done, 1u);
-      wait_drain(done, 0, a.status);
+      mbar_drain(done, 0, a.status);
     }
     __syncwarp();
   } else if (RAGK && warp == 2) {
@@ -699,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     // after an abort, let the zeros in flight land
     if (rank == 0 && lane == 0 && *abort_flag)
       for (int s = 0; s < STAGES; ++s)
-        wait_drain(&cut_ok[s], ~(cut_phase >> s) & 1u, a.status);
+        mbar_drain(&cut_ok[s], ~(cut_phase >> s) & 1u, a.status);
     __syncwarp();
   } else if (KIND8 && warp == 3) {
     // ------------------------------------------------ scales

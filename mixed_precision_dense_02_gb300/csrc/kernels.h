@@ -283,6 +283,14 @@ struct QuantProblem {
 };
 mma_status_t launch_quantize_f8(const Ctx& ctx, const QuantProblem& p);
 
+// Failure-detection self-tests of the quantiser's tile kernel and of the norm's
+// gradient: no loads are issued and waits are limited to limit_ns (sizes at
+// mma_selftest_f8_abort).
+mma_status_t launch_quantize_abort_selftest(const Ctx& ctx, int64_t limit_ns, int transpose,
+                                            const void* X, void* Q, float* S);
+mma_status_t launch_rmsnorm_abort_selftest(const Ctx& ctx, int64_t limit_ns, const void* X,
+                                           void* DX, float* DW, void* workspace);
+
 // Failure-detection self-test of the tcgen05 GEMM itself: a 256 x 256 x
 // 256 BF16 product on single CTAs (cluster 1) or a CTA pair (cluster 2)
 // whose producer issues no loads and whose bounded waits give up after

@@ -230,6 +230,30 @@ __device__ __forceinline__ bool mbar_wait(
   }
 }
 
+// Wait for what is in flight on `bar` whether or not a wait has failed: before
+// a CTA leaves after one, so that no copy lands in shared memory that is
+// another CTA's by then.  Bounded like the others.
+__device__ __forceinline__ void mbar_drain(
+    uint64_t* bar, uint32_t parity, unsigned* status,
+    unsigned long long limit_ns = kWaitLimitNs) {
+  const uint32_t a = smem_u32(bar);
+  const unsigned long long t0 = global_timer_ns();
+  while (!mbar_try_wait(a, parity)) {
+    if (global_timer_ns() - t0 > limit_ns) {
+      atomicOr(status, kStatusTimeout);
+      return;
+    }
+  }
+}
+
+// For the self-tests of failed waits (every call passes {kWaitLimitNs, 0}): the
+// limit of a kernel's waits; with `withhold` it issues no loads, so that its
+// first wait runs out.
+struct WaitHook {
+  unsigned long long limit_ns;
+  int withhold;
+};
+
 // The bounded wait of mbar_wait with mbar_try_wait_cluster.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
                                                   volatile int* abort_flag,

@@ -98,7 +98,7 @@ template <class T, bool E5M2, bool SQUARE, bool TRANS>
 __global__ void __launch_bounds__(Tile<T>::THREADS, Tile<T>::PER_SM)
     quantize_tile_kernel(const __grid_constant__ CUtensorMap map,
                          const QuantProblem p, int64_t tiles_n, int64_t tiles,
-                         unsigned* status) {
+                         unsigned* status, const WaitHook hook) {
   using L = Tile<T>;
   constexpr int E = L::E, VEC = L::VEC, RPT = L::RPT;
   constexpr int TR = kScaleBlock / RPT;  // rows of threads
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(Tile<T>::THREADS, Tile<T>::PER_SM)
   }
   __syncthreads();
   auto fetch = [&](int64_t t, int s) {
-    if (t >= tiles) return;
+    if (t >= tiles || hook.withhold) return;
     mbar_arrive_expect_tx(&full[s], L::BYTES);
     tma_load_3d(&map, &full[s], smem + s * L::BYTES,
                 int(t % tiles_n) * kScaleBlock, int(t / tiles_n) * kScaleBlock, 0);
@@ -133,9 +133,16 @@ __global__ void __launch_bounds__(Tile<T>::THREADS, Tile<T>::PER_SM)
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, flip ^= 1) {
     const int64_t tm = t / tiles_n, tn = t - tm * tiles_n;
     const int64_t m0 = tm * kScaleBlock, n0 = tn * kScaleBlock;
-    // (after a failed wait the rest runs on whatever is there; the status
-    // word tells)
-    mbar_wait(&full[s], phase, &abort_flag, status);
+    // A failed wait ends the block behind the next barrier, before anything is
+    // stored or fetched.
+    const bool failed = !mbar_wait(&full[s], phase, &abort_flag, status, hook.limit_ns);
+    // thread 0 lets this tile's and the next ones' loads land
+    auto drain = [&] {
+      if (threadIdx.x == 0)
+        for (int k = 0; k < L::STAGES && t + k * int64_t(gridDim.x) < tiles; ++k)
+          mbar_drain(&full[(s + k) % L::STAGES], phase ^ uint32_t(s + k >= L::STAGES), status,
+                     hook.limit_ns);
+    };
     float x[RPT][E];
     const uint4* src = reinterpret_cast<const uint4*>(smem + s * L::BYTES);
 #pragma unroll
@@ -149,7 +156,7 @@ __global__ void __launch_bounds__(Tile<T>::THREADS, Tile<T>::PER_SM)
         for (int j = 0; j < E; j += 2) m = abs_max(m, x[i][j], x[i][j + 1]);
       const uint32_t w = __reduce_max_sync(0xffffffffu, abs_bits(m));
       if ((threadIdx.x & 31) == 0) red[flip * WARPS + (threadIdx.x >> 5)] = __uint_as_float(w);
-      __syncthreads();
+      if (__syncthreads_or(failed)) return drain();
       m = 0.f;
 #pragma unroll
       for (int k = 0; k < WARPS; ++k) m = abs_max(m, red[flip * WARPS + k]);
@@ -165,7 +172,7 @@ __global__ void __launch_bounds__(Tile<T>::THREADS, Tile<T>::PER_SM)
         for (int i = 0; i < RPT; i += 2) m = abs_max(m, x[i][j], x[i + 1][j]);
         red[tr * kScaleBlock + j * VEC + c] = m;  // j-major: no conflicts
       }
-      __syncthreads();
+      if (__syncthreads_or(failed)) return drain();
       if (threadIdx.x < kScaleBlock) {
         const int col = (threadIdx.x % VEC) * E + threadIdx.x / VEC;
         float m = 0.f;
@@ -235,7 +242,8 @@ __global__ void __launch_bounds__(Tile<T>::THREADS, Tile<T>::PER_SM)
 }
 
 template <class T, bool E5M2, bool SQUARE, bool TRANS>
-mma_status_t run_tiles(const Ctx& ctx, const QuantProblem& p) {
+mma_status_t run_tiles(const Ctx& ctx, const QuantProblem& p,
+                       WaitHook hook = WaitHook{kWaitLimitNs, 0}) {
   using L = Tile<T>;
   const int64_t tiles_n = (p.N + kScaleBlock - 1) / kScaleBlock;
   const int64_t tiles = (p.M + kScaleBlock - 1) / kScaleBlock * tiles_n;
@@ -264,7 +272,8 @@ mma_status_t run_tiles(const Ctx& ctx, const QuantProblem& p) {
     return MMA_ERR_LAUNCH;
   const unsigned grid =
       unsigned(std::min<int64_t>(tiles, int64_t(ctx.num_sms) * L::PER_SM));
-  kern<<<grid, L::THREADS, L::SMEM, ctx.stream>>>(map, p, tiles_n, tiles, ctx.status);
+  kern<<<grid, L::THREADS, L::SMEM, ctx.stream>>>(map, p, tiles_n, tiles, ctx.status,
+                                                hook);
   return cudaGetLastError() == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
 }
 
@@ -294,6 +303,15 @@ mma_status_t by_format(const Ctx& ctx, const QuantProblem& p) {
 }
 
 }  // namespace
+
+mma_status_t launch_quantize_abort_selftest(const Ctx& ctx, int64_t limit_ns, int transpose,
+                                            const void* X, void* Q, float* S) {
+  const QuantProblem p = {MMA_BF16, false, transpose != 0, false, transpose ? 1 : 128,
+                          1024, 1024, X, 1024, Q, 1024, S, 8, 1};
+  const WaitHook hook = {static_cast<unsigned long long>(limit_ns), 1};
+  return transpose ? run_tiles<__nv_bfloat16, false, false, true>(ctx, p, hook)
+                   : run_tiles<__nv_bfloat16, false, true, false>(ctx, p, hook);
+}
 
 mma_status_t launch_quantize_f8(const Ctx& ctx, const QuantProblem& p) {
   switch (p.type) {

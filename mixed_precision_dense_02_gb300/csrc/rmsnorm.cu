@@ -30,16 +30,25 @@ namespace {
 
 // Sum of two values over the block, the same in every thread.  `buf` holds
 // 64 floats; calls in turn use different buffers, so one barrier is enough.
-__device__ __forceinline__ float2 block_sum2(float a, float b, float2* buf) {
+// VOTE: *any becomes whether any thread's is set.
+template <bool VOTE = false>
+__device__ __forceinline__ float2 block_sum2(float a, float b, float2* buf,
+                                             bool* any = nullptr) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
     a += __shfl_xor_sync(0xffffffffu, a, d);
     b += __shfl_xor_sync(0xffffffffu, b, d);
   }
   const int warps = blockDim.x >> 5;
-  if (warps == 1) return make_float2(a, b);
+  if (warps == 1) {
+    if constexpr (VOTE) *any = __any_sync(0xffffffffu, *any);
+    return make_float2(a, b);
+  }
   if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
+  if constexpr (VOTE)
+    *any = __syncthreads_or(*any);
+  else
+    __syncthreads();
   // every thread adds the warps' sums in their order (independent reads; a
   // second tree of shuffles took longer)
   a = 0.f;
@@ -235,7 +244,7 @@ template <class T, int VPT, bool TAIL>
 __global__ void __launch_bounds__(512, VPT <= 2 ? 2 : 1)
     rmsnorm_backward_kernel(const NormBackProblem p, bool w32, int stages,
                             int row_bytes, float* __restrict__ part,
-                            unsigned* status) {
+                            unsigned* status, const WaitHook hook) {
   constexpr int E = Vec<T>::kN;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[2][32];
@@ -252,7 +261,7 @@ __global__ void __launch_bounds__(512, VPT <= 2 ? 2 : 1)
   }
   __syncthreads();
   auto fetch = [&](int64_t row, int s) {
-    if (row >= p.M) return;
+    if (row >= p.M || hook.withhold) return;
     uint8_t* dst = ring + s * stage_bytes;
     mbar_arrive_expect_tx(&full[s], uint32_t(stage_bytes));
     bulk_load(dst, static_cast<const T*>(p.H) + row * p.ldh, row_bytes, &full[s]);
@@ -296,9 +305,10 @@ __global__ void __launch_bounds__(512, VPT <= 2 ? 2 : 1)
     const uint8_t* hs = ring + s * stage_bytes;
     const uint8_t* ds = hs + row_bytes;
     const uint8_t* rs = ds + row_bytes;
-    // (after a failed wait the rest runs on whatever is there; the status
-    // word tells)
-    mbar_wait(&full[s], phase, &abort_flag, status);
+    // A failed wait ends the block behind the sums' barrier, before anything is
+    // stored or fetched.  (8190 x 5000 BF16 64 us; with threads that remember it
+    // and go on without storing 70.)
+    bool failed = !mbar_wait(&full[s], phase, &abort_flag, status, hook.limit_ns);
     float ss = 0.f, gh = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -314,7 +324,17 @@ __global__ void __launch_bounds__(512, VPT <= 2 ? 2 : 1)
         gh = fmaf(dy[j] * w[j], h[j], gh);
       }
     }
-    const float2 sum = block_sum2(ss, gh, red[flip]);
+    const float2 sum = block_sum2<true>(ss, gh, red[flip], &failed);
+    if (failed) {
+      // the loads of this row and of those ahead (all but the one that would be
+      // fetched below)
+      const int ahead = row == blockIdx.x ? stages : stages - 1;
+      if (threadIdx.x == 0)
+        for (int k = 0; k < ahead && row + k * int64_t(gridDim.x) < p.M; ++k)
+          mbar_drain(&full[(s + k) % stages], phase ^ uint32_t(s + k >= stages), status,
+                     hook.limit_ns);
+      return;
+    }
     if (blockDim.x == 32) __syncwarp();
     // Every thread is past the row before: its stage takes the row that is
     // `stages` rows after it.
@@ -486,7 +506,7 @@ mma_status_t forward(const Ctx& ctx, const NormProblem& p, bool w32) {
 
 template <class T>
 mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32,
-                      float* part) {
+                      float* part, WaitHook hook = WaitHook{kWaitLimitNs, 0}) {
   constexpr int E = Vec<T>::kN;
   const int64_t vectors = (p.N + E - 1) / E;
   const int tensors = p.R ? 3 : 2;
@@ -505,7 +525,8 @@ mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32,
           }))
         return false;
       kernel<<<grid, shape.threads, size_t(shape.stages) * tensors * vectors * 16,
-               ctx.stream>>>(p, w32, shape.stages, int(vectors * 16), part, ctx.status);
+               ctx.stream>>>(p, w32, shape.stages, int(vectors * 16), part, ctx.status,
+                             hook);
       return true;
     };
     static PerContext<bool> a1, a2, a4;
@@ -546,6 +567,14 @@ mma_status_t launch_rmsnorm(const Ctx& ctx, const NormProblem& p) {
     case MMA_F16: return forward<__half>(ctx, p, w32);
     default: return forward<float>(ctx, p, false);
   }
+}
+
+mma_status_t launch_rmsnorm_abort_selftest(const Ctx& ctx, int64_t limit_ns, const void* X,
+                                           void* DX, float* DW, void* workspace) {
+  const NormBackProblem p = {MMA_BF16, MMA_BF16, 1024, 1024, X, 1024, X, 1024, X, 1e-6f,
+                             nullptr, 0, DX, 1024, DW};
+  return backward<__nv_bfloat16>(ctx, p, false, static_cast<float*>(workspace),
+                                 WaitHook{static_cast<unsigned long long>(limit_ns), 1});
 }
 
 int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t N) {

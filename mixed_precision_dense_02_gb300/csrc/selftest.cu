@@ -1,5 +1,5 @@
-// mma_selftest_wait_timeout, mma_selftest_gemm_abort: the failure-detection
-// path of the pipeline kernels, exercised on purpose without faulting or
+// mma_selftest_wait_timeout, mma_selftest_gemm_abort, mma_selftest_f8_abort: the
+// failure-detection path of the pipeline kernels, exercised on purpose without faulting or
 // hanging the GPU.
 //
 // Every wait of the tcgen05 pipeline (TMA stage, accumulator hand-off, C
@@ -13,7 +13,8 @@
 // told to issue no loads and its waits limited to limit_ns: the MMA
 // issuer's first stage wait runs out with no copy or MMA in flight, and
 // the kernel's own abort path (abort flag, drain, tensor-memory release,
-// cluster exit) runs for real.
+// cluster exit) runs for real.  mma_selftest_f8_abort does the same with the
+// quantiser's and the norm gradient's kernels.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -68,4 +69,19 @@ extern "C" mma_status_t mma_selftest_gemm_abort(int cluster, int64_t limit_ns,
   Ctx ctx{};
   if (!current_ctx(stream, &ctx)) return MMA_ERR_NO_DEVICE;
   return launch_gemm_tc_abort_selftest(ctx, cluster, limit_ns, A, B, D);
+}
+
+extern "C" mma_status_t mma_selftest_f8_abort(int kernel, int64_t limit_ns, const void* X,
+                                              void* Q, float* S, void* workspace,
+                                              void* stream) {
+  if (kernel < 0 || kernel > 2) return MMA_ERR_INVALID_ARG;
+  if (limit_ns < 1000000 || limit_ns > 10000000000ll) return MMA_ERR_INVALID_ARG;
+  if (!X || !Q || !S || (kernel == 2 && !workspace)) return MMA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(Q) |
+       reinterpret_cast<uintptr_t>(S) | reinterpret_cast<uintptr_t>(workspace)) & 15u)
+    return MMA_ERR_MISALIGNED;
+  Ctx ctx{};
+  if (!current_ctx(stream, &ctx)) return MMA_ERR_NO_DEVICE;
+  return kernel == 2 ? launch_rmsnorm_abort_selftest(ctx, limit_ns, X, Q, S, workspace)
+                     : launch_quantize_abort_selftest(ctx, limit_ns, kernel, X, Q, S);
 }

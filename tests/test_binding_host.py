@@ -44,3 +44,16 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     assert binding._raw_stream(1) == 7
     with pytest.raises(ValueError, match="cuda:0"):
         binding._raw_stream(0)
+
+
+def test_abort_selftest_arguments():
+    from mixed_precision_dense_02_gb300 import build
+    build.build()
+    p, ok, invalid, misaligned, nodev = 1 << 20, 0, 1, 3, 6
+    f = binding.mma_selftest_f8_abort
+    assert f(-1, 10 ** 7, p, p, p, None, None) == f(3, 10 ** 7, p, p, p, p, None) == invalid
+    assert f(0, 10, p, p, p, None, None) == f(1, 10 ** 11, p, p, p, None, None) == invalid
+    assert f(0, 10 ** 7, None, p, p, None, None) == f(2, 10 ** 7, p, p, p, None, None) == invalid
+    assert f(0, 10 ** 7, p, p + 8, p, None, None) == misaligned
+    if not torch.cuda.is_available():  # (these addresses are fake)
+        assert f(0, 10 ** 7, p, p, p, None, None) == f(2, 10 ** 7, p, p, p, p, None) == nodev
