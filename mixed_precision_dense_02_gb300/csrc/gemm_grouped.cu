@@ -142,7 +142,7 @@ struct Layout {
   // that a half's MMAs wait for half the epilogue.
   static constexpr int HV = KIND8 && BN == 256 ? 2 : 1;
   static constexpr int NUM_BARS =
-      4 * STAGES + 1 + 2 * ACCS * HV + 2 * SLOTS + (SPLIT ? 2 * kEpiWarps : 0);
+      4 * STAGES + 1 + 2 * ACCS * HV + 2 * SLOTS + (SPLIT ? kEpiWarps : 0);
   static constexpr int GROUP_OFFSET = BAR_OFFSET + NUM_BARS * 8 + 24;
   static constexpr int round16(int v) { return (v + 15) & ~15; }
   // SPLIT: sums of the other ranks, 128 rows of P times the columns in use
@@ -261,12 +261,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
   uint64_t* cut_ok = cut_in + STAGES;  // and its zeros are in place (leader)
   uint64_t* sfull = cut_ok + STAGES;
   uint64_t* sempty = sfull + L::SLOTS;
-  // SPLIT, one per epilogue warp: the other ranks' sums are here (rank 0);
-  // this rank's have been taken (the others)
+  // SPLIT, one per epilogue warp: the other ranks' sums are here (rank 0)
   uint64_t* part_full = sempty + L::SLOTS;
-  uint64_t* part_free = part_full + (SPLIT ? kEpiWarps : 0);
   uint32_t* tmem_slot =
-      reinterpret_cast<uint32_t*>(part_free + (SPLIT ? kEpiWarps : 0));
+      reinterpret_cast<uint32_t*>(part_full + (SPLIT ? kEpiWarps : 0));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* grow = reinterpret_cast<int*>(smem + L::GROUP_OFFSET);  // groups + 1
   int* gunit = grow + a.groups + 1;                            // groups + 1
@@ -302,10 +300,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     }
     mbar_init(done, 1);
     if constexpr (SPLIT)
-      for (int i = 0; i < kEpiWarps; ++i) {
-        mbar_init(&part_full[i], 1);
-        mbar_init(&part_free[i], 1);
-      }
+      for (int i = 0; i < kEpiWarps; ++i) mbar_init(&part_full[i], 1);
     *abort_flag = 0;
     fence_mbarrier_init();
     fence_proxy_async_smem();
@@ -768,7 +763,6 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     // the issuing CTA's barriers that hand the accumulators back
     const uint32_t tempty_lead =
         mapa_shared(smem_u32(&tempty[0]), CL > 1 ? 0 : cluster_ctarank());
-    [[maybe_unused]] uint32_t part_phase = 0;
     [[maybe_unused]] int block = 0;  // of the ring of blocks of D
     grid_dependency_wait();
     [[maybe_unused]] const int part_at =
@@ -928,10 +922,11 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
       if constexpr (SPLIT) {
         if (ksplit > 1) {
           // Only the columns that hold rows of D travel, as stores that
-          // complete on rank 0's barrier: no release, no arrival.
+          // complete on rank 0's barrier: no release, no arrival.  (The launch
+          // has a cluster for every tile there can be, so that a cluster takes
+          // one at most and the room for the sums is used once.)
           const int cols = t.q1 - t.q0;
           if (krank > 0) {
-            mbar_wait_lean(&part_free[ew], part_phase ^ 1u, abort_flag, a.status);
             const uint32_t dst = mapa_shared(
                 smem_u32(smem + part_at + (krank - 1) * a.part_cols * kP * 4), 0);
             const uint32_t bar = mapa_shared(smem_u32(&part_full[ew]), 0);
@@ -939,7 +934,6 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
             for (int j = 0; j < HALF; ++j)
               if (const int c = column(j / CB) + j % CB; c < cols)
                 st_async_f32(dst + c * kP * 4, sum[j], bar);
-            part_phase ^= 1u;
             continue;
           }
           if (lane == 0) {
@@ -949,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
             mbar_arrive_expect_tx(&part_full[ew], uint32_t((ksplit - 1) * mine * 128));
           }
           const bool got =
-              mbar_wait_cluster(&part_full[ew], part_phase, abort_flag, a.status);
+              mbar_wait_cluster(&part_full[ew], 0, abort_flag, a.status);
           if (!__all_sync(0xffffffffu, got)) break;
           for (int r = 1; r < ksplit; ++r) {
             const float* src = reinterpret_cast<const float*>(
@@ -958,14 +952,6 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
             for (int j = 0; j < HALF; ++j)
               if (const int c = column(j / CB) + j % CB; c < cols) sum[j] += src[c * kP];
           }
-          if (u + unit_step < units) {
-            __syncwarp();
-            if (lane == 0)
-              for (int r = 1; r < ksplit; ++r)
-                mbar_arrive_remote(mapa_shared(smem_u32(&part_free[ew]), r));
-            __syncwarp();
-          }
-          part_phase ^= 1u;
         }
       }
       if constexpr (ROWS) {

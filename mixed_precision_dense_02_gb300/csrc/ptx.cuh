@@ -94,14 +94,6 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
       : "memory");
 }
 
-// As mbar_arrive_cluster without its release at cluster scope (which took
-// about 1200 cycles): for handing back tensor memory, where no memory write
-// is published and the tcgen05 fences order the accesses.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
-
 // mbar_arrive by the lanes that have `doit`, without a branch.
 __device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool doit) {
   asm volatile(
@@ -112,7 +104,10 @@ __device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool doit) {
       : "memory");
 }
 
-// mbar_arrive_remote by the lanes that have `doit`, without a branch.
+// As mbar_arrive_cluster without its release at cluster scope (which took
+// about 1200 cycles), by the lanes that have `doit`, without a branch: for
+// handing back tensor memory, where no memory write is published and the
+// tcgen05 fences order the accesses.
 __device__ __forceinline__ void mbar_arrive_remote_if(uint32_t cluster_addr,
                                                       bool doit) {
   asm volatile(
