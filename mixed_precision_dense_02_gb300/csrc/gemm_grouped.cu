@@ -520,6 +520,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     // One thread.  Issuing waits for room in the tensor pipe, so the next
     // stage's barrier is looked at before the last MMA of a stage is issued.
     if (elect_one()) {
+      // (touches no memory, but its bounded waits are not to run while the
+      // kernel before does)
+      grid_dependency_wait();
       int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
       [[maybe_unused]] uint32_t cut_phase = 0;  // one bit per stage
@@ -648,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     int stage = 0;
     uint32_t cut_phase = 0;  // one bit per stage
     bool ok = true;
+    grid_dependency_wait();  // (as the MMA issuer)
     const uint32_t cut_lead = mapa_shared(smem_u32(&cut_ok[0]), CL > 1 ? 0 : cluster_ctarank());
     for (int u = first_unit; u < units; u += unit_step) {
       const Tile t = decode(u);
