@@ -299,17 +299,22 @@ mma_status_t mma_selftest_gemm_abort(int cluster, int64_t limit_ns,
                                      void *stream);
 
 /*
- * mma_selftest_f8_abort -- the same for the kernels of the norm and quantiser
- * that fetch ahead: kernel 0 is mma_quantize_f8 with blocks of 128 x 128 of a
- * 1024 x 1024 BF16 X (Q: 1024 x 1024 E4M3, S: 64 floats), kernel 1 that of the
- * transpose with blocks of 1 x 128 (S: 8192 floats), kernel 2
- * mma_rmsnorm_backward of 1024 x 1024 BF16 (X as DY, H and W; Q: DX, 1024 x
- * 1024 BF16; S: DW, 1024 floats; workspace: 456 * 1024 floats).  No loads are
- * issued and waits end after limit_ns (10^6 .. 10^10 ns): every block stops at
- * its first wait, drains and returns, Q is not written, nor S by kernels 0 and
- * 1 (kernel 2 adds up the untouched workspace there).  Buffers are 16-byte
- * aligned device memory of the caller; workspace is NULL for kernels 0 and 1.
- * Returns as mma_selftest_gemm_abort.
+ * mma_selftest_f8_abort -- the same for the kernels of the 8-bit and grouped
+ * calls.  X and Q are buffers of 1024 x 1024 BF16, S one of 8192 floats:
+ *
+ *   kernel 0, 1 : mma_quantize_f8 of X, blocks of 128 x 128 as is, blocks of 1 x
+ *                 128 of the transpose
+ *   kernel 2    : mma_rmsnorm_backward, X as DY, H and W; Q is DX, S is DW;
+ *                 workspace: 456 * 1024 floats
+ *   kernel 3, 4 : mma_gemm_f8 of X's first 1 or 1024 rows by its first 1024 (of
+ *                 1024 bytes each), k split over a cluster or on CTA pairs
+ *   kernel 5    : mma_gemm_grouped_wgrad, X as DY and X, S as the offsets
+ *
+ * No loads are issued.  Waits end after limit_ns (10^6 .. 10^10 ns; kernels 3 to
+ * 5: after their own limit of two seconds), every block stops, drains and
+ * returns, and Q is not written, nor is S (but kernel 2 adds up the untouched
+ * workspace there).  Buffers are 16-byte aligned device memory of the caller;
+ * workspace may be NULL but for kernel 2.  Returns as mma_selftest_gemm_abort.
  */
 mma_status_t mma_selftest_f8_abort(int kernel, int64_t limit_ns, const void *X,
                                    void *Q, float *S, void *workspace,

@@ -186,8 +186,8 @@ def mma_selftest_gemm_abort(cluster, limit_ns, A, B, D, stream) -> int:
 
 
 def mma_selftest_f8_abort(kernel, limit_ns, X, Q, S, workspace, stream) -> int:
-    """Run a tile quantiser (kernel 0, 1) or the norm's gradient (2) with no
-    loads and waits limited to limit_ns; mma_device_status then reports
+    """Run a tile quantiser (kernel 0, 1), the norm's gradient (2) or a product
+    (3, 4, 5) with no loads and bounded waits; mma_device_status then reports
     MMA_ERR_TIMEOUT once."""
     return load().mma_selftest_f8_abort(kernel, limit_ns, X, Q, S, workspace, stream)
 

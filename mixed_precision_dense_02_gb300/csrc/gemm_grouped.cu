@@ -110,6 +110,7 @@ struct GroupedArgs {
   const float* sq;
   int64_t sq_group, sq_row, sq_blk;
   int q_shift;
+  int withhold;  // (self-test) issue no loads
   unsigned* status;
 };
 
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
       int stage = 0;
       uint32_t phase = 0, issued = 0;
       uint32_t cut_fills = 0;  // parity of the cut fills of each stage
-      bool ok = true;
+      bool ok = !a.withhold;
       // the leader CTA's full barriers, which count both CTAs' bytes
       const uint32_t full_lead =
           CL > 1 ? mapa_shared(smem_u32(&full[0]), 0) : 0u;
@@ -922,7 +923,21 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
         }
       }
       ok = !__any_sync(0xffffffffu, *abort_flag != 0);
-      if (!ok) break;
+      // (SPLIT, lane 0 of rank 0) await this warp's columns of the other ranks'
+      [[maybe_unused]] auto expect_parts = [&] {
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) mine += min(max(t.q1 - t.q0 - column(i), 0), CB);
+        mbar_arrive_expect_tx(&part_full[ew], uint32_t((ksplit - 1) * mine * 128));
+      };
+      if (!ok) {
+        // after an abort, let the sums that other ranks still send land
+        if (SPLIT && ksplit > 1 && krank == 0 && lane == 0) {
+          expect_parts();
+          mbar_drain(&part_full[ew], 0, a.status);
+        }
+        break;
+      }
       if constexpr (SPLIT) {
         if (ksplit > 1) {
           // Only the columns that hold rows of D travel, as stores that
@@ -940,15 +955,13 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
                 st_async_f32(dst + c * kP * 4, sum[j], bar);
             continue;
           }
-          if (lane == 0) {
-            int mine = 0;  // columns of this warp
-#pragma unroll
-            for (int i = 0; i < NB; ++i) mine += min(max(cols - column(i), 0), CB);
-            mbar_arrive_expect_tx(&part_full[ew], uint32_t((ksplit - 1) * mine * 128));
-          }
+          if (lane == 0) expect_parts();
           const bool got =
               mbar_wait_cluster(&part_full[ew], 0, abort_flag, a.status);
-          if (!__all_sync(0xffffffffu, got)) break;
+          if (!__all_sync(0xffffffffu, got)) {
+            if (lane == 0) mbar_drain(&part_full[ew], 0, a.status);
+            break;
+          }
           for (int r = 1; r < ksplit; ++r) {
             const float* src = reinterpret_cast<const float*>(
                 smem + part_at + (r - 1) * a.part_cols * kP * 4);
@@ -1353,6 +1366,7 @@ mma_status_t launch_gemm_f8(const Ctx& ctx, const F8Problem& f) {
   a.D = f.D;
   a.ldd = f.ldd;
   a.status = ctx.status;
+  a.withhold = f.withhold;
   const Operand A = {f.A, f.lda, f.rows, 1, 0};
   const Operand B = {f.B, f.ldb, f.N, f.groups, f.stride_b};
   const int shift = f.sb_rows == 128 ? 7 : 0;
@@ -1454,10 +1468,42 @@ mma_status_t launch_gemm_grouped_wgrad(const Ctx& ctx, const WgradProblem& g) {
   a.ldd = g.ldd;
   a.d_group = g.stride_d;
   a.status = ctx.status;
+  a.withhold = g.withhold;
   a.idesc = idesc_f32(g.bf16, g.bf16, true, true, 2 * kP);
   const Operand X = {g.X, g.ldx, g.rows, 1, 0};
   const Operand DY = {g.DY, g.lddy, g.rows, 1, 0};
   return run<false, true, true, true, false, false, 2, 256, 6>(ctx, X, DY, a);
+}
+
+mma_status_t launch_products_abort_selftest(const Ctx& ctx, int kind, const void* X, void* D,
+                                            float* S) {
+  if (kind == 2) {
+    WgradProblem g = {};
+    g.bf16 = true;
+    g.d_type = MMA_BF16;
+    g.groups = 1;
+    g.rows = g.N = g.K = 1024;
+    g.DY = g.X = X;
+    g.lddy = g.ldx = g.ldd = 1024;
+    g.offsets = reinterpret_cast<const int*>(S);
+    g.D = D;
+    g.withhold = 1;
+    return launch_gemm_grouped_wgrad(ctx, g);
+  }
+  F8Problem f = {};
+  f.d_type = MMA_BF16;
+  f.groups = 1;
+  f.rows = kind == 0 ? 1 : 1024;
+  f.N = f.K = 1024;
+  f.A = f.B = X;
+  f.lda = f.ldb = f.ldd = 1024;
+  f.SA = f.SB = S;
+  f.sa_row = f.sb_row = 1;
+  f.sa_blk = f.sb_blk = 1024;
+  f.sb_rows = 128;
+  f.D = D;
+  f.withhold = 1;
+  return launch_gemm_f8(ctx, f);
 }
 
 }  // namespace mmagb

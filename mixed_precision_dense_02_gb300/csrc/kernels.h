@@ -189,6 +189,7 @@ struct F8Problem {
   int64_t ldc;
   void* D;
   int64_t ldd;
+  int withhold;  // self-test: issue no loads
 };
 mma_status_t launch_gemm_f8(const Ctx& ctx, const F8Problem& f);
 
@@ -223,6 +224,7 @@ struct WgradProblem {
   int64_t ldc, stride_c;
   void* D;
   int64_t ldd, stride_d;
+  int withhold;  // self-test: issue no loads
 };
 mma_status_t launch_gemm_grouped_wgrad(const Ctx& ctx, const WgradProblem& g);
 
@@ -283,11 +285,13 @@ struct QuantProblem {
 };
 mma_status_t launch_quantize_f8(const Ctx& ctx, const QuantProblem& p);
 
-// Failure-detection self-tests of the quantiser's tile kernel and of the norm's
-// gradient: no loads are issued and waits are limited to limit_ns (sizes at
-// mma_selftest_f8_abort).
+// Failure-detection self-tests of the quantiser's tile kernel, the norm's
+// gradient and the products: no loads are issued, and waits are limited to
+// limit_ns (the products': kWaitLimitNs).  Sizes at mma_selftest_f8_abort.
 mma_status_t launch_quantize_abort_selftest(const Ctx& ctx, int64_t limit_ns, int transpose,
                                             const void* X, void* Q, float* S);
+mma_status_t launch_products_abort_selftest(const Ctx& ctx, int kind, const void* X, void* D,
+                                            float* S);
 mma_status_t launch_rmsnorm_abort_selftest(const Ctx& ctx, int64_t limit_ns, const void* X,
                                            void* DX, float* DW, void* workspace);
 

@@ -14,7 +14,7 @@
 // issuer's first stage wait runs out with no copy or MMA in flight, and
 // the kernel's own abort path (abort flag, drain, tensor-memory release,
 // cluster exit) runs for real.  mma_selftest_f8_abort does the same with the
-// quantiser's and the norm gradient's kernels.
+// kernels of the quantiser, the norm's gradient and the products.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -74,7 +74,7 @@ extern "C" mma_status_t mma_selftest_gemm_abort(int cluster, int64_t limit_ns,
 extern "C" mma_status_t mma_selftest_f8_abort(int kernel, int64_t limit_ns, const void* X,
                                               void* Q, float* S, void* workspace,
                                               void* stream) {
-  if (kernel < 0 || kernel > 2) return MMA_ERR_INVALID_ARG;
+  if (kernel < 0 || kernel > 5) return MMA_ERR_INVALID_ARG;
   if (limit_ns < 1000000 || limit_ns > 10000000000ll) return MMA_ERR_INVALID_ARG;
   if (!X || !Q || !S || (kernel == 2 && !workspace)) return MMA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(Q) |
@@ -82,6 +82,7 @@ extern "C" mma_status_t mma_selftest_f8_abort(int kernel, int64_t limit_ns, cons
     return MMA_ERR_MISALIGNED;
   Ctx ctx{};
   if (!current_ctx(stream, &ctx)) return MMA_ERR_NO_DEVICE;
+  if (kernel > 2) return launch_products_abort_selftest(ctx, kernel - 3, X, Q, S);
   return kernel == 2 ? launch_rmsnorm_abort_selftest(ctx, limit_ns, X, Q, S, workspace)
                      : launch_quantize_abort_selftest(ctx, limit_ns, kernel, X, Q, S);
 }

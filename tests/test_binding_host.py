@@ -51,9 +51,10 @@ def test_abort_selftest_arguments():
     build.build()
     p, ok, invalid, misaligned, nodev = 1 << 20, 0, 1, 3, 6
     f = binding.mma_selftest_f8_abort
-    assert f(-1, 10 ** 7, p, p, p, None, None) == f(3, 10 ** 7, p, p, p, p, None) == invalid
+    assert f(-1, 10 ** 7, p, p, p, None, None) == f(6, 10 ** 7, p, p, p, p, None) == invalid
     assert f(0, 10, p, p, p, None, None) == f(1, 10 ** 11, p, p, p, None, None) == invalid
     assert f(0, 10 ** 7, None, p, p, None, None) == f(2, 10 ** 7, p, p, p, None, None) == invalid
     assert f(0, 10 ** 7, p, p + 8, p, None, None) == misaligned
     if not torch.cuda.is_available():  # (these addresses are fake)
         assert f(0, 10 ** 7, p, p, p, None, None) == f(2, 10 ** 7, p, p, p, p, None) == nodev
+        assert f(3, 10 ** 7, p, p, p, None, None) == f(5, 10 ** 7, p, p, p, None, None) == nodev
