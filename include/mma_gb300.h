@@ -513,7 +513,10 @@ mma_status_t mma_quantize_f8(int type, int f8_type, int64_t M, int64_t N,
  * B, SB          : N x K, scales of sb_rows x 128 blocks, sb_rows 1 or 128.
  * C              : M x N or NULL; may be D with the same leading dimension.
  * Block products are summed in the tensor core's FP32, scaled by the FP32
- * product of the two scales and added in FP32; D is rounded once.  The
+ * product of the two scales and added in FP32; D is rounded once.  SA * SB
+ * must be in FP32's range: a block for which it is below 2^-126 loses bits and
+ * below 2^-150 all of its share, also where the share itself (up to 2^25 for
+ * E4M3, 2^39 for E5M2, times that) would be in range.  The
  * gradients are the same call on quantised gradients and transposes (see
  * mma_quantize_f8); sb_rows = 1 serves the weight's.
  */
