@@ -31,7 +31,6 @@ struct Vec<float> {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]),
                       __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
-  __device__ static float one(float v) { return v; }
   __device__ static float round(float v) { return v; }
 };
 
@@ -55,7 +54,6 @@ struct Vec<__nv_bfloat16> {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ static float one(__nv_bfloat16 v) { return __bfloat162float(v); }
   __device__ static __nv_bfloat16 round(float v) { return __float2bfloat16_rn(v); }
 };
 
@@ -80,7 +78,6 @@ struct Vec<__half> {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ static float one(__half v) { return __half2float(v); }
   __device__ static __half round(float v) { return __float2half_rn(v); }
 };
 
@@ -213,11 +210,11 @@ struct Divisor {
   }
 };
 
-// Two values over their scale, in 8 bits (to nearest, ties to even; beyond
-// the largest value that value; NaN stays NaN).
+// Two values, already divided by their scale, in 8 bits (to nearest, ties
+// to even; beyond the largest value that value; NaN stays NaN).
 template <bool E5M2>
-__device__ __forceinline__ uint32_t to_f8x2(const Divisor& d, float lo, float hi) {
-  return uint32_t(__nv_cvt_float2_to_fp8x2(d(lo, hi), __NV_SATFINITE,
+__device__ __forceinline__ uint32_t to_f8x2(float2 v) {
+  return uint32_t(__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE,
                                            E5M2 ? __NV_E5M2 : __NV_E4M3));
 }
 
@@ -228,8 +225,8 @@ __device__ __forceinline__ void store_f8(uint8_t* row, int64_t v, int64_t n,
   uint32_t w[E / 4];
 #pragma unroll
   for (int i = 0; i < E / 4; ++i)
-    w[i] = to_f8x2<E5M2>(d, y[4 * i], y[4 * i + 1]) |
-           (to_f8x2<E5M2>(d, y[4 * i + 2], y[4 * i + 3]) << 16);
+    w[i] = to_f8x2<E5M2>(d(y[4 * i], y[4 * i + 1])) |
+           (to_f8x2<E5M2>(d(y[4 * i + 2], y[4 * i + 3])) << 16);
   if (!TAIL || (v + 1) * E <= n) {
     if constexpr (E == 8)
       *reinterpret_cast<uint2*>(row + v * 8) = make_uint2(w[0], w[1]);
