@@ -40,21 +40,28 @@
 // CTAs shares a tile's k range (SPLIT); the sums meet in the shared memory of
 // its first CTA, which adds them in order of rank.
 //
-// Measured, operands rotating through more than L2, and what bounds it:
-//   8-bit 8192 x 8192 x 4096, square scales, BF16 D: 210 us, 2610 TFLOP/s.
-//     The additions: a chunk's loads of tensor memory and FMAs keep an
-//     epilogue warp some 830 clocks, its MMAs take 530.
-//   8-bit 2048 x 4096 x 8200, row scales, FP32 C and D: 99 us, 1384 TFLOP/s.
-//     The same with a multiplication more per element, and 128 tiles are two
-//     waves of 76 pairs, the second two thirds full.
-//   32 experts of 4096 x 2048, 16384 tokens, BF16: forward 186 us, input
-//     gradient 188, 1480 TFLOP/s.  The tensor pipe at a power-capped clock,
-//     and tiles that a group does not fill.
-//   The same weight gradient in FP32: 310 us.  Writes of D: 1.07 GB, which
-//     take 186 us when there is nothing to add up.
+// Measured, operands rotating through more than L2, and what bounds it.  First
+// in a graph of a few calls, then under a load of half a second and more, when
+// the power limit has lowered the clock:
+//   8-bit 8192 x 8192 x 4096, square scales, BF16 D: 207-212 us, 222-234
+//     (2350 to 2660 TFLOP/s).  The additions: a chunk's loads of tensor memory
+//     and FMAs keep an epilogue warp some 830 clocks, its MMAs take 530.
+//   8-bit 2048 x 4096 x 8200, row scales, FP32 C and D: 99 us, 99 (1384
+//     TFLOP/s).  The same with a multiplication more per element, and 128 tiles
+//     are two waves of 76 pairs, the second two thirds full.
+//   32 experts of 4096 x 2048, 16384 tokens, BF16: forward 184-192 us, 212-220;
+//     input gradient 182-220, 210-221 (1250 to 1510 TFLOP/s).  The tensor pipe
+//     at a power-capped clock; groups rounded to 32 rows are 3 % more work, and
+//     tiles of some 205 of the 256 columns read P more often.
+//   The same weight gradient: FP32 307-350 us, 315-327; BF16 242-248, 254-262.
+//     Writes of D: 1.07 GB, which take 186 us when there is nothing to add up.
+//   The same forward in 8 bits: 157 us, 165-169 (1640 TFLOP/s).  The additions.
 //   64 experts of 2048 x 4096, 96 tokens, 8-bit: 63 us, 5.9 TB/s.  HBM.
-//   One token, 8192 x 4096, 8-bit: 10.2 us, 3.3 TB/s.  Some 2 us each for the
+//   One token, 8192 x 4096, 8-bit: 10.0 us, 3.4 TB/s.  Some 2 us each for the
 //     first loads' latency and for the join of a cluster's sums.
+// All with the scales of one k block side by side.  Scales with a row's side by
+// side (a gather of rows makes them so) are 32 lines per copy: 221-225 us, the
+// row scales 139, one token 10.0-10.8, the experts' the same.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

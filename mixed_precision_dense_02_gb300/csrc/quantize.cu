@@ -11,8 +11,8 @@
 // output's rows, that is, down the input's columns.
 //
 // Bound by memory: x is read once, q written once.  16384 x 2048 BF16 by rows:
-// 19.2 us, 5.3 TB/s; 4000 x 8192 FP32 by squares, transposed: 28.6 us,
-// 5.7 TB/s.
+// 19.5 us, 5.2 TB/s; 4000 x 8192 FP32 by squares, transposed: 29.4 us,
+// 5.6 TB/s; 8192 x 8192 BF16 by squares 33.8 us, by rows transposed 34.7.
 #include <algorithm>
 
 #include <cudaTypedefs.h>

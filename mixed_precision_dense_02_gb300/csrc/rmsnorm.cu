@@ -15,9 +15,12 @@
 //
 // Both are bound by memory: each input is read once and each output written
 // once, a row is held on chip between its two uses.  BF16, 8192 x 8192:
-// forward 77 us, 6.1 TB/s; one row of 4096 2.7 us, all latency.  Backward,
-// 8190 x 5000 BF16: 63 us, 5.2 TB/s, some 6 us of them for the shares of dw
-// (456 rows written, read and added up by a second kernel).
+// forward 77 us, 6.1 TB/s; one row of 4096 2.5 us, all latency.  Backward, 8190
+// x 5000 BF16: 64 us, 5.1 TB/s, some 6 us of them for the shares of dw (456
+// rows written, read and added up by a second kernel); 8192 x 8192 94 us.
+// Rows of more than 2048 vectors are read twice: forward 2048 x 32768 BF16 183
+// us of 69 (floor), 4096 x 16384 FP32 266 of 129; backward 2048 x 32768 387 of
+// 79, where the share of dw also goes through memory for every row.
 #include <algorithm>
 #include <type_traits>
 
