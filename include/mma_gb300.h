@@ -481,6 +481,42 @@ mma_status_t mma_rmsnorm_backward(int type, int w_type, int64_t M, int64_t N,
                                   int64_t workspace_bytes, void *stream);
 
 /*
+ * mma_layernorm -- layer norm of the rows of X + R, in `type`, in 8 bits or both.
+ *
+ *     h = x + r,   c = h - mean(h),   y = c / sqrt(mean(c^2) + eps) * w + b
+ *
+ * in FP32 throughout; H, Y, Q and S and all other arguments as in mma_rmsnorm_f8.
+ * B is the bias, N elements of w_type, or NULL.  The mean is taken first and the
+ * variance from the distances to it, so that a row far from zero keeps its own.
+ * A NaN or infinity in a row makes its row NaN.
+ */
+mma_status_t mma_layernorm(int type, int w_type, int64_t M, int64_t N,
+                           const void *X, int64_t ldx, const void *R,
+                           int64_t ldr, const void *W, const void *B, float eps,
+                           int pow2, void *H, int64_t ldh, void *Y, int64_t ldy,
+                           void *Q, int64_t ldq, float *S, int64_t s_row,
+                           int64_t s_blk, void *stream);
+
+/*
+ * mma_layernorm_backward -- gradient of the layer norm, from the stored sum H:
+ *
+ *     g = dy * w,  g' = g - mean(g),  DX = g' / std - c * mean(g' c) / std^3 + R
+ *     DW[j] = sum over rows of dy * c / std,   DB[j] = sum over rows of dy
+ *
+ * DW and DB in FP32, summed in a fixed order through `workspace` of at least
+ * mma_layernorm_backward_workspace(M, N) bytes (at most 912 * N * 4).  All else
+ * as in mma_rmsnorm_backward.
+ */
+int64_t mma_layernorm_backward_workspace(int64_t M, int64_t N);
+mma_status_t mma_layernorm_backward(int type, int w_type, int64_t M, int64_t N,
+                                    const void *DY, int64_t lddy, const void *H,
+                                    int64_t ldh, const void *W, float eps,
+                                    const void *R, int64_t ldr, void *DX,
+                                    int64_t lddx, float *DW, float *DB,
+                                    void *workspace, int64_t workspace_bytes,
+                                    void *stream);
+
+/*
  * mma_quantize_f8 -- X (M x N; MMA_F16, MMA_BF16 or MMA_F32) as 8-bit values
  * of type f8_type with scales:
  *

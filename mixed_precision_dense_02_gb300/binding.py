@@ -48,6 +48,13 @@ SIGNATURES = {
                                     _p, _f32, _p, _i64, _p, _i64, _p, _p, _i64,
                                     _p]),
     "mma_rmsnorm_backward_workspace": (_i64, [_i64, _i64]),
+    "mma_layernorm": (_int, [_int, _int, _i64, _i64, _p, _i64, _p, _i64, _p,
+                             _p, _f32, _int, _p, _i64, _p, _i64, _p, _i64, _p,
+                             _i64, _i64, _p]),
+    "mma_layernorm_backward": (_int, [_int, _int, _i64, _i64, _p, _i64, _p,
+                                      _i64, _p, _f32, _p, _i64, _p, _i64, _p,
+                                      _p, _p, _i64, _p]),
+    "mma_layernorm_backward_workspace": (_i64, [_i64, _i64]),
     "mma_quantize_f8": (_int, [_int, _int, _i64, _i64, _int, _int, _int, _p,
                                _i64, _p, _i64, _p, _i64, _i64, _p]),
     "mma_gemm_f8": (_int, [_int, _int, _int, _i64, _i64, _i64, _p, _i64, _p,
@@ -483,13 +490,13 @@ def _scale_strides(t):
     return (stride[-2] if shape[-2] > 1 else 1, stride[-1] if shape[-1] > 1 else 0)
 
 
-def _weight(W, X, n):
+def _weight(W, X, n, name="W"):
     """The ABI code of a norm's weights: of X's type or float32."""
-    code = _take("W", W, _kinds()["wide"], n)
+    code = _take(name, W, _kinds()["wide"], n)
     if code != MMA_F32 and W.dtype != X.dtype:
-        raise TypeError(f"W must be {X.dtype} or torch.float32, not {W.dtype}")
+        raise TypeError(f"{name} must be {X.dtype} or torch.float32, not {W.dtype}")
     if n > 1 and W.stride(0) != 1:
-        raise ValueError("W must be contiguous")
+        raise ValueError(f"{name} must be contiguous")
     return code
 
 
@@ -606,6 +613,101 @@ def rmsnorm_backward(dY, H, W, dH=None, *, eps: float = 1e-6, stream=None):
     if st:
         _check("mma_rmsnorm_backward", st)
     return dX, dW
+
+
+def _plan_layernorm(X, W, bias, residual):
+    plan = _plan_rmsnorm(X, W, residual)
+    if bias is not None:
+        if _weight(bias, X, X.shape[1], "bias") != plan[1]:
+            raise TypeError("W and bias must have one type")
+        _one_device(X, bias)
+    return plan
+
+
+def _layernorm(X, W, bias, residual, eps, pow2, y, q, stream):
+    """Both layer norms: (Q, S, H, Y), None where not asked for."""
+    torch = _torch()
+    (code, w_code, M, N, ldx, ldr, ldh, f8, ldq, blocks, index) = _plan(
+        ("layer norm", _key(X), _key(W), _key(bias), _key(residual)), _plan_layernorm, X, W,
+        bias, residual)
+    if stream is not None:
+        return _under(stream, index, _layernorm, X, W, bias, residual, eps, pow2, y, q, None)
+    dtype, device = X.dtype, X.device
+    H, r_ptr, h_ptr = X, None, None
+    if residual is not None:
+        H = torch.empty_strided((M, N), (ldh, 1), dtype=dtype, device=device)
+        r_ptr, h_ptr = residual.data_ptr(), H.data_ptr()
+    Y = Q = S = None
+    if y:
+        Y = torch.empty_strided((M, N), (ldh, 1), dtype=dtype, device=device)
+    if q:
+        Q = torch.empty_strided((M, N), (ldq, 1), dtype=f8, device=device)
+        # the scales of one block side by side
+        S = torch.empty_strided((M, blocks), (1, M), dtype=torch.float32, device=device)
+    st = load().mma_layernorm(
+        code, w_code, M, N, X.data_ptr(), ldx, r_ptr, ldr, W.data_ptr(),
+        None if bias is None else bias.data_ptr(), eps, 1 if pow2 else 0, h_ptr, ldh,
+        None if Y is None else Y.data_ptr(), ldh, None if Q is None else Q.data_ptr(), ldq,
+        None if S is None else S.data_ptr(), 1, M, _raw_stream(index))
+    if st:
+        _check("mma_layernorm", st)
+    return Q, S, H, Y
+
+
+def layernorm(X, W, bias=None, residual=None, *, eps: float = 1e-5, stream=None):
+    """Layer norm of ``X + residual``.
+
+    ``h = X + residual``, ``c = h - mean(h)``, ``y = c * W / sqrt(mean(c**2) +
+    eps) + bias`` per row.  ``X``, ``residual``: (M, N) float16, bfloat16 or
+    float32; ``W``, ``bias``: (N,), both of that type or both float32.  Returns
+    ``(Y, H)`` in X's type, H being the sum (X itself without a residual).
+    """
+    _, _, H, Y = _layernorm(X, W, bias, residual, eps, False, True, False, stream)
+    return Y, H
+
+
+def layernorm_f8(X, W, bias=None, residual=None, *, eps: float = 1e-5, pow2: bool = False,
+                 y: bool = False, stream=None):
+    """``layernorm`` with an 8-bit output: returns ``(Q, S, H)``, with ``y=True``
+    also Y, as ``rmsnorm_f8`` does.
+    """
+    out = _layernorm(X, W, bias, residual, eps, bool(pow2), bool(y), True, stream)
+    return out if y else out[:3]
+
+
+def _plan_layernorm_backward(dY, H, W, dH):
+    plan = _plan_rmsnorm_backward(dY, H, W, dH)
+    M, N = H.shape
+    return (*plan[:8], load().mma_layernorm_backward_workspace(M, N), plan[9])
+
+
+def layernorm_backward(dY, H, W, dH=None, *, eps: float = 1e-5, stream=None):
+    """Gradient of the layer norm (taken at the unrounded y).
+
+    ``dY``: gradient of y; ``H``: the sum that the forward returned; ``dH``:
+    gradient that reaches H from elsewhere.  Returns ``(dX, dW, dbias)``: dX, the
+    gradient of X and of the residual alike, in H's type, and dW and dbias (N,)
+    float32.
+    """
+    torch = _torch()
+    code, w_code, M, N, ldy, ldh, ldr, ldx, need, index = _plan(
+        ("layer back", _key(dY), _key(H), _key(W), _key(dH)), _plan_layernorm_backward,
+        dY, H, W, dH)
+    if stream is not None:
+        return _under(stream, index, layernorm_backward, dY, H, W, dH, eps=eps)
+    device = H.device
+    dX = torch.empty_strided((M, N), (ldx, 1), dtype=H.dtype, device=device)
+    dW = torch.empty((N,), dtype=torch.float32, device=device)
+    dB = torch.empty((N,), dtype=torch.float32, device=device)
+    # (its memory goes to other work of the current stream only after the call's)
+    ws = torch.empty((need,), dtype=torch.uint8, device=device)
+    st = load().mma_layernorm_backward(
+        code, w_code, M, N, dY.data_ptr(), ldy, H.data_ptr(), ldh, W.data_ptr(),
+        eps, None if dH is None else dH.data_ptr(), ldr, dX.data_ptr(), ldx,
+        dW.data_ptr(), dB.data_ptr(), ws.data_ptr(), need, _raw_stream(index))
+    if st:
+        _check("mma_layernorm_backward", st)
+    return dX, dW, dB
 
 
 def _plan_quantize(X, fmt, block_rows, transpose):

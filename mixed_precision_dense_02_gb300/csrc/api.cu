@@ -878,39 +878,91 @@ extern "C" mma_status_t mma_gemm_grouped_wgrad(
   return launch_gemm_grouped_wgrad(ctx, g);
 }
 
-extern "C" mma_status_t mma_rmsnorm_f8(
-    int type, int w_type, int64_t M, int64_t N, const void* X, int64_t ldx,
-    const void* R, int64_t ldr, const void* W, float eps, int pow2, void* H,
-    int64_t ldh, void* Y, int64_t ldy, void* Q, int64_t ldq, float* S,
-    int64_t s_row, int64_t s_blk, void* stream) {
-  const int64_t eb = float_bytes(type);
-  if (eb == 0 || (w_type != type && w_type != MMA_F32)) return MMA_ERR_UNSUPPORTED;
-  if (!dim_ok(M) || !dim_ok(N) || !(eps >= 0.f)) return MMA_ERR_INVALID_ARG;
-  if (M == 0 || N == 0) return MMA_OK;
-  if (Y == nullptr && Q == nullptr) return MMA_ERR_INVALID_ARG;
-  if ((H != nullptr && H == X && ldh != ldx) ||
-      (H != nullptr && H == R && ldh != ldr))
+namespace {
+
+// Both norms (B and DB: the layer norm's bias and its gradient).
+mma_status_t norm(bool centre, const NormProblem& p, void* stream) {
+  const int64_t eb = float_bytes(p.type);
+  if (eb == 0 || (p.w_type != p.type && p.w_type != MMA_F32)) return MMA_ERR_UNSUPPORTED;
+  if (!dim_ok(p.M) || !dim_ok(p.N) || !(p.eps >= 0.f)) return MMA_ERR_INVALID_ARG;
+  if (p.M == 0 || p.N == 0) return MMA_OK;
+  if (p.Y == nullptr && p.Q == nullptr) return MMA_ERR_INVALID_ARG;
+  if ((p.H != nullptr && p.H == p.X && p.ldh != p.ldx) ||
+      (p.H != nullptr && p.H == p.R && p.ldh != p.ldr))
     return MMA_ERR_INVALID_ARG;
-  MMA_CHECK(check_in(X, ldx, N, eb));
-  if (R) MMA_CHECK(check_in(R, ldr, N, eb));
-  MMA_CHECK(check_in(W, N, N, 16));
-  if (H) MMA_CHECK(check_in(H, ldh, N, eb));
-  if (Y) MMA_CHECK(check_in(Y, ldy, N, eb));
-  if (Q) {
-    MMA_CHECK(check_scales(S, s_row, s_blk));
-    MMA_CHECK(check_in(Q, ldq, N, 1));
+  MMA_CHECK(check_in(p.X, p.ldx, p.N, eb));
+  if (p.R) MMA_CHECK(check_in(p.R, p.ldr, p.N, eb));
+  MMA_CHECK(check_in(p.W, p.N, p.N, 16));
+  if (p.B) MMA_CHECK(check_in(p.B, p.N, p.N, 16));
+  if (p.H) MMA_CHECK(check_in(p.H, p.ldh, p.N, eb));
+  if (p.Y) MMA_CHECK(check_in(p.Y, p.ldy, p.N, eb));
+  if (p.Q) {
+    MMA_CHECK(check_scales(p.S, p.s_row, p.s_blk));
+    MMA_CHECK(check_in(p.Q, p.ldq, p.N, 1));
   }
   int dev = -1;
   const DeviceInfo* info = device_info(&dev);
   if (!info) return MMA_ERR_NO_DEVICE;
   Ctx ctx = make_ctx(stream, dev, info);
-  return launch_rmsnorm(ctx, NormProblem{type, w_type, M, N, X, ldx, R, ldr, W,
-                                         eps, pow2 != 0, H, ldh, Y, ldy, Q, ldq,
-                                         S, s_row, s_blk});
+  return centre ? launch_layernorm(ctx, p) : launch_rmsnorm(ctx, p);
+}
+
+mma_status_t norm_backward(bool centre, const NormBackProblem& p, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  const int64_t eb = float_bytes(p.type);
+  if (eb == 0 || (p.w_type != p.type && p.w_type != MMA_F32)) return MMA_ERR_UNSUPPORTED;
+  if (!dim_ok(p.M) || !dim_ok(p.N) || !(p.eps >= 0.f)) return MMA_ERR_INVALID_ARG;
+  if (p.N == 0) return MMA_OK;
+  if (p.DW == nullptr || (centre && p.DB == nullptr)) return MMA_ERR_INVALID_ARG;
+  if (!aligned4(p.DW) || !aligned4(p.DB)) return MMA_ERR_MISALIGNED;
+  const int64_t need = rmsnorm_backward_workspace_bytes(p.M, p.N) * (centre ? 2 : 1);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+    return MMA_ERR_INVALID_ARG;
+  if (need > 0 && !aligned4(workspace)) return MMA_ERR_MISALIGNED;
+  if (p.M > 0) {
+    if ((p.DX == p.DY && p.lddx != p.lddy) ||
+        (p.R != nullptr && p.DX == p.R && p.lddx != p.ldr))
+      return MMA_ERR_INVALID_ARG;
+    MMA_CHECK(check_in(p.DY, p.lddy, p.N, eb));
+    MMA_CHECK(check_in(p.H, p.ldh, p.N, eb));
+    MMA_CHECK(check_in(p.W, p.N, p.N, 16));
+    if (p.R) MMA_CHECK(check_in(p.R, p.ldr, p.N, eb));
+    MMA_CHECK(check_in(p.DX, p.lddx, p.N, eb));
+  }
+  int dev = -1;
+  const DeviceInfo* info = device_info(&dev);
+  if (!info) return MMA_ERR_NO_DEVICE;
+  Ctx ctx = make_ctx(stream, dev, info);
+  return centre ? launch_layernorm_backward(ctx, p, workspace)
+                : launch_rmsnorm_backward(ctx, p, workspace);
+}
+
+}  // namespace
+
+extern "C" mma_status_t mma_rmsnorm_f8(
+    int type, int w_type, int64_t M, int64_t N, const void* X, int64_t ldx,
+    const void* R, int64_t ldr, const void* W, float eps, int pow2, void* H,
+    int64_t ldh, void* Y, int64_t ldy, void* Q, int64_t ldq, float* S,
+    int64_t s_row, int64_t s_blk, void* stream) {
+  return norm(false, NormProblem{type, w_type, M, N, X, ldx, R, ldr, W, eps, pow2 != 0,
+                                 H, ldh, Y, ldy, Q, ldq, S, s_row, s_blk}, stream);
+}
+
+extern "C" mma_status_t mma_layernorm(
+    int type, int w_type, int64_t M, int64_t N, const void* X, int64_t ldx,
+    const void* R, int64_t ldr, const void* W, const void* B, float eps, int pow2,
+    void* H, int64_t ldh, void* Y, int64_t ldy, void* Q, int64_t ldq, float* S,
+    int64_t s_row, int64_t s_blk, void* stream) {
+  return norm(true, NormProblem{type, w_type, M, N, X, ldx, R, ldr, W, eps, pow2 != 0,
+                                H, ldh, Y, ldy, Q, ldq, S, s_row, s_blk, B}, stream);
 }
 
 extern "C" int64_t mma_rmsnorm_backward_workspace(int64_t M, int64_t N) {
   return dim_ok(M) && dim_ok(N) ? rmsnorm_backward_workspace_bytes(M, N) : 0;
+}
+
+extern "C" int64_t mma_layernorm_backward_workspace(int64_t M, int64_t N) {
+  return 2 * mma_rmsnorm_backward_workspace(M, N);
 }
 
 extern "C" mma_status_t mma_rmsnorm_backward(
@@ -918,32 +970,19 @@ extern "C" mma_status_t mma_rmsnorm_backward(
     const void* H, int64_t ldh, const void* W, float eps, const void* R,
     int64_t ldr, void* DX, int64_t lddx, float* DW, void* workspace,
     int64_t workspace_bytes, void* stream) {
-  const int64_t eb = float_bytes(type);
-  if (eb == 0 || (w_type != type && w_type != MMA_F32)) return MMA_ERR_UNSUPPORTED;
-  if (!dim_ok(M) || !dim_ok(N) || !(eps >= 0.f)) return MMA_ERR_INVALID_ARG;
-  if (N == 0) return MMA_OK;
-  if (DW == nullptr) return MMA_ERR_INVALID_ARG;
-  if (!aligned4(DW)) return MMA_ERR_MISALIGNED;
-  const int64_t need = rmsnorm_backward_workspace_bytes(M, N);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need))
-    return MMA_ERR_INVALID_ARG;
-  if (need > 0 && !aligned4(workspace)) return MMA_ERR_MISALIGNED;
-  if (M > 0) {
-    if ((DX == DY && lddx != lddy) || (R != nullptr && DX == R && lddx != ldr))
-      return MMA_ERR_INVALID_ARG;
-    MMA_CHECK(check_in(DY, lddy, N, eb));
-    MMA_CHECK(check_in(H, ldh, N, eb));
-    MMA_CHECK(check_in(W, N, N, 16));
-    if (R) MMA_CHECK(check_in(R, ldr, N, eb));
-    MMA_CHECK(check_in(DX, lddx, N, eb));
-  }
-  int dev = -1;
-  const DeviceInfo* info = device_info(&dev);
-  if (!info) return MMA_ERR_NO_DEVICE;
-  Ctx ctx = make_ctx(stream, dev, info);
-  const NormBackProblem p = {type, w_type, M, N, DY, lddy, H, ldh, W, eps,
-                             R, ldr, DX, lddx, DW};
-  return launch_rmsnorm_backward(ctx, p, workspace);
+  return norm_backward(false, NormBackProblem{type, w_type, M, N, DY, lddy, H, ldh, W, eps,
+                                              R, ldr, DX, lddx, DW, nullptr},
+                       workspace, workspace_bytes, stream);
+}
+
+extern "C" mma_status_t mma_layernorm_backward(
+    int type, int w_type, int64_t M, int64_t N, const void* DY, int64_t lddy,
+    const void* H, int64_t ldh, const void* W, float eps, const void* R,
+    int64_t ldr, void* DX, int64_t lddx, float* DW, float* DB, void* workspace,
+    int64_t workspace_bytes, void* stream) {
+  return norm_backward(true, NormBackProblem{type, w_type, M, N, DY, lddy, H, ldh, W, eps,
+                                             R, ldr, DX, lddx, DW, DB},
+                       workspace, workspace_bytes, stream);
 }
 
 extern "C" mma_status_t mma_quantize_f8(

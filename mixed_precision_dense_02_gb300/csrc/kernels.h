@@ -248,6 +248,7 @@ struct NormProblem {
   int64_t ldq;
   float* S;
   int64_t s_row, s_blk;
+  const void* B = nullptr;  // layer norm: bias of W's type, or NULL
 };
 mma_status_t launch_rmsnorm(const Ctx& ctx, const NormProblem& p);
 
@@ -265,10 +266,16 @@ struct NormBackProblem {
   void* DX;
   int64_t lddx;
   float* DW;
+  float* DB;  // layer norm
 };
 int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t N);
 mma_status_t launch_rmsnorm_backward(const Ctx& ctx, const NormBackProblem& p,
                                      void* workspace);
+
+// Layer norm (rmsnorm.cu); the gradient's workspace is twice the above.
+mma_status_t launch_layernorm(const Ctx& ctx, const NormProblem& p);
+mma_status_t launch_layernorm_backward(const Ctx& ctx, const NormBackProblem& p,
+                                       void* workspace);
 
 // 8-bit quantisation (quantize.cu).
 struct QuantProblem {
