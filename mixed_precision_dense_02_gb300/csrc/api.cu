@@ -915,7 +915,8 @@ mma_status_t norm_backward(bool centre, const NormBackProblem& p, void* workspac
   if (p.N == 0) return MMA_OK;
   if (p.DW == nullptr || (centre && p.DB == nullptr)) return MMA_ERR_INVALID_ARG;
   if (!aligned4(p.DW) || !aligned4(p.DB)) return MMA_ERR_MISALIGNED;
-  const int64_t need = rmsnorm_backward_workspace_bytes(p.M, p.N) * (centre ? 2 : 1);
+  const int64_t need = centre ? layernorm_backward_workspace_bytes(p.M, p.N)
+                              : rmsnorm_backward_workspace_bytes(p.M, p.N);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need))
     return MMA_ERR_INVALID_ARG;
   if (need > 0 && !aligned4(workspace)) return MMA_ERR_MISALIGNED;
@@ -962,7 +963,7 @@ extern "C" int64_t mma_rmsnorm_backward_workspace(int64_t M, int64_t N) {
 }
 
 extern "C" int64_t mma_layernorm_backward_workspace(int64_t M, int64_t N) {
-  return 2 * mma_rmsnorm_backward_workspace(M, N);
+  return dim_ok(M) && dim_ok(N) ? layernorm_backward_workspace_bytes(M, N) : 0;
 }
 
 extern "C" mma_status_t mma_rmsnorm_backward(

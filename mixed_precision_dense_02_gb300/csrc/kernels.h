@@ -272,7 +272,8 @@ int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t N);
 mma_status_t launch_rmsnorm_backward(const Ctx& ctx, const NormBackProblem& p,
                                      void* workspace);
 
-// Layer norm (rmsnorm.cu); the gradient's workspace is twice the above.
+// Layer norm (rmsnorm.cu).
+int64_t layernorm_backward_workspace_bytes(int64_t M, int64_t N);
 mma_status_t launch_layernorm(const Ctx& ctx, const NormProblem& p);
 mma_status_t launch_layernorm_backward(const Ctx& ctx, const NormBackProblem& p,
                                        void* workspace);

@@ -13,14 +13,7 @@
 // (dx is the gradient of x and of the residual alike; dr the gradient that
 // reaches h from elsewhere).
 //
-// The layer norm (CENTRE) has the row's mean and distances to it instead:
-//     c = h - mean(h),  y = c / sqrt(mean(c^2) + eps) * w + b
-//     dx = (g - mean(g)) / std - c * mean((g - mean(g)) c) / std^3 + dr
-//     dw = sum over rows dy c / std,   db = sum over rows dy
-// (mean(c) = 0, so that g's mean may be taken off in the second sum, which
-// then has no large terms that cancel).
-//
-// All are bound by memory: each input is read once and each output written
+// Both are bound by memory: each input is read once and each output written
 // once, a row is held on chip between its two uses.  BF16, 8192 x 8192:
 // forward 77 us, 6.1 TB/s; one row of 4096 2.5 us, all latency.  Backward, 8190
 // x 5000 BF16: 64 us, 5.1 TB/s, some 6 us of them for the shares of dw (456
@@ -31,85 +24,19 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "f8_common.cuh"
+#include "norm_common.cuh"
 #include "norm_shape.h"
-#include "ptx.cuh"
 
 namespace mmagb {
 namespace {
 
-// Sum of two values over the block, the same in every thread.  `buf` holds
-// 64 floats; calls in turn use different buffers, so one barrier is enough.
-// VOTE: *any becomes whether any thread's is set.
-template <bool VOTE = false>
-__device__ __forceinline__ float2 block_sum2(float a, float b, float2* buf,
-                                             bool* any = nullptr) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, d);
-    b += __shfl_xor_sync(0xffffffffu, b, d);
-  }
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) {
-    if constexpr (VOTE) *any = __any_sync(0xffffffffu, *any);
-    return make_float2(a, b);
-  }
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
-  if constexpr (VOTE)
-    *any = __syncthreads_or(*any);
-  else
-    __syncthreads();
-  // every thread adds the warps' sums in their order (independent reads; a
-  // second tree of shuffles took longer)
-  a = 0.f;
-  b = 0.f;
-#pragma unroll 4
-  for (int w = 0; w < warps; ++w) {
-    a += buf[w].x;
-    b += buf[w].y;
-  }
-  return make_float2(a, b);
-}
-
-// The weights of vector v: of the input's type or FP32.
-template <class T>
-__device__ __forceinline__ void load_weight(const void* W, bool w32, int64_t v,
-                                            int64_t n, float (&f)[Vec<T>::kN]) {
-  constexpr int E = Vec<T>::kN;
-  if (!w32) {
-    load_row(static_cast<const T*>(W), v, n, f);
-  } else {
-#pragma unroll
-    for (int j = 0; j < E / 4; ++j) {
-      float t[4];
-      load_row(static_cast<const float*>(W), v * (E / 4) + j, n, t);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[4 * j + i] = t[i];
-    }
-  }
-}
-
-// The bias, or zeros where there is none.
-template <class T>
-__device__ __forceinline__ void load_bias(const void* B, bool w32, int64_t v,
-                                          int64_t n, float (&f)[Vec<T>::kN]) {
-  if (B) {
-    load_weight<T>(B, w32, v, n, f);
-  } else {
-#pragma unroll
-    for (int j = 0; j < Vec<T>::kN; ++j) f[j] = 0.f;
-  }
-}
-
-// CENTRE: the layer norm, else the root-mean-square norm.
 // Rows b, b + gridDim.x, ... per block, a row at a time: VPT 16-byte vectors
 // per thread stay in registers between the sum of squares and the output,
 // and the next row's loads are issued before this row's sum is exchanged.
-template <class T, int VPT, int MAXT, bool TAIL, bool CENTRE>
+template <class T, int VPT, int MAXT, bool TAIL>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1)
     rmsnorm_kernel(const NormProblem p, bool w32) {
   constexpr int E = Vec<T>::kN;
-  constexpr int kLanes = kScaleBlock / E;  // lanes that share a block
   __shared__ float2 red[2][32];
   const T* const X = static_cast<const T*>(p.X);
   const T* const R = static_cast<const T*>(p.R);
@@ -139,106 +66,27 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1)
 #pragma unroll
         for (int j = 0; j < E; ++j) h[i][j] += t[j];
       }
-      const int64_t v = threadIdx.x + i * blockDim.x;
-      if constexpr (TAIL) clear_tail<T>(v, n, h[i]);
-      if constexpr (CENTRE) {
-        if (p.H && v * E < n)
-          store_row<T, TAIL>(static_cast<T*>(p.H) + row * p.ldh, v, n, h[i]);
+      if constexpr (TAIL) clear_tail<T>(threadIdx.x + i * blockDim.x, n, h[i]);
 #pragma unroll
-        for (int j = 0; j < E; ++j) ss += h[i][j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < E; ++j) ss = fmaf(h[i][j], h[i][j], ss);
-      }
+      for (int j = 0; j < E; ++j) ss = fmaf(h[i][j], h[i][j], ss);
     }
     if (row + gridDim.x < p.M) fetch(row + gridDim.x);
-    if constexpr (CENTRE) {
-      // the variance from the distances to the mean: a difference of two sums
-      // of squares would lose it where the mean is large
-      const float mean = block_sum2(ss, 0.f, red[0]).x / float(n);
-      ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int64_t v = threadIdx.x + i * blockDim.x;
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          // (vectors past the row hold zeros)
-          h[i][j] = v * E + (TAIL ? j : 0) < n ? h[i][j] - mean : 0.f;
-          ss = fmaf(h[i][j], h[i][j], ss);
-        }
-      }
-      ss = block_sum2(ss, 0.f, red[1]).x;
-    } else {
-      ss = block_sum2(ss, 0.f, red[flip]).x;
-    }
+    ss = block_sum2(ss, 0.f, red[flip]).x;
     const float rstd = __frsqrt_rn(ss / float(n) + p.eps);
-    // y replaces h; m: the largest magnitude of each vector's scale block
-    float m[VPT];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int64_t v = threadIdx.x + i * blockDim.x;
-      const bool live = v * E < n;
-      if (!CENTRE && p.H && live)
-        store_row<T, TAIL>(static_cast<T*>(p.H) + row * p.ldh, v, n, h[i]);
-      float w[E], b[E];
-      load_weight<T>(p.W, w32, v, n, w);
-      if constexpr (CENTRE) load_bias<T>(p.B, w32, v, n, b);
-      m[i] = 0.f;
-#pragma unroll
-      for (int j = 0; j < E; j += 2) {
-        float2 y = __fmul2_rn(make_float2(h[i][j], h[i][j + 1]), make_float2(rstd, rstd));
-        if constexpr (CENTRE)
-          y = __ffma2_rn(y, make_float2(w[j], w[j + 1]), make_float2(b[j], b[j + 1]));
-        else
-          y = __fmul2_rn(y, make_float2(w[j], w[j + 1]));
-        // columns past the end (rstd may be infinite or NaN) do not count
-        h[i][j] = TAIL && v * E + j >= n ? 0.f : y.x;
-        h[i][j + 1] = TAIL && v * E + j + 1 >= n ? 0.f : y.y;
-        m[i] = abs_max(m[i], h[i][j], h[i][j + 1]);
-      }
-      if (!live) m[i] = 0.f;
-      if (p.Y && live)
-        store_row<T, TAIL>(static_cast<T*>(p.Y) + row * p.ldy, v, n, h[i]);
-    }
-    if (p.Q) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int d = kLanes / 2; d > 0; d >>= 1)
-          m[i] = abs_max(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
-      // the thread's VPT scales and their reciprocals, each made by another
-      // lane of the block's group
-      const int mine = threadIdx.x % kLanes % 4;
-      float mm = m[0];
-#pragma unroll
-      for (int i = 1; i < VPT; ++i) mm = mine == i ? m[i] : mm;
-      const float s = block_scale<false>(mm, p.pow2);
-      const Divisor by(s);
-      const int lane0 = threadIdx.x & 31 & ~(kLanes - 1);
-      if (threadIdx.x % kLanes < VPT) {
-        const int64_t b = (threadIdx.x + int64_t(mine) * blockDim.x) / kLanes;
-        if (b * kScaleBlock < n) p.S[row * p.s_row + b * p.s_blk] = s;
-      }
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int64_t v = threadIdx.x + i * blockDim.x;
-        const Divisor d = by.from(lane0 + i);
-        if (v * E < n)
-          store_f8<false, E, TAIL>(static_cast<uint8_t*>(p.Q) + row * p.ldq, v, n,
-                                   h[i], d);
-      }
-    }
+    norm_out<T, VPT, TAIL, false, true>(
+        p, row, h, rstd, [&](int, int64_t v, float (&w)[E], float (&)[E]) {
+          load_weight<T>(p.W, w32, v, n, w);
+        });
   }
 }
 
 // Rows wider than the registers hold: one row per block, read twice.
-// (CENTRE: three times)
-template <class T, bool CENTRE>
+template <class T>
 __global__ void __launch_bounds__(1024)
     rmsnorm_wide_kernel(const NormProblem p, bool w32) {
   constexpr int E = Vec<T>::kN;
   constexpr int kLanes = kScaleBlock / E;
-  __shared__ float2 red[CENTRE ? 2 : 1][32];
+  __shared__ float2 red[32];
   const int64_t row = blockIdx.x, n = p.N;
   const T* x = static_cast<const T*>(p.X) + row * p.ldx;
   const T* r = p.R ? static_cast<const T*>(p.R) + row * p.ldr : nullptr;
@@ -253,40 +101,25 @@ __global__ void __launch_bounds__(1024)
     }
   };
   const int64_t vectors = (n + E - 1) / E;
-  float ss = 0.f, mean = 0.f;
-  if constexpr (CENTRE) {
-    for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
-      load(v);
-#pragma unroll
-      for (int j = 0; j < E; ++j) mean += h[j];
-    }
-    mean = block_sum2(mean, 0.f, red[1]).x / float(n);
-  }
+  float ss = 0.f;
   for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
     load(v);
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      if constexpr (CENTRE) h[j] = v * E + j < n ? h[j] - mean : 0.f;
-      ss = fmaf(h[j], h[j], ss);
-    }
+    for (int j = 0; j < E; ++j) ss = fmaf(h[j], h[j], ss);
   }
-  ss = block_sum2(ss, 0.f, red[0]).x;
+  ss = block_sum2(ss, 0.f, red).x;
   const float rstd = __frsqrt_rn(ss / float(n) + p.eps);
   // whole warps take part in the block maxima: round up to the block
   for (int64_t v = threadIdx.x; v < (vectors + 31) / 32 * 32; v += blockDim.x) {
     load(v);
     const bool live = v < vectors;
     if (p.H && live) store_row(static_cast<T*>(p.H) + row * p.ldh, v, n, h);
-    float y[E], b[E];
+    float y[E];
     load_weight<T>(p.W, w32, v, n, y);
-    if constexpr (CENTRE) load_bias<T>(p.B, w32, v, n, b);
     float m = 0.f;
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      if constexpr (CENTRE)
-        y[j] = v * E + j < n ? fmaf((h[j] - mean) * rstd, y[j], b[j]) : 0.f;
-      else
-        y[j] = v * E + j < n ? h[j] * rstd * y[j] : 0.f;
+      y[j] = v * E + j < n ? h[j] * rstd * y[j] : 0.f;
       m = abs_max(m, y[j]);
     }
     if (p.Y && live) store_row(static_cast<T*>(p.Y) + row * p.ldy, v, n, y);
@@ -309,10 +142,8 @@ __global__ void __launch_bounds__(1024)
 // its share of dw stays in registers.  That goes to row b of `part` at the
 // end; the shares are added in a fixed order by sum_parts_kernel, so the
 // result does not change from run to run.
-// CENTRE: a third reading between the two, of the distances to the mean, and
-// shares of db beside those of dw (row b of part: n of dw, n of db).
-template <class T, int VPT, bool TAIL, bool CENTRE>
-__global__ void __launch_bounds__(512, VPT <= (CENTRE ? 1 : 2) ? 2 : 1)
+template <class T, int VPT, bool TAIL>
+__global__ void __launch_bounds__(512, VPT <= 2 ? 2 : 1)
     rmsnorm_backward_kernel(const NormBackProblem p, bool w32, int stages,
                             int row_bytes, float* __restrict__ part,
                             unsigned* status, const WaitHook hook) {
@@ -346,14 +177,10 @@ __global__ void __launch_bounds__(512, VPT <= (CENTRE ? 1 : 2) ? 2 : 1)
     for (int s = 0; s < stages; ++s)
       fetch(blockIdx.x + int64_t(s) * gridDim.x, s);
   float dw[VPT][E];
-  [[maybe_unused]] float db[CENTRE ? VPT : 1][E];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      dw[i][j] = 0.f;
-      if constexpr (CENTRE) db[i][j] = 0.f;
-    }
+    for (int j = 0; j < E; ++j) dw[i][j] = 0.f;
   // vector v of a row in the ring
   auto load = [&](const uint8_t* row, int v, float (&f)[E]) {
     Vec<T>::unpack(*(reinterpret_cast<const uint4*>(row) + v), f);
@@ -395,16 +222,11 @@ __global__ void __launch_bounds__(512, VPT <= (CENTRE ? 1 : 2) ? 2 : 1)
       weight(i, v, w);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        if constexpr (CENTRE) {
-          ss += h[j];
-          gh = fmaf(dy[j], w[j], gh);
-        } else {
-          ss = fmaf(h[j], h[j], ss);
-          gh = fmaf(dy[j] * w[j], h[j], gh);
-        }
+        ss = fmaf(h[j], h[j], ss);
+        gh = fmaf(dy[j] * w[j], h[j], gh);
       }
     }
-    float2 sum = block_sum2<true>(ss, gh, red[CENTRE ? 0 : flip], &failed);
+    const float2 sum = block_sum2<true>(ss, gh, red[flip], &failed);
     if (failed) {
       // the loads of this row and of those ahead (all but the one that would be
       // fetched below)
@@ -420,29 +242,6 @@ __global__ void __launch_bounds__(512, VPT <= (CENTRE ? 1 : 2) ? 2 : 1)
     // `stages` rows after it.
     if (threadIdx.x == 0 && row != blockIdx.x)
       fetch(row + int64_t(stages - 1) * gridDim.x, s == 0 ? stages - 1 : s - 1);
-    [[maybe_unused]] float mean = 0.f, mean_g = 0.f;
-    if constexpr (CENTRE) {
-      mean = sum.x / float(n);
-      mean_g = sum.y / float(n);
-      ss = 0.f;
-      gh = 0.f;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (v >= vectors) continue;
-        float h[E], dy[E], w[E];
-        load(hs, v, h);
-        load(ds, v, dy);
-        weight(i, v, w);
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const float c = TAIL && v * E + j >= n ? 0.f : h[j] - mean;
-          ss = fmaf(c, c, ss);
-          gh = fmaf(fmaf(dy[j], w[j], -mean_g), c, gh);
-        }
-      }
-      sum = block_sum2(ss, gh, red[1]);
-    }
     const float rstd = __frsqrt_rn(sum.x * over_n + p.eps);
     // (rstd^3 by itself leaves the range of FP32 at rms of 2^42 and 2^-42)
     const float c = -(sum.y * over_n) * rstd * rstd * rstd;
@@ -456,16 +255,9 @@ __global__ void __launch_bounds__(512, VPT <= (CENTRE ? 1 : 2) ? 2 : 1)
       weight(i, v, w);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        if constexpr (CENTRE) {
-          const float x = h[j] - mean;
-          dw[i][j] = fmaf(dy[j] * rstd, x, dw[i][j]);
-          db[i][j] += dy[j];
-          o[j] = fmaf(fmaf(dy[j], w[j], -mean_g), rstd, c * x);
-        } else {
-          const float d = dy[j] * rstd;
-          dw[i][j] = fmaf(d, h[j], dw[i][j]);
-          o[j] = fmaf(d, w[j], c * h[j]);
-        }
+        const float d = dy[j] * rstd;
+        dw[i][j] = fmaf(d, h[j], dw[i][j]);
+        o[j] = fmaf(d, w[j], c * h[j]);
       }
       if (p.R) {
         float r[E];
@@ -482,28 +274,25 @@ __global__ void __launch_bounds__(512, VPT <= (CENTRE ? 1 : 2) ? 2 : 1)
     flip ^= 1;
   }
   grid_dependents_start();
-  float* mine = part + int64_t(blockIdx.x) * n * (CENTRE ? 2 : 1);
+  float* mine = part + int64_t(blockIdx.x) * n;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int64_t at = int64_t(threadIdx.x + i * blockDim.x) * E;
 #pragma unroll
     for (int j = 0; j < E; ++j)
-      if (at + j < n) {
-        mine[at + j] = dw[i][j];
-        if constexpr (CENTRE) mine[n + at + j] = db[i][j];
-      }
+      if (at + j < n) mine[at + j] = dw[i][j];
   }
 }
 
 // Rows too wide for that: read twice, dw added up in `part`.
-template <class T, bool CENTRE>
+template <class T>
 __global__ void __launch_bounds__(1024)
     rmsnorm_backward_wide_kernel(const NormBackProblem p, bool w32,
                                  float* __restrict__ part) {
   constexpr int E = Vec<T>::kN;
   __shared__ float2 red[2][32];
   const int64_t n = p.N, vectors = (n + E - 1) / E;
-  float* mine = part + int64_t(blockIdx.x) * n * (CENTRE ? 2 : 1);
+  float* mine = part + int64_t(blockIdx.x) * n;
   float dy[E], h[E], w[E];
   int flip = 0;
   for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, flip ^= 1) {
@@ -512,36 +301,16 @@ __global__ void __launch_bounds__(1024)
       load_row(static_cast<const T*>(p.DY) + row * p.lddy, v, n, dy);
       load_weight<T>(p.W, w32, v, n, w);
     };
-    float ss = 0.f, gh = 0.f, mean = 0.f, mean_g = 0.f;
-    if constexpr (CENTRE) {
-      for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
-        load(v);
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          ss += h[j];
-          gh = fmaf(dy[j], w[j], gh);
-        }
-      }
-      const float2 s = block_sum2(ss, gh, red[1]);
-      mean = s.x / float(n);
-      mean_g = s.y / float(n);
-      ss = 0.f;
-      gh = 0.f;
-    }
+    float ss = 0.f, gh = 0.f;
     for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
       load(v);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        if constexpr (CENTRE) {
-          h[j] = v * E + j < n ? h[j] - mean : 0.f;
-          gh = fmaf(fmaf(dy[j], w[j], -mean_g), h[j], gh);
-        } else {
-          gh = fmaf(dy[j] * w[j], h[j], gh);
-        }
         ss = fmaf(h[j], h[j], ss);
+        gh = fmaf(dy[j] * w[j], h[j], gh);
       }
     }
-    const float2 s = block_sum2(ss, gh, red[CENTRE ? 0 : flip]);
+    const float2 s = block_sum2(ss, gh, red[flip]);
     const float rstd = __frsqrt_rn(s.x / float(n) + p.eps);
     const float c = s.y / float(n) * rstd * rstd * rstd;
     for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
@@ -550,55 +319,14 @@ __global__ void __launch_bounds__(1024)
       if (p.R) load_row(static_cast<const T*>(p.R) + row * p.ldr, v, n, r);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        const int64_t at = v * E + j;
         const float d = dy[j] * rstd;
-        if constexpr (CENTRE) {
-          h[j] -= mean;
-          o[j] = fmaf(fmaf(dy[j], w[j], -mean_g), rstd, -c * h[j]) + (p.R ? r[j] : 0.f);
-          if (at < n) mine[n + at] = dy[j] + (row == blockIdx.x ? 0.f : mine[n + at]);
-        } else {
-          o[j] = fmaf(d, w[j], -c * h[j]) + (p.R ? r[j] : 0.f);
-        }
+        o[j] = fmaf(d, w[j], -c * h[j]) + (p.R ? r[j] : 0.f);
+        const int64_t at = v * E + j;
         if (at < n)
           mine[at] = fmaf(d, h[j], row == blockIdx.x ? 0.f : mine[at]);
       }
       store_row(static_cast<T*>(p.DX) + row * p.lddx, v, n, o);
     }
-  }
-}
-
-// out[n] = sum of part[g][n] over g (of the columns from n1 on to out1): 32 columns per block, 32 rows of
-// threads that each add up every 32nd part, two loads at once (more got in
-// each other's way: backward pass of 8190 x 5000 62.7 us, four 63.7, sixteen
-// 69.9).  Starts beside the end of the kernel that makes the parts.
-__global__ void __launch_bounds__(1024)
-    sum_parts_kernel(const float* __restrict__ part, int parts, int64_t n,
-                     float* __restrict__ out, int64_t n1, float* __restrict__ out1) {
-  __shared__ float t[32][33];
-  const int64_t col = int64_t(blockIdx.x) * 32 + threadIdx.x;
-  float s = 0.f;
-  grid_dependency_wait();
-  for (int from = threadIdx.y; from < parts; from += 2 * 32) {
-    float v[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int g = from + i * 32;
-      v[i] = g < parts && col < n ? part[g * n + col] : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) s += v[i];
-  }
-  t[threadIdx.y][threadIdx.x] = s;
-  __syncthreads();
-  s = t[threadIdx.x][threadIdx.y];
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-  const int64_t c = int64_t(blockIdx.x) * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && c < n) {
-    if (c < n1)
-      out[c] = s;
-    else
-      out1[c - n1] = s;
   }
 }
 
@@ -622,7 +350,7 @@ bool with_shape(int64_t vectors, F&& f) {
   return false;
 }
 
-template <class T, bool CENTRE>
+template <class T>
 mma_status_t forward(const Ctx& ctx, const NormProblem& p, bool w32) {
   constexpr int E = Vec<T>::kN;
   const int64_t vectors = (p.N + E - 1) / E;
@@ -632,9 +360,9 @@ mma_status_t forward(const Ctx& ctx, const NormProblem& p, bool w32) {
     const int64_t most = int64_t(ctx.num_sms) * (768 / threads + (threads > 768));
     const unsigned grid = unsigned(std::min(p.M, most));
     if (p.N % E)
-      rmsnorm_kernel<T, V, B, true, CENTRE><<<grid, threads, 0, ctx.stream>>>(p, w32);
+      rmsnorm_kernel<T, V, B, true><<<grid, threads, 0, ctx.stream>>>(p, w32);
     else
-      rmsnorm_kernel<T, V, B, false, CENTRE><<<grid, threads, 0, ctx.stream>>>(p, w32);
+      rmsnorm_kernel<T, V, B, false><<<grid, threads, 0, ctx.stream>>>(p, w32);
   };
   bool fits = true;
   if (p.M <= ctx.num_sms && vectors <= 1024)
@@ -644,17 +372,17 @@ mma_status_t forward(const Ctx& ctx, const NormProblem& p, bool w32) {
   else
     fits = with_shape(vectors, launch);
   if (!fits)
-    rmsnorm_wide_kernel<T, CENTRE><<<unsigned(p.M), 1024, 0, ctx.stream>>>(p, w32);
+    rmsnorm_wide_kernel<T><<<unsigned(p.M), 1024, 0, ctx.stream>>>(p, w32);
   return cudaGetLastError() == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
 }
 
-template <class T, bool CENTRE>
+template <class T>
 mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32,
                       float* part, WaitHook hook = WaitHook{kWaitLimitNs, 0}) {
   constexpr int E = Vec<T>::kN;
   const int64_t vectors = (p.N + E - 1) / E;
   const int tensors = p.R ? 3 : 2;
-  const NormBackShape shape = norm_back_shape(vectors, tensors, CENTRE);
+  const NormBackShape shape = norm_back_shape(vectors, tensors);
   const int vpt = shape.vpt;
   const int at_once = (vpt ? shape.per_sm : 3) * ctx.num_sms;
   const int grid = int(std::min<int64_t>(p.M, std::min(kMostParts, at_once)));
@@ -676,31 +404,17 @@ mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32,
     static PerContext<bool> a1, a2, a4;
     static PerContext<bool> t1, t2, t4;
     const bool ok =
-        p.N % E ? vpt == 1   ? run(rmsnorm_backward_kernel<T, 1, true, CENTRE>, t1)
-                  : vpt == 2 ? run(rmsnorm_backward_kernel<T, 2, true, CENTRE>, t2)
-                             : run(rmsnorm_backward_kernel<T, 4, true, CENTRE>, t4)
-        : vpt == 1 ? run(rmsnorm_backward_kernel<T, 1, false, CENTRE>, a1)
-        : vpt == 2 ? run(rmsnorm_backward_kernel<T, 2, false, CENTRE>, a2)
-                   : run(rmsnorm_backward_kernel<T, 4, false, CENTRE>, a4);
+        p.N % E ? vpt == 1   ? run(rmsnorm_backward_kernel<T, 1, true>, t1)
+                  : vpt == 2 ? run(rmsnorm_backward_kernel<T, 2, true>, t2)
+                             : run(rmsnorm_backward_kernel<T, 4, true>, t4)
+        : vpt == 1 ? run(rmsnorm_backward_kernel<T, 1, false>, a1)
+        : vpt == 2 ? run(rmsnorm_backward_kernel<T, 2, false>, a2)
+                   : run(rmsnorm_backward_kernel<T, 4, false>, a4);
     if (!ok) return MMA_ERR_LAUNCH;
   } else if (grid > 0) {
-    rmsnorm_backward_wide_kernel<T, CENTRE><<<grid, 1024, 0, ctx.stream>>>(p, w32, part);
+    rmsnorm_backward_wide_kernel<T><<<grid, 1024, 0, ctx.stream>>>(p, w32, part);
   }
-  cudaLaunchConfig_t cfg = {};
-  const int64_t columns = p.N * (CENTRE ? 2 : 1);
-  cfg.gridDim = dim3(unsigned((columns + 31) / 32), 1, 1);
-  cfg.blockDim = dim3(32, 32, 1);
-  cfg.stream = ctx.stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e =
-      cudaLaunchKernelEx(&cfg, sum_parts_kernel, static_cast<const float*>(part), grid,
-                         columns, p.DW, p.N, p.DB);
-  const cudaError_t last = cudaGetLastError();
-  return e == cudaSuccess && last == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
+  return sum_parts(ctx, part, grid, p.N, p.DW, p.N, nullptr);
 }
 
 }  // namespace
@@ -708,18 +422,9 @@ mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32,
 mma_status_t launch_rmsnorm(const Ctx& ctx, const NormProblem& p) {
   const bool w32 = p.w_type == MMA_F32;
   switch (p.type) {
-    case MMA_BF16: return forward<__nv_bfloat16, false>(ctx, p, w32);
-    case MMA_F16: return forward<__half, false>(ctx, p, w32);
-    default: return forward<float, false>(ctx, p, false);
-  }
-}
-
-mma_status_t launch_layernorm(const Ctx& ctx, const NormProblem& p) {
-  const bool w32 = p.w_type == MMA_F32;
-  switch (p.type) {
-    case MMA_BF16: return forward<__nv_bfloat16, true>(ctx, p, w32);
-    case MMA_F16: return forward<__half, true>(ctx, p, w32);
-    default: return forward<float, true>(ctx, p, false);
+    case MMA_BF16: return forward<__nv_bfloat16>(ctx, p, w32);
+    case MMA_F16: return forward<__half>(ctx, p, w32);
+    default: return forward<float>(ctx, p, false);
   }
 }
 
@@ -727,8 +432,8 @@ mma_status_t launch_rmsnorm_abort_selftest(const Ctx& ctx, int64_t limit_ns, con
                                            void* DX, float* DW, void* workspace) {
   const NormBackProblem p = {MMA_BF16, MMA_BF16, 1024, 1024, X, 1024, X, 1024, X, 1e-6f,
                              nullptr, 0, DX, 1024, DW, nullptr};
-  return backward<__nv_bfloat16, false>(ctx, p, false, static_cast<float*>(workspace),
-                                        WaitHook{static_cast<unsigned long long>(limit_ns), 1});
+  return backward<__nv_bfloat16>(ctx, p, false, static_cast<float*>(workspace),
+                                 WaitHook{static_cast<unsigned long long>(limit_ns), 1});
 }
 
 int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t N) {
@@ -740,20 +445,9 @@ mma_status_t launch_rmsnorm_backward(const Ctx& ctx, const NormBackProblem& p,
   const bool w32 = p.w_type == MMA_F32;
   float* part = static_cast<float*>(workspace);
   switch (p.type) {
-    case MMA_BF16: return backward<__nv_bfloat16, false>(ctx, p, w32, part);
-    case MMA_F16: return backward<__half, false>(ctx, p, w32, part);
-    default: return backward<float, false>(ctx, p, false, part);
-  }
-}
-
-mma_status_t launch_layernorm_backward(const Ctx& ctx, const NormBackProblem& p,
-                                       void* workspace) {
-  const bool w32 = p.w_type == MMA_F32;
-  float* part = static_cast<float*>(workspace);
-  switch (p.type) {
-    case MMA_BF16: return backward<__nv_bfloat16, true>(ctx, p, w32, part);
-    case MMA_F16: return backward<__half, true>(ctx, p, w32, part);
-    default: return backward<float, true>(ctx, p, false, part);
+    case MMA_BF16: return backward<__nv_bfloat16>(ctx, p, w32, part);
+    case MMA_F16: return backward<__half>(ctx, p, w32, part);
+    default: return backward<float>(ctx, p, false, part);
   }
 }
 

@@ -244,3 +244,51 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         assert torch.equal(y, mma.layernorm(x, w)[0])
         assert all(torch.equal(a, b) for a, b in zip(grads, mma.layernorm_backward(dy, x, w)))
+
+
+@pytest.mark.parametrize("t,n", [("f32", 4096), ("bf16", 4096), ("f32", 5003), ("f16", 264), ("bf16", 10000)])
+def test_many_rows_of_every_kind(t, n):
+    """Rows in turn per block: far from zero, with the 32 elements that a row is
+    sampled at far from the others, without deviation, with
+    infinities.  The samples' mean is then far from the row's, and both the
+    variance and the gradient's sums have to be those about the row's own mean."""
+    m = 700
+    h = rnd(n, m, n)
+    q = n // 32
+    at = torch.arange(32) * q + 2 * torch.arange(32) % q
+    h[1::7] += 300.0
+    for i in range(2, m, 7):
+        h[i, at] += 1000.0
+    h[3::7] = 0.0
+    h[3::7, at[:9]] = 200.0
+    h[4::7] = 7.0
+    h[5::28, 3] = float("inf")
+    h[12::28, n - 1] = float("nan")
+    x = rows16(h, T[t])
+    w, b = (1 + 0.3 * rnd(3, n)).to(T[t]).cuda(), rnd(4, n).to(T[t]).cuda()
+    y, _ = mma.layernorm(x, w, b)
+    bad = ~host(x).isfinite().all(1)
+    assert bool(host(y)[bad].isnan().all())
+    good = ~bad
+    want, tol = want_y(host(x)[good], host(w), host(b), 1e-5)
+    err = (host(y)[good] - want).abs()
+    bound = (want.abs() + tol) * U[t] + tol
+    assert bool((err <= bound).all()), float((err / bound).max())
+    dy = rows16(rnd(5, m, n), T[t])
+    dx, _, _ = mma.layernorm_backward(dy, x, w)
+    assert bool(host(dx)[bad].isnan().all())
+    flat = torch.zeros(m, dtype=torch.bool)
+    flat[4::7] = True  # (no deviation: the factor is 1 / sqrt(eps), of rounded means)
+    keep = good & ~flat
+    want, tol, *_ = want_back(host(dy)[keep], host(x)[keep], host(w), torch.zeros(1, dtype=torch.float64), 1e-5)
+    err = (host(dx)[keep] - want).abs()
+    bound = (want.abs() + tol) * U[t] + tol
+    assert bool((err <= bound).all()), float((err / bound).max())
+    assert bool(host(dx)[good & flat].isfinite().all())
+    # the weights' gradient over the rows without infinities
+    rows = good.nonzero()[:, 0].cuda()
+    xs, ds = rows16(host(x)[good], T[t]), rows16(host(dy)[good], T[t])
+    _, dw, db = mma.layernorm_backward(ds, xs, w)
+    _, _, dw64, dw_tol, db64, db_tol = want_back(host(ds), host(xs), host(w), torch.zeros(1, dtype=torch.float64), 1e-5)
+    assert rows.numel() == xs.shape[0]
+    assert bool(((host(dw) - dw64).abs() <= dw_tol).all()) and bool(((host(db) - db64).abs() <= db_tol).all())
