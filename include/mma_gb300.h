@@ -625,6 +625,65 @@ mma_status_t mma_gemm_grouped_f8(int type_a, int type_b, int type_d,
                                  const void *C, int64_t ldc, void *D,
                                  int64_t ldd, void *stream);
 
+/*
+ * mma_route -- the router of a layer of experts.  Of each of T tokens' E logits
+ * the k largest (of equal ones the lowest index) are its choices:
+ *
+ *     p = softmax(x) in FP32,  weights[t][j] = p of choice j, with `normalize`
+ *     over the sum of the token's chosen p
+ *     experts[t][j]  its expert, the best first
+ *     offsets[e]     choices of the experts before e (E + 1 of them): the row
+ *                    ranges of mma_gemm_grouped
+ *     order[i]       the choice (t * k + j) at place i when the choices are
+ *                    sorted by expert, within an expert by token
+ *     place[t][j]    the place of that choice: order's inverse
+ *     share[e]       mean of p_e over the tokens
+ *     loss           E * sum over e of share[e] * (choices of e) / (tokens * k)
+ *
+ * type     : MMA_F16, MMA_BF16 or MMA_F32, of X (T x E, rows ldx apart, aligned to
+ *            one element); E at most MMA_MAX_GROUPS, k at most MMA_MAX_CHOICES,
+ *            T * k at most 2^30 (more: MMA_ERR_UNSUPPORTED).
+ * mask     : T bytes or NULL; a token with 0 takes no part in anything.
+ * tokens   : one int32, how many tokens take part.
+ * An expert whose logit is -inf is not chosen.  Where no expert is left, and for a
+ * masked token, experts is -1 and the weight 0; such choices stand behind
+ * offsets[E] in `order`, so that it is a permutation whatever the mask.  Without
+ * tokens share and loss are 0.  A NaN or +inf in a token's logits makes its
+ * weights, share and loss NaN, its choices being experts all the same.
+ * All outputs are contiguous device memory, the same bits from run to run.
+ * workspace: device memory, 4-byte aligned, of mma_route_workspace(T, E) bytes (0
+ * up to 256 tokens), which the call's work on `stream` uses and nothing else may
+ * meanwhile.
+ */
+#define MMA_MAX_CHOICES 32
+int64_t mma_route_workspace(int64_t T, int64_t E);
+mma_status_t mma_route(int type, int64_t T, int64_t E, int64_t k, const void *X,
+                       int64_t ldx, const uint8_t *mask, int normalize,
+                       float *weights, int32_t *experts, int32_t *order,
+                       int32_t *place, int32_t *offsets, float *share,
+                       float *loss, int32_t *tokens, void *workspace,
+                       int64_t workspace_bytes, void *stream);
+
+/*
+ * mma_route_backward -- gradient of the logits from DW (T x k, of the weights) and
+ * DLOSS (one value in device memory, of the loss), either of which may be NULL:
+ *
+ *     a_e = DLOSS * E * (choices of e) / (tokens^2 * k)
+ *     DX = p (a - sum p a), and at the chosen  w (DW - sum over chosen w DW)
+ *
+ * (without normalize p (a + DW - sum p (a + DW)), DW standing at the chosen), the
+ * choices and their numbers being taken as given.  weights, experts, offsets and
+ * tokens are mma_route's; those of NULL gradients may be NULL.  DX (T x E of X's
+ * type) may be X; a masked token's row is 0.
+ */
+mma_status_t mma_route_backward(int type, int64_t T, int64_t E, int64_t k,
+                                const void *X, int64_t ldx, const uint8_t *mask,
+                                int normalize, const float *weights,
+                                const int32_t *experts, const int32_t *offsets,
+                                const int32_t *tokens, const float *DW,
+                                const float *DLOSS, void *DX, int64_t lddx,
+                                void *stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *mma_status_string(int status);
 

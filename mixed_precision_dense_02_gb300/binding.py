@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import Any, NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIBNAME = "libmma_gb300.so"
@@ -70,6 +71,11 @@ SIGNATURES = {
                                    _p, _i64, _p, _i64, _i64, _p, _i64, _i64,
                                    _p, _int, _i64, _i64, _i64, _p, _p, _i64,
                                    _p, _i64, _p]),
+    "mma_route": (_int, [_int, _i64, _i64, _i64, _p, _i64, _p, _int, _p, _p, _p,
+                         _p, _p, _p, _p, _p, _p, _i64, _p]),
+    "mma_route_workspace": (_i64, [_i64, _i64]),
+    "mma_route_backward": (_int, [_int, _i64, _i64, _i64, _p, _i64, _p, _int, _p,
+                                  _p, _p, _p, _p, _p, _p, _i64, _p]),
     "mma_device_status": (_int, [_p]),
     "mma_selftest_wait_timeout": (_int, [_i64, _p]),
     "mma_selftest_gemm_abort": (_int, [_int, _i64, _p, _p, _p, _p]),
@@ -968,6 +974,137 @@ def gemm_grouped_f8(A, SA, B, SB, offsets, C=None, D=None, *, out_dtype=None,
     if st:
         _check("mma_gemm_grouped_f8", st)
     return D
+
+
+# --------------------------------------------------------------------------
+# the router of a layer of experts
+
+class Routing(NamedTuple):
+    """What ``route`` returns (tensors on the GPU, T tokens, k choices each)."""
+
+    weights: Any  # (T, k) float32, 0 where there is no expert
+    experts: Any  # (T, k) int32, the best first, -1: none
+    order: Any    # (T * k,) int32, the choices t * k + j sorted by expert
+    place: Any    # (T, k) int32, each choice's place in `order`
+    offsets: Any  # (E + 1,) int32, expert e has the places offsets[e] to offsets[e + 1]
+    share: Any    # (E,) float32, mean probability of each expert
+    loss: Any     # () float32, the balance loss
+    tokens: Any   # () int32, tokens that take part
+
+
+def _mask(mask, T):
+    torch = _torch()
+    if mask is not None:
+        _take("mask", mask, {torch.bool: 1}, T)
+        if T > 1 and mask.stride(0) != 1:
+            raise ValueError("mask must be contiguous")
+
+
+def _row_stride(name, t) -> int:
+    """Leading dimension of a matrix of contiguous rows of any alignment."""
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _plan_route(logits, k, mask):
+    code = _take("logits", logits, _kinds()["wide"], None, None)
+    T, E = logits.shape
+    if not 1 <= k <= E:
+        raise ValueError(f"k must be between 1 and {E}, not {k}")
+    _mask(mask, T)
+    return (code, T, E, _row_stride("logits", logits),
+            load().mma_route_workspace(T, E) // 4, _one_device(logits, mask))
+
+
+def route(logits, k: int, *, mask=None, normalize: bool = True, stream=None) -> Routing:
+    """The router of a layer of experts.
+
+    ``logits``: (T, E) float32, float16 or bfloat16.  A token's choices are its k
+    largest logits (of equal ones the lowest index), weighted by their softmax
+    probabilities, with ``normalize`` over the sum of the chosen ones.  ``mask``:
+    (T,) bool, False for tokens that take no part (padding).  Returns a
+    ``Routing``: weights and experts, the choices sorted by expert for
+    ``gemm_grouped`` (``order``, ``place``, ``offsets``), the experts' mean
+    probabilities and the balance loss ``E * sum(share * counts) / (tokens * k)``.
+    """
+    torch = _torch()
+    k = int(k)
+    code, T, E, ldx, need, index = _plan(
+        ("route", _key(logits), _key(mask), k), _plan_route, logits, k, mask)
+    if stream is not None:
+        return _under(stream, index, route, logits, k, mask=mask, normalize=normalize)
+    device = logits.device
+    # two allocations, cut up: this call serves single tokens too
+    ints = torch.empty((3 * T * k + E + 2 + need,), dtype=torch.int32, device=device)
+    floats = torch.empty((T * k + E + 1,), dtype=torch.float32, device=device)
+    n = T * k
+    experts, order, place, offsets, tokens, ws = ints.split((n, n, n, E + 1, 1, need))
+    weights, share, loss = floats.split((n, E, 1))
+    at, fat = ints.data_ptr(), floats.data_ptr()
+    st = load().mma_route(
+        code, T, E, k, logits.data_ptr(), ldx, None if mask is None else mask.data_ptr(),
+        1 if normalize else 0, fat, at, at + 4 * n, at + 8 * n, at + 12 * n,
+        fat + 4 * n, fat + 4 * (n + E), at + 4 * (3 * n + E + 1),
+        at + 4 * (3 * n + E + 2) if need else None, 4 * need, _raw_stream(index))
+    if st:
+        _check("mma_route", st)
+    return Routing(weights.view(T, k), experts.view(T, k), order, place.view(T, k), offsets,
+                   share, loss.view(()), tokens.view(()))
+
+
+def _plan_route_backward(logits, routing, d_weights, d_loss, mask, normalize):
+    torch = _torch()
+    code = _take("logits", logits, _kinds()["wide"], None, None)
+    T, E = logits.shape
+    k = routing.experts.shape[1] if routing.experts.dim() == 2 else 0
+    f32, i32 = {torch.float32: MMA_F32}, {torch.int32: MMA_I32}
+    whole = [("experts", routing.experts, i32, (T, k)), ("weights", routing.weights, f32, (T, k)),
+             ("offsets", routing.offsets, i32, (E + 1,))]
+    if d_weights is not None:
+        whole.append(("d_weights", d_weights, f32, (T, k)))
+    for name, t, kinds, shape in whole:
+        _take(name, t, kinds, *shape)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    one = [("tokens", routing.tokens, i32)]
+    if d_loss is not None:
+        one.append(("d_loss", d_loss, f32))
+    for name, t, kinds in one:
+        if t.numel() != 1:
+            raise ValueError(f"{name} must be a single value")
+        _take(name, t, kinds, *t.shape)
+    _mask(mask, T)
+    return (code, T, E, k, _row_stride("logits", logits),
+            _one_device(logits, routing.experts, routing.weights, routing.offsets,
+                        routing.tokens, d_weights, d_loss, mask))
+
+
+def route_backward(logits, routing, d_weights=None, d_loss=None, *, mask=None,
+                   normalize: bool = True, stream=None):
+    """Gradient of ``route``'s logits, the choices being taken as given.
+
+    ``logits``, ``mask``, ``normalize``: as the forward's; ``routing``: what it
+    returned; ``d_weights``: (T, k) float32, ``d_loss``: one float32 on the GPU
+    (either may be None).  Returns (T, E) in the logits' type.
+    """
+    code, T, E, k, ldx, index = _plan(
+        ("route back", _key(logits), _key(routing.experts), _key(routing.weights),
+         _key(routing.offsets), _key(routing.tokens), _key(d_weights), _key(d_loss), _key(mask)),
+        _plan_route_backward, logits, routing, d_weights, d_loss, mask, normalize)
+    if stream is not None:
+        return _under(stream, index, route_backward, logits, routing, d_weights, d_loss,
+                      mask=mask, normalize=normalize)
+    dX = _torch().empty((T, E), dtype=logits.dtype, device=logits.device)
+    st = load().mma_route_backward(
+        code, T, E, k, logits.data_ptr(), ldx, None if mask is None else mask.data_ptr(),
+        1 if normalize else 0, routing.weights.data_ptr(), routing.experts.data_ptr(),
+        routing.offsets.data_ptr(), routing.tokens.data_ptr(),
+        None if d_weights is None else d_weights.data_ptr(),
+        None if d_loss is None else d_loss.data_ptr(), dX.data_ptr(), E, _raw_stream(index))
+    if st:
+        _check("mma_route_backward", st)
+    return dX
 
 
 def profile_begin() -> None:

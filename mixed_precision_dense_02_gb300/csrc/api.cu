@@ -1007,3 +1007,88 @@ extern "C" mma_status_t mma_quantize_f8(
                                               block_rows, M, N, X, ldx, Q, ldq,
                                               S, s_row, s_blk});
 }
+
+// ------------------------------------------------- router of a layer of experts
+
+namespace {
+
+// What both directions ask of the sizes; choices are counted in ints, those of
+// the last block's rounding among them.
+mma_status_t check_route(int type, int64_t T, int64_t E, int64_t k) {
+  if (float_bytes(type) == 0) return MMA_ERR_UNSUPPORTED;
+  if (!dim_ok(T) || E < 1 || k < 1 || k > E) return MMA_ERR_INVALID_ARG;
+  if (E > kMaxGroups || k > MMA_MAX_CHOICES || T * k > (int64_t(1) << 30))
+    return MMA_ERR_UNSUPPORTED;
+  return MMA_OK;
+}
+
+mma_status_t check_words(const void* p) {
+  return p == nullptr ? MMA_ERR_INVALID_ARG : aligned4(p) ? MMA_OK : MMA_ERR_MISALIGNED;
+}
+
+}  // namespace
+
+extern "C" int64_t mma_route_workspace(int64_t T, int64_t E) {
+  return dim_ok(T) && E >= 1 && E <= kMaxGroups ? route_workspace_bytes(T, E) : 0;
+}
+
+extern "C" mma_status_t mma_route(int type, int64_t T, int64_t E, int64_t k,
+                                  const void* X, int64_t ldx, const uint8_t* mask,
+                                  int normalize, float* weights, int32_t* experts,
+                                  int32_t* order, int32_t* place, int32_t* offsets,
+                                  float* share, float* loss, int32_t* tokens,
+                                  void* workspace, int64_t workspace_bytes,
+                                  void* stream) {
+  MMA_CHECK(check_route(type, T, E, k));
+  for (const void* q : {static_cast<const void*>(offsets), static_cast<const void*>(share),
+                        static_cast<const void*>(loss), static_cast<const void*>(tokens)})
+    MMA_CHECK(check_words(q));
+  if (T > 0) {
+    MMA_CHECK(check_out(X, ldx, E, float_bytes(type)));
+    for (const void* q : {static_cast<const void*>(weights), static_cast<const void*>(experts),
+                          static_cast<const void*>(order), static_cast<const void*>(place)})
+      MMA_CHECK(check_words(q));
+  }
+  const int64_t need = route_workspace_bytes(T, E);
+  if (need > 0) {
+    MMA_CHECK(check_words(workspace));
+    if (workspace_bytes < need) return MMA_ERR_INVALID_ARG;
+  }
+  int dev = -1;
+  const DeviceInfo* info = device_info(&dev);
+  if (!info) return MMA_ERR_NO_DEVICE;
+  Ctx ctx = make_ctx(stream, dev, info);
+  return launch_route(ctx, RouteProblem{type, T, E, k, X, ldx, mask, normalize != 0, weights,
+                                        experts, order, place, offsets, share, loss, tokens},
+                      workspace);
+}
+
+extern "C" mma_status_t mma_route_backward(
+    int type, int64_t T, int64_t E, int64_t k, const void* X, int64_t ldx,
+    const uint8_t* mask, int normalize, const float* weights, const int32_t* experts,
+    const int32_t* offsets, const int32_t* tokens, const float* DW, const float* DLOSS,
+    void* DX, int64_t lddx, void* stream) {
+  MMA_CHECK(check_route(type, T, E, k));
+  if (T == 0) return MMA_OK;
+  const int64_t eb = float_bytes(type);
+  MMA_CHECK(check_out(X, ldx, E, eb));
+  MMA_CHECK(check_out(DX, lddx, E, eb));
+  if (DX == X && lddx != ldx) return MMA_ERR_INVALID_ARG;
+  if (DW) {
+    MMA_CHECK(check_words(DW));
+    MMA_CHECK(check_words(experts));
+    if (normalize) MMA_CHECK(check_words(weights));
+  }
+  if (DLOSS) {
+    MMA_CHECK(check_words(DLOSS));
+    MMA_CHECK(check_words(offsets));
+    MMA_CHECK(check_words(tokens));
+  }
+  int dev = -1;
+  const DeviceInfo* info = device_info(&dev);
+  if (!info) return MMA_ERR_NO_DEVICE;
+  Ctx ctx = make_ctx(stream, dev, info);
+  return launch_route_backward(
+      ctx, RouteBackProblem{type, T, E, k, X, ldx, mask, normalize != 0, weights, experts,
+                            offsets, tokens, DW, DLOSS, DX, lddx});
+}

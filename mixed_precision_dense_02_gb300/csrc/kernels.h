@@ -278,6 +278,37 @@ mma_status_t launch_layernorm(const Ctx& ctx, const NormProblem& p);
 mma_status_t launch_layernorm_backward(const Ctx& ctx, const NormBackProblem& p,
                                        void* workspace);
 
+// The router of a layer of experts (route.cu).
+struct RouteProblem {
+  int type;
+  int64_t T, E, k;
+  const void* x;
+  int64_t ldx;
+  const uint8_t* mask;  // per token, 0: takes no part; or NULL
+  bool normalize;
+  float* weights;  // T x k, as chosen and place
+  int32_t *chosen, *order, *place, *offsets;
+  float *share, *loss;
+  int32_t* tokens;
+};
+int64_t route_workspace_bytes(int64_t T, int64_t E);
+mma_status_t launch_route(const Ctx& ctx, const RouteProblem& p, void* workspace);
+
+struct RouteBackProblem {
+  int type;
+  int64_t T, E, k;
+  const void* x;
+  int64_t ldx;
+  const uint8_t* mask;
+  bool normalize;
+  const float* weights;
+  const int32_t *chosen, *offsets, *tokens;
+  const float *dweights, *dloss;  // either may be NULL
+  void* dx;
+  int64_t lddx;
+};
+mma_status_t launch_route_backward(const Ctx& ctx, const RouteBackProblem& p);
+
 // 8-bit quantisation (quantize.cu).
 struct QuantProblem {
   int type;
