@@ -12,9 +12,7 @@
 // or, without normalize, p_e (a_e + dw_e - sum p (a + dw)).
 //
 // A warp has a token, lane l its experts l, l + 32, ... (any alignment of a row,
-// 128 bytes per load).  The k choices are k maxima over the warp of the lanes' best
-// ones; each lane keeps its best two, because few lanes lose more, and looks
-// through all of its own again when it has lost both.
+// 128 bytes per load).
 //
 // Sorting is by counting, without atomics whose order would show.  A block sets,
 // for each expert, a bit for each of 64 tokens: an expert's tokens before a given
@@ -33,7 +31,6 @@ namespace {
 constexpr int kBatch = 64;       // tokens whose bits are set at a time
 constexpr int kMostBlocks = 304;  // of the first kernel
 constexpr int kOneBlock = 256;   // tokens that one block takes alone
-constexpr int kMostChoices = 32;  // k: a lane each
 
 struct Choices {
   int tokens, experts, k, per_block, blocks;
@@ -49,12 +46,12 @@ struct Choices {
   int* totals;    // [experts + 2]
 };
 
-// FP32 in the order of its bits as a signed integer; its own inverse.
-__device__ __forceinline__ int ordered(int bits) {
-  return bits ^ ((bits >> 31) & 0x7FFFFFFF);
+// FP32 in the order of its bits as an unsigned integer (0: no number).
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ (uint32_t(int(u) >> 31) | 0x80000000u);
 }
-constexpr int kNone = INT32_MIN;
-constexpr int kMinusInf = int(0xFF800000u ^ 0x7FFFFFFFu);
+constexpr uint32_t kMinusInf = 0x007FFFFFu;
 
 // (+ 0: one zero, one NaN, which is above infinity)
 __device__ __forceinline__ float logit(float v) { return v + 0.f; }
@@ -68,12 +65,108 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// exp(d) for d <= 0 (or NaN), zero where it is below 2^-126: the special function
+// alone, without the scaling that subnormal results take.
+__device__ __forceinline__ float exp_of(float d) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d * 1.4426950408889634f));
+  return r;
+}
+
 template <class T, int V>
 __device__ __forceinline__ void load_logits(const T* row, int experts, float (&x)[V]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int c = 0; c < V; ++c)
     x[c] = c * 32 + lane < experts ? logit(to_float(row[c * 32 + lane])) : -INFINITY;
+}
+
+// The k largest of the warp's x, the best first: lane j gets the j-th one's expert,
+// or -1 where there is none that is above -inf.
+//
+// A number's upper 22 bits and, below them, the expert counted from the top: the
+// maximum over the warp is one instruction, and of equal ones the lowest index
+// wins.  Of 16-bit logits these are all the bits.  FP32 ones that agree in them are
+// told apart by `exact_choices`, which is asked if a choice and the next one do.  A
+// lane keeps its three largest, and looks through all of its own again when those
+// are gone.
+template <int V>
+__device__ __forceinline__ int exact_choices(const float (&x)[V], int experts, int k) {
+  const int lane = threadIdx.x & 31;
+  int id = -1;
+  uint32_t gone = 0;
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) {
+    uint32_t m = 0;
+    int c1 = 0;
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      const uint32_t q =
+          c * 32 + lane < experts && !((gone >> c) & 1) ? ordered(x[c]) : 0u;
+      if (q > m) {
+        m = q;
+        c1 = c;
+      }
+    }
+    const uint32_t best = __reduce_max_sync(0xffffffffu, m);
+    if (best <= kMinusInf) break;
+    const int e = __reduce_min_sync(0xffffffffu, m == best ? c1 * 32 + lane : INT32_MAX);
+    if (lane == j) id = e;
+    if (lane == (e & 31)) gone |= 1u << c1;
+  }
+  return id;
+}
+
+template <bool WIDE, int V>
+__device__ __forceinline__ int choices(const float (&x)[V], int experts, int k) {
+  const int lane = threadIdx.x & 31;
+  uint32_t q[V], m1 = 0, m2 = 0, m3 = 0;
+  auto add = [&](uint32_t v) {
+    const uint32_t a = min(m1, v), b = min(m2, a);
+    m1 = max(m1, v);
+    m2 = max(m2, a);
+    m3 = max(m3, b);
+  };
+#pragma unroll
+  for (int c = 0; c < V; ++c) {
+    const int e = c * 32 + lane;
+    q[c] = e < experts ? (ordered(x[c]) & ~1023u) | uint32_t(1023 - e) : 0u;
+    add(q[c]);
+  }
+  [[maybe_unused]] int left = experts > lane ? (experts - lane + 31) / 32 : 0;
+  uint32_t mine = 0, after = 0;
+#pragma unroll 1
+  for (int j = 0; j <= k; ++j) {
+    const uint32_t best = __reduce_max_sync(0xffffffffu, m1);
+    if (best <= kMinusInf) break;
+    if (j == k) {
+      after = best;
+      break;
+    }
+    if (lane == j) mine = best;
+    if (m1 == best) {
+      m1 = m2;
+      m2 = m3;
+      m3 = 0;
+      --left;
+    }
+    if constexpr (V > 3) {
+      if (__any_sync(0xffffffffu, m1 == 0 && left > 0)) {
+        // what this lane has left is below what it has given
+        if (m1 == 0) {
+#pragma unroll
+          for (int c = 0; c < V; ++c) add(q[c] < best ? q[c] : 0u);
+        }
+      }
+    }
+  }
+  if constexpr (WIDE) {
+    uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
+    if (lane >= k - 1) next = after;
+    if (__any_sync(0xffffffffu, mine != 0 && next != 0 && ((mine ^ next) >> 10) == 0))
+      return exact_choices<V>(x, experts, k);
+  }
+  return mine ? 1023 - int(mine & 1023u) : -1;
 }
 
 // Exclusive sums of the block's values, one per thread, in `sums` (32 ints).
@@ -106,12 +199,14 @@ __device__ __forceinline__ int block_scan(int v, int* sums) {
 __device__ __forceinline__ float balance(const int* counts, const float* share, int experts,
                                          int k, int live, float* buf) {
   float s = 0.f;
+#pragma unroll 1
   for (int e = threadIdx.x; e < experts; e += blockDim.x)
     s = fmaf(float(counts[e]), share[e], s);
   s = warp_sum(s);
   if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = s;
   __syncthreads();
   s = 0.f;
+#pragma unroll 4
   for (int w = 0; w < int(blockDim.x) / 32; ++w) s += buf[w];
   return live > 0 ? s * float(experts) / (float(live) * float(k)) : 0.f;
 }
@@ -132,7 +227,9 @@ __global__ void __launch_bounds__(ONE ? 1024 : 512)
   float* psum = reinterpret_cast<float*>(count + E + 1);       // [warps][E]
   uint16_t* ids = reinterpret_cast<uint16_t*>(psum + warps * E);  // E: none
   uint16_t* ranks = ids + (ONE ? kOneBlock : kBatch) * k;         // (ONE)
+#pragma unroll 1
   for (int e = threadIdx.x; e < E + k; e += blockDim.x) bits[e] = make_uint2(0, 0);
+#pragma unroll 1
   for (int e = threadIdx.x; e <= E; e += blockDim.x) count[e] = 0;
   if constexpr (!ONE) grid_dependents_start();
   const int first = ONE ? 0 : blockIdx.x * a.per_block;
@@ -147,6 +244,7 @@ __global__ void __launch_bounds__(ONE ? 1024 : 512)
   __syncthreads();
   for (int t0 = first; t0 < last; t0 += kBatch) {
     uint16_t* const id0 = ids + (ONE ? t0 * k : 0);
+#pragma unroll 1
     for (int i = warp; i < kBatch && t0 + i < last; i += warps) {
       const int t = t0 + i;
       float y[V];
@@ -156,70 +254,32 @@ __global__ void __launch_bounds__(ONE ? 1024 : 512)
       const int next = i + warps < kBatch ? t + warps : t0 + kBatch + warp;
       if (next < last) load_logits<T, V>(X + next * a.ldx, E, x);
       const bool on = a.mask == nullptr || a.mask[t] != 0;
-      int id = -1, key = kNone;  // lane j: choice j
-      int top = kNone;
+      int id = -1;  // lane j: choice j
+      float top = -INFINITY;
       if (on) {
         ++live;
-        uint32_t gone = 0;  // experts past the last, and those chosen
-#pragma unroll
-        for (int c = 0; c < V; ++c)
-          if (c * 32 + lane >= E) gone |= 1u << c;
-        int m1, m2, c1 = 0, c2 = 0;
-        auto look = [&] {
-          m1 = m2 = kNone;
-#pragma unroll
-          for (int c = 0; c < V; ++c) {
-            const int q = (gone >> c) & 1 ? kNone : ordered(__float_as_int(y[c]));
-            if (q > m1) {
-              m2 = m1;
-              c2 = c1;
-              m1 = q;
-              c1 = c;
-            } else if (q > m2) {
-              m2 = q;
-              c2 = c;
-            }
-          }
-        };
-        look();
-        for (int j = 0; j < k; ++j) {
-          const int best = __reduce_max_sync(0xffffffffu, m1);
-          if (j == 0) top = best;
-          if (best <= kMinusInf) break;
-          const int e = __reduce_min_sync(0xffffffffu, m1 == best ? c1 * 32 + lane : INT32_MAX);
-          if (lane == j) {
-            id = e;
-            key = best;
-          }
-          bool again = false;
-          if (lane == (e & 31)) {
-            gone |= 1u << c1;
-            m1 = m2;
-            c1 = c2;
-            m2 = kNone;
-            again = m1 == kNone;
-          }
-          if (__any_sync(0xffffffffu, again)) look();
-        }
+        id = choices<sizeof(T) == 4, V>(y, E, k);
+        const T* row = X + t * a.ldx;
+        if (id >= 0) top = logit(to_float(row[id]));
       }
       // weights
-      const float most = __int_as_float(ordered(top));
-      const bool some = top > kMinusInf;
+      const float most = __shfl_sync(0xffffffffu, top, 0);
+      const bool some = __shfl_sync(0xffffffffu, id, 0) >= 0;
       float sum = 0.f;
 #pragma unroll
       for (int c = 0; c < V; ++c) {
-        y[c] = some ? __expf(y[c] - most) : 0.f;
+        y[c] = some ? exp_of(y[c] - most) : 0.f;
         sum += y[c];
       }
       sum = warp_sum(sum);
-      const float over = some ? 1.f / sum : 0.f;
+      const float over = some ? __fdividef(1.f, sum) : 0.f;
 #pragma unroll
       for (int c = 0; c < V; ++c) acc[c] = fmaf(y[c], over, acc[c]);
-      float w = id >= 0 ? __expf(__int_as_float(ordered(key)) - most) : 0.f;
+      float w = id >= 0 ? exp_of(top - most) : 0.f;
       if (a.normalize) {
         // (a NaN among the logits is in every weight)
         const float chosen = warp_sum(w);
-        w = id < 0 ? 0.f : sum == sum ? w / chosen : sum;
+        w = id < 0 ? 0.f : sum == sum ? __fdividef(w, chosen) : sum;
       } else {
         w = id < 0 ? 0.f : w * over;
       }
@@ -233,6 +293,7 @@ __global__ void __launch_bounds__(ONE ? 1024 : 512)
     }
     __syncthreads();
     const int here = min(kBatch, last - t0) * k;
+#pragma unroll 1
     for (int c = threadIdx.x; c < here; c += blockDim.x) {
       const int i = c / k, j = c - i * k, id = id0[c];
       const uint2 below = i < 32 ? make_uint2((1u << i) - 1, 0u)
@@ -245,6 +306,7 @@ __global__ void __launch_bounds__(ONE ? 1024 : 512)
         rank += before(id);
       } else {
         // choices without an expert: of earlier tokens, and this one's earlier
+#pragma unroll 1
         for (int q = 0; q < k; ++q) {
           rank += before(E + q);
           if (q < j) rank += ((i < 32 ? bits[E + q].x : bits[E + q].y) >> (i & 31)) & 1;
@@ -256,8 +318,10 @@ __global__ void __launch_bounds__(ONE ? 1024 : 512)
         a.place[int64_t(t0) * k + c] = rank;
     }
     __syncthreads();
+#pragma unroll 1
     for (int e = threadIdx.x; e <= E; e += blockDim.x) {
       int n = 0;
+#pragma unroll 1
       for (int b = e; b < (e < E ? e + 1 : E + k); ++b) {
         n += __popc(bits[b].x) + __popc(bits[b].y);
         bits[b] = make_uint2(0, 0);
@@ -272,9 +336,12 @@ __global__ void __launch_bounds__(ONE ? 1024 : 512)
   if (lane == 0) warp_live[warp] = live;
   __syncthreads();
   live = 0;
+#pragma unroll 4
   for (int w = 0; w < warps; ++w) live += warp_live[w];
+#pragma unroll 1
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     float s = 0.f;
+#pragma unroll 4
     for (int w = 0; w < warps; ++w) s += psum[w * E + e];
     if constexpr (ONE) {
       psum[e] = live > 0 ? s / float(live) : 0.f;  // (this thread's own column)
@@ -285,6 +352,7 @@ __global__ void __launch_bounds__(ONE ? 1024 : 512)
   }
   if constexpr (!ONE) {
     int* out = a.counts + int64_t(blockIdx.x) * (E + 2);
+#pragma unroll 1
     for (int e = threadIdx.x; e <= E; e += blockDim.x) out[e] = count[e];
     if (threadIdx.x == 0) out[E + 1] = live;
   } else {
@@ -306,6 +374,7 @@ __global__ void __launch_bounds__(ONE ? 1024 : 512)
       *a.live = live;
     }
     __syncthreads();
+#pragma unroll 1
     for (int c = threadIdx.x; c < a.tokens * k; c += blockDim.x) {
       const int at = count[ids[c]] + ranks[c];
       a.place[c] = at;
@@ -329,9 +398,11 @@ __global__ void __launch_bounds__(1024) route_scan_kernel(const Choices a) {
   int n = 0;
   float s = 0.f;
   if (e < columns)
-    for (int r = r0; r < r1; ++r) n += a.counts[int64_t(r) * columns + e];
+#pragma unroll 2
+    for (int r = r0; r < r1; ++r) n += a.counts[r * columns + e];
   if (e < a.experts)
-    for (int r = r0; r < r1; ++r) s += a.shares[int64_t(r) * a.experts + e];
+#pragma unroll 2
+    for (int r = r0; r < r1; ++r) s += a.shares[r * a.experts + e];
   part[threadIdx.y][threadIdx.x] = n;
   fpart[threadIdx.y][threadIdx.x] = s;
   // tokens that are not masked, over all blocks
@@ -342,13 +413,16 @@ __global__ void __launch_bounds__(1024) route_scan_kernel(const Choices a) {
   // (column E + 1 stays as it is)
   __syncthreads();
   live = 0;
+#pragma unroll 4
   for (int w = 0; w < 32; ++w) live += live_of[w];
   int before = 0;
+#pragma unroll 2
   for (int y = 0; y < int(threadIdx.y); ++y) before += part[y][threadIdx.x];
   if (e <= a.experts) {
     if (threadIdx.y == 31) a.totals[e] = before + n;
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) {
-      int* p = a.counts + int64_t(r) * columns + e;
+      int* p = a.counts + r * columns + e;
       const int c = *p;
       *p = before;
       before += c;
@@ -356,6 +430,7 @@ __global__ void __launch_bounds__(1024) route_scan_kernel(const Choices a) {
   }
   if (e < a.experts && threadIdx.y == 0) {
     s = 0.f;
+#pragma unroll 4
     for (int y = 0; y < 32; ++y) s += fpart[y][threadIdx.x];
     a.share[e] = live > 0 ? s / float(live) : 0.f;
   }
@@ -377,17 +452,23 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const Choices a) {
   }
   __syncthreads();
   if (blockIdx.x == 0) {
+#pragma unroll 1
     for (int e = threadIdx.x; e <= E; e += blockDim.x) a.offsets[e] = offset[e];
     const float loss = balance(a.totals, a.share, E, a.k, *a.live, fsum);
     if (threadIdx.x == 0) *a.loss = loss;
   }
-  const int choices = a.tokens * a.k, per = a.per_block * a.k;
-  for (int64_t c = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; c < choices;
-       c += int64_t(gridDim.x) * blockDim.x) {
-    const int id = a.chosen[c], e = id < 0 ? E : id;
-    const int p = offset[e] + a.counts[(c / per) * (E + 2) + e] + a.place[c];
-    a.place[c] = p;
-    a.order[p] = int(c);
+  // (a block of the first kernel after the other: its counts are one row)
+#pragma unroll 1
+  for (int b = blockIdx.x; b < a.blocks; b += gridDim.x) {
+    const int per = a.per_block * a.k, from = b * per, to = min(from + per, a.tokens * a.k);
+    const int* before = a.counts + int64_t(b) * (E + 2);
+#pragma unroll 1
+    for (int c = from + threadIdx.x; c < to; c += blockDim.x) {
+      const int id = a.chosen[c], e = id < 0 ? E : id;
+      const int p = offset[e] + before[e] + a.place[c];
+      a.place[c] = p;
+      a.order[p] = c;
+    }
   }
 }
 
@@ -410,6 +491,7 @@ __global__ void __launch_bounds__(256)
       if (e < E) a[c] = f * float(p.offsets[e + 1] - p.offsets[e]);
     }
   }
+#pragma unroll 1
   for (int e = lane; e < E; e += 32) slab[e] = 0.f;
   __syncwarp();
   const int warps = gridDim.x * (blockDim.x >> 5);
@@ -440,11 +522,11 @@ __global__ void __launch_bounds__(256)
     float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      x[c] = some ? __expf(x[c] - most) : 0.f;
+      x[c] = some ? exp_of(x[c] - most) : 0.f;
       sum += x[c];
     }
     sum = warp_sum(sum);
-    const float over = some ? 1.f / sum : 0.f;
+    const float over = some ? __fdividef(1.f, sum) : 0.f;
     __syncwarp();
     float dot = 0.f, add[V];
 #pragma unroll
@@ -516,11 +598,8 @@ mma_status_t route(const Ctx& ctx, const Choices& a) {
   if (!one) {
     if (e == cudaSuccess)
       e = launch(ctx, route_scan_kernel, dim3((a.experts + 2 + 31) / 32), dim3(32, 32), 0, true, a);
-    const int64_t choices = int64_t(a.tokens) * a.k;
     if (e == cudaSuccess)
-      e = launch(ctx, route_place_kernel,
-                 dim3(unsigned(std::min<int64_t>((choices + 1023) / 1024, ctx.num_sms * 2))),
-                 dim3(1024), 0, true, a);
+      e = launch(ctx, route_place_kernel, dim3(a.blocks), dim3(1024), 0, true, a);
   }
   const cudaError_t last = cudaGetLastError();
   return e == cudaSuccess && last == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
