@@ -684,6 +684,84 @@ mma_status_t mma_route_backward(int type, int64_t T, int64_t E, int64_t k,
                                 const float *DLOSS, void *DX, int64_t lddx,
                                 void *stream);
 
+/*
+ * mma_gemm_lora -- a product shared by many requests, each with a low-rank adapter
+ * beside it.  The T rows of X are sorted by request, request i has the rows
+ * [offsets[i], offsets[i + 1]) and the adapter a = adapters[i]:
+ *
+ *     S = scales[a] * X A_a             (T x rank, FP32)
+ *     D = X W + C + S B_a               for the rows of request i
+ *
+ * type_in : MMA_F16 or MMA_BF16 (X, W, A, B); type_d : that or MMA_F32 (C, D).
+ * layout  : MMA_COL_MAJOR -- W is stored N x K, A_a rank x K, B_a N x rank;
+ *           MMA_ROW_MAJOR -- W K x N, A_a K x rank, B_a rank x N: the gradient of
+ *           the other layout's X, with N and K exchanged and its B as A, its A as
+ *           B (S is then what mma_gemm_lora_wgrad calls U).
+ * A, B    : adapter a's matrices at A + a * stride_a and B + a * stride_b
+ *           elements, adapters_total of them (at most 65535), of one rank, at most
+ *           MMA_MAX_RANK (a smaller one is padded with zeros).
+ * requests: 0 .. MMA_MAX_GROUPS; offsets: as mma_gemm_grouped's, but no row is left
+ *           out: rows of no request have no adapter.
+ * adapters: int32 in device memory, or NULL (request i has adapter i).  Outside [0,
+ *           adapters_total): none.  Requests may share an adapter.
+ * scales  : one float per adapter, in device memory, or NULL (1).
+ * C       : T x N or NULL; may be D with the same leading dimension.
+ * S       : T x lds, 16-byte aligned, lds a multiple of 8; written whole (zeros
+ *           where there is no adapter), columns from rank to the next eighth one
+ *           included.
+ * workspace: 16-byte aligned device memory of mma_gemm_lora_workspace(type_d, T,
+ *           rank) bytes, which the call's work on `stream` uses and nothing else
+ *           may meanwhile.
+ * S is FP32 in the products of requests with fewer than 8 rows in a tile.  For the
+ * others it is rounded to type_in (an FP32 D: to a sum of two numbers of type_in),
+ * whose range it has to keep.  A NaN or infinity in one adapter or row stays with
+ * the rows of that adapter, or that row.
+ */
+#define MMA_MAX_RANK 128
+int64_t mma_gemm_lora_workspace(int type_d, int64_t T, int64_t rank);
+mma_status_t mma_gemm_lora(int type_in, int type_d, int64_t T, int64_t N,
+                           int64_t K, int64_t rank, const void *X, int64_t ldx,
+                           const void *W, int64_t ldw, const void *A,
+                           int64_t lda, int64_t stride_a, const void *B,
+                           int64_t ldb, int64_t stride_b, int layout,
+                           int64_t requests, const int32_t *offsets,
+                           const int32_t *adapters, int64_t adapters_total,
+                           const float *scales, const void *C, int64_t ldc,
+                           void *D, int64_t ldd, float *S, int64_t lds,
+                           void *workspace, int64_t workspace_bytes,
+                           void *stream);
+
+/*
+ * mma_gemm_lora_wgrad -- the gradients of the adapters of mma_gemm_lora, over the
+ * rows t of all requests with adapter a:
+ *
+ *     DA_a = sum U_t^T X_t   (rank x K),     DB_a = sum DY_t^T S_t   (N x rank)
+ *
+ * with S of the forward call (T x lds) and U of the call for the input's gradient
+ * (T x ldu), both FP32, rows on 16-byte boundaries, scales included.
+ * type_d  : of DA and DB, type_in or MMA_F32.  An FP32 result takes S and U as sums
+ *           of two numbers of type_in, a 16-bit one as one.
+ * accumulate : nonzero -- added to DA and DB; else an adapter without rows gets
+ *           zeros.
+ * Sums are FP32, in a fixed order, through `workspace`: 4-byte aligned device
+ * memory of mma_gemm_lora_wgrad_workspace(T, N, K, rank, requests) bytes.  Other
+ * arguments as above.
+ */
+int64_t mma_gemm_lora_wgrad_workspace(int64_t T, int64_t N, int64_t K,
+                                      int64_t rank, int64_t requests);
+mma_status_t mma_gemm_lora_wgrad(int type_in, int type_d, int64_t T, int64_t N,
+                                 int64_t K, int64_t rank, const void *DY,
+                                 int64_t lddy, const void *X, int64_t ldx,
+                                 const float *S, int64_t lds, const float *U,
+                                 int64_t ldu, int64_t requests,
+                                 const int32_t *offsets,
+                                 const int32_t *adapters,
+                                 int64_t adapters_total, void *DA, int64_t ldda,
+                                 int64_t stride_da, void *DB, int64_t lddb,
+                                 int64_t stride_db, int accumulate,
+                                 void *workspace, int64_t workspace_bytes,
+                                 void *stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *mma_status_string(int status);
 

@@ -13,9 +13,10 @@ compute call raises -- there is no CPU fallback.
 from .binding import (gemm, gemm_ex, gemm_batched, gemm_i8_ex, library_path, load,  # noqa: F401
                       rmsnorm_f8, rmsnorm_backward, layernorm, layernorm_f8,
                       layernorm_backward, quantize_f8, gemm_f8, gemm_grouped,
-                      gemm_grouped_wgrad, gemm_grouped_f8, Routing, route, route_backward,
-                      MMAError)
+                      gemm_grouped_wgrad, gemm_grouped_f8, gemm_lora, gemm_lora_wgrad, Routing,
+                      route, route_backward, MMAError)
 
 __all__ = ["gemm", "gemm_ex", "gemm_batched", "gemm_i8_ex", "rmsnorm_f8",
            "rmsnorm_backward", "layernorm", "layernorm_f8", "layernorm_backward", "quantize_f8", "gemm_f8", "gemm_grouped",
-           "gemm_grouped_wgrad", "gemm_grouped_f8", "Routing", "route", "route_backward", "load", "library_path", "MMAError"]
+           "gemm_grouped_wgrad", "gemm_grouped_f8", "gemm_lora",
+           "gemm_lora_wgrad", "Routing", "route", "route_backward", "load", "library_path", "MMAError"]

@@ -76,6 +76,16 @@ SIGNATURES = {
     "mma_route_workspace": (_i64, [_i64, _i64]),
     "mma_route_backward": (_int, [_int, _i64, _i64, _i64, _p, _i64, _p, _int, _p,
                                   _p, _p, _p, _p, _p, _p, _i64, _p]),
+    "mma_gemm_lora": (_int, [_int, _int, _i64, _i64, _i64, _i64, _p, _i64, _p,
+                             _i64, _p, _i64, _i64, _p, _i64, _i64, _int, _i64,
+                             _p, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _p,
+                             _i64, _p]),
+    "mma_gemm_lora_workspace": (_i64, [_int, _i64, _i64]),
+    "mma_gemm_lora_wgrad": (_int, [_int, _int, _i64, _i64, _i64, _i64, _p, _i64,
+                                   _p, _i64, _p, _i64, _p, _i64, _i64, _p, _p,
+                                   _i64, _p, _i64, _i64, _p, _i64, _i64, _int,
+                                   _p, _i64, _p]),
+    "mma_gemm_lora_wgrad_workspace": (_i64, [_i64, _i64, _i64, _i64, _i64]),
     "mma_device_status": (_int, [_p]),
     "mma_selftest_wait_timeout": (_int, [_i64, _p]),
     "mma_selftest_gemm_abort": (_int, [_int, _i64, _p, _p, _p, _p]),
@@ -974,6 +984,172 @@ def gemm_grouped_f8(A, SA, B, SB, offsets, C=None, D=None, *, out_dtype=None,
     if st:
         _check("mma_gemm_grouped_f8", st)
     return D
+
+
+# --------------------------------------------------------------------------
+# low-rank adapters of many requests
+
+def _requests(offsets, adapters) -> int:
+    """The number of requests, from their offsets."""
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must hold one value more than there are requests")
+    requests = offsets.shape[0] - 1
+    _check_offsets(offsets, requests)
+    if adapters is not None:
+        _take("adapters", adapters, _kinds()["offset"], requests)
+        if requests > 1 and adapters.stride(0) != 1:
+            raise ValueError("adapters must be contiguous")
+    return requests
+
+
+def _plan_lora(X, W, A, B, offsets, adapters, scales, C, D, b_layout, out_dtype):
+    code = _take("X", X, _kinds()["half"], None, None)
+    T, K = X.shape
+    if b_layout not in ("col", "row"):
+        raise ValueError(b_layout)
+    row = b_layout == "row"
+    if row:
+        _same("W", W, X, K, None)
+        _same("A", A, X, None, K, None)
+        N, total, rank = W.shape[1], A.shape[0], A.shape[2]
+        _same("B", B, X, total, rank, N)
+    else:
+        _same("W", W, X, None, K)
+        _same("A", A, X, None, None, K)
+        N, total, rank = W.shape[0], A.shape[0], A.shape[1]
+        _same("B", B, X, total, N, rank)
+    requests = _requests(offsets, adapters)
+    if scales is not None:
+        _take("scales", scales, _kinds()["scale"], total)
+        if total > 1 and scales.stride(0) != 1:
+            raise ValueError("scales must be contiguous")
+    if out_dtype is None and C is None and D is None:
+        out_dtype = X.dtype
+    dtype, d_code = _result("gemm_lora", C, D, (T, N), out_dtype)
+    lds = -(-rank // 8) * 8
+    return (code, d_code, T, N, K, rank, _rows("X", X), _rows("W", W), _rows("A", A),
+            _slices("A", A), _rows("B", B), _slices("B", B),
+            MMA_ROW_MAJOR if row else MMA_COL_MAJOR, requests, total,
+            0 if C is None else _rows("C", C), N if D is None else _rows("D", D), dtype, lds,
+            load().mma_gemm_lora_workspace(d_code, T, rank),
+            _one_device(X, W, A, B, offsets, adapters, scales, C, D))
+
+
+def gemm_lora(X, W, A, B, offsets, adapters=None, scales=None, C=None, D=None, *,
+              b_layout: str = "col", out_dtype=None, sums: bool = False, stream=None):
+    """A product shared by many requests, each with a low-rank adapter beside it:
+    ``D[i] = X[i] @ W^T + scales[a] * (X[i] @ A[a]^T) @ B[a]^T + C[i]`` for the rows i
+    in ``[offsets[j], offsets[j + 1])`` of each request j, ``a = adapters[j]``.
+
+    ``X``: (T, K) float16 or bfloat16, rows sorted by request; ``W``: (N, K), ``A``:
+    (adapters, rank, K), ``B``: (adapters, N, rank), or with ``b_layout="row"`` (K,
+    N), (adapters, K, rank) and (adapters, rank, N): the input's gradient is
+    ``gemm_lora(dY, W, B, A, ..., b_layout="row")`` of the forward's matrices.
+    ``offsets``: (requests + 1,), ``adapters``: (requests,) int32 on the GPU (None:
+    request j has adapter j; a negative one: none); ``scales``: (adapters,) float32.
+    ``C``, ``D``: (T, N) of X's type or float32 (``out_dtype``, X's unless C or D is
+    given).  Rank at most 128.  Returns D; with ``sums=True`` also the rows' sums
+    ``scales[a] * X[i] @ A[a]^T``, (T, rank) float32, for ``gemm_lora_wgrad``.
+    """
+    torch = _torch()
+    (code, d_code, T, N, K, rank, ldx, ldw, lda, stride_a, ldb, stride_b, layout, requests,
+     total, ldc, ldd, dtype, lds, need, index) = _plan(
+        ("lora", _key(X), _key(W), _key(A), _key(B), _key(offsets), _key(adapters),
+         _key(scales), _key(C), _key(D), b_layout, out_dtype),
+        _plan_lora, X, W, A, B, offsets, adapters, scales, C, D, b_layout, out_dtype)
+    if stream is not None:
+        return _under(stream, index, gemm_lora, X, W, A, B, offsets, adapters, scales, C, D,
+                      b_layout=b_layout, out_dtype=out_dtype, sums=sums)
+    device = X.device
+    if D is None:
+        D = torch.empty((T, N), dtype=dtype, device=device)
+    S = torch.empty((T, lds), dtype=torch.float32, device=device)
+    # (its memory goes to other work of the current stream only after the call's)
+    ws = torch.empty((need,), dtype=torch.uint8, device=device)
+    st = load().mma_gemm_lora(
+        code, d_code, T, N, K, rank, X.data_ptr(), ldx, W.data_ptr(), ldw, A.data_ptr(), lda,
+        stride_a, B.data_ptr(), ldb, stride_b, layout, requests, offsets.data_ptr(),
+        None if adapters is None else adapters.data_ptr(), total,
+        None if scales is None else scales.data_ptr(), None if C is None else C.data_ptr(),
+        ldc, D.data_ptr(), ldd, S.data_ptr(), lds, ws.data_ptr(), need, _raw_stream(index))
+    if st:
+        _check("mma_gemm_lora", st)
+    return (D, S[:, :rank]) if sums else D
+
+
+def _plan_lora_wgrad(dY, X, S, U, offsets, adapters, adapters_total, dA, dB, accumulate,
+                     out_dtype):
+    kinds = _kinds()
+    code = _take("dY", dY, kinds["half"], None, None)
+    T, N = dY.shape
+    _same("X", X, dY, T, None)
+    K = X.shape[1]
+    _take("S", S, kinds["scale"], T, None)
+    rank = S.shape[1]
+    _take("U", U, kinds["scale"], T, rank)
+    requests = _requests(offsets, adapters)
+    total = requests if adapters_total is None else int(adapters_total)
+    if (dA is None) != (dB is None) or (accumulate and dA is None):
+        raise ValueError("dA and dB go together, and accumulate needs both")
+    dtype = out_dtype
+    if dA is not None:
+        if dA.dtype != dB.dtype or (out_dtype is not None and dA.dtype != out_dtype):
+            raise TypeError("dA and dB must be of one type, out_dtype where it is given")
+        dtype = dA.dtype
+        _take("dA", dA, kinds["wide"], total, rank, K)
+        _take("dB", dB, kinds["wide"], total, N, rank)
+    if dtype is None:
+        dtype = _torch().float32
+    d_code = kinds["wide"].get(dtype)
+    if d_code is None:
+        raise TypeError(f"gemm_lora_wgrad: unsupported result type {dtype}")
+    return (code, d_code, T, N, K, rank, _rows("dY", dY), _rows("X", X), _rows("S", S),
+            _rows("U", U), requests, total, K if dA is None else _rows("dA", dA),
+            rank * K if dA is None else _slices("dA", dA),
+            rank if dB is None else _rows("dB", dB),
+            N * rank if dB is None else _slices("dB", dB), dtype,
+            load().mma_gemm_lora_wgrad_workspace(T, N, K, rank, requests),
+            _one_device(dY, X, S, U, offsets, adapters, dA, dB))
+
+
+def gemm_lora_wgrad(dY, X, S, U, offsets, adapters=None, *, adapters_total=None, dA=None,
+                    dB=None, accumulate: bool = False, out_dtype=None, stream=None):
+    """Gradients of ``gemm_lora``'s adapters: ``dA[a] = sum U[i]^T X[i]`` and
+    ``dB[a] = sum dY[i]^T S[i]`` over the rows i of all requests with adapter a.
+
+    ``dY``: (T, N), ``X``: (T, K), float16 or bfloat16; ``S``: the forward's sums,
+    ``U``: those of the input's gradient, (T, rank) float32; ``offsets`` and
+    ``adapters`` as there, ``adapters_total`` adapters (None: as many as requests).
+    Returns ``(dA, dB)``, (adapters, rank, K) and (adapters, N, rank), float32 unless
+    ``out_dtype``, or dA and dB, say otherwise; with ``accumulate`` added to the
+    given dA and dB.  An adapter without rows gets zeros.
+    """
+    torch = _torch()
+    accumulate = bool(accumulate)
+    (code, d_code, T, N, K, rank, ldy, ldx, lds, ldu, requests, total, ldda, stride_da, lddb,
+     stride_db, dtype, need, index) = _plan(
+        ("lora wgrad", _key(dY), _key(X), _key(S), _key(U), _key(offsets), _key(adapters),
+         adapters_total, _key(dA), _key(dB), accumulate, out_dtype),
+        _plan_lora_wgrad, dY, X, S, U, offsets, adapters, adapters_total, dA, dB, accumulate,
+        out_dtype)
+    if stream is not None:
+        return _under(stream, index, gemm_lora_wgrad, dY, X, S, U, offsets, adapters,
+                      adapters_total=adapters_total, dA=dA, dB=dB, accumulate=accumulate,
+                      out_dtype=out_dtype)
+    device = dY.device
+    if dA is None:
+        dA = torch.empty((total, rank, K), dtype=dtype, device=device)
+        dB = torch.empty((total, N, rank), dtype=dtype, device=device)
+    ws = torch.empty((need,), dtype=torch.uint8, device=device)
+    st = load().mma_gemm_lora_wgrad(
+        code, d_code, T, N, K, rank, dY.data_ptr(), ldy, X.data_ptr(), ldx, S.data_ptr(), lds,
+        U.data_ptr(), ldu, requests, offsets.data_ptr(),
+        None if adapters is None else adapters.data_ptr(), total, dA.data_ptr(), ldda,
+        stride_da, dB.data_ptr(), lddb, stride_db, 1 if accumulate else 0, ws.data_ptr(), need,
+        _raw_stream(index))
+    if st:
+        _check("mma_gemm_lora_wgrad", st)
+    return dA, dB
 
 
 # --------------------------------------------------------------------------

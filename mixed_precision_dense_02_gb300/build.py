@@ -20,7 +20,7 @@ SOURCES = ["api.cu", "gemm_tc.cu", "gemm_i8.cu", "gemm_f64.cu", "batched16.cu",
            "noalloc.cu", "selftest.cu", "batched_mma.cu",
            "batched_tile.cu", "gemm_sk.cu", "peaks.cu", "gemm_grouped.cu",
            "rmsnorm.cu", "layernorm.cu", "quantize.cu",
-           "route.cu"]
+           "route.cu", "lora.cu"]
 HEADERS = ["ptx.cuh", "kernels.h", "f8_common.cuh", "norm_shape.h",
            "norm_common.cuh"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1092,3 +1092,192 @@ extern "C" mma_status_t mma_route_backward(
       ctx, RouteBackProblem{type, T, E, k, X, ldx, mask, normalize != 0, weights, experts,
                             offsets, tokens, DW, DLOSS, DX, lddx});
 }
+
+// ------------------------------------------------------------ low-rank adapters
+
+namespace {
+
+mma_status_t check_lora(int type_in, int type_d, int64_t T, int64_t N, int64_t K,
+                        int64_t rank, int64_t requests, const int32_t* offsets,
+                        int64_t adapters_total) {
+  if ((type_in != MMA_F16 && type_in != MMA_BF16) ||
+      (type_d != type_in && type_d != MMA_F32))
+    return MMA_ERR_UNSUPPORTED;
+  if (!dim_ok(T) || !dim_ok(N) || !dim_ok(K) || rank < 0 || requests < 0 ||
+      adapters_total < 0)
+    return MMA_ERR_INVALID_ARG;
+  if (rank > MMA_MAX_RANK || requests > kMaxGroups || adapters_total > 65535 ||
+      T > INT32_MAX - 1024 || N > INT32_MAX - 1024 || K > INT32_MAX - 1024)
+    return MMA_ERR_UNSUPPORTED;
+  return rank > 0 && T > 0 ? check_words(offsets) : MMA_OK;
+}
+
+int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
+
+// The rows' sums: FP32, 16-byte rows of at least `rank`.
+mma_status_t check_sums(const float* s, int64_t ld, int64_t rank) {
+  if (s == nullptr || ld < rank) return MMA_ERR_INVALID_ARG;
+  return aligned16(s) && ld % 4 == 0 ? MMA_OK : MMA_ERR_MISALIGNED;
+}
+
+// (an FP32 result takes the sums in two parts of 16 bits)
+int lora_parts(int type_d) { return type_d == MMA_F32 ? 2 : 1; }
+
+}  // namespace
+
+extern "C" int64_t mma_gemm_lora_workspace(int type_d, int64_t T, int64_t rank) {
+  return dim_ok(T) && rank > 0 && rank <= MMA_MAX_RANK
+             ? lora_parts(type_d) * T * round8(rank) * 2
+             : 0;
+}
+
+extern "C" mma_status_t mma_gemm_lora(
+    int type_in, int type_d, int64_t T, int64_t N, int64_t K, int64_t rank, const void* X,
+    int64_t ldx, const void* W, int64_t ldw, const void* A, int64_t lda, int64_t stride_a,
+    const void* B, int64_t ldb, int64_t stride_b, int layout, int64_t requests,
+    const int32_t* offsets, const int32_t* adapters, int64_t adapters_total,
+    const float* scales, const void* C, int64_t ldc, void* D, int64_t ldd, float* S,
+    int64_t lds, void* workspace, int64_t workspace_bytes, void* stream) {
+  MMA_CHECK(check_lora(type_in, type_d, T, N, K, rank, requests, offsets, adapters_total));
+  if (layout != MMA_COL_MAJOR && layout != MMA_ROW_MAJOR) return MMA_ERR_INVALID_ARG;
+  if (T == 0) return MMA_OK;
+  const bool row = layout == MMA_ROW_MAJOR;
+  if (N > 0) MMA_CHECK(check_cd(C, ldc, D, ldd, N, float_bytes(type_d)));
+  if (K > 0) {
+    MMA_CHECK(check_in(X, ldx, K, 2));
+    if (N > 0) MMA_CHECK(check_in(W, ldw, row ? N : K, 2));
+  }
+  if (rank > 0) {
+    MMA_CHECK(check_sums(S, lds, rank));
+    if (lds % 8 != 0 || lds > INT32_MAX) return MMA_ERR_MISALIGNED;
+    if (adapters) MMA_CHECK(check_words(adapters));
+    if (scales) MMA_CHECK(check_words(scales));
+    if (workspace == nullptr ||
+        workspace_bytes < mma_gemm_lora_workspace(type_d, T, rank))
+      return MMA_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return MMA_ERR_MISALIGNED;
+    if (adapters_total > 0 && K > 0) {
+      MMA_CHECK(check_in(A, lda, row ? rank : K, 2));
+      if (!slices_ok(adapters_total, stride_a, row ? K : rank, lda, row ? rank : K))
+        return MMA_ERR_INVALID_ARG;
+      if (adapters_total > 1 && !ld_ok(stride_a, 2)) return MMA_ERR_MISALIGNED;
+      if (N > 0) {
+        MMA_CHECK(check_in(B, ldb, row ? N : rank, 2));
+        if (!slices_ok(adapters_total, stride_b, row ? rank : N, ldb, row ? N : rank))
+          return MMA_ERR_INVALID_ARG;
+        if (adapters_total > 1 && !ld_ok(stride_b, 2)) return MMA_ERR_MISALIGNED;
+      }
+    }
+  }
+  int dev = -1;
+  const DeviceInfo* info = device_info(&dev);
+  if (!info) return MMA_ERR_NO_DEVICE;
+  Ctx ctx = make_ctx(stream, dev, info);
+  attach_profile(ctx);
+  LoraProblem g = {};
+  g.bf16 = type_in == MMA_BF16;
+  g.row_major = row;
+  g.d_type = type_d;
+  g.rows = T;
+  g.N = N;
+  g.K = K;
+  g.rank = rank;
+  g.requests = requests;
+  g.adapters_total = adapters_total;
+  g.X = X;
+  g.ldx = ldx;
+  g.W = W;
+  g.ldw = ldw;
+  g.A = A;
+  g.lda = lda;
+  g.stride_a = stride_a;
+  g.B = B;
+  g.ldb = ldb;
+  g.stride_b = stride_b;
+  g.offsets = offsets;
+  g.adapters = adapters;
+  g.scales = scales;
+  g.C = C;
+  g.ldc = ldc;
+  g.D = D;
+  g.ldd = ldd;
+  LoraLow low = {S, workspace, int(lds), int(round8(rank)), lora_parts(type_d)};
+  if (rank > 0) MMA_CHECK(launch_lora_shrink(ctx, g, low));
+  if (N == 0) return MMA_OK;
+  // without them there is nothing to add
+  if (rank == 0 || requests == 0 || adapters_total == 0 || K == 0) low.parts = 0;
+  return launch_gemm_lora(ctx, g, low);
+}
+
+extern "C" int64_t mma_gemm_lora_wgrad_workspace(int64_t T, int64_t N, int64_t K,
+                                                 int64_t rank, int64_t requests) {
+  if (!dim_ok(T) || !dim_ok(N) || !dim_ok(K) || rank < 1 || rank > MMA_MAX_RANK ||
+      requests < 0 || requests > kMaxGroups)
+    return 0;
+  return lora_wgrad_workspace_bytes(T, N, K, rank, requests);
+}
+
+extern "C" mma_status_t mma_gemm_lora_wgrad(
+    int type_in, int type_d, int64_t T, int64_t N, int64_t K, int64_t rank, const void* DY,
+    int64_t lddy, const void* X, int64_t ldx, const float* S, int64_t lds, const float* U,
+    int64_t ldu, int64_t requests, const int32_t* offsets, const int32_t* adapters,
+    int64_t adapters_total, void* DA, int64_t ldda, int64_t stride_da, void* DB,
+    int64_t lddb, int64_t stride_db, int accumulate, void* workspace,
+    int64_t workspace_bytes, void* stream) {
+  MMA_CHECK(check_lora(type_in, type_d, T, N, K, rank, requests, offsets, adapters_total));
+  if ((N + 127) / 128 + (K + 127) / 128 > 65535) return MMA_ERR_UNSUPPORTED;
+  if (rank == 0 || adapters_total == 0 || N + K == 0) return MMA_OK;
+  MMA_CHECK(check_words(offsets));
+  if (adapters) MMA_CHECK(check_words(adapters));
+  const int64_t eb = float_bytes(type_d);
+  if (K > 0) {
+    MMA_CHECK(check_out(DA, ldda, K, eb));
+    if (!slices_ok(adapters_total, stride_da, rank, ldda, K)) return MMA_ERR_INVALID_ARG;
+  }
+  if (N > 0) {
+    MMA_CHECK(check_out(DB, lddb, rank, eb));
+    if (!slices_ok(adapters_total, stride_db, N, lddb, rank)) return MMA_ERR_INVALID_ARG;
+  }
+  if (T > 0) {
+    if (N > 0) MMA_CHECK(check_in(DY, lddy, N, 2));
+    if (K > 0) MMA_CHECK(check_in(X, ldx, K, 2));
+    if (N > 0) MMA_CHECK(check_sums(S, lds, rank));
+    if (K > 0) MMA_CHECK(check_sums(U, ldu, rank));
+    if (workspace == nullptr) return MMA_ERR_INVALID_ARG;
+    if (!aligned4(workspace)) return MMA_ERR_MISALIGNED;
+    if (workspace_bytes < lora_wgrad_workspace_bytes(T, N, K, rank, requests))
+      return MMA_ERR_INVALID_ARG;
+  }
+  int dev = -1;
+  const DeviceInfo* info = device_info(&dev);
+  if (!info) return MMA_ERR_NO_DEVICE;
+  Ctx ctx = make_ctx(stream, dev, info);
+  attach_profile(ctx);
+  LoraWgradProblem g = {};
+  g.bf16 = type_in == MMA_BF16;
+  g.d_type = type_d;
+  g.rows = T;
+  g.N = N;
+  g.K = K;
+  g.rank = rank;
+  g.requests = requests;
+  g.adapters_total = adapters_total;
+  g.DY = DY;
+  g.lddy = lddy;
+  g.X = X;
+  g.ldx = ldx;
+  g.S = S;
+  g.lds = lds;
+  g.U = U;
+  g.ldu = ldu;
+  g.offsets = offsets;
+  g.adapters = adapters;
+  g.DA = DA;
+  g.ldda = ldda;
+  g.stride_da = stride_da;
+  g.DB = DB;
+  g.lddb = lddb;
+  g.stride_db = stride_db;
+  g.accumulate = accumulate != 0;
+  return launch_lora_wgrad(ctx, g, static_cast<float*>(workspace));
+}

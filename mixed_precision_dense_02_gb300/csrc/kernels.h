@@ -228,6 +228,63 @@ struct WgradProblem {
 };
 mma_status_t launch_gemm_grouped_wgrad(const Ctx& ctx, const WgradProblem& g);
 
+// Product with low-rank adapters (lora.cu, gemm_grouped.cu): D = X W + C, and for
+// the rows of request i scale * (X A) B of its adapter besides.
+struct LoraProblem {
+  bool bf16, row_major;  // W, A, B: K-major (N x K, rank x K, N x rank) or
+                         // row-major (K x N, K x rank, rank x N)
+  int d_type;
+  int64_t rows, N, K, rank, requests, adapters_total;
+  const void* X;
+  int64_t ldx;
+  const void* W;
+  int64_t ldw;
+  const void* A;
+  int64_t lda, stride_a;
+  const void* B;
+  int64_t ldb, stride_b;
+  const int *offsets, *adapters;
+  const float* scales;
+  const void* C;
+  int64_t ldc;
+  void* D;
+  int64_t ldd;
+};
+// The rows' sums scale * (X A): in FP32 (ld32 a multiple of 8, so that eight can be
+// read from any eighth one) and as `parts` matrices of 16 bits whose sum they are.
+struct LoraLow {
+  float* f32;
+  void* f16;
+  int ld32, ld16, parts;
+};
+mma_status_t launch_lora_shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low);
+mma_status_t launch_gemm_lora(const Ctx& ctx, const LoraProblem& g, const LoraLow& low);
+
+// The adapters' gradients: DB = sum of DY^T S (N x rank), DA = sum of U^T X (rank x
+// K) over each adapter's rows.
+struct LoraWgradProblem {
+  bool bf16;
+  int d_type;
+  int64_t rows, N, K, rank, requests, adapters_total;
+  const void* DY;
+  int64_t lddy;
+  const void* X;
+  int64_t ldx;
+  const float* S;
+  int64_t lds;
+  const float* U;
+  int64_t ldu;
+  const int *offsets, *adapters;
+  void* DA;
+  int64_t ldda, stride_da;
+  void* DB;
+  int64_t lddb, stride_db;
+  bool accumulate;
+};
+int64_t lora_wgrad_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t rank,
+                                   int64_t requests);
+mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& g, float* workspace);
+
 // Root-mean-square norm with the residual's addition (rmsnorm.cu).  Element
 // types MMA_F16, MMA_BF16, MMA_F32; NULL pointers as in the C ABI.
 struct NormProblem {
