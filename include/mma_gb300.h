@@ -709,16 +709,17 @@ mma_status_t mma_route_backward(int type, int64_t T, int64_t E, int64_t k,
  * S       : T x lds, 16-byte aligned, lds a multiple of 8; written whole (zeros
  *           where there is no adapter), columns from rank to the next eighth one
  *           included.
- * workspace: 16-byte aligned device memory of mma_gemm_lora_workspace(type_d, T,
- *           rank) bytes, which the call's work on `stream` uses and nothing else
- *           may meanwhile.
- * S is FP32 in the products of requests with fewer than 8 rows in a tile.  For the
- * others it is rounded to type_in (an FP32 D: to a sum of two numbers of type_in),
- * whose range it has to keep.  A NaN or infinity in one adapter or row stays with
+ * workspace: 16-byte aligned device memory of mma_gemm_lora_workspace(type_in,
+ *           type_d, T, N, rank, requests) bytes, which the call's work on `stream`
+ *           uses and nothing else may meanwhile.
+ * With up to 128 rows, and for requests of fewer than 8, the product with B takes S
+ * as it is.  For the others S is rounded to type_in (an FP32 D: to a sum of two FP16
+ * or three BF16 numbers), whose range it has to keep.  A NaN or infinity in one adapter or row stays with
  * the rows of that adapter, or that row.
  */
 #define MMA_MAX_RANK 128
-int64_t mma_gemm_lora_workspace(int type_d, int64_t T, int64_t rank);
+int64_t mma_gemm_lora_workspace(int type_in, int type_d, int64_t T, int64_t N,
+                                int64_t rank, int64_t requests);
 mma_status_t mma_gemm_lora(int type_in, int type_d, int64_t T, int64_t N,
                            int64_t K, int64_t rank, const void *X, int64_t ldx,
                            const void *W, int64_t ldw, const void *A,
@@ -738,9 +739,9 @@ mma_status_t mma_gemm_lora(int type_in, int type_d, int64_t T, int64_t N,
  *     DA_a = sum U_t^T X_t   (rank x K),     DB_a = sum DY_t^T S_t   (N x rank)
  *
  * with S of the forward call (T x lds) and U of the call for the input's gradient
- * (T x ldu), both FP32, rows on 16-byte boundaries, scales included.
- * type_d  : of DA and DB, type_in or MMA_F32.  An FP32 result takes S and U as sums
- *           of two numbers of type_in, a 16-bit one as one.
+ * (T x ldu), both FP32, any lds and ldu, scales included.
+ * type_d  : of DA and DB, type_in or MMA_F32.  An FP32 result takes S and U as
+ *           sums of two FP16 or three BF16 numbers, a 16-bit one as one.
  * accumulate : nonzero -- added to DA and DB; else an adapter without rows gets
  *           zeros.
  * Sums are FP32, in a fixed order, through `workspace`: 4-byte aligned device

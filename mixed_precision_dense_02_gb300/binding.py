@@ -80,7 +80,7 @@ SIGNATURES = {
                              _i64, _p, _i64, _i64, _p, _i64, _i64, _int, _i64,
                              _p, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _p,
                              _i64, _p]),
-    "mma_gemm_lora_workspace": (_i64, [_int, _i64, _i64]),
+    "mma_gemm_lora_workspace": (_i64, [_int, _int, _i64, _i64, _i64, _i64]),
     "mma_gemm_lora_wgrad": (_int, [_int, _int, _i64, _i64, _i64, _i64, _p, _i64,
                                    _p, _i64, _p, _i64, _p, _i64, _i64, _p, _p,
                                    _i64, _p, _i64, _i64, _p, _i64, _i64, _int,
@@ -1031,7 +1031,7 @@ def _plan_lora(X, W, A, B, offsets, adapters, scales, C, D, b_layout, out_dtype)
             _slices("A", A), _rows("B", B), _slices("B", B),
             MMA_ROW_MAJOR if row else MMA_COL_MAJOR, requests, total,
             0 if C is None else _rows("C", C), N if D is None else _rows("D", D), dtype, lds,
-            load().mma_gemm_lora_workspace(d_code, T, rank),
+            load().mma_gemm_lora_workspace(code, d_code, T, N, rank, requests),
             _one_device(X, W, A, B, offsets, adapters, scales, C, D))
 
 
@@ -1063,15 +1063,23 @@ def gemm_lora(X, W, A, B, offsets, adapters=None, scales=None, C=None, D=None, *
     device = X.device
     if D is None:
         D = torch.empty((T, N), dtype=dtype, device=device)
-    S = torch.empty((T, lds), dtype=torch.float32, device=device)
-    # (its memory goes to other work of the current stream only after the call's)
-    ws = torch.empty((need,), dtype=torch.uint8, device=device)
+    # the sums and behind them the workspace (the memory goes to other work of the
+    # current stream only after the call's)
+    own = 4 * T * lds
+    if sums:
+        S = torch.empty((T, lds), dtype=torch.float32, device=device)
+        ws = torch.empty((need,), dtype=torch.uint8, device=device)
+        s_ptr, w_ptr = S.data_ptr(), ws.data_ptr()
+    else:
+        ws = torch.empty((own + need,), dtype=torch.uint8, device=device)
+        s_ptr = ws.data_ptr()
+        w_ptr = s_ptr + own
     st = load().mma_gemm_lora(
         code, d_code, T, N, K, rank, X.data_ptr(), ldx, W.data_ptr(), ldw, A.data_ptr(), lda,
         stride_a, B.data_ptr(), ldb, stride_b, layout, requests, offsets.data_ptr(),
         None if adapters is None else adapters.data_ptr(), total,
         None if scales is None else scales.data_ptr(), None if C is None else C.data_ptr(),
-        ldc, D.data_ptr(), ldd, S.data_ptr(), lds, ws.data_ptr(), need, _raw_stream(index))
+        ldc, D.data_ptr(), ldd, s_ptr, lds, w_ptr, need, _raw_stream(index))
     if st:
         _check("mma_gemm_lora", st)
     return (D, S[:, :rank]) if sums else D
@@ -1103,8 +1111,8 @@ def _plan_lora_wgrad(dY, X, S, U, offsets, adapters, adapters_total, dA, dB, acc
     d_code = kinds["wide"].get(dtype)
     if d_code is None:
         raise TypeError(f"gemm_lora_wgrad: unsupported result type {dtype}")
-    return (code, d_code, T, N, K, rank, _rows("dY", dY), _rows("X", X), _rows("S", S),
-            _rows("U", U), requests, total, K if dA is None else _rows("dA", dA),
+    return (code, d_code, T, N, K, rank, _rows("dY", dY), _rows("X", X),
+            _row_stride("S", S), _row_stride("U", U), requests, total, K if dA is None else _rows("dA", dA),
             rank * K if dA is None else _slices("dA", dA),
             rank if dB is None else _rows("dB", dB),
             N * rank if dB is None else _slices("dB", dB), dtype,
@@ -1215,8 +1223,9 @@ def route(logits, k: int, *, mask=None, normalize: bool = True, stream=None) -> 
     ints = torch.empty((3 * T * k + E + 2 + need,), dtype=torch.int32, device=device)
     floats = torch.empty((T * k + E + 1,), dtype=torch.float32, device=device)
     n = T * k
-    experts, order, place, offsets, tokens, ws = ints.split((n, n, n, E + 1, 1, need))
-    weights, share, loss = floats.split((n, E, 1))
+    cut = torch.unsafe_split_with_sizes
+    experts, order, place, offsets, tokens = cut(ints, (n, n, n, E + 1, 1 + need))[:5]
+    weights, share, loss = cut(floats, (n, E, 1))
     at, fat = ints.data_ptr(), floats.data_ptr()
     st = load().mma_route(
         code, T, E, k, logits.data_ptr(), ldx, None if mask is None else mask.data_ptr(),
@@ -1226,7 +1235,7 @@ def route(logits, k: int, *, mask=None, normalize: bool = True, stream=None) -> 
     if st:
         _check("mma_route", st)
     return Routing(weights.view(T, k), experts.view(T, k), order, place.view(T, k), offsets,
-                   share, loss.view(()), tokens.view(()))
+                   share, loss[0], tokens[0])
 
 
 def _plan_route_backward(logits, routing, d_weights, d_loss, mask, normalize):

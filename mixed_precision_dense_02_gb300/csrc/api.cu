@@ -1114,21 +1114,34 @@ mma_status_t check_lora(int type_in, int type_d, int64_t T, int64_t N, int64_t K
 
 int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
 
-// The rows' sums: FP32, 16-byte rows of at least `rank`.
+// The rows' sums: FP32, rows of at least `rank`.
 mma_status_t check_sums(const float* s, int64_t ld, int64_t rank) {
   if (s == nullptr || ld < rank) return MMA_ERR_INVALID_ARG;
-  return aligned16(s) && ld % 4 == 0 ? MMA_OK : MMA_ERR_MISALIGNED;
+  return aligned4(s) ? MMA_OK : MMA_ERR_MISALIGNED;
 }
 
-// (an FP32 result takes the sums in two parts of 16 bits)
-int lora_parts(int type_d) { return type_d == MMA_F32 ? 2 : 1; }
+// The workspace: the adapters' rows, then the sums in 16 bits.
+struct LoraSpace {
+  int64_t extra, halves;
+};
+
+LoraSpace lora_space(int type_in, int type_d, int64_t T, int64_t N, int64_t rank,
+                     int64_t requests) {
+  const bool every = T <= kLoraEveryRow;
+  const int64_t rows = every ? T : requests * (kLoraRows - 1);
+  const int64_t parts = every ? 0 : lora_parts(type_in == MMA_BF16, type_d);
+  return LoraSpace{(rows * N * 4 + 15) / 16 * 16, parts * T * round8(rank) * 2};
+}
 
 }  // namespace
 
-extern "C" int64_t mma_gemm_lora_workspace(int type_d, int64_t T, int64_t rank) {
-  return dim_ok(T) && rank > 0 && rank <= MMA_MAX_RANK
-             ? lora_parts(type_d) * T * round8(rank) * 2
-             : 0;
+extern "C" int64_t mma_gemm_lora_workspace(int type_in, int type_d, int64_t T, int64_t N,
+                                           int64_t rank, int64_t requests) {
+  if (!dim_ok(T) || !dim_ok(N) || rank < 1 || rank > MMA_MAX_RANK || requests < 0 ||
+      requests > kMaxGroups)
+    return 0;
+  const LoraSpace s = lora_space(type_in, type_d, T, N, rank, requests);
+  return s.extra + s.halves;
 }
 
 extern "C" mma_status_t mma_gemm_lora(
@@ -1149,11 +1162,11 @@ extern "C" mma_status_t mma_gemm_lora(
   }
   if (rank > 0) {
     MMA_CHECK(check_sums(S, lds, rank));
-    if (lds % 8 != 0 || lds > INT32_MAX) return MMA_ERR_MISALIGNED;
+    if (!aligned16(S) || lds % 8 != 0 || lds > INT32_MAX) return MMA_ERR_MISALIGNED;
     if (adapters) MMA_CHECK(check_words(adapters));
     if (scales) MMA_CHECK(check_words(scales));
-    if (workspace == nullptr ||
-        workspace_bytes < mma_gemm_lora_workspace(type_d, T, rank))
+    const int64_t need = mma_gemm_lora_workspace(type_in, type_d, T, N, rank, requests);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need))
       return MMA_ERR_INVALID_ARG;
     if (!aligned16(workspace)) return MMA_ERR_MISALIGNED;
     if (adapters_total > 0 && K > 0) {
@@ -1201,12 +1214,16 @@ extern "C" mma_status_t mma_gemm_lora(
   g.ldc = ldc;
   g.D = D;
   g.ldd = ldd;
-  LoraLow low = {S, workspace, int(lds), int(round8(rank)), lora_parts(type_d)};
+  const LoraSpace space = lora_space(type_in, type_d, T, N, rank, requests);
+  const int parts = T <= kLoraEveryRow ? 0 : lora_parts(g.bf16, type_d);
+  LoraLow low = {S, static_cast<uint8_t*>(workspace) + space.extra,
+                 static_cast<float*>(workspace), int(lds), int(round8(rank)), parts};
   if (rank > 0) MMA_CHECK(launch_lora_shrink(ctx, g, low));
   if (N == 0) return MMA_OK;
   // without them there is nothing to add
-  if (rank == 0 || requests == 0 || adapters_total == 0 || K == 0) low.parts = 0;
-  return launch_gemm_lora(ctx, g, low);
+  const bool plain = rank == 0 || requests == 0 || adapters_total == 0 || K == 0;
+  if (!plain) MMA_CHECK(launch_lora_expand(ctx, g, low));
+  return launch_gemm_lora(ctx, g, plain ? nullptr : &low);
 }
 
 extern "C" int64_t mma_gemm_lora_wgrad_workspace(int64_t T, int64_t N, int64_t K,

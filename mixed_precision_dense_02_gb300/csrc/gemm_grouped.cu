@@ -119,17 +119,15 @@ struct GroupedArgs {
   int q_shift;
   int withhold;  // (self-test) issue no loads
   unsigned* status;
-  // LORA: `offsets` are those of `groups` requests, which cut nothing.  Request i's
-  // rows have the adapter adapters[i] (NULL: i; outside [0, adapters_total): none),
-  // whose `rank` sums per row are in low (FP32, low_ld apart) and, in `parts` parts
-  // of 16 bits, behind tmD; its second matrix is at up + adapter * up_slice, rows
-  // of P up_ld apart (P_MN: sums up_ld apart), and behind tmZ.rows[0].
+  // LORA: what the adapters add in FP32, rows of p_size.  kEveryRow: of every row of
+  // Q.  kRequests: `offsets` are those of `groups` requests, which cut nothing.
+  // Request i's rows have the adapter adapters[i] (NULL: i; outside [0,
+  // adapters_total): none), whose `rank` sums per row are, in `parts` parts of 16
+  // bits, behind tmD, and whose second matrix is behind tmZ.rows[0]; `extra` has
+  // rows for the requests of fewer than kLoraRows rows, kLoraRows - 1 for each.
+  const float* extra;
   const int* adapters;
   int adapters_total, rank, parts;
-  const float* low;
-  int low_ld;
-  const uint16_t* up;
-  int64_t up_ld, up_slice;
 };
 
 template <bool KIND8, bool ROWS, bool SPLIT, int CL, int BN, int STAGES>
@@ -246,19 +244,23 @@ __device__ __forceinline__ void store_d4(void* d, int64_t i, int t, float4 v) {
 __device__ constexpr int pairs_row(int s) { return ((s >> 4) & 1) * 16 + ((s >> 1) & 1) * 8; }
 __device__ constexpr int pairs_q(int s) { return (s >> 5) * 32 + ((s >> 2) & 3) * 8 + (s & 1); }
 
-// LORA: rows of a request in a tile from which its share is a product of the
-// tensor core's, with an accumulator of its own of which only those rows are
-// added; fewer rows' shares are summed by the epilogue's lanes.
-constexpr int kLoraRows = 8;
+// LORA: what the adapters of requests add to a product's rows.  kEveryRow: FP32
+// rows that another kernel has made.  kRequests: products of the tensor core's, a
+// request at a time, with an accumulator of its own of which only the request's
+// columns are added, so that an adapter's infinities stay with it; requests of fewer
+// than kLoraRows rows as with kEveryRow.  (Both wait for the kernels before only
+// where they read what those make, so that the shared product runs beside them.)
+enum Lora { kNoLora, kEveryRow, kRequests };
 
 // KIND8: 8-bit operands with scales, else 16-bit.  P_MN, Q_MN: the operand
 // is stored with its row index contiguous (16-bit only).  RAGK: the groups
 // cut the k range (the weight gradient).  ROWS: D[p][q], the groups cut P.
 // SPLIT: the CTAs of a cluster share the k range (CL = 1, K-major).  LORA: one
-// group, whose rows have adapters (16-bit, neither RAGK nor ROWS).
+// group (16-bit, neither RAGK nor ROWS).
 template <bool KIND8, bool P_MN, bool Q_MN, bool RAGK, bool ROWS, bool SPLIT, int CL,
-          int BN, int STAGES, bool LORA>
-__global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
+          int BN, int STAGES, Lora LORA>
+__global__ void __launch_bounds__(kThreads,
+                                  SPLIT && (BN == 32 || (LORA && BN == 64)) ? 2 : 1)
     gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP,
                         const __grid_constant__ CUtensorMap tmQ,
                         const __grid_constant__ CUtensorMap tmD,
@@ -346,9 +348,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
   // All of this overlaps the end of the kernel before this one, which every
   // role waits for before its first global access.
   if (warp == 0) {
-    if constexpr (LORA) {
+    if constexpr (LORA == kRequests) {
       // the requests' bounds and, in the place of the groups' units, adapters
-      grid_dependency_wait();
       int row = min(max(__ldg(a.offsets), 0), a.rows_total);
       if (lane == 0) grow[0] = row;
       for (int base = 0; base < a.groups; base += 32) {
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
   tc_fence_after();
   grid_dependents_start();
   const uint32_t tmem_base = *tmem_slot;
-  const int units = LORA ? units_of(a.rows_total) : gunit[a.groups];
+  const int units = LORA == kRequests ? units_of(a.rows_total) : gunit[a.groups];
   const int first_unit = blockIdx.x / (CL * ksplit);
   const int unit_step = gridDim.x / (CL * ksplit);
 
@@ -434,15 +435,16 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
   // fastest a group's few q tiles read its P panels at different times:
   // grouped forward 181 us, so 176).
   auto decode = [&](int u) {
-    int lo = 0, hi = LORA ? 1 : a.groups;
+    int lo = 0, hi = LORA == kRequests ? 1 : a.groups;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (gunit[mid] <= u) lo = mid; else hi = mid;
     }
     Tile t;
     t.e = lo;
-    const int r = LORA ? u : u - gunit[lo];
-    const int g0 = LORA ? 0 : grow[lo], g1 = LORA ? a.rows_total : grow[lo + 1];
+    const int r = LORA == kRequests ? u : u - gunit[lo];
+    const int g0 = LORA == kRequests ? 0 : grow[lo];
+    const int g1 = LORA == kRequests ? a.rows_total : grow[lo + 1];
     const int np = ROWS ? (g1 - g0 + PT - 1) / PT : p_tiles;
     const int nq = RAGK || ROWS ? q_tiles : (g1 - g0 + BN - 1) / BN;
     // (divisions cost a lone thread some hundred clocks each)
@@ -480,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     return t;
   };
 
-  // (LORA) f(request, its first row, one past its last) for the requests with an
+  // (kRequests) f(request, its first row, one past its last) for the requests with an
   // adapter that have rows in the tile.
   [[maybe_unused]] auto each_request = [&](const Tile& t, auto&& f) {
     int lo = 0, hi = a.groups;  // the last request that starts by the tile's start
@@ -493,12 +495,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
       if (to > from && gunit[i] >= 0) f(i, from, to);
     }
   };
-  // (LORA) whether a request's share of the tile is a product of this CTA's: the
-  // CTAs that share a tile's k range share its requests.
-  [[maybe_unused]] auto as_product = [&](int i, int from, int to) {
-    return to - from >= kLoraRows && (!SPLIT || i % ksplit == krank);
-  };
-  [[maybe_unused]] const int lora_blocks = LORA ? (a.rank + 63) / 64 : 0;
+  [[maybe_unused]] auto as_product = [&](int i) { return grow[i + 1] - grow[i] >= kLoraRows; };
+  [[maybe_unused]] const int lora_blocks = LORA == kRequests ? (a.rank + 63) / 64 : 0;
 
   if (warp < 4) {
   if constexpr (kSplitRegs) registers_give<kLoadRegs>();
@@ -512,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
       // the leader CTA's full barriers, which count both CTAs' bytes
       const uint32_t full_lead =
           CL > 1 ? mapa_shared(smem_u32(&full[0]), 0) : 0u;
-      grid_dependency_wait();
+      if constexpr (!LORA) grid_dependency_wait();
       for (int u = first_unit; u < units && ok; u += unit_step) {
         const Tile t = decode(u);
         const int py = t.p0 + rank * kP;
@@ -567,9 +565,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
             phase ^= 1u;
           }
         }
-        if constexpr (LORA) {
-          each_request(t, [&](int i, int from, int to) {
-            if (!as_product(i, from, to)) return;
+        if constexpr (LORA == kRequests) {
+          grid_dependency_wait();
+          each_request(t, [&](int i, int, int) {
+            if (!as_product(i)) return;
             for (int b = 0; b < lora_blocks * a.parts && ok; ++b) {
               if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.status)) {
                 ok = false;
@@ -620,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     if (elect_one()) {
       // (touches no memory, but its bounded waits are not to run while the
       // kernel before does)
-      grid_dependency_wait();
+      if constexpr (!LORA) grid_dependency_wait();
       int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
       [[maybe_unused]] uint32_t cut_phase = 0;  // one bit per stage
@@ -727,9 +726,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
             acc_phase ^= 1u;
           }
         }
-        if constexpr (LORA) {
-          each_request(t, [&](int i, int from, int to) {
-            if (!ok || !as_product(i, from, to)) return;
+        if constexpr (LORA == kRequests) {
+          each_request(t, [&](int i, int, int) {
+            if (!ok || !as_product(i)) return;
             ok = mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, a.status);
             if (!ok) return;
             tc_fence_after();
@@ -909,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
     const uint32_t tempty_lead =
         mapa_shared(smem_u32(&tempty[0]), CL > 1 ? 0 : cluster_ctarank());
     [[maybe_unused]] int block = 0;  // of the ring of blocks of D
-    grid_dependency_wait();
+    if constexpr (!LORA) grid_dependency_wait();
     [[maybe_unused]] const int part_at =
         L::part_offset(a.groups) + (quarter * 32 + lane) * 4;
     for (int u = first_unit; u < units && ok; u += unit_step) {
@@ -1005,9 +1004,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
 #pragma unroll
             for (int j = 0; j < CB; ++j) sum[i * CB + j] += __uint_as_float(r[j]);
           });
-        if constexpr (LORA) {
+        if constexpr (LORA == kRequests) {
           each_request(t, [&](int i, int from, int to) {
-            if (!as_product(i, from, to)) return;
+            if (!as_product(i)) return;
             // (what other rows' sums with this adapter are does not matter)
             take([&](int b, const uint32_t (&r)[CB]) {
               const int first = t.q0 + column(b) - from;
@@ -1017,95 +1016,36 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
                   sum[b * CB + j] += __uint_as_float(r[j]);
             });
           });
-          // Requests of a few rows: a lane's row of P of the adapter's second matrix
-          // times the row's sums, kAtOnce rows' loads under way together.
+          // the rows of small requests, kAtOnce of the warp's columns at a time
+          grid_dependency_wait();
           constexpr int kAtOnce = 4;
-          int req = 0, q = t.q0;
-          for (int hi = a.groups; hi - req > 1;) {
-            const int mid = (req + hi) >> 1;
-            if (grow[mid] <= t.q0) req = mid; else hi = mid;
-          }
-          while (true) {
-            // the warp's next rows: q of request req and on
-            int n = 0, row[kAtOnce], who[kAtOnce];
-            while (n < kAtOnce && req < a.groups && q < t.q1) {
-              if (grow[req] >= t.q1) break;
-              const int from = max(grow[req], t.q0), to = min(grow[req + 1], t.q1);
-              if (q < from) q = from;
-              if (q >= to || gunit[req] < 0 || to - from >= kLoraRows) {
-                ++req;
-                continue;
-              }
+          int n = 0, at[kAtOnce];
+          float v[kAtOnce];
+          auto add = [&] {
+#pragma unroll
+            for (int x = 0; x < kAtOnce; ++x)
+#pragma unroll
+              for (int j = 0; j < HALF; ++j) sum[j] += x < n && j == at[x] ? v[x] : 0.f;
+            n = 0;
+          };
+          each_request(t, [&](int i, int from, int to) {
+            if (as_product(i)) return;
+            for (int q = from; q < to; ++q) {
               const int c = q - t.q0;
-              if ((c / CB & 1) == h && (!SPLIT || c % ksplit == krank)) {
+              if ((c / CB & 1) != h) continue;
+              const float* e =
+                  a.extra + int64_t(i * (kLoraRows - 1) + q - grow[i]) * a.p_size + p;
+              const float w = p < t.p1 ? *e : 0.f;
 #pragma unroll
-                for (int x = 0; x < kAtOnce; ++x)
-                  if (x == n) {
-                    row[x] = q;
-                    who[x] = gunit[req];
-                  }
-                ++n;
-              }
-              ++q;
-            }
-            if (n == 0) break;
-            float v[kAtOnce];
-#pragma unroll
-            for (int x = 0; x < kAtOnce; ++x) {
-              v[x] = 0.f;
-              if (x >= n) {  // (what there is twice is not added)
-                row[x] = row[0];
-                who[x] = who[0];
-              }
-            }
-#pragma unroll 1
-            for (int k = 0; k < a.rank; k += 8) {
-              uint4 w[kAtOnce];
-#pragma unroll
-              for (int x = 0; x < kAtOnce; ++x) {
-                w[x] = make_uint4(0, 0, 0, 0);
-                if (p >= t.p1) continue;
-                const uint16_t* src = a.up + who[x] * a.up_slice;
-                if constexpr (P_MN) {
-                  uint32_t f[8];
-#pragma unroll
-                  for (int y = 0; y < 8; ++y)
-                    f[y] = k + y < a.rank ? src[int64_t(k + y) * a.up_ld + p] : 0u;
-                  w[x] = make_uint4(f[0] | f[1] << 16, f[2] | f[3] << 16, f[4] | f[5] << 16,
-                                    f[6] | f[7] << 16);
-                } else {
-                  w[x] = __ldg(reinterpret_cast<const uint4*>(src + int64_t(p) * a.up_ld + k));
+              for (int x = 0; x < kAtOnce; ++x)
+                if (x == n) {
+                  at[x] = c / (2 * CB) * CB + c % CB;
+                  v[x] = w;
                 }
-              }
-              // (what stands behind a row's rank numbers is none of them)
-              const int left = a.rank - k;
-#pragma unroll
-              for (int x = 0; x < kAtOnce; ++x) {
-                const float4* s =
-                    reinterpret_cast<const float4*>(a.low + int64_t(row[x]) * a.low_ld + k);
-                uint32_t f[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  if (!P_MN && left < 2 * y + 2) f[y] = left <= 2 * y ? 0u : f[y] & 0xFFFFu;
-                  const float2 b =
-                      (a.idesc >> 7) & 1
-                          ? make_float2(__uint_as_float(f[y] << 16),
-                                        __uint_as_float(f[y] & 0xFFFF0000u))
-                          : __half22float2(*reinterpret_cast<const __half2*>(&f[y]));
-                  const float2 l = reinterpret_cast<const float2*>(s)[y];
-                  v[x] = fmaf(l.x, b.x, v[x]);
-                  v[x] = fmaf(l.y, b.y, v[x]);
-                }
-              }
+              if (++n == kAtOnce) add();
             }
-#pragma unroll
-            for (int x = 0; x < kAtOnce; ++x) {
-              const int c = row[x] - t.q0;
-              const int at = x < n ? c / (2 * CB) * CB + c % CB : -1;
-#pragma unroll
-              for (int j = 0; j < HALF; ++j) sum[j] += j == at ? v[x] : 0.f;
-            }
-          }
+          });
+          if (n) add();
         }
       } else {
         static_assert(L::SLOTS == 2);
@@ -1370,7 +1310,20 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BN == 32 ? 2 : 1)
               d[pairs_q(s) * a.ldd + pairs_row(s)] = uint16_t(pack16(sum[s], 0.f, bf16));
         }
       } else {
+        if constexpr (LORA) grid_dependency_wait();
         if (p >= t.p1) continue;
+        if constexpr (LORA == kEveryRow) {
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const float* e = a.extra + int64_t(t.q0 + column(i)) * a.p_size + p;
+            const int left = t.q1 - t.q0 - column(i);
+            float v[CB];
+#pragma unroll
+            for (int j = 0; j < CB; ++j) v[j] = j < left ? e[int64_t(j) * a.p_size] : 0.f;
+#pragma unroll
+            for (int j = 0; j < CB; ++j) sum[i * CB + j] += v[j];
+          }
+        }
         const int64_t group = RAGK ? t.e : 0;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
@@ -1447,7 +1400,7 @@ struct LoraMaps {
 };
 
 template <bool KIND8, bool P_MN, bool Q_MN, bool RAGK, bool ROWS, bool SPLIT, int CL,
-          int BN, int STAGES, bool LORA = false>
+          int BN, int STAGES, Lora LORA = kNoLora>
 mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
                  const GroupedArgs& args, const LoraMaps* lora = nullptr) {
   using L = Layout<KIND8, ROWS, SPLIT, CL, BN, STAGES>;
@@ -1459,7 +1412,7 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
   // an upper bound of the units, whatever the offsets: a group with n rows
   // has at most n tiles' rows of them, and full tiles besides one
   auto tiles_of = [&](int64_t rows, int64_t per) {
-    return args.offsets && !LORA
+    return args.offsets && LORA != kRequests
                ? std::min<int64_t>(rows, rows / per + args.groups)
                : (rows + per - 1) / per;
   };
@@ -1487,8 +1440,7 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
     return MMA_ERR_LAUNCH;
   GroupedArgs a = args;
   td = tp;
-  if constexpr (LORA) {
-    // (one slice more than there are adapters or parts is never addressed)
+  if constexpr (LORA == kRequests) {
     const Operand &u = lora->up, &l = lora->low;
     if (!(P_MN ? make_map(&tz.rows[0], u.p, EB, args.p_size, args.rank, u.ld, u.slices,
                           u.slices > 1 ? u.slice : u.ld, 64, 64)
@@ -1497,7 +1449,7 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
         !make_map(&td, l.p, EB, args.rank, l.rows, l.ld, l.slices, l.slice, KE, BN / CL))
       return MMA_ERR_LAUNCH;
   }
-  for (int e = LORA ? 1 : 0; e < 4; ++e) {
+  for (int e = LORA == kRequests ? 1 : 0; e < 4; ++e) {
     tz.rows[e] = tp;  // (read beyond their end only)
     if (RAGK && args.k_size > 0 &&
         !make_map(&tz.rows[e], P.p, EB, args.p_size, P.rows, P.ld, 1, P.ld, 64, 1 << e,
@@ -1528,7 +1480,7 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
   int split = 1;
   if constexpr (SPLIT) {
     const int64_t blocks = (int64_t(a.k_size) + KE - 1) / KE;
-    a.part_cols = a.offsets && !LORA ? BN : std::min(BN, a.rows_total);
+    a.part_cols = a.offsets ? BN : std::min(BN, a.rows_total);
     for (int s = kMostSplit; s > 1 && split == 1; --s) {
       const int64_t slots =
           ctx.num_sms * (2 * (L::alloc(a.groups, s, a.part_cols) + 1024) <= 233472 ? 2 : 1);
@@ -1595,20 +1547,19 @@ bool elements_aligned(const void* p, int64_t ld, int bytes, int n) {
 // 32 rows: 32 columns 10.4 us, 64 11.0, 128 11.3; 64 rows: 64 columns 12.5 us,
 // 128 12.7; 128 rows: 128 columns 16.0 us, pairs with 256 17.9.  32 experts of
 // 4096 x 2048 by 64 rows, 16-bit, streamed: 64 columns 94.7 us, 128 87.9.
-template <bool KIND8, bool LORA = false>
+template <bool KIND8, Lora LORA = kNoLora>
 mma_status_t few_rows(const Ctx& ctx, const Operand& B, const Operand& A,
-                      const GroupedArgs& a, int64_t per, const LoraMaps* lora = nullptr) {
-  const int64_t tiles =
-      (a.p_size + kP - 1) / kP *
-      (a.offsets && !LORA ? std::min<int64_t>(a.rows_total, a.groups) : 1);
+                      const GroupedArgs& a, int64_t per) {
+  const int64_t tiles = (a.p_size + kP - 1) / kP *
+                        (a.offsets ? std::min<int64_t>(a.rows_total, a.groups) : 1);
   const bool split = tiles < ctx.num_sms;
   if (per <= 32)
-    return split ? run<KIND8, false, false, false, false, true, 1, 32, 4, LORA>(ctx, B, A, a, lora)
-                 : run<KIND8, false, false, false, false, false, 1, 32, 8, LORA>(ctx, B, A, a, lora);
+    return split ? run<KIND8, false, false, false, false, true, 1, 32, 4, LORA>(ctx, B, A, a)
+                 : run<KIND8, false, false, false, false, false, 1, 32, 8, LORA>(ctx, B, A, a);
   if (per <= 64 && split)
-    return run<KIND8, false, false, false, false, true, 1, 64, 4, LORA>(ctx, B, A, a, lora);
-  return split ? run<KIND8, false, false, false, false, true, 1, 128, 4, LORA>(ctx, B, A, a, lora)
-               : run<KIND8, false, false, false, false, false, 1, 128, 6, LORA>(ctx, B, A, a, lora);
+    return run<KIND8, false, false, false, false, true, 1, 64, 4, LORA>(ctx, B, A, a);
+  return split ? run<KIND8, false, false, false, false, true, 1, 128, 4, LORA>(ctx, B, A, a)
+               : run<KIND8, false, false, false, false, false, 1, 128, 6, LORA>(ctx, B, A, a);
 }
 
 }  // namespace
@@ -1710,7 +1661,7 @@ mma_status_t launch_gemm_grouped(const Ctx& ctx, const GroupedProblem& g) {
   return few_rows<false>(ctx, B, A, a, per);
 }
 
-mma_status_t launch_gemm_lora(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
+mma_status_t launch_gemm_lora(const Ctx& ctx, const LoraProblem& g, const LoraLow* low) {
   GroupedArgs a = {};
   a.p_size = int(g.N);
   a.q_size = int(g.rows);
@@ -1725,10 +1676,10 @@ mma_status_t launch_gemm_lora(const Ctx& ctx, const LoraProblem& g, const LoraLo
   a.status = ctx.status;
   const Operand X = {g.X, g.ldx, g.rows, 1, 0};
   const Operand W = {g.W, g.ldw, g.row_major ? g.K : g.N, 1, 0};
-  const bool pair = g.rows > 128;
+  const bool pair = g.rows > kLoraEveryRow;
   a.idesc = idesc_f32(g.bf16, g.bf16, g.row_major, false, pair ? 2 * kP : kP);
   a.groups = 1;
-  if (low.parts == 0) {  // no requests, no sums: the shared product alone
+  if (!low) {
     if (g.row_major) {
       if (pair) return run<false, true, false, false, false, false, 2, 256, 6>(ctx, W, X, a);
       return run<false, true, false, false, false, false, 1, 128, 6>(ctx, W, X, a);
@@ -1736,27 +1687,23 @@ mma_status_t launch_gemm_lora(const Ctx& ctx, const LoraProblem& g, const LoraLo
     if (pair) return run<false, false, false, false, false, false, 2, 256, 6>(ctx, W, X, a);
     return few_rows<false>(ctx, W, X, a, g.rows);
   }
+  a.extra = low->extra;
+  if (!pair) {
+    if (g.row_major)
+      return run<false, true, false, false, false, false, 1, 128, 6, kEveryRow>(ctx, W, X, a);
+    return few_rows<false, kEveryRow>(ctx, W, X, a, g.rows);
+  }
   a.groups = int(g.requests);
   a.offsets = g.offsets;
   a.adapters = g.adapters;
   a.adapters_total = int(g.adapters_total);
   a.rank = int(g.rank);
-  a.parts = low.parts;
-  a.low = low.f32;
-  a.low_ld = low.ld32;
-  a.up = static_cast<const uint16_t*>(g.B);
-  a.up_ld = g.ldb;
-  a.up_slice = g.stride_b;
+  a.parts = low->parts;
   const LoraMaps m = {{g.B, g.ldb, g.N, g.adapters_total, g.stride_b},
-                      {low.f16, low.ld16, g.rows, low.parts, int64_t(low.ld16) * g.rows}};
-  if (g.row_major) {
-    if (pair)
-      return run<false, true, false, false, false, false, 2, 256, 6, true>(ctx, W, X, a, &m);
-    return run<false, true, false, false, false, false, 1, 128, 6, true>(ctx, W, X, a, &m);
-  }
-  if (pair)
-    return run<false, false, false, false, false, false, 2, 256, 6, true>(ctx, W, X, a, &m);
-  return few_rows<false, true>(ctx, W, X, a, g.rows, &m);
+                      {low->f16, low->ld16, g.rows, low->parts, int64_t(low->ld16) * g.rows}};
+  if (g.row_major)
+    return run<false, true, false, false, false, false, 2, 256, 6, kRequests>(ctx, W, X, a, &m);
+  return run<false, false, false, false, false, false, 2, 256, 6, kRequests>(ctx, W, X, a, &m);
 }
 
 mma_status_t launch_gemm_grouped_wgrad(const Ctx& ctx, const WgradProblem& g) {

@@ -250,15 +250,28 @@ struct LoraProblem {
   void* D;
   int64_t ldd;
 };
-// The rows' sums scale * (X A): in FP32 (ld32 a multiple of 8, so that eight can be
-// read from any eighth one) and as `parts` matrices of 16 bits whose sum they are.
+// What its kernels hand on.  The rows' sums scale * (X A): in FP32 (ld32 a multiple
+// of 8, so that eight can be read from any eighth one) and, for more rows than
+// kLoraEveryRow, as `parts` matrices of 16 bits whose sum they are.  In `extra` what
+// the adapters add, FP32 rows of N: with up to kLoraEveryRow rows for all of them,
+// else for the requests of fewer than kLoraRows rows, kLoraRows - 1 for each request.
+constexpr int kLoraEveryRow = 128, kLoraRows = 8;
+// Numbers of 16 bits that stand for an FP32 sum in a product: for an FP32 result as
+// many as hold its 24 bits (BF16 three of 8, FP16 two of 11, which leave 2^-22 of
+// it), for a 16-bit one, whose own rounding is as large, one.
+constexpr int lora_parts(bool bf16, int d_type) {
+  return d_type != MMA_F32 ? 1 : bf16 ? 3 : 2;
+}
 struct LoraLow {
   float* f32;
   void* f16;
+  float* extra;
   int ld32, ld16, parts;
 };
 mma_status_t launch_lora_shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low);
-mma_status_t launch_gemm_lora(const Ctx& ctx, const LoraProblem& g, const LoraLow& low);
+mma_status_t launch_lora_expand(const Ctx& ctx, const LoraProblem& g, const LoraLow& low);
+// (low NULL: the shared product alone)
+mma_status_t launch_gemm_lora(const Ctx& ctx, const LoraProblem& g, const LoraLow* low);
 
 // The adapters' gradients: DB = sum of DY^T S (N x rank), DA = sum of U^T X (rank x
 // K) over each adapter's rows.

@@ -104,16 +104,16 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
     mma_f16_16816(d, a, b);
 }
 
-// 16 bits of v, and (lo) of what they leave of it.
+// 16 bits of v; v becomes what they leave of it.
 template <bool BF16>
-__device__ __forceinline__ uint16_t half_of(float v, uint16_t* lo) {
+__device__ __forceinline__ uint16_t take_half(float& v) {
   if constexpr (BF16) {
     const __nv_bfloat16 h = __float2bfloat16_rn(v);
-    *lo = __bfloat16_as_ushort(__float2bfloat16_rn(v - __bfloat162float(h)));
+    v -= __bfloat162float(h);
     return __bfloat16_as_ushort(h);
   } else {
     const __half h = __float2half_rn(v);
-    *lo = __half_as_ushort(__float2half_rn(v - __half2float(h)));
+    v -= __half2float(h);
     return __half_as_ushort(h);
   }
 }
@@ -162,10 +162,8 @@ __global__ void __launch_bounds__(kThreads)
     if (n >= rank) v = 0.f;
     if (n < low.ld32) low.f32[t * low.ld32 + n] = v;
     if (n < low.ld16) {
-      uint16_t lo;
       uint16_t* d = static_cast<uint16_t*>(low.f16) + t * low.ld16 + n;
-      d[0] = half_of<BF16>(v, &lo);
-      if (low.parts > 1) d[g.rows * low.ld16] = lo;
+      for (int i = 0; i < low.parts; ++i) d[i * g.rows * low.ld16] = take_half<BF16>(v);
     }
   };
   if (who < 0) {
@@ -315,6 +313,121 @@ mma_status_t by_rank(int64_t rank, F&& f) {
   return f(std::integral_constant<int, 128>{});
 }
 
+// ----------------------------------------------- what the sums add, few rows
+
+// extra[row][p] = sum over n of s[row][n] B[n][p], FP32, a lane per p: of every row
+// (EVERY: pieces of eight rows, zeros where there is no adapter) or of the requests
+// of fewer than kLoraRows rows.  Bound by B's bytes and latency.  The grid is small
+// enough to be on the SMs at once with its neighbours, so that the shared product
+// after it starts before it ends.
+template <bool BF16, bool ROW, bool EVERY>
+__global__ void __launch_bounds__(kThreads)
+    lora_expand_kernel(const LoraProblem g, const LoraLow low, int units) {
+  constexpr int kCols = 4;  // p per thread at a time, their loads together
+  __shared__ int bound[MMA_MAX_GROUPS + 3], scan[kThreads / 32];
+  grid_dependents_start();
+  const int requests = int(g.requests), rank = int(g.rank), N = int(g.N);
+  load_bounds(bound, g.offsets, requests, int(g.rows), scan);
+  bool ready = false;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    Piece piece;
+    if constexpr (EVERY) {
+      piece = piece_of(bound, requests, 8, u);
+    } else {
+      piece = Piece{u + 1, bound[u + 1], bound[u + 2]};
+      if (piece.to - piece.from >= kLoraRows) continue;
+    }
+    if (piece.to <= piece.from) continue;
+    const int who = adapter_of(piece.request, requests, g.adapters, int(g.adapters_total));
+    if (!EVERY && who < 0) continue;
+    const uint16_t* const B = static_cast<const uint16_t*>(g.B) + (who < 0 ? 0 : who * g.stride_b);
+    // (the offsets and B are older than the kernel before this one, the sums are not)
+    if (!ready) grid_dependency_wait();
+    ready = true;
+    for (int p0 = blockIdx.y * kThreads * kCols; p0 < N; p0 += gridDim.y * kThreads * kCols) {
+      for (int t = piece.from; t < piece.to; ++t) {
+        const float* s = low.f32 + int64_t(t) * low.ld32;
+        float v[kCols];
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) v[x] = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < rank && who >= 0; k += 8) {
+          uint4 w[kCols];
+          const int left = rank - k;
+#pragma unroll
+          for (int x = 0; x < kCols; ++x) {
+            const int p = p0 + x * kThreads + threadIdx.x;
+            w[x] = make_uint4(0, 0, 0, 0);
+            if (p >= N) continue;
+            if constexpr (ROW) {
+              uint32_t f[8];
+#pragma unroll
+              for (int y = 0; y < 8; ++y) f[y] = y < left ? B[(k + y) * g.ldb + p] : 0u;
+              w[x] = make_uint4(f[0] | f[1] << 16, f[2] | f[3] << 16, f[4] | f[5] << 16,
+                                f[6] | f[7] << 16);
+            } else {
+              w[x] = __ldg(reinterpret_cast<const uint4*>(B + p * g.ldb + k));
+            }
+          }
+          const float4 s0 = *reinterpret_cast<const float4*>(s + k);
+          const float4 s1 = *reinterpret_cast<const float4*>(s + k + 4);
+          const float2 f[4] = {make_float2(s0.x, s0.y), make_float2(s0.z, s0.w),
+                               make_float2(s1.x, s1.y), make_float2(s1.z, s1.w)};
+#pragma unroll
+          for (int x = 0; x < kCols; ++x) {
+            uint32_t q[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              // (what stands behind a row's rank numbers is none of them)
+              if (!ROW && left < 2 * y + 2) q[y] = left <= 2 * y ? 0u : q[y] & 0xFFFFu;
+              float2 b;
+              if constexpr (BF16)
+                b = make_float2(__uint_as_float(q[y] << 16), __uint_as_float(q[y] & 0xFFFF0000u));
+              else
+                b = __half22float2(*reinterpret_cast<const __half2*>(&q[y]));
+              v[x] = fmaf(f[y].x, b.x, v[x]);
+              v[x] = fmaf(f[y].y, b.y, v[x]);
+            }
+          }
+        }
+        const int64_t row =
+            EVERY ? t : int64_t(u) * (kLoraRows - 1) + t - piece.from;
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) {
+          const int p = p0 + x * kThreads + threadIdx.x;
+          if (p < N) low.extra[row * N + p] = v[x];
+        }
+      }
+    }
+  }
+  // (a kernel after this one may count on the one before being done)
+  if (!ready) grid_dependency_wait();
+}
+
+template <bool BF16, bool ROW>
+mma_status_t expand(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
+  const bool every = g.rows <= kLoraEveryRow;
+  const int64_t units = every ? (g.rows + 7) / 8 + g.requests + 1 : g.requests;
+  const int64_t columns = (g.N + kThreads * 4 - 1) / (kThreads * 4);
+  const int64_t most = ctx.num_sms * 2;
+  const int64_t x = std::min(units, most);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(x), unsigned(std::max<int64_t>(1, std::min(columns, most / x))), 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = ctx.stream;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, every ? lora_expand_kernel<BF16, ROW, true>
+                                     : lora_expand_kernel<BF16, ROW, false>,
+                         g, low, int(units));
+  const cudaError_t after = cudaGetLastError();
+  return e == cudaSuccess && after == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
+}
+
 // ------------------------------------------------- the adapters' own gradients
 
 // One side of the gradient: features of M (T x F) times the rows' sums.
@@ -334,7 +447,7 @@ struct WgradArgs {
   int tiles0;    // tiles of 128 features of the first side
   int T, rank, requests, total, per;
   const int *offsets, *adapters;
-  int d_type;
+  int d_type, parts;
   bool accumulate;
   float* part;  // [pieces][rank][features of both sides]
 };
@@ -348,13 +461,12 @@ struct Wgrad {
   static constexpr int STAGE = M_BYTES + L_BYTES;
   static constexpr int HALF_BYTES = kStageRows * RP * 2;  // the sums in 16 bits, a part
   static constexpr int STAGES = RP <= 64 ? 4 : 3;
-  static constexpr int SMEM = STAGES * STAGE + 2 * HALF_BYTES;
+  static constexpr int SMEM = STAGES * STAGE + 3 * HALF_BYTES;
 };
 
 // Piece blockIdx.x's share of 128 features: G[f][n] = sum over its rows M[t][f] *
-// low[t][n] on the tensor cores, FP32.  The sums come in FP32 and are taken as two
-// parts of 16 bits for an FP32 gradient, whose rounding would show otherwise, as
-// one for a 16-bit one.
+// low[t][n] on the tensor cores, FP32.  The sums come in FP32 and are taken as a sum
+// of `parts` numbers of 16 bits (see lora_parts).
 template <bool BF16, int RP>
 __global__ void __launch_bounds__(kThreads)
     lora_wgrad_kernel(const WgradArgs a) {
@@ -372,7 +484,8 @@ __global__ void __launch_bounds__(kThreads)
   const uint16_t* const M = side.m + piece.from * side.ldm + f0;
   const float* const S = side.low + piece.from * side.ldl;
   const int F = side.F - f0, rank = a.rank;
-  const bool two = a.d_type == MMA_F32;
+  // 16 bytes of a row of sums at a time
+  const bool wide = side.ldl % 4 == 0 && (reinterpret_cast<uintptr_t>(side.low) & 15) == 0;
   const uint32_t base = smem_u32(smem), half = base + L::STAGES * L::STAGE;
   const int steps = (rows + kStageRows - 1) / kStageRows;
   auto load = [&](int step) {
@@ -386,8 +499,15 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = threadIdx.x; i < kStageRows * RP / 4; i += kThreads) {
       const int row = i / (RP / 4), c = i % (RP / 4), t = step * kStageRows + row;
-      const int n = t < rows ? min(max(rank - c * 4, 0), 4) * 4 : 0;
-      cp_async_16_zfill(ls + i * 16, n ? S + t * side.ldl + c * 4 : side.low, n);
+      const int n = t < rows ? min(max(rank - c * 4, 0), 4) : 0;
+      const float* src = S + t * side.ldl + c * 4;
+      if (wide) {
+        cp_async_16_zfill(ls + i * 16, n ? src : side.low, n * 4);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          cp_async_4_zfill(ls + i * 16 + j * 4, j < n ? src + j : side.low, j < n ? 4 : 0);
+      }
     }
   };
   float acc[RP / 8][4];
@@ -410,19 +530,19 @@ __global__ void __launch_bounds__(kThreads)
                                                      L::M_BYTES);
     for (int i = threadIdx.x; i < kStageRows * RP / 8; i += kThreads) {
       const int row = i / (RP / 8), c = i % (RP / 8);
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint16_t l0, l1;
-        const float2 v = *reinterpret_cast<const float2*>(ls + i * 8 + 2 * j);
-        const uint32_t h0 = half_of<BF16>(v.x, &l0), h1 = half_of<BF16>(v.y, &l1);
-        hi[j] = h0 | h1 << 16;
-        lo[j] = uint32_t(l0) | uint32_t(l1) << 16;
-      }
+      float v[8];
+      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(ls + i * 8);
+      *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(ls + i * 8 + 4);
       uint8_t* d = smem + L::STAGES * L::STAGE + swizzled<RP * 2>(row, c);
-      *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      if (two)
-        *reinterpret_cast<uint4*>(d + L::HALF_BYTES) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      for (int part = 0; part < a.parts; ++part, d += L::HALF_BYTES) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t h0 = take_half<BF16>(v[2 * j]), h1 = take_half<BF16>(v[2 * j + 1]);
+          w[j] = h0 | h1 << 16;
+        }
+        *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
     __syncthreads();
 #pragma unroll
@@ -434,11 +554,10 @@ __global__ void __launch_bounds__(kThreads)
       for (int n = 0; n < RP / 16; ++n) {
         uint32_t b[4];
         const int where = swizzled<RP * 2>(k + (m & 1) * 8 + at, n * 2 + (m >> 1));
-        ldmatrix_x4_trans(b, half + where);
-        mma16<BF16>(acc[2 * n], f, b[0], b[1]);
-        mma16<BF16>(acc[2 * n + 1], f, b[2], b[3]);
-        if (two) {
-          ldmatrix_x4_trans(b, half + L::HALF_BYTES + where);
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          if (part >= a.parts) continue;
+          ldmatrix_x4_trans(b, half + part * L::HALF_BYTES + where);
           mma16<BF16>(acc[2 * n], f, b[0], b[1]);
           mma16<BF16>(acc[2 * n + 1], f, b[2], b[3]);
         }
@@ -572,6 +691,12 @@ mma_status_t launch_lora_shrink(const Ctx& ctx, const LoraProblem& g, const Lora
   });
 }
 
+mma_status_t launch_lora_expand(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
+  if (g.bf16)
+    return g.row_major ? expand<true, true>(ctx, g, low) : expand<true, false>(ctx, g, low);
+  return g.row_major ? expand<false, true>(ctx, g, low) : expand<false, false>(ctx, g, low);
+}
+
 int64_t lora_wgrad_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t rank,
                                    int64_t requests) {
   const int64_t per = rows_per_piece(T, N, K);
@@ -593,6 +718,7 @@ mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& g, float*
   a.offsets = g.offsets;
   a.adapters = g.adapters;
   a.d_type = g.d_type;
+  a.parts = lora_parts(g.bf16, g.d_type);
   a.accumulate = g.accumulate;
   a.part = workspace;
   const int tiles = a.tiles0 + int((g.K + kTile - 1) / kTile);

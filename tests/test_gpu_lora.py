@@ -5,8 +5,8 @@ Tolerances.  A tensor core's FP32 sums are off by at most 2^-16 of the sum of th
 terms' magnitudes at the lengths here (measured 4.2e-6 = 2^-17.9 at 4096 terms in a
 row; the kernels add at most 1024 of them before they round to nearest).  The rows'
 sums S inherit that from x A; in the second product S may be rounded to the inputs'
-type, half a step U of it, or with an FP32 result to a sum of two such numbers, U^2;
-the products with W and with B are off by another 2^-16 of their magnitudes, and the
+type, half a step U of it, or with an FP32 result to a sum of three BF16 numbers,
+U^3, or two FP16 ones, U^2; the products with W and with B are off by another 2^-16 of their magnitudes, and the
 result is rounded to its type.  FP16 numbers below 2^-14 have steps of 2^-24: half of
 that for each S and, with two parts, for what the first leaves.
 """
@@ -112,7 +112,7 @@ class Case:
         got, s = self.run(out, c, **kw)
         want, mag, u_in, s64, s_tol = self.want()
         u = U[self.kind]
-        tol = mag + u_in * (u * u if out == "f32" else u) + getattr(self, "half", 0.0)
+        tol = mag + u_in * ((u ** 3 if self.kind == "bf16" else u * u) if out == "f32" else u) + getattr(self, "half", 0.0)
         if c is not None:
             want = want + host(c)
             tol = tol + 2.0 ** -23 * host(c).abs()
@@ -249,10 +249,10 @@ def test_adapters_gradient(lengths, n, k, r, kind, out):
     adapters = [rng.choice([-1, total] + list(range(total)) * 4) for _ in lengths]
     c = Case(lengths, n, k, r, adapters, total, kind, gap=(rng.choice([0, 4]), rng.choice([0, 9])), seed=k)
     dy = rows16(rnd(5, c.t, n), T[kind], 1)
-    s, u = rows16(rnd(6, c.t, r), torch.float32, 1), rows16(rnd(7, c.t, r), torch.float32)
+    s, u = rows16(rnd(6, c.t, r), torch.float32, 1), rnd(7, c.t, r).float().cuda()
     da, db = mma.gemm_lora_wgrad(dy, c.x, s, u, c.offsets, c.adapters, adapters_total=total, out_dtype=T[out])
     a64, b64, ma, mb = wgrad_want(c, dy, s, u)
-    rel = SUM + (U[kind] ** 2 if out == "f32" else U[kind])
+    rel = SUM + (U[kind] ** (3 if kind == "bf16" else 2) if out == "f32" else U[kind])
     for got, ref, mag in ((da, a64, ma), (db, b64, mb)):
         tol = mag * rel + 2.0 ** -20 * STEP[kind]
         # (FP16 sums below 2^-14 have steps of 2^-24)

@@ -44,7 +44,7 @@ def product(**kw):
     (dict(ldb=20, sb=8192), MISAL), (dict(sb=4000), INVALID), (dict(D=0), INVALID), (dict(ldd=255), INVALID),
     (dict(D=Q + 1), MISAL), (dict(C=Q, ldc=512), INVALID), (dict(C=P, ldc=8), INVALID), (dict(S=0), INVALID),
     (dict(S=R + 4), MISAL), (dict(lds=20), MISAL), (dict(lds=8), INVALID), (dict(ws=0), INVALID),
-    (dict(ws=R + 8), MISAL), (dict(bytes=100 * 16 * 2 - 1), INVALID), (dict(td=F32, bytes=100 * 16 * 2), INVALID),
+    (dict(ws=R + 8), MISAL), (dict(bytes=100 * 256 * 4 - 1), INVALID), (dict(T=200, bytes=35 * 256 * 4 + 200 * 16 * 2 - 1), INVALID),
     (dict(T=0, X=0, D=0, off=0), OK),
 ])
 def test_product(kw, code):
@@ -62,7 +62,7 @@ def wgrad(**kw):
     (dict(ti=E4M3), UNSUP), (dict(td=F16), UNSUP), (dict(N=-1), INVALID), (dict(rank=129), UNSUP),
     (dict(N=128 * 65535, lddy=128 * 65535), UNSUP), (dict(off=0), INVALID), (dict(dY=0), INVALID),
     (dict(X=0), INVALID), (dict(lddy=128), INVALID), (dict(ldx=130), MISAL), (dict(S=0), INVALID),
-    (dict(U=0), INVALID), (dict(S=P + 8), MISAL), (dict(ldu=18), MISAL), (dict(lds=8), INVALID),
+    (dict(U=0), INVALID), (dict(S=P + 2), MISAL), (dict(ldu=15), INVALID), (dict(lds=8), INVALID),
     (dict(dA=0), INVALID), (dict(dB=0), INVALID), (dict(ldda=64), INVALID), (dict(sda=100), INVALID),
     (dict(lddb=8), INVALID), (dict(dB=Q + 2), MISAL), (dict(ws=0), INVALID), (dict(bytes=1000), INVALID),
     (dict(ws=R + 2), MISAL), (dict(rank=0), OK), (dict(total=0), OK),
@@ -73,7 +73,8 @@ def test_wgrad(kw, code):
 
 def test_workspaces():
     f, g = binding.load().mma_gemm_lora_workspace, binding.load().mma_gemm_lora_wgrad_workspace
-    assert f(BF16, 100, 16) == 3200 and f(F32, 100, 17) == 100 * 24 * 4 and f(BF16, 10, 0) == 0
+    assert f(BF16, BF16, 100, 30, 16, 3) == 12000 and f(BF16, F32, 200, 32, 17, 3) == 21 * 32 * 4 + 200 * 24 * 6
+    assert f(F16, F32, 200, 32, 17, 3) == 21 * 32 * 4 + 200 * 24 * 4 and f(BF16, BF16, 10, 8, 0, 1) == 0
     assert g(0, 8, 8, 8, 3) == 0 and g(100, 256, 128, 16, 5) == 7 * 16 * 384 * 4 and g(1, 1, 1, 129, 1) == 0
 
 
