@@ -744,12 +744,13 @@ mma_status_t mma_gemm_lora(int type_in, int type_d, int64_t T, int64_t N,
  *           sums of two FP16 or three BF16 numbers, a 16-bit one as one.
  * accumulate : nonzero -- added to DA and DB; else an adapter without rows gets
  *           zeros.
- * Sums are FP32, in a fixed order, through `workspace`: 4-byte aligned device
- * memory of mma_gemm_lora_wgrad_workspace(T, N, K, rank, requests) bytes.  Other
- * arguments as above.
+ * Sums are FP32, in a fixed order, through `workspace`: 16-byte aligned device
+ * memory of mma_gemm_lora_wgrad_workspace(type_in, type_d, T, N, K, rank, requests)
+ * bytes.  Other arguments as above.
  */
-int64_t mma_gemm_lora_wgrad_workspace(int64_t T, int64_t N, int64_t K,
-                                      int64_t rank, int64_t requests);
+int64_t mma_gemm_lora_wgrad_workspace(int type_in, int type_d, int64_t T,
+                                      int64_t N, int64_t K, int64_t rank,
+                                      int64_t requests);
 mma_status_t mma_gemm_lora_wgrad(int type_in, int type_d, int64_t T, int64_t N,
                                  int64_t K, int64_t rank, const void *DY,
                                  int64_t lddy, const void *X, int64_t ldx,

@@ -85,7 +85,8 @@ SIGNATURES = {
                                    _p, _i64, _p, _i64, _p, _i64, _i64, _p, _p,
                                    _i64, _p, _i64, _i64, _p, _i64, _i64, _int,
                                    _p, _i64, _p]),
-    "mma_gemm_lora_wgrad_workspace": (_i64, [_i64, _i64, _i64, _i64, _i64]),
+    "mma_gemm_lora_wgrad_workspace": (_i64, [_int, _int, _i64, _i64, _i64, _i64,
+                                             _i64]),
     "mma_device_status": (_int, [_p]),
     "mma_selftest_wait_timeout": (_int, [_i64, _p]),
     "mma_selftest_gemm_abort": (_int, [_int, _i64, _p, _p, _p, _p]),
@@ -1116,7 +1117,7 @@ def _plan_lora_wgrad(dY, X, S, U, offsets, adapters, adapters_total, dA, dB, acc
             rank * K if dA is None else _slices("dA", dA),
             rank if dB is None else _rows("dB", dB),
             N * rank if dB is None else _slices("dB", dB), dtype,
-            load().mma_gemm_lora_wgrad_workspace(T, N, K, rank, requests),
+            load().mma_gemm_lora_wgrad_workspace(code, d_code, T, N, K, rank, requests),
             _one_device(dY, X, S, U, offsets, adapters, dA, dB))
 
 

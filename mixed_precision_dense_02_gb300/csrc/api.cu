@@ -1222,16 +1222,16 @@ extern "C" mma_status_t mma_gemm_lora(
   if (N == 0) return MMA_OK;
   // without them there is nothing to add
   const bool plain = rank == 0 || requests == 0 || adapters_total == 0 || K == 0;
-  if (!plain) MMA_CHECK(launch_lora_expand(ctx, g, low));
   return launch_gemm_lora(ctx, g, plain ? nullptr : &low);
 }
 
-extern "C" int64_t mma_gemm_lora_wgrad_workspace(int64_t T, int64_t N, int64_t K,
-                                                 int64_t rank, int64_t requests) {
+extern "C" int64_t mma_gemm_lora_wgrad_workspace(int type_in, int type_d, int64_t T,
+                                                 int64_t N, int64_t K, int64_t rank,
+                                                 int64_t requests) {
   if (!dim_ok(T) || !dim_ok(N) || !dim_ok(K) || rank < 1 || rank > MMA_MAX_RANK ||
       requests < 0 || requests > kMaxGroups)
     return 0;
-  return lora_wgrad_workspace_bytes(T, N, K, rank, requests);
+  return lora_wgrad_workspace_bytes(type_in == MMA_BF16, type_d, T, N, K, rank, requests);
 }
 
 extern "C" mma_status_t mma_gemm_lora_wgrad(
@@ -1261,8 +1261,9 @@ extern "C" mma_status_t mma_gemm_lora_wgrad(
     if (N > 0) MMA_CHECK(check_sums(S, lds, rank));
     if (K > 0) MMA_CHECK(check_sums(U, ldu, rank));
     if (workspace == nullptr) return MMA_ERR_INVALID_ARG;
-    if (!aligned4(workspace)) return MMA_ERR_MISALIGNED;
-    if (workspace_bytes < lora_wgrad_workspace_bytes(T, N, K, rank, requests))
+    if (!aligned16(workspace)) return MMA_ERR_MISALIGNED;
+    if (workspace_bytes <
+        mma_gemm_lora_wgrad_workspace(type_in, type_d, T, N, K, rank, requests))
       return MMA_ERR_INVALID_ARG;
   }
   int dev = -1;
@@ -1296,5 +1297,5 @@ extern "C" mma_status_t mma_gemm_lora_wgrad(
   g.lddb = lddb;
   g.stride_db = stride_db;
   g.accumulate = accumulate != 0;
-  return launch_lora_wgrad(ctx, g, static_cast<float*>(workspace));
+  return launch_lora_wgrad(ctx, g, workspace);
 }

@@ -45,6 +45,13 @@ struct Ctx {
 bool make_kmajor_map(CUtensorMap* map, const void* base, int64_t K,
                      int64_t rows, int64_t ld_elems, int box_rows, bool bf16,
                      int64_t count = 1);
+// A 3-D map over 1- or 2-byte elements (gemm_grouped.cu): `inner` contiguous
+// elements, `outer` rows `ld` elements apart, `count` slices `slice` elements apart;
+// box box_inner x box_outer x 1, zero fill out of bounds.
+bool make_map(CUtensorMap* map, const void* base, int elem, int64_t inner,
+              int64_t outer, int64_t ld, int64_t count, int64_t slice,
+              int box_inner, int box_outer,
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 bool make_cd_map(CUtensorMap* map, const void* base, int64_t N, int64_t M,
                  int64_t ld_elems, CUtensorMapDataType dt, int elem_bytes,
                  int64_t count = 1);
@@ -268,8 +275,8 @@ struct LoraLow {
   float* extra;
   int ld32, ld16, parts;
 };
+// The sums, and what they add where `extra` takes it.
 mma_status_t launch_lora_shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low);
-mma_status_t launch_lora_expand(const Ctx& ctx, const LoraProblem& g, const LoraLow& low);
 // (low NULL: the shared product alone)
 mma_status_t launch_gemm_lora(const Ctx& ctx, const LoraProblem& g, const LoraLow* low);
 
@@ -294,9 +301,9 @@ struct LoraWgradProblem {
   int64_t lddb, stride_db;
   bool accumulate;
 };
-int64_t lora_wgrad_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t rank,
-                                   int64_t requests);
-mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& g, float* workspace);
+int64_t lora_wgrad_workspace_bytes(bool bf16, int d_type, int64_t T, int64_t N, int64_t K,
+                                   int64_t rank, int64_t requests);
+mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& g, void* workspace);
 
 // Root-mean-square norm with the residual's addition (rmsnorm.cu).  Element
 // types MMA_F16, MMA_BF16, MMA_F32; NULL pointers as in the C ABI.

@@ -37,7 +37,7 @@ __device__ __forceinline__ void load_bounds(int* bound, const int* offsets, int 
                                             int T, int* scan) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int before = 0;
-  for (int base = 0; base <= requests; base += kThreads) {
+  for (int base = 0; base <= requests; base += blockDim.x) {
     const int i = base + threadIdx.x;
     int v = i <= requests ? min(max(__ldg(offsets + i), 0), T) : 0;
 #pragma unroll
@@ -50,7 +50,7 @@ __device__ __forceinline__ void load_bounds(int* bound, const int* offsets, int 
     for (int w = 0; w < warp; ++w) v = max(v, scan[w]);
     v = max(v, before);
     if (i <= requests) bound[i + 1] = v;
-    for (int w = 0; w < kThreads / 32; ++w) before = max(before, scan[w]);
+    for (int w = 0; w < int(blockDim.x) / 32; ++w) before = max(before, scan[w]);
     __syncthreads();
   }
   if (threadIdx.x == 0) {
@@ -68,7 +68,7 @@ struct Piece {
 
 __device__ __forceinline__ Piece piece_of(const int* bound, int requests, int per, int u) {
   int n = 0;
-  for (int base = 0; base < requests + 2; base += kThreads) {
+  for (int base = 0; base < requests + 2; base += blockDim.x) {
     const int j = base + threadIdx.x;
     n += __syncthreads_count(j < requests + 2 && bound[j] / per + j <= u);
   }
@@ -118,45 +118,105 @@ __device__ __forceinline__ uint16_t take_half(float& v) {
   }
 }
 
-// Copy 16 bytes of which the first `left` elements of two bytes are in the row.
-__device__ __forceinline__ void copy_chunk(uint32_t dst, const uint16_t* src, int left,
-                                           const void* any) {
-  const int n = min(max(left, 0), 8) * 2;
-  cp_async_16_zfill(dst, n ? static_cast<const void*>(src) : any, n);
+// What the threads of a block share to wait for loads.
+struct Ring {
+  uint64_t full[4], empty[4];
+  int abort_flag;
+};
+
+// A producer warp besides the eight that compute.
+constexpr int kRingThreads = kThreads + 32;
+
+__device__ __forceinline__ void ring_init(Ring& r, int stages) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&r.full[s], 1);
+      mbar_init(&r.empty[s], kThreads / 32);
+    }
+    r.abort_flag = 0;
+    fence_mbarrier_init();
+    fence_proxy_async_smem();
+  }
+}
+
+// The producer's lane: stage after stage through load(step, shared memory, barrier)
+// of `bytes`; it ends when all of them have landed, after a failed wait too.
+template <int STAGES, int STAGE, class F>
+__device__ __forceinline__ void ring_fill(Ring& r, uint8_t* smem, int steps, int bytes,
+                                          unsigned* status, F&& load) {
+  int step = 0;
+  for (; step < steps; ++step) {
+    const int s = step % STAGES;
+    const uint32_t phase = uint32_t(step / STAGES) & 1u;
+    if (!mbar_wait(&r.empty[s], phase ^ 1u, &r.abort_flag, status)) break;
+    mbar_arrive_expect_tx(&r.full[s], uint32_t(bytes));
+    load(step, smem + s * STAGE, &r.full[s]);
+  }
+  for (int i = max(step - STAGES, 0); i < step; ++i)
+    mbar_drain(&r.full[i % STAGES], uint32_t(i / STAGES) & 1u, status);
 }
 
 // ------------------------------------------------------------- a row's sums
 
 // Piece blockIdx.x of blocks of BM rows; the CTAs of a cluster (blockIdx.y) share
-// the k range, and so do the warps that have the same 16 rows.  Stages of KS k's by
-// cp.async; sums past the rank, rows past the piece and k's past K are zeros.
+// the k range, and so do the warps that have the same 16 rows.  Boxes of 64 k's by
+// TMA into a ring (cp.async's addresses were half of all instructions: 8192 x 4096,
+// rank 64, 33 us).  Rows of X past the piece are other requests' and their sums are
+// dropped; sums past the rank and k's past K are zeros.
+//
+// A few rows' share of the result, s B, is made here as well: of every row up to
+// kLoraEveryRow, else of the requests of fewer than kLoraRows.  Every CTA of the
+// cluster adds all of the piece's sums up, and a lane has kCols columns of B.
 template <int BM, int RP>
 struct Shrink {
   static constexpr int MW = BM / 16, KW = 8 / MW;  // warps along rows, along k
-  static constexpr int KS = KW * 32;
+  static constexpr int KS = BM == 16 ? 256 : 128;  // k's per stage
   static constexpr int X_BYTES = BM * KS * 2, A_BYTES = RP * KS * 2;
   static constexpr int STAGE = X_BYTES + A_BYTES;
-  static constexpr int STAGES = 4 * STAGE <= 200 * 1024 ? 4 : 3;
-  static constexpr int SMEM = STAGES * STAGE;  // (the sums: 512 * RP bytes of them)
+  static constexpr int STAGES = 4 * STAGE <= 100 * 1024 ? 4 : 3;
+  static constexpr int SMEM = STAGES * STAGE + 1024;  // (the sums: 512 * RP bytes)
 };
 
+// The swizzle of rows of `bytes` (the same that swizzled() computes).
+constexpr CUtensorMapSwizzle swizzle_of(int bytes) {
+  return bytes == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+         : bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                       : CU_TENSOR_MAP_SWIZZLE_128B;
+}
+
 template <bool BF16, bool ROW, int BM, int RP>
-__global__ void __launch_bounds__(kThreads)
-    lora_shrink_kernel(const LoraProblem g, const LoraLow low) {
+__global__ void __launch_bounds__(kRingThreads)
+    lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX,
+                       const __grid_constant__ CUtensorMap tmA, const LoraProblem g,
+                       const LoraLow low, unsigned* status) {
   using L = Shrink<BM, RP>;
-  constexpr int KS = L::KS;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int bound[MMA_MAX_GROUPS + 3], scan[kThreads / 32];
+  constexpr int KS = L::KS, KB = KS / 64;
+  constexpr int RB = RP < 64 ? RP : 64;  // (ROW) sums per box
+  constexpr int kCols = 4, kRows = 4;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  __shared__ int bound[MMA_MAX_GROUPS + 3], scan[kRingThreads / 32];
+  __shared__ Ring ring;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependents_start();
-  load_bounds(bound, g.offsets, int(g.requests), int(g.rows), scan);
-  const Piece piece = piece_of(bound, int(g.requests), BM, blockIdx.x);
-  const int who =
-      adapter_of(piece.request, int(g.requests), g.adapters, int(g.adapters_total));
-  const int rows = piece.to - piece.from, rank = int(g.rank);
+  ring_init(ring, L::STAGES);
+  const int requests = int(g.requests);
+  load_bounds(bound, g.offsets, requests, int(g.rows), scan);
+  const Piece piece = piece_of(bound, requests, BM, blockIdx.x);
+  const int who = adapter_of(piece.request, requests, g.adapters, int(g.adapters_total));
+  const int rows = piece.to - piece.from, rank = int(g.rank), N = int(g.N);
   // (the same in all CTAs of the cluster, so that all of them return)
   if (rows <= 0) return;
   const int part = blockIdx.y, parts = gridDim.y;
+  const bool every = g.rows <= kLoraEveryRow;
+  const int first_of = bound[piece.request];
+  const bool add = every || bound[piece.request + 1] - first_of < kLoraRows;
+  auto extra_row = [&](int row) {
+    const int64_t t = piece.from + row;
+    return low.extra +
+           (every ? t : int64_t(piece.request - 1) * (kLoraRows - 1) + t - first_of) * N;
+  };
   auto put = [&](int row, int n, float v) {
     const int64_t t = piece.from + row;
     if (n >= rank) v = 0.f;
@@ -167,86 +227,91 @@ __global__ void __launch_bounds__(kThreads)
     }
   };
   if (who < 0) {
-    for (int i = part * kThreads + threadIdx.x; i < rows * RP; i += parts * kThreads)
+    for (int i = part * kRingThreads + threadIdx.x; i < rows * RP; i += parts * kRingThreads)
       put(i / RP, i % RP, 0.f);
+    if (every)
+      for (int r = 0; r < rows; ++r)
+        for (int p = part * kRingThreads + threadIdx.x; p < N; p += parts * kRingThreads)
+          extra_row(r)[p] = 0.f;
     return;
   }
-  const uint16_t* const X = static_cast<const uint16_t*>(g.X) + piece.from * g.ldx;
-  const uint16_t* const A = static_cast<const uint16_t*>(g.A) + who * g.stride_a;
   const int K = int(g.K);
   const int all = (K + KS - 1) / KS;
-  const int first = int(int64_t(all) * part / parts), last = int(int64_t(all) * (part + 1) / parts);
-  const uint32_t base = smem_u32(smem);
-  auto load = [&](int step) {
-    const int k0 = step * KS;
-    const uint32_t xs = base + (step - first) % L::STAGES * L::STAGE, as = xs + L::X_BYTES;
+  const int first = int(int64_t(all) * part / parts);
+  const int steps = int(int64_t(all) * (part + 1) / parts) - first;
+  bool ok = true;
+  if (warp == kThreads / 32) {
+    if (lane == 0)
+      ring_fill<L::STAGES, L::STAGE>(
+          ring, smem, steps, L::STAGE, status, [&](int step, uint8_t* xs, uint64_t* bar) {
+            const int k = (first + step) * KS;
+            uint8_t* as = xs + L::X_BYTES;
 #pragma unroll
-    for (int i = threadIdx.x; i < BM * KS / 8; i += kThreads) {
-      const int row = i / (KS / 8), c = i % (KS / 8), k = k0 + c * 8;
-      copy_chunk(xs + swizzled<KS * 2>(row, c), X + row * g.ldx + k, row < rows ? K - k : 0,
-                 g.X);
-    }
-#pragma unroll
-    for (int i = threadIdx.x; i < RP * KS / 8; i += kThreads) {
-      if constexpr (!ROW) {
-        const int n = i / (KS / 8), c = i % (KS / 8), k = k0 + c * 8;
-        copy_chunk(as + swizzled<KS * 2>(n, c), A + n * g.lda + k, n < rank ? K - k : 0, g.X);
-      } else {
-        const int row = i / (RP / 8), c = i % (RP / 8), k = k0 + row;
-        copy_chunk(as + swizzled<RP * 2>(row, c), A + k * g.lda + c * 8,
-                   k < K ? rank - c * 8 : 0, g.X);
-      }
-    }
-  };
+            for (int b = 0; b < KB; ++b) {
+              tma_load_3d(&tmX, bar, xs + b * BM * 128, k + b * 64, piece.from, 0);
+              if constexpr (!ROW) tma_load_3d(&tmA, bar, as + b * RP * 128, k + b * 64, 0, who);
+            }
+            if constexpr (ROW)
+              for (int b = 0; b < RP / RB; ++b)
+                tma_load_3d(&tmA, bar, as + b * KS * RB * 2, b * RB, k, who);
+          });
+    __syncwarp();
+  }
   float acc[RP / 8][4];
-#pragma unroll
-  for (int n = 0; n < RP / 8; ++n)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
-#pragma unroll
-  for (int s = 0; s < L::STAGES - 1; ++s) {
-    if (first + s < last) load(first + s);
-    cp_async_commit();
-  }
   const int mw = warp % L::MW, kw = warp / L::MW;
-  for (int step = first; step < last; ++step) {
-    cp_async_wait<L::STAGES - 2>();
-    __syncthreads();  // this stage has landed, and the one before has been read
-    if (step + L::STAGES - 1 < last) load(step + L::STAGES - 1);
-    cp_async_commit();
-    const uint32_t xs = base + (step - first) % L::STAGES * L::STAGE, as = xs + L::X_BYTES;
+  if (warp < kThreads / 32) {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int k = kw * 32 + kk * 16;
-      uint32_t a[4];
-      ldmatrix_x4(a, xs + swizzled<KS * 2>(mw * 16 + (lane & 15), k / 8 + (lane >> 4)));
+    for (int n = 0; n < RP / 8; ++n)
 #pragma unroll
-      for (int n = 0; n < RP / 16; ++n) {
-        uint32_t b[4];
-        const int m = lane >> 3, at = lane & 7;
-        if constexpr (!ROW)
-          ldmatrix_x4(b, as + swizzled<KS * 2>(n * 16 + (m >> 1) * 8 + at, k / 8 + (m & 1)));
-        else
-          ldmatrix_x4_trans(b, as + swizzled<RP * 2>(k + (m & 1) * 8 + at, n * 2 + (m >> 1)));
-        mma16<BF16>(acc[2 * n], a, b[0], b[1]);
-        mma16<BF16>(acc[2 * n + 1], a, b[2], b[3]);
+      for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
+    const uint32_t base = smem_u32(smem);
+    const int m = lane >> 3, at = lane & 7;
+    for (int step = 0; step < steps && ok; ++step) {
+      const int s = step % L::STAGES;
+      ok = mbar_wait(&ring.full[s], uint32_t(step / L::STAGES) & 1u, &ring.abort_flag, status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t xs = base + s * L::STAGE, as = xs + L::X_BYTES;
+#pragma unroll
+      for (int kk = 0; kk < KS / L::KW / 16; ++kk) {
+        const int k = kw * (KS / L::KW) + kk * 16, box = k / 64, in = k % 64;
+        uint32_t a[4];
+        ldmatrix_x4(a, xs + box * BM * 128 +
+                           swizzled<128>(mw * 16 + (lane & 15), in / 8 + (lane >> 4)));
+#pragma unroll
+        for (int n = 0; n < RP / 16; ++n) {
+          uint32_t b[4];
+          if constexpr (!ROW)
+            ldmatrix_x4(b, as + box * RP * 128 +
+                               swizzled<128>(n * 16 + (m >> 1) * 8 + at, in / 8 + (m & 1)));
+          else
+            ldmatrix_x4_trans(b, as + n * 16 / RB * KS * RB * 2 +
+                                     swizzled<RB * 2>(k + (m & 1) * 8 + at,
+                                                      n * 2 % (RB / 8) + (m >> 1)));
+          mma16<BF16>(acc[2 * n], a, b[0], b[1]);
+          mma16<BF16>(acc[2 * n + 1], a, b[2], b[3]);
+        }
       }
+      __syncwarp();
+      mbar_arrive_if(&ring.empty[s], lane == 0);
     }
   }
-  cp_async_wait<0>();
-  __syncthreads();
-  // the warps' sums, then the CTAs', each in order
+  // the warps' sums, then the CTAs', each in order (nothing is on its way into
+  // shared memory any more)
+  ok = !__syncthreads_or(!ok || ring.abort_flag);
   float* sums = reinterpret_cast<float*>(smem);  // [KW][BM][RP]
+  if (warp < kThreads / 32) {
 #pragma unroll
-  for (int n = 0; n < RP / 8; ++n) {
-    float* d = sums + (kw * BM + mw * 16 + (lane >> 2)) * RP + n * 8 + 2 * (lane & 3);
-    d[0] = acc[n][0];
-    d[1] = acc[n][1];
-    d[8 * RP] = acc[n][2];
-    d[8 * RP + 1] = acc[n][3];
+    for (int n = 0; n < RP / 8; ++n) {
+      float* d = sums + (kw * BM + mw * 16 + (lane >> 2)) * RP + n * 8 + 2 * (lane & 3);
+      d[0] = acc[n][0];
+      d[1] = acc[n][1];
+      d[8 * RP] = acc[n][2];
+      d[8 * RP + 1] = acc[n][3];
+    }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < BM * RP; i += kThreads) {
+  for (int i = threadIdx.x; i < rows * RP; i += kRingThreads) {
     float v = sums[i];
 #pragma unroll
     for (int w = 1; w < L::KW; ++w) v += sums[w * BM * RP + i];
@@ -255,8 +320,10 @@ __global__ void __launch_bounds__(kThreads)
   const float scale = g.scales ? __ldg(g.scales + who) : 1.f;
   if (parts > 1) cluster_sync();
   else __syncthreads();
-  const int share = BM * RP / parts;
-  for (int i = part * share + threadIdx.x; i < (part + 1) * share; i += kThreads) {
+  float* mine = sums + BM * RP;  // all CTAs' (the room of a warp's sums, done with)
+  const int share = (rows * RP + parts - 1) / parts;
+  for (int i = add ? threadIdx.x : part * share + threadIdx.x;
+       i < (add ? rows * RP : min((part + 1) * share, rows * RP)); i += kRingThreads) {
     float v = 0.f;
     if (parts > 1) {
       for (int r = 0; r < parts; ++r)
@@ -264,14 +331,89 @@ __global__ void __launch_bounds__(kThreads)
     } else {
       v = sums[i];
     }
-    if (i / RP < rows) put(i / RP, i % RP, v * scale);
+    v *= scale;
+    if (add) mine[i] = i % RP < rank ? v : 0.f;
+    if (ok && i / share == part) put(i / RP, i % RP, v);
   }
   if (parts > 1) cluster_sync();  // no CTA leaves while another reads its sums
+  if (!add || !ok || N == 0) return;
+  __syncthreads();
+  const uint16_t* const B = static_cast<const uint16_t*>(g.B) + who * g.stride_b;
+  if (warp == kThreads / 32) return;
+  for (int p0 = part * kThreads * kCols; p0 < N; p0 += parts * kThreads * kCols) {
+    for (int r0 = 0; r0 < rows; r0 += kRows) {
+      float v[kRows][kCols];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) v[r][x] = 0.f;
+#pragma unroll 1
+      for (int k = 0; k < rank; k += 8) {
+        uint4 w[kCols];
+        const int left = rank - k;
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) {
+          const int p = p0 + x * kThreads + threadIdx.x;
+          w[x] = make_uint4(0, 0, 0, 0);
+          if (p >= N) continue;
+          if constexpr (ROW) {
+            uint32_t f[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) f[y] = y < left ? B[(k + y) * g.ldb + p] : 0u;
+            w[x] = make_uint4(f[0] | f[1] << 16, f[2] | f[3] << 16, f[4] | f[5] << 16,
+                              f[6] | f[7] << 16);
+          } else {
+            w[x] = __ldg(reinterpret_cast<const uint4*>(B + p * g.ldb + k));
+          }
+        }
+        float2 b[kCols][4];
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) {
+          uint32_t q[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            // (what stands behind a row's rank numbers is none of them)
+            if (!ROW && left < 2 * y + 2) q[y] = left <= 2 * y ? 0u : q[y] & 0xFFFFu;
+            if constexpr (BF16)
+              b[x][y] = make_float2(__uint_as_float(q[y] << 16),
+                                    __uint_as_float(q[y] & 0xFFFF0000u));
+            else
+              b[x][y] = __half22float2(*reinterpret_cast<const __half2*>(&q[y]));
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          if (r0 + r >= rows) continue;
+          const float4* s = reinterpret_cast<const float4*>(mine + (r0 + r) * RP + k);
+          const float4 s0 = s[0], s1 = s[1];
+#pragma unroll
+          for (int x = 0; x < kCols; ++x) {
+            v[r][x] = fmaf(s0.x, b[x][0].x, v[r][x]);
+            v[r][x] = fmaf(s0.y, b[x][0].y, v[r][x]);
+            v[r][x] = fmaf(s0.z, b[x][1].x, v[r][x]);
+            v[r][x] = fmaf(s0.w, b[x][1].y, v[r][x]);
+            v[r][x] = fmaf(s1.x, b[x][2].x, v[r][x]);
+            v[r][x] = fmaf(s1.y, b[x][2].y, v[r][x]);
+            v[r][x] = fmaf(s1.z, b[x][3].x, v[r][x]);
+            v[r][x] = fmaf(s1.w, b[x][3].y, v[r][x]);
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) {
+          const int p = p0 + x * kThreads + threadIdx.x;
+          if (r0 + r < rows && p < N) extra_row(r0 + r)[p] = v[r][x];
+        }
+    }
+  }
 }
 
 template <bool BF16, bool ROW, int BM, int RP>
 mma_status_t shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
   using L = Shrink<BM, RP>;
+  constexpr int RB = RP < 64 ? RP : 64;
   auto kernel = lora_shrink_kernel<BF16, ROW, BM, RP>;
   static PerContext<bool> attr;
   bool ok = false;
@@ -282,14 +424,28 @@ mma_status_t shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
         return *v;
       }))
     return MMA_ERR_LAUNCH;
+  // (without adapters or k there is nothing to load, but the maps have to be valid:
+  // over the sums, which are 16-byte aligned and eight numbers at least)
+  const bool any = g.K > 0 && g.adapters_total > 0;
+  const int64_t slices = any ? g.adapters_total : 1;
+  const int64_t slice = slices > 1 ? g.stride_a : any ? g.lda : 8;
+  const void* const a = any ? g.A : low.f32;
+  CUtensorMap tx, ta;
+  if (!make_map(&tx, any ? g.X : low.f32, 2, any ? g.K : 8, any ? g.rows : 1,
+                any ? g.ldx : 8, 1, any ? g.ldx : 8, 64, BM) ||
+      !(ROW ? make_map(&ta, a, 2, any ? g.rank : 8, any ? g.K : 1, any ? g.lda : 8,
+                       slices, slice, RB, L::KS, swizzle_of(RB * 2))
+            : make_map(&ta, a, 2, any ? g.K : 8, any ? g.rank : 1, any ? g.lda : 8,
+                       slices, slice, 64, RP)))
+    return MMA_ERR_LAUNCH;
   const int64_t pieces = (g.rows + BM - 1) / BM + g.requests + 1;
   const int64_t steps = (g.K + L::KS - 1) / L::KS;
-  // as many CTAs per piece as fill the SMs twice, each with four stages at least
+  // as many CTAs per piece as fill the SMs twice, each with two stages at least
   int parts = 1;
-  while (parts < 8 && pieces * parts * 2 <= 2 * ctx.num_sms && steps >= parts * 8) parts *= 2;
+  while (parts < 8 && pieces * parts * 2 <= 2 * ctx.num_sms && steps >= parts * 4) parts *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(pieces), unsigned(parts), 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(kRingThreads, 1, 1);
   cfg.dynamicSmemBytes = L::SMEM;
   cfg.stream = ctx.stream;
   cudaLaunchAttribute at = {};
@@ -299,7 +455,7 @@ mma_status_t shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
   at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, g, low);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tx, ta, g, low, ctx.status);
   const cudaError_t after = cudaGetLastError();
   return e == cudaSuccess && after == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
 }
@@ -313,127 +469,10 @@ mma_status_t by_rank(int64_t rank, F&& f) {
   return f(std::integral_constant<int, 128>{});
 }
 
-// ----------------------------------------------- what the sums add, few rows
-
-// extra[row][p] = sum over n of s[row][n] B[n][p], FP32, a lane per p: of every row
-// (EVERY: pieces of eight rows, zeros where there is no adapter) or of the requests
-// of fewer than kLoraRows rows.  Bound by B's bytes and latency.  The grid is small
-// enough to be on the SMs at once with its neighbours, so that the shared product
-// after it starts before it ends.
-template <bool BF16, bool ROW, bool EVERY>
-__global__ void __launch_bounds__(kThreads)
-    lora_expand_kernel(const LoraProblem g, const LoraLow low, int units) {
-  constexpr int kCols = 4;  // p per thread at a time, their loads together
-  __shared__ int bound[MMA_MAX_GROUPS + 3], scan[kThreads / 32];
-  grid_dependents_start();
-  const int requests = int(g.requests), rank = int(g.rank), N = int(g.N);
-  load_bounds(bound, g.offsets, requests, int(g.rows), scan);
-  bool ready = false;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    Piece piece;
-    if constexpr (EVERY) {
-      piece = piece_of(bound, requests, 8, u);
-    } else {
-      piece = Piece{u + 1, bound[u + 1], bound[u + 2]};
-      if (piece.to - piece.from >= kLoraRows) continue;
-    }
-    if (piece.to <= piece.from) continue;
-    const int who = adapter_of(piece.request, requests, g.adapters, int(g.adapters_total));
-    if (!EVERY && who < 0) continue;
-    const uint16_t* const B = static_cast<const uint16_t*>(g.B) + (who < 0 ? 0 : who * g.stride_b);
-    // (the offsets and B are older than the kernel before this one, the sums are not)
-    if (!ready) grid_dependency_wait();
-    ready = true;
-    for (int p0 = blockIdx.y * kThreads * kCols; p0 < N; p0 += gridDim.y * kThreads * kCols) {
-      for (int t = piece.from; t < piece.to; ++t) {
-        const float* s = low.f32 + int64_t(t) * low.ld32;
-        float v[kCols];
-#pragma unroll
-        for (int x = 0; x < kCols; ++x) v[x] = 0.f;
-#pragma unroll 1
-        for (int k = 0; k < rank && who >= 0; k += 8) {
-          uint4 w[kCols];
-          const int left = rank - k;
-#pragma unroll
-          for (int x = 0; x < kCols; ++x) {
-            const int p = p0 + x * kThreads + threadIdx.x;
-            w[x] = make_uint4(0, 0, 0, 0);
-            if (p >= N) continue;
-            if constexpr (ROW) {
-              uint32_t f[8];
-#pragma unroll
-              for (int y = 0; y < 8; ++y) f[y] = y < left ? B[(k + y) * g.ldb + p] : 0u;
-              w[x] = make_uint4(f[0] | f[1] << 16, f[2] | f[3] << 16, f[4] | f[5] << 16,
-                                f[6] | f[7] << 16);
-            } else {
-              w[x] = __ldg(reinterpret_cast<const uint4*>(B + p * g.ldb + k));
-            }
-          }
-          const float4 s0 = *reinterpret_cast<const float4*>(s + k);
-          const float4 s1 = *reinterpret_cast<const float4*>(s + k + 4);
-          const float2 f[4] = {make_float2(s0.x, s0.y), make_float2(s0.z, s0.w),
-                               make_float2(s1.x, s1.y), make_float2(s1.z, s1.w)};
-#pragma unroll
-          for (int x = 0; x < kCols; ++x) {
-            uint32_t q[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              // (what stands behind a row's rank numbers is none of them)
-              if (!ROW && left < 2 * y + 2) q[y] = left <= 2 * y ? 0u : q[y] & 0xFFFFu;
-              float2 b;
-              if constexpr (BF16)
-                b = make_float2(__uint_as_float(q[y] << 16), __uint_as_float(q[y] & 0xFFFF0000u));
-              else
-                b = __half22float2(*reinterpret_cast<const __half2*>(&q[y]));
-              v[x] = fmaf(f[y].x, b.x, v[x]);
-              v[x] = fmaf(f[y].y, b.y, v[x]);
-            }
-          }
-        }
-        const int64_t row =
-            EVERY ? t : int64_t(u) * (kLoraRows - 1) + t - piece.from;
-#pragma unroll
-        for (int x = 0; x < kCols; ++x) {
-          const int p = p0 + x * kThreads + threadIdx.x;
-          if (p < N) low.extra[row * N + p] = v[x];
-        }
-      }
-    }
-  }
-  // (a kernel after this one may count on the one before being done)
-  if (!ready) grid_dependency_wait();
-}
-
-template <bool BF16, bool ROW>
-mma_status_t expand(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
-  const bool every = g.rows <= kLoraEveryRow;
-  const int64_t units = every ? (g.rows + 7) / 8 + g.requests + 1 : g.requests;
-  const int64_t columns = (g.N + kThreads * 4 - 1) / (kThreads * 4);
-  const int64_t most = ctx.num_sms * 2;
-  const int64_t x = std::min(units, most);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(x), unsigned(std::max<int64_t>(1, std::min(columns, most / x))), 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.stream = ctx.stream;
-  cudaLaunchAttribute at = {};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  const cudaError_t e =
-      cudaLaunchKernelEx(&cfg, every ? lora_expand_kernel<BF16, ROW, true>
-                                     : lora_expand_kernel<BF16, ROW, false>,
-                         g, low, int(units));
-  const cudaError_t after = cudaGetLastError();
-  return e == cudaSuccess && after == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
-}
-
 // ------------------------------------------------- the adapters' own gradients
 
 // One side of the gradient: features of M (T x F) times the rows' sums.
 struct Side {
-  const uint16_t* m;
-  int64_t ldm;
   int F;
   const float* low;  // T x rank, FP32
   int64_t ldl;
@@ -447,9 +486,15 @@ struct WgradArgs {
   int tiles0;    // tiles of 128 features of the first side
   int T, rank, requests, total, per;
   const int *offsets, *adapters;
-  int d_type, parts;
+  int d_type, parts, ld16;
   bool accumulate;
-  float* part;  // [pieces][rank][features of both sides]
+  float* part;      // [pieces][rank][features of both sides]
+  uint16_t* halves;  // [2][parts][T][ld16]
+  unsigned* status;
+};
+
+struct WgradMaps {
+  CUtensorMap m[2], low[2];
 };
 
 constexpr int kTile = 128;      // features per CTA, 16 per warp
@@ -457,127 +502,141 @@ constexpr int kStageRows = 64;  // rows per stage
 
 template <int RP>
 struct Wgrad {
-  static constexpr int M_BYTES = kStageRows * kTile * 2, L_BYTES = kStageRows * RP * 4;
-  static constexpr int STAGE = M_BYTES + L_BYTES;
-  static constexpr int HALF_BYTES = kStageRows * RP * 2;  // the sums in 16 bits, a part
+  static constexpr int RB = RP < 64 ? RP : 64;  // sums per box
+  static constexpr int M_BYTES = kStageRows * kTile * 2;
+  static constexpr int PART = kStageRows * RP * 2;  // one part of the sums
+  static constexpr int STAGE = M_BYTES + 3 * PART;
   static constexpr int STAGES = RP <= 64 ? 4 : 3;
-  static constexpr int SMEM = STAGES * STAGE + 3 * HALF_BYTES;
+  static constexpr int SMEM = STAGES * STAGE + 1024;
 };
 
-// Piece blockIdx.x's share of 128 features: G[f][n] = sum over its rows M[t][f] *
-// low[t][n] on the tensor cores, FP32.  The sums come in FP32 and are taken as a sum
-// of `parts` numbers of 16 bits (see lora_parts).
-template <bool BF16, int RP>
+// Both sides' sums in parts of 16 bits.
+template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
-    lora_wgrad_kernel(const WgradArgs a) {
+    lora_halves_kernel(const WgradArgs a) {
+  grid_dependents_start();
+  const Side& side = a.side[blockIdx.y];
+  const int64_t all = int64_t(a.T) * a.ld16;
+  if (side.F == 0) return;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < all;
+       i += int64_t(gridDim.x) * kThreads) {
+    const int64_t t = i / a.ld16;
+    const int n = int(i - t * a.ld16);
+    float v = n < a.rank ? side.low[t * side.ldl + n] : 0.f;
+    for (int part = 0; part < a.parts; ++part)
+      a.halves[(int64_t(blockIdx.y) * a.parts + part) * all + i] = take_half<BF16>(v);
+  }
+}
+
+// Piece blockIdx.x's share of 128 features: G[f][n] = sum over its rows M[t][f] *
+// low[t][n] on the tensor cores, FP32.  Rows and sums by TMA into a ring; what
+// stands in the last stage behind the piece is another request's and becomes zeros
+// in both (in one alone, an infinity in the other would leave NaN).
+template <bool BF16, int RP>
+__global__ void __launch_bounds__(kRingThreads)
+    lora_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) {
   using L = Wgrad<RP>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int bound[MMA_MAX_GROUPS + 3], scan[kThreads / 32];
+  constexpr int RB = L::RB;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  __shared__ int bound[MMA_MAX_GROUPS + 3], scan[kRingThreads / 32];
+  __shared__ Ring ring;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  ring_init(ring, L::STAGES);
   load_bounds(bound, a.offsets, a.requests, a.T, scan);
   const Piece piece = piece_of(bound, a.requests, a.per, blockIdx.x);
   const int rows = piece.to - piece.from;
+  grid_dependency_wait();  // (the halves; before any return, for the kernel after)
   if (rows <= 0 || adapter_of(piece.request, a.requests, a.adapters, a.total) < 0) return;
   const bool second = int(blockIdx.y) >= a.tiles0;
   const Side& side = a.side[second];
   const int f0 = (int(blockIdx.y) - (second ? a.tiles0 : 0)) * kTile;
-  const uint16_t* const M = side.m + piece.from * side.ldm + f0;
-  const float* const S = side.low + piece.from * side.ldl;
   const int F = side.F - f0, rank = a.rank;
-  // 16 bytes of a row of sums at a time
-  const bool wide = side.ldl % 4 == 0 && (reinterpret_cast<uintptr_t>(side.low) & 15) == 0;
-  const uint32_t base = smem_u32(smem), half = base + L::STAGES * L::STAGE;
   const int steps = (rows + kStageRows - 1) / kStageRows;
-  auto load = [&](int step) {
-    const uint32_t ms = base + step % L::STAGES * L::STAGE, ls = ms + L::M_BYTES;
+  bool ok = true;
+  if (warp == kThreads / 32) {
+    if (lane == 0)
+      ring_fill<L::STAGES, L::STAGE>(
+          ring, smem, steps, L::M_BYTES + a.parts * L::PART, a.status,
+          [&](int step, uint8_t* ms, uint64_t* bar) {
+            const int t = piece.from + step * kStageRows;
 #pragma unroll
-    for (int i = threadIdx.x; i < kStageRows * kTile / 8; i += kThreads) {
-      const int row = i / (kTile / 8), c = i % (kTile / 8), t = step * kStageRows + row;
-      copy_chunk(ms + swizzled<kTile * 2>(row, c), M + t * side.ldm + c * 8,
-                 t < rows ? F - c * 8 : 0, side.m);
-    }
+            for (int b = 0; b < kTile / 64; ++b)
+              tma_load_3d(&maps.m[second], bar, ms + b * kStageRows * 128, f0 + b * 64, t, 0);
+            for (int part = 0; part < a.parts; ++part)
 #pragma unroll
-    for (int i = threadIdx.x; i < kStageRows * RP / 4; i += kThreads) {
-      const int row = i / (RP / 4), c = i % (RP / 4), t = step * kStageRows + row;
-      const int n = t < rows ? min(max(rank - c * 4, 0), 4) : 0;
-      const float* src = S + t * side.ldl + c * 4;
-      if (wide) {
-        cp_async_16_zfill(ls + i * 16, n ? src : side.low, n * 4);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          cp_async_4_zfill(ls + i * 16 + j * 4, j < n ? src + j : side.low, j < n ? 4 : 0);
-      }
-    }
-  };
+              for (int b = 0; b < RP / RB; ++b)
+                tma_load_3d(&maps.low[second], bar,
+                            ms + L::M_BYTES + part * L::PART + b * kStageRows * RB * 2, b * RB, t,
+                            part);
+          });
+    __syncwarp();
+  }
   float acc[RP / 8][4];
+  if (warp < kThreads / 32) {
 #pragma unroll
-  for (int n = 0; n < RP / 8; ++n)
+    for (int n = 0; n < RP / 8; ++n)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
-#pragma unroll
-  for (int s = 0; s < L::STAGES - 1; ++s) {
-    if (s < steps) load(s);
-    cp_async_commit();
-  }
-  for (int step = 0; step < steps; ++step) {
-    cp_async_wait<L::STAGES - 2>();
-    __syncthreads();  // this stage has landed, and the one before has been read
-    if (step + L::STAGES - 1 < steps) load(step + L::STAGES - 1);
-    cp_async_commit();
-    const uint32_t ms = base + step % L::STAGES * L::STAGE;
-    const float* ls = reinterpret_cast<const float*>(smem + step % L::STAGES * L::STAGE +
-                                                     L::M_BYTES);
-    for (int i = threadIdx.x; i < kStageRows * RP / 8; i += kThreads) {
-      const int row = i / (RP / 8), c = i % (RP / 8);
-      float v[8];
-      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(ls + i * 8);
-      *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(ls + i * 8 + 4);
-      uint8_t* d = smem + L::STAGES * L::STAGE + swizzled<RP * 2>(row, c);
-      for (int part = 0; part < a.parts; ++part, d += L::HALF_BYTES) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t h0 = take_half<BF16>(v[2 * j]), h1 = take_half<BF16>(v[2 * j + 1]);
-          w[j] = h0 | h1 << 16;
-        }
-        *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
+    const int m = lane >> 3, at = lane & 7;
+    for (int step = 0; step < steps; ++step) {
+      const int s = step % L::STAGES;
+      ok = mbar_wait(&ring.full[s], uint32_t(step / L::STAGES) & 1u, &ring.abort_flag, a.status);
+      const int valid = rows - step * kStageRows;
+      if (valid < kStageRows) {  // (the last stage of all)
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        for (int b = 0; b < kTile / 64; ++b)
+          for (int i = valid * 8 + threadIdx.x; i < kStageRows * 8; i += kThreads)
+            *reinterpret_cast<uint4*>(smem + s * L::STAGE + b * kStageRows * 128 + i * 16) = zero;
+        for (int b = 0; b < a.parts * RP / RB; ++b)
+          for (int i = valid * (RB / 8) + threadIdx.x; i < kStageRows * (RB / 8); i += kThreads)
+            *reinterpret_cast<uint4*>(smem + s * L::STAGE + L::M_BYTES +
+                                      b * kStageRows * RB * 2 + i * 16) = zero;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
       }
-    }
-    __syncthreads();
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t ms = smem_u32(smem + s * L::STAGE), ls = ms + L::M_BYTES;
 #pragma unroll
-    for (int k = 0; k < kStageRows; k += 16) {
-      const int m = lane >> 3, at = lane & 7;
-      uint32_t f[4];
-      ldmatrix_x4_trans(f, ms + swizzled<kTile * 2>(k + (m >> 1) * 8 + at, warp * 2 + (m & 1)));
+      for (int k = 0; k < kStageRows; k += 16) {
+        uint32_t f[4];
+        ldmatrix_x4_trans(f, ms + warp / 4 * kStageRows * 128 +
+                                 swizzled<128>(k + (m >> 1) * 8 + at, warp % 4 * 2 + (m & 1)));
 #pragma unroll
-      for (int n = 0; n < RP / 16; ++n) {
-        uint32_t b[4];
-        const int where = swizzled<RP * 2>(k + (m & 1) * 8 + at, n * 2 + (m >> 1));
+        for (int n = 0; n < RP / 16; ++n) {
+          uint32_t b[4];
+          const int where = n * 16 / RB * kStageRows * RB * 2 +
+                            swizzled<RB * 2>(k + (m & 1) * 8 + at, n * 2 % (RB / 8) + (m >> 1));
 #pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          if (part >= a.parts) continue;
-          ldmatrix_x4_trans(b, half + part * L::HALF_BYTES + where);
-          mma16<BF16>(acc[2 * n], f, b[0], b[1]);
-          mma16<BF16>(acc[2 * n + 1], f, b[2], b[3]);
+          for (int part = 0; part < 3; ++part) {
+            if (part >= a.parts) continue;
+            ldmatrix_x4_trans(b, ls + part * L::PART + where);
+            mma16<BF16>(acc[2 * n], f, b[0], b[1]);
+            mma16<BF16>(acc[2 * n + 1], f, b[2], b[3]);
+          }
         }
       }
+      __syncwarp();
+      mbar_arrive_if(&ring.empty[s], lane == 0);
     }
   }
-  cp_async_wait<0>();
+  ok = !__syncthreads_or(!ok || ring.abort_flag);
+  if (!ok) return;
   // rows of features per sum, through shared memory
-  __syncthreads();
   float* t = reinterpret_cast<float*>(smem);  // [RP][kTile + 4]
+  if (warp < kThreads / 32) {
 #pragma unroll
-  for (int n = 0; n < RP / 8; ++n)
+    for (int n = 0; n < RP / 8; ++n)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      t[(n * 8 + 2 * (lane & 3) + (j & 1)) * (kTile + 4) + warp * 16 + (lane >> 2) +
-        (j >> 1) * 8] = acc[n][j];
+      for (int j = 0; j < 4; ++j)
+        t[(n * 8 + 2 * (lane & 3) + (j & 1)) * (kTile + 4) + warp * 16 + (lane >> 2) +
+          (j >> 1) * 8] = acc[n][j];
+  }
   __syncthreads();
-  const int64_t features = a.side[0].F + a.side[1].F;
+  const int64_t features = int64_t(a.side[0].F) + a.side[1].F;
   float* out = a.part + int64_t(blockIdx.x) * rank * features + (second ? a.side[0].F : 0) + f0;
-  for (int i = threadIdx.x; i < rank * kTile; i += kThreads)
+  for (int i = threadIdx.x; i < rank * kTile; i += kRingThreads)
     if (i % kTile < F) out[i / kTile * features + i % kTile] = t[i / kTile * (kTile + 4) + i % kTile];
 }
 
@@ -596,8 +655,8 @@ __device__ __forceinline__ void store_out(void* p, int64_t i, int type, float v)
     static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
-// Adapter blockIdx.y: its pieces' shares added in order, for 256 features of each
-// of the rank's sums in turn.
+// Adapter blockIdx.y: its pieces' shares added in order, for 256 features, four of
+// the rank's sums at a time.
 __global__ void __launch_bounds__(kThreads)
     lora_wgrad_sum_kernel(const WgradArgs a) {
   __shared__ int bound[MMA_MAX_GROUPS + 3], scan[kThreads / 32], list[MMA_MAX_GROUPS], found;
@@ -622,20 +681,34 @@ __global__ void __launch_bounds__(kThreads)
   const Side& side = a.side[second];
   const int f = at - (second ? a.side[0].F : 0);
   const int64_t out = int64_t(blockIdx.y) * side.slice;
-  for (int n = blockIdx.z; n < a.rank; n += gridDim.z) {
-    float v = 0.f;
+  for (int n0 = blockIdx.z * 4; n0 < a.rank; n0 += gridDim.z * 4) {
+    const int many = min(a.rank - n0, 4);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
     for (int i = 0; i < found; ++i) {
       const int j = list[i] + 1;
       const int first = bound[j] / a.per, last = (bound[j + 1] - 1) / a.per;
-      for (int b = first; b <= last; ++b)
-        v += a.part[(int64_t(b + j) * a.rank + n) * features + at];
+      for (int b = first; b <= last; ++b) {
+        const float* p = a.part + (int64_t(b + j) * a.rank + n0) * features + at;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (x < many) v[x] += p[int64_t(x) * features];
+      }
     }
-    const int64_t o = out + (side.by_rank ? n * side.ldo + f : f * side.ldo + n);
-    if (a.accumulate) {
-      if (found == 0) continue;
-      v += load_out(side.out, o, a.d_type);
+    if (a.accumulate && found == 0) continue;
+    const int64_t o = out + (side.by_rank ? n0 * side.ldo + f : f * side.ldo + n0);
+    const int64_t step = side.by_rank ? side.ldo : 1;
+    if (!side.by_rank && a.d_type == MMA_F32 && !a.accumulate && many == 4 &&
+        (reinterpret_cast<uintptr_t>(static_cast<float*>(side.out) + o) & 15) == 0) {
+      *reinterpret_cast<float4*>(static_cast<float*>(side.out) + o) =
+          make_float4(v[0], v[1], v[2], v[3]);
+      continue;
     }
-    store_out(side.out, o, a.d_type, v);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (x >= many) continue;
+      const float old = a.accumulate ? load_out(side.out, o + x * step, a.d_type) : 0.f;
+      store_out(side.out, o + x * step, a.d_type, v[x] + old);
+    }
   }
 }
 
@@ -647,8 +720,24 @@ int rows_per_piece(int64_t T, int64_t N, int64_t K) {
   return int(std::min<int64_t>(std::max<int64_t>((per + 63) / 64 * 64, 256), 1 << 20));
 }
 
+template <class K, class... Args>
+cudaError_t launch_after(const Ctx& ctx, K kernel, dim3 grid, int threads, int smem,
+                         const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = ctx.stream;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <bool BF16, int RP>
-mma_status_t wgrad(const Ctx& ctx, const WgradArgs& a, int tiles, int64_t pieces) {
+mma_status_t wgrad(const Ctx& ctx, const LoraWgradProblem& g, const WgradArgs& a) {
   using L = Wgrad<RP>;
   auto kernel = lora_wgrad_kernel<BF16, RP>;
   static PerContext<bool> attr;
@@ -660,16 +749,37 @@ mma_status_t wgrad(const Ctx& ctx, const WgradArgs& a, int tiles, int64_t pieces
         return *v;
       }))
     return MMA_ERR_LAUNCH;
-  static_assert(RP * (kTile + 4) * 4 <= L::SMEM, "the sums' transposition");
-  ctx.mark_start();
-  if (a.T > 0)
-    kernel<<<dim3(unsigned(pieces), unsigned(tiles)), kThreads, L::SMEM, ctx.stream>>>(a);
-  ctx.mark_stop();
+  static_assert(RP * (kTile + 4) * 4 <= L::SMEM - 1024, "the sums' transposition");
+  cudaError_t e = cudaSuccess;
+  if (a.T > 0) {
+    WgradMaps maps;
+    const int64_t all = int64_t(a.T) * a.ld16;
+    for (int i = 0; i < 2; ++i) {
+      const bool there = a.side[i].F > 0;  // (else the maps are never used)
+      const void* m = !there ? a.halves : i ? g.X : g.DY;
+      const int64_t ld = !there ? 8 : i ? g.ldx : g.lddy;
+      if (!make_map(&maps.m[i], m, 2, there ? a.side[i].F : 8, there ? a.T : 1, ld, 1, ld, 64,
+                    kStageRows) ||
+          !make_map(&maps.low[i], a.halves + i * a.parts * all, 2, a.rank, a.T, a.ld16, a.parts,
+                    a.parts > 1 ? all : a.ld16, L::RB, kStageRows, swizzle_of(L::RB * 2)))
+        return MMA_ERR_LAUNCH;
+    }
+    const int64_t blocks = std::min<int64_t>((all + kThreads - 1) / kThreads, ctx.num_sms * 4);
+    lora_halves_kernel<BF16><<<dim3(unsigned(blocks), 2), kThreads, 0, ctx.stream>>>(a);
+    const int64_t pieces = (g.rows + a.per - 1) / a.per + g.requests + 1;
+    const int64_t tiles = a.tiles0 + (g.K + kTile - 1) / kTile;
+    ctx.mark_start();
+    e = launch_after(ctx, kernel, dim3(unsigned(pieces), unsigned(tiles)), kRingThreads, L::SMEM,
+                     maps, a);
+    ctx.mark_stop();
+  }
   const int64_t features = int64_t(a.side[0].F) + a.side[1].F;
-  lora_wgrad_sum_kernel<<<dim3(unsigned((features + kThreads - 1) / kThreads), unsigned(a.total),
-                               unsigned(std::min(a.rank, 8))),
-                          kThreads, 0, ctx.stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
+  if (e == cudaSuccess)
+    lora_wgrad_sum_kernel<<<dim3(unsigned((features + kThreads - 1) / kThreads),
+                                 unsigned(a.total), unsigned(std::min((a.rank + 3) / 4, 4))),
+                            kThreads, 0, ctx.stream>>>(a);
+  const cudaError_t after = cudaGetLastError();
+  return e == cudaSuccess && after == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -691,24 +801,18 @@ mma_status_t launch_lora_shrink(const Ctx& ctx, const LoraProblem& g, const Lora
   });
 }
 
-mma_status_t launch_lora_expand(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
-  if (g.bf16)
-    return g.row_major ? expand<true, true>(ctx, g, low) : expand<true, false>(ctx, g, low);
-  return g.row_major ? expand<false, true>(ctx, g, low) : expand<false, false>(ctx, g, low);
-}
-
-int64_t lora_wgrad_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t rank,
-                                   int64_t requests) {
+int64_t lora_wgrad_workspace_bytes(bool bf16, int d_type, int64_t T, int64_t N, int64_t K,
+                                   int64_t rank, int64_t requests) {
+  if (T == 0) return 0;
   const int64_t per = rows_per_piece(T, N, K);
-  return T == 0 ? 0 : ((T + per - 1) / per + requests + 1) * rank * (N + K) * 4;
+  const int64_t part = ((T + per - 1) / per + requests + 1) * rank * (N + K) * 4;
+  return (part + 15) / 16 * 16 + 2 * lora_parts(bf16, d_type) * T * ((rank + 7) / 8 * 8) * 2;
 }
 
-mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& g, float* workspace) {
+mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& g, void* workspace) {
   WgradArgs a = {};
-  a.side[0] = {static_cast<const uint16_t*>(g.DY), g.lddy, int(g.N), g.S, g.lds,
-               g.DB, g.lddb, g.stride_db, false};
-  a.side[1] = {static_cast<const uint16_t*>(g.X), g.ldx, int(g.K), g.U, g.ldu,
-               g.DA, g.ldda, g.stride_da, true};
+  a.side[0] = {int(g.N), g.S, g.lds, g.DB, g.lddb, g.stride_db, false};
+  a.side[1] = {int(g.K), g.U, g.ldu, g.DA, g.ldda, g.stride_da, true};
   a.tiles0 = int((g.N + kTile - 1) / kTile);
   a.T = int(g.rows);
   a.rank = int(g.rank);
@@ -719,14 +823,16 @@ mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& g, float*
   a.adapters = g.adapters;
   a.d_type = g.d_type;
   a.parts = lora_parts(g.bf16, g.d_type);
+  a.ld16 = (a.rank + 7) / 8 * 8;
   a.accumulate = g.accumulate;
-  a.part = workspace;
-  const int tiles = a.tiles0 + int((g.K + kTile - 1) / kTile);
   const int64_t pieces = (g.rows + a.per - 1) / a.per + g.requests + 1;
+  a.part = static_cast<float*>(workspace);
+  a.halves = reinterpret_cast<uint16_t*>(
+      static_cast<uint8_t*>(workspace) + (pieces * g.rank * (g.N + g.K) * 4 + 15) / 16 * 16);
+  a.status = ctx.status;
   return by_rank(g.rank, [&](auto r) {
     constexpr int RP = decltype(r)::value;
-    return g.bf16 ? wgrad<true, RP>(ctx, a, tiles, pieces)
-                  : wgrad<false, RP>(ctx, a, tiles, pieces);
+    return g.bf16 ? wgrad<true, RP>(ctx, g, a) : wgrad<false, RP>(ctx, g, a);
   });
 }
 

@@ -65,7 +65,7 @@ def wgrad(**kw):
     (dict(U=0), INVALID), (dict(S=P + 2), MISAL), (dict(ldu=15), INVALID), (dict(lds=8), INVALID),
     (dict(dA=0), INVALID), (dict(dB=0), INVALID), (dict(ldda=64), INVALID), (dict(sda=100), INVALID),
     (dict(lddb=8), INVALID), (dict(dB=Q + 2), MISAL), (dict(ws=0), INVALID), (dict(bytes=1000), INVALID),
-    (dict(ws=R + 2), MISAL), (dict(rank=0), OK), (dict(total=0), OK),
+    (dict(ws=R + 4), MISAL), (dict(rank=0), OK), (dict(total=0), OK),
 ])
 def test_wgrad(kw, code):
     assert wgrad(**kw) == code
@@ -75,7 +75,9 @@ def test_workspaces():
     f, g = binding.load().mma_gemm_lora_workspace, binding.load().mma_gemm_lora_wgrad_workspace
     assert f(BF16, BF16, 100, 30, 16, 3) == 12000 and f(BF16, F32, 200, 32, 17, 3) == 21 * 32 * 4 + 200 * 24 * 6
     assert f(F16, F32, 200, 32, 17, 3) == 21 * 32 * 4 + 200 * 24 * 4 and f(BF16, BF16, 10, 8, 0, 1) == 0
-    assert g(0, 8, 8, 8, 3) == 0 and g(100, 256, 128, 16, 5) == 7 * 16 * 384 * 4 and g(1, 1, 1, 129, 1) == 0
+    assert g(BF16, F32, 0, 8, 8, 8, 3) == 0 and g(BF16, F32, 1, 1, 1, 129, 1) == 0
+    assert g(BF16, F32, 100, 256, 128, 20, 5) == 7 * 20 * 384 * 4 + 2 * 3 * 100 * 24 * 2
+    assert g(F16, F16, 100, 256, 128, 20, 5) == 7 * 20 * 384 * 4 + 2 * 100 * 24 * 2
 
 
 def test_binding():
