@@ -1220,23 +1220,27 @@ def route(logits, k: int, *, mask=None, normalize: bool = True, stream=None) -> 
     if stream is not None:
         return _under(stream, index, route, logits, k, mask=mask, normalize=normalize)
     device = logits.device
-    # two allocations, cut up: this call serves single tokens too
-    ints = torch.empty((3 * T * k + E + 2 + need,), dtype=torch.int32, device=device)
-    floats = torch.empty((T * k + E + 1,), dtype=torch.float32, device=device)
-    n = T * k
-    cut = torch.unsafe_split_with_sizes
-    experts, order, place, offsets, tokens = cut(ints, (n, n, n, E + 1, 1 + need))[:5]
-    weights, share, loss = cut(floats, (n, E, 1))
-    at, fat = ints.data_ptr(), floats.data_ptr()
+    i32, f32 = torch.int32, torch.float32
+    # (allocations by themselves: views of one took longer)
+    empty = torch.empty
+    weights = empty((T, k), dtype=f32, device=device)
+    experts = empty((T, k), dtype=i32, device=device)
+    order = empty((T * k,), dtype=i32, device=device)
+    place = empty((T, k), dtype=i32, device=device)
+    offsets = empty((E + 1,), dtype=i32, device=device)
+    share = empty((E,), dtype=f32, device=device)
+    loss = empty((), dtype=f32, device=device)
+    tokens = empty((), dtype=i32, device=device)
+    # (its memory goes to other work of the current stream only after the call's)
+    ws = empty((need,), dtype=i32, device=device) if need else None
     st = load().mma_route(
         code, T, E, k, logits.data_ptr(), ldx, None if mask is None else mask.data_ptr(),
-        1 if normalize else 0, fat, at, at + 4 * n, at + 8 * n, at + 12 * n,
-        fat + 4 * n, fat + 4 * (n + E), at + 4 * (3 * n + E + 1),
-        at + 4 * (3 * n + E + 2) if need else None, 4 * need, _raw_stream(index))
+        1 if normalize else 0, weights.data_ptr(), experts.data_ptr(), order.data_ptr(),
+        place.data_ptr(), offsets.data_ptr(), share.data_ptr(), loss.data_ptr(),
+        tokens.data_ptr(), None if ws is None else ws.data_ptr(), 4 * need, _raw_stream(index))
     if st:
         _check("mma_route", st)
-    return Routing(weights.view(T, k), experts.view(T, k), order, place.view(T, k), offsets,
-                   share, loss[0], tokens[0])
+    return Routing(weights, experts, order, place, offsets, share, loss, tokens)
 
 
 def _plan_route_backward(logits, routing, d_weights, d_loss, mask, normalize):

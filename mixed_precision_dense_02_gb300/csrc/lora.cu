@@ -235,6 +235,18 @@ __global__ void __launch_bounds__(kRingThreads)
           extra_row(r)[p] = 0.f;
     return;
   }
+  const uint16_t* const B = static_cast<const uint16_t*>(g.B) + who * g.stride_b;
+  if (add && warp < kThreads / 32 && g.ldb <= (ROW ? int64_t(1) << 40 : 2 * rank + 8)) {
+    // this CTA's part of B on its way to L2 while the sums are made
+    for (int p0 = part * kThreads * kCols; p0 < N; p0 += parts * kThreads * kCols) {
+      const int cols = min(kThreads * kCols, N - p0);
+      const int lines = ROW ? (cols + 63) / 64 : int((cols * g.ldb + 63) / 64);
+      for (int i = threadIdx.x; i < (ROW ? lines * rank : lines); i += kThreads)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            ROW ? B + i / lines * g.ldb + p0 + min(i % lines * 64, cols - 1)
+                : B + p0 * g.ldb + min(int64_t(i) * 64, (cols - 1) * g.ldb)));
+    }
+  }
   const int K = int(g.K);
   const int all = (K + KS - 1) / KS;
   const int first = int(int64_t(all) * part / parts);
@@ -338,7 +350,6 @@ __global__ void __launch_bounds__(kRingThreads)
   if (parts > 1) cluster_sync();  // no CTA leaves while another reads its sums
   if (!add || !ok || N == 0) return;
   __syncthreads();
-  const uint16_t* const B = static_cast<const uint16_t*>(g.B) + who * g.stride_b;
   if (warp == kThreads / 32) return;
   for (int p0 = part * kThreads * kCols; p0 < N; p0 += parts * kThreads * kCols) {
     for (int r0 = 0; r0 < rows; r0 += kRows) {

@@ -52,6 +52,9 @@ __device__ __forceinline__ uint32_t ordered(float v) {
   return u ^ (uint32_t(int(u) >> 31) | 0x80000000u);
 }
 constexpr uint32_t kMinusInf = 0x007FFFFFu;
+__device__ __forceinline__ float unordered(uint32_t q) {
+  return __uint_as_float(q & 0x80000000u ? q ^ 0x80000000u : ~q);
+}
 
 // (+ 0: one zero, one NaN, which is above infinity)
 __device__ __forceinline__ float logit(float v) { return v + 0.f; }
@@ -240,7 +243,12 @@ __global__ void __launch_bounds__(ONE ? 1024 : 512)
   for (int c = 0; c < V; ++c) acc[c] = 0.f;
   int live = 0;
   float x[V];
-  if (first + warp < last) load_logits<T, V>(X + (first + warp) * a.ldx, E, x);
+  bool on = true;  // (the next token's, as x)
+  auto fetch = [&](int t) {
+    load_logits<T, V>(X + t * a.ldx, E, x);
+    if (a.mask) on = __ldg(a.mask + t) != 0;
+  };
+  if (first + warp < last) fetch(first + warp);
   __syncthreads();
   for (int t0 = first; t0 < last; t0 += kBatch) {
     uint16_t* const id0 = ids + (ONE ? t0 * k : 0);
@@ -252,19 +260,21 @@ __global__ void __launch_bounds__(ONE ? 1024 : 512)
       for (int c = 0; c < V; ++c) y[c] = x[c];
       // the warp's next token, in this batch or the one after
       const int next = i + warps < kBatch ? t + warps : t0 + kBatch + warp;
-      if (next < last) load_logits<T, V>(X + next * a.ldx, E, x);
-      const bool on = a.mask == nullptr || a.mask[t] != 0;
-      int id = -1;  // lane j: choice j
-      float top = -INFINITY;
-      if (on) {
-        ++live;
+      const bool live_one = on;
+      if (next < last) fetch(next);
+      int id = -1;      // lane j: choice j
+      float top = 0.f;  // its logit
+      uint32_t most_key = 0;
+#pragma unroll
+      for (int c = 0; c < V; ++c) most_key = max(most_key, ordered(y[c]));
+      most_key = __reduce_max_sync(0xffffffffu, most_key);
+      const bool some = live_one && most_key > kMinusInf;
+      const float most = unordered(most_key);
+      if (some) {
         id = choices<sizeof(T) == 4, V>(y, E, k);
-        const T* row = X + t * a.ldx;
-        if (id >= 0) top = logit(to_float(row[id]));
+        if (id >= 0) top = logit(to_float(X[t * a.ldx + id]));
       }
-      // weights
-      const float most = __shfl_sync(0xffffffffu, top, 0);
-      const bool some = __shfl_sync(0xffffffffu, id, 0) >= 0;
+      live += live_one;
       float sum = 0.f;
 #pragma unroll
       for (int c = 0; c < V; ++c) {
@@ -384,57 +394,61 @@ __global__ void __launch_bounds__(ONE ? 1024 : 512)
 }
 
 // For each of 32 columns of the counts, the sums over the blocks before; the
-// totals; the shares.
+// totals; the shares.  A thread has up to ten consecutive blocks of a column, which
+// stay in registers between the two readings; the sums of the threads of a column
+// are added up by a warp.
 __global__ void __launch_bounds__(1024) route_scan_kernel(const Choices a) {
-  __shared__ int part[32][33];
+  constexpr int kRows = (kMostBlocks + 31) / 32;
+  __shared__ int part[32][33], live_of[32];
   __shared__ float fpart[32][33];
-  __shared__ int live_of[32];
-  const int columns = a.experts + 2;
-  const int e = blockIdx.x * 32 + threadIdx.x;
-  const int rows = (a.blocks + 31) / 32;
-  const int r0 = min(int(threadIdx.y) * rows, a.blocks), r1 = min(r0 + rows, a.blocks);
+  const int columns = a.experts + 2, x = threadIdx.x, y = threadIdx.y;
+  const int e = blockIdx.x * 32 + x;
   grid_dependency_wait();
   grid_dependents_start();
-  int n = 0;
+  int n[kRows], sum = 0;
   float s = 0.f;
-  if (e < columns)
-#pragma unroll 2
-    for (int r = r0; r < r1; ++r) n += a.counts[r * columns + e];
-  if (e < a.experts)
-#pragma unroll 2
-    for (int r = r0; r < r1; ++r) s += a.shares[r * a.experts + e];
-  part[threadIdx.y][threadIdx.x] = n;
-  fpart[threadIdx.y][threadIdx.x] = s;
-  // tokens that are not masked, over all blocks
-  const int thread = threadIdx.y * 32 + threadIdx.x;
-  int live = thread < a.blocks ? a.counts[int64_t(thread) * columns + a.experts + 1] : 0;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = y * kRows + i;
+    n[i] = r < a.blocks && e <= a.experts ? a.counts[r * columns + e] : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = y * kRows + i;
+    if (r < a.blocks && e < a.experts) s += a.shares[r * a.experts + e];
+    sum += n[i];
+  }
+  part[y][x] = sum;
+  fpart[y][x] = s;
+  // tokens that take part, over all blocks (column E + 1 stays as it is)
+  const int thread = y * 32 + x;
+  int live = thread < a.blocks ? a.counts[thread * columns + a.experts + 1] : 0;
   live = __reduce_add_sync(0xffffffffu, live);
-  if (threadIdx.x == 0) live_of[threadIdx.y] = live;
-  // (column E + 1 stays as it is)
+  if (x == 0) live_of[y] = live;
   __syncthreads();
-  live = 0;
-#pragma unroll 4
-  for (int w = 0; w < 32; ++w) live += live_of[w];
-  int before = 0;
-#pragma unroll 2
-  for (int y = 0; y < int(threadIdx.y); ++y) before += part[y][threadIdx.x];
-  if (e <= a.experts) {
-    if (threadIdx.y == 31) a.totals[e] = before + n;
-#pragma unroll 1
-    for (int r = r0; r < r1; ++r) {
-      int* p = a.counts + r * columns + e;
-      const int c = *p;
-      *p = before;
-      before += c;
-    }
+  live = __reduce_add_sync(0xffffffffu, live_of[x]);
+  // column y of this block's 32, thread rows along the lanes
+  const int col = blockIdx.x * 32 + y;
+  const int mine = part[x][y];
+  int before = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, before, d);
+    if (x >= d) before += o;
   }
-  if (e < a.experts && threadIdx.y == 0) {
-    s = 0.f;
-#pragma unroll 4
-    for (int y = 0; y < 32; ++y) s += fpart[y][threadIdx.x];
-    a.share[e] = live > 0 ? s / float(live) : 0.f;
-  }
+  if (x == 31 && col <= a.experts) a.totals[col] = before;
+  const float share = warp_sum(fpart[x][y]);
+  if (x == 0 && col < a.experts) a.share[col] = live > 0 ? share / float(live) : 0.f;
+  part[x][y] = before - mine;
   if (blockIdx.x == 0 && thread == 0) *a.live = live;
+  __syncthreads();
+  int at = part[y][x];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = y * kRows + i;
+    if (r < a.blocks && e <= a.experts) a.counts[r * columns + e] = at;
+    at += n[i];
+  }
 }
 
 // Every choice's place.
@@ -607,7 +621,8 @@ mma_status_t route(const Ctx& ctx, const Choices& a) {
 
 template <class T, int V>
 mma_status_t route_back(const Ctx& ctx, const RouteBackProblem& p) {
-  const int64_t blocks = std::min<int64_t>((p.T + 7) / 8, int64_t(ctx.num_sms) * 8);
+  // (a warp's share of the counts is some hundred instructions, so several tokens)
+  const int64_t blocks = std::min<int64_t>((p.T + 7) / 8, int64_t(ctx.num_sms) * 4);
   route_backward_kernel<T, V><<<unsigned(blocks), 256, size_t(8) * p.E * 4, ctx.stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
 }
