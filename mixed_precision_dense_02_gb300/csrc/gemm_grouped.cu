@@ -293,7 +293,8 @@ __global__ void __launch_bounds__(kThreads,
   constexpr int HALF = BN / 2;          // most columns of an epilogue warp
   constexpr int HV = L::HV;
   constexpr int QPART = BN / CL / HV;   // rows of Q per box
-  constexpr int CB = HALF < 32 ? HALF : 32;
+  // (with 80 registers, so that two CTAs fit an SM, 32 sums leave room for 16 more)
+  constexpr int CB = HALF < 32 || (LORA && SPLIT && BN == 64) ? 16 : 32;
   constexpr int NB = HALF / CB;
   constexpr bool kSplitRegs = HALF == 128;
   extern __shared__ uint8_t smem_raw[];
@@ -1061,12 +1062,21 @@ __global__ void __launch_bounds__(kThreads,
             grid_dependency_wait();
             const float* e = a.extra + min(p, t.p1 - 1);
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+            for (int b = 0; b < NB; ++b) {
+              const unsigned which = __ballot_sync(0xffffffffu, slot[b] >= 0);
 #pragma unroll
-              for (int j = 0; j < CB; ++j) {
-                const int r = __shfl_sync(0xffffffffu, slot[b], j);
-                if (r >= 0) sum[b * CB + j] += e[int64_t(r) * a.p_size];
+              for (int j = 0; j < CB; j += 8) {
+                if (!((which >> j) & 255u)) continue;
+                float v[8];  // (their loads together)
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                  const int r = __shfl_sync(0xffffffffu, slot[b], j + x);
+                  v[x] = r >= 0 ? e[int64_t(r) * a.p_size] : 0.f;
+                }
+#pragma unroll
+                for (int x = 0; x < 8; ++x) sum[b * CB + j + x] += v[x];
               }
+            }
           }
         }
       } else {

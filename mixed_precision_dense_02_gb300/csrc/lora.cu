@@ -31,15 +31,27 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The requests' bounds in shared memory: bound[0] = 0, then the offsets, within
-// [0, T] and none below the one before it, then T; requests + 3 values.
-__device__ __forceinline__ void load_bounds(int* bound, const int* offsets, int requests,
-                                            int T, int* scan) {
+// The requests, in shared memory.
+struct Requests {
+  // 0, then the offsets, within [0, T] and none below the one before it, then T
+  int bound[MMA_MAX_GROUPS + 3];
+  int who[MMA_MAX_GROUPS];  // their adapters, or -1
+  int scan[kThreads / 32];
+};
+
+__device__ __forceinline__ void load_requests(Requests& r, const int* offsets,
+                                              const int* adapters, int total, int requests,
+                                              int T) {
+  int *bound = r.bound, *scan = r.scan;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int before = 0;
   for (int base = 0; base <= requests; base += blockDim.x) {
     const int i = base + threadIdx.x;
     int v = i <= requests ? min(max(__ldg(offsets + i), 0), T) : 0;
+    if (i < requests) {
+      const int a = adapters ? __ldg(adapters + i) : i;
+      r.who[i] = a < total ? a : -1;
+    }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, v, d);
@@ -79,10 +91,8 @@ __device__ __forceinline__ Piece piece_of(const int* bound, int requests, int pe
 }
 
 // The adapter of a request counted from the one before the first, or -1.
-__device__ __forceinline__ int adapter_of(int j, int requests, const int* adapters, int total) {
-  if (j < 1 || j > requests) return -1;
-  const int a = adapters ? __ldg(adapters + j - 1) : j - 1;
-  return a >= 0 && a < total ? a : -1;
+__device__ __forceinline__ int adapter_of(const Requests& r, int j, int requests) {
+  return j < 1 || j > requests ? -1 : max(r.who[j - 1], -1);
 }
 
 // Byte offset of 16-byte chunk c of a row of ROW_BYTES, so that eight rows' chunks
@@ -121,11 +131,9 @@ __device__ __forceinline__ uint16_t take_half(float& v) {
 // What the threads of a block share to wait for loads.
 struct Ring {
   uint64_t full[4], empty[4];
+  uint64_t cleared;  // (the gradient's last stage)
   int abort_flag;
 };
-
-// A producer warp besides the eight that compute.
-constexpr int kRingThreads = kThreads + 32;
 
 __device__ __forceinline__ void ring_init(Ring& r, int stages) {
   if (threadIdx.x == 0) {
@@ -133,27 +141,55 @@ __device__ __forceinline__ void ring_init(Ring& r, int stages) {
       mbar_init(&r.full[s], 1);
       mbar_init(&r.empty[s], kThreads / 32);
     }
+    mbar_init(&r.cleared, kThreads / 32);
     r.abort_flag = 0;
     fence_mbarrier_init();
     fence_proxy_async_smem();
   }
 }
 
-// The producer's lane: stage after stage through load(step, shared memory, barrier)
-// of `bytes`; it ends when all of them have landed, after a failed wait too.
-template <int STAGES, int STAGE, class F>
-__device__ __forceinline__ void ring_fill(Ring& r, uint8_t* smem, int steps, int bytes,
-                                          unsigned* status, F&& load) {
-  int step = 0;
-  for (; step < steps; ++step) {
+// Stages of loads for a block's eight warps.  Thread 0 issues them: the first ones
+// before the loop, later ones when every warp has left the stage (a warp for it alone
+// kept the shared product off the SM: its registers and two of these blocks' did not
+// fit).  load(step, shared memory, barrier) issues a stage of `bytes`; use(step,
+// stage) is what a warp does with it.  Returns, to every thread,
+// whether all waits were met; no load is on its way any more.
+template <int STAGES, int STAGE, class Load, class Use>
+__device__ __forceinline__ bool ring_run(Ring& r, uint8_t* smem, int steps, int bytes,
+                                         unsigned* status, Load&& load, Use&& use) {
+  const int lane = threadIdx.x & 31;
+  bool ok = true;
+  int issued = 0;
+  auto issue = [&] {
+    const int s = issued % STAGES;
+    mbar_arrive_expect_tx(&r.full[s], uint32_t(bytes));
+    load(issued, smem + s * STAGE, &r.full[s]);
+    ++issued;
+  };
+  if (threadIdx.x == 0)
+    while (issued < steps && issued < STAGES) issue();
+  __syncwarp();
+  for (int step = 0; step < steps; ++step) {
     const int s = step % STAGES;
     const uint32_t phase = uint32_t(step / STAGES) & 1u;
-    if (!mbar_wait(&r.empty[s], phase ^ 1u, &r.abort_flag, status)) break;
-    mbar_arrive_expect_tx(&r.full[s], uint32_t(bytes));
-    load(step, smem + s * STAGE, &r.full[s]);
+    ok = mbar_wait(&r.full[s], phase, &r.abort_flag, status);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    use(step, smem + s * STAGE);
+    __syncwarp();
+    mbar_arrive_if(&r.empty[s], lane == 0);
+    if (threadIdx.x == 0 && issued < steps) {
+      ok = mbar_wait(&r.empty[s], phase, &r.abort_flag, status);
+      if (ok) issue();
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
   }
-  for (int i = max(step - STAGES, 0); i < step; ++i)
-    mbar_drain(&r.full[i % STAGES], uint32_t(i / STAGES) & 1u, status);
+  if (threadIdx.x == 0)
+    for (int i = max(issued - STAGES, 0); i < issued; ++i)
+      mbar_drain(&r.full[i % STAGES], uint32_t(i / STAGES) & 1u, status);
+  __syncwarp();
+  return !__syncthreads_or(!ok || r.abort_flag);
 }
 
 // ------------------------------------------------------------- a row's sums
@@ -173,7 +209,9 @@ struct Shrink {
   static constexpr int KS = BM == 16 ? 256 : 128;  // k's per stage
   static constexpr int X_BYTES = BM * KS * 2, A_BYTES = RP * KS * 2;
   static constexpr int STAGE = X_BYTES + A_BYTES;
-  static constexpr int STAGES = 4 * STAGE <= 100 * 1024 ? 4 : 3;
+  // (BM 16: two CTAs leave an SM room for one of the shared product's)
+  static constexpr int STAGES = BM == 16 ? 2 : 4 * STAGE <= 100 * 1024 ? 4 : 3;
+  static constexpr int BLOCKS = BM == 16 && RP <= 32 ? 4 : 2;  // 56 or 112 registers
   static constexpr int SMEM = STAGES * STAGE + 1024;  // (the sums: 512 * RP bytes)
 };
 
@@ -185,26 +223,34 @@ constexpr CUtensorMapSwizzle swizzle_of(int bytes) {
 }
 
 template <bool BF16, bool ROW, int BM, int RP>
-__global__ void __launch_bounds__(kRingThreads)
+__global__ void __launch_bounds__(kThreads, Shrink<BM, RP>::BLOCKS)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ CUtensorMap tmA, const LoraProblem g,
                        const LoraLow low, unsigned* status) {
   using L = Shrink<BM, RP>;
   constexpr int KS = L::KS, KB = KS / 64;
   constexpr int RB = RP < 64 ? RP : 64;  // (ROW) sums per box
-  constexpr int kCols = 4, kRows = 4;
+  constexpr int kCols = 4, kRows = BM == 16 ? 2 : 4;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  __shared__ int bound[MMA_MAX_GROUPS + 3], scan[kRingThreads / 32];
+  __shared__ Requests req;
   __shared__ Ring ring;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  grid_dependents_start();
   ring_init(ring, L::STAGES);
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmA);
+  }
+  // The kernel after this one reads what is older than this one without waiting: it
+  // may start when that is there.
+  grid_dependency_wait();
+  grid_dependents_start();
   const int requests = int(g.requests);
-  load_bounds(bound, g.offsets, requests, int(g.rows), scan);
+  load_requests(req, g.offsets, g.adapters, int(g.adapters_total), requests, int(g.rows));
+  const int* bound = req.bound;
   const Piece piece = piece_of(bound, requests, BM, blockIdx.x);
-  const int who = adapter_of(piece.request, requests, g.adapters, int(g.adapters_total));
+  const int who = adapter_of(req, piece.request, requests);
   const int rows = piece.to - piece.from, rank = int(g.rank), N = int(g.N);
   // (the same in all CTAs of the cluster, so that all of them return)
   if (rows <= 0) return;
@@ -227,16 +273,17 @@ __global__ void __launch_bounds__(kRingThreads)
     }
   };
   if (who < 0) {
-    for (int i = part * kRingThreads + threadIdx.x; i < rows * RP; i += parts * kRingThreads)
+    for (int i = part * kThreads + threadIdx.x; i < rows * RP; i += parts * kThreads)
       put(i / RP, i % RP, 0.f);
     if (every)
       for (int r = 0; r < rows; ++r)
-        for (int p = part * kRingThreads + threadIdx.x; p < N; p += parts * kRingThreads)
+        for (int p = part * kThreads + threadIdx.x; p < N; p += parts * kThreads)
           extra_row(r)[p] = 0.f;
     return;
   }
+  const float scale = g.scales ? __ldg(g.scales + who) : 1.f;
   const uint16_t* const B = static_cast<const uint16_t*>(g.B) + who * g.stride_b;
-  if (add && warp < kThreads / 32 && g.ldb <= (ROW ? int64_t(1) << 40 : 2 * rank + 8)) {
+  if (add && g.ldb <= (ROW ? int64_t(1) << 40 : 2 * rank + 8)) {
     // this CTA's part of B on its way to L2 while the sums are made
     for (int p0 = part * kThreads * kCols; p0 < N; p0 += parts * kThreads * kCols) {
       const int cols = min(kThreads * kCols, N - p0);
@@ -251,91 +298,73 @@ __global__ void __launch_bounds__(kRingThreads)
   const int all = (K + KS - 1) / KS;
   const int first = int(int64_t(all) * part / parts);
   const int steps = int(int64_t(all) * (part + 1) / parts) - first;
-  bool ok = true;
-  if (warp == kThreads / 32) {
-    if (lane == 0)
-      ring_fill<L::STAGES, L::STAGE>(
-          ring, smem, steps, L::STAGE, status, [&](int step, uint8_t* xs, uint64_t* bar) {
-            const int k = (first + step) * KS;
-            uint8_t* as = xs + L::X_BYTES;
-#pragma unroll
-            for (int b = 0; b < KB; ++b) {
-              tma_load_3d(&tmX, bar, xs + b * BM * 128, k + b * 64, piece.from, 0);
-              if constexpr (!ROW) tma_load_3d(&tmA, bar, as + b * RP * 128, k + b * 64, 0, who);
-            }
-            if constexpr (ROW)
-              for (int b = 0; b < RP / RB; ++b)
-                tma_load_3d(&tmA, bar, as + b * KS * RB * 2, b * RB, k, who);
-          });
-    __syncwarp();
-  }
   float acc[RP / 8][4];
+#pragma unroll
+  for (int n = 0; n < RP / 8; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
   const int mw = warp % L::MW, kw = warp / L::MW;
-  if (warp < kThreads / 32) {
+  const bool ok = ring_run<L::STAGES, L::STAGE>(
+      ring, smem, steps, L::STAGE, status,
+      [&](int step, uint8_t* xs, uint64_t* bar) {
+        const int k = (first + step) * KS;
+        uint8_t* as = xs + L::X_BYTES;
 #pragma unroll
-    for (int n = 0; n < RP / 8; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
-    const uint32_t base = smem_u32(smem);
-    const int m = lane >> 3, at = lane & 7;
-    for (int step = 0; step < steps && ok; ++step) {
-      const int s = step % L::STAGES;
-      ok = mbar_wait(&ring.full[s], uint32_t(step / L::STAGES) & 1u, &ring.abort_flag, status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint32_t xs = base + s * L::STAGE, as = xs + L::X_BYTES;
-#pragma unroll
-      for (int kk = 0; kk < KS / L::KW / 16; ++kk) {
-        const int k = kw * (KS / L::KW) + kk * 16, box = k / 64, in = k % 64;
-        uint32_t a[4];
-        ldmatrix_x4(a, xs + box * BM * 128 +
-                           swizzled<128>(mw * 16 + (lane & 15), in / 8 + (lane >> 4)));
-#pragma unroll
-        for (int n = 0; n < RP / 16; ++n) {
-          uint32_t b[4];
-          if constexpr (!ROW)
-            ldmatrix_x4(b, as + box * RP * 128 +
-                               swizzled<128>(n * 16 + (m >> 1) * 8 + at, in / 8 + (m & 1)));
-          else
-            ldmatrix_x4_trans(b, as + n * 16 / RB * KS * RB * 2 +
-                                     swizzled<RB * 2>(k + (m & 1) * 8 + at,
-                                                      n * 2 % (RB / 8) + (m >> 1)));
-          mma16<BF16>(acc[2 * n], a, b[0], b[1]);
-          mma16<BF16>(acc[2 * n + 1], a, b[2], b[3]);
+        for (int b = 0; b < KB; ++b) {
+          tma_load_3d(&tmX, bar, xs + b * BM * 128, k + b * 64, piece.from, 0);
+          if constexpr (!ROW) tma_load_3d(&tmA, bar, as + b * RP * 128, k + b * 64, 0, who);
         }
-      }
-      __syncwarp();
-      mbar_arrive_if(&ring.empty[s], lane == 0);
-    }
-  }
-  // the warps' sums, then the CTAs', each in order (nothing is on its way into
-  // shared memory any more)
-  ok = !__syncthreads_or(!ok || ring.abort_flag);
-  float* sums = reinterpret_cast<float*>(smem);  // [KW][BM][RP]
-  if (warp < kThreads / 32) {
+        if constexpr (ROW)
+          for (int b = 0; b < RP / RB; ++b)
+            tma_load_3d(&tmA, bar, as + b * KS * RB * 2, b * RB, k, who);
+      },
+      [&](int, const uint8_t* stage) {
+        const uint32_t xs = smem_u32(stage), as = xs + L::X_BYTES;
+        const int m = lane >> 3, at = lane & 7;
 #pragma unroll
-    for (int n = 0; n < RP / 8; ++n) {
-      float* d = sums + (kw * BM + mw * 16 + (lane >> 2)) * RP + n * 8 + 2 * (lane & 3);
-      d[0] = acc[n][0];
-      d[1] = acc[n][1];
-      d[8 * RP] = acc[n][2];
-      d[8 * RP + 1] = acc[n][3];
-    }
+        for (int kk = 0; kk < KS / L::KW / 16; ++kk) {
+          const int k = kw * (KS / L::KW) + kk * 16, box = k / 64, in = k % 64;
+          uint32_t a[4];
+          ldmatrix_x4(a, xs + box * BM * 128 +
+                             swizzled<128>(mw * 16 + (lane & 15), in / 8 + (lane >> 4)));
+#pragma unroll
+          for (int n = 0; n < RP / 16; ++n) {
+            uint32_t b[4];
+            if constexpr (!ROW)
+              ldmatrix_x4(b, as + box * RP * 128 +
+                                 swizzled<128>(n * 16 + (m >> 1) * 8 + at, in / 8 + (m & 1)));
+            else
+              ldmatrix_x4_trans(b, as + n * 16 / RB * KS * RB * 2 +
+                                       swizzled<RB * 2>(k + (m & 1) * 8 + at,
+                                                        n * 2 % (RB / 8) + (m >> 1)));
+            mma16<BF16>(acc[2 * n], a, b[0], b[1]);
+            mma16<BF16>(acc[2 * n + 1], a, b[2], b[3]);
+          }
+        }
+      });
+  // the warps' sums, then the CTAs', each in order
+  float* sums = reinterpret_cast<float*>(smem);  // [KW][BM][RP]
+#pragma unroll
+  for (int n = 0; n < RP / 8; ++n) {
+    float* d = sums + (kw * BM + mw * 16 + (lane >> 2)) * RP + n * 8 + 2 * (lane & 3);
+    d[0] = acc[n][0];
+    d[1] = acc[n][1];
+    d[8 * RP] = acc[n][2];
+    d[8 * RP + 1] = acc[n][3];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < rows * RP; i += kRingThreads) {
+  for (int i = threadIdx.x; i < rows * RP; i += kThreads) {
     float v = sums[i];
 #pragma unroll
     for (int w = 1; w < L::KW; ++w) v += sums[w * BM * RP + i];
     sums[i] = v;  // (read by this thread alone)
   }
-  const float scale = g.scales ? __ldg(g.scales + who) : 1.f;
   if (parts > 1) cluster_sync();
   else __syncthreads();
   float* mine = sums + BM * RP;  // all CTAs' (the room of a warp's sums, done with)
   const int share = (rows * RP + parts - 1) / parts;
   for (int i = add ? threadIdx.x : part * share + threadIdx.x;
-       i < (add ? rows * RP : min((part + 1) * share, rows * RP)); i += kRingThreads) {
+       i < (add ? rows * RP : min((part + 1) * share, rows * RP)); i += kThreads) {
     float v = 0.f;
     if (parts > 1) {
       for (int r = 0; r < parts; ++r)
@@ -350,7 +379,6 @@ __global__ void __launch_bounds__(kRingThreads)
   if (parts > 1) cluster_sync();  // no CTA leaves while another reads its sums
   if (!add || !ok || N == 0) return;
   __syncthreads();
-  if (warp == kThreads / 32) return;
   for (int p0 = part * kThreads * kCols; p0 < N; p0 += parts * kThreads * kCols) {
     for (int r0 = 0; r0 < rows; r0 += kRows) {
       float v[kRows][kCols];
@@ -358,7 +386,7 @@ __global__ void __launch_bounds__(kRingThreads)
       for (int r = 0; r < kRows; ++r)
 #pragma unroll
         for (int x = 0; x < kCols; ++x) v[r][x] = 0.f;
-#pragma unroll 1
+#pragma unroll 2
       for (int k = 0; k < rank; k += 8) {
         uint4 w[kCols];
         const int left = rank - k;
@@ -377,36 +405,34 @@ __global__ void __launch_bounds__(kRingThreads)
             w[x] = __ldg(reinterpret_cast<const uint4*>(B + p * g.ldb + k));
           }
         }
-        float2 b[kCols][4];
 #pragma unroll
         for (int x = 0; x < kCols; ++x) {
           uint32_t q[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+          float2 b[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             // (what stands behind a row's rank numbers is none of them)
             if (!ROW && left < 2 * y + 2) q[y] = left <= 2 * y ? 0u : q[y] & 0xFFFFu;
             if constexpr (BF16)
-              b[x][y] = make_float2(__uint_as_float(q[y] << 16),
-                                    __uint_as_float(q[y] & 0xFFFF0000u));
+              b[y] = make_float2(__uint_as_float(q[y] << 16),
+                                 __uint_as_float(q[y] & 0xFFFF0000u));
             else
-              b[x][y] = __half22float2(*reinterpret_cast<const __half2*>(&q[y]));
+              b[y] = __half22float2(*reinterpret_cast<const __half2*>(&q[y]));
           }
-        }
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          if (r0 + r >= rows) continue;
-          const float4* s = reinterpret_cast<const float4*>(mine + (r0 + r) * RP + k);
-          const float4 s0 = s[0], s1 = s[1];
-#pragma unroll
-          for (int x = 0; x < kCols; ++x) {
-            v[r][x] = fmaf(s0.x, b[x][0].x, v[r][x]);
-            v[r][x] = fmaf(s0.y, b[x][0].y, v[r][x]);
-            v[r][x] = fmaf(s0.z, b[x][1].x, v[r][x]);
-            v[r][x] = fmaf(s0.w, b[x][1].y, v[r][x]);
-            v[r][x] = fmaf(s1.x, b[x][2].x, v[r][x]);
-            v[r][x] = fmaf(s1.y, b[x][2].y, v[r][x]);
-            v[r][x] = fmaf(s1.z, b[x][3].x, v[r][x]);
-            v[r][x] = fmaf(s1.w, b[x][3].y, v[r][x]);
+          for (int r = 0; r < kRows; ++r) {
+            if (r0 + r >= rows) continue;
+            const float4* s = reinterpret_cast<const float4*>(mine + (r0 + r) * RP + k);
+            const float4 s0 = s[0], s1 = s[1];
+            float t = v[r][x];
+            t = fmaf(s0.x, b[0].x, t);
+            t = fmaf(s0.y, b[0].y, t);
+            t = fmaf(s0.z, b[1].x, t);
+            t = fmaf(s0.w, b[1].y, t);
+            t = fmaf(s1.x, b[2].x, t);
+            t = fmaf(s1.y, b[2].y, t);
+            t = fmaf(s1.z, b[3].x, t);
+            v[r][x] = fmaf(s1.w, b[3].y, t);
           }
         }
       }
@@ -429,8 +455,12 @@ mma_status_t shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
   static PerContext<bool> attr;
   bool ok = false;
   if (!attr.get(ctx, &ok, [&](bool* v) {
+        // (all of an SM's memory as shared memory: the shared product's CTAs cannot
+        // start beside these on an SM that is divided otherwise)
         *v = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  L::SMEM) == cudaSuccess;
+                                  L::SMEM) == cudaSuccess &&
+             cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                  cudaSharedmemCarveoutMaxShared) == cudaSuccess;
         if (!*v) cudaGetLastError();
         return *v;
       }))
@@ -456,16 +486,18 @@ mma_status_t shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
   while (parts < 8 && pieces * parts * 2 <= 2 * ctx.num_sms && steps >= parts * 4) parts *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(pieces), unsigned(parts), 1);
-  cfg.blockDim = dim3(kRingThreads, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = L::SMEM;
   cfg.stream = ctx.stream;
-  cudaLaunchAttribute at = {};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = 1;
-  at.val.clusterDim.y = unsigned(parts);
-  at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 1;
+  at[0].val.clusterDim.y = unsigned(parts);
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tx, ta, g, low, ctx.status);
   const cudaError_t after = cudaGetLastError();
   return e == cudaSuccess && after == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
@@ -544,99 +576,90 @@ __global__ void __launch_bounds__(kThreads)
 // stands in the last stage behind the piece is another request's and becomes zeros
 // in both (in one alone, an infinity in the other would leave NaN).
 template <bool BF16, int RP>
-__global__ void __launch_bounds__(kRingThreads)
+__global__ void __launch_bounds__(kThreads)
     lora_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) {
   using L = Wgrad<RP>;
   constexpr int RB = L::RB;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  __shared__ int bound[MMA_MAX_GROUPS + 3], scan[kRingThreads / 32];
+  __shared__ Requests req;
   __shared__ Ring ring;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   ring_init(ring, L::STAGES);
-  load_bounds(bound, a.offsets, a.requests, a.T, scan);
-  const Piece piece = piece_of(bound, a.requests, a.per, blockIdx.x);
+  load_requests(req, a.offsets, a.adapters, a.total, a.requests, a.T);
+  const Piece piece = piece_of(req.bound, a.requests, a.per, blockIdx.x);
   const int rows = piece.to - piece.from;
   grid_dependency_wait();  // (the halves; before any return, for the kernel after)
-  if (rows <= 0 || adapter_of(piece.request, a.requests, a.adapters, a.total) < 0) return;
+  if (rows <= 0 || adapter_of(req, piece.request, a.requests) < 0) return;
   const bool second = int(blockIdx.y) >= a.tiles0;
   const Side& side = a.side[second];
   const int f0 = (int(blockIdx.y) - (second ? a.tiles0 : 0)) * kTile;
   const int F = side.F - f0, rank = a.rank;
   const int steps = (rows + kStageRows - 1) / kStageRows;
-  bool ok = true;
-  if (warp == kThreads / 32) {
-    if (lane == 0)
-      ring_fill<L::STAGES, L::STAGE>(
-          ring, smem, steps, L::M_BYTES + a.parts * L::PART, a.status,
-          [&](int step, uint8_t* ms, uint64_t* bar) {
-            const int t = piece.from + step * kStageRows;
-#pragma unroll
-            for (int b = 0; b < kTile / 64; ++b)
-              tma_load_3d(&maps.m[second], bar, ms + b * kStageRows * 128, f0 + b * 64, t, 0);
-            for (int part = 0; part < a.parts; ++part)
-#pragma unroll
-              for (int b = 0; b < RP / RB; ++b)
-                tma_load_3d(&maps.low[second], bar,
-                            ms + L::M_BYTES + part * L::PART + b * kStageRows * RB * 2, b * RB, t,
-                            part);
-          });
-    __syncwarp();
-  }
   float acc[RP / 8][4];
-  if (warp < kThreads / 32) {
 #pragma unroll
-    for (int n = 0; n < RP / 8; ++n)
+  for (int n = 0; n < RP / 8; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
-    const int m = lane >> 3, at = lane & 7;
-    for (int step = 0; step < steps; ++step) {
-      const int s = step % L::STAGES;
-      ok = mbar_wait(&ring.full[s], uint32_t(step / L::STAGES) & 1u, &ring.abort_flag, a.status);
-      const int valid = rows - step * kStageRows;
-      if (valid < kStageRows) {  // (the last stage of all)
-        const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
+  const bool ok = ring_run<L::STAGES, L::STAGE>(
+      ring, smem, steps, L::M_BYTES + a.parts * L::PART, a.status,
+      [&](int step, uint8_t* ms, uint64_t* bar) {
+        const int t = piece.from + step * kStageRows;
+#pragma unroll
         for (int b = 0; b < kTile / 64; ++b)
-          for (int i = valid * 8 + threadIdx.x; i < kStageRows * 8; i += kThreads)
-            *reinterpret_cast<uint4*>(smem + s * L::STAGE + b * kStageRows * 128 + i * 16) = zero;
-        for (int b = 0; b < a.parts * RP / RB; ++b)
-          for (int i = valid * (RB / 8) + threadIdx.x; i < kStageRows * (RB / 8); i += kThreads)
-            *reinterpret_cast<uint4*>(smem + s * L::STAGE + L::M_BYTES +
-                                      b * kStageRows * RB * 2 + i * 16) = zero;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-      }
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint32_t ms = smem_u32(smem + s * L::STAGE), ls = ms + L::M_BYTES;
+          tma_load_3d(&maps.m[second], bar, ms + b * kStageRows * 128, f0 + b * 64, t, 0);
+        for (int part = 0; part < a.parts; ++part)
 #pragma unroll
-      for (int k = 0; k < kStageRows; k += 16) {
-        uint32_t f[4];
-        ldmatrix_x4_trans(f, ms + warp / 4 * kStageRows * 128 +
-                                 swizzled<128>(k + (m >> 1) * 8 + at, warp % 4 * 2 + (m & 1)));
+          for (int b = 0; b < RP / RB; ++b)
+            tma_load_3d(&maps.low[second], bar,
+                        ms + L::M_BYTES + part * L::PART + b * kStageRows * RB * 2, b * RB, t,
+                        part);
+      },
+      [&](int step, uint8_t* stage) {
+        const int valid = rows - step * kStageRows;
+        if (valid < kStageRows) {  // (the last stage of all: no warp gives up before it)
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          for (int b = 0; b < kTile / 64; ++b)
+            for (int i = valid * 8 + threadIdx.x; i < kStageRows * 8; i += kThreads)
+              *reinterpret_cast<uint4*>(stage + b * kStageRows * 128 + i * 16) = zero;
+          for (int b = 0; b < a.parts * RP / RB; ++b)
+            for (int i = valid * (RB / 8) + threadIdx.x; i < kStageRows * (RB / 8);
+                 i += kThreads)
+              *reinterpret_cast<uint4*>(stage + L::M_BYTES + b * kStageRows * RB * 2 + i * 16) =
+                  zero;
+          __syncwarp();
+          mbar_arrive_if(&ring.cleared, lane == 0);
+          if (!__all_sync(0xffffffffu,
+                          mbar_wait(&ring.cleared, 0, &ring.abort_flag, a.status)))
+            return;
+        }
+        const uint32_t ms = smem_u32(stage), ls = ms + L::M_BYTES;
+        const int m = lane >> 3, at = lane & 7;
 #pragma unroll
-        for (int n = 0; n < RP / 16; ++n) {
-          uint32_t b[4];
-          const int where = n * 16 / RB * kStageRows * RB * 2 +
-                            swizzled<RB * 2>(k + (m & 1) * 8 + at, n * 2 % (RB / 8) + (m >> 1));
+        for (int k = 0; k < kStageRows; k += 16) {
+          uint32_t f[4];
+          ldmatrix_x4_trans(f, ms + warp / 4 * kStageRows * 128 +
+                                   swizzled<128>(k + (m >> 1) * 8 + at, warp % 4 * 2 + (m & 1)));
 #pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            if (part >= a.parts) continue;
-            ldmatrix_x4_trans(b, ls + part * L::PART + where);
-            mma16<BF16>(acc[2 * n], f, b[0], b[1]);
-            mma16<BF16>(acc[2 * n + 1], f, b[2], b[3]);
+          for (int n = 0; n < RP / 16; ++n) {
+            uint32_t b[4];
+            const int where = n * 16 / RB * kStageRows * RB * 2 +
+                              swizzled<RB * 2>(k + (m & 1) * 8 + at, n * 2 % (RB / 8) + (m >> 1));
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+              if (part >= a.parts) continue;
+              ldmatrix_x4_trans(b, ls + part * L::PART + where);
+              mma16<BF16>(acc[2 * n], f, b[0], b[1]);
+              mma16<BF16>(acc[2 * n + 1], f, b[2], b[3]);
+            }
           }
         }
-      }
-      __syncwarp();
-      mbar_arrive_if(&ring.empty[s], lane == 0);
-    }
-  }
-  ok = !__syncthreads_or(!ok || ring.abort_flag);
+      });
   if (!ok) return;
   // rows of features per sum, through shared memory
   float* t = reinterpret_cast<float*>(smem);  // [RP][kTile + 4]
-  if (warp < kThreads / 32) {
+  {
 #pragma unroll
     for (int n = 0; n < RP / 8; ++n)
 #pragma unroll
@@ -647,7 +670,7 @@ __global__ void __launch_bounds__(kRingThreads)
   __syncthreads();
   const int64_t features = int64_t(a.side[0].F) + a.side[1].F;
   float* out = a.part + int64_t(blockIdx.x) * rank * features + (second ? a.side[0].F : 0) + f0;
-  for (int i = threadIdx.x; i < rank * kTile; i += kRingThreads)
+  for (int i = threadIdx.x; i < rank * kTile; i += kThreads)
     if (i % kTile < F) out[i / kTile * features + i % kTile] = t[i / kTile * (kTile + 4) + i % kTile];
 }
 
@@ -670,13 +693,15 @@ __device__ __forceinline__ void store_out(void* p, int64_t i, int type, float v)
 // the rank's sums at a time.
 __global__ void __launch_bounds__(kThreads)
     lora_wgrad_sum_kernel(const WgradArgs a) {
-  __shared__ int bound[MMA_MAX_GROUPS + 3], scan[kThreads / 32], list[MMA_MAX_GROUPS], found;
-  load_bounds(bound, a.offsets, a.requests, a.T, scan);
+  __shared__ Requests req;
+  __shared__ int list[MMA_MAX_GROUPS], found;
+  load_requests(req, a.offsets, a.adapters, a.total, a.requests, a.T);
+  const int* bound = req.bound;
   if (threadIdx.x < 32) {
     int n = 0;
     for (int base = 0; base < a.requests; base += 32) {
       const int i = base + threadIdx.x;
-      const bool mine = i < a.requests && (a.adapters ? a.adapters[i] : i) == int(blockIdx.y) &&
+      const bool mine = i < a.requests && req.who[i] == int(blockIdx.y) &&
                         bound[i + 2] > bound[i + 1];
       const unsigned which = __ballot_sync(0xffffffffu, mine);
       if (mine) list[n + __popc(which & ((1u << threadIdx.x) - 1))] = i;
@@ -780,7 +805,7 @@ mma_status_t wgrad(const Ctx& ctx, const LoraWgradProblem& g, const WgradArgs& a
     const int64_t pieces = (g.rows + a.per - 1) / a.per + g.requests + 1;
     const int64_t tiles = a.tiles0 + (g.K + kTile - 1) / kTile;
     ctx.mark_start();
-    e = launch_after(ctx, kernel, dim3(unsigned(pieces), unsigned(tiles)), kRingThreads, L::SMEM,
+    e = launch_after(ctx, kernel, dim3(unsigned(pieces), unsigned(tiles)), kThreads, L::SMEM,
                      maps, a);
     ctx.mark_stop();
   }
