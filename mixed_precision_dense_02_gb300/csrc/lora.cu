@@ -36,7 +36,7 @@ struct Requests {
   // 0, then the offsets, within [0, T] and none below the one before it, then T
   int bound[MMA_MAX_GROUPS + 3];
   int who[MMA_MAX_GROUPS];  // their adapters, or -1
-  int scan[kThreads / 32];
+  int scan[kThreads / 32 + 1];
 };
 
 __device__ __forceinline__ void load_requests(Requests& r, const int* offsets,
@@ -148,13 +148,15 @@ __device__ __forceinline__ void ring_init(Ring& r, int stages) {
   }
 }
 
-// Stages of loads for a block's eight warps.  Thread 0 issues them: the first ones
-// before the loop, later ones when every warp has left the stage (a warp for it alone
-// kept the shared product off the SM: its registers and two of these blocks' did not
-// fit).  load(step, shared memory, barrier) issues a stage of `bytes`; use(step,
-// stage) is what a warp does with it.  Returns, to every thread,
-// whether all waits were met; no load is on its way any more.
-template <int STAGES, int STAGE, class Load, class Use>
+// Stages of loads for a block's eight warps.  load(step, shared memory, barrier)
+// issues a stage of `bytes`; use(step, stage) is what a warp does with it.  PRODUCER: a
+// ninth warp issues them.  Else thread 0 does, the first ones before the loop, later
+// ones when every warp has left the stage: for blocks beside which another kernel's is
+// to fit (two of nine warps and the shared product's twelve need more registers than an
+// SM has).  8192 x 4096 and 8192 rows, rank 16, the gradients: 50 us with a ninth warp,
+// 62 without.  Returns, to every thread, whether all waits were met; no load is on its
+// way any more.
+template <bool PRODUCER, int STAGES, int STAGE, class Load, class Use>
 __device__ __forceinline__ bool ring_run(Ring& r, uint8_t* smem, int steps, int bytes,
                                          unsigned* status, Load&& load, Use&& use) {
   const int lane = threadIdx.x & 31;
@@ -166,28 +168,40 @@ __device__ __forceinline__ bool ring_run(Ring& r, uint8_t* smem, int steps, int 
     load(issued, smem + s * STAGE, &r.full[s]);
     ++issued;
   };
-  if (threadIdx.x == 0)
+  auto parity = [](int step) { return uint32_t(step / STAGES) & 1u; };
+  const bool issuer = threadIdx.x == (PRODUCER ? kThreads : 0);
+  if (issuer)
     while (issued < steps && issued < STAGES) issue();
-  __syncwarp();
-  for (int step = 0; step < steps; ++step) {
-    const int s = step % STAGES;
-    const uint32_t phase = uint32_t(step / STAGES) & 1u;
-    ok = mbar_wait(&r.full[s], phase, &r.abort_flag, status);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    use(step, smem + s * STAGE);
+  if (PRODUCER && threadIdx.x >= kThreads) {
+    if (issuer)
+      while (issued < steps && ok) {
+        const int before = issued - STAGES;
+        ok = mbar_wait(&r.empty[before % STAGES], parity(before), &r.abort_flag, status);
+        if (ok) issue();
+      }
+  } else {
     __syncwarp();
-    mbar_arrive_if(&r.empty[s], lane == 0);
-    if (threadIdx.x == 0 && issued < steps) {
-      ok = mbar_wait(&r.empty[s], phase, &r.abort_flag, status);
-      if (ok) issue();
+    for (int step = 0; step < steps; ++step) {
+      const int s = step % STAGES;
+      ok = mbar_wait(&r.full[s], parity(step), &r.abort_flag, status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      use(step, smem + s * STAGE);
+      __syncwarp();
+      mbar_arrive_if(&r.empty[s], lane == 0);
+      if constexpr (!PRODUCER) {
+        if (issuer && issued < steps) {
+          ok = mbar_wait(&r.empty[s], parity(step), &r.abort_flag, status);
+          if (ok) issue();
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
     }
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
   }
-  if (threadIdx.x == 0)
+  if (issuer)
     for (int i = max(issued - STAGES, 0); i < issued; ++i)
-      mbar_drain(&r.full[i % STAGES], uint32_t(i / STAGES) & 1u, status);
+      mbar_drain(&r.full[i % STAGES], parity(i), status);
   __syncwarp();
   return !__syncthreads_or(!ok || r.abort_flag);
 }
@@ -211,7 +225,9 @@ struct Shrink {
   static constexpr int STAGE = X_BYTES + A_BYTES;
   // (BM 16: two CTAs leave an SM room for one of the shared product's)
   static constexpr int STAGES = BM == 16 ? 2 : 4 * STAGE <= 100 * 1024 ? 4 : 3;
-  static constexpr int BLOCKS = BM == 16 && RP <= 32 ? 4 : 2;  // 56 or 112 registers
+  static constexpr bool PRODUCER = BM != 16;
+  static constexpr int THREADS = kThreads + (PRODUCER ? 32 : 0);
+  static constexpr int BLOCKS = BM == 16 && RP <= 32 ? 4 : 2;  // 64 or 96 registers
   static constexpr int SMEM = STAGES * STAGE + 1024;  // (the sums: 512 * RP bytes)
 };
 
@@ -223,7 +239,7 @@ constexpr CUtensorMapSwizzle swizzle_of(int bytes) {
 }
 
 template <bool BF16, bool ROW, int BM, int RP>
-__global__ void __launch_bounds__(kThreads, Shrink<BM, RP>::BLOCKS)
+__global__ void __launch_bounds__(Shrink<BM, RP>::THREADS, Shrink<BM, RP>::BLOCKS)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ CUtensorMap tmA, const LoraProblem g,
                        const LoraLow low, unsigned* status) {
@@ -273,11 +289,11 @@ __global__ void __launch_bounds__(kThreads, Shrink<BM, RP>::BLOCKS)
     }
   };
   if (who < 0) {
-    for (int i = part * kThreads + threadIdx.x; i < rows * RP; i += parts * kThreads)
+    for (int i = part * L::THREADS + threadIdx.x; i < rows * RP; i += parts * L::THREADS)
       put(i / RP, i % RP, 0.f);
     if (every)
       for (int r = 0; r < rows; ++r)
-        for (int p = part * kThreads + threadIdx.x; p < N; p += parts * kThreads)
+        for (int p = part * L::THREADS + threadIdx.x; p < N; p += parts * L::THREADS)
           extra_row(r)[p] = 0.f;
     return;
   }
@@ -288,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, Shrink<BM, RP>::BLOCKS)
     for (int p0 = part * kThreads * kCols; p0 < N; p0 += parts * kThreads * kCols) {
       const int cols = min(kThreads * kCols, N - p0);
       const int lines = ROW ? (cols + 63) / 64 : int((cols * g.ldb + 63) / 64);
-      for (int i = threadIdx.x; i < (ROW ? lines * rank : lines); i += kThreads)
+      for (int i = threadIdx.x; i < (ROW ? lines * rank : lines); i += L::THREADS)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(
             ROW ? B + i / lines * g.ldb + p0 + min(i % lines * 64, cols - 1)
                 : B + p0 * g.ldb + min(int64_t(i) * 64, (cols - 1) * g.ldb)));
@@ -304,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, Shrink<BM, RP>::BLOCKS)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
   const int mw = warp % L::MW, kw = warp / L::MW;
-  const bool ok = ring_run<L::STAGES, L::STAGE>(
+  const bool ok = ring_run<L::PRODUCER, L::STAGES, L::STAGE>(
       ring, smem, steps, L::STAGE, status,
       [&](int step, uint8_t* xs, uint64_t* bar) {
         const int k = (first + step) * KS;
@@ -346,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, Shrink<BM, RP>::BLOCKS)
   float* sums = reinterpret_cast<float*>(smem);  // [KW][BM][RP]
 #pragma unroll
   for (int n = 0; n < RP / 8; ++n) {
+    if (L::PRODUCER && warp == kThreads / 32) break;
     float* d = sums + (kw * BM + mw * 16 + (lane >> 2)) * RP + n * 8 + 2 * (lane & 3);
     d[0] = acc[n][0];
     d[1] = acc[n][1];
@@ -353,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, Shrink<BM, RP>::BLOCKS)
     d[8 * RP + 1] = acc[n][3];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < rows * RP; i += kThreads) {
+  for (int i = threadIdx.x; i < rows * RP; i += L::THREADS) {
     float v = sums[i];
 #pragma unroll
     for (int w = 1; w < L::KW; ++w) v += sums[w * BM * RP + i];
@@ -364,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, Shrink<BM, RP>::BLOCKS)
   float* mine = sums + BM * RP;  // all CTAs' (the room of a warp's sums, done with)
   const int share = (rows * RP + parts - 1) / parts;
   for (int i = add ? threadIdx.x : part * share + threadIdx.x;
-       i < (add ? rows * RP : min((part + 1) * share, rows * RP)); i += kThreads) {
+       i < (add ? rows * RP : min((part + 1) * share, rows * RP)); i += L::THREADS) {
     float v = 0.f;
     if (parts > 1) {
       for (int r = 0; r < parts; ++r)
@@ -379,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, Shrink<BM, RP>::BLOCKS)
   if (parts > 1) cluster_sync();  // no CTA leaves while another reads its sums
   if (!add || !ok || N == 0) return;
   __syncthreads();
+  if (L::PRODUCER && warp == kThreads / 32) return;
   for (int p0 = part * kThreads * kCols; p0 < N; p0 += parts * kThreads * kCols) {
     for (int r0 = 0; r0 < rows; r0 += kRows) {
       float v[kRows][kCols];
@@ -486,7 +504,7 @@ mma_status_t shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
   while (parts < 8 && pieces * parts * 2 <= 2 * ctx.num_sms && steps >= parts * 4) parts *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(pieces), unsigned(parts), 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(L::THREADS, 1, 1);
   cfg.dynamicSmemBytes = L::SMEM;
   cfg.stream = ctx.stream;
   cudaLaunchAttribute at[2] = {};
@@ -576,7 +594,7 @@ __global__ void __launch_bounds__(kThreads)
 // stands in the last stage behind the piece is another request's and becomes zeros
 // in both (in one alone, an infinity in the other would leave NaN).
 template <bool BF16, int RP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads + 32)
     lora_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) {
   using L = Wgrad<RP>;
   constexpr int RB = L::RB;
@@ -602,7 +620,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int n = 0; n < RP / 8; ++n)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
-  const bool ok = ring_run<L::STAGES, L::STAGE>(
+  const bool ok = ring_run<true, L::STAGES, L::STAGE>(
       ring, smem, steps, L::M_BYTES + a.parts * L::PART, a.status,
       [&](int step, uint8_t* ms, uint64_t* bar) {
         const int t = piece.from + step * kStageRows;
@@ -659,7 +677,7 @@ __global__ void __launch_bounds__(kThreads)
   if (!ok) return;
   // rows of features per sum, through shared memory
   float* t = reinterpret_cast<float*>(smem);  // [RP][kTile + 4]
-  {
+  if (warp < kThreads / 32) {
 #pragma unroll
     for (int n = 0; n < RP / 8; ++n)
 #pragma unroll
@@ -670,7 +688,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   const int64_t features = int64_t(a.side[0].F) + a.side[1].F;
   float* out = a.part + int64_t(blockIdx.x) * rank * features + (second ? a.side[0].F : 0) + f0;
-  for (int i = threadIdx.x; i < rank * kTile; i += kThreads)
+  for (int i = threadIdx.x; i < rank * kTile; i += kThreads + 32)
     if (i % kTile < F) out[i / kTile * features + i % kTile] = t[i / kTile * (kTile + 4) + i % kTile];
 }
 
@@ -805,7 +823,7 @@ mma_status_t wgrad(const Ctx& ctx, const LoraWgradProblem& g, const WgradArgs& a
     const int64_t pieces = (g.rows + a.per - 1) / a.per + g.requests + 1;
     const int64_t tiles = a.tiles0 + (g.K + kTile - 1) / kTile;
     ctx.mark_start();
-    e = launch_after(ctx, kernel, dim3(unsigned(pieces), unsigned(tiles)), kThreads, L::SMEM,
+    e = launch_after(ctx, kernel, dim3(unsigned(pieces), unsigned(tiles)), kThreads + 32, L::SMEM,
                      maps, a);
     ctx.mark_stop();
   }
