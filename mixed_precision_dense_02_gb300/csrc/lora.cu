@@ -217,19 +217,23 @@ __device__ __forceinline__ bool ring_run(Ring& r, uint8_t* smem, int steps, int 
 // A few rows' share of the result, s B, is made here as well: of every row up to
 // kLoraEveryRow, else of the requests of fewer than kLoraRows.  Every CTA of the
 // cluster adds all of the piece's sums up, and a lane has kCols columns of B.
-template <int BM, int RP>
+// BM 16: two stages and 64 registers a thread.  With EVERY (up to kLoraEveryRow rows)
+// two CTAs then leave an SM room for one of the shared product's, which runs beside
+// them.
+template <int BM, int RP, bool EVERY>
 struct Shrink {
   static constexpr int MW = BM / 16, KW = 8 / MW;  // warps along rows, along k
   static constexpr int KS = BM == 16 ? 256 : 128;  // k's per stage
   static constexpr int X_BYTES = BM * KS * 2, A_BYTES = RP * KS * 2;
   static constexpr int STAGE = X_BYTES + A_BYTES;
-  // (BM 16: two CTAs leave an SM room for one of the shared product's)
   static constexpr int STAGES = BM == 16 ? 2 : 4 * STAGE <= 100 * 1024 ? 4 : 3;
   static constexpr bool PRODUCER = BM != 16;
   static constexpr int THREADS = kThreads + (PRODUCER ? 32 : 0);
-  static constexpr int BLOCKS = BM == 16 && RP <= 32 ? 4 : 2;  // 64 or 96 registers
+  static constexpr int BLOCKS = BM == 16 && RP <= 32 ? 4 : 2;
   static constexpr int SMEM = STAGES * STAGE + 1024;  // (the sums: 512 * RP bytes)
 };
+
+constexpr int kSmallBlocks = 4096;  // rows up to which blocks have 16
 
 // The swizzle of rows of `bytes` (the same that swizzled() computes).
 constexpr CUtensorMapSwizzle swizzle_of(int bytes) {
@@ -238,15 +242,81 @@ constexpr CUtensorMapSwizzle swizzle_of(int bytes) {
                        : CU_TENSOR_MAP_SWIZZLE_128B;
 }
 
-template <bool BF16, bool ROW, int BM, int RP>
-__global__ void __launch_bounds__(Shrink<BM, RP>::THREADS, Shrink<BM, RP>::BLOCKS)
+// `many` rows of extra, up to R: their sums `s` (RP apart, zeros past the rank; the
+// room behind the last is read too) times kCols columns of B per thread from p0 on,
+// kThreads apart, whose loads go together.
+constexpr int kCols = 4;
+
+template <bool BF16, bool ROW, int R, int RP>
+__device__ __forceinline__ void expand(const LoraProblem& g, const uint16_t* B, const float* s,
+                                       int many, int p0, float* out) {
+  const int rank = int(g.rank), N = int(g.N);
+  float2 v[R][kCols];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) v[r][x] = make_float2(0.f, 0.f);
+  const int p1 = p0 + threadIdx.x;
+#pragma unroll 2
+  for (int k = 0; k < rank; k += 8) {
+    uint4 w[kCols];
+    const int left = rank - k;
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) {
+      const int p = min(p1 + x * kThreads, N - 1);
+      if constexpr (ROW) {
+        uint32_t f[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) f[y] = y < left ? B[(k + y) * g.ldb + p] : 0u;
+        w[x] = make_uint4(f[0] | f[1] << 16, f[2] | f[3] << 16, f[4] | f[5] << 16,
+                          f[6] | f[7] << 16);
+      } else {
+        w[x] = __ldg(reinterpret_cast<const uint4*>(B + p * g.ldb + k));
+      }
+    }
+    if (!ROW && left < 8) {  // what stands behind a row's rank numbers is none of them
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) {
+        uint32_t q[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (left < 2 * y + 2) q[y] = left <= 2 * y ? 0u : q[y] & 0xFFFFu;
+        w[x] = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) {
+      const uint32_t q[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        float2 b;
+        if constexpr (BF16)
+          b = make_float2(__uint_as_float(q[y] << 16), __uint_as_float(q[y] & 0xFFFF0000u));
+        else
+          b = __half22float2(*reinterpret_cast<const __half2*>(&q[y]));
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          v[r][x] = __ffma2_rn(*reinterpret_cast<const float2*>(s + r * RP + k + 2 * y), b,
+                               v[r][x]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int x = 0; x < kCols; ++x)
+      if (r < many && p1 + x * kThreads < N) out[int64_t(r) * N + p1 + x * kThreads] = v[r][x].x + v[r][x].y;
+}
+
+template <bool BF16, bool ROW, int BM, int RP, bool EVERY>
+__global__ void __launch_bounds__(Shrink<BM, RP, EVERY>::THREADS, Shrink<BM, RP, EVERY>::BLOCKS)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ CUtensorMap tmA, const LoraProblem g,
                        const LoraLow low, unsigned* status) {
-  using L = Shrink<BM, RP>;
+  using L = Shrink<BM, RP, EVERY>;
   constexpr int KS = L::KS, KB = KS / 64;
   constexpr int RB = RP < 64 ? RP : 64;  // (ROW) sums per box
-  constexpr int kCols = 4, kRows = BM == 16 ? 2 : 4;
+  constexpr int kRows = L::BLOCKS == 4 ? 1 : 2;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -271,13 +341,12 @@ __global__ void __launch_bounds__(Shrink<BM, RP>::THREADS, Shrink<BM, RP>::BLOCK
   // (the same in all CTAs of the cluster, so that all of them return)
   if (rows <= 0) return;
   const int part = blockIdx.y, parts = gridDim.y;
-  const bool every = g.rows <= kLoraEveryRow;
   const int first_of = bound[piece.request];
-  const bool add = every || bound[piece.request + 1] - first_of < kLoraRows;
+  const bool add = EVERY || bound[piece.request + 1] - first_of < kLoraRows;
   auto extra_row = [&](int row) {
     const int64_t t = piece.from + row;
     return low.extra +
-           (every ? t : int64_t(piece.request - 1) * (kLoraRows - 1) + t - first_of) * N;
+           (EVERY ? t : int64_t(piece.request - 1) * (kLoraRows - 1) + t - first_of) * N;
   };
   auto put = [&](int row, int n, float v) {
     const int64_t t = piece.from + row;
@@ -291,7 +360,7 @@ __global__ void __launch_bounds__(Shrink<BM, RP>::THREADS, Shrink<BM, RP>::BLOCK
   if (who < 0) {
     for (int i = part * L::THREADS + threadIdx.x; i < rows * RP; i += parts * L::THREADS)
       put(i / RP, i % RP, 0.f);
-    if (every)
+    if (EVERY)
       for (int r = 0; r < rows; ++r)
         for (int p = part * L::THREADS + threadIdx.x; p < N; p += parts * L::THREADS)
           extra_row(r)[p] = 0.f;
@@ -398,78 +467,17 @@ __global__ void __launch_bounds__(Shrink<BM, RP>::THREADS, Shrink<BM, RP>::BLOCK
   __syncthreads();
   if (L::PRODUCER && warp == kThreads / 32) return;
   for (int p0 = part * kThreads * kCols; p0 < N; p0 += parts * kThreads * kCols) {
-    for (int r0 = 0; r0 < rows; r0 += kRows) {
-      float v[kRows][kCols];
-#pragma unroll
-      for (int r = 0; r < kRows; ++r)
-#pragma unroll
-        for (int x = 0; x < kCols; ++x) v[r][x] = 0.f;
-#pragma unroll 2
-      for (int k = 0; k < rank; k += 8) {
-        uint4 w[kCols];
-        const int left = rank - k;
-#pragma unroll
-        for (int x = 0; x < kCols; ++x) {
-          const int p = p0 + x * kThreads + threadIdx.x;
-          w[x] = make_uint4(0, 0, 0, 0);
-          if (p >= N) continue;
-          if constexpr (ROW) {
-            uint32_t f[8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) f[y] = y < left ? B[(k + y) * g.ldb + p] : 0u;
-            w[x] = make_uint4(f[0] | f[1] << 16, f[2] | f[3] << 16, f[4] | f[5] << 16,
-                              f[6] | f[7] << 16);
-          } else {
-            w[x] = __ldg(reinterpret_cast<const uint4*>(B + p * g.ldb + k));
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < kCols; ++x) {
-          uint32_t q[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-          float2 b[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            // (what stands behind a row's rank numbers is none of them)
-            if (!ROW && left < 2 * y + 2) q[y] = left <= 2 * y ? 0u : q[y] & 0xFFFFu;
-            if constexpr (BF16)
-              b[y] = make_float2(__uint_as_float(q[y] << 16),
-                                 __uint_as_float(q[y] & 0xFFFF0000u));
-            else
-              b[y] = __half22float2(*reinterpret_cast<const __half2*>(&q[y]));
-          }
-#pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            if (r0 + r >= rows) continue;
-            const float4* s = reinterpret_cast<const float4*>(mine + (r0 + r) * RP + k);
-            const float4 s0 = s[0], s1 = s[1];
-            float t = v[r][x];
-            t = fmaf(s0.x, b[0].x, t);
-            t = fmaf(s0.y, b[0].y, t);
-            t = fmaf(s0.z, b[1].x, t);
-            t = fmaf(s0.w, b[1].y, t);
-            t = fmaf(s1.x, b[2].x, t);
-            t = fmaf(s1.y, b[2].y, t);
-            t = fmaf(s1.z, b[3].x, t);
-            v[r][x] = fmaf(s1.w, b[3].y, t);
-          }
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < kRows; ++r)
-#pragma unroll
-        for (int x = 0; x < kCols; ++x) {
-          const int p = p0 + x * kThreads + threadIdx.x;
-          if (r0 + r < rows && p < N) extra_row(r0 + r)[p] = v[r][x];
-        }
-    }
+    for (int r0 = 0; r0 < rows; r0 += kRows)
+      expand<BF16, ROW, kRows, RP>(g, B, mine + r0 * RP, min(rows - r0, kRows), p0,
+                                   extra_row(r0));
   }
 }
 
-template <bool BF16, bool ROW, int BM, int RP>
+template <bool BF16, bool ROW, int BM, int RP, bool EVERY>
 mma_status_t shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
-  using L = Shrink<BM, RP>;
+  using L = Shrink<BM, RP, EVERY>;
   constexpr int RB = RP < 64 ? RP : 64;
-  auto kernel = lora_shrink_kernel<BF16, ROW, BM, RP>;
+  auto kernel = lora_shrink_kernel<BF16, ROW, BM, RP, EVERY>;
   static PerContext<bool> attr;
   bool ok = false;
   if (!attr.get(ctx, &ok, [&](bool* v) {
@@ -499,9 +507,12 @@ mma_status_t shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
     return MMA_ERR_LAUNCH;
   const int64_t pieces = (g.rows + BM - 1) / BM + g.requests + 1;
   const int64_t steps = (g.K + L::KS - 1) / L::KS;
-  // as many CTAs per piece as fill the SMs twice, each with two stages at least
+  // As many CTAs per piece as there is room for at once (with few rows twice per SM,
+  // beside the shared product), each with two stages at least.
+  const int per_sm = EVERY ? 2 : std::min(BM == 16 ? 4 : 2, 224 * 1024 / (L::SMEM + 10 * 1024));
   int parts = 1;
-  while (parts < 8 && pieces * parts * 2 <= 2 * ctx.num_sms && steps >= parts * 4) parts *= 2;
+  while (parts < 8 && pieces * parts * 2 <= int64_t(per_sm) * ctx.num_sms && steps >= parts * 4)
+    parts *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(pieces), unsigned(parts), 1);
   cfg.blockDim = dim3(L::THREADS, 1, 1);
@@ -844,8 +855,9 @@ mma_status_t launch_lora_shrink(const Ctx& ctx, const LoraProblem& g, const Lora
     auto go = [&](auto bf16, auto row) {
       constexpr bool B = decltype(bf16)::value, R = decltype(row)::value;
       // (few rows: the k range over all eight warps)
-      return g.rows <= 256 ? shrink<B, R, 16, RP>(ctx, g, low)
-                           : shrink<B, R, 64, RP>(ctx, g, low);
+      return g.rows <= kLoraEveryRow ? shrink<B, R, 16, RP, true>(ctx, g, low)
+             : g.rows <= kSmallBlocks ? shrink<B, R, 16, RP, false>(ctx, g, low)
+                                      : shrink<B, R, 64, RP, false>(ctx, g, low);
     };
     if (g.bf16)
       return g.row_major ? go(std::true_type{}, std::true_type{})
