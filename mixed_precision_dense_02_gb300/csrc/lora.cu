@@ -577,9 +577,15 @@ struct Wgrad {
   static constexpr int RB = RP < 64 ? RP : 64;  // sums per box
   static constexpr int M_BYTES = kStageRows * kTile * 2;
   static constexpr int PART = kStageRows * RP * 2;  // one part of the sums
-  static constexpr int STAGE = M_BYTES + 3 * PART;
-  static constexpr int STAGES = RP <= 64 ? 4 : 3;
-  static constexpr int SMEM = STAGES * STAGE + 1024;
+  static constexpr int stage(int parts) { return M_BYTES + parts * PART; }
+  // two CTAs per SM if that leaves them two stages each
+  static constexpr int per_sm(int parts) { return 2 * stage(parts) <= 102 * 1024 ? 2 : 1; }
+  static constexpr int stages(int parts) {
+    const int n = (per_sm(parts) == 2 ? 102 : 210) * 1024 / stage(parts);
+    return n < 4 ? n : 4;
+  }
+  static constexpr int smem(int parts) { return stages(parts) * stage(parts) + 1024; }
+  static_assert(stages(3) >= 2 && smem(3) <= 216 * 1024, "the ring");
 };
 
 // Both sides' sums in parts of 16 bits.
@@ -588,119 +594,179 @@ __global__ void __launch_bounds__(kThreads)
     lora_halves_kernel(const WgradArgs a) {
   grid_dependents_start();
   const Side& side = a.side[blockIdx.y];
-  const int64_t all = int64_t(a.T) * a.ld16;
   if (side.F == 0) return;
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < all;
-       i += int64_t(gridDim.x) * kThreads) {
-    const int64_t t = i / a.ld16;
-    const int n = int(i - t * a.ld16);
-    float v = n < a.rank ? side.low[t * side.ldl + n] : 0.f;
-    for (int part = 0; part < a.parts; ++part)
-      a.halves[(int64_t(blockIdx.y) * a.parts + part) * all + i] = take_half<BF16>(v);
-  }
+  const int64_t all = int64_t(a.T) * a.ld16;
+  uint16_t* const out = a.halves + blockIdx.y * a.parts * all;
+  // 8, 16 or 32 lanes for a row
+  const int width = a.ld16 <= 8 ? 8 : a.ld16 <= 16 ? 16 : 32;
+  const int per = kThreads / width;
+  for (int64_t t = int64_t(blockIdx.x) * per + threadIdx.x / width; t < a.T;
+       t += int64_t(gridDim.x) * per)
+    for (int n = threadIdx.x % width; n < a.ld16; n += width) {
+      float v = n < a.rank ? side.low[t * side.ldl + n] : 0.f;
+      for (int part = 0; part < a.parts; ++part)
+        out[part * all + t * a.ld16 + n] = take_half<BF16>(v);
+    }
 }
 
-// Piece blockIdx.x's share of 128 features: G[f][n] = sum over its rows M[t][f] *
-// low[t][n] on the tensor cores, FP32.  Rows and sums by TMA into a ring; what
-// stands in the last stage behind the piece is another request's and becomes zeros
-// in both (in one alone, an infinity in the other would leave NaN).
-template <bool BF16, int RP>
+// A piece's share of 128 features: G[f][n] = sum over its rows M[t][f] * low[t][n] on
+// the tensor cores, FP32.  As many CTAs as run at once take the shares in turn, the
+// features of a piece side by side, through one ring of rows and sums that runs on from
+// share to share (a CTA for each share: 51 us of 8192 x (8192 + 4096), rank 16, so 41).
+// What stands in a share's last stage behind the piece is another request's and becomes
+// zeros in both (in one alone, an infinity in the other would leave NaN).
+template <bool BF16, int RP, int PARTS>
 __global__ void __launch_bounds__(kThreads + 32)
-    lora_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a) {
+    lora_wgrad_kernel(const __grid_constant__ WgradMaps maps, const WgradArgs a, int pieces,
+                      int tiles) {
   using L = Wgrad<RP>;
   constexpr int RB = L::RB;
+  constexpr int stages = L::stages(PARTS), stage_bytes = L::stage(PARTS);
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   __shared__ Requests req;
   __shared__ Ring ring;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  ring_init(ring, L::STAGES);
+  grid_dependents_start();
+  ring_init(ring, stages);
   load_requests(req, a.offsets, a.adapters, a.total, a.requests, a.T);
-  const Piece piece = piece_of(req.bound, a.requests, a.per, blockIdx.x);
-  const int rows = piece.to - piece.from;
-  grid_dependency_wait();  // (the halves; before any return, for the kernel after)
-  if (rows <= 0 || adapter_of(req, piece.request, a.requests) < 0) return;
-  const bool second = int(blockIdx.y) >= a.tiles0;
-  const Side& side = a.side[second];
-  const int f0 = (int(blockIdx.y) - (second ? a.tiles0 : 0)) * kTile;
-  const int F = side.F - f0, rank = a.rank;
-  const int steps = (rows + kStageRows - 1) / kStageRows;
-  float acc[RP / 8][4];
+  grid_dependency_wait();  // (the halves)
+  struct Share {
+    int from, rows, second, f0;
+  };
+  // share i, the shares of a piece in a row; without rows or an adapter: rows 0
+  auto share_of = [&](int i) {
+    const int u = i / tiles, tile = i - u * tiles;
+    int j = 0;
+    for (int hi = a.requests + 2; hi - j > 1;) {
+      const int mid = (j + hi) >> 1;
+      if (req.bound[mid] / a.per + mid <= u) j = mid; else hi = mid;
+    }
+    const int64_t from = max(int64_t(u - j) * a.per, int64_t(req.bound[j]));
+    const int to = int(min(int64_t(u - j + 1) * a.per, int64_t(req.bound[j + 1])));
+    const bool none = adapter_of(req, j, a.requests) < 0 || from >= to;
+    const int second = tile >= a.tiles0;
+    return Share{int(from), none ? 0 : int(to - from), second,
+                 (tile - (second ? a.tiles0 : 0)) * kTile};
+  };
+  const int shares = pieces * tiles;
+  bool ok = true;
+  int s = 0;
+  uint32_t phase = 0;
+  auto next = [&] {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  };
+  if (warp == kThreads / 32) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int i = blockIdx.x; i < shares && ok; i += gridDim.x) {
+        const Share w = share_of(i);
+        for (int t = 0; t < w.rows; t += kStageRows) {
+          ok = mbar_wait(&ring.empty[s], phase ^ 1u, &ring.abort_flag, a.status);
+          if (!ok) break;
+          uint8_t* ms = smem + s * stage_bytes;
+          uint64_t* bar = &ring.full[s];
+          mbar_arrive_expect_tx(bar, uint32_t(stage_bytes));
 #pragma unroll
-  for (int n = 0; n < RP / 8; ++n)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
-  const bool ok = ring_run<true, L::STAGES, L::STAGE>(
-      ring, smem, steps, L::M_BYTES + a.parts * L::PART, a.status,
-      [&](int step, uint8_t* ms, uint64_t* bar) {
-        const int t = piece.from + step * kStageRows;
-#pragma unroll
-        for (int b = 0; b < kTile / 64; ++b)
-          tma_load_3d(&maps.m[second], bar, ms + b * kStageRows * 128, f0 + b * 64, t, 0);
-        for (int part = 0; part < a.parts; ++part)
-#pragma unroll
-          for (int b = 0; b < RP / RB; ++b)
-            tma_load_3d(&maps.low[second], bar,
-                        ms + L::M_BYTES + part * L::PART + b * kStageRows * RB * 2, b * RB, t,
-                        part);
-      },
-      [&](int step, uint8_t* stage) {
-        const int valid = rows - step * kStageRows;
-        if (valid < kStageRows) {  // (the last stage of all: no warp gives up before it)
-          const uint4 zero = make_uint4(0, 0, 0, 0);
           for (int b = 0; b < kTile / 64; ++b)
-            for (int i = valid * 8 + threadIdx.x; i < kStageRows * 8; i += kThreads)
-              *reinterpret_cast<uint4*>(stage + b * kStageRows * 128 + i * 16) = zero;
-          for (int b = 0; b < a.parts * RP / RB; ++b)
-            for (int i = valid * (RB / 8) + threadIdx.x; i < kStageRows * (RB / 8);
-                 i += kThreads)
-              *reinterpret_cast<uint4*>(stage + L::M_BYTES + b * kStageRows * RB * 2 + i * 16) =
-                  zero;
-          __syncwarp();
-          mbar_arrive_if(&ring.cleared, lane == 0);
-          if (!__all_sync(0xffffffffu,
-                          mbar_wait(&ring.cleared, 0, &ring.abort_flag, a.status)))
-            return;
+            tma_load_3d(&maps.m[w.second], bar, ms + b * kStageRows * 128, w.f0 + b * 64,
+                        w.from + t, 0);
+          for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+            for (int b = 0; b < RP / RB; ++b)
+              tma_load_3d(&maps.low[w.second], bar,
+                          ms + L::M_BYTES + part * L::PART + b * kStageRows * RB * 2, b * RB,
+                          w.from + t, part);
+          ++issued;
+          next();
         }
-        const uint32_t ms = smem_u32(stage), ls = ms + L::M_BYTES;
-        const int m = lane >> 3, at = lane & 7;
+      }
+      // (the stages from s on are those of the round before)
+      for (int c = 0; c < stages; ++c)
+        if (c < s || issued >= stages)
+          mbar_drain(&ring.full[c], c < s ? phase : phase ^ 1u, a.status);
+    }
+    return;
+  }
+  const int64_t features = int64_t(a.side[0].F) + a.side[1].F;
+  // This lane's addresses of the first rows' blocks (16 rows on the swizzle is the
+  // same).
+  const int m = lane >> 3, at = lane & 7;
+  const uint32_t f_at = warp / 4 * kStageRows * 128 +
+                        swizzled<128>((m >> 1) * 8 + at, warp % 4 * 2 + (m & 1));
+  uint32_t low_at[RB / 16];
 #pragma unroll
-        for (int k = 0; k < kStageRows; k += 16) {
-          uint32_t f[4];
-          ldmatrix_x4_trans(f, ms + warp / 4 * kStageRows * 128 +
-                                   swizzled<128>(k + (m >> 1) * 8 + at, warp % 4 * 2 + (m & 1)));
-#pragma unroll
-          for (int n = 0; n < RP / 16; ++n) {
-            uint32_t b[4];
-            const int where = n * 16 / RB * kStageRows * RB * 2 +
-                              swizzled<RB * 2>(k + (m & 1) * 8 + at, n * 2 % (RB / 8) + (m >> 1));
-#pragma unroll
-            for (int part = 0; part < 3; ++part) {
-              if (part >= a.parts) continue;
-              ldmatrix_x4_trans(b, ls + part * L::PART + where);
-              mma16<BF16>(acc[2 * n], f, b[0], b[1]);
-              mma16<BF16>(acc[2 * n + 1], f, b[2], b[3]);
-            }
-          }
-        }
-      });
-  if (!ok) return;
-  // rows of features per sum, through shared memory
-  float* t = reinterpret_cast<float*>(smem);  // [RP][kTile + 4]
-  if (warp < kThreads / 32) {
+  for (int n = 0; n < RB / 16; ++n)
+    low_at[n] = swizzled<RB * 2>((m & 1) * 8 + at, n * 2 + (m >> 1));
+  uint32_t cleared = 0;
+  for (int i = blockIdx.x; i < shares && ok; i += gridDim.x) {
+    const Share w = share_of(i);
+    if (w.rows == 0) continue;
+    float acc[RP / 8][4];
 #pragma unroll
     for (int n = 0; n < RP / 8; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        t[(n * 8 + 2 * (lane & 3) + (j & 1)) * (kTile + 4) + warp * 16 + (lane >> 2) +
-          (j >> 1) * 8] = acc[n][j];
+      for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
+    for (int t = 0; t < w.rows; t += kStageRows, next()) {
+      uint8_t* stage = smem + s * stage_bytes;
+      ok = mbar_wait(&ring.full[s], phase, &ring.abort_flag, a.status);
+      const int valid = w.rows - t;
+      if (valid < kStageRows) {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        for (int b = 0; b < kTile / 64; ++b)
+          for (int x = valid * 8 + threadIdx.x; x < kStageRows * 8; x += kThreads)
+            *reinterpret_cast<uint4*>(stage + b * kStageRows * 128 + x * 16) = zero;
+        for (int b = 0; b < PARTS * RP / RB; ++b)
+          for (int x = valid * (RB / 8) + threadIdx.x; x < kStageRows * (RB / 8); x += kThreads)
+            *reinterpret_cast<uint4*>(stage + L::M_BYTES + b * kStageRows * RB * 2 + x * 16) =
+                zero;
+        // (the loads that follow into this stage come after these writes)
+        fence_proxy_async_smem();
+        __syncwarp();
+        mbar_arrive_if(&ring.cleared, lane == 0);
+        ok = mbar_wait(&ring.cleared, cleared, &ring.abort_flag, a.status) && ok;
+        cleared ^= 1u;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t ms = smem_u32(stage) + f_at;
+      const uint32_t ls = smem_u32(stage) + L::M_BYTES;
+#pragma unroll
+      for (int k = 0; k < kStageRows; k += 16) {
+        uint32_t f[4];
+        ldmatrix_x4_trans(f, ms + k * 128);
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+          for (int n = 0; n < RP / 16; ++n) {
+            uint32_t b[4];
+            ldmatrix_x4_trans(b, ls + part * L::PART + n * 16 / RB * kStageRows * RB * 2 +
+                                     k * RB * 2 + low_at[n * 16 % RB / 16]);
+            mma16<BF16>(acc[2 * n], f, b[0], b[1]);
+            mma16<BF16>(acc[2 * n + 1], f, b[2], b[3]);
+          }
+      }
+      __syncwarp();
+      mbar_arrive_if(&ring.empty[s], lane == 0);
+    }
+    if (!ok) break;
+    // (eight lanes: 32 consecutive bytes of four of the sums' rows)
+    float* out = a.part + int64_t(i / tiles) * a.rank * features +
+                 (w.second ? a.side[0].F : 0) + w.f0;
+    const int F = a.side[w.second].F - w.f0;
+#pragma unroll
+    for (int n = 0; n < RP / 8; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = n * 8 + 2 * (lane & 3) + (j & 1);
+        const int f = warp * 16 + (lane >> 2) + (j >> 1) * 8;
+        if (row < a.rank && f < F) out[row * features + f] = acc[n][j];
+      }
   }
-  __syncthreads();
-  const int64_t features = int64_t(a.side[0].F) + a.side[1].F;
-  float* out = a.part + int64_t(blockIdx.x) * rank * features + (second ? a.side[0].F : 0) + f0;
-  for (int i = threadIdx.x; i < rank * kTile; i += kThreads + 32)
-    if (i % kTile < F) out[i / kTile * features + i % kTile] = t[i / kTile * (kTile + 4) + i % kTile];
 }
 
 __device__ __forceinline__ float load_out(const void* p, int64_t i, int type) {
@@ -718,12 +784,18 @@ __device__ __forceinline__ void store_out(void* p, int64_t i, int type, float v)
     static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
-// Adapter blockIdx.y: its pieces' shares added in order, for 256 features, four of
-// the rank's sums at a time.
+// Adapter blockIdx.y: its pieces' shares of 256 features added in order, a lane per
+// feature and kSums of the rank's sums at a time, whose loads go together (64 features
+// to a block, four sums to a thread: 8192 features of rank 64 62 us, so 20).
+constexpr int kSums = 8;
+// (at most 2^31 rows in blocks of 2^20 and 1024 requests; rows_per_piece)
+constexpr int kMostPieces = 2048 + MMA_MAX_GROUPS + 2;
+
 __global__ void __launch_bounds__(kThreads)
     lora_wgrad_sum_kernel(const WgradArgs a) {
   __shared__ Requests req;
-  __shared__ int list[MMA_MAX_GROUPS], found;
+  __shared__ int list[kMostPieces], found;  // its pieces
+  // (older than the kernel before)
   load_requests(req, a.offsets, a.adapters, a.total, a.requests, a.T);
   const int* bound = req.bound;
   if (threadIdx.x < 32) {
@@ -732,57 +804,72 @@ __global__ void __launch_bounds__(kThreads)
       const int i = base + threadIdx.x;
       const bool mine = i < a.requests && req.who[i] == int(blockIdx.y) &&
                         bound[i + 2] > bound[i + 1];
-      const unsigned which = __ballot_sync(0xffffffffu, mine);
-      if (mine) list[n + __popc(which & ((1u << threadIdx.x) - 1))] = i;
-      n += __popc(which);
+      for (unsigned left = __ballot_sync(0xffffffffu, mine); left; left &= left - 1) {
+        const int j = base + __ffs(left);  // counted from the one before the first
+        const int first = bound[j] / a.per, last = (bound[j + 1] - 1) / a.per;
+        for (int b = first + threadIdx.x; b <= last; b += 32) list[n + b - first] = b + j;
+        n += last - first + 1;
+      }
     }
     if (threadIdx.x == 0) found = n;
   }
   __syncthreads();
-  const int features = a.side[0].F + a.side[1].F;
-  const int at = blockIdx.x * kThreads + threadIdx.x;
-  if (at >= features) return;
-  const bool second = at >= a.side[0].F;
+  if (a.accumulate && found == 0) return;
+  grid_dependency_wait();
+  const int tiles0 = (a.side[0].F + kThreads - 1) / kThreads;
+  const bool second = int(blockIdx.x) >= tiles0;
   const Side& side = a.side[second];
-  const int f = at - (second ? a.side[0].F : 0);
-  const int64_t out = int64_t(blockIdx.y) * side.slice;
-  for (int n0 = blockIdx.z * 4; n0 < a.rank; n0 += gridDim.z * 4) {
-    const int many = min(a.rank - n0, 4);
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < found; ++i) {
-      const int j = list[i] + 1;
-      const int first = bound[j] / a.per, last = (bound[j + 1] - 1) / a.per;
-      for (int b = first; b <= last; ++b) {
-        const float* p = a.part + (int64_t(b + j) * a.rank + n0) * features + at;
+  const int64_t features = int64_t(a.side[0].F) + a.side[1].F;
+  const int f = (int(blockIdx.x) - (second ? tiles0 : 0)) * kThreads + threadIdx.x;
+  if (f >= side.F) return;
+  const int n0 = blockIdx.z * kSums, many = min(a.rank - n0, kSums);
+  const float* const part = a.part + (second ? a.side[0].F : 0) + f + n0 * features;
+  float v[kSums] = {};
+#pragma unroll 2
+  for (int i = 0; i < found; ++i) {
+    const float* p = part + int64_t(list[i]) * a.rank * features;
+    float w[kSums];
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (x < many) v[x] += p[int64_t(x) * features];
-      }
-    }
-    if (a.accumulate && found == 0) continue;
-    const int64_t o = out + (side.by_rank ? n0 * side.ldo + f : f * side.ldo + n0);
-    const int64_t step = side.by_rank ? side.ldo : 1;
-    if (!side.by_rank && a.d_type == MMA_F32 && !a.accumulate && many == 4 &&
-        (reinterpret_cast<uintptr_t>(static_cast<float*>(side.out) + o) & 15) == 0) {
-      *reinterpret_cast<float4*>(static_cast<float*>(side.out) + o) =
-          make_float4(v[0], v[1], v[2], v[3]);
-      continue;
-    }
+    for (int x = 0; x < kSums; ++x) w[x] = x < many ? p[x * features] : 0.f;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      if (x >= many) continue;
-      const float old = a.accumulate ? load_out(side.out, o + x * step, a.d_type) : 0.f;
-      store_out(side.out, o + x * step, a.d_type, v[x] + old);
-    }
+    for (int x = 0; x < kSums; ++x) v[x] += w[x];
   }
+  const int64_t o = int64_t(blockIdx.y) * side.slice +
+                    (side.by_rank ? n0 * side.ldo + f : f * side.ldo + n0);
+  const int64_t step = side.by_rank ? side.ldo : 1;
+  if (a.accumulate) {
+#pragma unroll
+    for (int x = 0; x < kSums; ++x)
+      if (x < many) v[x] += load_out(side.out, o + x * step, a.d_type);
+  }
+  const int eb = a.d_type == MMA_F32 ? 4 : 2;
+  uint8_t* const d = static_cast<uint8_t*>(side.out) + o * eb;
+  if (!side.by_rank && many == kSums && (reinterpret_cast<uintptr_t>(d) & 15) == 0) {
+    // a row's eight numbers
+    if (a.d_type == MMA_F32) {
+      reinterpret_cast<float4*>(d)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(d)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      uint16_t h[8];
+#pragma unroll
+      for (int x = 0; x < kSums; ++x) store_out(h, x, a.d_type, v[x]);
+      *reinterpret_cast<uint4*>(d) = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16,
+                                                h[4] | h[5] << 16, h[6] | h[7] << 16);
+    }
+    return;
+  }
+#pragma unroll
+  for (int x = 0; x < kSums; ++x)
+    if (x < many) store_out(side.out, o + x * step, a.d_type, v[x]);
 }
 
-// Rows per block: some four pieces of work per SM (of 152, so that the workspace
-// needs no device), 256 rows at least, in whole stages.
-int rows_per_piece(int64_t T, int64_t N, int64_t K) {
+// Rows per block, in whole stages: some three shares per SM (of 152, so that the
+// workspace needs no device), but 16 for each of the rank's sums and 256 at least, so
+// that the shares' FP32 sums are a fraction of the rows they are made of.
+int rows_per_piece(int64_t T, int64_t N, int64_t K, int64_t rank) {
   const int64_t tiles = (N + kTile - 1) / kTile + (K + kTile - 1) / kTile;
-  const int64_t per = T * tiles / (4 * 152);
-  return int(std::min<int64_t>(std::max<int64_t>((per + 63) / 64 * 64, 256), 1 << 20));
+  const int64_t per = std::max<int64_t>(T * tiles / (3 * 152), std::max<int64_t>(16 * rank, 256));
+  return int(std::min<int64_t>((per + 63) / 64 * 64, 1 << 20));
 }
 
 template <class K, class... Args>
@@ -801,20 +888,19 @@ cudaError_t launch_after(const Ctx& ctx, K kernel, dim3 grid, int threads, int s
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <bool BF16, int RP>
+template <bool BF16, int RP, int PARTS>
 mma_status_t wgrad(const Ctx& ctx, const LoraWgradProblem& g, const WgradArgs& a) {
   using L = Wgrad<RP>;
-  auto kernel = lora_wgrad_kernel<BF16, RP>;
+  auto kernel = lora_wgrad_kernel<BF16, RP, PARTS>;
   static PerContext<bool> attr;
   bool ok = false;
   if (!attr.get(ctx, &ok, [&](bool* v) {
         *v = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  L::SMEM) == cudaSuccess;
+                                  L::smem(PARTS)) == cudaSuccess;
         if (!*v) cudaGetLastError();
         return *v;
       }))
     return MMA_ERR_LAUNCH;
-  static_assert(RP * (kTile + 4) * 4 <= L::SMEM - 1024, "the sums' transposition");
   cudaError_t e = cudaSuccess;
   if (a.T > 0) {
     WgradMaps maps;
@@ -829,20 +915,23 @@ mma_status_t wgrad(const Ctx& ctx, const LoraWgradProblem& g, const WgradArgs& a
                     a.parts > 1 ? all : a.ld16, L::RB, kStageRows, swizzle_of(L::RB * 2)))
         return MMA_ERR_LAUNCH;
     }
-    const int64_t blocks = std::min<int64_t>((all + kThreads - 1) / kThreads, ctx.num_sms * 4);
+    const int64_t blocks = std::min<int64_t>((all + kThreads - 1) / kThreads, ctx.num_sms * 8);
     lora_halves_kernel<BF16><<<dim3(unsigned(blocks), 2), kThreads, 0, ctx.stream>>>(a);
     const int64_t pieces = (g.rows + a.per - 1) / a.per + g.requests + 1;
     const int64_t tiles = a.tiles0 + (g.K + kTile - 1) / kTile;
+    if (pieces * tiles > INT32_MAX / 2) return MMA_ERR_UNSUPPORTED;
+    const int64_t at_once = int64_t(ctx.num_sms) * L::per_sm(PARTS);
     ctx.mark_start();
-    e = launch_after(ctx, kernel, dim3(unsigned(pieces), unsigned(tiles)), kThreads + 32, L::SMEM,
-                     maps, a);
+    e = launch_after(ctx, kernel, dim3(unsigned(std::min(pieces * tiles, at_once))),
+                     kThreads + 32, L::smem(PARTS), maps, a, int(pieces), int(tiles));
     ctx.mark_stop();
   }
-  const int64_t features = int64_t(a.side[0].F) + a.side[1].F;
+  const int64_t sums = (g.N + kThreads - 1) / kThreads + (g.K + kThreads - 1) / kThreads;
   if (e == cudaSuccess)
-    lora_wgrad_sum_kernel<<<dim3(unsigned((features + kThreads - 1) / kThreads),
-                                 unsigned(a.total), unsigned(std::min((a.rank + 3) / 4, 4))),
-                            kThreads, 0, ctx.stream>>>(a);
+    e = launch_after(ctx, lora_wgrad_sum_kernel,
+                     dim3(unsigned(sums), unsigned(a.total),
+                          unsigned((a.rank + kSums - 1) / kSums)),
+                     kThreads, 0, a);
   const cudaError_t after = cudaGetLastError();
   return e == cudaSuccess && after == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
 }
@@ -870,7 +959,7 @@ mma_status_t launch_lora_shrink(const Ctx& ctx, const LoraProblem& g, const Lora
 int64_t lora_wgrad_workspace_bytes(bool bf16, int d_type, int64_t T, int64_t N, int64_t K,
                                    int64_t rank, int64_t requests) {
   if (T == 0) return 0;
-  const int64_t per = rows_per_piece(T, N, K);
+  const int64_t per = rows_per_piece(T, N, K, rank);
   const int64_t part = ((T + per - 1) / per + requests + 1) * rank * (N + K) * 4;
   return (part + 15) / 16 * 16 + 2 * lora_parts(bf16, d_type) * T * ((rank + 7) / 8 * 8) * 2;
 }
@@ -884,11 +973,11 @@ mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& g, void* 
   a.rank = int(g.rank);
   a.requests = int(g.requests);
   a.total = int(g.adapters_total);
-  a.per = rows_per_piece(g.rows, g.N, g.K);
+  a.per = rows_per_piece(g.rows, g.N, g.K, g.rank);
   a.offsets = g.offsets;
   a.adapters = g.adapters;
   a.d_type = g.d_type;
-  a.parts = lora_parts(g.bf16, g.d_type);
+  a.parts = lora_parts(g.bf16, g.d_type);  // (1, or 3 of BF16 and 2 of FP16)
   a.ld16 = (a.rank + 7) / 8 * 8;
   a.accumulate = g.accumulate;
   const int64_t pieces = (g.rows + a.per - 1) / a.per + g.requests + 1;
@@ -898,7 +987,9 @@ mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& g, void* 
   a.status = ctx.status;
   return by_rank(g.rank, [&](auto r) {
     constexpr int RP = decltype(r)::value;
-    return g.bf16 ? wgrad<true, RP>(ctx, g, a) : wgrad<false, RP>(ctx, g, a);
+    const bool one = a.parts == 1;
+    if (g.bf16) return one ? wgrad<true, RP, 1>(ctx, g, a) : wgrad<true, RP, 3>(ctx, g, a);
+    return one ? wgrad<false, RP, 1>(ctx, g, a) : wgrad<false, RP, 2>(ctx, g, a);
   });
 }
 
