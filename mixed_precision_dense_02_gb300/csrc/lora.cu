@@ -609,10 +609,19 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+template <bool FIRST, class T>
+__device__ __forceinline__ T& select(T& a, T& b) {
+  if constexpr (FIRST) return a;
+  return b;
+}
+
 // A piece's share of 128 features: G[f][n] = sum over its rows M[t][f] * low[t][n] on
 // the tensor cores, FP32.  As many CTAs as run at once take the shares in turn, the
 // features of a piece side by side, through one ring of rows and sums that runs on from
 // share to share (a CTA for each share: 51 us of 8192 x (8192 + 4096), rank 16, so 41).
+// The tensor cores' FP32 sums drop low bits on the way, so that for an FP32 gradient
+// (PARTS > 1) they run over a stage's 64 rows and are added to others to nearest (8192
+// rows: 3.9e-6 off without, so 4e-7).
 // What stands in a share's last stage behind the piece is another request's and becomes
 // zeros in both (in one alone, an infinity in the other would leave NaN).
 template <bool BF16, int RP, int PARTS>
@@ -735,6 +744,14 @@ __global__ void __launch_bounds__(kThreads + 32)
       if (!ok) break;
       const uint32_t ms = smem_u32(stage) + f_at;
       const uint32_t ls = smem_u32(stage) + L::M_BYTES;
+      float part_acc[RP / 8][4];
+      if constexpr (PARTS > 1) {
+#pragma unroll
+        for (int n = 0; n < RP / 8; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) part_acc[n][j] = 0.f;
+      }
+      auto& sum = select<(PARTS > 1)>(part_acc, acc);
 #pragma unroll
       for (int k = 0; k < kStageRows; k += 16) {
         uint32_t f[4];
@@ -746,9 +763,15 @@ __global__ void __launch_bounds__(kThreads + 32)
             uint32_t b[4];
             ldmatrix_x4_trans(b, ls + part * L::PART + n * 16 / RB * kStageRows * RB * 2 +
                                      k * RB * 2 + low_at[n * 16 % RB / 16]);
-            mma16<BF16>(acc[2 * n], f, b[0], b[1]);
-            mma16<BF16>(acc[2 * n + 1], f, b[2], b[3]);
+            mma16<BF16>(sum[2 * n], f, b[0], b[1]);
+            mma16<BF16>(sum[2 * n + 1], f, b[2], b[3]);
           }
+      }
+      if constexpr (PARTS > 1) {
+#pragma unroll
+        for (int n = 0; n < RP / 8; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[n][j] += part_acc[n][j];
       }
       __syncwarp();
       mbar_arrive_if(&ring.empty[s], lane == 0);
