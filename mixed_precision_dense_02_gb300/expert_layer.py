@@ -7,8 +7,8 @@ experts (two matrices with a gate between them), and what they return is
 added up with the router's weights.  ``serve`` runs it on 8-bit operands:
 norm with 8-bit output, grouped 8-bit products, quantiser in between.
 ``Trainer.step`` runs a step of training on 16-bit operands: grouped
-products, their gradients for the inputs and the weights, and the norm's
-gradient.  The command runs both on the GPU and prints how far they are from
+products, their gradients for the inputs and the weights, the norm's
+gradient and, where asked for, the router's, with its balance loss.  The command runs both on the GPU and prints how far they are from
 the same formulas in 32 bits.
 """
 from __future__ import annotations
@@ -27,13 +27,12 @@ def route(logits, k):
     ``weight`` are the sorted choices' tokens and router weights; expert e has
     the rows ``offsets[e]`` to ``offsets[e + 1]`` of them.
     """
-    weight, expert = torch.topk(torch.softmax(logits.float(), -1), k)
-    weight = weight / weight.sum(-1, keepdim=True)
-    order = torch.argsort(expert.reshape(-1), stable=True)
-    counts = torch.bincount(expert.reshape(-1), minlength=logits.shape[-1])
-    offsets = torch.zeros(counts.numel() + 1, dtype=torch.int32, device=logits.device)
-    offsets[1:] = counts.cumsum(0)
-    return order, order // k, weight.reshape(-1)[order], offsets
+    return _sorted(mma.route(logits, k), k)
+
+
+def _sorted(r, k):
+    order = r.order.long()
+    return order, order // k, r.weights.reshape(-1)[order], r.offsets
 
 
 def gate(h):
@@ -88,13 +87,18 @@ class Trainer:
     def __init__(self, w):
         self.w = w
 
-    def step(self, x, residual, d_out, rate, k=2):
+    def step(self, x, residual, d_out, rate, k=2, balance=None):
         """One step of gradient descent for a loss whose gradient by the
         output is ``d_out``.  Returns (output, gradients): the gradients of
-        x (and of the residual), the norm's weights, up and down."""
+        x (and of the residual), the norm's weights, up and down.  With
+        ``balance`` the router is trained too: by its weights, and by
+        ``balance`` times its balance loss (gradients: "router" as well).
+        """
         w = self.w
         _, _, h, y = mma.rmsnorm_f8(x, w.norm, residual, eps=EPS, y=True)
-        order, token, weight, offsets = route(mma.gemm(y, w.router), k)
+        logits = mma.gemm(y, w.router)
+        routing = mma.route(logits, k)
+        order, token, weight, offsets = _sorted(routing, k)
         rows = y[token]
         a = mma.gemm_grouped(rows, w.up, offsets)
         with torch.enable_grad():
@@ -102,7 +106,8 @@ class Trainer:
             m = gate(leaf)
         b = mma.gemm_grouped(m.detach(), w.down, offsets, out_dtype=torch.float32)
         out = torch.zeros_like(x, dtype=torch.float32).index_add_(0, token, b * weight[:, None])
-        # backward (the router's choice is taken as given)
+        # backward (the router's choice is taken as given, and its weights too
+        # unless it is trained)
         db = (d_out[token].float() * weight[:, None]).to(x.dtype)
         d_down = mma.gemm_grouped_wgrad(db, m.detach(), offsets)
         dm = mma.gemm_grouped(db, w.down, offsets, b_layout="row")
@@ -111,11 +116,29 @@ class Trainer:
         d_up = mma.gemm_grouped_wgrad(da, rows, offsets)
         d_rows = mma.gemm_grouped(da, w.up, offsets, b_layout="row", out_dtype=torch.float32)
         dy = torch.zeros_like(x, dtype=torch.float32).index_add_(0, token, d_rows)
+        d_router = None
+        if balance is not None:
+            place = routing.place.long()
+            d_weight = (b[place] * d_out[:, None].float()).sum(-1)
+            d_loss = torch.full((), balance, dtype=torch.float32, device=x.device)
+            # (rows that start on 16-byte boundaries, as the products read them)
+            experts = logits.shape[1]
+            d_logits = torch.zeros(x.shape[0], -(-experts // 8) * 8, dtype=x.dtype,
+                                   device=x.device)[:, :experts]
+            d_logits.copy_(mma.route_backward(logits, routing, d_weight, d_loss))
+            whole = torch.tensor([0, x.shape[0]], dtype=torch.int32, device=x.device)
+            d_router = mma.gemm_grouped_wgrad(d_logits, y, whole)[0]
+            dy += mma.gemm_grouped(d_logits, w.router[None], whole, b_layout="row",
+                                   out_dtype=torch.float32)
         dx, d_norm = mma.rmsnorm_backward(dy.to(x.dtype), h, w.norm, eps=EPS)
         w.up = (w.up.float() - rate * d_up).bfloat16()
         w.down = (w.down.float() - rate * d_down).bfloat16()
         w.norm = (w.norm.float() - rate * d_norm).bfloat16()
-        return out, {"x": dx, "norm": d_norm, "up": d_up, "down": d_down}
+        grads = {"x": dx, "norm": d_norm, "up": d_up, "down": d_down}
+        if d_router is not None:
+            w.router = (w.router.float() - rate * d_router).bfloat16()
+            grads["router"] = d_router
+        return out, grads
 
 
 def reference(x, residual, w, k=2, norm=None, up=None, down=None):
