@@ -1128,7 +1128,7 @@ struct LoraSpace {
 LoraSpace lora_space(int type_in, int type_d, int64_t T, int64_t N, int64_t rank,
                      int64_t requests) {
   const bool every = T <= kLoraEveryRow;
-  const int64_t rows = every ? T : requests * (kLoraRows - 1);
+  const int64_t rows = lora_own_places(T, requests) ? T : requests * (kLoraRows - 1);
   const int64_t parts = every ? 0 : lora_parts(type_in == MMA_BF16, type_d);
   return LoraSpace{(rows * N * 4 + 15) / 16 * 16, parts * T * round8(rank) * 2};
 }

@@ -144,7 +144,7 @@ struct GroupedArgs {
   // Request i's rows have the adapter adapters[i] (NULL: i; outside [0,
   // adapters_total): none), whose `rank` sums per row are, in `parts` parts of 16
   // bits, behind tmD, and whose second matrix is behind tmZ.rows[0]; `extra` has
-  // rows for the requests of fewer than kLoraRows rows, kLoraRows - 1 for each.
+  // those of requests of fewer than kLoraRows rows (places: lora_own_places).
   const float* extra;
   const int* adapters;
   int adapters_total, rank, parts;
@@ -1054,7 +1054,9 @@ __global__ void __launch_bounds__(kThreads,
                 if (grow[mid] <= q) lo = mid; else hi = mid;
               }
               if (q >= grow[lo] && q < grow[lo + 1] && gunit[lo] >= 0 && !as_product(lo))
-                slot[b] = lo * (kLoraRows - 1) + q - grow[lo];
+                slot[b] = lora_own_places(a.rows_total, a.groups)
+                              ? q
+                              : lo * (kLoraRows - 1) + q - grow[lo];
             }
             some = some || slot[b] >= 0;
           }

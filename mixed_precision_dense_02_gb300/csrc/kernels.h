@@ -261,8 +261,12 @@ struct LoraProblem {
 // of 8, so that eight can be read from any eighth one) and, for more rows than
 // kLoraEveryRow, as `parts` matrices of 16 bits whose sum they are.  In `extra` what
 // the adapters add, FP32 rows of N: with up to kLoraEveryRow rows for all of them,
-// else for the requests of fewer than kLoraRows rows, kLoraRows - 1 for each request.
+// else for those of requests of fewer than kLoraRows rows, at the row's own place or
+// (where that takes fewer) in kLoraRows - 1 places for each request.
 constexpr int kLoraEveryRow = 128, kLoraRows = 8;
+constexpr bool lora_own_places(int64_t rows, int64_t requests) {
+  return rows <= kLoraEveryRow || rows <= requests * (kLoraRows - 1);
+}
 // Numbers of 16 bits that stand for an FP32 sum in a product: for an FP32 result as
 // many as hold its 24 bits (BF16 three of 8, FP16 two of 11, which leave 2^-22 of
 // it), for a 16-bit one, whose own rounding is as large, one.

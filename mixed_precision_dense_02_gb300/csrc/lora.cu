@@ -346,7 +346,9 @@ __global__ void __launch_bounds__(Shrink<BM, RP, EVERY>::THREADS, Shrink<BM, RP,
   auto extra_row = [&](int row) {
     const int64_t t = piece.from + row;
     return low.extra +
-           (EVERY ? t : int64_t(piece.request - 1) * (kLoraRows - 1) + t - first_of) * N;
+           (lora_own_places(g.rows, requests)
+                ? t
+                : int64_t(piece.request - 1) * (kLoraRows - 1) + t - first_of) * N;
   };
   auto put = [&](int row, int n, float v) {
     const int64_t t = piece.from + row;

@@ -229,6 +229,24 @@ def test_no_rows_and_in_place_and_streams():
     assert torch.equal(out, mma.layernorm(keep, w, None, r)[0])
 
 
+@pytest.mark.parametrize("m", [5, 700])
+def test_gradient_in_place(m):
+    """The ABI's DX over DY, and over the residual's gradient."""
+    n = 264
+    h, w = rows16(rnd(1, m, n), torch.float32), torch.ones(n, device="cuda")
+    dy, r = rows16(rnd(2, m, n), torch.float32), rows16(rnd(3, m, n), torch.float32)
+    want = mma.layernorm_backward(dy, h, w, r)
+    need = binding.load().mma_layernorm_backward_workspace(m, n)
+    for over in range(2):
+        d, g = dy.clone(), r.clone()
+        dx = (d, g)[over]
+        dw, db, ws = torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty(need, dtype=torch.uint8, device="cuda")
+        st = binding.load().mma_layernorm_backward(5, 5, m, n, d.data_ptr(), n, h.data_ptr(), n, w.data_ptr(), 1e-5, g.data_ptr(), n,
+                                                   dx.data_ptr(), n, dw.data_ptr(), db.data_ptr(), ws.data_ptr(), need,
+                                                   torch.cuda.current_stream().cuda_stream)
+        assert st == 0 and torch.equal(dx, want[0]) and torch.equal(dw, want[1]) and torch.equal(db, want[2])
+
+
 def test_captured_and_replayed():
     x, dy = rows16(rnd(11, 500, 1024), torch.bfloat16), rows16(rnd(12, 500, 1024), torch.bfloat16)
     w = torch.ones(1024, device="cuda", dtype=torch.bfloat16)

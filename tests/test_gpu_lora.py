@@ -296,6 +296,30 @@ def test_gradient_against_differences():
             assert abs(slope - float((host(g) * host(step)).sum())) <= 2.0 ** -12 * scale
 
 
+def test_bad_numbers_stay_with_their_adapters_gradient():
+    """Rows of one request with NaN and infinities, next to others inside a block."""
+    lengths = [100, 30, 70, 300, 5]
+    c = Case(lengths, 136, 200, 24, [0, 1, 2, 3, 4], 5, "bf16", seed=21)
+    dy = rows16(rnd(5, c.t, 136), T["bf16"])
+    s, u = rnd(6, c.t, 24).float().cuda(), rnd(7, c.t, 24).float().cuda()
+    want = mma.gemm_lora_wgrad(dy, c.x, s, u, c.offsets, c.adapters, adapters_total=5)
+    for t, v in ((dy, float("nan")), (c.x, float("inf")), (s, float("inf")), (u, float("nan"))):
+        t[c.at[1]:c.at[2]] = v
+    got = mma.gemm_lora_wgrad(dy, c.x, s, u, c.offsets, c.adapters, adapters_total=5)
+    keep = torch.tensor([0, 2, 3, 4], device="cuda")
+    for a, b in zip(got, want):
+        assert torch.equal(a[keep], b[keep]) and not bool(a[1].isfinite().all())
+
+
+def test_many_small_requests_among_many_rows():
+    """More rows than are added one by one, in fewer places than requests have."""
+    for lengths in ([1, 2, 3] * 60, [1] * 129, [7, 8] * 20 + [1] * 100):
+        total = 6
+        adapters = [i % (total + 1) - 1 for i in range(len(lengths))]
+        for row in (False, True):
+            Case(lengths, 200, 136, 20, adapters, total, "f16", row, gap=(3, 2), seed=len(lengths)).check("f32")
+
+
 def test_streams_and_graphs():
     cases = [Case([1] * 20, 512, 512, 16, [i % 5 for i in range(20)], 5, seed=1), Case([400, 1, 90], 512, 512, 32, [2, 0, 1], 3, seed=2)]
     alone = [c.run("bf16") for c in cases]
