@@ -504,8 +504,8 @@ mma_status_t mma_layernorm(int type, int w_type, int64_t M, int64_t N,
  *     DW[j] = sum over rows of dy * c / std,   DB[j] = sum over rows of dy
  *
  * DW and DB in FP32, summed in a fixed order through `workspace` of at least
- * mma_layernorm_backward_workspace(M, N) bytes (at most 912 * N * 4, and 2432 * N
- * * 4 with N <= 2048).  All else as in mma_rmsnorm_backward.
+ * mma_layernorm_backward_workspace(M, N) bytes (at most 912 * N * 4, with N <= 2048
+ * 2432 * N * 4, with N > 8192 16 * M more).  All else as in mma_rmsnorm_backward.
  */
 int64_t mma_layernorm_backward_workspace(int64_t M, int64_t N);
 mma_status_t mma_layernorm_backward(int type, int w_type, int64_t M, int64_t N,

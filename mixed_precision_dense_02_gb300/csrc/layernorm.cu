@@ -250,12 +250,17 @@ __global__ void __launch_bounds__(512, 1)
   }
 }
 
-// Rows too wide for that: one row per block, read three times.
+constexpr int64_t kRowBytes = 212 * 1024;  // shared memory for one row
+
+// Rows too wide for that: one row per block, which a block keeps in shared memory (h in
+// FP32; 2048 x 32768 BF16 with residual 211 us, 224 without) or, `cached` false, reads
+// three times.  A thread reads what it has written.
 template <class T>
 __global__ void __launch_bounds__(1024)
-    layernorm_wide_kernel(const NormProblem p, bool w32) {
+    layernorm_wide_kernel(const NormProblem p, bool w32, bool cached) {
   constexpr int E = Vec<T>::kN;
   constexpr int kLanes = kScaleBlock / E;
+  extern __shared__ __align__(16) float kept[];
   __shared__ float2 red[2][32];
   const int64_t row = blockIdx.x, n = p.N;
   const T* x = static_cast<const T*>(p.X) + row * p.ldx;
@@ -270,17 +275,29 @@ __global__ void __launch_bounds__(1024)
       for (int j = 0; j < E; ++j) h[j] += t[j];
     }
   };
+  auto again = [&](int64_t v) {
+    if (!cached) return load(v);
+#pragma unroll
+    for (int j = 0; j < E; j += 4)
+      *reinterpret_cast<float4*>(h + j) = *reinterpret_cast<const float4*>(kept + v * E + j);
+  };
   const int64_t vectors = (n + E - 1) / E;
   float s = 0.f;
+#pragma unroll 2
   for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
     load(v);
+    if (cached) {
+#pragma unroll
+      for (int j = 0; j < E; j += 4)
+        *reinterpret_cast<float4*>(kept + v * E + j) = *reinterpret_cast<const float4*>(h + j);
+    }
 #pragma unroll
     for (int j = 0; j < E; ++j) s += h[j];
   }
   const float mean = block_sum2(s, 0.f, red[0]).x / float(n);
   s = 0.f;
   for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
-    load(v);
+    again(v);
 #pragma unroll
     for (int j = 0; j < E; ++j) {
       const float c = v * E + j < n ? h[j] - mean : 0.f;
@@ -290,8 +307,8 @@ __global__ void __launch_bounds__(1024)
   const float rstd = over_std(block_sum2(s, 0.f, red[1]).x / float(n), p.eps);
   // whole warps take part in the block maxima: round up to the block
   for (int64_t v = threadIdx.x; v < (vectors + 31) / 32 * 32; v += blockDim.x) {
-    load(v);
     const bool live = v < vectors;
+    if (live) again(v);
     if (p.H && live) store_row(static_cast<T*>(p.H) + row * p.ldh, v, n, h);
     float y[E], b[E];
     load_weight<T>(p.W, w32, v, n, y);
@@ -510,25 +527,43 @@ __global__ void __launch_bounds__(MAXT, MINB)
   }
 }
 
-// Rows too wide for that: read three times, dw and db added up in `part`.
+// Rows too wide for that, in two kernels.  First what dx and dw take from a whole row:
+// its mean, 1 / std, mean(g) and -mean(g' c) / std^3.  A block keeps the row (h and dy)
+// in shared memory or, `cached` false, reads it twice.  (2048 x 32768 BF16: 233 us for
+// both; a block per row that adds to its share of dw and db in memory took 708.)
 template <class T>
 __global__ void __launch_bounds__(1024)
-    layernorm_backward_wide_kernel(const NormBackProblem p, bool w32,
-                                   float* __restrict__ part) {
+    layernorm_stats_kernel(const NormBackProblem p, bool w32, bool cached,
+                           float* __restrict__ stats) {
   constexpr int E = Vec<T>::kN;
+  extern __shared__ __align__(16) uint4 kept_rows[];
   __shared__ float2 red[2][32];
   const int64_t n = p.N, vectors = (n + E - 1) / E;
-  float* mine = part + int64_t(blockIdx.x) * n * 2;
   float dy[E], h[E], w[E];
   for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
-    auto load = [&](int64_t v) {
-      load_row(static_cast<const T*>(p.H) + row * p.ldh, v, n, h);
-      load_row(static_cast<const T*>(p.DY) + row * p.lddy, v, n, dy);
+    auto load = [&](int64_t v, bool first) {
+      uint4 hv, dv;
+      if (first || !cached) {
+        hv = load_raw(static_cast<const T*>(p.H) + row * p.ldh, v, n);
+        dv = load_raw(static_cast<const T*>(p.DY) + row * p.lddy, v, n);
+      } else {
+        hv = kept_rows[v];
+        dv = kept_rows[vectors + v];
+      }
+      if (first && cached) {  // (read again by this thread alone)
+        kept_rows[v] = hv;
+        kept_rows[vectors + v] = dv;
+      }
+      Vec<T>::unpack(hv, h);
+      Vec<T>::unpack(dv, dy);
+      clear_tail<T>(v, n, h);
+      clear_tail<T>(v, n, dy);
       load_weight<T>(p.W, w32, v, n, w);
     };
     float a = 0.f, b = 0.f;
+#pragma unroll 2
     for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
-      load(v);
+      load(v, true);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         a += h[j];
@@ -538,8 +573,9 @@ __global__ void __launch_bounds__(1024)
     float2 s = block_sum2(a, b, red[0]);
     const float mean = s.x / float(n), mean_g = s.y / float(n);
     a = b = 0.f;
+#pragma unroll 2
     for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
-      load(v);
+      load(v, false);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const float c = v * E + j < n ? h[j] - mean : 0.f;
@@ -548,26 +584,71 @@ __global__ void __launch_bounds__(1024)
       }
     }
     s = block_sum2(a, b, red[1]);
-    const float rstd = over_std(s.x / float(n), p.eps);
-    const float f = -(s.y / float(n)) * rstd * rstd * rstd;
-    for (int64_t v = threadIdx.x; v < vectors; v += blockDim.x) {
-      load(v);
-      float o[E], r[E];
-      if (p.R) load_row(static_cast<const T*>(p.R) + row * p.ldr, v, n, r);
+    if (threadIdx.x == 0) {
+      const float rstd = over_std(s.x / float(n), p.eps);
+      stats[4 * row] = mean;
+      stats[4 * row + 1] = rstd;
+      stats[4 * row + 2] = mean_g;
+      stats[4 * row + 3] = -(s.y / float(n)) * rstd * rstd * rstd;
+    }
+  }
+}
+
+// Then dx and shares of dw and db: a vector of columns per thread, rows [b * per, ...)
+// for row b of part, four on their way at a time.  dx is stored where dy or r was read.
+template <class T>
+__global__ void __launch_bounds__(128)
+    layernorm_columns_kernel(const NormBackProblem p, bool w32,
+                             const float* __restrict__ stats, int64_t per,
+                             float* __restrict__ part) {
+  constexpr int E = Vec<T>::kN;
+  constexpr int U = 4;
+  const int64_t v = int64_t(blockIdx.x) * blockDim.x + threadIdx.x, n = p.N;
+  const int64_t from = blockIdx.y * per, to = min(from + per, p.M);
+  if (v * E >= n) return;
+  float w[E], dw[E], db[E];
+  load_weight<T>(p.W, w32, v, n, w);
+#pragma unroll
+  for (int j = 0; j < E; ++j) dw[j] = db[j] = 0.f;
+  for (int64_t base = from; base < to; base += U) {
+    uint4 hv[U], dv[U], rv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = base + u;
+      if (row >= to) break;
+      hv[u] = load_raw(static_cast<const T*>(p.H) + row * p.ldh, v, n);
+      dv[u] = load_raw(static_cast<const T*>(p.DY) + row * p.lddy, v, n);
+      if (p.R) rv[u] = load_raw(static_cast<const T*>(p.R) + row * p.ldr, v, n);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = base + u;
+      if (row >= to) break;
+      float h[E], dy[E], r[E];
+      Vec<T>::unpack(hv[u], h);
+      Vec<T>::unpack(dv[u], dy);
+#pragma unroll
+      for (int j = 0; j < E; ++j) r[j] = 0.f;
+      if (p.R) Vec<T>::unpack(rv[u], r);
+      const float mean = stats[4 * row], rstd = stats[4 * row + 1];
+      const float mean_g = stats[4 * row + 2], f = stats[4 * row + 3];
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         const float c = h[j] - mean;
-        o[j] = fmaf(fmaf(dy[j], w[j], -mean_g), rstd, f * c) + (p.R ? r[j] : 0.f);
-        const int64_t at = v * E + j;
-        if (at < n) {
-          const bool first = row == blockIdx.x;
-          mine[at] = fmaf(dy[j] * rstd, c, first ? 0.f : mine[at]);
-          mine[n + at] = dy[j] + (first ? 0.f : mine[n + at]);
-        }
+        dw[j] = fmaf(dy[j] * rstd, c, dw[j]);
+        db[j] += dy[j];
+        r[j] += fmaf(fmaf(dy[j], w[j], -mean_g), rstd, f * c);
       }
-      store_row(static_cast<T*>(p.DX) + row * p.lddx, v, n, o);
+      store_row(static_cast<T*>(p.DX) + row * p.lddx, v, n, r);
     }
   }
+  float* const mine = part + blockIdx.y * 2 * n;
+#pragma unroll
+  for (int j = 0; j < E; ++j)
+    if (v * E + j < n) {
+      mine[v * E + j] = dw[j];
+      mine[n + v * E + j] = db[j];
+    }
 }
 
 // Launches a kernel with a ring in up to 220 KB of shared memory.
@@ -617,7 +698,11 @@ mma_status_t forward(const Ctx& ctx, const NormProblem& p, bool w32) {
       else run(layernorm_kernel<T, 4, false>, a4);
     }
   } else {
-    layernorm_wide_kernel<T><<<unsigned(p.M), 1024, 0, ctx.stream>>>(p, w32);
+    static PerContext<bool> wide;
+    const int64_t row = vectors * E * 4;
+    const bool cached = row <= kRowBytes;
+    ok = launch_ring(ctx, wide, layernorm_wide_kernel<T>, p.M, 1024, cached ? row : 0, p, w32,
+                     cached);
   }
   return cudaGetLastError() == cudaSuccess && ok ? MMA_OK : MMA_ERR_LAUNCH;
 }
@@ -628,8 +713,8 @@ mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32, float*
   const int64_t vectors = (p.N + E - 1) / E;
   const int tensors = p.R ? 3 : 2;
   const NormRingShape shape = layernorm_back_shape(vectors, tensors);
-  const int64_t at_once = int64_t(shape.vpt ? shape.per_sm : 3) * ctx.num_sms;
-  const int64_t grid = std::min(p.M, std::min(layernorm_most_parts(p.N), at_once));
+  const int64_t most = std::min(p.M, layernorm_most_parts(p.N));
+  int64_t grid = std::min(most, int64_t(shape.per_sm) * ctx.num_sms);  // rows of part
   bool ok = true;
   if (grid > 0 && shape.vpt) {
     auto run = [&](auto kernel, PerContext<bool>& attr) {
@@ -647,17 +732,32 @@ mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32, float*
       else if (shape.vpt == 2) run(layernorm_backward_kernel<T, 2, 384, 2, false>, a2);
       else run(layernorm_backward_kernel<T, 4, 512, 1, false>, a4);
     }
-  } else if (grid > 0) {
-    layernorm_backward_wide_kernel<T><<<unsigned(grid), 1024, 0, ctx.stream>>>(p, w32, part);
+  } else if (p.M > 0) {
+    static PerContext<bool> wide;
+    float* const stats = part + most * 2 * p.N;
+    const bool cached = vectors * 32 <= kRowBytes;
+    ok = launch_ring(ctx, wide, layernorm_stats_kernel<T>,
+                     std::min<int64_t>(p.M, ctx.num_sms * (cached ? 1 : 2)), 1024,
+                     cached ? vectors * 32 : 0, p, w32, cached, stats);
+    // as many blocks of rows as give every SM some sixteen of columns
+    const int64_t columns = (vectors + 127) / 128;
+    const int64_t want = std::max<int64_t>(1, 16 * ctx.num_sms / columns);
+    const int64_t per = (p.M + std::min(most, want) - 1) / std::min(most, want);
+    grid = (p.M + per - 1) / per;
+    layernorm_columns_kernel<T>
+        <<<dim3(unsigned(columns), unsigned(grid)), 128, 0, ctx.stream>>>(p, w32, stats, per,
+                                                                          part);
   }
-  if (!ok) return MMA_ERR_LAUNCH;
+  if (!ok || cudaPeekAtLastError() != cudaSuccess) return MMA_ERR_LAUNCH;
   return sum_parts(ctx, part, int(grid), 2 * p.N, p.DW, p.N, p.DB);
 }
 
 }  // namespace
 
 int64_t layernorm_backward_workspace_bytes(int64_t M, int64_t N) {
-  return std::min(M, layernorm_most_parts(N)) * N * 8;
+  // (behind the shares four floats per row, where rows may be too wide for the ring)
+  return std::min(M, layernorm_most_parts(N)) * N * 8 +
+         (N > 4 * kNormBackMostVectors ? 16 * M : 0);
 }
 
 mma_status_t launch_layernorm(const Ctx& ctx, const NormProblem& p) {

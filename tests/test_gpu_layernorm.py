@@ -70,7 +70,8 @@ def want_y(h, w, b, eps):
 
 
 SHAPES = [(1, 1), (1, 7), (3, 8), (1, 4096), (5, 100), (200, 264), (160, 2048), (400, 2056), (7, 4100),
-          (300, 5000), (170, 8192), (33, 8190), (3, 16384), (155, 16384), (2, 16392), (3, 40000)]
+          (300, 5000), (170, 8192), (33, 8190), (3, 16384), (155, 16384), (2, 16392), (3, 40000), (400, 9001),
+          (300, 16400), (5, 60000)]
 
 
 @pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
@@ -229,10 +230,9 @@ def test_no_rows_and_in_place_and_streams():
     assert torch.equal(out, mma.layernorm(keep, w, None, r)[0])
 
 
-@pytest.mark.parametrize("m", [5, 700])
-def test_gradient_in_place(m):
+@pytest.mark.parametrize("m,n", [(5, 264), (700, 264), (9, 8200), (500, 9000)])
+def test_gradient_in_place(m, n):
     """The ABI's DX over DY, and over the residual's gradient."""
-    n = 264
     h, w = rows16(rnd(1, m, n), torch.float32), torch.ones(n, device="cuda")
     dy, r = rows16(rnd(2, m, n), torch.float32), rows16(rnd(3, m, n), torch.float32)
     want = mma.layernorm_backward(dy, h, w, r)

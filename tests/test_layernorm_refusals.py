@@ -63,7 +63,8 @@ def test_backward(kw, code):
 def test_workspace():
     f = binding.load().mma_layernorm_backward_workspace
     assert f(0, 4096) == 0 and f(4, 256) == 8 * 256 * 4
-    assert f(10 ** 6, 256) == 2432 * 256 * 4 and f(10 ** 6, 4096) == 912 * 4096 * 4 and f(-1, 5) == 0
+    assert f(10 ** 6, 256) == 2432 * 256 * 4 and f(10 ** 6, 4096) == 912 * 4096 * 4
+    assert f(10 ** 6, 16384) == 912 * 16384 * 4 + 16 * 10 ** 6 and f(-1, 5) == 0
 
 
 def test_binding():
