@@ -183,12 +183,12 @@ struct Layout {
   static constexpr int GROUP_OFFSET = BAR_OFFSET + NUM_BARS * 8 + 24;
   static constexpr int round16(int v) { return (v + 15) & ~15; }
   // SPLIT: sums of the other ranks, 128 rows of P times the columns in use
-  static constexpr int part_offset(int groups) {
-    return round16(GROUP_OFFSET + 2 * (groups + 1) * 4);
+  static constexpr int part_offset(int groups, int lists = 2) {
+    return round16(GROUP_OFFSET + lists * (groups + 1) * 4);
   }
-  static constexpr int alloc(int groups, int split, int part_cols) {
+  static constexpr int alloc(int groups, int split, int part_cols, int lists = 2) {
     // (1024: alignment of the base)
-    return part_offset(groups) + (split - 1) * part_cols * kP * 4 + 1024;
+    return part_offset(groups, lists) + (split - 1) * part_cols * kP * 4 + 1024;
   }
   static constexpr uint32_t TMEM_COLS = ACCS * BN;
 };
@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(kThreads,
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* grow = reinterpret_cast<int*>(smem + L::GROUP_OFFSET);  // groups + 1
   int* gunit = grow + a.groups + 1;                            // groups + 1
+  [[maybe_unused]] int* glist = gunit + a.groups + 1;          // (kRequests) groups + 1
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -370,8 +371,12 @@ __global__ void __launch_bounds__(kThreads,
   // role waits for before its first global access.
   if (warp == 0) {
     if constexpr (LORA == kRequests) {
-      // the requests' bounds and, in the place of the groups' units, adapters
-      int row = min(max(__ldg(a.offsets), 0), a.rows_total);
+      // the requests' bounds, in the place of the groups' units adapters (behind them
+      // whether there are small requests), and which are done as products (behind
+      // them their number).  Lone threads that went through all requests of a tile
+      // took 100 clocks for each: 2100 rows, 63 requests without adapters 57 us.
+      int row = min(max(__ldg(a.offsets), 0), a.rows_total), listed = 0;
+      bool small = false;
       if (lane == 0) grow[0] = row;
       for (int base = 0; base < a.groups; base += 32) {
         const int i = base + lane;
@@ -381,12 +386,26 @@ __global__ void __launch_bounds__(kThreads,
           if (lane >= d) hi = max(hi, o);
         }
         hi = max(hi, row);
+        int lo = __shfl_up_sync(0xffffffffu, hi, 1);
+        if (lane == 0) lo = row;
+        int who = -1;
         if (i < a.groups) {
-          const int who = a.adapters ? __ldg(a.adapters + i) : i;
+          who = a.adapters ? __ldg(a.adapters + i) : i;
+          if (who >= a.adapters_total) who = -1;
           grow[i + 1] = hi;
-          gunit[i] = who < a.adapters_total ? who : -1;
+          gunit[i] = who;
         }
+        const bool product = who >= 0 && hi - lo >= kLoraRows;
+        const unsigned all = __ballot_sync(0xffffffffu, product);
+        if (product) glist[listed + __popc(all & ((1u << lane) - 1u))] = i;
+        listed += __popc(all);
+        small = small || (who >= 0 && hi > lo && !product);
         row = __shfl_sync(0xffffffffu, hi, 31);
+      }
+      small = __any_sync(0xffffffffu, small);
+      if (lane == 0) {
+        gunit[a.groups] = small;
+        glist[a.groups] = listed;
       }
     } else if (!a.offsets) {
       if (lane == 0) {
@@ -503,20 +522,22 @@ __global__ void __launch_bounds__(kThreads,
     return t;
   };
 
-  // (kRequests) f(request, its first row, one past its last) for the requests with an
-  // adapter that have rows in the tile.
-  [[maybe_unused]] auto each_request = [&](const Tile& t, auto&& f) {
-    int lo = 0, hi = a.groups;  // the last request that starts by the tile's start
+  // (kRequests) f(request, its first row, one past its last) for the requests done as
+  // products that have rows in the tile.
+  [[maybe_unused]] auto each_product = [&](const Tile& t, auto&& f) {
+    const int n = glist[a.groups];
+    int lo = 0, hi = n;  // the last that starts by the tile's start
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (grow[mid] <= t.q0) lo = mid; else hi = mid;
+      if (grow[glist[mid]] <= t.q0) lo = mid; else hi = mid;
     }
-    for (int i = lo; i < a.groups && grow[i] < t.q1; ++i) {
+    for (; lo < n; ++lo) {
+      const int i = glist[lo];
       const int from = max(grow[i], t.q0), to = min(grow[i + 1], t.q1);
-      if (to > from && gunit[i] >= 0) f(i, from, to);
+      if (from >= t.q1) break;
+      if (to > from) f(i, from, to);
     }
   };
-  [[maybe_unused]] auto as_product = [&](int i) { return grow[i + 1] - grow[i] >= kLoraRows; };
   [[maybe_unused]] const int lora_blocks = LORA == kRequests ? (a.rank + 63) / 64 : 0;
 
   if (warp < 4) {
@@ -588,8 +609,7 @@ __global__ void __launch_bounds__(kThreads,
         }
         if constexpr (LORA == kRequests) {
           grid_dependency_wait();
-          each_request(t, [&](int i, int, int) {
-            if (!as_product(i)) return;
+          each_product(t, [&](int i, int, int) {
             for (int b = 0; b < lora_blocks * a.parts && ok; ++b) {
               if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.status)) {
                 ok = false;
@@ -748,8 +768,8 @@ __global__ void __launch_bounds__(kThreads,
           }
         }
         if constexpr (LORA == kRequests) {
-          each_request(t, [&](int i, int, int) {
-            if (!ok || !as_product(i)) return;
+          each_product(t, [&](int, int, int) {
+            if (!ok) return;
             ok = mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, a.status);
             if (!ok) return;
             tc_fence_after();
@@ -1026,8 +1046,7 @@ __global__ void __launch_bounds__(kThreads,
             for (int j = 0; j < CB; ++j) sum[i * CB + j] += __uint_as_float(r[j]);
           });
         if constexpr (LORA == kRequests) {
-          each_request(t, [&](int i, int from, int to) {
-            if (!as_product(i)) return;
+          each_product(t, [&](int, int from, int to) {
             // (what other rows' sums with this adapter are does not matter)
             take([&](int b, const uint32_t (&r)[CB]) {
               const int first = t.q0 + column(b) - from;
@@ -1040,24 +1059,32 @@ __global__ void __launch_bounds__(kThreads,
           // The rows of small requests: lane l has the place in `extra` of column l
           // of each block, or -1.  (One row after the other, each added to the sum
           // that a comparison picks, was 128 comparisons a row: 2100 rows, 60 of them
-          // small, 123 us, so 66.)
-          int slot[NB];
+          // small, 123 us where 83 were taken in all.)
+          int slot[NB], lo[NB];
           bool some = false;
+          if (gunit[a.groups]) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) lo[b] = 0;
+            // (the blocks' bisections side by side)
+            for (int step = 512; step > 0; step >>= 1) {
+              if (step >= a.groups) continue;
+#pragma unroll
+              for (int b = 0; b < NB; ++b) {
+                const int mid = lo[b] + step;
+                if (mid < a.groups && grow[mid] <= t.q0 + column(b) + lane) lo[b] = mid;
+              }
+            }
+          }
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            const int q = t.q0 + column(b) + lane;
             slot[b] = -1;
-            if (lane < CB && q < t.q1) {
-              int lo = 0, hi = a.groups;
-              while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (grow[mid] <= q) lo = mid; else hi = mid;
-              }
-              if (q >= grow[lo] && q < grow[lo + 1] && gunit[lo] >= 0 && !as_product(lo))
-                slot[b] = lora_own_places(a.rows_total, a.groups)
-                              ? q
-                              : lo * (kLoraRows - 1) + q - grow[lo];
-            }
+            if (!gunit[a.groups]) continue;
+            const int q = t.q0 + column(b) + lane, i = lo[b];
+            if (lane < CB && q < t.q1 && q >= grow[i] && q < grow[i + 1] && gunit[i] >= 0 &&
+                grow[i + 1] - grow[i] < kLoraRows)
+              slot[b] = lora_own_places(a.rows_total, a.groups)
+                            ? q
+                            : i * (kLoraRows - 1) + q - grow[i];
             some = some || slot[b] >= 0;
           }
           if (__any_sync(0xffffffffu, some)) {
@@ -1483,8 +1510,9 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
   }
   auto kern =
       gemm_grouped_kernel<KIND8, P_MN, Q_MN, RAGK, ROWS, SPLIT, CL, BN, STAGES, LORA>;
+  constexpr int kLists = LORA == kRequests ? 3 : 2;
   constexpr int kMostSplit = !SPLIT ? 1 : BN == 32 ? 6 : BN == 64 ? 4 : 2;
-  static_assert(L::alloc(kMaxGroups, kMostSplit, BN) <= 232448, "shared memory per CTA");
+  static_assert(L::alloc(kMaxGroups, kMostSplit, BN, kLists) <= 232448, "shared memory per CTA");
   // SPLIT: as many CTAs per tile as leave every tile's cluster room at once
   // (two CTAs per SM if their shared memory fits twice), each with four k
   // blocks at least.  One row, 8192 x 4096: 64 tiles, 14.7 us without.
@@ -1503,7 +1531,7 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
   // One CTA per SM when there is no more than one for each: were there room
   // for two, the next call's CTAs would come in pairs beside this one's and
   // leave SMs idle (16 rows, 8192 x 4096: 10.4 us, else 11.9).
-  int smem = L::alloc(a.groups, split, a.part_cols);
+  int smem = L::alloc(a.groups, split, a.part_cols, kLists);
   if (SPLIT && most * split <= ctx.num_sms) smem = std::max(smem, 118 * 1024);
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = ctx.stream;
@@ -1521,7 +1549,7 @@ mma_status_t run(const Ctx& ctx, const Operand& P, const Operand& Q,
   int at_once = 0;
   if (!resident.get(ctx, &at_once, [&](int* v) {
         bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       L::alloc(kMaxGroups, kMostSplit, BN)) == cudaSuccess;
+                                       L::alloc(kMaxGroups, kMostSplit, BN, kLists)) == cudaSuccess;
         // the split of the registers counts on the launch's
         cudaFuncAttributes fa = {};
         ok = ok && cudaFuncGetAttributes(&fa, kern) == cudaSuccess &&
