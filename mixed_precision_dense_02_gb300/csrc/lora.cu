@@ -231,8 +231,14 @@ struct Shrink {
   static constexpr int THREADS = kThreads + (PRODUCER ? 32 : 0);
   static constexpr int BLOCKS = BM == 16 && RP <= 32 ? 4 : 2;
   static constexpr int SMEM = STAGES * STAGE + 1024;  // (the sums: 512 * RP bytes)
+  // columns of B behind the piece's own and its cluster's sums
+  static constexpr int B_BYTES = kThreads * RP * 2, B_AT = 2 * BM * RP * 4;
+  static constexpr int B_ROOM = (STAGES * STAGE - B_AT) / B_BYTES;
+  static constexpr int B_STAGES = B_ROOM < 4 ? B_ROOM : 4;
+  static_assert(B_STAGES >= 1 && B_AT % 1024 == 0);
 };
 
+constexpr int kMostParts = 8;       // CTAs that share a piece's k range
 constexpr int kSmallBlocks = 4096;  // rows up to which blocks have 16
 
 // The swizzle of rows of `bytes` (the same that swizzled() computes).
@@ -243,13 +249,43 @@ constexpr CUtensorMapSwizzle swizzle_of(int bytes) {
 }
 
 // `many` rows of extra, up to R: their sums `s` (RP apart, zeros past the rank; the
-// room behind the last is read too) times kCols columns of B per thread from p0 on,
-// kThreads apart, whose loads go together.
+// room behind the last is read too) times a column of B, this thread's in `stage`.
+template <bool BF16, int R, int RP>
+__device__ __forceinline__ void expand(const uint8_t* stage, const float* s, int many,
+                                       float* out, int N) {
+  constexpr int RB = RP < 64 ? RP : 64;
+  float2 v[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) v[r] = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < RP; k += 8) {
+    const uint4 w = *reinterpret_cast<const uint4*>(
+        stage + k / RB * kThreads * RB * 2 + swizzled<RB * 2>(threadIdx.x, k % RB / 8));
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      float2 b;
+      if constexpr (BF16)
+        b = make_float2(__uint_as_float(q[y] << 16), __uint_as_float(q[y] & 0xFFFF0000u));
+      else
+        b = __half22float2(*reinterpret_cast<const __half2*>(&q[y]));
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        v[r] = __ffma2_rn(*reinterpret_cast<const float2*>(s + r * RP + k + 2 * y), b, v[r]);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (r < many) out[int64_t(r) * N] = v[r].x + v[r].y;
+}
+
+// The same of a row-major B, kCols columns per thread from p0 on, kThreads apart, whose
+// loads go together.
 constexpr int kCols = 4;
 
-template <bool BF16, bool ROW, int R, int RP>
-__device__ __forceinline__ void expand(const LoraProblem& g, const uint16_t* B, const float* s,
-                                       int many, int p0, float* out) {
+template <bool BF16, int R, int RP>
+__device__ __forceinline__ void expand_rows(const LoraProblem& g, const uint16_t* B,
+                                            const float* s, int many, int p0, float* out) {
   const int rank = int(g.rank), N = int(g.N);
   float2 v[R][kCols];
 #pragma unroll
@@ -259,45 +295,24 @@ __device__ __forceinline__ void expand(const LoraProblem& g, const uint16_t* B, 
   const int p1 = p0 + threadIdx.x;
 #pragma unroll 2
   for (int k = 0; k < rank; k += 8) {
-    uint4 w[kCols];
     const int left = rank - k;
 #pragma unroll
     for (int x = 0; x < kCols; ++x) {
       const int p = min(p1 + x * kThreads, N - 1);
-      if constexpr (ROW) {
-        uint32_t f[8];
+      uint32_t f[8];
 #pragma unroll
-        for (int y = 0; y < 8; ++y) f[y] = y < left ? B[(k + y) * g.ldb + p] : 0u;
-        w[x] = make_uint4(f[0] | f[1] << 16, f[2] | f[3] << 16, f[4] | f[5] << 16,
-                          f[6] | f[7] << 16);
-      } else {
-        w[x] = __ldg(reinterpret_cast<const uint4*>(B + p * g.ldb + k));
-      }
-    }
-    if (!ROW && left < 8) {  // what stands behind a row's rank numbers is none of them
+      for (int y = 0; y < 8; ++y) f[y] = y < left ? B[(k + y) * g.ldb + p] : 0u;
 #pragma unroll
-      for (int x = 0; x < kCols; ++x) {
-        uint32_t q[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          if (left < 2 * y + 2) q[y] = left <= 2 * y ? 0u : q[y] & 0xFFFFu;
-        w[x] = make_uint4(q[0], q[1], q[2], q[3]);
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < kCols; ++x) {
-      const uint32_t q[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
+      for (int y = 0; y < 8; y += 2) {
+        const uint32_t q = f[y] | f[y + 1] << 16;
         float2 b;
         if constexpr (BF16)
-          b = make_float2(__uint_as_float(q[y] << 16), __uint_as_float(q[y] & 0xFFFF0000u));
+          b = make_float2(__uint_as_float(q << 16), __uint_as_float(q & 0xFFFF0000u));
         else
-          b = __half22float2(*reinterpret_cast<const __half2*>(&q[y]));
+          b = __half22float2(*reinterpret_cast<const __half2*>(&q));
 #pragma unroll
         for (int r = 0; r < R; ++r)
-          v[r][x] = __ffma2_rn(*reinterpret_cast<const float2*>(s + r * RP + k + 2 * y), b,
-                               v[r][x]);
+          v[r][x] = __ffma2_rn(*reinterpret_cast<const float2*>(s + r * RP + k + y), b, v[r][x]);
       }
     }
   }
@@ -305,28 +320,32 @@ __device__ __forceinline__ void expand(const LoraProblem& g, const uint16_t* B, 
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int x = 0; x < kCols; ++x)
-      if (r < many && p1 + x * kThreads < N) out[int64_t(r) * N + p1 + x * kThreads] = v[r][x].x + v[r][x].y;
+      if (r < many && p1 + x * kThreads < N)
+        out[int64_t(r) * N + p1 + x * kThreads] = v[r][x].x + v[r][x].y;
 }
 
 template <bool BF16, bool ROW, int BM, int RP, bool EVERY>
 __global__ void __launch_bounds__(Shrink<BM, RP, EVERY>::THREADS, Shrink<BM, RP, EVERY>::BLOCKS)
     lora_shrink_kernel(const __grid_constant__ CUtensorMap tmX,
-                       const __grid_constant__ CUtensorMap tmA, const LoraProblem g,
+                       const __grid_constant__ CUtensorMap tmA,
+                       const __grid_constant__ CUtensorMap tmB, const LoraProblem g,
                        const LoraLow low, unsigned* status) {
   using L = Shrink<BM, RP, EVERY>;
   constexpr int KS = L::KS, KB = KS / 64;
-  constexpr int RB = RP < 64 ? RP : 64;  // (ROW) sums per box
+  constexpr int RB = RP < 64 ? RP : 64;  // (ROW) sums per box of A, else of B
   constexpr int kRows = L::BLOCKS == 4 ? 1 : 2;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   __shared__ Requests req;
-  __shared__ Ring ring;
+  __shared__ Ring ring, columns;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   ring_init(ring, L::STAGES);
+  ring_init(columns, L::B_STAGES);
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
   }
   // The kernel after this one reads what is older than this one without waiting: it
   // may start when that is there.
@@ -447,6 +466,7 @@ __global__ void __launch_bounds__(Shrink<BM, RP, EVERY>::THREADS, Shrink<BM, RP,
     for (int w = 1; w < L::KW; ++w) v += sums[w * BM * RP + i];
     sums[i] = v;  // (read by this thread alone)
   }
+  fence_proxy_async_smem();  // (the columns of B land where other sums were)
   if (parts > 1) cluster_sync();
   else __syncthreads();
   float* mine = sums + BM * RP;  // all CTAs' (the room of a warp's sums, done with)
@@ -455,8 +475,12 @@ __global__ void __launch_bounds__(Shrink<BM, RP, EVERY>::THREADS, Shrink<BM, RP,
        i < (add ? rows * RP : min((part + 1) * share, rows * RP)); i += L::THREADS) {
     float v = 0.f;
     if (parts > 1) {
-      for (int r = 0; r < parts; ++r)
-        v += ld_shared_cluster_f32(mapa_shared(smem_u32(sums + i), r));
+      float w[kMostParts];  // (their loads together)
+#pragma unroll
+      for (int r = 0; r < kMostParts; ++r)
+        w[r] = r < parts ? ld_shared_cluster_f32(mapa_shared(smem_u32(sums + i), r)) : 0.f;
+#pragma unroll
+      for (int r = 0; r < kMostParts; ++r) v += w[r];
     } else {
       v = sums[i];
     }
@@ -467,11 +491,29 @@ __global__ void __launch_bounds__(Shrink<BM, RP, EVERY>::THREADS, Shrink<BM, RP,
   if (parts > 1) cluster_sync();  // no CTA leaves while another reads its sums
   if (!add || !ok || N == 0) return;
   __syncthreads();
-  if (L::PRODUCER && warp == kThreads / 32) return;
-  for (int p0 = part * kThreads * kCols; p0 < N; p0 += parts * kThreads * kCols) {
-    for (int r0 = 0; r0 < rows; r0 += kRows)
-      expand<BF16, ROW, kRows, RP>(g, B, mine + r0 * RP, min(rows - r0, kRows), p0,
-                                   extra_row(r0));
+  if constexpr (ROW) {
+    if (L::PRODUCER && warp == kThreads / 32) return;
+    for (int p0 = part * kThreads * kCols; p0 < N; p0 += parts * kThreads * kCols)
+      for (int r0 = 0; r0 < rows; r0 += kRows)
+        expand_rows<BF16, kRows, RP>(g, B, mine + r0 * RP, min(rows - r0, kRows), p0,
+                                     extra_row(r0));
+  } else {
+    const int blocks = ((N + kThreads - 1) / kThreads - part + parts - 1) / parts;
+    ring_run<L::PRODUCER, L::B_STAGES, L::B_BYTES>(
+        columns, smem + L::B_AT, blocks, L::B_BYTES, status,
+        [&](int step, uint8_t* bs, uint64_t* bar) {
+          const int p = (part + step * parts) * kThreads;
+#pragma unroll
+          for (int b = 0; b < RP / RB; ++b)
+            tma_load_3d(&tmB, bar, bs + b * kThreads * RB * 2, b * RB, p, who);
+        },
+        [&](int step, const uint8_t* stage) {
+          const int p = (part + step * parts) * kThreads + threadIdx.x;
+          if (p >= N) return;
+          if (rows == 1) return expand<BF16, 1, RP>(stage, mine, 1, extra_row(0) + p, N);
+          for (int r = 0; r < rows; r += 4)
+            expand<BF16, 4, RP>(stage, mine + r * RP, rows - r, extra_row(r) + p, N);
+        });
   }
 }
 
@@ -499,7 +541,7 @@ mma_status_t shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
   const int64_t slices = any ? g.adapters_total : 1;
   const int64_t slice = slices > 1 ? g.stride_a : any ? g.lda : 8;
   const void* const a = any ? g.A : low.f32;
-  CUtensorMap tx, ta;
+  CUtensorMap tx, ta, tb;
   if (!make_map(&tx, any ? g.X : low.f32, 2, any ? g.K : 8, any ? g.rows : 1,
                 any ? g.ldx : 8, 1, any ? g.ldx : 8, 64, BM) ||
       !(ROW ? make_map(&ta, a, 2, any ? g.rank : 8, any ? g.K : 1, any ? g.lda : 8,
@@ -507,13 +549,18 @@ mma_status_t shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
             : make_map(&ta, a, 2, any ? g.K : 8, any ? g.rank : 1, any ? g.lda : 8,
                        slices, slice, 64, RP)))
     return MMA_ERR_LAUNCH;
+  tb = ta;
+  if (!ROW && g.adapters_total > 0 && g.N > 0 &&  // (whatever K is)
+      !make_map(&tb, g.B, 2, g.rank, g.N, g.ldb, g.adapters_total,
+                g.adapters_total > 1 ? g.stride_b : g.ldb, RB, kThreads, swizzle_of(RB * 2)))
+    return MMA_ERR_LAUNCH;
   const int64_t pieces = (g.rows + BM - 1) / BM + g.requests + 1;
   const int64_t steps = (g.K + L::KS - 1) / L::KS;
   // As many CTAs per piece as there is room for at once (with few rows twice per SM,
   // beside the shared product), each with two stages at least.
   const int per_sm = EVERY ? 2 : std::min(BM == 16 ? 4 : 2, 224 * 1024 / (L::SMEM + 10 * 1024));
   int parts = 1;
-  while (parts < 8 && pieces * parts * 2 <= int64_t(per_sm) * ctx.num_sms && steps >= parts * 4)
+  while (parts < kMostParts && pieces * parts * 2 <= int64_t(per_sm) * ctx.num_sms && steps >= parts * 4)
     parts *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(pieces), unsigned(parts), 1);
@@ -529,7 +576,7 @@ mma_status_t shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tx, ta, g, low, ctx.status);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tx, ta, tb, g, low, ctx.status);
   const cudaError_t after = cudaGetLastError();
   return e == cudaSuccess && after == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
 }
