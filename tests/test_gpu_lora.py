@@ -182,6 +182,21 @@ def test_no_requests_no_adapters_no_rank():
     assert mma.gemm_lora(x[:0], w, rows16(rnd(3, 2, 8, 64), T["bf16"]), rows16(rnd(4, 2, 72, 8), T["bf16"]), ints([0, 0])).shape == (0, 72)
 
 
+@pytest.mark.parametrize("row", [False, True])
+@pytest.mark.parametrize("lengths", [[1, 3, 0, 2], [150, 1, 2, 40]])
+def test_no_k(lengths, row):
+    """Without k nothing is read of X, W and A, and the sums are zeros: the result is the addend."""
+    t, n, r = T["bf16"], 328, 12
+    m = sum(lengths)
+    x, c = torch.empty(m, 0, dtype=t, device="cuda"), rows16(rnd(1, m, n), t)
+    w = torch.empty((0, n) if row else (n, 0), dtype=t, device="cuda")
+    a = torch.empty((4, 0, r) if row else (4, r, 0), dtype=t, device="cuda")
+    b = rows16(rnd(2, 4, r, n) if row else rnd(2, 4, n, r), t)
+    offsets = ints([0] + list(torch.tensor(lengths).cumsum(0)))
+    d, s = mma.gemm_lora(x, w, a, b, offsets, C=c, b_layout="row" if row else "col", sums=True)
+    assert torch.equal(d, c) and not s.any()
+
+
 def test_offsets_out_of_range_and_order():
     """Clamped, and decreasing ones raised to the one before, as in grouped products."""
     good = Case([10, 0, 30, 20], 136, 128, 16, [0, 1, 2, 3], 4, seed=3)
