@@ -652,8 +652,8 @@ mma_status_t mma_gemm_grouped_f8(int type_a, int type_b, int type_d,
  * weights, share and loss NaN, its choices being experts all the same.
  * All outputs are contiguous device memory, the same bits from run to run.
  * workspace: device memory, 4-byte aligned, of mma_route_workspace(T, E) bytes (0
- * up to 128 tokens), which the call's work on `stream` uses and nothing else may
- * meanwhile.
+ * for up to 96 tokens and 8192 logits), which the call's work on `stream` uses and
+ * nothing else may meanwhile.
  */
 #define MMA_MAX_CHOICES 32
 int64_t mma_route_workspace(int64_t T, int64_t E);

@@ -17,10 +17,10 @@
 // Sorting is by counting, without atomics whose order would show.  A block sets,
 // for each expert, a bit for each of 64 tokens: an expert's tokens before a given
 // one are the bits below it.  Blocks of consecutive tokens count, a second kernel
-// adds the counts up over the blocks, a third puts every choice in its place.  Up
-// to kOneBlock tokens one block does all of it: one launch for generated tokens.
+// adds the counts up over the blocks, a third puts every choice in its place.  Of
+// few tokens one block does all of it: one launch for generated tokens.
 //
-// 16384 tokens, 256 experts, 8 each, FP32: 26 us, of which the choices take some 15,
+// 16384 tokens, 256 experts, 8 each, FP32: 25 us, of which the choices take some 14,
 // bound by instructions (600 per token; the logits' 17 MB are read at 0.9 TB/s), the
 // other two kernels the rest by their launches and latencies.  Gradient 12.3 us (3 TB/s).
 #include <algorithm>
@@ -32,11 +32,15 @@
 namespace mmagb {
 namespace {
 
-constexpr int kBatch = 64;       // tokens whose bits are set at a time
+constexpr int kBatch = 64;        // tokens whose bits are set at a time
 constexpr int kMostBlocks = 304;  // of the first kernel
-// Tokens that one block takes alone: 64 experts, 6 each, 96 tokens 9.6 us and 256
-// 19.5; by three kernels 257 tokens 12.3.
-constexpr int kOneBlock = 128;
+// Least tokens of one, a warp for each (64 experts, 257 tokens: 9.4 us, with 64 13.2).
+constexpr int kLeast = 16;
+constexpr int kOneBlock = 96;  // most tokens that one block takes alone
+// One block or three kernels, device time: 64 experts, 6 each, 32 tokens 5.6 and 8.4 us,
+// 64 7.3 and 8.4, 96 9.6 and 8.9 (but two launches more); 256 experts, 8 each, 32 tokens
+// 8.0 and 9.6, 128 19.7 and 11.0; 1024, 32 tokens 22 and 14.9.
+constexpr bool one_block(int64_t T, int64_t E) { return T <= kOneBlock && T * E <= 8192; }
 
 struct Choices {
   int tokens, experts, k, per_block, blocks;
@@ -591,15 +595,13 @@ struct Split {
 };
 
 Split split_of(int64_t T) {
-  const int64_t batches = (T + kBatch - 1) / kBatch;
-  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(batches, kMostBlocks));
-  const int64_t each = (batches + blocks - 1) / blocks;
-  return Split{int(each * kBatch), int(std::max<int64_t>(1, each ? (batches + each - 1) / each : 1))};
+  const int64_t per = std::max<int64_t>(kLeast, (T + kMostBlocks - 1) / kMostBlocks);
+  return Split{int(per), int(std::max<int64_t>(1, (T + per - 1) / per))};
 }
 
 template <class T, int V>
 mma_status_t route(const Ctx& ctx, const Choices& a) {
-  const bool one = a.tokens <= kOneBlock;
+  const bool one = one_block(a.tokens, a.experts);
   const int warps = one ? 32 : 16;
   const size_t smem = size_t(a.experts + a.k) * 8 + size_t(a.experts + 1) * 4 +
                       size_t(warps) * a.experts * 4 +
@@ -647,7 +649,7 @@ mma_status_t by_width(int64_t experts, F&& f) {
 }  // namespace
 
 int64_t route_workspace_bytes(int64_t T, int64_t E) {
-  return T <= kOneBlock ? 0 : (int64_t(split_of(T).blocks) * (2 * E + 2) + E + 2) * 4;
+  return one_block(T, E) ? 0 : (int64_t(split_of(T).blocks) * (2 * E + 2) + E + 2) * 4;
 }
 
 mma_status_t launch_route(const Ctx& ctx, const RouteProblem& p, void* workspace) {
@@ -656,7 +658,7 @@ mma_status_t launch_route(const Ctx& ctx, const RouteProblem& p, void* workspace
   a.tokens = int(p.T);
   a.experts = int(p.E);
   a.k = int(p.k);
-  a.per_block = p.T <= kOneBlock ? kOneBlock : s.per_block;
+  a.per_block = one_block(p.T, p.E) ? kOneBlock : s.per_block;
   a.blocks = s.blocks;
   a.ldx = p.ldx;
   a.x = p.x;

@@ -100,7 +100,7 @@ def check(got, ref, e, k):
     assert abs(float(got.loss) - float(ref["loss"])) <= lim
 
 
-SIZES = [(1, 1, 1), (1, 64, 6), (3, 7, 7), (5, 1024, 32), (63, 33, 2), (64, 32, 1), (65, 100, 8), (96, 64, 6), (128, 64, 6), (129, 64, 6),
+SIZES = [(1, 1, 1), (1, 64, 6), (3, 7, 7), (5, 1024, 32), (63, 33, 2), (64, 32, 1), (65, 100, 8), (96, 64, 6), (97, 64, 6), (8, 1024, 3), (9, 1024, 3), (4864, 40, 3), (4865, 40, 3),
          (256, 300, 4), (257, 64, 8), (1000, 16, 2), (1000, 1000, 10), (4096, 256, 8), (20000, 8, 2),
          (20001, 130, 5), (300, 512, 32), (40000, 5, 1)]
 

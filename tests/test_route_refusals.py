@@ -47,8 +47,8 @@ def test_forward(kw, code):
 
 def test_workspace():
     f = binding.load().mma_route_workspace
-    assert f(0, 64) == 0 and f(128, 64) == 0 and f(-1, 64) == 0 and f(1000, 0) == 0
-    assert f(129, 64) == (3 * (2 * 64 + 2) + 66) * 4
+    assert f(0, 64) == 0 and f(96, 64) == 0 and f(32, 256) == 0 and f(-1, 64) == 0 and f(1000, 0) == 0
+    assert f(97, 64) == (7 * (2 * 64 + 2) + 66) * 4 and f(33, 256) > 0
     assert f(10 ** 8, 64) <= (304 * (2 * 64 + 2) + 66) * 4
 
 
