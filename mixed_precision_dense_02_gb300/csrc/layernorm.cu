@@ -743,6 +743,7 @@ mma_status_t backward(const Ctx& ctx, const NormBackProblem& p, bool w32, float*
     ok = launch_ring(ctx, wide, layernorm_stats_kernel<T>,
                      std::min<int64_t>(p.M, ctx.num_sms * (cached ? 1 : 2)), 1024,
                      cached ? vectors * 32 : 0, p, w32, cached, stats);
+    if (!ok) return MMA_ERR_LAUNCH;
     // as many blocks of rows as give every SM some sixteen of columns
     const int64_t columns = (vectors + 127) / 128;
     const int64_t want = std::max<int64_t>(1, 16 * ctx.num_sms / columns);

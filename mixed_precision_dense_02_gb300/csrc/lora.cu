@@ -368,7 +368,8 @@ __global__ void __launch_bounds__(Shrink<BM, RP, EVERY>::THREADS, Shrink<BM, RP,
   if (rows <= 0) return;
   const int part = blockIdx.y, parts = gridDim.y;
   const int first_of = bound[piece.request];
-  const bool add = EVERY || bound[piece.request + 1] - first_of < kLoraRows;
+  // (without k there is nothing to add, and B need not exist)
+  const bool add = g.K > 0 && (EVERY || bound[piece.request + 1] - first_of < kLoraRows);
   auto extra_row = [&](int row) {
     const int64_t t = piece.from + row;
     return low.extra +
@@ -557,7 +558,7 @@ mma_status_t shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
                        slices, slice, 64, RP)))
     return MMA_ERR_LAUNCH;
   tb = ta;
-  if (!ROW && g.adapters_total > 0 && g.N > 0 &&  // (whatever K is)
+  if (!ROW && any && g.N > 0 &&
       !make_map(&tb, g.B, 2, g.rank, g.N, g.ldb, g.adapters_total,
                 g.adapters_total > 1 ? g.stride_b : g.ldb, RB, kThreads, swizzle_of(RB * 2)))
     return MMA_ERR_LAUNCH;

@@ -195,6 +195,15 @@ def test_no_k(lengths, row):
     offsets = ints([0] + list(torch.tensor(lengths).cumsum(0)))
     d, s = mma.gemm_lora(x, w, a, b, offsets, C=c, b_layout="row" if row else "col", sums=True)
     assert torch.equal(d, c) and not s.any()
+    # the ABI takes no matrices at all then
+    need = binding.load().mma_gemm_lora_workspace(2, 2, m, n, r, 4)
+    ws, s = torch.empty(need, dtype=torch.uint8, device="cuda"), torch.ones(m, 16, device="cuda")
+    d.zero_()
+    assert c.stride(0) == d.stride(0) == n
+    st = binding.load().mma_gemm_lora(2, 2, m, n, 0, r, None, 0, None, 0, None, 0, 0, None, 0, 0, 1 if row else 0, 4,
+                                      offsets.data_ptr(), None, 4, None, c.data_ptr(), n, d.data_ptr(), n, s.data_ptr(), 16,
+                                      ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and torch.equal(d, c) and not s[:, :r].any()
 
 
 def test_offsets_out_of_range_and_order():
