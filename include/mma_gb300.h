@@ -700,7 +700,7 @@ mma_status_t mma_route_backward(int type, int64_t T, int64_t E, int64_t k,
  * A, B    : adapter a's matrices at A + a * stride_a and B + a * stride_b
  *           elements, adapters_total of them (at most 65535), of one rank, at most
  *           MMA_MAX_RANK (a smaller one is padded with zeros).
- * requests: 0 .. MMA_MAX_GROUPS; offsets: as mma_gemm_grouped's, but no row is left
+ * requests: 0 .. MMA_MAX_REQUESTS; offsets: as mma_gemm_grouped's, but no row is left
  *           out: rows of no request have no adapter.
  * adapters: int32 in device memory, or NULL (request i has adapter i).  Outside [0,
  *           adapters_total): none.  Requests may share an adapter.
@@ -712,12 +712,14 @@ mma_status_t mma_route_backward(int type, int64_t T, int64_t E, int64_t k,
  * workspace: 16-byte aligned device memory of mma_gemm_lora_workspace(type_in,
  *           type_d, T, N, rank, requests) bytes, which the call's work on `stream`
  *           uses and nothing else may meanwhile.
- * With up to 128 rows, and for requests of fewer than 8, the product with B takes S
- * as it is.  For the others S is rounded to type_in (an FP32 D: to a sum of two FP16
- * or three BF16 numbers), whose range it has to keep.  A NaN or infinity in one adapter or row stays with
- * the rows of that adapter, or that row.
+ * With up to 128 rows or more than MMA_MAX_GROUPS requests, and for requests of fewer
+ * than 8 rows, the product with B takes S as it is.  For the others S is rounded to
+ * type_in (an FP32 D: to a sum of two FP16 or three BF16 numbers), whose range it has
+ * to keep.  A NaN or infinity in one adapter or row stays with the rows of that
+ * adapter, or that row.
  */
 #define MMA_MAX_RANK 128
+#define MMA_MAX_REQUESTS 65536
 int64_t mma_gemm_lora_workspace(int type_in, int type_d, int64_t T, int64_t N,
                                 int64_t rank, int64_t requests);
 mma_status_t mma_gemm_lora(int type_in, int type_d, int64_t T, int64_t N,
@@ -745,12 +747,13 @@ mma_status_t mma_gemm_lora(int type_in, int type_d, int64_t T, int64_t N,
  * accumulate : nonzero -- added to DA and DB; else an adapter without rows gets
  *           zeros.
  * Sums are FP32, in a fixed order, through `workspace`: 16-byte aligned device
- * memory of mma_gemm_lora_wgrad_workspace(type_in, type_d, T, N, K, rank, requests)
- * bytes.  Other arguments as above.
+ * memory of mma_gemm_lora_wgrad_workspace(type_in, type_d, T, N, K, rank, requests,
+ * adapters_total) bytes.  Not both more than MMA_MAX_GROUPS requests and adapters
+ * (MMA_ERR_UNSUPPORTED).  Other arguments as above.
  */
 int64_t mma_gemm_lora_wgrad_workspace(int type_in, int type_d, int64_t T,
                                       int64_t N, int64_t K, int64_t rank,
-                                      int64_t requests);
+                                      int64_t requests, int64_t adapters_total);
 mma_status_t mma_gemm_lora_wgrad(int type_in, int type_d, int64_t T, int64_t N,
                                  int64_t K, int64_t rank, const void *DY,
                                  int64_t lddy, const void *X, int64_t ldx,

@@ -86,7 +86,7 @@ SIGNATURES = {
                                    _i64, _p, _i64, _i64, _p, _i64, _i64, _int,
                                    _p, _i64, _p]),
     "mma_gemm_lora_wgrad_workspace": (_i64, [_int, _int, _i64, _i64, _i64, _i64,
-                                             _i64]),
+                                             _i64, _i64]),
     "mma_device_status": (_int, [_p]),
     "mma_selftest_wait_timeout": (_int, [_i64, _p]),
     "mma_selftest_gemm_abort": (_int, [_int, _i64, _p, _p, _p, _p]),
@@ -1049,7 +1049,7 @@ def gemm_lora(X, W, A, B, offsets, adapters=None, scales=None, C=None, D=None, *
     ``offsets``: (requests + 1,), ``adapters``: (requests,) int32 on the GPU (None:
     request j has adapter j; a negative one: none); ``scales``: (adapters,) float32.
     ``C``, ``D``: (T, N) of X's type or float32 (``out_dtype``, X's unless C or D is
-    given).  Rank at most 128.  Returns D; with ``sums=True`` also the rows' sums
+    given).  Rank at most 128, requests 65536.  Returns D; with ``sums=True`` also the rows' sums
     ``scales[a] * X[i] @ A[a]^T``, (T, rank) float32, for ``gemm_lora_wgrad``.
     """
     torch = _torch()
@@ -1117,7 +1117,7 @@ def _plan_lora_wgrad(dY, X, S, U, offsets, adapters, adapters_total, dA, dB, acc
             rank * K if dA is None else _slices("dA", dA),
             rank if dB is None else _rows("dB", dB),
             N * rank if dB is None else _slices("dB", dB), dtype,
-            load().mma_gemm_lora_wgrad_workspace(code, d_code, T, N, K, rank, requests),
+            load().mma_gemm_lora_wgrad_workspace(code, d_code, T, N, K, rank, requests, total),
             _one_device(dY, X, S, U, offsets, adapters, dA, dB))
 
 

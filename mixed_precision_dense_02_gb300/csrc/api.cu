@@ -1106,7 +1106,7 @@ mma_status_t check_lora(int type_in, int type_d, int64_t T, int64_t N, int64_t K
   if (!dim_ok(T) || !dim_ok(N) || !dim_ok(K) || rank < 0 || requests < 0 ||
       adapters_total < 0)
     return MMA_ERR_INVALID_ARG;
-  if (rank > MMA_MAX_RANK || requests > kMaxGroups || adapters_total > 65535 ||
+  if (rank > MMA_MAX_RANK || requests > MMA_MAX_REQUESTS || adapters_total > 65535 ||
       T > INT32_MAX - 1024 || N > INT32_MAX - 1024 || K > INT32_MAX - 1024)
     return MMA_ERR_UNSUPPORTED;
   return rank > 0 && T > 0 ? check_words(offsets) : MMA_OK;
@@ -1127,7 +1127,7 @@ struct LoraSpace {
 
 LoraSpace lora_space(int type_in, int type_d, int64_t T, int64_t N, int64_t rank,
                      int64_t requests) {
-  const bool every = T <= kLoraEveryRow;
+  const bool every = lora_every(T, requests);
   const int64_t rows = lora_own_places(T, requests) ? T : requests * (kLoraRows - 1);
   const int64_t parts = every ? 0 : lora_parts(type_in == MMA_BF16, type_d);
   return LoraSpace{(rows * N * 4 + 15) / 16 * 16, parts * T * round8(rank) * 2};
@@ -1138,7 +1138,7 @@ LoraSpace lora_space(int type_in, int type_d, int64_t T, int64_t N, int64_t rank
 extern "C" int64_t mma_gemm_lora_workspace(int type_in, int type_d, int64_t T, int64_t N,
                                            int64_t rank, int64_t requests) {
   if (!dim_ok(T) || !dim_ok(N) || rank < 1 || rank > MMA_MAX_RANK || requests < 0 ||
-      requests > kMaxGroups)
+      requests > MMA_MAX_REQUESTS)
     return 0;
   const LoraSpace s = lora_space(type_in, type_d, T, N, rank, requests);
   return s.extra + s.halves;
@@ -1215,7 +1215,7 @@ extern "C" mma_status_t mma_gemm_lora(
   g.D = D;
   g.ldd = ldd;
   const LoraSpace space = lora_space(type_in, type_d, T, N, rank, requests);
-  const int parts = T <= kLoraEveryRow ? 0 : lora_parts(g.bf16, type_d);
+  const int parts = lora_every(T, requests) ? 0 : lora_parts(g.bf16, type_d);
   LoraLow low = {S, static_cast<uint8_t*>(workspace) + space.extra,
                  static_cast<float*>(workspace), int(lds), int(round8(rank)), parts};
   if (rank > 0) MMA_CHECK(launch_lora_shrink(ctx, g, low));
@@ -1227,11 +1227,13 @@ extern "C" mma_status_t mma_gemm_lora(
 
 extern "C" int64_t mma_gemm_lora_wgrad_workspace(int type_in, int type_d, int64_t T,
                                                  int64_t N, int64_t K, int64_t rank,
-                                                 int64_t requests) {
+                                                 int64_t requests,
+                                                 int64_t adapters_total) {
   if (!dim_ok(T) || !dim_ok(N) || !dim_ok(K) || rank < 1 || rank > MMA_MAX_RANK ||
-      requests < 0 || requests > kMaxGroups)
+      requests < 0 || requests > MMA_MAX_REQUESTS || adapters_total < 0)
     return 0;
-  return lora_wgrad_workspace_bytes(type_in == MMA_BF16, type_d, T, N, K, rank, requests);
+  return lora_wgrad_workspace_bytes(type_in == MMA_BF16, type_d, T, N, K, rank, requests,
+                                    adapters_total);
 }
 
 extern "C" mma_status_t mma_gemm_lora_wgrad(
@@ -1243,6 +1245,7 @@ extern "C" mma_status_t mma_gemm_lora_wgrad(
     int64_t workspace_bytes, void* stream) {
   MMA_CHECK(check_lora(type_in, type_d, T, N, K, rank, requests, offsets, adapters_total));
   if ((N + 127) / 128 + (K + 127) / 128 > 65535) return MMA_ERR_UNSUPPORTED;
+  if (requests > kMaxGroups && adapters_total > kMaxGroups) return MMA_ERR_UNSUPPORTED;
   if (rank == 0 || adapters_total == 0 || N + K == 0) return MMA_OK;
   MMA_CHECK(check_words(offsets));
   if (adapters) MMA_CHECK(check_words(adapters));
@@ -1263,7 +1266,8 @@ extern "C" mma_status_t mma_gemm_lora_wgrad(
     if (workspace == nullptr) return MMA_ERR_INVALID_ARG;
     if (!aligned16(workspace)) return MMA_ERR_MISALIGNED;
     if (workspace_bytes <
-        mma_gemm_lora_wgrad_workspace(type_in, type_d, T, N, K, rank, requests))
+        mma_gemm_lora_wgrad_workspace(type_in, type_d, T, N, K, rank, requests,
+                                      adapters_total))
       return MMA_ERR_INVALID_ARG;
   }
   int dev = -1;

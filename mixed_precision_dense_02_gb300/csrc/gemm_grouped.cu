@@ -1715,7 +1715,9 @@ mma_status_t launch_gemm_lora(const Ctx& ctx, const LoraProblem& g, const LoraLo
   a.status = ctx.status;
   const Operand X = {g.X, g.ldx, g.rows, 1, 0};
   const Operand W = {g.W, g.ldw, g.row_major ? g.K : g.N, 1, 0};
-  const bool pair = g.rows > kLoraEveryRow;
+  // (with more requests than fit beside a pair's tiles every row is added)
+  const bool every = low && lora_every(g.rows, g.requests);
+  const bool pair = g.rows > kLoraEveryRow && !every;
   a.idesc = idesc_f32(g.bf16, g.bf16, g.row_major, false, pair ? 2 * kP : kP);
   a.groups = 1;
   if (!low) {
@@ -1730,6 +1732,8 @@ mma_status_t launch_gemm_lora(const Ctx& ctx, const LoraProblem& g, const LoraLo
   if (!pair) {
     if (g.row_major)
       return run<false, true, false, false, false, false, 1, 128, 6, kEveryRow>(ctx, W, X, a);
+    if (g.rows > kLoraEveryRow)
+      return run<false, false, false, false, false, false, 1, 128, 6, kEveryRow>(ctx, W, X, a);
     return few_rows<false, kEveryRow>(ctx, W, X, a, g.rows);
   }
   a.groups = int(g.requests);

@@ -260,12 +260,16 @@ struct LoraProblem {
 // What its kernels hand on.  The rows' sums scale * (X A): in FP32 (ld32 a multiple
 // of 8, so that eight can be read from any eighth one) and, for more rows than
 // kLoraEveryRow, as `parts` matrices of 16 bits whose sum they are.  In `extra` what
-// the adapters add, FP32 rows of N: with up to kLoraEveryRow rows for all of them,
+// the adapters add, FP32 rows of N: with up to kLoraEveryRow rows, or more requests than
+// the shared product can list (MMA_MAX_GROUPS), for all of them,
 // else for those of requests of fewer than kLoraRows rows, at the row's own place or
 // (where that takes fewer) in kLoraRows - 1 places for each request.
 constexpr int kLoraEveryRow = 128, kLoraRows = 8;
+constexpr bool lora_every(int64_t rows, int64_t requests) {
+  return rows <= kLoraEveryRow || requests > MMA_MAX_GROUPS;
+}
 constexpr bool lora_own_places(int64_t rows, int64_t requests) {
-  return rows <= kLoraEveryRow || rows <= requests * (kLoraRows - 1);
+  return lora_every(rows, requests) || rows <= requests * (kLoraRows - 1);
 }
 // Numbers of 16 bits that stand for an FP32 sum in a product: for an FP32 result as
 // many as hold its 24 bits (BF16 three of 8, FP16 two of 11, which leave 2^-22 of
@@ -306,7 +310,7 @@ struct LoraWgradProblem {
   bool accumulate;
 };
 int64_t lora_wgrad_workspace_bytes(bool bf16, int d_type, int64_t T, int64_t N, int64_t K,
-                                   int64_t rank, int64_t requests);
+                                   int64_t rank, int64_t requests, int64_t total);
 mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& g, void* workspace);
 
 // Root-mean-square norm with the residual's addition (rmsnorm.cu).  Element

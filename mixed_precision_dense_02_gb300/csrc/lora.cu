@@ -100,6 +100,67 @@ __device__ __forceinline__ int adapter_of(const Requests& r, int j, int requests
   return j < 1 || j > requests ? -1 : max(r.who[j - 1], -1);
 }
 
+// Piece `u` of blocks of `per` rows (a power of two), as piece_of, of any number of
+// requests: each thread has kAtOnce of them, and only the piece's own is kept.
+struct OnePiece {
+  int scan[kThreads / 32 + 1];
+  int request, first, next, who;  // `next`: the request's end; who: its adapter, or -1
+};
+
+constexpr int kAtOnce = 4;
+
+__device__ __forceinline__ Piece find_piece(OnePiece& o, const int* offsets,
+                                            const int* adapters, int total, int requests,
+                                            int T, int per, int u) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  if (threadIdx.x == 0) o.request = -1;
+  int before = 0;
+  // element j is the bound behind request j - 1, which is the last one there is for u
+  // if its own first piece is not above u and that of request j is
+  for (int base = 1; base <= requests + 2; base += blockDim.x * kAtOnce) {
+    int v[kAtOnce], who[kAtOnce], most = 0;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int j = base + threadIdx.x * kAtOnce + i;
+      v[i] = j <= requests + 1 ? min(max(__ldg(offsets + j - 1), 0), T) : T;
+      who[i] = j < 2 || j > requests + 1 ? -1 : adapters ? __ldg(adapters + j - 2) : j - 2;
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) most = v[i] = max(v[i], most);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, most, d);
+      if (lane >= d) most = max(most, up);
+    }
+    if (lane == 31) o.scan[warp] = most;
+    int last = __shfl_up_sync(0xffffffffu, most, 1);
+    last = max(lane > 0 ? last : 0, before);
+    __syncthreads();
+    for (int w = 0; w < warps; ++w) {
+      if (w < warp) last = max(last, o.scan[w]);
+      before = max(before, o.scan[w]);
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int j = base + threadIdx.x * kAtOnce + i, end = max(last, v[i]);
+      if (j <= requests + 2 && last / per + j - 1 <= u &&
+          (j == requests + 2 || end / per + j > u)) {
+        o.request = j - 1;
+        o.first = last;
+        o.next = end;
+        o.who = who[i] < total ? max(who[i], -1) : -1;
+      }
+      last = end;
+    }
+    __syncthreads();
+    if (o.request >= 0) break;
+  }
+  const int j = o.request;
+  const int64_t from = max(int64_t(u - j) * per, int64_t(o.first));
+  const int to = int(min(int64_t(u - j + 1) * per, int64_t(o.next)));
+  return Piece{j, int(min(from, int64_t(to))), to};
+}
+
 // Byte offset of 16-byte chunk c of a row of ROW_BYTES, so that eight rows' chunks
 // c are in different banks.
 template <int ROW_BYTES>
@@ -344,7 +405,7 @@ __global__ void __launch_bounds__(Shrink<BM, RP, EVERY>::THREADS, Shrink<BM, RP,
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  __shared__ Requests req;
+  __shared__ OnePiece one;
   __shared__ Ring ring, columns;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   ring_init(ring, L::STAGES);
@@ -359,17 +420,17 @@ __global__ void __launch_bounds__(Shrink<BM, RP, EVERY>::THREADS, Shrink<BM, RP,
   grid_dependency_wait();
   grid_dependents_start();
   const int requests = int(g.requests);
-  load_requests(req, g.offsets, g.adapters, int(g.adapters_total), requests, int(g.rows));
-  const int* bound = req.bound;
-  const Piece piece = piece_of(bound, requests, BM, blockIdx.x);
-  const int who = adapter_of(req, piece.request, requests);
+  const Piece piece = find_piece(one, g.offsets, g.adapters, int(g.adapters_total), requests,
+                                 int(g.rows), BM, blockIdx.x);
+  const int who = one.who;
   const int rows = piece.to - piece.from, rank = int(g.rank), N = int(g.N);
   // (the same in all CTAs of the cluster, so that all of them return)
   if (rows <= 0) return;
   const int part = blockIdx.y, parts = gridDim.y;
-  const int first_of = bound[piece.request];
+  const int first_of = one.first;
   // (without k there is nothing to add, and B need not exist)
-  const bool add = g.K > 0 && (EVERY || bound[piece.request + 1] - first_of < kLoraRows);
+  const bool every = EVERY || lora_every(g.rows, requests);
+  const bool add = g.K > 0 && (every || one.next - first_of < kLoraRows);
   auto extra_row = [&](int row) {
     const int64_t t = piece.from + row;
     return low.extra +
@@ -389,7 +450,7 @@ __global__ void __launch_bounds__(Shrink<BM, RP, EVERY>::THREADS, Shrink<BM, RP,
   if (who < 0) {
     for (int i = part * L::THREADS + threadIdx.x; i < rows * RP; i += parts * L::THREADS)
       put(i / RP, i % RP, 0.f);
-    if (EVERY)
+    if (every)
       for (int r = 0; r < rows; ++r)
         for (int p = part * L::THREADS + threadIdx.x; p < N; p += parts * L::THREADS)
           extra_row(r)[p] = 0.f;
@@ -617,6 +678,7 @@ struct WgradArgs {
   const int *offsets, *adapters;
   int d_type, parts, ld16;
   bool accumulate;
+  const int* to;    // gathered rows: each row's place, or -1; else null
   float* part;      // [pieces][rank][features of both sides]
   uint16_t* halves;  // [2][parts][T][ld16]
   unsigned* status;
@@ -645,6 +707,134 @@ struct Wgrad {
   static_assert(stages(3) >= 2 && smem(3) <= 216 * 1024, "the ring");
 };
 
+// Gathered rows: many small requests of few adapters would make a piece each, with a
+// share of the gradient as large as an adapter (1000 single tokens, 8192 + 8192
+// features, rank 128: 8 GB).  Instead the rows are copied in the order of their
+// adapters, which then are the requests.
+struct Gather {
+  int T, requests, total;
+  const int *offsets, *adapters;
+  int* bound;   // [requests + 1]: the offsets, clamped and in order
+  int* first;   // [requests]: the place of a request's first row, or -1
+  int* starts;  // [total + 1]: the adapters' rows
+  int* to;      // [T]: each row's place, or -1
+  const uint16_t* in[2];  // dy, x
+  int64_t ld[2], ld_out[2];
+  int F[2];
+  uint16_t* out[2];
+};
+
+// One block.  The adapters' rows are counted by 32 warps, each with consecutive
+// requests; a request's place is behind those of its adapter's in earlier warps and in
+// its own before it.
+__global__ void __launch_bounds__(1024) lora_order_kernel(const Gather g) {
+  extern __shared__ int count[];  // [32][total]
+  __shared__ int scan[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int before = 0;
+  for (int base = 0; base <= g.requests; base += 1024) {
+    const int i = base + threadIdx.x;
+    int v = i <= g.requests ? min(max(__ldg(g.offsets + i), 0), g.T) : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v = max(v, o);
+    }
+    if (lane == 31) scan[warp] = v;
+    __syncthreads();
+    v = max(v, before);
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) v = max(v, scan[w]);
+      before = max(before, scan[w]);
+    }
+    if (i <= g.requests) g.bound[i] = v;
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < 32 * g.total; i += 1024) count[i] = 0;
+  __syncthreads();
+  const int per = (g.requests + 1023) / 1024 * 32;  // requests of a warp
+  const int from = min(warp * per, g.requests), to = min(from + per, g.requests);
+  int* const mine = count + warp * g.total;
+  auto request = [&](int i, int* rows) {
+    int who = -1;
+    *rows = 0;
+    if (i < to) {
+      who = g.adapters ? __ldg(g.adapters + i) : i;
+      who = who < g.total ? max(who, -1) : -1;
+      *rows = g.bound[i + 1] - g.bound[i];
+    }
+    return who;
+  };
+  for (int i = from + lane; i < to; i += 32) {
+    int rows;
+    const int who = request(i, &rows);
+    if (who >= 0) atomicAdd(mine + who, rows);
+  }
+  __syncthreads();
+  int sum = 0;  // of adapter threadIdx.x, in place of each warp's those before it
+  if (int(threadIdx.x) < g.total)
+    for (int w = 0; w < 32; ++w) {
+      const int n = count[w * g.total + threadIdx.x];
+      count[w * g.total + threadIdx.x] = sum;
+      sum += n;
+    }
+  int s = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, s, d);
+    if (lane >= d) s += o;
+  }
+  if (lane == 31) scan[warp] = s;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) s += scan[w];
+  if (int(threadIdx.x) < g.total) {
+    g.starts[threadIdx.x] = s - sum;
+    if (int(threadIdx.x) == g.total - 1) g.starts[g.total] = s;
+    for (int w = 0; w < 32; ++w) count[w * g.total + threadIdx.x] += s - sum;
+  }
+  __syncthreads();
+  for (int base = from; base < to; base += 32) {
+    const int i = base + lane;
+    int rows, earlier = 0;
+    const int who = request(i, &rows);
+    bool last = true;
+    for (int d = 0; d < 32; ++d) {
+      const int n = __shfl_sync(0xffffffffu, rows, d);
+      const int w = __shfl_sync(0xffffffffu, who, d);
+      if (w == who && d < lane) earlier += n;
+      if (w == who && d > lane) last = false;
+    }
+    const int at = who >= 0 ? mine[who] + earlier : -1;
+    __syncwarp();
+    if (who >= 0 && last) mine[who] = at + rows;
+    __syncwarp();
+    if (i < to) g.first[i] = at;
+  }
+}
+
+// Each row to its place.
+__global__ void __launch_bounds__(256) lora_gather_kernel(const Gather g) {
+  for (int t = blockIdx.x; t < g.T; t += gridDim.x) {
+    int lo = 0, hi = g.requests;  // the last request that starts by row t
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (g.bound[mid] <= t) lo = mid; else hi = mid;
+    }
+    int place = -1;
+    if (t >= g.bound[lo] && t < g.bound[lo + 1] && g.first[lo] >= 0)
+      place = g.first[lo] + t - g.bound[lo];
+    if (threadIdx.x == 0) g.to[t] = place;
+    if (place < 0) continue;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4* in = reinterpret_cast<const uint4*>(g.in[i] + t * g.ld[i]);
+      uint4* out = reinterpret_cast<uint4*>(g.out[i] + place * g.ld_out[i]);
+#pragma unroll 4
+      for (int v = threadIdx.x; v < (g.F[i] + 7) / 8; v += 256) out[v] = __ldg(in + v);
+    }
+  }
+}
+
 // Both sides' sums in parts of 16 bits.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
@@ -658,12 +848,15 @@ __global__ void __launch_bounds__(kThreads)
   const int width = a.ld16 <= 8 ? 8 : a.ld16 <= 16 ? 16 : 32;
   const int per = kThreads / width;
   for (int64_t t = int64_t(blockIdx.x) * per + threadIdx.x / width; t < a.T;
-       t += int64_t(gridDim.x) * per)
+       t += int64_t(gridDim.x) * per) {
+    const int64_t row = a.to ? a.to[t] : t;
+    if (row < 0) continue;
     for (int n = threadIdx.x % width; n < a.ld16; n += width) {
       float v = n < a.rank ? side.low[t * side.ldl + n] : 0.f;
       for (int part = 0; part < a.parts; ++part)
-        out[part * all + t * a.ld16 + n] = take_half<BF16>(v);
+        out[part * all + row * a.ld16 + n] = take_half<BF16>(v);
     }
+  }
 }
 
 template <bool FIRST, class T>
@@ -1036,16 +1229,92 @@ mma_status_t launch_lora_shrink(const Ctx& ctx, const LoraProblem& g, const Lora
   });
 }
 
-int64_t lora_wgrad_workspace_bytes(bool bf16, int d_type, int64_t T, int64_t N, int64_t K,
-                                   int64_t rank, int64_t requests) {
-  if (T == 0) return 0;
-  const int64_t per = rows_per_piece(T, N, K, rank);
-  const int64_t part = ((T + per - 1) / per + requests + 1) * rank * (N + K) * 4;
-  return (part + 15) / 16 * 16 + 2 * lora_parts(bf16, d_type) * T * ((rank + 7) / 8 * 8) * 2;
+namespace {
+
+int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
+
+// More requests than a kernel lists, or shares of small requests that take more than
+// the rows' copies (8 bytes per sum and feature, 8 per row and feature).
+bool gathers(int64_t T, int64_t rank, int64_t requests, int64_t total) {
+  return total <= MMA_MAX_GROUPS &&
+         (requests > MMA_MAX_GROUPS || (requests - total) * rank > T);
 }
 
-mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& g, void* workspace) {
+int64_t gather_ints(int64_t T, int64_t requests, int64_t total) {
+  return round16((2 * requests + total + 2 + T) * 4);
+}
+
+// The rows in the order of their adapters.
+mma_status_t gather(const Ctx& ctx, LoraWgradProblem& p, WgradArgs& a, uint8_t*& room) {
+  Gather g = {};
+  g.T = int(p.rows);
+  g.requests = int(p.requests);
+  g.total = int(p.adapters_total);
+  g.offsets = p.offsets;
+  g.adapters = p.adapters;
+  g.bound = reinterpret_cast<int*>(room);
+  g.first = g.bound + g.requests + 1;
+  g.starts = g.first + g.requests;
+  g.to = g.starts + g.total + 1;
+  room += gather_ints(p.rows, p.requests, p.adapters_total);
+  const void* const in[2] = {p.DY, p.X};
+  const int64_t ld[2] = {p.lddy, p.ldx}, features[2] = {p.N, p.K};
+  for (int i = 0; i < 2; ++i) {
+    g.in[i] = static_cast<const uint16_t*>(in[i]);
+    g.ld[i] = ld[i];
+    g.F[i] = int(features[i]);
+    g.ld_out[i] = (features[i] + 7) / 8 * 8;
+    g.out[i] = reinterpret_cast<uint16_t*>(room);
+    room += round16(p.rows * g.ld_out[i] * 2);
+  }
+  static PerContext<bool> attr;
+  bool ok = false;
+  if (!attr.get(ctx, &ok, [&](bool* v) {
+        *v = cudaFuncSetAttribute(lora_order_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  32 * MMA_MAX_GROUPS * 4) == cudaSuccess;
+        if (!*v) cudaGetLastError();
+        return *v;
+      }))
+    return MMA_ERR_LAUNCH;
+  lora_order_kernel<<<1, 1024, size_t(32 * g.total * 4), ctx.stream>>>(g);
+  lora_gather_kernel<<<unsigned(std::min<int64_t>(p.rows, ctx.num_sms * 8)), 256, 0,
+                       ctx.stream>>>(g);
+  a.to = g.to;
+  p.DY = g.out[0];
+  p.X = g.out[1];
+  p.lddy = g.ld_out[0];
+  p.ldx = g.ld_out[1];
+  p.offsets = g.starts;
+  p.adapters = nullptr;
+  p.requests = p.adapters_total;
+  return cudaGetLastError() == cudaSuccess ? MMA_OK : MMA_ERR_LAUNCH;
+}
+
+}  // namespace
+
+int64_t lora_wgrad_workspace_bytes(bool bf16, int d_type, int64_t T, int64_t N, int64_t K,
+                                   int64_t rank, int64_t requests, int64_t total) {
+  if (T == 0) return 0;
+  if (gathers(T, rank, requests, total))
+    return gather_ints(T, requests, total) + round16(T * ((N + 7) / 8 * 8) * 2) +
+           round16(T * ((K + 7) / 8 * 8) * 2) +
+           lora_wgrad_workspace_bytes(bf16, d_type, T, N, K, rank, total, total);
+  const int64_t per = rows_per_piece(T, N, K, rank);
+  const int64_t part = ((T + per - 1) / per + requests + 1) * rank * (N + K) * 4;
+  return round16(part) + 2 * lora_parts(bf16, d_type) * T * ((rank + 7) / 8 * 8) * 2;
+}
+
+mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& p, void* workspace) {
   WgradArgs a = {};
+  LoraWgradProblem g = p;
+  uint8_t* room = static_cast<uint8_t*>(workspace);
+  if (p.rows > 0 && gathers(p.rows, p.rank, p.requests, p.adapters_total)) {
+    const mma_status_t st = gather(ctx, g, a, room);
+    if (st != MMA_OK) return st;
+  } else if (p.requests > MMA_MAX_GROUPS) {
+    if (p.rows > 0) return MMA_ERR_UNSUPPORTED;
+    g.requests = 0;  // (no rows, so none with an adapter)
+  }
   a.side[0] = {int(g.N), g.S, g.lds, g.DB, g.lddb, g.stride_db, false};
   a.side[1] = {int(g.K), g.U, g.ldu, g.DA, g.ldda, g.stride_da, true};
   a.tiles0 = int((g.N + kTile - 1) / kTile);
@@ -1061,9 +1330,8 @@ mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& g, void* 
   a.ld16 = (a.rank + 7) / 8 * 8;
   a.accumulate = g.accumulate;
   const int64_t pieces = (g.rows + a.per - 1) / a.per + g.requests + 1;
-  a.part = static_cast<float*>(workspace);
-  a.halves = reinterpret_cast<uint16_t*>(
-      static_cast<uint8_t*>(workspace) + (pieces * g.rank * (g.N + g.K) * 4 + 15) / 16 * 16);
+  a.part = reinterpret_cast<float*>(room);
+  a.halves = reinterpret_cast<uint16_t*>(room + round16(pieces * g.rank * (g.N + g.K) * 4));
   a.status = ctx.status;
   return by_rank(g.rank, [&](auto r) {
     constexpr int RP = decltype(r)::value;

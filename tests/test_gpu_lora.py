@@ -135,7 +135,9 @@ def random_lengths(seed, count, most):
     ([1], 256, 512, 16), ([1, 1, 1], 200, 264, 8), ([5, 0, 7, 1], 136, 72, 1), ([1] * 32, 1000, 1024, 16),
     ([1] * 33, 264, 520, 24), ([64], 512, 4096, 64), ([1] * 64, 4104, 256, 7), ([3] * 40, 520, 136, 65),
     ([128], 130, 1000, 128), ([129], 256, 300, 16), ([200, 1, 1, 1, 30, 9, 8, 7], 776, 512, 32),
-    ([700, 300], 1100, 264, 128), ([1] * 300, 264, 264, 16), ([9] * 90, 300, 520, 40)])
+    ([700, 300], 1100, 264, 128), ([1] * 300, 264, 264, 16), ([9] * 90, 300, 520, 40),
+    ([1] * 1024, 136, 264, 16), ([1] * 1025, 264, 136, 20), ([0] * 1500 + [3, 0, 40], 264, 264, 16),
+    (([1, 0, 2] * 50 + [90] + [0] * 1000) * 4 + [1, 30], 300, 200, 33)])
 def test_product(lengths, n, k, r, kind, out, row):
     rng = random.Random(n + k)
     total = max(1, min(len(lengths), 11))
@@ -206,6 +208,34 @@ def test_no_k(lengths, row):
     assert st == 0 and torch.equal(d, c) and not s[:, :r].any()
 
 
+def test_most_requests():
+    """As many as the call takes, most of them empty, and offsets that go back."""
+    lengths = [0] * 65536
+    for i in range(0, 65536, 701):
+        lengths[i] = 1 + i % 5
+    lengths[30000], lengths[65535] = 70, 2
+    adapters = [(i // 3) % 8 - 1 for i in range(65536)]
+    c = Case(lengths, 200, 136, 16, adapters, 7, "bf16", seed=2, gap=(3, 9))
+    want, s = c.check("f32")
+    dy, u = rows16(rnd(5, c.t, 200), T["bf16"]), rnd(7, c.t, 16).float().cuda()
+    g = mma.gemm_lora_wgrad(dy, c.x, s, u, c.offsets, c.adapters, adapters_total=7)
+    a64, b64, ma, mb = wgrad_want(c, dy, s, u)
+    for got, ref, mag in zip(g, (a64, b64), (ma, mb)):
+        tol = mag * (SUM + U["bf16"] ** 3) + 2.0 ** -20 * STEP["bf16"]
+        assert bool(((host(got) - ref).abs() <= (ref.abs() + tol) * U["f32"] + tol + STEP["f32"]).all())
+    good = c.offsets.clone()
+    later = good.clone()
+    later[40000:40010] -= 50  # raised to the one before
+    later[0] = -3
+    c.offsets = later
+    low = torch.cummax(later.clamp(0, c.t), 0)[0]
+    got, _ = c.run("f32")
+    c.offsets = low
+    assert torch.equal(got, c.run("f32")[0])
+    h = [mma.gemm_lora_wgrad(dy, c.x, s, u, o, c.adapters, adapters_total=7) for o in (later, low)]
+    assert torch.equal(h[0][0], h[1][0]) and torch.equal(h[0][1], h[1][1])
+
+
 def test_offsets_out_of_range_and_order():
     """Clamped, and decreasing ones raised to the one before, as in grouped products."""
     good = Case([10, 0, 30, 20], 136, 128, 16, [0, 1, 2, 3], 4, seed=3)
@@ -266,7 +296,8 @@ def wgrad_want(c, dy, s, u):
 @pytest.mark.parametrize("kind,out", [("bf16", "f32"), ("bf16", "bf16"), ("f16", "f32"), ("f16", "f16")])
 @pytest.mark.parametrize("lengths,n,k,r", [
     ([1], 256, 512, 16), ([5, 0, 7, 1], 136, 72, 1), ([1] * 33, 264, 520, 24), ([700, 300], 1100, 264, 128),
-    ([64, 65, 63], 200, 136, 64), ([2000], 128, 128, 8), ([300] * 9, 520, 392, 40), ([3] * 200, 144, 130, 12)])
+    ([64, 65, 63], 200, 136, 64), ([2000], 128, 128, 8), ([300] * 9, 520, 392, 40), ([3] * 200, 144, 130, 12),
+    ([1] * 1100, 136, 200, 16), ([2, 1] * 40 + [90], 264, 130, 65), (([1, 0, 2] * 50 + [90] + [0] * 1000) * 4 + [1, 30], 300, 200, 33)])
 def test_adapters_gradient(lengths, n, k, r, kind, out):
     rng = random.Random(n * k)
     total = max(1, min(len(lengths), 7))

@@ -35,7 +35,7 @@ def product(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(ti=F32), UNSUP), (dict(td=F16), UNSUP), (dict(T=-1), INVALID), (dict(rank=-1), INVALID),
-    (dict(rank=129, lds=136, ldb=136), UNSUP), (dict(requests=-1), INVALID), (dict(requests=1025), UNSUP),
+    (dict(rank=129, lds=136, ldb=136), UNSUP), (dict(requests=-1), INVALID), (dict(requests=65537), UNSUP),
     (dict(total=-1), INVALID), (dict(total=65536), UNSUP), (dict(layout=2), INVALID), (dict(off=0), INVALID),
     (dict(off=P + 2), MISAL), (dict(of=P + 1), MISAL), (dict(sc=P + 2), MISAL), (dict(X=0), INVALID),
     (dict(ldx=120), INVALID), (dict(ldx=132), MISAL), (dict(X=P + 2), MISAL), (dict(W=0), INVALID),
@@ -66,6 +66,7 @@ def wgrad(**kw):
     (dict(dA=0), INVALID), (dict(dB=0), INVALID), (dict(ldda=64), INVALID), (dict(sda=100), INVALID),
     (dict(lddb=8), INVALID), (dict(dB=Q + 2), MISAL), (dict(ws=0), INVALID), (dict(bytes=1000), INVALID),
     (dict(ws=R + 4), MISAL), (dict(rank=0), OK), (dict(total=0), OK),
+    (dict(requests=65537), UNSUP), (dict(requests=1025, total=1025, bytes=1 << 40), UNSUP), (dict(requests=1025, bytes=1 << 17), INVALID),
 ])
 def test_wgrad(kw, code):
     assert wgrad(**kw) == code
@@ -75,9 +76,14 @@ def test_workspaces():
     f, g = binding.load().mma_gemm_lora_workspace, binding.load().mma_gemm_lora_wgrad_workspace
     assert f(BF16, BF16, 100, 30, 16, 3) == 12000 and f(BF16, F32, 200, 32, 17, 3) == 21 * 32 * 4 + 200 * 24 * 6
     assert f(F16, F32, 200, 32, 17, 3) == 21 * 32 * 4 + 200 * 24 * 4 and f(BF16, BF16, 10, 8, 0, 1) == 0
-    assert g(BF16, F32, 0, 8, 8, 8, 3) == 0 and g(BF16, F32, 1, 1, 1, 129, 1) == 0
-    assert g(BF16, F32, 100, 256, 128, 20, 5) == 7 * 20 * 384 * 4 + 2 * 3 * 100 * 24 * 2
-    assert g(F16, F16, 100, 256, 128, 20, 5) == 7 * 20 * 384 * 4 + 2 * 100 * 24 * 2
+    assert g(BF16, F32, 0, 8, 8, 8, 3, 3) == 0 and g(BF16, F32, 1, 1, 1, 129, 1, 1) == 0
+    assert g(BF16, F32, 100, 256, 128, 20, 5, 5) == 7 * 20 * 384 * 4 + 2 * 3 * 100 * 24 * 2
+    assert g(F16, F16, 100, 256, 128, 20, 5, 5) == 7 * 20 * 384 * 4 + 2 * 100 * 24 * 2
+    # rows in the order of their adapters: where that takes less, and with many requests
+    few = g(F16, F16, 100, 256, 128, 20, 3, 3)
+    assert g(F16, F16, 100, 256, 128, 20, 8, 3) == 10 * 20 * 384 * 4 + 2 * 100 * 24 * 2
+    assert g(F16, F16, 100, 256, 128, 20, 9, 3) == few + (2 * 9 + 3 + 2 + 100 + 1) * 4 + 100 * 384 * 2
+    assert f(BF16, BF16, 2000, 32, 16, 1025) == 2000 * 32 * 4
 
 
 def test_binding():
