@@ -404,3 +404,33 @@ def test_streams_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(out, step()))
+
+
+@pytest.mark.parametrize("lengths", [[1] * 1100 + [30], [1, 2] * 60])
+def test_many_requests_captured_and_on_a_stream(lengths):
+    """Rows in the order of their adapters: in a graph whose inputs change, and on a stream."""
+    rng = random.Random(1)
+    adapters = [rng.randint(-1, 5) for _ in lengths]
+    c = Case(lengths, 136, 264, 48, adapters, 5, "bf16", seed=21)
+    dy, u = rows16(rnd(5, c.t, 136), T["bf16"]), rnd(7, c.t, 48).float().cuda()
+
+    def both():
+        d, s = c.run("bf16")
+        return d, s, *mma.gemm_lora_wgrad(dy, c.x, s, u, c.offsets, c.adapters, adapters_total=5)
+
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both()
+    for seed in (31, 32):
+        c.x.copy_(rnd(seed, c.t, 264).to(T["bf16"]))
+        c.adapters.copy_(ints([rng.randint(-1, 5) for _ in lengths]))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, both()))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    d, s = c.run("bf16", stream=side)
+    g = mma.gemm_lora_wgrad(dy, c.x, s, u, c.offsets, c.adapters, adapters_total=5, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, (d, s, *g)))
