@@ -281,7 +281,8 @@ __device__ __forceinline__ bool ring_run(Ring& r, uint8_t* smem, int steps, int 
 // dropped; sums past the rank and k's past K are zeros.
 //
 // A few rows' share of the result, s B, is made here as well: of every row up to
-// kLoraEveryRow, else of the requests of fewer than kLoraRows.  Every CTA of the
+// kLoraEveryRow or with more requests than the product lists (lora_every), else of the
+// requests of fewer than kLoraRows.  Every CTA of the
 // cluster adds all of the piece's sums up, and a thread has one of 256 columns of B, which
 // come through a ring of their own (2100 rows, 60 of them single tokens, 4096 x 4096, rank
 // 32: 72 us with the product, 76 with plain loads of B; the kernel itself some 23).
