@@ -627,7 +627,8 @@ mma_status_t shrink(const Ctx& ctx, const LoraProblem& g, const LoraLow& low) {
   const int64_t pieces = (g.rows + BM - 1) / BM + g.requests + 1;
   const int64_t steps = (g.K + L::KS - 1) / L::KS;
   // As many CTAs per piece as there is room for at once (with few rows twice per SM,
-  // beside the shared product), each with two stages at least.
+  // beside the shared product; of rank 32 three, though four fit: 200 single tokens, 4096 x
+  // 4096, 43 us, 46), each with two stages at least.
   const int per_sm = EVERY ? 2 : std::min(BM == 16 ? 4 : 2, 224 * 1024 / (L::SMEM + 10 * 1024));
   int parts = 1;
   while (parts < kMostParts && pieces * parts * 2 <= int64_t(per_sm) * ctx.num_sms && steps >= parts * 4)
