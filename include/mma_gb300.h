@@ -743,7 +743,9 @@ mma_status_t mma_gemm_lora(int type_in, int type_d, int64_t T, int64_t N,
  * with S of the forward call (T x lds) and U of the call for the input's gradient
  * (T x ldu), both FP32, any lds and ldu, scales included.
  * type_d  : of DA and DB, type_in or MMA_F32.  An FP32 result takes S and U as
- *           sums of two FP16 or three BF16 numbers, a 16-bit one as one.
+ *           sums of two FP16 or three BF16 numbers, a 16-bit one as one.  S and U may
+ *           be of any size: FP16 ones are scaled by a power of two for each column of
+ *           at most 64 rows of a request, and keep what is above 2^-38 of its largest.
  * accumulate : nonzero -- added to DA and DB; else an adapter without rows gets
  *           zeros.
  * Sums are FP32, in a fixed order, through `workspace`: 16-byte aligned device

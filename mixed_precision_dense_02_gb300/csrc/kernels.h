@@ -272,8 +272,9 @@ constexpr bool lora_own_places(int64_t rows, int64_t requests) {
   return lora_every(rows, requests) || rows <= requests * (kLoraRows - 1);
 }
 // Numbers of 16 bits that stand for an FP32 sum in a product: for an FP32 result as
-// many as hold its 24 bits (BF16 three of 8, FP16 two of 11, which leave 2^-22 of
-// it), for a 16-bit one, whose own rounding is as large, one.
+// many as hold its 24 bits (BF16 three of 8, FP16 two of 11, which leave 2^-22 of it
+// where FP16's smallest step does not count), for a 16-bit one, whose own rounding is as
+// large, one.
 constexpr int lora_parts(bool bf16, int d_type) {
   return d_type != MMA_F32 ? 1 : bf16 ? 3 : 2;
 }

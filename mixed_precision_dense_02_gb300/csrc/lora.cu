@@ -180,18 +180,37 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
     mma_f16_16816(d, a, b);
 }
 
-// 16 bits of v; v becomes what they leave of it.
+// 16 bits of v; v becomes what they leave of it, nothing of NaN and infinities.
 template <bool BF16>
 __device__ __forceinline__ uint16_t take_half(float& v) {
+  uint16_t bits;
+  float f;
   if constexpr (BF16) {
-    const __nv_bfloat16 h = __float2bfloat16_rn(v);
-    v -= __bfloat162float(h);
-    return __bfloat16_as_ushort(h);
+    __nv_bfloat16 h = __float2bfloat16_rn(v);
+    f = __bfloat162float(h);
+    if (fabsf(f) == INFINITY && fabsf(v) < INFINITY) {  // (rounded up from a number)
+      h = __ushort_as_bfloat16(v < 0.f ? 0xFF7F : 0x7F7F);
+      f = __bfloat162float(h);
+    }
+    bits = __bfloat16_as_ushort(h);
   } else {
     const __half h = __float2half_rn(v);
-    v -= __half2float(h);
-    return __half_as_ushort(h);
+    f = __half2float(h);
+    bits = __half_as_ushort(h);
   }
+  v = fabsf(f) < INFINITY ? v - f : 0.f;
+  return bits;
+}
+
+// The exponent, as that of an FP32 number, of the power of two that brings `most`, the
+// largest magnitude of some sums, to 2^13 or above and below 2^14, and its inverse: FP16
+// numbers have steps of 2^-24 at the least.  Both are normal numbers.
+__device__ __forceinline__ int up_exponent(float most) {
+  return min(max(267 - (__float_as_int(most) >> 23), 1), 253);
+}
+__device__ __forceinline__ float up_of(int exponent) { return __int_as_float(exponent << 23); }
+__device__ __forceinline__ float down_of(int exponent) {
+  return __int_as_float((254 - exponent) << 23);
 }
 
 // What the threads of a block share to wait for loads.
@@ -680,9 +699,11 @@ struct WgradArgs {
   const int *offsets, *adapters;
   int d_type, parts, ld16;
   bool accumulate;
-  const int* to;    // gathered rows: each row's place, or -1; else null
-  float* part;      // [pieces][rank][features of both sides]
+  const int* from;   // gathered rows: the row at each place; else null
+  float* part;       // [pieces - 2][rank][features of both sides]
   uint16_t* halves;  // [2][parts][T][ld16]
+  float* down;       // (FP16) [2][chunks][RP]: what a chunk's sums are scaled back by
+  int chunks;
   unsigned* status;
 };
 
@@ -698,7 +719,8 @@ struct Wgrad {
   static constexpr int RB = RP < 64 ? RP : 64;  // sums per box
   static constexpr int M_BYTES = kStageRows * kTile * 2;
   static constexpr int PART = kStageRows * RP * 2;  // one part of the sums
-  static constexpr int stage(int parts) { return M_BYTES + parts * PART; }
+  // (a KB behind them for the sums' scales)
+  static constexpr int stage(int parts) { return M_BYTES + parts * PART + 1024; }
   // two CTAs per SM if that leaves them two stages each
   static constexpr int per_sm(int parts) { return 2 * stage(parts) <= 102 * 1024 ? 2 : 1; }
   static constexpr int stages(int parts) {
@@ -719,7 +741,7 @@ struct Gather {
   int* bound;   // [requests + 1]: the offsets, clamped and in order
   int* first;   // [requests]: the place of a request's first row, or -1
   int* starts;  // [total + 1]: the adapters' rows
-  int* to;      // [T]: each row's place, or -1
+  int* from;    // [T]: the row at each place
   const uint16_t* in[2];  // dy, x
   int64_t ld[2], ld_out[2];
   int F[2];
@@ -825,8 +847,8 @@ __global__ void __launch_bounds__(256) lora_gather_kernel(const Gather g) {
     int place = -1;
     if (t >= g.bound[lo] && t < g.bound[lo + 1] && g.first[lo] >= 0)
       place = g.first[lo] + t - g.bound[lo];
-    if (threadIdx.x == 0) g.to[t] = place;
     if (place < 0) continue;
+    if (threadIdx.x == 0) g.from[place] = t;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint4* in = reinterpret_cast<const uint4*>(g.in[i] + t * g.ld[i]);
@@ -837,42 +859,94 @@ __global__ void __launch_bounds__(256) lora_gather_kernel(const Gather g) {
   }
 }
 
-// Both sides' sums in parts of 16 bits.
-template <bool BF16>
+// Both sides' sums in parts of 16 bits: BF16, whose range is FP32's.
+template <int RP>
+__device__ __forceinline__ void split_rows(const WgradArgs& a, const Side& side, uint16_t* out) {
+  const int64_t all = int64_t(a.T) * a.ld16;
+  constexpr int kWidth = RP < 32 ? RP : 32;  // lanes for a row
+  constexpr int kRows = kThreads / kWidth;
+  // (the places of gathered rows end with the last adapter's)
+  const int last = a.from ? __ldg(a.offsets + a.requests) : a.T;
+  for (int64_t place = int64_t(blockIdx.x) * kRows + threadIdx.x / kWidth; place < last;
+       place += int64_t(gridDim.x) * kRows) {
+    const int64_t row = a.from ? a.from[place] : place;
+    for (int n = threadIdx.x % kWidth; n < a.ld16; n += kWidth) {
+      float v = n < a.rank ? side.low[row * side.ldl + n] : 0.f;
+      for (int part = 0; part < a.parts; ++part)
+        out[part * all + place * a.ld16 + n] = take_half<true>(v);
+    }
+  }
+}
+
+// FP16, with the sums' scales.  A block has a chunk, which is a stage of the kernel below:
+// 64 rows of a piece, counted from its first, and numbered by that row's block of 64 and
+// the piece's request (their sum, as the pieces).  Each column of it has a power of two
+// of its own, so that what stands beside small sums, other requests' or other columns',
+// does not take their bits: two numbers leave 2^-22 of a sum, and 2^-38 of the largest
+// of its column in the chunk.
+template <int RP>
+__device__ __forceinline__ void split_chunk(const WgradArgs& a, const Side& side, uint16_t* out) {
+  constexpr int kGroups = kThreads / RP, kEach = kStageRows / kGroups;
+  __shared__ OnePiece one;
+  __shared__ float most[kThreads];
+  const int request = find_piece(one, a.offsets, a.adapters, a.total, a.requests, a.T,
+                                 kStageRows, blockIdx.x).request;
+  // (a piece that starts with its request, or with a block of `per` rows)
+  const int64_t block = int64_t(blockIdx.x - request) * kStageRows;
+  const int64_t piece = block / a.per * a.per;
+  const int64_t from = block + (one.first > piece ? one.first % kStageRows : 0);
+  const int to = int(min(min(from + kStageRows, piece + a.per), int64_t(one.next)));
+  if (one.who < 0 || from >= to) return;
+  const int n = threadIdx.x % RP, first = int(from) + threadIdx.x / RP;
+  float v[kEach], m = 0.f;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int place = first + i * kGroups;
+    v[i] = 0.f;
+    if (place < to && n < a.rank)
+      v[i] = side.low[int64_t(a.from ? a.from[place] : place) * side.ldl + n];
+    const float size = fabsf(v[i]);
+    m = fmaxf(m, size < INFINITY ? size : 0.f);
+  }
+  most[threadIdx.x] = m;
+  __syncthreads();
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) m = fmaxf(m, most[g * RP + n]);
+  const int exponent = up_exponent(m);
+  const float up = up_of(exponent);
+  if (threadIdx.x < RP)
+    a.down[(int64_t(blockIdx.y) * a.chunks + blockIdx.x) * RP + n] = down_of(exponent);
+  if (n >= a.ld16) return;
+  const int64_t all = int64_t(a.T) * a.ld16;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int place = first + i * kGroups;
+    if (place >= to) break;
+    float left = v[i] * up;
+    for (int part = 0; part < a.parts; ++part)
+      out[part * all + int64_t(place) * a.ld16 + n] = take_half<false>(left);
+  }
+}
+
+template <bool BF16, int RP>
 __global__ void __launch_bounds__(kThreads)
     lora_halves_kernel(const WgradArgs a) {
   grid_dependents_start();
   const Side& side = a.side[blockIdx.y];
   if (side.F == 0) return;
-  const int64_t all = int64_t(a.T) * a.ld16;
-  uint16_t* const out = a.halves + blockIdx.y * a.parts * all;
-  // 8, 16 or 32 lanes for a row
-  const int width = a.ld16 <= 8 ? 8 : a.ld16 <= 16 ? 16 : 32;
-  const int per = kThreads / width;
-  for (int64_t t = int64_t(blockIdx.x) * per + threadIdx.x / width; t < a.T;
-       t += int64_t(gridDim.x) * per) {
-    const int64_t row = a.to ? a.to[t] : t;
-    if (row < 0) continue;
-    for (int n = threadIdx.x % width; n < a.ld16; n += width) {
-      float v = n < a.rank ? side.low[t * side.ldl + n] : 0.f;
-      for (int part = 0; part < a.parts; ++part)
-        out[part * all + row * a.ld16 + n] = take_half<BF16>(v);
-    }
-  }
-}
-
-template <bool FIRST, class T>
-__device__ __forceinline__ T& select(T& a, T& b) {
-  if constexpr (FIRST) return a;
-  return b;
+  uint16_t* const out = a.halves + int64_t(blockIdx.y) * a.parts * a.T * a.ld16;
+  if constexpr (BF16)
+    split_rows<RP>(a, side, out);
+  else
+    split_chunk<RP>(a, side, out);
 }
 
 // A piece's share of 128 features: G[f][n] = sum over its rows M[t][f] * low[t][n] on
 // the tensor cores, FP32.  As many CTAs as run at once take the shares in turn, the
 // features of a piece side by side, through one ring of rows and sums that runs on from
 // share to share (a CTA for each share: 51 us of 8192 x (8192 + 4096), rank 16, so 44).
-// The tensor cores' FP32 sums drop low bits on the way, so that for an FP32 gradient
-// (PARTS > 1) they run over a stage's 64 rows and are added to others to nearest (8192
+// The tensor cores' FP32 sums drop low bits on the way, so that they run over a stage's
+// rows, 64 of a request at most, and are added to others to nearest, scaled back (8192
 // rows: 3.9e-6 off without, so 4e-7).
 // What stands in a share's last stage behind the piece is another request's and becomes
 // zeros in both (in one alone, an infinity in the other would leave NaN).
@@ -894,9 +968,9 @@ __global__ void __launch_bounds__(kThreads + 32)
   load_requests(req, a.offsets, a.adapters, a.total, a.requests, a.T);
   grid_dependency_wait();  // (the halves)
   struct Share {
-    int from, rows, second, f0;
+    int from, to, request, second, f0;
   };
-  // share i, the shares of a piece in a row; without rows or an adapter: rows 0
+  // share i, the shares of a piece in a row; without rows or an adapter: from == to
   auto share_of = [&](int i) {
     const int u = i / tiles, tile = i - u * tiles;
     int j = 0;
@@ -908,7 +982,7 @@ __global__ void __launch_bounds__(kThreads + 32)
     const int to = int(min(int64_t(u - j + 1) * a.per, int64_t(req.bound[j + 1])));
     const bool none = adapter_of(req, j, a.requests) < 0 || from >= to;
     const int second = tile >= a.tiles0;
-    return Share{int(from), none ? 0 : int(to - from), second,
+    return Share{none ? to : int(from), to, j, second,
                  (tile - (second ? a.tiles0 : 0)) * kTile};
   };
   const int shares = pieces * tiles;
@@ -926,22 +1000,26 @@ __global__ void __launch_bounds__(kThreads + 32)
       int issued = 0;
       for (int i = blockIdx.x; i < shares && ok; i += gridDim.x) {
         const Share w = share_of(i);
-        for (int t = 0; t < w.rows; t += kStageRows) {
+        for (int t = w.from; t < w.to; t += kStageRows) {
           ok = mbar_wait(&ring.empty[s], phase ^ 1u, &ring.abort_flag, a.status);
           if (!ok) break;
           uint8_t* ms = smem + s * stage_bytes;
           uint64_t* bar = &ring.full[s];
-          mbar_arrive_expect_tx(bar, uint32_t(stage_bytes));
+          mbar_arrive_expect_tx(
+              bar, uint32_t(L::M_BYTES + PARTS * L::PART + (BF16 ? 0 : RP * 4)));
 #pragma unroll
           for (int b = 0; b < kTile / 64; ++b)
-            tma_load_3d(&maps.m[w.second], bar, ms + b * kStageRows * 128, w.f0 + b * 64,
-                        w.from + t, 0);
+            tma_load_3d(&maps.m[w.second], bar, ms + b * kStageRows * 128, w.f0 + b * 64, t, 0);
           for (int part = 0; part < PARTS; ++part)
 #pragma unroll
             for (int b = 0; b < RP / RB; ++b)
               tma_load_3d(&maps.low[w.second], bar,
                           ms + L::M_BYTES + part * L::PART + b * kStageRows * RB * 2, b * RB,
-                          w.from + t, part);
+                          t, part);
+          if constexpr (!BF16)
+            bulk_load(ms + L::M_BYTES + PARTS * L::PART,
+                      a.down + (int64_t(w.second) * a.chunks + t / kStageRows + w.request) * RP,
+                      RP * 4, bar);
           ++issued;
           next();
         }
@@ -966,16 +1044,16 @@ __global__ void __launch_bounds__(kThreads + 32)
   uint32_t cleared = 0;
   for (int i = blockIdx.x; i < shares && ok; i += gridDim.x) {
     const Share w = share_of(i);
-    if (w.rows == 0) continue;
+    if (w.from >= w.to) continue;
     float acc[RP / 8][4];
 #pragma unroll
     for (int n = 0; n < RP / 8; ++n)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
-    for (int t = 0; t < w.rows; t += kStageRows, next()) {
+    for (int t = w.from; t < w.to; t += kStageRows, next()) {
       uint8_t* stage = smem + s * stage_bytes;
       ok = mbar_wait(&ring.full[s], phase, &ring.abort_flag, a.status);
-      const int valid = w.rows - t;
+      const int valid = w.to - t;
       if (valid < kStageRows) {
         const uint4 zero = make_uint4(0, 0, 0, 0);
         for (int b = 0; b < kTile / 64; ++b)
@@ -996,41 +1074,41 @@ __global__ void __launch_bounds__(kThreads + 32)
       if (!ok) break;
       const uint32_t ms = smem_u32(stage) + f_at;
       const uint32_t ls = smem_u32(stage) + L::M_BYTES;
-      float part_acc[RP / 8][4];
-      if constexpr (PARTS > 1) {
+      [[maybe_unused]] const float* const down =
+          reinterpret_cast<const float*>(stage + L::M_BYTES + PARTS * L::PART);
+      uint32_t f[kStageRows / 16][4];
 #pragma unroll
-        for (int n = 0; n < RP / 8; ++n)
+      for (int k = 0; k < kStageRows / 16; ++k) ldmatrix_x4_trans(f[k], ms + k * 16 * 128);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) part_acc[n][j] = 0.f;
-      }
-      auto& sum = select<(PARTS > 1)>(part_acc, acc);
-#pragma unroll
-      for (int k = 0; k < kStageRows; k += 16) {
-        uint32_t f[4];
-        ldmatrix_x4_trans(f, ms + k * 128);
+      for (int n = 0; n < RP / 16; ++n) {
+        float sum[2][4] = {};
 #pragma unroll
         for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-          for (int n = 0; n < RP / 16; ++n) {
+          for (int k = 0; k < kStageRows / 16; ++k) {
             uint32_t b[4];
             ldmatrix_x4_trans(b, ls + part * L::PART + n * 16 / RB * kStageRows * RB * 2 +
-                                     k * RB * 2 + low_at[n * 16 % RB / 16]);
-            mma16<BF16>(sum[2 * n], f, b[0], b[1]);
-            mma16<BF16>(sum[2 * n + 1], f, b[2], b[3]);
+                                     k * 16 * RB * 2 + low_at[n * 16 % RB / 16]);
+            mma16<BF16>(sum[0], f[k], b[0], b[1]);
+            mma16<BF16>(sum[1], f[k], b[2], b[3]);
           }
-      }
-      if constexpr (PARTS > 1) {
 #pragma unroll
-        for (int n = 0; n < RP / 8; ++n)
+        for (int x = 0; x < 2; ++x) {
+          float2 d = make_float2(1.f, 1.f);
+          if constexpr (!BF16)
+            d = *reinterpret_cast<const float2*>(down + n * 16 + x * 8 + 2 * (lane & 3));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[n][j] += part_acc[n][j];
+          for (int j = 0; j < 4; ++j)
+            acc[2 * n + x][j] = BF16 ? acc[2 * n + x][j] + sum[x][j]
+                                     : fmaf(sum[x][j], j & 1 ? d.y : d.x, acc[2 * n + x][j]);
+        }
       }
       __syncwarp();
       mbar_arrive_if(&ring.empty[s], lane == 0);
     }
     if (!ok) break;
     // (eight lanes: 32 consecutive bytes of four of the sums' rows)
-    float* out = a.part + int64_t(i / tiles) * a.rank * features +
+    float* out = a.part + int64_t(i / tiles - 1) * a.rank * features +
                  (w.second ? a.side[0].F : 0) + w.f0;
     const int F = a.side[w.second].F - w.f0;
 #pragma unroll
@@ -1102,7 +1180,7 @@ __global__ void __launch_bounds__(kThreads)
   float v[kSums] = {};
 #pragma unroll 2
   for (int i = 0; i < found; ++i) {
-    const float* p = part + int64_t(list[i]) * a.rank * features;
+    const float* p = part + int64_t(list[i] - 1) * a.rank * features;
     float w[kSums];
 #pragma unroll
     for (int x = 0; x < kSums; ++x) w[x] = x < many ? p[x * features] : 0.f;
@@ -1190,8 +1268,9 @@ mma_status_t wgrad(const Ctx& ctx, const LoraWgradProblem& g, const WgradArgs& a
                     a.parts > 1 ? all : a.ld16, L::RB, kStageRows, swizzle_of(L::RB * 2)))
         return MMA_ERR_LAUNCH;
     }
-    const int64_t blocks = std::min<int64_t>((all + kThreads - 1) / kThreads, ctx.num_sms * 8);
-    lora_halves_kernel<BF16><<<dim3(unsigned(blocks), 2), kThreads, 0, ctx.stream>>>(a);
+    const int64_t blocks =
+        BF16 ? std::min<int64_t>((all + kThreads - 1) / kThreads, ctx.num_sms * 8) : a.chunks;
+    lora_halves_kernel<BF16, RP><<<dim3(unsigned(blocks), 2), kThreads, 0, ctx.stream>>>(a);
     const int64_t pieces = (g.rows + a.per - 1) / a.per + g.requests + 1;
     const int64_t tiles = a.tiles0 + (g.K + kTile - 1) / kTile;
     if (pieces * tiles > INT32_MAX / 2) return MMA_ERR_UNSUPPORTED;
@@ -1246,6 +1325,28 @@ int64_t gather_ints(int64_t T, int64_t requests, int64_t total) {
   return round16((2 * requests + total + 2 + T) * 4);
 }
 
+// Where the shares, the sums' parts and their scales lie.  A piece's number is its block
+// and its request, counted from the one before the first: number 0 and the last are of no
+// request, so that two shares less are stored than there are pieces.  They are counted in
+// `bytes` all the same, and hold the scales where those fit.
+struct WgradSpace {
+  int64_t pieces, chunks, halves, down, bytes;
+};
+
+WgradSpace wgrad_space(bool bf16, int d_type, int64_t T, int64_t N, int64_t K, int64_t rank,
+                       int64_t requests) {
+  const int64_t per = rows_per_piece(T, N, K, rank), share = rank * (N + K) * 4;
+  const int64_t sums = 2 * lora_parts(bf16, d_type) * T * ((rank + 7) / 8 * 8) * 2;
+  const int64_t room = rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128;
+  WgradSpace s;
+  s.pieces = (T + per - 1) / per + requests + 1;
+  s.chunks = (T + kStageRows - 1) / kStageRows + requests + 1;
+  s.halves = round16(std::max<int64_t>(s.pieces - 2, 0) * share);  // (T 0: no pieces)
+  s.down = s.halves + round16(sums);
+  s.bytes = std::max(round16(s.pieces * share) + sums, s.down + (bf16 ? 0 : 2 * s.chunks * room * 4));
+  return s;
+}
+
 // The rows in the order of their adapters.
 mma_status_t gather(const Ctx& ctx, LoraWgradProblem& p, WgradArgs& a, uint8_t*& room) {
   Gather g = {};
@@ -1257,7 +1358,7 @@ mma_status_t gather(const Ctx& ctx, LoraWgradProblem& p, WgradArgs& a, uint8_t*&
   g.bound = reinterpret_cast<int*>(room);
   g.first = g.bound + g.requests + 1;
   g.starts = g.first + g.requests;
-  g.to = g.starts + g.total + 1;
+  g.from = g.starts + g.total + 1;
   room += gather_ints(p.rows, p.requests, p.adapters_total);
   const void* const in[2] = {p.DY, p.X};
   const int64_t ld[2] = {p.lddy, p.ldx}, features[2] = {p.N, p.K};
@@ -1281,7 +1382,7 @@ mma_status_t gather(const Ctx& ctx, LoraWgradProblem& p, WgradArgs& a, uint8_t*&
   lora_order_kernel<<<1, 1024, size_t(32 * g.total * 4), ctx.stream>>>(g);
   lora_gather_kernel<<<unsigned(std::min<int64_t>(p.rows, ctx.num_sms * 8)), 256, 0,
                        ctx.stream>>>(g);
-  a.to = g.to;
+  a.from = g.from;
   p.DY = g.out[0];
   p.X = g.out[1];
   p.lddy = g.ld_out[0];
@@ -1301,9 +1402,7 @@ int64_t lora_wgrad_workspace_bytes(bool bf16, int d_type, int64_t T, int64_t N, 
     return gather_ints(T, requests, total) + round16(T * ((N + 7) / 8 * 8) * 2) +
            round16(T * ((K + 7) / 8 * 8) * 2) +
            lora_wgrad_workspace_bytes(bf16, d_type, T, N, K, rank, total, total);
-  const int64_t per = rows_per_piece(T, N, K, rank);
-  const int64_t part = ((T + per - 1) / per + requests + 1) * rank * (N + K) * 4;
-  return round16(part) + 2 * lora_parts(bf16, d_type) * T * ((rank + 7) / 8 * 8) * 2;
+  return wgrad_space(bf16, d_type, T, N, K, rank, requests).bytes;
 }
 
 mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& p, void* workspace) {
@@ -1331,9 +1430,11 @@ mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& p, void* 
   a.parts = lora_parts(g.bf16, g.d_type);  // (1, or 3 of BF16 and 2 of FP16)
   a.ld16 = (a.rank + 7) / 8 * 8;
   a.accumulate = g.accumulate;
-  const int64_t pieces = (g.rows + a.per - 1) / a.per + g.requests + 1;
+  const WgradSpace space = wgrad_space(g.bf16, g.d_type, g.rows, g.N, g.K, g.rank, g.requests);
   a.part = reinterpret_cast<float*>(room);
-  a.halves = reinterpret_cast<uint16_t*>(room + round16(pieces * g.rank * (g.N + g.K) * 4));
+  a.halves = reinterpret_cast<uint16_t*>(room + space.halves);
+  a.down = reinterpret_cast<float*>(room + space.down);
+  a.chunks = int(space.chunks);
   a.status = ctx.status;
   return by_rank(g.rank, [&](auto r) {
     constexpr int RP = decltype(r)::value;
