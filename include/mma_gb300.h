@@ -714,8 +714,9 @@ mma_status_t mma_route_backward(int type, int64_t T, int64_t E, int64_t k,
  *           uses and nothing else may meanwhile.
  * With up to 128 rows or more than MMA_MAX_GROUPS requests, and for requests of fewer
  * than 8 rows, the product with B takes S as it is.  For the others S is rounded to
- * type_in (an FP32 D: to a sum of two FP16 or three BF16 numbers), whose range it has
- * to keep.  A NaN or infinity in one adapter or row stays with the rows of that
+ * type_in (an FP32 D: to a sum of two FP16 or three BF16 numbers); FP16 ones are scaled
+ * by a power of two for each row, whatever their size, and keep what is above 2^-38 of
+ * the row's largest.  A NaN or infinity in one adapter or row stays with the rows of that
  * adapter, or that row.
  */
 #define MMA_MAX_RANK 128

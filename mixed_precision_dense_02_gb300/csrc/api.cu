@@ -1112,8 +1112,6 @@ mma_status_t check_lora(int type_in, int type_d, int64_t T, int64_t N, int64_t K
   return rank > 0 && T > 0 ? check_words(offsets) : MMA_OK;
 }
 
-int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
-
 // The rows' sums: FP32, rows of at least `rank`.
 mma_status_t check_sums(const float* s, int64_t ld, int64_t rank) {
   if (s == nullptr || ld < rank) return MMA_ERR_INVALID_ARG;
@@ -1130,7 +1128,8 @@ LoraSpace lora_space(int type_in, int type_d, int64_t T, int64_t N, int64_t rank
   const bool every = lora_every(T, requests);
   const int64_t rows = lora_own_places(T, requests) ? T : requests * (kLoraRows - 1);
   const int64_t parts = every ? 0 : lora_parts(type_in == MMA_BF16, type_d);
-  return LoraSpace{(rows * N * 4 + 15) / 16 * 16, parts * T * round8(rank) * 2};
+  return LoraSpace{(rows * N * 4 + 15) / 16 * 16,
+                   parts * T * lora_ld16(type_in == MMA_BF16, rank) * 2};
 }
 
 }  // namespace
@@ -1217,7 +1216,8 @@ extern "C" mma_status_t mma_gemm_lora(
   const LoraSpace space = lora_space(type_in, type_d, T, N, rank, requests);
   const int parts = lora_every(T, requests) ? 0 : lora_parts(g.bf16, type_d);
   LoraLow low = {S, static_cast<uint8_t*>(workspace) + space.extra,
-                 static_cast<float*>(workspace), int(lds), int(round8(rank)), parts};
+                 static_cast<float*>(workspace), int(lds), int(lora_ld16(g.bf16, rank)),
+                 parts};
   if (rank > 0) MMA_CHECK(launch_lora_shrink(ctx, g, low));
   if (N == 0) return MMA_OK;
   // without them there is nothing to add

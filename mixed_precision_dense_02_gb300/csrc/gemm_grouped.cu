@@ -145,9 +145,12 @@ struct GroupedArgs {
   // adapters_total): none), whose `rank` sums per row are, in `parts` parts of 16
   // bits, behind tmD, and whose second matrix is behind tmZ.rows[0]; `extra` has
   // those of requests of fewer than kLoraRows rows (places: lora_own_places).
+  // `up`: the exponents of the rows' scales, ld_up apart (FP16), or null.
   const float* extra;
   const int* adapters;
   int adapters_total, rank, parts;
+  const uint16_t* up;
+  int ld_up;
 };
 
 template <bool KIND8, bool ROWS, bool SPLIT, int CL, int BN, int STAGES>
@@ -1046,14 +1049,25 @@ __global__ void __launch_bounds__(kThreads,
             for (int j = 0; j < CB; ++j) sum[i * CB + j] += __uint_as_float(r[j]);
           });
         if constexpr (LORA == kRequests) {
+          grid_dependency_wait();
+          // (lane l has the scales of column l of each block)
+          static_assert(LORA != kRequests || CB == 32);
+          float down[NB];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const int64_t q = min(t.q0 + column(b) + lane, a.rows_total - 1);
+            down[b] = a.up ? down_of(a.up[q * a.ld_up]) : 1.f;
+          }
           each_product(t, [&](int, int from, int to) {
             // (what other rows' sums with this adapter are does not matter)
             take([&](int b, const uint32_t (&r)[CB]) {
               const int first = t.q0 + column(b) - from;
 #pragma unroll
-              for (int j = 0; j < CB; ++j)
+              for (int j = 0; j < CB; ++j) {
+                const float d = __shfl_sync(0xffffffffu, down[b], j);
                 if (unsigned(first + j) < unsigned(to - from))
-                  sum[b * CB + j] += __uint_as_float(r[j]);
+                  sum[b * CB + j] = fmaf(__uint_as_float(r[j]), d, sum[b * CB + j]);
+              }
             });
           });
           // The rows of small requests: lane l has the place in `extra` of column l
@@ -1088,7 +1102,6 @@ __global__ void __launch_bounds__(kThreads,
             some = some || slot[b] >= 0;
           }
           if (__any_sync(0xffffffffu, some)) {
-            grid_dependency_wait();
             const float* e = a.extra + min(p, t.p1 - 1);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
@@ -1742,6 +1755,8 @@ mma_status_t launch_gemm_lora(const Ctx& ctx, const LoraProblem& g, const LoraLo
   a.adapters_total = int(g.adapters_total);
   a.rank = int(g.rank);
   a.parts = low->parts;
+  a.up = g.bf16 ? nullptr : static_cast<const uint16_t*>(low->f16) + g.rank;
+  a.ld_up = low->ld16;
   const LoraMaps m = {{g.B, g.ldb, g.N, g.adapters_total, g.stride_b},
                       {low->f16, low->ld16, g.rows, low->parts, int64_t(low->ld16) * g.rows}};
   if (g.row_major)

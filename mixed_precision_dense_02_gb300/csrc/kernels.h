@@ -259,7 +259,9 @@ struct LoraProblem {
 };
 // What its kernels hand on.  The rows' sums scale * (X A): in FP32 (ld32 a multiple
 // of 8, so that eight can be read from any eighth one) and, for more rows than
-// kLoraEveryRow, as `parts` matrices of 16 bits whose sum they are.  In `extra` what
+// kLoraEveryRow, as `parts` matrices of 16 bits whose sum they are, FP16 ones times a
+// power of two of the row's own (ptx.cuh), whose exponent stands behind the first
+// matrix's row.  In `extra` what
 // the adapters add, FP32 rows of N: with up to kLoraEveryRow rows, or more requests than
 // the shared product can list (MMA_MAX_GROUPS), for all of them,
 // else for those of requests of fewer than kLoraRows rows, at the row's own place or
@@ -278,6 +280,7 @@ constexpr bool lora_own_places(int64_t rows, int64_t requests) {
 constexpr int lora_parts(bool bf16, int d_type) {
   return d_type != MMA_F32 ? 1 : bf16 ? 3 : 2;
 }
+constexpr int64_t lora_ld16(bool bf16, int64_t rank) { return (rank + !bf16 + 7) / 8 * 8; }
 struct LoraLow {
   float* f32;
   void* f16;

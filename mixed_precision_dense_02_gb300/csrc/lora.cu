@@ -202,17 +202,6 @@ __device__ __forceinline__ uint16_t take_half(float& v) {
   return bits;
 }
 
-// The exponent, as that of an FP32 number, of the power of two that brings `most`, the
-// largest magnitude of some sums, to 2^13 or above and below 2^14, and its inverse: FP16
-// numbers have steps of 2^-24 at the least.  Both are normal numbers.
-__device__ __forceinline__ int up_exponent(float most) {
-  return min(max(267 - (__float_as_int(most) >> 23), 1), 253);
-}
-__device__ __forceinline__ float up_of(int exponent) { return __int_as_float(exponent << 23); }
-__device__ __forceinline__ float down_of(int exponent) {
-  return __int_as_float((254 - exponent) << 23);
-}
-
 // What the threads of a block share to wait for loads.
 struct Ring {
   uint64_t full[4], empty[4];
@@ -459,13 +448,7 @@ __global__ void __launch_bounds__(Shrink<BM, RP, EVERY>::THREADS, Shrink<BM, RP,
                 : int64_t(piece.request - 1) * (kLoraRows - 1) + t - first_of) * N;
   };
   auto put = [&](int row, int n, float v) {
-    const int64_t t = piece.from + row;
-    if (n >= rank) v = 0.f;
-    if (n < low.ld32) low.f32[t * low.ld32 + n] = v;
-    if (n < low.ld16) {
-      uint16_t* d = static_cast<uint16_t*>(low.f16) + t * low.ld16 + n;
-      for (int i = 0; i < low.parts; ++i) d[i * g.rows * low.ld16] = take_half<BF16>(v);
-    }
+    if (n < low.ld32) low.f32[(int64_t(piece.from) + row) * low.ld32 + n] = v;
   };
   if (who < 0) {
     for (int i = part * L::THREADS + threadIdx.x; i < rows * RP; i += parts * L::THREADS)
@@ -559,7 +542,7 @@ __global__ void __launch_bounds__(Shrink<BM, RP, EVERY>::THREADS, Shrink<BM, RP,
   if (parts > 1) cluster_sync();
   else __syncthreads();
   float* mine = sums + BM * RP;  // all CTAs' (the room of a warp's sums, done with)
-  const int share = (rows * RP + parts - 1) / parts;
+  const int share_rows = (rows + parts - 1) / parts, share = share_rows * RP;
   for (int i = add ? threadIdx.x : part * share + threadIdx.x;
        i < (add ? rows * RP : min((part + 1) * share, rows * RP)); i += L::THREADS) {
     float v = 0.f;
@@ -573,13 +556,43 @@ __global__ void __launch_bounds__(Shrink<BM, RP, EVERY>::THREADS, Shrink<BM, RP,
     } else {
       v = sums[i];
     }
-    v *= scale;
-    if (add) mine[i] = i % RP < rank ? v : 0.f;
+    v = i % RP < rank ? v * scale : 0.f;
+    mine[i] = v;
     if (ok && i / share == part) put(i / RP, i % RP, v);
   }
   if (parts > 1) cluster_sync();  // no CTA leaves while another reads its sums
-  if (!add || !ok || N == 0) return;
-  __syncthreads();
+  else __syncthreads();
+  if (!ok) return;
+  // The rows' sums in 16 bits, a warp for each; FP16 ones scaled by a power of two of
+  // the row's own, whose exponent stands behind the first of them.
+  if (!EVERY && low.parts > 0) {
+    for (int row = part * share_rows + warp; row < min((part + 1) * share_rows, rows);
+         row += L::THREADS / 32) {
+      float v[(RP + 31) / 32], m = 0.f;
+#pragma unroll
+      for (int x = 0; x < (RP + 31) / 32; ++x) {
+        v[x] = x * 32 + lane < rank ? mine[row * RP + x * 32 + lane] : 0.f;
+        const float size = fabsf(v[x]);
+        m = fmaxf(m, size < INFINITY ? size : 0.f);
+      }
+      uint16_t* d = static_cast<uint16_t*>(low.f16) + (int64_t(piece.from) + row) * low.ld16;
+      float up = 1.f;
+      if constexpr (!BF16) {
+        const int exponent =
+            up_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))));
+        up = up_of(exponent);
+        if (lane == 0) d[rank] = uint16_t(exponent);
+      }
+#pragma unroll
+      for (int x = 0; x < (RP + 31) / 32; ++x) {
+        if (x * 32 + lane >= rank) break;
+        float left = v[x] * up;
+        for (int i = 0; i < low.parts; ++i)
+          d[i * g.rows * low.ld16 + x * 32 + lane] = take_half<BF16>(left);
+      }
+    }
+  }
+  if (!add || N == 0) return;
   if constexpr (ROW) {
     if (L::PRODUCER && warp == kThreads / 32) return;
     for (int p0 = part * kThreads * kCols; p0 < N; p0 += parts * kThreads * kCols)

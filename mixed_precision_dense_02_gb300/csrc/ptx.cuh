@@ -715,6 +715,17 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t sad
       : "r"(saddr));
 }
 
+// FP32 sums as FP16 numbers, whose steps are 2^-24 at the least: scaled by a power of
+// two that brings `most`, the largest magnitude among some, to 2^13 or above and below
+// 2^14.  The exponent of that as an FP32 number, the power and its inverse, all normal.
+__device__ __forceinline__ int up_exponent(float most) {
+  return min(max(267 - (__float_as_int(most) >> 23), 1), 253);
+}
+__device__ __forceinline__ float up_of(int exponent) { return __int_as_float(exponent << 23); }
+__device__ __forceinline__ float down_of(int exponent) {
+  return __int_as_float((254 - exponent) << 23);
+}
+
 // A float in the shared memory of a CTA of the cluster (address from mapa_shared).
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
   float v;
