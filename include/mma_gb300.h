@@ -713,11 +713,11 @@ mma_status_t mma_route_backward(int type, int64_t T, int64_t E, int64_t k,
  *           type_d, T, N, rank, requests) bytes, which the call's work on `stream`
  *           uses and nothing else may meanwhile.
  * With up to 128 rows or more than MMA_MAX_GROUPS requests, and for requests of fewer
- * than 8 rows, the product with B takes S as it is.  For the others S is rounded to
- * type_in (an FP32 D: to a sum of two FP16 or three BF16 numbers); FP16 ones are scaled
+ * than 8 rows, the product with B takes S as it is.  For the others S is rounded to a sum
+ * of two numbers of type_in (BF16 and an FP32 D: three); FP16 ones are scaled
  * by a power of two for each row, whatever their size, and keep what is above 2^-38 of
  * the row's largest.  A NaN or infinity in one adapter or row stays with the rows of that
- * adapter, or that row.
+ * adapter, or that row, which may have either there.
  */
 #define MMA_MAX_RANK 128
 #define MMA_MAX_REQUESTS 65536
@@ -743,10 +743,10 @@ mma_status_t mma_gemm_lora(int type_in, int type_d, int64_t T, int64_t N,
  *
  * with S of the forward call (T x lds) and U of the call for the input's gradient
  * (T x ldu), both FP32, any lds and ldu, scales included.
- * type_d  : of DA and DB, type_in or MMA_F32.  An FP32 result takes S and U as
- *           sums of two FP16 or three BF16 numbers, a 16-bit one as one.  S and U may
- *           be of any size: FP16 ones are scaled by a power of two for each column of
- *           at most 64 rows of a request, and keep what is above 2^-38 of its largest.
+ * type_d  : of DA and DB, type_in or MMA_F32.  S and U are taken as sums of two
+ *           numbers of type_in (BF16 and an FP32 result: three).  They may be of any
+ *           size: FP16 ones are scaled by a power of two for each column of at most 64
+ *           rows of a request, and keep what is above 2^-38 of its largest.
  * accumulate : nonzero -- added to DA and DB; else an adapter without rows gets
  *           zeros.
  * Sums are FP32, in a fixed order, through `workspace`: 16-byte aligned device

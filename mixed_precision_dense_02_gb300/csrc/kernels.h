@@ -273,12 +273,14 @@ constexpr bool lora_every(int64_t rows, int64_t requests) {
 constexpr bool lora_own_places(int64_t rows, int64_t requests) {
   return lora_every(rows, requests) || rows <= requests * (kLoraRows - 1);
 }
-// Numbers of 16 bits that stand for an FP32 sum in a product: for an FP32 result as
-// many as hold its 24 bits (BF16 three of 8, FP16 two of 11, which leave 2^-22 of it
-// where FP16's smallest step does not count), for a 16-bit one, whose own rounding is as
-// large, one.
+// Numbers of 16 bits that stand for an FP32 sum in a product: two, which leave 2^-16 of it
+// (BF16) or 2^-22 (FP16), and three of BF16 for an FP32 result.  (One number for a 16-bit
+// result put its rounding, as large as the result's own, beside that: 8192 rows, 8192 x
+// 4096, rank 64, BF16 1.88e-3 off where rounding alone is 1.66e-3.  Two cost that product
+// 3 %, and the adapters' gradients in 16 bits, bound by the tensor cores, 8192 rows, 4096
+// + 4096 features: rank 32 44 us, so 55, rank 64 63 and 95.)
 constexpr int lora_parts(bool bf16, int d_type) {
-  return d_type != MMA_F32 ? 1 : bf16 ? 3 : 2;
+  return bf16 && d_type == MMA_F32 ? 3 : 2;
 }
 constexpr int64_t lora_ld16(bool bf16, int64_t rank) { return (rank + !bf16 + 7) / 8 * 8; }
 struct LoraLow {

@@ -1089,31 +1089,37 @@ __global__ void __launch_bounds__(kThreads + 32)
       const uint32_t ls = smem_u32(stage) + L::M_BYTES;
       [[maybe_unused]] const float* const down =
           reinterpret_cast<const float*>(stage + L::M_BYTES + PARTS * L::PART);
-      uint32_t f[kStageRows / 16][4];
+      // (64 of the rank's sums at a time: eight products that do not wait for one another,
+      // in registers that leave room for two blocks per SM)
+      constexpr int kAt = RP < 64 ? RP / 16 : 4;
 #pragma unroll
-      for (int k = 0; k < kStageRows / 16; ++k) ldmatrix_x4_trans(f[k], ms + k * 16 * 128);
+      for (int n0 = 0; n0 < RP / 16; n0 += kAt) {
+        float sum[2 * kAt][4] = {};
 #pragma unroll
-      for (int n = 0; n < RP / 16; ++n) {
-        float sum[2][4] = {};
+        for (int k = 0; k < kStageRows; k += 16) {
+          uint32_t f[4];
+          ldmatrix_x4_trans(f, ms + k * 128);
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part)
+          for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-          for (int k = 0; k < kStageRows / 16; ++k) {
-            uint32_t b[4];
-            ldmatrix_x4_trans(b, ls + part * L::PART + n * 16 / RB * kStageRows * RB * 2 +
-                                     k * 16 * RB * 2 + low_at[n * 16 % RB / 16]);
-            mma16<BF16>(sum[0], f[k], b[0], b[1]);
-            mma16<BF16>(sum[1], f[k], b[2], b[3]);
-          }
+            for (int x = 0; x < kAt; ++x) {
+              const int n = n0 + x;
+              uint32_t b[4];
+              ldmatrix_x4_trans(b, ls + part * L::PART + n * 16 / RB * kStageRows * RB * 2 +
+                                       k * RB * 2 + low_at[n * 16 % RB / 16]);
+              mma16<BF16>(sum[2 * x], f, b[0], b[1]);
+              mma16<BF16>(sum[2 * x + 1], f, b[2], b[3]);
+            }
+        }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float2 d = make_float2(1.f, 1.f);
+        for (int x = 0; x < 2 * kAt; ++x) {
+          float* const d = acc[2 * n0 + x];
+          float2 scale = make_float2(1.f, 1.f);
           if constexpr (!BF16)
-            d = *reinterpret_cast<const float2*>(down + n * 16 + x * 8 + 2 * (lane & 3));
+            scale = *reinterpret_cast<const float2*>(down + n0 * 16 + x * 8 + 2 * (lane & 3));
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            acc[2 * n + x][j] = BF16 ? acc[2 * n + x][j] + sum[x][j]
-                                     : fmaf(sum[x][j], j & 1 ? d.y : d.x, acc[2 * n + x][j]);
+            d[j] = BF16 ? d[j] + sum[x][j] : fmaf(sum[x][j], j & 1 ? scale.y : scale.x, d[j]);
         }
       }
       __syncwarp();
@@ -1341,7 +1347,8 @@ int64_t gather_ints(int64_t T, int64_t requests, int64_t total) {
 // Where the shares, the sums' parts and their scales lie.  A piece's number is its block
 // and its request, counted from the one before the first: number 0 and the last are of no
 // request, so that two shares less are stored than there are pieces.  They are counted in
-// `bytes` all the same, and hold the scales where those fit.
+// `bytes` all the same, and make room for the scales and, with a 16-bit result, for the
+// sums' second numbers where those fit.
 struct WgradSpace {
   int64_t pieces, chunks, halves, down, bytes;
 };
@@ -1349,14 +1356,16 @@ struct WgradSpace {
 WgradSpace wgrad_space(bool bf16, int d_type, int64_t T, int64_t N, int64_t K, int64_t rank,
                        int64_t requests) {
   const int64_t per = rows_per_piece(T, N, K, rank), share = rank * (N + K) * 4;
-  const int64_t sums = 2 * lora_parts(bf16, d_type) * T * ((rank + 7) / 8 * 8) * 2;
+  const int64_t number = 2 * T * ((rank + 7) / 8 * 8) * 2;
+  const int64_t sums = number * lora_parts(bf16, d_type);
   const int64_t room = rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128;
   WgradSpace s;
   s.pieces = (T + per - 1) / per + requests + 1;
   s.chunks = (T + kStageRows - 1) / kStageRows + requests + 1;
   s.halves = round16(std::max<int64_t>(s.pieces - 2, 0) * share);  // (T 0: no pieces)
   s.down = s.halves + round16(sums);
-  s.bytes = std::max(round16(s.pieces * share) + sums, s.down + (bf16 ? 0 : 2 * s.chunks * room * 4));
+  s.bytes = std::max(round16(s.pieces * share) + (d_type == MMA_F32 ? sums : number),
+                     s.down + (bf16 ? 0 : 2 * s.chunks * room * 4));
   return s;
 }
 
@@ -1440,7 +1449,7 @@ mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& p, void* 
   a.offsets = g.offsets;
   a.adapters = g.adapters;
   a.d_type = g.d_type;
-  a.parts = lora_parts(g.bf16, g.d_type);  // (1, or 3 of BF16 and 2 of FP16)
+  a.parts = lora_parts(g.bf16, g.d_type);
   a.ld16 = (a.rank + 7) / 8 * 8;
   a.accumulate = g.accumulate;
   const WgradSpace space = wgrad_space(g.bf16, g.d_type, g.rows, g.N, g.K, g.rank, g.requests);
@@ -1451,9 +1460,8 @@ mma_status_t launch_lora_wgrad(const Ctx& ctx, const LoraWgradProblem& p, void* 
   a.status = ctx.status;
   return by_rank(g.rank, [&](auto r) {
     constexpr int RP = decltype(r)::value;
-    const bool one = a.parts == 1;
-    if (g.bf16) return one ? wgrad<true, RP, 1>(ctx, g, a) : wgrad<true, RP, 3>(ctx, g, a);
-    return one ? wgrad<false, RP, 1>(ctx, g, a) : wgrad<false, RP, 2>(ctx, g, a);
+    if (!g.bf16) return wgrad<false, RP, 2>(ctx, g, a);
+    return a.parts == 2 ? wgrad<true, RP, 2>(ctx, g, a) : wgrad<true, RP, 3>(ctx, g, a);
   });
 }
 
