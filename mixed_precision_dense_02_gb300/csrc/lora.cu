@@ -499,25 +499,37 @@ __global__ void __launch_bounds__(Shrink<BM, RP, EVERY>::THREADS, Shrink<BM, RP,
       [&](int, const uint8_t* stage) {
         const uint32_t xs = smem_u32(stage), as = xs + L::X_BYTES;
         const int m = lane >> 3, at = lane & 7;
+        // (the tensor cores' FP32 sums drop low bits: they run over a warp's k's of a stage,
+        // 32 or 64, and are added to others to nearest)
+        constexpr int kAt = RP == 128 ? 2 : RP / 16;
 #pragma unroll
-        for (int kk = 0; kk < KS / L::KW / 16; ++kk) {
-          const int k = kw * (KS / L::KW) + kk * 16, box = k / 64, in = k % 64;
-          uint32_t a[4];
-          ldmatrix_x4(a, xs + box * BM * 128 +
-                             swizzled<128>(mw * 16 + (lane & 15), in / 8 + (lane >> 4)));
+        for (int n0 = 0; n0 < RP / 16; n0 += kAt) {
+          float sum[2 * kAt][4] = {};
 #pragma unroll
-          for (int n = 0; n < RP / 16; ++n) {
-            uint32_t b[4];
-            if constexpr (!ROW)
-              ldmatrix_x4(b, as + box * RP * 128 +
-                                 swizzled<128>(n * 16 + (m >> 1) * 8 + at, in / 8 + (m & 1)));
-            else
-              ldmatrix_x4_trans(b, as + n * 16 / RB * KS * RB * 2 +
-                                       swizzled<RB * 2>(k + (m & 1) * 8 + at,
-                                                        n * 2 % (RB / 8) + (m >> 1)));
-            mma16<BF16>(acc[2 * n], a, b[0], b[1]);
-            mma16<BF16>(acc[2 * n + 1], a, b[2], b[3]);
+          for (int kk = 0; kk < KS / L::KW / 16; ++kk) {
+            const int k = kw * (KS / L::KW) + kk * 16, box = k / 64, in = k % 64;
+            uint32_t a[4];
+            ldmatrix_x4(a, xs + box * BM * 128 +
+                               swizzled<128>(mw * 16 + (lane & 15), in / 8 + (lane >> 4)));
+#pragma unroll
+            for (int x = 0; x < kAt; ++x) {
+              const int n = n0 + x;
+              uint32_t b[4];
+              if constexpr (!ROW)
+                ldmatrix_x4(b, as + box * RP * 128 +
+                                   swizzled<128>(n * 16 + (m >> 1) * 8 + at, in / 8 + (m & 1)));
+              else
+                ldmatrix_x4_trans(b, as + n * 16 / RB * KS * RB * 2 +
+                                         swizzled<RB * 2>(k + (m & 1) * 8 + at,
+                                                          n * 2 % (RB / 8) + (m >> 1)));
+              mma16<BF16>(sum[2 * x], a, b[0], b[1]);
+              mma16<BF16>(sum[2 * x + 1], a, b[2], b[3]);
+            }
           }
+#pragma unroll
+          for (int x = 0; x < 2 * kAt; ++x)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[2 * n0 + x][j] += sum[x][j];
         }
       });
   // the warps' sums, then the CTAs', each in order
