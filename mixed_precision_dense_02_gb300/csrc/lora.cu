@@ -1198,8 +1198,10 @@ __global__ void __launch_bounds__(kThreads)
     if (threadIdx.x == 0) found = n;
   }
   __syncthreads();
-  if (a.accumulate && found == 0) return;
+  // (also where there is nothing to add: what follows this kernel may count on the ends
+  // of those before it)
   grid_dependency_wait();
+  if (a.accumulate && found == 0) return;
   const int tiles0 = (a.side[0].F + kThreads - 1) / kThreads;
   const bool second = int(blockIdx.x) >= tiles0;
   const Side& side = a.side[second];
