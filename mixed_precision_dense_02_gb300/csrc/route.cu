@@ -537,12 +537,13 @@ __global__ void __launch_bounds__(256)
       g = w * (g - mean);
     }
     if (id >= 0) slab[id] = g;
-    float most = x[0];
+    // (as the forward kernel: a NaN is the largest, and makes the whole row NaN)
+    uint32_t most_key = 0;
 #pragma unroll
-    for (int c = 1; c < V; ++c) most = fmaxf(most, x[c]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-    const bool some = on && !(most == -INFINITY);
+    for (int c = 0; c < V; ++c) most_key = max(most_key, ordered(x[c]));
+    most_key = __reduce_max_sync(0xffffffffu, most_key);
+    const bool some = on && most_key > kMinusInf;
+    const float most = unordered(most_key);
     float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < V; ++c) {
