@@ -78,12 +78,17 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// exp(d) for d <= 0 (or NaN), zero where it is below 2^-126: the special function
-// alone, without the scaling that subnormal results take.
+// exp(d) for d <= 0 (or NaN), zero where it is below 2^-126: the special function by
+// itself, without the scaling that subnormal results take.  d log2(e) in two numbers,
+// h + l, because the rounding of one grows with d: 2^h 2^l, 2^l = 1 + l ln 2.
 __device__ __forceinline__ float exp_of(float d) {
+  d = d < -200.f ? -200.f : d;  // (infinite distances would leave a NaN in l)
+  const float h = d * 1.4426950408889634f;
+  // (the second constant: what is left of log2(e) beyond FP32, 1.92596e-8)
+  const float l = fmaf(d, 1.92596299e-8f, fmaf(d, 1.4426950408889634f, -h));
   float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d * 1.4426950408889634f));
-  return r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(h));
+  return fmaf(r, l * 0.69314718056f, r);
 }
 
 template <class T, int V>
