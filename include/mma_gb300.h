@@ -486,9 +486,10 @@ mma_status_t mma_rmsnorm_backward(int type, int w_type, int64_t M, int64_t N,
  *     h = x + r,   c = h - mean(h),   y = c / sqrt(mean(c^2) + eps) * w + b
  *
  * in FP32 throughout; H, Y, Q and S and all other arguments as in mma_rmsnorm_f8.
- * B is the bias, N elements of w_type, or NULL.  The mean is taken first and the
- * variance from the distances to it, so that a row far from zero keeps its own.
- * A NaN or infinity in a row makes its row NaN.
+ * B is the bias, N elements of w_type, or NULL.  The variance is taken from the distances
+ * to the mean, or to a number whose distance to the mean is at most a deviation (the mean
+ * of some of the row's elements), so that a row far from zero keeps its own.  A variance
+ * beyond FP32 is infinite and y the bias.  A NaN or infinity in a row makes its row NaN.
  */
 mma_status_t mma_layernorm(int type, int w_type, int64_t M, int64_t N,
                            const void *X, int64_t ldx, const void *R,
