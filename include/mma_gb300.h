@@ -701,6 +701,7 @@ mma_status_t mma_route_backward(int type, int64_t T, int64_t E, int64_t k,
  * A, B    : adapter a's matrices at A + a * stride_a and B + a * stride_b
  *           elements, adapters_total of them (at most 65535), of one rank, at most
  *           MMA_MAX_RANK (a smaller one is padded with zeros).
+ * T, N, K : at most 2^31 - 65536 (more: MMA_ERR_UNSUPPORTED).
  * requests: 0 .. MMA_MAX_REQUESTS; offsets: as mma_gemm_grouped's, but no row is left
  *           out: rows of no request have no adapter.
  * adapters: int32 in device memory, or NULL (request i has adapter i).  Outside [0,

@@ -1106,8 +1106,10 @@ mma_status_t check_lora(int type_in, int type_d, int64_t T, int64_t N, int64_t K
   if (!dim_ok(T) || !dim_ok(N) || !dim_ok(K) || rank < 0 || requests < 0 ||
       adapters_total < 0)
     return MMA_ERR_INVALID_ARG;
+  // (the kernels' counters go on by up to 8192 past an end)
+  constexpr int64_t kMost = INT32_MAX - 65535;
   if (rank > MMA_MAX_RANK || requests > MMA_MAX_REQUESTS || adapters_total > 65535 ||
-      T > INT32_MAX - 1024 || N > INT32_MAX - 1024 || K > INT32_MAX - 1024)
+      T > kMost || N > kMost || K > kMost)
     return MMA_ERR_UNSUPPORTED;
   return rank > 0 && T > 0 ? check_words(offsets) : MMA_OK;
 }
