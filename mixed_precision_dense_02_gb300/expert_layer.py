@@ -8,8 +8,9 @@ added up with the router's weights.  ``serve`` runs it on 8-bit operands:
 norm with 8-bit output, grouped 8-bit products, quantiser in between.
 ``Trainer.step`` runs a step of training on 16-bit operands: grouped
 products, their gradients for the inputs and the weights, the norm's
-gradient and, where asked for, the router's, with its balance loss.  The command runs both on the GPU and prints how far they are from
-the same formulas in 32 bits.
+gradient and, where asked for, the router's, with its balance loss.  The
+command runs both on the GPU and prints how far they are from the same
+formulas in 32 bits.
 """
 from __future__ import annotations
 
@@ -25,9 +26,30 @@ def route(logits, k):
 
     ``order`` sorts the k choices of every token by expert; ``token`` and
     ``weight`` are the sorted choices' tokens and router weights; expert e has
-    the rows ``offsets[e]`` to ``offsets[e + 1]`` of them.
+    the rows ``offsets[e]`` to ``offsets[e + 1]`` of them.  Logits that the GPU's
+    router does not take (on the CPU, of other types, more than 1024 experts or 32
+    choices, or with a gradient to be taken through the weights) go through torch.
     """
-    return _sorted(mma.route(logits, k), k)
+    if (logits.is_cuda and logits.dim() == 2 and not logits.requires_grad
+            and logits.dtype in (torch.float32, torch.float16, torch.bfloat16)
+            and logits.shape[1] <= 1024 and 1 <= k <= 32):
+        return _sorted(mma.route(logits.contiguous(), k), k)
+    return plain_route(logits, k)
+
+
+def plain_route(logits, k):
+    """``route`` in torch operations, of equal logits the lowest expert first."""
+    if not 0 <= k <= logits.shape[-1]:
+        raise ValueError(f"k must be at most {logits.shape[-1]}, not {k}")
+    weight = torch.softmax(logits.float(), -1)
+    expert = torch.sort(logits, dim=-1, descending=True, stable=True).indices[..., :k]
+    weight = weight.gather(-1, expert)
+    weight = weight / weight.sum(-1, keepdim=True)
+    order = torch.argsort(expert.reshape(-1), stable=True)
+    counts = torch.bincount(expert.reshape(-1), minlength=logits.shape[-1])
+    offsets = torch.zeros(counts.numel() + 1, dtype=torch.int32, device=logits.device)
+    offsets[1:] = counts.cumsum(0)
+    return order, order // k, weight.reshape(-1)[order], offsets
 
 
 def _sorted(r, k):
@@ -142,8 +164,8 @@ class Trainer:
 
 
 def reference(x, residual, w, k=2, norm=None, up=None, down=None):
-    """The layer in 32 bits, with autograd's tensors where given; the router
-    sees the same 16-bit rows as the kernels'."""
+    """The layer in 32 bits and torch operations, with autograd's tensors where given;
+    the router sees the same logits of 16-bit rows as the kernels'."""
     norm = w.norm.float() if norm is None else norm
     up = w.up.float() if up is None else up
     down = w.down.float() if down is None else down
@@ -151,7 +173,7 @@ def reference(x, residual, w, k=2, norm=None, up=None, down=None):
     y = h * torch.rsqrt(h.square().mean(-1, keepdim=True) + EPS) * norm
     _, _, _, y16 = mma.rmsnorm_f8(x.detach().to(residual.dtype), w.norm, residual, eps=EPS,
                                   y=True)
-    _, token, weight, offsets = route(mma.gemm(y16, w.router), k)
+    _, token, weight, offsets = plain_route(mma.gemm(y16, w.router), k)
     at = offsets.tolist()
     parts = [gate(y[token[i:j]] @ up[e].t()) @ down[e].t()
              for e, (i, j) in enumerate(zip(at, at[1:]))]
