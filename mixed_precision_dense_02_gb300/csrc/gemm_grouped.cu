@@ -272,7 +272,10 @@ __device__ constexpr int pairs_q(int s) { return (s >> 5) * 32 + ((s >> 2) & 3) 
 // request at a time, with an accumulator of its own of which only the request's
 // columns are added, so that an adapter's infinities stay with it; requests of fewer
 // than kLoraRows rows as with kEveryRow.  (Both wait for the kernels before only
-// where they read what those make, so that the shared product runs beside them.)
+// where they read what those make, so that the shared product runs beside them: a CTA's
+// first tile up to its sums.  From there on a bounded wait could last as long as those
+// kernels, for accumulators whose sums wait for them, and every role waits for their end
+// first.)
 enum Lora { kNoLora, kEveryRow, kRequests };
 
 // KIND8: 8-bit operands with scales, else 16-bit.  P_MN, Q_MN: the operand
@@ -557,6 +560,7 @@ __global__ void __launch_bounds__(kThreads,
           CL > 1 ? mapa_shared(smem_u32(&full[0]), 0) : 0u;
       if constexpr (!LORA) grid_dependency_wait();
       for (int u = first_unit; u < units && ok; u += unit_step) {
+        if (LORA && u != first_unit) grid_dependency_wait();
         const Tile t = decode(u);
         const int py = t.p0 + rank * kP;
         const int qy = t.q0 + rank * (t.nt / CL);
@@ -677,6 +681,7 @@ __global__ void __launch_bounds__(kThreads,
       constexpr uint32_t kStepP = P_MN ? 128 : 2;
       constexpr uint32_t kStepQ = Q_MN ? 128 : 2;
       for (int u = first_unit; u < units && ok; u += unit_step) {
+        if (LORA && u != first_unit) grid_dependency_wait();
         const Tile t = decode(u);
         const uint32_t idesc = a.idesc | (uint32_t(t.nt >> 3) << 17);
         int left = t.k1 - t.k0;  // k still to be issued
@@ -771,6 +776,7 @@ __global__ void __launch_bounds__(kThreads,
           }
         }
         if constexpr (LORA == kRequests) {
+          grid_dependency_wait();
           each_product(t, [&](int, int, int) {
             if (!ok) return;
             ok = mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, a.status);
@@ -957,6 +963,7 @@ __global__ void __launch_bounds__(kThreads,
         L::part_offset(a.groups) + (quarter * 32 + lane) * 4;
     for (int u = first_unit; u < units && ok; u += unit_step) {
       __syncwarp();
+      if (LORA && u != first_unit) grid_dependency_wait();
       const Tile t = decode(u);
       const int pw = t.p0 + rank * kP + quarter * 32;
       const int p = pw + lane;
