@@ -257,8 +257,9 @@ struct LoraProblem {
   void* D;
   int64_t ldd;
 };
-// What its kernels hand on.  The rows' sums scale * (X A): in FP32 (ld32 a multiple
-// of 8, so that eight can be read from any eighth one) and, for more rows than
+// What its kernels hand on.  The rows' sums scale * (X A): in FP32 (16-byte aligned and
+// ld32 a multiple of 8, because they stand in for the operands in the tensor maps of a
+// call without any) and, for more rows than
 // kLoraEveryRow, as `parts` matrices of 16 bits whose sum they are, FP16 ones times a
 // power of two of the row's own (ptx.cuh), whose exponent stands behind the first
 // matrix's row.  In `extra` what
@@ -363,7 +364,7 @@ int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t N);
 mma_status_t launch_rmsnorm_backward(const Ctx& ctx, const NormBackProblem& p,
                                      void* workspace);
 
-// Layer norm (rmsnorm.cu).
+// Layer norm (layernorm.cu).
 int64_t layernorm_backward_workspace_bytes(int64_t M, int64_t N);
 mma_status_t launch_layernorm(const Ctx& ctx, const NormProblem& p);
 mma_status_t launch_layernorm_backward(const Ctx& ctx, const NormBackProblem& p,

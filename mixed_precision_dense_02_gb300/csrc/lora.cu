@@ -77,31 +77,18 @@ __device__ __forceinline__ void load_requests(Requests& r, const int* offsets,
   __syncthreads();
 }
 
-// Piece `u` of blocks of `per` rows: its request (counted from the one before the
-// first) and rows; none: from == to.
+// A piece: its request (counted from the one before the first) and rows; none: from == to.
 struct Piece {
   int request, from, to;
 };
-
-__device__ __forceinline__ Piece piece_of(const int* bound, int requests, int per, int u) {
-  int n = 0;
-  for (int base = 0; base < requests + 2; base += blockDim.x) {
-    const int j = base + threadIdx.x;
-    n += __syncthreads_count(j < requests + 2 && bound[j] / per + j <= u);
-  }
-  const int j = n - 1;  // (request 0 starts in block 0)
-  const int64_t from = max(int64_t(u - j) * per, int64_t(bound[j]));
-  const int to = int(min(int64_t(u - j + 1) * per, int64_t(bound[j + 1])));
-  return Piece{j, int(min(from, int64_t(to))), to};
-}
 
 // The adapter of a request counted from the one before the first, or -1.
 __device__ __forceinline__ int adapter_of(const Requests& r, int j, int requests) {
   return j < 1 || j > requests ? -1 : max(r.who[j - 1], -1);
 }
 
-// Piece `u` of blocks of `per` rows (a power of two), as piece_of, of any number of
-// requests: each thread has kAtOnce of them, and only the piece's own is kept.
+// Piece `u` of blocks of `per` rows (a power of two), of any number of requests: each thread
+// has kAtOnce of them, and only the piece's own is kept.
 struct OnePiece {
   int scan[kThreads / 32 + 1];
   int request, first, next, who;  // `next`: the request's end; who: its adapter, or -1
