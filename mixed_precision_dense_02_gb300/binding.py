@@ -1205,8 +1205,8 @@ def _plan_route(logits, k, mask):
 def route(logits, k: int, *, mask=None, normalize: bool = True, stream=None) -> Routing:
     """The router of a layer of experts.
 
-    ``logits``: (T, E) float32, float16 or bfloat16.  A token's choices are its k
-    largest logits (of equal ones the lowest index), weighted by their softmax
+    ``logits``: (T, E) float32, float16 or bfloat16, E at most 1024.  A token's
+    choices are its k (at most 32) largest logits (of equal ones the lowest index), weighted by their softmax
     probabilities, with ``normalize`` over the sum of the chosen ones.  ``mask``:
     (T,) bool, False for tokens that take no part (padding).  Returns a
     ``Routing``: weights and experts, the choices sorted by expert for

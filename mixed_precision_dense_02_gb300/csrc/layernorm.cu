@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(1024)
 // of x and r in shared memory that bulk copies fill ahead.  A thread has VPT
 // vectors, because the exchange costs it some 150 instructions whatever it holds
 // (8192 x 8192 to 8 bits: with one vector 124 us and four fifths of all issue
-// slots taken).
+// slots taken).  Four take 128 registers, of BF16 with some 32 bytes a thread spilled.
 template <class T, int VPT, bool TAIL>
 __global__ void __launch_bounds__(512, 1)
     layernorm_kernel(const NormProblem p, bool w32, int stages, int row_bytes,

@@ -18,10 +18,11 @@
 // is the last j whose first block + j is not above it.  The rows before the first
 // and after the last request count as requests without an adapter.
 //
-// One token, 8192 x 4096, rank 16: 17.4 us, the shared product alone 16; 64 requests'
-// tokens 25, the product 23 (bound by latency: the sums, their exchange, s B); 8192 rows
-// of 6 prompts, 8192 x 4096, rank 64: 325, the product 300 (the tensor pipe); the
-// gradients of that batch's adapters, rank 16, FP32: 56 with its sums (3.7 TB/s).
+// One token, 8192 x 4096, rank 16: 17.5 us, the shared product alone 16; 64 requests'
+// tokens 25.5, the product 23 (bound by latency: the sums, their exchange, s B); 8192 rows
+// of 6 prompts, 8192 x 4096, rank 64: 337, the product 300 (the tensor pipe); the
+// gradients of that batch's adapters, rank 16, FP32: 56 with its sums (3.7 TB/s).  These are
+// device times in a graph; a call by itself takes 23 us at least, the host's time.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -723,7 +723,7 @@ __device__ __forceinline__ int up_exponent(float most) {
 }
 __device__ __forceinline__ float up_of(int exponent) { return __int_as_float(exponent << 23); }
 __device__ __forceinline__ float down_of(int exponent) {
-  return __int_as_float((254 - exponent) << 23);
+  return __uint_as_float(uint32_t(254 - exponent) << 23);
 }
 
 // A float in the shared memory of a CTA of the cluster (address from mapa_shared).

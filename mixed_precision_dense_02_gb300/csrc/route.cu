@@ -20,9 +20,11 @@
 // adds the counts up over the blocks, a third puts every choice in its place.  Of
 // few tokens one block does all of it: one launch for generated tokens.
 //
-// 16384 tokens, 256 experts, 8 each, FP32: 25 us, of which the choices take some 14,
+// 16384 tokens, 256 experts, 8 each, FP32: 25.5 us, of which the choices take some 15,
 // bound by instructions (600 per token; the logits' 17 MB are read at 0.9 TB/s), the
-// other two kernels the rest by their launches and latencies.  Gradient 12.3 us (3 TB/s).
+// other two kernels the rest by their launches and latencies.  Gradient 12 us (3 TB/s).
+// A lane's share of more than 512 experts does not fit its registers: 144 to 168 bytes a
+// thread are spilled, in one block 600 to 660 (from 257 experts 140 to 170).
 #include <algorithm>
 #include <type_traits>
 
@@ -38,8 +40,9 @@ constexpr int kMostBlocks = 304;  // of the first kernel
 constexpr int kLeast = 16;
 constexpr int kOneBlock = 96;  // most tokens that one block takes alone
 // One block or three kernels, device time: 64 experts, 6 each, 32 tokens 5.6 and 8.4 us,
-// 64 7.3 and 8.4, 96 9.6 and 8.9 (but two launches more); 256 experts, 8 each, 32 tokens
-// 8.0 and 9.6, 128 19.7 and 11.0; 1024, 32 tokens 22 and 14.9.
+// 64 7.4 and 8.4, 80 9.2 and 8.8, 96 9.5 and 9.1, where a whole call still takes less with
+// one launch and no workspace (96 tokens 22.8 us, 97 30.8); 256 experts, 8 each, 32 tokens
+// 8.2 and 9.6, 128 19.7 and 11.0; 1024, 32 tokens 22 and 14.9.
 constexpr bool one_block(int64_t T, int64_t E) { return T <= kOneBlock && T * E <= 8192; }
 
 struct Choices {
