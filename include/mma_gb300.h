@@ -749,6 +749,8 @@ mma_status_t mma_gemm_lora(int type_in, int type_d, int64_t T, int64_t N,
  *           numbers of type_in (BF16 and an FP32 result: three).  They may be of any
  *           size: FP16 ones are scaled by a power of two for each column of at most 64
  *           rows of a request, and keep what is above 2^-38 of its largest.
+ *           An infinity in DY, X, S or U makes infinities or NaN of its adapter's sums
+ *           that it is in.
  * accumulate : nonzero -- added to DA and DB; else an adapter without rows gets
  *           zeros.
  * Sums are FP32, in a fixed order, through `workspace`: 16-byte aligned device

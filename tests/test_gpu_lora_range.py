@@ -99,3 +99,27 @@ def test_bad_sums_stay_in_their_column():
     assert not bool(gb[0, :, 3].isfinite().any()) and bool(ga[1, 5].isnan().all())
     gb[0, :, 3], ga[1, 5] = db[0, :, 3], da[1, 5]
     assert torch.equal(ga, da) and torch.equal(gb, db)
+
+
+def test_captured_and_replayed():
+    """Sums of another size in each replay, their scales with them."""
+    for lengths in ([200, 1, 90], [1, 2] * 90):
+        c = Case(lengths, 136, 200, 32, [i % 3 for i in range(len(lengths))], 3, "f16", seed=4)
+        dy = rows16(rnd(5, c.t, 136), T["f16"])
+
+        def step():
+            d, s = c.run("f32")
+            dx, u = mma.gemm_lora(dy, c.w, c.b, c.a, c.offsets, c.adapters, c.scales, b_layout="row", sums=True)
+            return d, s, dx, u, *mma.gemm_lora_wgrad(dy, c.x, s, u, c.offsets, c.adapters, adapters_total=3)
+
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        for size in (1e-8, 1e6, 1.0):
+            c.scales.copy_(size * torch.tensor([1.0, 0.01, 30.0]))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(out, step())), size
+            check_wgrad(c, dy, out[1], out[3])
